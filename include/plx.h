@@ -258,11 +258,110 @@ size_t plx_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int nsplit);
  * kernel itself uses fewer for small batches, since lengths are on the device). */
 int plx_decode_default_nsplit(int B, int Hkv);
 
+/*
+ * Paged KV cache. A server that appends tokens to many sequences keeps the
+ * cache in pages; the calls below write it, read it back, and attend over it.
+ * The paper describes no cache layout; the mathematics is that of the calls
+ * above. Arguments shared by them:
+ *   kpages, vpages : [num_pages, Hkv, page_size, d], bf16, or e4m3 codes (one
+ *                    byte each) if kscale and vscale are given. page_size is
+ *                    16, 32, 64, 128 or 256; d must be 128.
+ *   kscale, vscale : uint8 [num_pages, Hkv, page_size], both or neither. A row
+ *                    of codes stands for code * 2^(E - 127), E its byte in
+ *                    1 .. 254 (a row with E = 0 counts as zeros).
+ *   block_table    : int32 [B, max_pages] on the device. Position p of sequence
+ *                    b is in slot p % page_size of page
+ *                    block_table[b, p / page_size]. Entries behind a sequence's
+ *                    last page are not read, and pages may be shared between
+ *                    sequences that only read them.
+ *   seqlens        : int32 [B] on the device: the keys of each sequence, the
+ *                    call's new tokens included; at most max_pages * page_size.
+ *   cu_q           : int32 [B + 1] on the device, non-decreasing from
+ *                    cu_q[0] = 0: the n_b = cu_q[b + 1] - cu_q[b] >= 0 new
+ *                    tokens of sequence b are rows cu_q[b] .. of the T packed
+ *                    rows. Rows behind cu_q[B] belong to no sequence.
+ * New token i (0 .. n_b - 1) of sequence b has position seqlens[b] - n_b + i; a
+ * negative one marks padding (a row that has no place in the cache and sees no
+ * key). Whatever the pages hold behind seqlens[b], NaN included, does not reach
+ * any result. Packed rows have strides in elements, for the token and the head;
+ * a row's d values are contiguous. Strides are multiples of 8 and at least d,
+ * pointers 16-byte aligned (a byte's alignment for the scales, 4 bytes for
+ * int32 and fp32). A page number outside 0 .. num_pages - 1 or a length beyond
+ * max_pages * page_size is not followed: the row's results are undefined and
+ * plx_check_device_error reports PLX_ERR_INVALID_ARG.
+ */
+
+/*
+ * Write the new tokens' keys and values into their pages (bf16 rows copied, or
+ * quantised to e4m3 as they are written): k, v bf16 [T, Hkv, d] with the given
+ * strides. e4m3: with a = max|x| of the row, E is the smallest exponent >= 1
+ * with a <= 448 * 2^(E - 127), and each code is x * 2^(127 - E) rounded to
+ * nearest even. A row with a NaN or an infinity is stored undefined in e4m3 and
+ * reported as PLX_ERR_INVALID_ARG by plx_check_device_error. cu_q may be NULL
+ * for one new token a sequence (T = B). Padding rows, and rows behind cu_q[B],
+ * write nothing. Two rows of one call must not have the same place. T >= 0.
+ */
+plx_status plx_kv_append(const void *k, const void *v, long long token_stride,
+                         long long head_stride, void *kpages, void *vpages, unsigned char *kscale,
+                         unsigned char *vscale, const int *block_table, const int *seqlens,
+                         const int *cu_q, int T, int B, int Hkv, int d, int num_pages,
+                         int page_size, int max_pages, void *stream);
+
+/*
+ * Read sequences back into the packed layout that plx_decode_fwd takes: the
+ * first cu_k[b + 1] - cu_k[b] tokens of sequence b go to rows cu_k[b] .. of
+ *   k, v : bf16 [T, Hkv, d], contiguous, written
+ * (codes times their scale, rounded to nearest even: exact unless the value is
+ * below 2^-126). cu_k is int32 [B + 1] like cu_q. Rows behind cu_k[B] are left
+ * as they were. T >= 0.
+ */
+plx_status plx_kv_read(const void *kpages, const void *vpages, const unsigned char *kscale,
+                       const unsigned char *vscale, const int *block_table, const int *cu_k, void *k,
+                       void *v, int T, int B, int Hkv, int d, int num_pages, int page_size,
+                       int max_pages, void *stream);
+
+/*
+ * plx_decode_fwd over a paged cache: one new query per sequence, which sees all
+ * seqlens[b] keys (its own, appended before, included).
+ *   q, r, out : bf16 [B, Hq, d], contiguous. A sequence of length 0 gets zeros.
+ * workspace: at least plx_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes on
+ * the device, 16-byte aligned, or NULL to allocate them in stream order
+ * (cudaMallocAsync / cudaFreeAsync on `stream`). Calls that may overlap on the
+ * GPU must not share one.
+ */
+plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages,
+                                const void *vpages, const unsigned char *kscale,
+                                const unsigned char *vscale, const int *block_table,
+                                const int *seqlens, void *out, int B, int Hq, int Hkv, int d,
+                                int num_pages, int page_size, int max_pages, void *workspace,
+                                size_t workspace_bytes, void *stream);
+size_t plx_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
+
+/*
+ * plx_prefill_fwd_chunk for a ragged batch over a paged cache: chunks of new
+ * tokens, each token seeing the keys 0 .. its own position (appended before).
+ *   q, r : bf16 [T, Hq, d] with the qr strides (both the same)
+ *   out  : bf16 [T, Hq, d] with the out strides; its rows must not overlap
+ *   lse  : fp32 [T, Hq] contiguous, or NULL
+ * A padding row (negative position) gets out = 0 and lse = -infinity; rows
+ * behind cu_q[B] are left as they were. T >= 0. workspace as for
+ * plx_decode_fwd_paged, of plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d).
+ */
+plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_token_stride,
+                                 long long qr_head_stride, const void *kpages, const void *vpages,
+                                 const unsigned char *kscale, const unsigned char *vscale,
+                                 const int *block_table, const int *seqlens, const int *cu_q,
+                                 void *out, long long out_token_stride, long long out_head_stride,
+                                 float *lse, int T, int B, int Hq, int Hkv, int d, int num_pages,
+                                 int page_size, int max_pages, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
+
 /* Synchronises `stream`, then reads and clears the device error word.
  * PLX_ERR_DEVICE_TIMEOUT if a bounded wait ran out since the last check,
  * PLX_ERR_INVALID_ARG if a kernel found its device-side inputs out of range
  * (decode lengths summing to 2^30 tokens or more; that call did no work and
- * its outputs are undefined), PLX_ERR_BOUNDS if a device-side index check of
+ * its outputs are undefined; for a paged cache the cases named there), PLX_ERR_BOUNDS if a device-side index check of
  * a debug build failed (below), PLX_ERR_CUDA if the stream reports an error,
  * else PLX_OK.
  *

@@ -41,6 +41,13 @@ SIGNATURES = {
     "plx_decode_fwd_cor": (_i, [_vp] * 7 + [_i] * 4 + [_vp]),
     "plx_decode_workspace_bytes": (_sz, [_i] * 5),
     "plx_decode_default_nsplit": (_i, [_i] * 2),
+    "plx_kv_append": (_i, [_vp] * 2 + [_ll] * 2 + [_vp] * 7 + [_i] * 7 + [_vp]),
+    "plx_kv_read": (_i, [_vp] * 8 + [_i] * 7 + [_vp]),
+    "plx_decode_fwd_paged": (_i, [_vp] * 9 + [_i] * 7 + [_vp, _sz, _vp]),
+    "plx_decode_paged_workspace_bytes": (_sz, [_i] * 4),
+    "plx_prefill_fwd_paged": (_i, [_vp] * 2 + [_ll] * 2 + [_vp] * 8 + [_ll] * 2 + [_vp] + [_i] * 8
+                              + [_vp, _sz, _vp]),
+    "plx_prefill_paged_workspace_bytes": (_sz, [_i] * 5),
     "plx_check_device_error": (_i, [_vp]),
     "plx_debug_timeout_probe": (_i, [_ll, _vp]),
     "plx_status_string": (ctypes.c_char_p, [_i]),
@@ -405,6 +412,202 @@ def plx_decode_workspace_bytes(B, Hq, Hkv, d, nsplit) -> int:
 
 def plx_decode_default_nsplit(B, Hkv) -> int:
     return int(lib().plx_decode_default_nsplit(B, Hkv))
+
+
+def _pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
+    """Checks of a paged cache and of the int32 [B] lengths (or None) that go
+    with it; returns the pointers (kpages, vpages, kscale, vscale, block_table)
+    and the sizes (B, Hkv, d, num_pages, page_size, max_pages)."""
+    fp8 = kscale is not None or vscale is not None
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    if kpages.dim() != 4:
+        raise ValueError("kpages must be [num_pages, Hkv, page_size, d], got shape "
+                         f"{tuple(kpages.shape)}")
+    shape = kpages.shape
+    if vpages.shape != shape:
+        raise ValueError(f"vpages has shape {tuple(vpages.shape)}, expected {tuple(shape)}")
+    if block_table.dim() != 2 or block_table.shape[0] < 1:
+        raise ValueError(f"block_table must be [B, max_pages], got shape {tuple(block_table.shape)}")
+    B, width = block_table.shape
+    if seqlens is not None and tuple(seqlens.shape) != (B,):
+        raise ValueError(f"seqlens must have shape ({B},), got {tuple(seqlens.shape)}")
+    for name, t in (("kscale", kscale), ("vscale", vscale)):
+        if fp8 and (t is None or t.shape != shape[:3]):
+            raise ValueError(f"{name} must be given with shape {tuple(shape[:3])}")
+    _need(kpages, "kpages", dtype, 4, dev)
+    _need(vpages, "vpages", dtype, 4, dev)
+    if fp8:
+        _need(kscale, "kscale", torch.uint8, 3, dev)
+        _need(vscale, "vscale", torch.uint8, 3, dev)
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    if seqlens is not None:
+        _need(seqlens, "seqlens", torch.int32, 1, dev)
+    ptrs = (kpages.data_ptr(), vpages.data_ptr(), kscale.data_ptr() if fp8 else None,
+            vscale.data_ptr() if fp8 else None, block_table.data_ptr())
+    return ptrs, (B, shape[1], shape[3], shape[0], shape[2], width)
+
+
+def _cu(cu, name, B, dev):
+    if tuple(cu.shape) != (B + 1,):
+        raise ValueError(f"{name} must have shape ({B + 1},), got {tuple(cu.shape)}")
+    _need(cu, name, torch.int32, 1, dev)
+
+
+def _packed(t, name, heads, d, dev):
+    """(token, head) strides of packed rows [T, heads, d]; only a row's d
+    values must be contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {heads if heads is not None else 'heads'}, {d}], got "
+                         f"shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and d != 1:
+        raise ValueError(f"{name} must have its last dimension contiguous")
+    # A dimension of size one has no stride of its own.
+    hs = hs if t.shape[1] > 1 else d
+    ts = ts if t.shape[0] > 1 else max(d, hs * t.shape[1])
+    return ts, hs
+
+
+def _workspace(workspace, dev):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or workspace.device != dev:
+        raise ValueError("workspace must be on the device of q")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def plx_kv_append(k, v, kpages, vpages, block_table, seqlens, cu_q=None, kscale=None, vscale=None,
+                  stream=None):
+    """Write new tokens into a paged KV cache (see include/plx.h): k, v bf16
+    [T, Hkv, d] with any token and head strides (the projection's [Hkv, T, d]
+    transposed will do); pages bf16, or torch.float8_e4m3fn with uint8
+    ``kscale`` / ``vscale``. ``cu_q=None``: one new token a sequence. Returns
+    (kpages, vpages)."""
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, Hkv, d], got shape {tuple(k.shape)}")
+    if v.shape != k.shape:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected the shape of k {tuple(k.shape)}")
+    dev = k.device
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
+                                               dev)
+    strides = _packed(k, "k", Hkv, d, dev)
+    if _packed(v, "v", Hkv, d, dev) != strides:
+        raise ValueError("k and v must have the same strides")
+    T = k.shape[0]
+    if cu_q is not None:
+        _cu(cu_q, "cu_q", B, dev)
+    elif T != B:
+        raise ValueError(f"without cu_q, k must have one row for each of the {B} sequences, got {T}")
+    with torch.cuda.device(dev):
+        st = lib().plx_kv_append(k.data_ptr(), v.data_ptr(), *strides, *ptrs, seqlens.data_ptr(),
+                                 cu_q.data_ptr() if cu_q is not None else None, T, B, Hkv, d, n,
+                                 page, width, _stream(stream, dev))
+    _check(st)
+    return kpages, vpages
+
+
+def plx_kv_read(kpages, vpages, block_table, cu_k, T, kscale=None, vscale=None, k=None, v=None,
+                stream=None):
+    """Read sequences of a paged KV cache back (see include/plx.h): the first
+    cu_k[b + 1] - cu_k[b] tokens of sequence b at rows cu_k[b] .. of bf16
+    [T, Hkv, d], the packed cache of plx_decode_fwd. Returns (k, v)."""
+    dev = kpages.device
+    T = int(T)
+    if T < 0:
+        raise ValueError(f"T must be >= 0, got {T}")
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, None, dev)
+    _cu(cu_k, "cu_k", B, dev)
+    k = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        _need(t, name, torch.bfloat16, 3, dev)
+        if tuple(t.shape) != (T, Hkv, d):
+            raise ValueError(f"{name} must be ({T}, {Hkv}, {d}), got {tuple(t.shape)}")
+    with torch.cuda.device(dev):
+        st = lib().plx_kv_read(*ptrs, cu_k.data_ptr(), k.data_ptr(), v.data_ptr(), T, B, Hkv, d, n,
+                               page, width, _stream(stream, dev))
+    _check(st)
+    return k, v
+
+
+def plx_decode_fwd_paged(q, r, kpages, vpages, block_table, seqlens, kscale=None, vscale=None,
+                         out=None, workspace=None, stream=None):
+    """Decode over a paged KV cache (see include/plx.h): q, r bf16 [B, Hq, d].
+    Returns out."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [B, Hq, d], got shape {tuple(q.shape)}")
+    dev = q.device
+    Hq = q.shape[1]
+    out = torch.empty_like(q) if out is None else out
+    rows = (("q", q), ("r", r), ("out", out))
+    for name, t in rows:
+        if tuple(t.shape) != (block_table.shape[0], Hq, kpages.shape[-1]):
+            raise ValueError(f"{name} must be ({block_table.shape[0]}, {Hq}, {kpages.shape[-1]}), got "
+                             f"shape {tuple(t.shape)}")
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
+                                               dev)
+    for name, t in rows:
+        _need(t, name, torch.bfloat16, 3, dev)
+    with torch.cuda.device(dev):
+        st = lib().plx_decode_fwd_paged(q.data_ptr(), r.data_ptr(), *ptrs, seqlens.data_ptr(),
+                                        out.data_ptr(), B, Hq, Hkv, d, n, page, width,
+                                        *_workspace(workspace, dev), _stream(stream, dev))
+    _check(st)
+    return out
+
+
+def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, kscale=None,
+                          vscale=None, out=None, lse=None, workspace=None, stream=None):
+    """Causal prefill of a ragged batch of chunks over a paged KV cache (see
+    include/plx.h): q, r bf16 [T, Hq, d] with any token and head strides, the
+    same for both. ``lse`` is fp32 [T, Hq] or None. Returns (out, lse)."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, d], got shape {tuple(q.shape)}")
+    if r.shape != q.shape:
+        raise ValueError(f"r has shape {tuple(r.shape)}, expected the shape of q {tuple(q.shape)}")
+    dev = q.device
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
+                                               dev)
+    T, Hq, _ = q.shape
+    strides = _packed(q, "q", Hq, d, dev)
+    if _packed(r, "r", Hq, d, dev) != strides:
+        raise ValueError("q and r must have the same strides")
+    _cu(cu_q, "cu_q", B, dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    if out.shape != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    out_strides = _packed(out, "out", Hq, d, dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2, dev)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError(f"lse must be ({T}, {Hq}), got {tuple(lse.shape)}")
+    with torch.cuda.device(dev):
+        st = lib().plx_prefill_fwd_paged(q.data_ptr(), r.data_ptr(), *strides, *ptrs,
+                                         seqlens.data_ptr(), cu_q.data_ptr(), out.data_ptr(),
+                                         *out_strides, lse.data_ptr() if lse is not None else None,
+                                         T, B, Hq, Hkv, d, n, page, width,
+                                         *_workspace(workspace, dev), _stream(stream, dev))
+    _check(st)
+    return out, lse
+
+
+def plx_decode_paged_workspace_bytes(B, Hq, Hkv, d) -> int:
+    return int(lib().plx_decode_paged_workspace_bytes(B, Hq, Hkv, d))
+
+
+def plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d) -> int:
+    return int(lib().plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d))
 
 
 def plx_check_device_error(stream=None, device=None):

@@ -409,6 +409,196 @@ plx_status plx_decode_fwd_noalloc(const void *q, const void *r, const void *kcac
                      scratch, cap_bytes, stream);
 }
 
+namespace {
+
+// Checks of a paged cache's arguments that need no device, and its kernels' form.
+plx_status paged_cache(const char *fn, plx::PagedCache *c, const void *kpages, const void *vpages,
+                       const unsigned char *kscale, const unsigned char *vscale,
+                       const int *block_table, int B, int Hkv, int d, int num_pages, int page_size,
+                       int max_pages) {
+  if (!kpages || !vpages || !block_table) return fail(PLX_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if ((kscale == nullptr) != (vscale == nullptr))
+    return fail(PLX_ERR_INVALID_ARG, "%s: kscale and vscale must be given both or neither", fn);
+  if (B < 1 || Hkv < 1 || d < 1 || num_pages < 1 || max_pages < 1)
+    return fail(PLX_ERR_INVALID_ARG,
+                "%s: sizes must be >= 1 (B=%d Hkv=%d d=%d num_pages=%d max_pages=%d)", fn, B, Hkv, d,
+                num_pages, max_pages);
+  if (d != 128) return fail(PLX_ERR_UNSUPPORTED, "%s: head dim %d (only 128)", fn, d);
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != page_size) ++shift;
+  if ((1 << shift) != page_size)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: page_size %d (16, 32, 64, 128 or 256)", fn, page_size);
+  if (!aligned16(kpages) || !aligned16(vpages))
+    return fail(PLX_ERR_INVALID_ARG, "%s: page pointers must be 16-byte aligned", fn);
+  if (static_cast<long long>(num_pages) * Hkv > 0x7fffffffLL ||
+      static_cast<long long>(max_pages) * page_size > 0x7fffffffLL)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: num_pages * Hkv and max_pages * page_size must be < 2^31",
+                fn);
+  c->k = kpages;
+  c->v = vpages;
+  c->kscale = kscale;
+  c->vscale = vscale;
+  c->table = block_table;
+  c->B = B;
+  c->Hkv = Hkv;
+  c->num_pages = num_pages;
+  c->page_shift = shift;
+  c->max_pages = max_pages;
+  c->err = nullptr;
+  return PLX_OK;
+}
+
+// Strides of T x H packed rows of d values.
+plx_status check_strides(const char *fn, const char *what, long long token, long long head, int T,
+                         int H, int d, bool distinct) {
+  const long long most = 1LL << 38;  // elements: a tensor map's strides end below 2^40 bytes
+  if (token < d || head < d || token % 8 != 0 || head % 8 != 0 || token > most || head > most)
+    return fail(PLX_ERR_INVALID_ARG,
+                "%s: %s strides (%lld, %lld) must be multiples of 8, at least %d and at most 2^38", fn,
+                what, token, head, d);
+  if (distinct && token < (H - 1) * head + d && head < (T - 1) * token + d)
+    return fail(PLX_ERR_INVALID_ARG, "%s: %s rows overlap (strides %lld, %lld)", fn, what, token, head);
+  return PLX_OK;
+}
+
+plx_status check_heads(const char *fn, int Hq, int Hkv) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
+    return fail(PLX_ERR_INVALID_ARG, "%s: Hq (%d) must be a positive multiple of Hkv (%d)", fn, Hq, Hkv);
+  if (Hq / Hkv > 128) return fail(PLX_ERR_UNSUPPORTED, "%s: Hq / Hkv = %d (at most 128)", fn, Hq / Hkv);
+  return PLX_OK;
+}
+
+}  // namespace
+
+plx_status plx_kv_append(const void *k, const void *v, long long token_stride,
+                         long long head_stride, void *kpages, void *vpages, unsigned char *kscale,
+                         unsigned char *vscale, const int *block_table, const int *seqlens,
+                         const int *cu_q, int T, int B, int Hkv, int d, int num_pages,
+                         int page_size, int max_pages, void *stream) {
+  const char *fn = "plx_kv_append";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  if (!seqlens) return fail(PLX_ERR_INVALID_ARG, "%s: null seqlens", fn);
+  if (T < 0) return fail(PLX_ERR_INVALID_ARG, "%s: T (%d) must be >= 0", fn, T);
+  if (!cu_q && T != B)
+    return fail(PLX_ERR_INVALID_ARG, "%s: without cu_q, T (%d) must be B (%d)", fn, T, B);
+  if (T == 0) return PLX_OK;
+  if (!k || !v) return fail(PLX_ERR_INVALID_ARG, "%s: null k or v", fn);
+  if (!aligned16(k) || !aligned16(v))
+    return fail(PLX_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned", fn);
+  s = check_strides(fn, "k, v", token_stride, head_stride, T, Hkv, d, false);
+  if (s) return s;
+  if (static_cast<long long>(T) * Hkv > 0x7fffffffLL)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: problem too large for one launch", fn);
+  c.err = plx::device_error_word();
+  return finish_launch(plx::launch_kv_append(c, k, v, token_stride, head_stride, seqlens, cu_q, T,
+                                             static_cast<cudaStream_t>(stream)),
+                       fn);
+}
+
+plx_status plx_kv_read(const void *kpages, const void *vpages, const unsigned char *kscale,
+                       const unsigned char *vscale, const int *block_table, const int *cu_k, void *k,
+                       void *v, int T, int B, int Hkv, int d, int num_pages, int page_size,
+                       int max_pages, void *stream) {
+  const char *fn = "plx_kv_read";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  if (!cu_k) return fail(PLX_ERR_INVALID_ARG, "%s: null cu_k", fn);
+  if (T < 0) return fail(PLX_ERR_INVALID_ARG, "%s: T (%d) must be >= 0", fn, T);
+  if (T == 0) return PLX_OK;
+  if (!k || !v) return fail(PLX_ERR_INVALID_ARG, "%s: null k or v", fn);
+  if (!aligned16(k) || !aligned16(v))
+    return fail(PLX_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned", fn);
+  if (static_cast<long long>(T) * Hkv > 0x7fffffffLL)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: problem too large for one launch", fn);
+  c.err = plx::device_error_word();
+  return finish_launch(
+      plx::launch_kv_read(c, cu_k, k, v, T, static_cast<cudaStream_t>(stream)), fn);
+}
+
+size_t plx_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
+  return 16;
+}
+
+plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages,
+                                const void *vpages, const unsigned char *kscale,
+                                const unsigned char *vscale, const int *block_table,
+                                const int *seqlens, void *out, int B, int Hq, int Hkv, int d,
+                                int num_pages, int page_size, int max_pages, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+  const char *fn = "plx_decode_fwd_paged";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  s = check_heads(fn, Hq, Hkv);
+  if (s) return s;
+  if (!q || !r || !out || !seqlens) return fail(PLX_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(q) || !aligned16(r) || !aligned16(out))
+    return fail(PLX_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", fn);
+  if (static_cast<long long>(B) * Hq > (1LL << 24))
+    return fail(PLX_ERR_UNSUPPORTED, "%s: B * Hq must be <= 2^24", fn);
+  if (workspace && workspace_bytes < plx_decode_paged_workspace_bytes(B, Hq, Hkv, d))
+    return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes,
+                plx_decode_paged_workspace_bytes(B, Hq, Hkv, d));
+  if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  c.err = plx::device_error_word();
+  return finish_launch(
+      plx::launch_paged_attn(c, q, r, static_cast<long long>(Hq) * d, d, seqlens, nullptr, out,
+                             static_cast<long long>(Hq) * d, d, nullptr, B, Hq,
+                             static_cast<cudaStream_t>(stream)),
+      fn);
+}
+
+size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d) {
+  if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
+  return 16;
+}
+
+plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_token_stride,
+                                 long long qr_head_stride, const void *kpages, const void *vpages,
+                                 const unsigned char *kscale, const unsigned char *vscale,
+                                 const int *block_table, const int *seqlens, const int *cu_q,
+                                 void *out, long long out_token_stride, long long out_head_stride,
+                                 float *lse, int T, int B, int Hq, int Hkv, int d, int num_pages,
+                                 int page_size, int max_pages, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  const char *fn = "plx_prefill_fwd_paged";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  s = check_heads(fn, Hq, Hkv);
+  if (s) return s;
+  if (!seqlens || !cu_q) return fail(PLX_ERR_INVALID_ARG, "%s: null seqlens or cu_q", fn);
+  if (T < 0) return fail(PLX_ERR_INVALID_ARG, "%s: T (%d) must be >= 0", fn, T);
+  if (workspace && workspace_bytes < plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d))
+    return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes,
+                plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d));
+  if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  if (T == 0) return PLX_OK;
+  if (!q || !r || !out) return fail(PLX_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(q) || !aligned16(r) || !aligned16(out))
+    return fail(PLX_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", fn);
+  s = check_strides(fn, "q, r", qr_token_stride, qr_head_stride, T, Hq, d, false);
+  if (s) return s;
+  s = check_strides(fn, "out", out_token_stride, out_head_stride, T, Hq, d, true);
+  if (s) return s;
+  if (static_cast<long long>(T) * Hq > 0x7fffffffLL)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: problem too large for one launch", fn);
+  c.err = plx::device_error_word();
+  return finish_launch(
+      plx::launch_paged_attn(c, q, r, qr_token_stride, qr_head_stride, seqlens, cu_q, out,
+                             out_token_stride, out_head_stride, lse, T, Hq,
+                             static_cast<cudaStream_t>(stream)),
+      fn);
+}
+
 plx_status plx_check_device_error(void *stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(st);
@@ -435,7 +625,8 @@ plx_status plx_check_device_error(void *stream) {
   if (v & plx::kErrBadInput)
     return fail(PLX_ERR_INVALID_ARG,
                 "a kernel found device-side inputs out of range (decode: seqlens sum to 2^30 "
-                "tokens or more); its outputs are undefined (error word 0x%x)",
+                "tokens or more; paged cache: a page number, a length or a value to be "
+                "quantised); its outputs are undefined (error word 0x%x)",
                 v);
   return PLX_OK;
 }

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 namespace plx {
 
@@ -85,6 +86,28 @@ cudaError_t noalloc_scratch(float **ptr);
 cudaError_t launch_qkvr_proj(const void *x, const void *w, void *q, void *k, void *v, void *r,
                              int B, int L, int D, int Hq, int Hkv, unsigned *err,
                              cudaStream_t stream);
+
+// A paged KV cache (layout and scales in plx_paged.cuh). kscale and vscale
+// are null for bf16 pages. page_size = 1 << page_shift.
+struct PagedCache {
+  const void *k, *v;
+  const uint8_t *kscale, *vscale;
+  const int *table;  // [B, max_pages]
+  int B, Hkv, num_pages, page_shift, max_pages;
+  unsigned *err;
+};
+
+// Strides of the new tokens' rows are in elements.
+cudaError_t launch_kv_append(const PagedCache &c, const void *k, const void *v,
+                             long long token_stride, long long head_stride, const int *seqlens,
+                             const int *cu_q, int T, cudaStream_t stream);
+cudaError_t launch_kv_read(const PagedCache &c, const int *cu_k, void *k, void *v, int T,
+                           cudaStream_t stream);
+// lse ([T, Hq] fp32) may be null; cu_q null: one new token a sequence.
+cudaError_t launch_paged_attn(const PagedCache &c, const void *q, const void *r, long long qts,
+                              long long qhs, const int *seqlens, const int *cu_q, void *out,
+                              long long ots, long long ohs, float *lse, int T, int Hq,
+                              cudaStream_t stream);
 
 cudaError_t launch_timeout_probe(long long limit_cycles, unsigned *err, cudaStream_t stream);
 
