@@ -268,7 +268,8 @@ int plx_decode_default_nsplit(int B, int Hkv);
  *                    16, 32, 64, 128 or 256; d must be 128.
  *   kscale, vscale : uint8 [num_pages, Hkv, page_size], both or neither. A row
  *                    of codes stands for code * 2^(E - 127), E its byte in
- *                    1 .. 254 (a row with E = 0 counts as zeros).
+ *                    1 .. 254 (a row with E = 0 counts as zeros). Attention over
+ *                    e4m3 pages wants |q|, |r| < 2^63 and |v| < 2^70.
  *   block_table    : int32 [B, max_pages] on the device. Position p of sequence
  *                    b is in slot p % page_size of page
  *                    block_table[b, p / page_size]. Entries behind a sequence's
@@ -285,8 +286,7 @@ int plx_decode_default_nsplit(int B, int Hkv);
  * key). Whatever the pages hold behind seqlens[b], NaN included, does not reach
  * any result. Packed rows have strides in elements, for the token and the head;
  * a row's d values are contiguous. Strides are multiples of 8 and at least d,
- * pointers 16-byte aligned (a byte's alignment for the scales, 4 bytes for
- * int32 and fp32). A page number outside 0 .. num_pages - 1 or a length beyond
+ * pointers 16-byte aligned (4 bytes for int32 and fp32). A page number outside 0 .. num_pages - 1 or a length beyond
  * max_pages * page_size is not followed: the row's results are undefined and
  * plx_check_device_error reports PLX_ERR_INVALID_ARG.
  */

@@ -476,14 +476,23 @@ def _packed(t, name, heads, d, dev):
     return ts, hs
 
 
-def _workspace(workspace, dev):
+def _workspace(workspace, need, stream, dev):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one of `need`
+    bytes from torch's caching allocator, in the order of the call's stream (a
+    stream-ordered allocation by the library would give its memory back to the
+    driver whenever the GPU idles: 200 us for a call after a synchronize)."""
     if workspace is None:
-        return None, 0
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != dev:
         raise ValueError("workspace must be on the device of q")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def plx_kv_append(k, v, kpages, vpages, block_table, seqlens, cu_q=None, kscale=None, vscale=None,
@@ -558,10 +567,12 @@ def plx_decode_fwd_paged(q, r, kpages, vpages, block_table, seqlens, kscale=None
                                                dev)
     for name, t in rows:
         _need(t, name, torch.bfloat16, 3, dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, plx_decode_paged_workspace_bytes(B, Hq, Hkv, d),
+                                      stream, dev)
     with torch.cuda.device(dev):
         st = lib().plx_decode_fwd_paged(q.data_ptr(), r.data_ptr(), *ptrs, seqlens.data_ptr(),
-                                        out.data_ptr(), B, Hq, Hkv, d, n, page, width,
-                                        *_workspace(workspace, dev), _stream(stream, dev))
+                                        out.data_ptr(), B, Hq, Hkv, d, n, page, width, ws_ptr,
+                                        ws_bytes, _stream(stream, dev))
     _check(st)
     return out
 
@@ -592,12 +603,14 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
         _need(lse, "lse", torch.float32, 2, dev)
         if tuple(lse.shape) != (T, Hq):
             raise ValueError(f"lse must be ({T}, {Hq}), got {tuple(lse.shape)}")
+    ws, ws_ptr, ws_bytes = _workspace(workspace, plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d),
+                                      stream, dev)
     with torch.cuda.device(dev):
         st = lib().plx_prefill_fwd_paged(q.data_ptr(), r.data_ptr(), *strides, *ptrs,
                                          seqlens.data_ptr(), cu_q.data_ptr(), out.data_ptr(),
                                          *out_strides, lse.data_ptr() if lse is not None else None,
-                                         T, B, Hq, Hkv, d, n, page, width,
-                                         *_workspace(workspace, dev), _stream(stream, dev))
+                                         T, B, Hq, Hkv, d, n, page, width, ws_ptr, ws_bytes,
+                                         _stream(stream, dev))
     _check(st)
     return out, lse
 

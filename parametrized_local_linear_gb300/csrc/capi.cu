@@ -164,6 +164,22 @@ plx_status finish_launch(cudaError_t e, const char *fn) {
   return PLX_OK;
 }
 
+// launch(workspace) with the caller's workspace, or with `need` bytes allocated
+// and freed in stream order.
+template <class Launch>
+plx_status with_workspace(const char *fn, void *workspace, size_t need, cudaStream_t st,
+                          Launch launch) {
+  if (workspace != nullptr) return finish_launch(launch(workspace), fn);
+  void *ws = nullptr;
+  cudaError_t e = cudaMallocAsync(&ws, need, st);
+  if (e != cudaSuccess) return cuda_fail(e, "workspace allocation");
+  e = launch(ws);
+  cudaError_t e2 = cudaFreeAsync(ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  if (e2 != cudaSuccess) return cuda_fail(e2, "workspace release");
+  return PLX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -430,6 +446,8 @@ plx_status paged_cache(const char *fn, plx::PagedCache *c, const void *kpages, c
     return fail(PLX_ERR_UNSUPPORTED, "%s: page_size %d (16, 32, 64, 128 or 256)", fn, page_size);
   if (!aligned16(kpages) || !aligned16(vpages))
     return fail(PLX_ERR_INVALID_ARG, "%s: page pointers must be 16-byte aligned", fn);
+  if (!aligned16(kscale) || !aligned16(vscale))
+    return fail(PLX_ERR_INVALID_ARG, "%s: kscale and vscale must be 16-byte aligned", fn);
   if (static_cast<long long>(num_pages) * Hkv > 0x7fffffffLL ||
       static_cast<long long>(max_pages) * page_size > 0x7fffffffLL)
     return fail(PLX_ERR_UNSUPPORTED, "%s: num_pages * Hkv and max_pages * page_size must be < 2^31",
@@ -522,7 +540,7 @@ plx_status plx_kv_read(const void *kpages, const void *vpages, const unsigned ch
 
 size_t plx_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
-  return 16;
+  return plx::paged_rows_workspace_bytes(B, B, Hq / Hkv, Hkv, d, false);
 }
 
 plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages,
@@ -548,11 +566,13 @@ plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages
                 plx_decode_paged_workspace_bytes(B, Hq, Hkv, d));
   if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
   c.err = plx::device_error_word();
-  return finish_launch(
-      plx::launch_paged_attn(c, q, r, static_cast<long long>(Hq) * d, d, seqlens, nullptr, out,
-                             static_cast<long long>(Hq) * d, d, nullptr, B, Hq,
-                             static_cast<cudaStream_t>(stream)),
-      fn);
+  const long long row = static_cast<long long>(Hq) * d;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_workspace(fn, workspace, plx_decode_paged_workspace_bytes(B, Hq, Hkv, d), st,
+                        [&](void *ws) {
+                          return plx::launch_paged_rows(c, q, r, row, d, seqlens, nullptr, out, row,
+                                                        d, nullptr, B, Hq, ws, st);
+                        });
 }
 
 size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d) {

@@ -224,6 +224,28 @@ def test_scales_of_all_sizes(fp8):
     ref.assert_within(out, o, bound, "prefill")
 
 
+def test_subnormal_codes_are_not_flushed():
+    """Rows whose scale is set by one element, all others e4m3 subnormals:
+    the bound is relative to each dimension's own values."""
+    dev = device()
+    n = 90
+    g = torch.Generator().manual_seed(3)
+    k = torch.randint(-7, 8, (n, 1, 128), generator=g).double().numpy() * 2.0 ** -9
+    v = torch.randint(-7, 8, (n, 1, 128), generator=g).double().numpy() * 2.0 ** -9
+    k[:, :, 0] = v[:, :, 0] = 448.0
+    pool = ref.Pool([n], 1, 16, True, 3)
+    pool.put(0, 0, k, v)
+    q, r = ref.normal_rows(1, 4, 1, 300.0), ref.normal_rows(1, 4, 2, 10.0)
+    q[:, :, 0] = r[:, :, 0] = 0
+    o, _, bound = ref.reference(pool, q, r, [1])
+    kw = dict(seqlens=pool.seqlens.to(dev), **pool.to(dev))
+    out = plx_decode_fwd_paged(q.to(dev), r.to(dev), **kw)
+    ref.assert_within(out, o, bound, "decode")
+    out, _ = plx_prefill_fwd_paged(q.to(dev), r.to(dev), cu_q=ends([1]).to(dev), **kw)
+    plx_check_device_error()
+    ref.assert_within(out, o, bound, "prefill")
+
+
 # ------------------------------------------------------------ prefill
 PREFILL = [
     # lens, counts, Hq, Hkv, page, rows behind
