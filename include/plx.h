@@ -268,8 +268,8 @@ int plx_decode_default_nsplit(int B, int Hkv);
  *                    16, 32, 64, 128 or 256; d must be 128.
  *   kscale, vscale : uint8 [num_pages, Hkv, page_size], both or neither. A row
  *                    of codes stands for code * 2^(E - 127), E its byte in
- *                    1 .. 254 (a row with E = 0 counts as zeros). Attention over
- *                    e4m3 pages wants |q|, |r| < 2^63 and |v| < 2^70.
+ *                    1 .. 254 (E = 0 only for rows of zeros). Attention over e4m3
+ *                    pages wants |v| < 2^70.
  *   block_table    : int32 [B, max_pages] on the device. Position p of sequence
  *                    b is in slot p % page_size of page
  *                    block_table[b, p / page_size]. Entries behind a sequence's

@@ -3,10 +3,16 @@
 // partial records. One new token a sequence is decode; a handful (drafted
 // tokens to be checked) is the same kernel with more query rows.
 //
-// The mathematics and the tensor-core form are decode.cu's: A rows 0..7 of
-// an m16n8k16 product are eight query rows' q, rows 8..15 their probes r, so
-// one product per 16 dims gives s = q.k and t = r.k of the same key in the same
-// thread, and P, P o T are the A operand of the value product. What differs:
+// The streaming form is decode.cu's: s = q.k and t = r.k of a key from the same
+// products, P = exp(s) and P o T against the same value rows, one running max.
+// Here the KEYS are the M rows of the m16n8k16 products and the query rows the
+// N columns, column 2 h the query q_h and 2 h + 1 its probe r_h (NB blocks of
+// four query rows): S^T = K [q r], then O^T = V^T [P, P o T], whose
+// operand is S^T's own registers after one 8x8 transpose. Compared with the
+// queries as rows this halves the products, the accumulators and the softmax
+// work for the usual one to four query heads a kv head, whose rows would
+// leave most of an M of 16 idle; that is what lets e4m3 pages, at twice the
+// keys a byte, keep up with the memory.
 //   - Query rows. The n_b G rows (token, query head of the group) of a sequence
 //     and kv head are taken eight at a time as row groups; each group streams
 //     the keys for itself (the groups of a kv head run side by side and share
@@ -14,21 +20,26 @@
 //   - Pages. The stream is counted in tiles of KT keys, which never cross a
 //     page of a multiple of KT keys (page_size 16 gives two boxes a tile of 32).
 //     A (page, kv head) block is contiguous, so a tile is one 4 KB TMA box of
-//     K and one of V. The producer warp reads 32 page numbers ahead.
+//     K and one of V.
 //   - Slots behind the last key. The last tile of a sequence reads the rest of
 //     its page, which may hold anything: scores are masked by selection, and
 //     the V rows are zeroed in registers (0 x NaN would reach the sums).
-//   - e4m3 pages. A code's bits placed in a bf16 (sign, then the 7 magnitude
-//     bits over exponent and mantissa) are its value times 2^-120, exactly,
-//     subnormals included: three or four integer instructions for two codes
-//     and no conversion unit. q and r carry 2^64 to make up for half of it
-//     and the weights another 2^64, powers of two that the scores and the
-//     records take off again; the row scales 2^(E - 127) are applied to the
-//     scores (K) and to the weights (V), so they never touch the codes. The
-//     limits that follow, |q|, |r| < 2^63 and |v| < 2^70, are far outside any
-//     network's values. ldmatrix moves pairs of bytes: dims and keys pair up
-//     differently than for bf16, and the query fragments and output columns are
-//     permuted to match.
+//   - e4m3 pages. The row scales 2^(E - 127) are applied to the scores (K) and
+//     to the weights (V), never to the codes; every lane loads the two bytes
+//     of one key of the warp's next tile while it works on this one (as 32-byte
+//     bulk copies they alone held the stream at 5.2 TB/s). K codes become fp16
+//     (exact, one conversion for two codes) and meet q and r in fp16, each
+//     query row scaled by the power of two that puts its largest element into
+//     [2^14, 2^15): a bf16 value is exact in fp16 down to 2^-31 of that, below
+//     what the fp32 sum of the products keeps. V codes become bf16, whose
+//     range the weights need: a code's bits under a sign-extended shift
+//     (sign, then the 7 magnitude bits over exponent and mantissa) are its
+//     value times 2^-120, exactly, subnormals included, in three integer
+//     instructions for two codes; the weights carry 2^64 and the records the
+//     other 2^56. The limit that follows, |v| < 2^70, is far outside any
+//     network's values. ldmatrix moves pairs of bytes: dims pair up differently
+//     than for bf16, and the query fragments and output rows are permuted to
+//     match.
 #include <math.h>
 #include <string.h>
 
@@ -42,24 +53,23 @@ constexpr int NCW = 4;          // consumer warps
 constexpr int GMAX = 8;         // query rows of a group
 constexpr int NST = 2 * NCW;    // ring stages; tile i goes to warp i % NCW and stage i % NST
 constexpr int THREADS = 32 * (NCW + 1);
+constexpr int RS = D + 8;       // floats of a row of partials in shared memory (bank spread)
 constexpr int REC = 2 * D + 2;  // floats of a record: O1 / l, O2 / l, sigma / l, log2-sum-exp
-constexpr float kUp = 18446744073709551616.f;  // 2^64: the queries' and the weights' part of 2^120
+constexpr float k2p56 = 72057594037927936.f;  // 2^56 = 2^120 / 2^64
 
-// Keys of a tile and bytes of a stage: K rows, V rows (8 KB together), and the
-// scales of both for e4m3. The stages sit first in shared memory: the
-// 128-byte-swizzled boxes need 1024-byte alignment.
-template <bool FP8>
-struct Cfg {
-  static constexpr int KT = FP8 ? 32 : 16;
-  static constexpr int TILE = 4096;  // one tensor's rows
-  static constexpr int OFF_SC = NST * 2 * TILE;
-  static constexpr int SC = FP8 ? 2 * KT : 0;  // scale bytes of a stage
-  static constexpr int OFF_MLS = OFF_SC + NST * SC;
-  static constexpr int OFF_BAR = OFF_MLS + NCW * GMAX * 3 * 4;
-  static constexpr int OFF_FLAG = OFF_BAR + 2 * NST * 8;
-  static constexpr int OFF_PLAN = OFF_FLAG + 16;
-  static constexpr int OFF_RED = OFF_PLAN + 64;
-};
+// Shared memory. The stages (K rows and V rows of a tile, 4 KB each) come
+// first: the 128-byte-swizzled boxes need 1024-byte alignment.
+constexpr int TILE = 4096;
+constexpr int OFF_MLS = NST * 2 * TILE;
+constexpr int OFF_BAR = OFF_MLS + NCW * GMAX * 3 * 4;
+constexpr int OFF_FLAG = OFF_BAR + 2 * NST * 8;
+constexpr int OFF_PLAN = OFF_FLAG + 16;
+constexpr int OFF_RED = OFF_PLAN + 64;
+static_assert(NST % NCW == 0, "each stage must belong to one consumer warp");
+constexpr size_t rows_smem(int gs) { return OFF_RED + size_t(NCW) * gs * RS * 4 + 1024; }
+// CTAs of an SM: with one block of columns three fit its registers (128 a
+// thread) and shared memory, with two blocks two.
+constexpr int ctas_per_sm(int nb) { return nb == 1 ? 3 : 2; }
 
 struct RowsArgs {
   PagedCache c;
@@ -164,27 +174,69 @@ __device__ __forceinline__ uint32_t swz(int row, int c) {
   return (c >> 3) * 2048 + row * 128 + ((((c & 7) ^ (row & 7))) << 4);
 }
 
-// Codes 0, 2 (even) and 1, 3 (odd) of a word as bf16 pairs, times 2^-120.
+// Bytes of w by the selector's nibbles; a nibble's top bit takes the sign.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t prmt(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "n"(SEL));
+  return r;
+}
+// Codes 0, 2 (even) and 1, 3 (odd) of a word as bf16 pairs, times 2^-120: each
+// byte sign-extended to 16 bits, shifted to put the magnitude over the low
+// exponent and the high mantissa bits; the mask drops the sign's copies.
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-  return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+  return (prmt<0xa280>(w) << 4) & 0x87f087f0u;
 }
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
-  return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  return (prmt<0xb391>(w) << 4) & 0x87f087f0u;
 }
+// The two codes of a half word as fp16.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t r;
+  memcpy(&r, &h, 4);
+  return r;
+}
+// D(16x8, f32) += A(16x16, f16, row) * B(16x8, f16, col)
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Thread (g, tq) of a warp gives row g, columns 2 tq and 2 tq + 1 of an 8x8
+// matrix and gets column g, rows 2 tq and 2 tq + 1.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// The exponent a of the power of two that brings a row's largest magnitude m
+// into [2^14, 2^15) (at most 126: a smaller row stays smaller).
+__device__ __forceinline__ int row_shift(float m) {
+  return min(14 + 127 - static_cast<int>(__float_as_uint(m) >> 23), 126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-template <bool FP8>
-__global__ void __launch_bounds__(THREADS, 2)
+template <bool FP8, int NB>
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const RowsArgs a) {
-  using C = Cfg<FP8>;
-  constexpr int KT = C::KT;
+  constexpr int KT = FP8 ? 32 : 16;  // keys of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
   uint64_t *empty = full + NST;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
-  Plan *plan = reinterpret_cast<Plan *>(smem + C::OFF_PLAN);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_FLAG);
+  Plan *plan = reinterpret_cast<Plan *>(smem + OFF_PLAN);
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -283,72 +335,66 @@ __global__ void __launch_bounds__(THREADS, 2)
 
   if (warp == NCW) {
     // ------------------------------------------------------------ producer
-    // The whole warp walks the items (32 page numbers at a time); lane 0 waits
-    // and issues. A page number that does not exist is reported, and its box
-    // starts behind the pool, where TMA fills zeros.
+    // One thread; its time a tile bounds the stream, so it reads each page
+    // number one page ahead and keeps what does not change. A page number
+    // that does not exist is reported, and its box starts behind the pool,
+    // where TMA fills zeros, as do boxes behind the sequence's last key.
     if (lane == 0) {
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
-    }
-    constexpr int PARTS = KT / 16;  // page numbers of a tile for page_size 16, else used once
-    const int boxes = PARTS > 1 && a.c.page_shift == 4 ? PARTS : 1;
-    const int per = KT / boxes;  // keys of a box
-    Walk<KT> wk(pl, a);
-    Item it;
-    int g = 0;
-    bool ok = true;
-    while (ok && wk.next(it, a)) {
-      const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-      const int nbox = (it.t1 - it.t0) * boxes;
-      int held = 0;
-      for (int x = 0; x < nbox && ok; x += boxes, ++g) {
-        if ((x & 31) == 0) {
-          const int key = it.t0 * KT + (x + lane) * per;
-          int page = a.c.num_pages;  // boxes behind the last key read nothing
-          if (x + lane < nbox && key < it.s.len) {
-            page = table[key >> a.c.page_shift];
-            if (page < 0 || page >= a.c.num_pages) {
-              page = a.c.num_pages;
-              if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+      const int shift = a.c.page_shift, mask = (1 << shift) - 1;
+      const int per = KT > mask + 1 ? 16 : KT;  // keys of a box, as in the map
+      const int beyond = a.c.num_pages * a.c.Hkv;
+      Walk<KT> wk(pl, a);
+      Item it;
+      int g = 0;
+      bool ok = true;
+      while (ok && wk.next(it, a)) {
+        const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+        int key = it.t0 * KT;
+        const int end = it.t1 * KT;
+        int next = table[key >> shift];  // t0's tile holds a key
+        int z = beyond;
+        bool fresh = true;
+        while (key < end) {
+          const int st = g % NST;
+          if (g >= NST && !mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full[st]);
+          const uint32_t kb = smem_u32(smem + st * 2 * TILE);
+          mbar_arrive_expect_tx(bar, 2 * TILE);
+#pragma unroll 1
+          for (int y = 0; y < KT; y += per, key += per) {
+            const int slot = key & mask;
+            if (slot == 0 || fresh) {
+              fresh = false;
+              z = beyond;
+              if (key < it.s.len) {
+                if (next >= 0 && next < a.c.num_pages) z = next * a.c.Hkv + it.kvh;
+                else if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+                const int ahead = (key | mask) + 1;
+                if (ahead < min(end, it.s.len)) next = table[ahead >> shift];
+              }
+            }
+            const uint32_t dst = kb + y * 128;
+            if constexpr (FP8) {
+              tma_load_3d(dst, &tm_k, 0, slot, z, bar);
+              tma_load_3d(dst + TILE, &tm_v, 0, slot, z, bar);
+            } else {
+              tma_load_4d(dst, &tm_k, 0, slot, z, 0, bar);
+              tma_load_4d(dst + TILE, &tm_v, 0, slot, z, 0, bar);
             }
           }
-          held = page;
-        }
-        const int st = g % NST;
-        if (lane == 0 && g >= NST) ok = mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&full[st]);
-        const uint32_t kb = smem_u32(smem + st * 2 * C::TILE), vb = kb + C::TILE;
-        if (lane == 0) mbar_arrive_expect_tx(bar, 2 * C::TILE + C::SC);
-        for (int y = 0; y < boxes; ++y) {
-          const int page = __shfl_sync(0xffffffffu, held, (x + y) & 31);
-          if (lane != 0) continue;
-          const int key = it.t0 * KT + (x + y) * per;
-          const int slot = key & ((1 << a.c.page_shift) - 1);
-          // page == num_pages lies behind the map's last row: zero fill.
-          const int z = page * a.c.Hkv + (page < a.c.num_pages ? it.kvh : 0);
-          if constexpr (FP8) {
-            tma_load_3d(kb + y * per * 128, &tm_k, 0, slot, z, bar);
-            tma_load_3d(vb + y * per * 128, &tm_v, 0, slot, z, bar);
-            // The scales of a box that does not exist are not used: any
-            // valid address will do.
-            const long long row =
-                page < a.c.num_pages ? (static_cast<long long>(z) << a.c.page_shift) + slot : 0;
-            const uint32_t sc = smem_u32(smem + C::OFF_SC + st * C::SC) + y * per;
-            bulk_g2s(sc, a.c.kscale + row, per, bar);
-            bulk_g2s(sc + KT, a.c.vscale + row, per, bar);
-          } else {
-            tma_load_4d(kb, &tm_k, 0, slot, z, 0, bar);
-            tma_load_4d(vb, &tm_v, 0, slot, z, 0, bar);
-          }
+          ++g;
         }
       }
-    }
-    if (!ok && lane == 0) {
-      // Let this thread's own copies (tiles g - NST .. g - 1) land first.
-      for (int t = max(0, g - NST); t < g; ++t)
-        mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
+      if (!ok) {
+        // Let this thread's own copies (tiles g - NST .. g - 1) land first.
+        for (int t = max(0, g - NST); t < g; ++t)
+          mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
+      }
     }
     return;
   }
@@ -358,257 +404,329 @@ __global__ void __launch_bounds__(THREADS, 2)
   // after an abort, so the named barrier is always complete.
   const int g = lane >> 2, tq = lane & 3;
   const int gs = a.gs;
-  float *red = reinterpret_cast<float *>(smem + C::OFF_RED);  // [NCW][2 gs][D]
-  float *mls = reinterpret_cast<float *>(smem + C::OFF_MLS);  // [NCW][GMAX][3]
-  const float sc_s = FP8 ? a.scale_log2 * 72057594037927936.f : a.scale_log2;  // 2^56 = 2^(120 - 64)
+  constexpr int MT = KT / 16;  // m tiles of 16 keys
+  float *red = reinterpret_cast<float *>(smem + OFF_RED);  // [NCW][gs][RS]
+  float *mls = reinterpret_cast<float *>(smem + OFF_MLS);  // [NCW][GMAX][3]
   Walk<KT> wk(pl, a);
   Item it;
   int gt = 0;  // tiles of the previous items
   while (wk.next(it, a)) {
     const int nt = it.t1 - it.t0;
     const int r0 = it.grp * GMAX, nr = min(GMAX, it.s.n * a.G - r0);  // this group's rows
-    const bool live = g < nr;
-    const int tok = (r0 + (live ? g : 0)) / a.G;  // token of row g among the sequence's new ones
-    const int last = it.s.len - it.s.n + tok;     // the last key that it sees (< 0: none)
-    // Keys up to here are seen by every row of the group.
-    const int all_see = it.s.len - it.s.n + r0 / a.G;
-    float acc[16][4];
-    float m = -INFINITY, l = 0.f, sg = 0.f;
+    const int t_first = (warp - gt % NCW + NCW) % NCW;
+    // The scale bytes of key `lane` of the warp's tiles, one tile ahead, and
+    // the page number of the tile after it.
+    const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+    auto page_of = [&](int t) {
+      const int key = (it.t0 + t) * KT + lane;
+      return t < nt && key < it.s.len ? table[key >> a.c.page_shift] : -1;
+    };
+    auto scales_of = [&](int t, int page) -> uint32_t {
+      if (page < 0 || page >= a.c.num_pages) return 0u;
+      const int key = (it.t0 + t) * KT + lane;
+      const long long row = ((static_cast<long long>(page) * a.c.Hkv + it.kvh) << a.c.page_shift) +
+                            (key & ((1 << a.c.page_shift) - 1));
+      return a.c.kscale[row] | (static_cast<uint32_t>(a.c.vscale[row]) << 8);
+    };
+    uint32_t sc_next = 0u;
+    int page_next = -1;
+    if constexpr (FP8) {
+      sc_next = scales_of(t_first, page_of(t_first));
+      page_next = page_of(t_first + NCW);
+    }
+    // Column g of block nb is q (even g) or r (odd g) of row 4 nb + g / 2;
+    // this thread's scores are those of row 4 nb + tq.
+    uint32_t qb[NB][8][2];
+    float fs[NB], ft[NB];  // what the scores and the probe products still lack
+    int last[NB];          // the last key that row 4 nb + tq sees (< 0: none)
+    const int all_see = it.s.len - it.s.n + r0 / a.G;  // keys up to here are seen by all rows
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    uint32_t qa[8][4];
-    {
-      const int h = it.kvh * a.G + (r0 + (live ? g : 0)) % a.G;
-      const long long row = static_cast<long long>(it.s.first + tok) * a.qts + h * a.qhs;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = 4 * nb + (g >> 1);
+      const bool live = row < nr;
+      const int tok = (r0 + (live ? row : 0)) / a.G, h = it.kvh * a.G + (r0 + (live ? row : 0)) % a.G;
+      const __nv_bfloat16 *src = ((g & 1) ? a.r : a.q) + (it.s.first + tok) * a.qts + h * a.qhs;
+      fs[nb] = a.scale_log2;
+      ft[nb] = 1.f;
+      if constexpr (FP8) {
+        // Slots 2 tq, 2 tq + 1 hold dims 4 tq, 4 tq + 1 and slots + 8 dims
+        // 4 tq + 2, 4 tq + 3 of the 16, as the codes' words do.
+        uint2 x[8];
+        float mx = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        if constexpr (FP8) {
-          // Slots 2 tq, 2 tq + 1 hold dims 4 tq, 4 tq + 2 and slots + 8 dims
-          // 4 tq + 1, 4 tq + 3 of the 16, as the codes' pairs do; times 2^64.
-          const uint2 x = live ? *reinterpret_cast<const uint2 *>(a.q + row + 16 * kk + 4 * tq) : make_uint2(0u, 0u);
-          const uint2 y = live ? *reinterpret_cast<const uint2 *>(a.r + row + 16 * kk + 4 * tq) : make_uint2(0u, 0u);
-          qa[kk][0] = pack_bf16x2(bf16lo(x.x) * kUp, bf16lo(x.y) * kUp);
-          qa[kk][1] = pack_bf16x2(bf16lo(y.x) * kUp, bf16lo(y.y) * kUp);
-          qa[kk][2] = pack_bf16x2(bf16hi(x.x) * kUp, bf16hi(x.y) * kUp);
-          qa[kk][3] = pack_bf16x2(bf16hi(y.x) * kUp, bf16hi(y.y) * kUp);
-        } else {
-          const uint32_t *qr = reinterpret_cast<const uint32_t *>(a.q + row);
-          const uint32_t *rr = reinterpret_cast<const uint32_t *>(a.r + row);
-          qa[kk][0] = live ? qr[8 * kk + tq] : 0u;
-          qa[kk][1] = live ? rr[8 * kk + tq] : 0u;
-          qa[kk][2] = live ? qr[8 * kk + 4 + tq] : 0u;
-          qa[kk][3] = live ? rr[8 * kk + 4 + tq] : 0u;
+        for (int kk = 0; kk < 8; ++kk) {
+          x[kk] = live ? *reinterpret_cast<const uint2 *>(src + 16 * kk + 4 * tq) : make_uint2(0u, 0u);
+          mx = fmax3(mx, fmaxf(fabsf(bf16lo(x[kk].x)), fabsf(bf16hi(x[kk].x))),
+                     fmaxf(fabsf(bf16lo(x[kk].y)), fabsf(bf16hi(x[kk].y))));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int up = row_shift(mx);
+        const float u = pow2(up), back = pow2(-up);
+        fs[nb] *= __shfl_sync(0xffffffffu, back, 8 * tq);      // column 2 tq
+        ft[nb] *= __shfl_sync(0xffffffffu, back, 8 * tq + 4);  // column 2 tq + 1
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          qb[nb][kk][0] = pack_f16x2(bf16lo(x[kk].x) * u, bf16hi(x[kk].x) * u);
+          qb[nb][kk][1] = pack_f16x2(bf16lo(x[kk].y) * u, bf16hi(x[kk].y) * u);
+        }
+      } else {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          qb[nb][kk][0] = live ? w[8 * kk + tq] : 0u;
+          qb[nb][kk][1] = live ? w[8 * kk + 4 + tq] : 0u;
         }
       }
+      const int mine = 4 * nb + tq;
+      last[nb] = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
     }
-    for (int t = (warp - gt % NCW + NCW) % NCW; t < nt; t += NCW) {
+    // acc[nb][c]: O1, O2 of row 4 nb + tq at the chunk's dims g and g + 8
+    // (e4m3: 2 g and 2 g + 1).
+    float acc[NB][8][4], m[NB], l[NB], sg[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb] = -INFINITY;
+      l[nb] = sg[nb] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
+    }
+    for (int t = t_first; t < nt; t += NCW) {
       const int gi = gt + t, st = gi % NST;
+      const uint32_t sc = sc_next;
+      if constexpr (FP8) {
+        sc_next = scales_of(t + NCW, page_next);
+        page_next = page_of(t + 2 * NCW);
+      }
       bool ok = false;
       if (lane == 0) ok = !ab.raised() && mbar_wait(smem_u32(&full[st]), (gi / NST) & 1, ab);
       if (!__shfl_sync(0xffffffffu, ok, 0)) continue;  // aborting: skip the tile
-      const uint32_t kb = smem_u32(smem + st * 2 * C::TILE), vb = kb + C::TILE;
+      const uint32_t kb = smem_u32(smem + st * 2 * TILE), vb = kb + TILE;
       const int key0 = (it.t0 + t) * KT;
-      constexpr int NT = KT / 8;  // n tiles of 8 keys
-      float cc[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) cc[n][0] = cc[n][1] = cc[n][2] = cc[n][3] = 0.f;
+      // cc[nb][mt][0..1]: s and t of key 16 mt + g, [2..3]: of key 16 mt + 8 + g.
+      float cc[NB][MT][4];
+      const int arow = (lane & 7) + 8 * ((lane >> 3) & 1), acol = lane >> 4;
       if constexpr (FP8) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {  // 64 dims: four chunks of 16
-            uint32_t w[4];
-            const int row = 8 * n + (lane & 7);
-            ldsm_x4(kb + swz(row, 4 * hh + (lane >> 3)), w[0], w[1], w[2], w[3]);
+          for (int mt = 0; mt < MT; ++mt) cc[nb][mt][0] = cc[nb][mt][1] = cc[nb][mt][2] = cc[nb][mt][3] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma_bf16_16816(cc[n], qa[4 * hh + e], codes_even(w[e]), codes_odd(w[e]));
-          }
+        for (int cp = 0; cp < 4; ++cp) {  // two chunks of 16 dims
+          uint32_t w[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            ldsm_x4(kb + swz(16 * mt + arow, 2 * cp + acol), w[mt][0], w[mt][1], w[mt][2], w[mt][3]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint32_t a0 = w[mt][2 * e], a1 = w[mt][2 * e + 1];
+              const uint32_t af[4] = {codes_f16(a0), codes_f16(a1), codes_f16(a0 >> 16), codes_f16(a1 >> 16)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma_f16_16816(cc[nb][mt], af, qb[nb][2 * cp + e][0], qb[nb][2 * cp + e][1]);
+            }
         }
-      } else {
-        const int krow = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(kb + swz(krow, 2 * kk + ((lane >> 3) & 1)), b0, b1, b2, b3);
-          mma_bf16_16816(cc[0], qa[kk], b0, b1);
-          mma_bf16_16816(cc[1], qa[kk], b2, b3);
-        }
-      }
-      // cc[n][0..1]: s of keys 8 n + 2 tq + {0, 1}; cc[n][2..3]: t of the same keys.
-      float vs[NT][2];  // e4m3: the weights' factor 2^(E_v - 127 + 64)
-      if constexpr (FP8) {
-        const uint8_t *sc = smem + C::OFF_SC + st * C::SC;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t ek = *reinterpret_cast<const uint16_t *>(sc + 8 * n + 2 * tq);
-          const uint32_t ev = *reinterpret_cast<const uint16_t *>(sc + KT + 8 * n + 2 * tq);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t k8 = (ek >> (8 * e)) & 0xffu, v8 = (ev >> (8 * e)) & 0xffu;
-            const float f = scale_of(k8);
-            cc[n][e] = cc[n][e] * sc_s * f;
-            cc[n][2 + e] = cc[n][2 + e] * 72057594037927936.f * f;
-            vs[n][e] = v8 == 0u ? 0.f : scale_of(min(v8 + 64u, 254u));
-          }
-        }
-      } else {
+            const uint32_t two = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * e + g);
+            const float f = scale_of(two & 0xffu);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          cc[n][0] *= sc_s;
-          cc[n][1] *= sc_s;
+            for (int nb = 0; nb < NB; ++nb) {
+              cc[nb][mt][2 * e] *= fs[nb] * f;
+              cc[nb][mt][2 * e + 1] *= ft[nb] * f;
+            }
+          }
+      } else {
+        // Two sums over the even and the odd steps, added at the end.
+        float c2[NB][2][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) c2[nb][i][0] = c2[nb][i][1] = c2[nb][i][2] = c2[nb][i][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          uint32_t af[4];
+          ldsm_x4(kb + swz(arow, 2 * kk + acol), af[0], af[1], af[2], af[3]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(c2[nb][kk & 1], af, qb[nb][kk][0], qb[nb][kk][1]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          cc[nb][0][0] = (c2[nb][0][0] + c2[nb][1][0]) * fs[nb];
+          cc[nb][0][1] = c2[nb][0][1] + c2[nb][1][1];
+          cc[nb][0][2] = (c2[nb][0][2] + c2[nb][1][2]) * fs[nb];
+          cc[nb][0][3] = c2[nb][0][3] + c2[nb][1][3];
         }
       }
       if (key0 + KT - 1 > all_see) {
         // Some row does not see all of the tile. Slots behind the sequence's
         // end, which no row sees, may hold anything: select, do not multiply.
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool see = key0 + 8 * n + 2 * tq + e <= last;
-            cc[n][e] = see ? cc[n][e] : -INFINITY;
-            cc[n][2 + e] = see ? cc[n][2 + e] : 0.f;
-            if (FP8) vs[n][e] = see ? vs[n][e] : 0.f;
-          }
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool see = key0 + 16 * mt + 8 * e + g <= last[nb];
+              cc[nb][mt][2 * e] = see ? cc[nb][mt][2 * e] : -INFINITY;
+              cc[nb][mt][2 * e + 1] = see ? cc[nb][mt][2 * e + 1] : 0.f;
+            }
       }
-      float mx = -INFINITY;
+      float alpha[NB];
+      bool moved = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mx = fmax3(mx, cc[n][0], cc[n][1]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m, mx);
-      const float msub = mn == -INFINITY ? 0.f : mn;
-      const float alpha = fast_exp2(m - msub);  // m = -inf: 0
-      float ps = 0.f, pts = 0.f;
-      uint32_t pa[NT], pta[NT];
+      for (int nb = 0; nb < NB; ++nb) {
+        float mx = fmax3(m[nb], cc[nb][0][0], cc[nb][0][2]);
+        if (MT > 1) mx = fmax3(mx, cc[nb][MT - 1][0], cc[nb][MT - 1][2]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        alpha[nb] = mx == -INFINITY ? 1.f : fast_exp2(m[nb] - mx);  // m = -inf: 0
+        moved = moved || alpha[nb] != 1.f;
+        m[nb] = mx;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float p[2], pt[2];
+        for (int nb = 0; nb < NB; ++nb) {
+          l[nb] *= alpha[nb];
+          sg[nb] *= alpha[nb];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[nb][i][0] *= alpha[nb];
+            acc[nb][i][1] *= alpha[nb];
+            acc[nb][i][2] *= alpha[nb];
+            acc[nb][i][3] *= alpha[nb];
+          }
+        }
+      }
+      // The weights as B operands: (p, p t) of a key side by side, transposed
+      // to pairs of keys for the column.
+      uint32_t pb[NB][MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          p[e] = fast_exp2(cc[n][e] - msub);
-          pt[e] = p[e] * cc[n][2 + e];
-          ps += p[e];
-          pts += pt[e];
+          float fv = 1.f;  // e4m3: 2^(E_v - 127 + 64)
           if constexpr (FP8) {
-            p[e] *= vs[n][e];
-            pt[e] *= vs[n][e];
+            const uint32_t two = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * e + g);
+            fv = __uint_as_float(((two >> 8) + 64u) << 23);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float msub = m[nb] == -INFINITY ? 0.f : m[nb];
+            const float p = fast_exp2(cc[nb][mt][2 * e] - msub), pt = p * cc[nb][mt][2 * e + 1];
+            l[nb] += p;
+            sg[nb] += pt;
+            pb[nb][mt][e] = transpose_8x8(FP8 ? pack_bf16x2(p * fv, pt * fv) : pack_bf16x2(p, pt));
           }
         }
-        pa[n] = pack_bf16x2(p[0], p[1]);
-        pta[n] = pack_bf16x2(pt[0], pt[1]);
-      }
-      l = fmaf(l, alpha, ps);
-      sg = fmaf(sg, alpha, pts);
-      m = mn;
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          acc[i][0] *= alpha; acc[i][1] *= alpha; acc[i][2] *= alpha; acc[i][3] *= alpha;
-        }
-      }
-      const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7);
       if constexpr (FP8) {
-        // acc[2 c] and acc[2 c + 1]: the even and the odd dims of chunk c.
 #pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks) {
-          const uint32_t af[4] = {pa[2 * ks], pta[2 * ks], pa[2 * ks + 1], pta[2 * ks + 1]};
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int cp = 0; cp < 4; ++cp) {
-            uint32_t w0, w1, w2, w3;  // chunk 2 cp: keys 0-7, 8-15; chunk 2 cp + 1: the same
-            ldsm_x4_t(vb + swz(16 * ks + vrow, 2 * cp + (lane >> 4)), w0, w1, w2, w3);
-            mma_bf16_16816(acc[4 * cp], af, codes_even(w0), codes_even(w1));
-            mma_bf16_16816(acc[4 * cp + 1], af, codes_odd(w0), codes_odd(w1));
-            mma_bf16_16816(acc[4 * cp + 2], af, codes_even(w2), codes_even(w3));
-            mma_bf16_16816(acc[4 * cp + 3], af, codes_odd(w2), codes_odd(w3));
+            uint32_t w[4];  // chunk 2 cp: keys 0-7, 8-15; chunk 2 cp + 1: the same
+            ldsm_x4_t(vb + swz(16 * mt + arow, 2 * cp + acol), w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t af[4] = {codes_even(w[2 * e]), codes_odd(w[2 * e]), codes_even(w[2 * e + 1]),
+                                      codes_odd(w[2 * e + 1])};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma_bf16_16816(acc[nb][2 * cp + e], af, pb[nb][mt][0], pb[nb][mt][1]);
+            }
           }
-        }
       } else {
-        const uint32_t af[4] = {pa[0], pta[0], pa[1], pta[1]};
+        const int vrow = (lane & 7) + 8 * (lane >> 4), vcol = (lane >> 3) & 1;
         const int valid = it.s.len - key0;  // rows of the tile that hold keys
-        if (valid >= KT) {
+        // Registers 0, 1 hold keys 2 tq, 2 tq + 1, registers 2, 3 keys 8 later.
+        uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
+        if (valid < KT) {
+          k0 = 2 * tq < valid ? (2 * tq + 1 < valid ? 0xffffffffu : 0xffffu) : 0u;
+          k1 = 2 * tq + 8 < valid ? (2 * tq + 9 < valid ? 0xffffffffu : 0xffffu) : 0u;
+        }
 #pragma unroll
-          for (int nd = 0; nd < 8; ++nd) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(vb + swz(vrow, 2 * nd + (lane >> 4)), b0, b1, b2, b3);
-            mma_bf16_16816(acc[2 * nd], af, b0, b1);
-            mma_bf16_16816(acc[2 * nd + 1], af, b2, b3);
-          }
-        } else {
-          // Registers hold keys 2 tq, 2 tq + 1 (b0, b2) and 8 + 2 tq, ...
-          const uint32_t k0 = 2 * tq < valid ? (2 * tq + 1 < valid ? 0xffffffffu : 0xffffu) : 0u;
-          const uint32_t k1 = 2 * tq + 8 < valid ? (2 * tq + 9 < valid ? 0xffffffffu : 0xffffu) : 0u;
+        for (int i = 0; i < 8; ++i) {
+          uint32_t af[4];
+          ldsm_x4_t(vb + swz(vrow, 2 * i + vcol), af[0], af[1], af[2], af[3]);
+          af[0] &= k0;
+          af[1] &= k0;
+          af[2] &= k1;
+          af[3] &= k1;
 #pragma unroll
-          for (int nd = 0; nd < 8; ++nd) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(vb + swz(vrow, 2 * nd + (lane >> 4)), b0, b1, b2, b3);
-            mma_bf16_16816(acc[2 * nd], af, b0 & k0, b1 & k1);
-            mma_bf16_16816(acc[2 * nd + 1], af, b2 & k0, b3 & k1);
-          }
+          for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(acc[nb][i], af, pb[nb][0][0], pb[nb][0][1]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
     }
     gt += nt;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    sg += __shfl_xor_sync(0xffffffffu, sg, 1);
-    sg += __shfl_xor_sync(0xffffffffu, sg, 2);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) {
+        l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], o);
+        sg[nb] += __shfl_xor_sync(0xffffffffu, sg[nb], o);
+      }
 
     // ---------------------------------------------------------- merge warps
-    if (live) {
-      float *o1 = red + (warp * 2 * gs + g) * D;
-      float *o2 = red + (warp * 2 * gs + gs + g) * D;
+    // O1 first, then O2 through the same shared memory.
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int d0 = FP8 ? 16 * (i >> 1) + 4 * tq + (i & 1) : 8 * i + 2 * tq;
-        const int d1 = FP8 ? d0 + 2 : d0 + 1;
-        o1[d0] = acc[i][0];
-        o1[d1] = acc[i][1];
-        o2[d0] = acc[i][2];
-        o2[d1] = acc[i][3];
-      }
-      if (tq == 0) {
-        mls[(warp * GMAX + g) * 3 + 0] = m;
-        mls[(warp * GMAX + g) * 3 + 1] = l;
-        mls[(warp * GMAX + g) * 3 + 2] = sg;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = 4 * nb + tq;
+      if (g == 0 && row < nr) {
+        mls[(warp * GMAX + row) * 3 + 0] = m[nb];
+        mls[(warp * GMAX + row) * 3 + 1] = l[nb];
+        mls[(warp * GMAX + row) * 3 + 2] = sg[nb];
       }
     }
-    consumer_sync();
     const int dim = threadIdx.x;
-    const bool aborted = ab.raised();
-    const float down = FP8 ? 72057594037927936.f : 1.f;  // 2^56: what the codes and weights still lack
-    for (int gh = 0; gh < nr; ++gh) {
-      float M = -INFINITY;
+    const float down = FP8 ? k2p56 : 1.f;
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) M = fmaxf(M, mls[(w * GMAX + gh) * 3]);
-      float *rec = a.recs + ((c + it.vrow) * gs + gh) * REC;
-      if (M == -INFINITY || aborted) {
-        rec[dim] = 0.f;
-        rec[D + dim] = 0.f;
-        if (dim == 0) {
-          rec[2 * D] = 0.f;
-          rec[2 * D + 1] = -INFINITY;
+    for (int ph = 0; ph < 2; ++ph) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int row = 4 * nb + tq;
+        if (row < nr) {
+          float *o = red + (warp * gs + row) * RS;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[16 * i + (FP8 ? 2 * g : g)] = acc[nb][i][ph];
+            o[16 * i + (FP8 ? 2 * g + 1 : g + 8)] = acc[nb][i][2 + ph];
+          }
         }
-        continue;
       }
-      float L = 0.f, S = 0.f, O1 = 0.f, O2 = 0.f;
+      consumer_sync();
+      const bool aborted = ab.raised();
+      {
+        for (int gh = 0; gh < nr; ++gh) {
+          float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) {
-        const float f = fast_exp2(mls[(w * GMAX + gh) * 3] - M);
-        L = fmaf(f, mls[(w * GMAX + gh) * 3 + 1], L);
-        S = fmaf(f, mls[(w * GMAX + gh) * 3 + 2], S);
-        O1 = fmaf(f, red[(w * 2 * gs + gh) * D + dim], O1);
-        O2 = fmaf(f, red[(w * 2 * gs + gs + gh) * D + dim], O2);
+          for (int w = 0; w < NCW; ++w) M = fmaxf(M, mls[(w * GMAX + gh) * 3]);
+          float *rec = a.recs + ((c + it.vrow) * gs + gh) * REC;
+          if (M == -INFINITY || aborted) {
+            rec[ph * D + dim] = 0.f;
+            if (dim == 0) rec[2 * D + ph] = ph == 0 ? 0.f : -INFINITY;
+            continue;
+          }
+          float L = 0.f, S = 0.f, O = 0.f;
+#pragma unroll
+          for (int w = 0; w < NCW; ++w) {
+            const float f = fast_exp2(mls[(w * GMAX + gh) * 3] - M);
+            L = fmaf(f, mls[(w * GMAX + gh) * 3 + 1], L);
+            S = fmaf(f, mls[(w * GMAX + gh) * 3 + 2], S);
+            O = fmaf(f, red[(w * gs + gh) * RS + dim], O);
+          }
+          const float inv = 1.f / L;
+          rec[ph * D + dim] = O * inv * down;
+          if (dim == 0) rec[2 * D + ph] = ph == 0 ? S * inv : M + log2f(L);
+        }
       }
-      const float inv = 1.f / L;
-      rec[dim] = O1 * inv * down;
-      rec[D + dim] = O2 * inv * down;
-      if (dim == 0) {
-        rec[2 * D] = S * inv;
-        rec[2 * D + 1] = M + log2f(L);
-      }
+      consumer_sync();  // the next partials overwrite red (and mls)
     }
     if (it.t0 == 0 && dim == 0) {
       // This CTA holds the row's first tile, so it is the first of the CTAs
@@ -618,7 +736,6 @@ __global__ void __launch_bounds__(THREADS, 2)
       const int c_last = static_cast<int>(((x + 1) * pl.n - 1) / pl.W);
       a.meta[it.vrow] = make_int2(static_cast<int>(c + it.vrow), c_last - c + 1);
     }
-    consumer_sync();  // the next item's partials overwrite red and mls
   }
 }
 
@@ -722,27 +839,25 @@ bool make_page_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, con
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
+template <bool FP8, int NB>
 cudaError_t launch_rows(const RowsArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                         cudaStream_t stream) {
   static thread_local unsigned long long configured_ctx = 0;
-  const size_t most = Cfg<FP8>::OFF_RED + size_t(NCW) * 2 * GMAX * D * 4 + 1024;
   const unsigned long long ctx = context_id();
   if (ctx == 0 || configured_ctx != ctx) {
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8>,
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, NB>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(most));
+                                         static_cast<int>(rows_smem(4 * NB)));
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  const size_t smem = Cfg<FP8>::OFF_RED + size_t(NCW) * 2 * a.gs * D * 4 + 1024;
-  paged_rows_kernel<FP8><<<a.nshare, THREADS, smem, stream>>>(mk, mv, a);
+  paged_rows_kernel<FP8, NB><<<a.nshare, THREADS, rows_smem(a.gs), stream>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int paged_rows_shares() { return 2 * sm_count(); }
+int paged_rows_shares(int slot) { return ctas_per_sm(slot > 4 ? 2 : 1) * sm_count(); }
 
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
                               long long qhs, const int *seqlens, const int *cu_q, void *out,
@@ -765,13 +880,15 @@ cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r,
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.T = T;
-  a.nshare = paged_rows_shares();
   a.gs = paged_rows_slot(a.G, cu_q != nullptr);
+  a.nshare = paged_rows_shares(a.gs);
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const long long vrows = paged_rows_vrows(T, c.B, a.G, c.Hkv);
   a.meta = static_cast<int2 *>(workspace);
   a.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + paged_rows_meta_bytes(vrows));
-  cudaError_t e = fp8 ? launch_rows<true>(a, mk, mv, stream) : launch_rows<false>(a, mk, mv, stream);
+  cudaError_t e;
+  if (a.gs <= 4) e = fp8 ? launch_rows<true, 1>(a, mk, mv, stream) : launch_rows<false, 1>(a, mk, mv, stream);
+  else e = fp8 ? launch_rows<true, 2>(a, mk, mv, stream) : launch_rows<false, 2>(a, mk, mv, stream);
   if (e != cudaSuccess) return e;
   CombineArgs k;
   k.c = c;

@@ -114,7 +114,7 @@ cudaError_t launch_paged_attn(const PagedCache &c, const void *q, const void *r,
 // (sequence, kv head, group of 8 query rows), padded to 256 bytes, then
 // (shares + virtual rows) slots of `slot` records of 2 d + 2 floats. CTA c
 // writes its part of virtual row v to slot c + v.
-int paged_rows_shares();
+int paged_rows_shares(int slot);  // CTAs of the split kernel
 inline int paged_rows_slot(int G, bool many) { return many || G > 8 ? 8 : G; }
 inline long long paged_rows_vrows(int T, int B, int G, int Hkv) {
   return (static_cast<long long>(T) * G / 8 + B) * Hkv;
@@ -122,8 +122,9 @@ inline long long paged_rows_vrows(int T, int B, int G, int Hkv) {
 inline size_t paged_rows_meta_bytes(long long vrows) { return (size_t(vrows) * 8 + 255) / 256 * 256; }
 inline size_t paged_rows_workspace_bytes(int T, int B, int G, int Hkv, int d, bool many) {
   const long long vrows = paged_rows_vrows(T, B, G, Hkv);
-  return paged_rows_meta_bytes(vrows) + size_t(paged_rows_shares() + vrows) * paged_rows_slot(G, many) *
-                                            (2 * size_t(d) + 2) * sizeof(float);
+  const int slot = paged_rows_slot(G, many);
+  return paged_rows_meta_bytes(vrows) +
+         size_t(paged_rows_shares(slot) + vrows) * slot * (2 * size_t(d) + 2) * sizeof(float);
 }
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
                               long long qhs, const int *seqlens, const int *cu_q, void *out,

@@ -59,7 +59,7 @@ __device__ __forceinline__ int row_sequence(const int *cu, int B, int t) {
   return cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
 }
 
-// 2^(E - 127) (0 for the unused E = 0).
+// 2^(E - 127), 1 <= E <= 254.
 __device__ __forceinline__ float scale_of(uint32_t E) { return __uint_as_float(E << 23); }
 
 // Two e4m3 codes (low byte first) as fp32.
