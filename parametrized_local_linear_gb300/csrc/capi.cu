@@ -479,6 +479,10 @@ plx_status check_strides(const char *fn, const char *what, long long token, long
   return PLX_OK;
 }
 
+// Whether a prefill call has so few query rows a sequence that the kernel that
+// streams keys for eight rows at a time takes it.
+bool few_rows(int T, int B, int G) { return static_cast<long long>(T) * G <= 8ll * B; }
+
 plx_status check_heads(const char *fn, int Hq, int Hkv) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
     return fail(PLX_ERR_INVALID_ARG, "%s: Hq (%d) must be a positive multiple of Hkv (%d)", fn, Hq, Hkv);
@@ -577,7 +581,8 @@ plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages
 
 size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d) {
   if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
-  return 16;
+  return few_rows(T, B, Hq / Hkv) ? plx::paged_rows_workspace_bytes(T, B, Hq / Hkv, Hkv, d, true)
+                                  : plx::paged_prefill_workspace_bytes();
 }
 
 plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_token_stride,
@@ -612,11 +617,18 @@ plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_toke
   if (static_cast<long long>(T) * Hq > 0x7fffffffLL)
     return fail(PLX_ERR_UNSUPPORTED, "%s: problem too large for one launch", fn);
   c.err = plx::device_error_word();
-  return finish_launch(
-      plx::launch_paged_attn(c, q, r, qr_token_stride, qr_head_stride, seqlens, cu_q, out,
-                             out_token_stride, out_head_stride, lse, T, Hq,
-                             static_cast<cudaStream_t>(stream)),
-      fn);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_workspace(fn, workspace, plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d), st,
+                        [&](void *ws) {
+                          return few_rows(T, B, Hq / Hkv)
+                                     ? plx::launch_paged_rows(c, q, r, qr_token_stride, qr_head_stride,
+                                                              seqlens, cu_q, out, out_token_stride,
+                                                              out_head_stride, lse, T, Hq, ws, st)
+                                     : plx::launch_paged_prefill(c, q, r, qr_token_stride,
+                                                                 qr_head_stride, seqlens, cu_q, out,
+                                                                 out_token_stride, out_head_stride,
+                                                                 lse, T, Hq, ws, st);
+                        });
 }
 
 plx_status plx_check_device_error(void *stream) {

@@ -1,0 +1,1030 @@
+// Causal Parallax prefill of a ragged batch of chunks over a paged KV cache, on
+// the 5th-generation tensor cores (tcgen05, TMEM, TMA), d = 128.
+//
+// The tile mathematics is prefill_tc.cu's: per 64 keys S = Q K^T, T = R K^T,
+// O1 += P V, O2 += (P o T) V with one running max, the weights handed from the
+// softmax warps to the value products through tensor memory in two halves, four
+// threads issuing, O drained by an epilogue of its own. What differs:
+//   - Rows. A tile's 128 rows are TQ = floor(128 / G) tokens x the G query heads
+//     of one kv head (row = token * G + head), so a short chunk of a grouped
+//     model fills more of them, and K and V are read once for all G heads. Q and
+//     R come in one TMA box {64 dims, G heads, TQ tokens} a half, from any
+//     strides.
+//   - Work. The key tiles of all (sequence, kv head, row tile) items form one
+//     stream that is cut into equal shares, one CTA each; the causal lengths
+//     of the items need no evening out, and few long items are split over the
+//     keys. A CTA whose share starts or ends inside an item writes that part's
+//     raw O1, O2, m, l, sigma (fp32) to the workspace, and a second kernel
+//     merges the parts. Lengths live on the device, so each CTA finds its share
+//     itself: the tiles of the first t row tiles of a chunk are a sum of
+//     floor((a + i TQ) / 64), evaluated in closed form.
+//   - Pages. A key tile is 64 / page_size boxes (one for larger pages). Slots
+//     behind the last key may hold anything: S and T are masked by selection,
+//     and in the one tile that reaches them the softmax warps zero the V rows
+//     in shared memory before they hand P over (0 x NaN would reach O).
+//   - e4m3 pages. Raw tiles (8 KB K, 8 KB V) land in a ring of their own; four
+//     converter warps turn them into the bf16 tiles of the products: a code's
+//     bits under a sign-extended shift are a bf16 of its value times 2^-120
+//     (subnormals included), and one packed multiplication by 2^(E - 7) makes
+//     it the stored value, exactly.
+//
+// Warps: 0..3 softmax, 4..7 epilogue, 8 O1, 9 O2, 10 S (and the Q, R loads),
+// 11 T; bf16: 12 loads K and V; e4m3: 12..15 convert, warp 12 also loads.
+// Tensor memory as in prefill_tc.cu.
+#include <math.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "plx_paged.cuh"
+
+namespace plx {
+namespace {
+
+constexpr int D = 128;
+constexpr int BM = 128;  // rows of an item
+constexpr int BN = 64;   // keys of a tile
+constexpr int HALF_Q = BM * 64 * 2;
+constexpr int HALF_KV = BN * 64 * 2;
+constexpr int TILE_KV = 2 * HALF_KV;  // 16 KB: a bf16 K or V tile
+constexpr int RAW = BN * D;           // 8 KB: an e4m3 K or V tile
+constexpr int NRAW = 3;
+constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_T = 64, COL_O1 = 256, COL_O2 = 384;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int EP_WARP = 4, O1_WARP = 8, S_WARP = 10, LOAD_WARP = 12;
+
+template <bool FP8>
+struct Cfg {
+  static constexpr int NST = FP8 ? 3 : 4;  // bf16 K and V stages
+  static constexpr int WARPS = FP8 ? 16 : 13;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int OFF_R = 2 * HALF_Q;
+  static constexpr int OFF_K = 4 * HALF_Q;
+  static constexpr int OFF_V = OFF_K + NST * TILE_KV;
+  static constexpr int OFF_RAW = OFF_V + NST * TILE_KV;  // [NRAW][K, V]
+  static constexpr int OFF_STAT = OFF_RAW + (FP8 ? NRAW * 2 * RAW : 0);
+  static constexpr int OFF_OST = OFF_STAT + 2 * 3 * BM * 4;  // per epilogue warp: 32 rows x 64 bytes
+  static constexpr int OFF_PLAN = OFF_OST + 4 * 2048;
+  static constexpr int OFF_BAR = OFF_PLAN + 64;
+  static constexpr int NBAR = 2 + 4 * NST + 2 + 4 + 2 + 4 + 1 + 2 + 4 + (FP8 ? 4 * NRAW : 0);
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
+
+struct Args {
+  PagedCache c;
+  const int *seqlens, *cu;
+  __nv_bfloat16 *out;
+  float *lse;
+  float *parts;  // [2 grid][PART floats]
+  int *table;    // [grid][4] the item that CTA c starts and does not finish
+  long long ots, ohs;
+  int T, Hq, G, TQ, min_units;
+  float scale_log2;
+};
+// A part: [64][128 rows] float4 (O1's 128 columns, then O2's), then m, l, sigma.
+constexpr int PART = 2 * D * BM + 3 * BM;
+
+// ---------------------------------------------------------------- work list
+struct Seq {
+  int len, first, n, nq;  // keys, first packed row, new tokens, row tiles
+};
+__device__ __forceinline__ Seq seq_of(const Args &a, int b) {
+  Seq s;
+  s.len = cache_len(a.c, a.seqlens, b);
+  s.first = a.cu[b];
+  const int end = a.cu[b + 1];
+  s.n = end - s.first;
+  if (s.first < 0 || end > a.T || s.n < 0) {
+    if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+    s.first = s.n = 0;
+  }
+  s.nq = (s.n + a.TQ - 1) / a.TQ;
+  return s;
+}
+// Key tiles of row tile t: up to the last key that its last token sees, at
+// least one (a row tile of padding still writes its zeros).
+__device__ __forceinline__ int tiles_of(const Seq &s, int t, int TQ) {
+  const int seen = s.len - s.n + static_cast<int>(min(static_cast<long long>(t + 1) * TQ, static_cast<long long>(s.n)));
+  return max(1, (seen + BN - 1) / BN);
+}
+// sum over i < n of floor((b + i a) / m), all >= 0, m <= 2^16 (the Euclid-like
+// recursion of lattice-point counting).
+__device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t a, long long b) {
+  long long ans = 0;
+  while (n > 0) {
+    ans += (n - 1) * n / 2 * (a / m);
+    a %= m;
+    ans += n * (b / m);
+    const uint32_t r = static_cast<uint32_t>(b % m);
+    const long long y = static_cast<long long>(a) * n + r;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return ans;
+}
+// Key tiles of the first t row tiles (t <= nq).
+__device__ __forceinline__ long long tiles_before(const Seq &s, int t, int TQ) {
+  if (t <= 0) return 0;
+  long long extra = 0;
+  if (t == s.nq) extra = tiles_of(s, --t, TQ);  // the last row tile may be short
+  // Row tiles i < i0 see at most BN keys: one key tile each.
+  const long long base = static_cast<long long>(s.len) - s.n + TQ + BN - 1;  // i = 0's numerator
+  const long long i0 = base >= 2 * BN ? 0 : min(static_cast<long long>(t), (2 * BN - base + TQ - 1) / TQ);
+  return extra + i0 + floor_sum(t - i0, BN, static_cast<uint32_t>(TQ), max(0ll, base + i0 * TQ));
+}
+
+struct Plan {
+  long long U, s, e;  // key tiles of the batch; this CTA's share [s, e)
+  int n;              // CTAs with work
+  int b, kvh, t, j;   // where the share starts
+};
+
+struct Item {
+  Seq s;
+  int b, kvh, t, j0, j1, nt;
+};
+
+struct Walk {
+  Seq s;
+  long long left;
+  int b, kvh, t, j;
+  bool begun = false;
+  __device__ __forceinline__ Walk(const Plan &p, const Args &a)
+      : s(seq_of(a, p.b)), left(p.e - p.s), b(p.b), kvh(p.kvh), t(p.t), j(p.j) {}
+  __device__ __forceinline__ bool next(Item &it, const Args &a) {
+    if (left <= 0) return false;  // more units left: another item follows, so b stays below B
+    if (begun && ++t == s.nq) {
+      t = 0;
+      if (++kvh == a.c.Hkv) {
+        kvh = 0;
+        do s = seq_of(a, ++b);
+        while (s.nq == 0);
+      }
+    }
+    begun = true;
+    it.s = s;
+    it.b = b;
+    it.kvh = kvh;
+    it.t = t;
+    it.nt = tiles_of(s, t, a.TQ);
+    it.j0 = j;
+    j = 0;
+    it.j1 = static_cast<int>(min(static_cast<long long>(it.nt), it.j0 + left));
+    left -= it.j1 - it.j0;
+    return true;
+  }
+};
+
+// One warp: the CTA's share and where it starts.
+__device__ __forceinline__ void make_plan(const Args &a, Plan *plan, int lane) {
+  const int c = blockIdx.x;
+  long long U = 0;
+  for (int i = lane; i < a.c.B; i += 32) {
+    const Seq s = seq_of(a, i);
+    U += tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), U / a.min_units));
+  Plan p;
+  p.U = U;
+  p.n = static_cast<int>(n);
+  p.s = c < n ? c * U / n : 0;
+  p.e = c < n ? (c + 1) * U / n : 0;
+  p.b = p.kvh = p.t = p.j = 0;
+  if (p.s < p.e) {
+    long long base = 0;
+    for (int i0 = 0; i0 < a.c.B; i0 += 32) {
+      const int i = i0 + lane;
+      long long u = 0;
+      if (i < a.c.B) {
+        const Seq s = seq_of(a, i);
+        u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+      }
+      long long inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, i < a.c.B && base + inc > p.s);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        p.b = i0 + l;
+        base += __shfl_sync(0xffffffffu, inc - u, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const Seq s = seq_of(a, p.b);
+    const long long head = tiles_before(s, s.nq, a.TQ), off = p.s - base;
+    p.kvh = static_cast<int>(off / head);
+    const long long in = off - p.kvh * head;
+    // The last t with tiles_before(t) <= in: 32 candidates a round.
+    int lo = 0, step = s.nq;
+    while (step > 1) {
+      step = (step + 31) / 32;
+      const long long cand = lo + static_cast<long long>(step) * lane;
+      const bool below = cand < s.nq && tiles_before(s, static_cast<int>(cand), a.TQ) <= in;
+      lo += step * (31 - __clz(__ballot_sync(0xffffffffu, below)));
+    }
+    p.t = lo;
+    p.j = static_cast<int>(in - tiles_before(s, lo, a.TQ));
+  }
+  if (lane == 0) *plan = p;
+}
+
+// 4-D tiled load (box and swizzle come from the tensor map).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Codes 0, 1 (lo) and 2, 3 (hi) of a word as bf16 pairs, times 2^-120.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "n"(SEL));
+  return (r << 4) & 0x87f087f0u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
+    paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_r,
+                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const Args a) {
+  using C = Cfg<FP8>;
+  constexpr int NST = C::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  float *stat = reinterpret_cast<float *>(smem + C::OFF_STAT);  // [item parity][m, l, sigma][row]
+  Plan *plan = reinterpret_cast<Plan *>(smem + C::OFF_PLAN);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint64_t *q_full = bars;             // Q and R of the item loaded
+  uint64_t *q_empty = bars + 1;        // the item's last S and T UMMAs done (count 2)
+  uint64_t *k_full = bars + 2;         // bf16: TMA bytes; e4m3: count 4 (a lane per converter warp)
+  uint64_t *k_empty = k_full + NST;    // count 2 (S and T)
+  uint64_t *v_full = k_empty + NST;
+  uint64_t *v_empty = v_full + NST;    // count 2 (O1 and O2)
+  uint64_t *st_full = v_empty + NST;   // [2] count 2
+  uint64_t *p_full = st_full + 2;      // [2][2] count 4: P of keys [32 h, 32 h + 32) of buffer x
+  uint64_t *pv_done = p_full + 4;      // [2] count 2
+  uint64_t *pv_issued = pv_done + 2;   // [2][2]
+  uint64_t *o_free = pv_issued + 4;    // count 4: the epilogue has read O1 and O2
+  uint64_t *stat_full = o_free + 1;    // [2] count 4
+  uint64_t *drain = stat_full + 2;     // [4]
+  uint64_t *rk_full = drain + 4;       // e4m3: [NRAW] raw K loaded
+  uint64_t *rk_empty = rk_full + NRAW; // count 4
+  uint64_t *rv_full = rk_empty + NRAW;
+  uint64_t *rv_empty = rv_full + NRAW;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::NBAR);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == 0) make_plan(a, plan, lane);
+  if (threadIdx.x == 32) {
+    mbar_init(smem_u32(q_full), 1);
+    mbar_init(smem_u32(q_empty), 2);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(smem_u32(&k_full[s]), FP8 ? 4 : 1);
+      mbar_init(smem_u32(&k_empty[s]), 2);
+      mbar_init(smem_u32(&v_full[s]), FP8 ? 4 : 1);
+      mbar_init(smem_u32(&v_empty[s]), 2);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&st_full[x]), 2);
+      mbar_init(smem_u32(&p_full[2 * x]), 4);
+      mbar_init(smem_u32(&p_full[2 * x + 1]), 4);
+      mbar_init(smem_u32(&pv_done[x]), 2);
+      mbar_init(smem_u32(&pv_issued[2 * x]), 1);
+      mbar_init(smem_u32(&pv_issued[2 * x + 1]), 1);
+      mbar_init(smem_u32(&stat_full[x]), 4);
+    }
+    mbar_init(smem_u32(o_free), 4);
+    for (int x = 0; x < 4; ++x) mbar_init(smem_u32(&drain[x]), 1);
+    if (FP8)
+      for (int s = 0; s < NRAW; ++s) {
+        mbar_init(smem_u32(&rk_full[s]), 1);
+        mbar_init(smem_u32(&rk_empty[s]), 4);
+        mbar_init(smem_u32(&rv_full[s]), 1);
+        mbar_init(smem_u32(&rv_empty[s]), 4);
+      }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // Rows that the Q and R boxes do not fill stay zero.
+  if (a.G * a.TQ < BM) {
+    for (int i = threadIdx.x; i < 4 * HALF_Q / 16; i += C::THREADS)
+      st_shared_v4(smem_u32(smem) + i * 16, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Plan pl = *plan;
+  if (pl.s >= pl.e) {  // no share
+    if (threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
+    return;
+  }
+  if (warp == O1_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const Abort ab{abort_flag, a.c.err};
+  const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
+  const int beyond = a.c.num_pages * a.c.Hkv;  // a box there reads nothing: zero fill
+
+  // Row (page, kv head) of the tensor maps of a key of the item; `beyond` for
+  // keys behind its last one and for pages that do not exist (reported).
+  auto page_head = [&](const Item &it, int key) -> int {
+    if (key >= it.s.len) return beyond;
+    const int page = a.c.table[static_cast<long long>(it.b) * a.c.max_pages + (key >> shift)];
+    if (page < 0 || page >= a.c.num_pages) {
+      if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+      return beyond;
+    }
+    return page * a.c.Hkv + it.kvh;
+  };
+  const int box = min(1 << shift, BN);  // keys of a box, as in the maps
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ softmax
+    const int row = warp * 32 + lane;  // row of the item = TMEM lane
+    const uint32_t tl = tbase + (static_cast<uint32_t>(warp * 32) << 16);
+    const float c = a.scale_log2;
+    const int rtok = row / a.G;
+    int g = 0;
+    bool ok = true;
+    Walk wk(pl, a);
+    Item it;
+    for (int k = 0; ok && wk.next(it, a); ++k) {
+      const int pos0 = it.s.len - it.s.n + it.t * a.TQ;  // position of the tile's first token
+      const int pos = pos0 + rtok;                       // the last key that this row sees
+      float m_used = -INFINITY, l = 0.f, sg = 0.f;
+      for (int j = it.j0; j < it.j1; ++j) {
+        const int gg = g + j - it.j0, x = gg & 1;
+        const bool masked = j * BN + BN - 1 > pos0;
+        const int valid = it.s.len - j * BN;  // keys of the tile that exist
+        if (!FP8 && valid < BN) {
+          // The last tile: zero the V rows behind the last key.
+          const int st = gg % NST;
+          ok = mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
+          for (int i = max(valid, 0) * 8 + row; i < BN * 8; i += BM) {
+            st_shared_v4(vb + i * 16, 0u, 0u, 0u, 0u);
+            st_shared_v4(vb + HALF_KV + i * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        ok = mbar_wait(smem_u32(&st_full[x]), (gg >> 1) & 1, ab);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t cs = tl + (x ? COL_S1 : COL_S0);
+        float s[64];
+        tmem_ld32(cs, *reinterpret_cast<float(*)[32]>(&s[0]));
+        tmem_ld32(cs + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            if (j * BN + e > pos) s[e] = -INFINITY;
+        }
+        float mx8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(s[2 * e], s[2 * e + 1]);
+#pragma unroll
+        for (int e = 16; e < BN; e += 2) mx8[(e >> 1) & 7] = fmax3(mx8[(e >> 1) & 7], s[e], s[e + 1]);
+        const float mt =
+            fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * c;
+        const bool need = mt > m_used + kRescaleThreshold;
+        float alpha = 1.f;
+        if (need) {
+          alpha = fast_exp2(m_used - mt);  // m_used = -inf: 0
+          l *= alpha;
+          sg *= alpha;
+          m_used = mt;
+        }
+        if (j > it.j0 && __any_sync(0xffffffffu, need)) {
+          ok = mbar_wait(smem_u32(&pv_done[(gg - 1) & 1]), ((gg - 1) >> 1) & 1, ab);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int part = 0; part < 8; ++part) {
+            const uint32_t col = (part < 4 ? COL_O1 : COL_O2) + (part & 3) * 32;
+            float o[32];
+            tmem_ld32(tl + col, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(tl + col, o);
+          }
+          tmem_wait_st();
+        }
+        const float msub = m_used == -INFINITY ? 0.f : m_used;
+        const uint64_t c2 = f2(c, c), nm2 = f2(-msub, -msub);
+        uint64_t lp[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, sp[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) {
+          float t[16];
+          tmem_ld16(cs + COL_T + 16 * qq, t);
+          tmem_wait_ld();
+          if (masked) {
+            // p = 0 there, but t may be NaN (slots behind the last key).
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (j * BN + 16 * qq + e > pos) t[e] = 0.f;
+          }
+          uint32_t pk[8], ptk[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int col = 16 * qq + e;
+            const uint64_t xx = ffma2(f2(s[col], s[col + 1]), c2, nm2);
+            const uint64_t p = f2(fast_exp2(f2lo(xx)), fast_exp2(f2hi(xx)));
+            const uint64_t pt = fmul2(p, f2(t[e], t[e + 1]));
+            lp[(e >> 1) & 1] = fadd2(lp[(e >> 1) & 1], p);
+            sp[(e >> 1) & 1] = fadd2(sp[(e >> 1) & 1], pt);
+            pk[e >> 1] = pack_bf16x2(p);
+            ptk[e >> 1] = pack_bf16x2(pt);
+          }
+          tmem_st8(cs + 8 * qq, pk);
+          tmem_st8(cs + COL_T + 8 * qq, ptk);
+          if (qq == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * x]));
+          }
+        }
+        const uint64_t lsum = fadd2(lp[0], lp[1]), ssum = fadd2(sp[0], sp[1]);
+        l += f2lo(lsum) + f2hi(lsum);
+        sg += f2lo(ssum) + f2hi(ssum);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * x + 1]));
+      }
+      if (!ok) break;
+      float *st = stat + (k & 1) * 3 * BM;
+      st[row] = m_used;
+      st[BM + row] = l;
+      st[2 * BM + row] = sg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&stat_full[k & 1]));
+      g += it.j1 - it.j0;
+    }
+  } else if (warp < EP_WARP + 4) {
+    // ------------------------------------------------------------ epilogue
+    const int qw = warp & 3;
+    const int row = qw * 32 + lane;
+    const uint32_t tl = tbase + (static_cast<uint32_t>(qw * 32) << 16);
+    const uint32_t stage = smem_u32(smem + C::OFF_OST + qw * 2048);
+    int g = 0;
+    bool cut = false;  // the share ends inside an item that starts in it
+    Walk wk(pl, a);
+    Item it;
+    for (int k = 0; wk.next(it, a); ++k) {
+      const int glast = g + it.j1 - it.j0 - 1;
+      g = glast + 1;
+      bool ok = mbar_wait(smem_u32(&stat_full[k & 1]), (k >> 1) & 1, ab);
+      ok = ok && mbar_wait(smem_u32(&pv_done[glast & 1]), (glast >> 1) & 1, ab);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const float *st = stat + (k & 1) * 3 * BM;
+      const float m_used = st[row], l = st[BM + row], sg = st[2 * BM + row];
+      auto o_read = [&] {  // O has been read: the next item's value UMMAs may overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(o_free));
+      };
+      if (it.j0 != 0 || it.j1 != it.nt) {
+        // A part of an item: raw sums for the merge. The share's first item
+        // goes to slot 0, a later one (its last) to slot 1.
+        const int slot = k == 0 ? 0 : 1;
+        float4 *p4 = reinterpret_cast<float4 *>(a.parts + (2ll * blockIdx.x + slot) * PART);
+#pragma unroll 1
+        for (int part = 0; part < 8; ++part) {
+          float o[32];
+          tmem_ld32(tl + (part < 4 ? COL_O1 : COL_O2) + (part & 3) * 32, o);
+          tmem_wait_ld();
+          if (part == 7) o_read();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            p4[(part * 8 + e) * BM + row] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        float *ps = reinterpret_cast<float *>(p4) + 2 * D * BM;
+        ps[row] = m_used;
+        ps[BM + row] = l;
+        ps[2 * BM + row] = sg;
+        if (it.j0 == 0) {
+          cut = true;
+          if (warp == EP_WARP && lane == 0) {
+            int *te = a.table + 4 * blockIdx.x;
+            te[0] = it.b;
+            te[1] = it.kvh;
+            te[2] = it.t;
+            // The CTA that holds the item's last tile.
+            const long long x = pl.e + (it.nt - it.j1) - 1;
+            te[3] = static_cast<int>(((x + 1) * pl.n - 1) / pl.U) * 2 + slot;
+          }
+        }
+        continue;
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float g1 = (1.f + sg * inv) * inv;
+      // Output rows: 32 dims at a time through shared memory, so that four
+      // lanes write 64 contiguous bytes of a row.
+#pragma unroll 1
+      for (int part = 0; part < 4; ++part) {
+        float o1[32], o2[32];
+        tmem_ld32(tl + COL_O1 + part * 32, o1);
+        tmem_ld32(tl + COL_O2 + part * 32, o2);
+        tmem_wait_ld();
+        if (part == 3) o_read();
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float x0 = fmaf(o1[e], g1, -o2[e] * inv), x1 = fmaf(o1[e + 1], g1, -o2[e + 1] * inv);
+          pk[e >> 1] = l > 0.f ? pack_bf16x2(x0, x1) : 0u;
+        }
+        __syncwarp();  // the previous part has been read
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
+                       pk[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), orow = qw * 32 + rr, ch = lane & 3;
+          const uint4 v = *reinterpret_cast<const uint4 *>(smem + C::OFF_OST + qw * 2048 + rr * 64 +
+                                                          ((ch ^ ((rr >> 1) & 3)) << 4));
+          const int ot = orow / a.G, tok = it.t * a.TQ + ot;
+          if (ot < a.TQ && tok < it.s.n)
+            *reinterpret_cast<uint4 *>(a.out + (it.s.first + tok) * a.ots +
+                                       (it.kvh * a.G + orow - ot * a.G) * a.ohs + part * 32 + ch * 8) = v;
+        }
+      }
+      const int ot = row / a.G, tok = it.t * a.TQ + ot;
+      if (a.lse != nullptr && ot < a.TQ && tok < it.s.n)
+        a.lse[static_cast<long long>(it.s.first + tok) * a.Hq + it.kvh * a.G + row - ot * a.G] =
+            l > 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+    if (!cut && warp == EP_WARP && lane == 0) a.table[4 * blockIdx.x] = -1;
+  } else if (warp < S_WARP) {
+    // ------------------------------------------------------------ value UMMAs
+    // Warp O1_WARP: O1 += P V (P over S); the next: O2 += (P o T) V (over T).
+    if (lane == 0) {
+      const bool is_o1 = warp == O1_WARP;
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 1);
+      const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), HALF_KV, 1024);
+      const uint32_t col_off = is_o1 ? 0u : COL_T;
+      const uint32_t dout = tbase + (is_o1 ? COL_O1 : COL_O2);
+      int g = 0;
+      bool ok = true;
+      Walk wk(pl, a);
+      Item it;
+      for (int k = 0; ok && wk.next(it, a); ++k) {
+        const int nt = it.j1 - it.j0;
+        for (int j = 0; j < nt; ++j) {
+          const int gg = g + j, x = gg & 1, st = gg % NST;
+          if (j == 0 && k > 0 && !mbar_wait_spin(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (!mbar_wait_spin(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
+          const uint32_t ap = tbase + (x ? COL_S1 : COL_S0) + col_off;
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks) {
+            if (ks == 2 && !mbar_wait_spin(smem_u32(&p_full[2 * x + 1]), (gg >> 1) & 1, ab)) { ok = false; break; }
+            umma_ts(dout, ap + ks * 8, vdesc + ks * (2048 >> 4), idesc_pv, (j > 0 || ks > 0));
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&pv_done[x]));
+          umma_commit(smem_u32(&v_empty[st]));
+          tc_fence_before();
+          mbar_arrive(smem_u32(&pv_issued[2 * x + (is_o1 ? 0 : 1)]));
+        }
+        g += nt;
+      }
+      // Every UMMA this thread issued must finish before TMEM is released.
+      umma_commit(smem_u32(&drain[is_o1 ? 0 : 1]));
+      mbar_wait_drain(smem_u32(&drain[is_o1 ? 0 : 1]), 0);
+    }
+  } else if (warp < LOAD_WARP) {
+    // ------------------------------------------------------------ score UMMAs
+    // Warp S_WARP: S = Q K^T, and the loads of Q and R; the next: T = R K^T.
+    if (lane == 0) {
+      const bool is_s = warp == S_WARP;
+      constexpr uint32_t idesc_st = idesc_bf16_f32(BM, BN, 0);
+      const uint64_t adesc = smem_desc_sw128(smem_u32(smem + (is_s ? 0 : C::OFF_R)), 16, 1024);
+      const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+      const uint32_t col_off = is_s ? 0u : COL_T;
+      const uint32_t qb = smem_u32(q_full);
+      int g = 0, q_issued = 0;
+      bool ok = true;
+      Walk wk(pl, a);
+      Item it;
+      for (int k = 0; ok && wk.next(it, a); ++k) {
+        if (is_s) {
+          // Q and R of the previous item are dead once its last S and T finish.
+          if (k > 0 && !mbar_wait(smem_u32(q_empty), (k - 1) & 1, ab)) break;
+          mbar_arrive_expect_tx(qb, 4 * a.G * a.TQ * 128);
+          const int h0 = it.kvh * a.G, t0 = it.s.first + it.t * a.TQ;
+          tma_load_3d(smem_u32(smem), &tm_q, 0, h0, t0, qb);
+          tma_load_3d(smem_u32(smem + HALF_Q), &tm_q, 64, h0, t0, qb);
+          tma_load_3d(smem_u32(smem + C::OFF_R), &tm_r, 0, h0, t0, qb);
+          tma_load_3d(smem_u32(smem + C::OFF_R + HALF_Q), &tm_r, 64, h0, t0, qb);
+          q_issued = k + 1;
+        }
+        if (!mbar_wait(qb, k & 1, ab)) break;
+        const int nt = it.j1 - it.j0;
+        for (int j = 0; j < nt; ++j) {
+          const int gg = g + j, x = gg & 1, st = gg % NST;
+          if (!mbar_wait(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (gg >= 2 && !mbar_wait_spin(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t kdesc = kdesc0 + st * (TILE_KV >> 4);
+          const uint32_t d = tbase + (x ? COL_S1 : COL_S0) + col_off;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_ss(d, adesc + (ks >> 2) * (HALF_Q >> 4) + (ks & 3) * 2,
+                    kdesc + (ks >> 2) * (HALF_KV >> 4) + (ks & 3) * 2, idesc_st, ks > 0);
+          umma_commit(smem_u32(&st_full[x]));
+          umma_commit(smem_u32(&k_empty[st]));
+        }
+        if (ok) umma_commit(smem_u32(q_empty));  // Q / R of this item no longer read
+        g += nt;
+      }
+      umma_commit(smem_u32(&drain[is_s ? 2 : 3]));
+      mbar_wait_drain(smem_u32(&drain[is_s ? 2 : 3]), 0);
+      if (q_issued > 0) mbar_wait_drain(qb, (q_issued - 1) & 1);  // this thread's own copies
+    }
+  } else if (!FP8) {
+    // ------------------------------------------------------------ K, V loads
+    if (lane == 0) {
+      int g = 0, k_issued = 0, v_issued = 0;
+      bool ok = true;
+      Walk wk(pl, a);
+      Item it;
+      while (ok && wk.next(it, a)) {
+        for (int j = it.j0; j < it.j1; ++j, ++g) {
+          const int st = g % NST;
+          int z[4];  // the tile's boxes, looked up before the waits
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = i * box < BN ? page_head(it, j * BN + i * box) : beyond;
+          const int slot = (j * BN) & pmask;  // 0 unless pages are larger than a tile
+          if (g >= NST && !mbar_wait(smem_u32(&k_empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
+          const uint32_t kf = smem_u32(&k_full[st]), vf = smem_u32(&v_full[st]);
+          mbar_arrive_expect_tx(kf, TILE_KV);
+          const uint32_t kb = smem_u32(smem + C::OFF_K + st * TILE_KV);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i * box < BN) {
+              tma_load_4d(kb + i * box * 128, &tm_k, 0, slot, z[i], 0, kf);
+              tma_load_4d(kb + HALF_KV + i * box * 128, &tm_k, 0, slot, z[i], 1, kf);
+            }
+          k_issued = g + 1;
+          if (g >= NST && !mbar_wait(smem_u32(&v_empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
+          mbar_arrive_expect_tx(vf, TILE_KV);
+          const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i * box < BN) {
+              tma_load_4d(vb + i * box * 128, &tm_v, 0, slot, z[i], 0, vf);
+              tma_load_4d(vb + HALF_KV + i * box * 128, &tm_v, 0, slot, z[i], 1, vf);
+            }
+          v_issued = g + 1;
+        }
+      }
+      if (ab.raised()) {
+        // Let this thread's own copies land before the CTA exits.
+        for (int gg = max(0, k_issued - NST); gg < k_issued; ++gg)
+          mbar_wait_drain(smem_u32(&k_full[gg % NST]), (gg / NST) & 1);
+        for (int gg = max(0, v_issued - NST); gg < v_issued; ++gg)
+          mbar_wait_drain(smem_u32(&v_full[gg % NST]), (gg / NST) & 1);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ e4m3: loads and conversion
+    const int cw = warp - LOAD_WARP;
+    // Loads of raw tile gl (warp LOAD_WARP, lane 0): up to NRAW tiles in flight.
+    Walk lw(pl, a);
+    Item lit;
+    int lj = 0, gl = 0;
+    bool more = cw == 0 && lw.next(lit, a);
+    if (more) lj = lit.j0;
+    auto load_one = [&]() -> bool {  // by lane 0 of warp LOAD_WARP
+      const int st = gl % NRAW;
+      int z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = i * box < BN ? page_head(lit, lj * BN + i * box) : beyond;
+      const int slot = (lj * BN) & pmask;
+      if (gl >= NRAW && (!mbar_wait(smem_u32(&rk_empty[st]), ((gl / NRAW) - 1) & 1, ab) ||
+                         !mbar_wait(smem_u32(&rv_empty[st]), ((gl / NRAW) - 1) & 1, ab)))
+        return false;
+      const uint32_t kf = smem_u32(&rk_full[st]), vf = smem_u32(&rv_full[st]);
+      const uint32_t kb = smem_u32(smem + C::OFF_RAW + st * 2 * RAW), vb = kb + RAW;
+      mbar_arrive_expect_tx(kf, RAW);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * box < BN) tma_load_3d(kb + i * box * 128, &tm_k, 0, slot, z[i], kf);
+      mbar_arrive_expect_tx(vf, RAW);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * box < BN) tma_load_3d(vb + i * box * 128, &tm_v, 0, slot, z[i], vf);
+      return true;
+    };
+    auto load_ahead = [&](int upto) {  // issue the tiles below upto; false if a wait ran out
+      bool ok = true;
+      while (ok && more && gl < upto) {
+        ok = load_one();
+        if (!ok) break;
+        ++gl;
+        if (++lj == lit.j1) {
+          more = lw.next(lit, a);
+          if (more) lj = lit.j0;
+        }
+      }
+      return ok;
+    };
+    if (cw == 0 && lane == 0) load_ahead(NRAW);
+    // A warp converts 16 of the tile's rows; a thread four 16-byte pieces of K
+    // and of V: rows r and r + 8, pieces c and c ^ 4. Lanes of odd rows start
+    // in the other half of the row, which keeps both the reads and the
+    // swizzled writes free of bank conflicts.
+    const int odd = (lane >> 2) & 1;
+    const int r = cw * 16 + 2 * (lane >> 3) + odd, c0 = (lane & 3) + 4 * odd;
+    int g = 0;
+    bool ok = true;
+    Walk wk(pl, a);
+    Item it;
+    while (ok && wk.next(it, a)) {
+      const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+      // Scale bytes of the thread's rows of a tile (0: a row that is not there).
+      auto scales_of = [&](int j, uint32_t (&e)[4]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = j * BN + r + 8 * i;
+          e[i] = e[2 + i] = 0u;
+          if (j < it.j1 && key < it.s.len) {
+            const int page = table[key >> shift];
+            if (page >= 0 && page < a.c.num_pages) {
+              const long long at = ((static_cast<long long>(page) * a.c.Hkv + it.kvh) << shift) + (key & pmask);
+              e[i] = a.c.kscale[at];
+              e[2 + i] = a.c.vscale[at];
+            }
+          }
+        }
+      };
+      uint32_t e_next[4];
+      scales_of(it.j0, e_next);
+      for (int j = it.j0; j < it.j1; ++j, ++g) {
+        if (cw == 0) {
+          if (lane == 0) load_ahead(g + NRAW);  // a wait that ran out shows below
+          __syncwarp();
+        }
+        const uint32_t e4[4] = {e_next[0], e_next[1], e_next[2], e_next[3]};
+        scales_of(j + 1, e_next);
+        const int rs = g % NRAW, st = g % NST;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = mbar_wait(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
+          if (ok && g >= NST) ok = mbar_wait(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          const uint8_t *raw = smem + C::OFF_RAW + (rs * 2 + kv) * RAW;
+          const uint32_t dst = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K) + st * TILE_KV);
+          uint4 x[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              x[i][h] = *reinterpret_cast<const uint4 *>(raw + (r + 8 * i) * 128 + ((c0 ^ (4 * h)) << 4));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
+            // need a second factor. E = 0: no row, zeros.
+            const int E = static_cast<int>(e4[2 * kv + i]);
+            const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
+            const uint32_t f2x = f1 | (f1 << 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), f2x);
+                y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), f2x);
+              }
+              if (E > 134) {
+                const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f3x = f3 | (f3 << 16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f3x);
+              }
+              const int c = c0 ^ (4 * h), row = r + 8 * i;
+              const uint32_t at = dst + (c >> 2) * HALF_KV + row * 128;
+              st_shared_v4(at + (((2 * (c & 3)) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
+              st_shared_v4(at + (((2 * (c & 3) + 1) ^ (row & 7)) << 4), y[4], y[5], y[6], y[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(kv ? &rv_empty[rs] : &rk_empty[rs]));
+            mbar_arrive(smem_u32(kv ? &v_full[st] : &k_full[st]));
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    if (cw == 0 && lane == 0) {
+      // Let this thread's own copies land before the CTA exits.
+      for (int gg = max(0, gl - NRAW); gg < gl; ++gg) {
+        mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
+        mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == O1_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Merge of the items that several CTAs share: block (c, i) forms dims
+// [8 i, 8 i + 8) of the item that CTA c starts and does not finish, thread = row.
+__global__ void __launch_bounds__(BM) paged_prefill_merge_kernel(const Args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, i = blockIdx.y, row = threadIdx.x;
+  const int *te = a.table + 4 * c;
+  const int b = te[0];
+  if (b < 0) return;
+  const int kvh = te[1], t = te[2], last = te[3] >> 1, slot = te[3] & 1;
+  const Seq s = seq_of(a, b);
+  const int ot = row / a.G, tok = t * a.TQ + ot;
+  if (ot >= a.TQ || tok >= s.n) return;
+  // Parts: CTA c's, then slot 0 of the CTAs up to the last.
+  auto part = [&](int p) { return a.parts + (p == c ? 2ll * c + slot : 2ll * p) * PART; };
+  float M = -INFINITY;
+  for (int p = c; p <= last; ++p) M = fmaxf(M, part(p)[2 * D * BM + row]);
+  float L = 0.f, S = 0.f, o1[8] = {}, o2[8] = {};
+  if (M != -INFINITY) {
+#pragma unroll 2
+    for (int p = c; p <= last; ++p) {
+      const float *st = part(p) + 2 * D * BM;
+      const float f = fast_exp2(st[row] - M);
+      L = fmaf(f, st[BM + row], L);
+      S = fmaf(f, st[2 * BM + row], S);
+      const float4 *p4 = reinterpret_cast<const float4 *>(part(p));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = p4[(2 * i + h) * BM + row], y = p4[(32 + 2 * i + h) * BM + row];
+        o1[4 * h] = fmaf(f, x.x, o1[4 * h]);
+        o1[4 * h + 1] = fmaf(f, x.y, o1[4 * h + 1]);
+        o1[4 * h + 2] = fmaf(f, x.z, o1[4 * h + 2]);
+        o1[4 * h + 3] = fmaf(f, x.w, o1[4 * h + 3]);
+        o2[4 * h] = fmaf(f, y.x, o2[4 * h]);
+        o2[4 * h + 1] = fmaf(f, y.y, o2[4 * h + 1]);
+        o2[4 * h + 2] = fmaf(f, y.z, o2[4 * h + 2]);
+        o2[4 * h + 3] = fmaf(f, y.w, o2[4 * h + 3]);
+      }
+    }
+  }
+  const int h = kvh * a.G + row - ot * a.G;
+  uint32_t pk[4] = {};
+  if (L > 0.f) {
+    const float inv = 1.f / L, g1 = (1.f + S * inv) * inv;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      pk[e] = pack_bf16x2(fmaf(o1[2 * e], g1, -o2[2 * e] * inv), fmaf(o1[2 * e + 1], g1, -o2[2 * e + 1] * inv));
+  }
+  *reinterpret_cast<uint4 *>(a.out + (s.first + tok) * a.ots + h * a.ohs + 8 * i) =
+      make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  if (i == 0 && a.lse != nullptr)
+    a.lse[static_cast<long long>(s.first + tok) * a.Hq + h] =
+        L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Q, R: [T, Hq, 128] with any strides, boxes of 64 dims x G heads x TQ tokens.
+bool make_rows_map(EncodeTiledFn enc, CUtensorMap *map, const void *ptr, int T, int Hq, int G, int TQ,
+                   long long ts, long long hs) {
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(ts) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(TQ)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Pages: bf16 {64, page, pages Hkv, 2 halves}, boxes of up to 64 rows of one
+// half, swizzled; e4m3 {128, page, pages Hkv}, plain rows.
+bool make_tile_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, const void *ptr, bool fp8) {
+  const cuuint64_t page = 1ull << c.page_shift, heads = static_cast<cuuint64_t>(c.num_pages) * c.Hkv;
+  const cuuint32_t rows = static_cast<cuuint32_t>(page < BN ? page : BN);
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  if (fp8) {
+    const cuuint64_t dims[3] = {D, page, heads};
+    const cuuint64_t strides[2] = {D, page * D};
+    const cuuint32_t box[3] = {D, rows, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dims[4] = {64, page, heads, 2};
+  const cuuint64_t strides[3] = {2 * D, page * 2 * D, 128};
+  const cuuint32_t box[4] = {64, rows, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+cudaError_t launch_tiles(const Args &a, int grid, const CUtensorMap (&m)[4], cudaStream_t stream) {
+  static thread_local unsigned long long configured_ctx = 0;
+  const unsigned long long ctx = context_id();
+  if (ctx == 0 || configured_ctx != ctx) {
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_kernel<FP8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::SMEM);
+    if (e != cudaSuccess) return e;
+    configured_ctx = ctx;
+  }
+  paged_prefill_kernel<FP8><<<grid, Cfg<FP8>::THREADS, Cfg<FP8>::SMEM, stream>>>(m[0], m[1], m[2], m[3], a);
+  return cudaGetLastError();
+}
+
+constexpr size_t table_bytes(int grid) { return (size_t(grid) * 16 + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t paged_prefill_workspace_bytes() {
+  const int grid = sm_count();
+  return table_bytes(grid) + size_t(2 * grid) * PART * sizeof(float);
+}
+
+cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void *r, long long qts,
+                                 long long qhs, const int *seqlens, const int *cu_q, void *out,
+                                 long long ots, long long ohs, float *lse, int T, int Hq,
+                                 void *workspace, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return cudaErrorInvalidValue;
+  const bool fp8 = c.kscale != nullptr;
+  Args a;
+  a.c = c;
+  a.seqlens = seqlens;
+  a.cu = cu_q;
+  a.out = static_cast<__nv_bfloat16 *>(out);
+  a.lse = lse;
+  a.ots = ots;
+  a.ohs = ohs;
+  a.T = T;
+  a.Hq = Hq;
+  a.G = Hq / c.Hkv;
+  a.TQ = BM / a.G;
+  a.min_units = 4;
+  a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+  const int grid = sm_count();
+  a.table = static_cast<int *>(workspace);
+  a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + table_bytes(grid));
+  CUtensorMap m[4];
+  if (!make_rows_map(enc, &m[0], q, T, Hq, a.G, a.TQ, qts, qhs) ||
+      !make_rows_map(enc, &m[1], r, T, Hq, a.G, a.TQ, qts, qhs) ||
+      !make_tile_map(enc, &m[2], c, c.k, fp8) || !make_tile_map(enc, &m[3], c, c.v, fp8))
+    return cudaErrorInvalidValue;
+  cudaError_t e = fp8 ? launch_tiles<true>(a, grid, m, stream) : launch_tiles<false>(a, grid, m, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, D / 8);
+  cfg.blockDim = dim3(BM);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_prefill_merge_kernel, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace plx

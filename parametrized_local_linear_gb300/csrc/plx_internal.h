@@ -103,12 +103,6 @@ cudaError_t launch_kv_append(const PagedCache &c, const void *k, const void *v,
                              const int *cu_q, int T, cudaStream_t stream);
 cudaError_t launch_kv_read(const PagedCache &c, const int *cu_k, void *k, void *v, int T,
                            cudaStream_t stream);
-// lse ([T, Hq] fp32) may be null; cu_q null: one new token a sequence.
-cudaError_t launch_paged_attn(const PagedCache &c, const void *q, const void *r, long long qts,
-                              long long qhs, const int *seqlens, const int *cu_q, void *out,
-                              long long ots, long long ohs, float *lse, int T, int Hq,
-                              cudaStream_t stream);
-
 // Few new tokens a sequence (decode: one): split over equal shares of the key
 // stream and combined. Workspace: {first record slot, slots} per virtual row
 // (sequence, kv head, group of 8 query rows), padded to 256 bytes, then
@@ -126,10 +120,18 @@ inline size_t paged_rows_workspace_bytes(int T, int B, int G, int Hkv, int d, bo
   return paged_rows_meta_bytes(vrows) +
          size_t(paged_rows_shares(slot) + vrows) * slot * (2 * size_t(d) + 2) * sizeof(float);
 }
+// lse ([T, Hq] fp32) may be null; cu_q null: one new token a sequence.
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
                               long long qhs, const int *seqlens, const int *cu_q, void *out,
                               long long ots, long long ohs, float *lse, int T, int Hq,
                               void *workspace, cudaStream_t stream);
+
+// Chunks of any length (tcgen05). lse ([T, Hq] fp32) may be null.
+size_t paged_prefill_workspace_bytes();
+cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void *r, long long qts,
+                                 long long qhs, const int *seqlens, const int *cu_q, void *out,
+                                 long long ots, long long ohs, float *lse, int T, int Hq,
+                                 void *workspace, cudaStream_t stream);
 
 cudaError_t launch_timeout_probe(long long limit_cycles, unsigned *err, cudaStream_t stream);
 
