@@ -29,8 +29,10 @@
 //     it the stored value, exactly.
 //
 // Warps: 0..3 softmax, 4..7 epilogue, 8 O1, 9 O2, 10 S (and the Q, R loads),
-// 11 T; bf16: 12 loads K and V; e4m3: 12..15 convert, warp 12 also loads.
-// Tensor memory as in prefill_tc.cu.
+// 11 T; bf16: 12 loads K, 13 loads V; e4m3: 12..15 convert, and the T thread
+// issues the raw loads (16 warps are what 128 registers a thread allow; a
+// converter warp that also loaded held the others up). Tensor memory as in
+// prefill_tc.cu.
 #include <math.h>
 #include <string.h>
 
@@ -56,7 +58,7 @@ constexpr int EP_WARP = 4, O1_WARP = 8, S_WARP = 10, LOAD_WARP = 12;
 template <bool FP8>
 struct Cfg {
   static constexpr int NST = FP8 ? 3 : 4;  // bf16 K and V stages
-  static constexpr int WARPS = FP8 ? 16 : 13;
+  static constexpr int WARPS = FP8 ? 16 : 14;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int OFF_R = 2 * HALF_Q;
   static constexpr int OFF_K = 4 * HALF_Q;
@@ -128,7 +130,7 @@ __device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t
   return ans;
 }
 // Key tiles of the first t row tiles (t <= nq).
-__device__ __forceinline__ long long tiles_before(const Seq &s, int t, int TQ) {
+__device__ __noinline__ long long tiles_before(const Seq &s, int t, int TQ) {
   if (t <= 0) return 0;
   long long extra = 0;
   if (t == s.nq) extra = tiles_of(s, --t, TQ);  // the last row tile may be short
@@ -149,29 +151,28 @@ struct Item {
   int b, kvh, t, j0, j1, nt;
 };
 
+// The walk keeps little across an item (the softmax warps have no registers to
+// spare): the sequence is looked up again for every item.
 struct Walk {
-  Seq s;
   long long left;
-  int b, kvh, t, j;
-  bool begun = false;
+  int b, kvh, t, j;  // t, j: of the next item
   __device__ __forceinline__ Walk(const Plan &p, const Args &a)
-      : s(seq_of(a, p.b)), left(p.e - p.s), b(p.b), kvh(p.kvh), t(p.t), j(p.j) {}
-  __device__ __forceinline__ bool next(Item &it, const Args &a) {
-    if (left <= 0) return false;  // more units left: another item follows, so b stays below B
-    if (begun && ++t == s.nq) {
+      : left(p.e - p.s), b(p.b), kvh(p.kvh), t(p.t), j(p.j) {}
+  __device__ __noinline__ bool next(Item &it, const Args &a) {
+    if (left <= 0) return false;  // more tiles left: another item follows, so b stays below B
+    it.s = seq_of(a, b);
+    if (t == it.s.nq) {
       t = 0;
       if (++kvh == a.c.Hkv) {
         kvh = 0;
-        do s = seq_of(a, ++b);
-        while (s.nq == 0);
+        do it.s = seq_of(a, ++b);
+        while (it.s.nq == 0);
       }
     }
-    begun = true;
-    it.s = s;
     it.b = b;
     it.kvh = kvh;
-    it.t = t;
-    it.nt = tiles_of(s, t, a.TQ);
+    it.t = t++;
+    it.nt = tiles_of(it.s, it.t, a.TQ);
     it.j0 = j;
     j = 0;
     it.j1 = static_cast<int>(min(static_cast<long long>(it.nt), it.j0 + left));
@@ -181,7 +182,7 @@ struct Walk {
 };
 
 // One warp: the CTA's share and where it starts.
-__device__ __forceinline__ void make_plan(const Args &a, Plan *plan, int lane) {
+__device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   const int c = blockIdx.x;
   long long U = 0;
   for (int i = lane; i < a.c.B; i += 32) {
@@ -237,6 +238,24 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, int lane) {
     p.j = static_cast<int>(in - tiles_before(s, lo, a.TQ));
   }
   if (lane == 0) *plan = p;
+}
+
+// mbar_wait_spin with a loop that stays a loop: unrolled, the four issuing
+// threads' polls alone are tens of KB of code, which take instruction cache
+// from the softmax warps.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const Abort &ab) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test_wait(bar, parity)) return true;
+    if (ab.raised()) return false;
+    if (clock64() - t0 > kSpinLimitCycles) {
+      ab.raise(kErrTimeout);
+      return false;
+    }
+  }
 }
 
 // 4-D tiled load (box and swizzle come from the tensor map).
@@ -380,15 +399,17 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const int pos0 = it.s.len - it.s.n + it.t * a.TQ;  // position of the tile's first token
       const int pos = pos0 + rtok;                       // the last key that this row sees
       float m_used = -INFINITY, l = 0.f, sg = 0.f;
-      for (int j = it.j0; j < it.j1; ++j) {
-        const int gg = g + j - it.j0, x = gg & 1;
-        const bool masked = j * BN + BN - 1 > pos0;
-        const int valid = it.s.len - j * BN;  // keys of the tile that exist
-        if (!FP8 && valid < BN) {
+      // One key tile; the mask is a compile-time choice, so that the tiles
+      // below the diagonal run straight through. lim: keys of the tile that
+      // the row sees, valid: that exist.
+      auto tile = [&](auto mask_tag, int gg, int lim, int valid) -> bool {
+        constexpr bool MASK = decltype(mask_tag)::value;
+        const int x = gg & 1;
+        if (MASK && !FP8 && valid < BN) {
           // The last tile: zero the V rows behind the last key.
           const int st = gg % NST;
-          ok = mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          bool ok = mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab);
+          if (!__all_sync(0xffffffffu, ok)) return false;
           const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
           for (int i = max(valid, 0) * 8 + row; i < BN * 8; i += BM) {
             st_shared_v4(vb + i * 16, 0u, 0u, 0u, 0u);
@@ -396,18 +417,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           }
           fence_proxy_async_smem();
         }
-        ok = mbar_wait(smem_u32(&st_full[x]), (gg >> 1) & 1, ab);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const bool ok = mbar_wait(smem_u32(&st_full[x]), (gg >> 1) & 1, ab);
+        if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         const uint32_t cs = tl + (x ? COL_S1 : COL_S0);
         float s[64];
         tmem_ld32(cs, *reinterpret_cast<float(*)[32]>(&s[0]));
         tmem_ld32(cs + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
         tmem_wait_ld();
-        if (masked) {
+        if (MASK) {
 #pragma unroll
           for (int e = 0; e < BN; ++e)
-            if (j * BN + e > pos) s[e] = -INFINITY;
+            if (e >= lim) s[e] = -INFINITY;
         }
         float mx8[8];
 #pragma unroll
@@ -424,9 +445,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           sg *= alpha;
           m_used = mt;
         }
-        if (j > it.j0 && __any_sync(0xffffffffu, need)) {
-          ok = mbar_wait(smem_u32(&pv_done[(gg - 1) & 1]), ((gg - 1) >> 1) & 1, ab);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (gg > g && __any_sync(0xffffffffu, need)) {
+          bool ok = mbar_wait(smem_u32(&pv_done[(gg - 1) & 1]), ((gg - 1) >> 1) & 1, ab);
+          if (!__all_sync(0xffffffffu, ok)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int part = 0; part < 8; ++part) {
@@ -448,11 +469,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           float t[16];
           tmem_ld16(cs + COL_T + 16 * qq, t);
           tmem_wait_ld();
-          if (masked) {
+          if (MASK) {
             // p = 0 there, but t may be NaN (slots behind the last key).
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (j * BN + 16 * qq + e > pos) t[e] = 0.f;
+              if (16 * qq + e >= lim) t[e] = 0.f;
           }
           uint32_t pk[8], ptk[8];
 #pragma unroll
@@ -482,8 +503,22 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * x + 1]));
+        return true;
+      };
+      // Tiles that every row of the item sees whole, then the others.
+      const int n = it.j1 - it.j0, whole = min(n, max(0, (pos0 + 1) / BN - it.j0));
+      int j = 0;
+      for (; ok && j < whole; ++j) ok = tile(std::false_type{}, g + j, BN, BN);
+      for (; ok && j < n; ++j) {
+        const int key0 = (it.j0 + j) * BN;
+        ok = tile(std::true_type{}, g + j, pos - key0 + 1, it.s.len - key0);
       }
-      if (!ok) break;
+      // The epilogue must have read item k - 2's statistics before its buffer
+      // is written again. It has once it released item k - 1's O, which the
+      // item's own value UMMAs wait for too. (Items of one or two tiles would
+      // otherwise let the softmax run two items ahead of a busy epilogue.)
+      if (ok && k > 0) ok = mbar_wait(smem_u32(o_free), (k - 1) & 1, ab);
+      if (!__all_sync(0xffffffffu, ok)) break;
       float *st = stat + (k & 1) * 3 * BM;
       st[row] = m_used;
       st[BM + row] = l;
@@ -606,15 +641,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
-          if (j == 0 && k > 0 && !mbar_wait_spin(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
+          if (j == 0 && k > 0 && !mbar_poll(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
           if (!mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
-          if (!mbar_wait_spin(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
+          if (!mbar_poll(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
           const uint32_t ap = tbase + (x ? COL_S1 : COL_S0) + col_off;
 #pragma unroll
           for (int ks = 0; ks < BN / 16; ++ks) {
-            if (ks == 2 && !mbar_wait_spin(smem_u32(&p_full[2 * x + 1]), (gg >> 1) & 1, ab)) { ok = false; break; }
+            if (ks == 2 && !mbar_poll(smem_u32(&p_full[2 * x + 1]), (gg >> 1) & 1, ab)) { ok = false; break; }
             umma_ts(dout, ap + ks * 8, vdesc + ks * (2048 >> 4), idesc_pv, (j > 0 || ks > 0));
           }
           if (!ok) break;
@@ -641,6 +676,51 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t qb = smem_u32(q_full);
       int g = 0, q_issued = 0;
       bool ok = true;
+      // e4m3, T: the next raw tile to load is gl, key tile lj of item lit; its
+      // page numbers are fetched when the one before it is issued. Its stage
+      // held tile gl - NRAW, whose V all converter warps have left by the time
+      // that the K of the tile after it is converted, so there is no wait.
+      Walk lw(pl, a);
+      Item lit;
+      int lj = 0, gl = 0, page[4];
+      bool more = FP8 && !is_s && lw.next(lit, a);
+      auto fetch_pages = [&] {
+        const int *table = a.c.table + static_cast<long long>(lit.b) * a.c.max_pages;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = lj * BN + i * box;
+          page[i] = i * box < BN && key < lit.s.len ? table[key >> shift] : a.c.num_pages;
+        }
+      };
+      if (more) {
+        lj = lit.j0;
+        fetch_pages();
+      }
+      auto load_raw = [&] {
+        const int st = gl % NRAW, slot = (lj * BN) & pmask;
+        const uint32_t kf = smem_u32(&rk_full[st]), vf = smem_u32(&rv_full[st]);
+        const uint32_t kb = smem_u32(smem + C::OFF_RAW + st * 2 * RAW), vb = kb + RAW;
+        mbar_arrive_expect_tx(kf, RAW);
+        mbar_arrive_expect_tx(vf, RAW);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i * box >= BN) continue;
+          int z = beyond;
+          if (page[i] >= 0 && page[i] < a.c.num_pages) z = page[i] * a.c.Hkv + lit.kvh;
+          else if (page[i] != a.c.num_pages || lj * BN + i * box < lit.s.len)
+            if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+          tma_load_3d(kb + i * box * 128, &tm_k, 0, slot, z, kf);
+          tma_load_3d(vb + i * box * 128, &tm_v, 0, slot, z, vf);
+        }
+        ++gl;
+        if (++lj == lit.j1) {
+          more = lw.next(lit, a);
+          if (!more) return;
+          lj = lit.j0;
+        }
+        fetch_pages();
+      };
+      while (more && gl < NRAW - 1) load_raw();
       Walk wk(pl, a);
       Item it;
       for (int k = 0; ok && wk.next(it, a); ++k) {
@@ -660,7 +740,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
           if (!mbar_wait(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
-          if (gg >= 2 && !mbar_wait_spin(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
+          if (FP8 && more) {  // (S: never)
+            const int rs = gl % NRAW, par = ((gl / NRAW) - 1) & 1;
+            if (gl >= NRAW && (!mbar_wait(smem_u32(&rk_empty[rs]), par, ab) ||
+                               !mbar_wait(smem_u32(&rv_empty[rs]), par, ab))) { ok = false; break; }
+            load_raw();
+          }
+          if (gg >= 2 && !mbar_poll(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t kdesc = kdesc0 + st * (TILE_KV >> 4);
           const uint32_t d = tbase + (x ? COL_S1 : COL_S0) + col_off;
@@ -677,172 +763,135 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       umma_commit(smem_u32(&drain[is_s ? 2 : 3]));
       mbar_wait_drain(smem_u32(&drain[is_s ? 2 : 3]), 0);
       if (q_issued > 0) mbar_wait_drain(qb, (q_issued - 1) & 1);  // this thread's own copies
+      for (int gg = max(0, gl - NRAW); gg < gl; ++gg) {
+        mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
+        mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
+      }
     }
   } else if (!FP8) {
     // ------------------------------------------------------------ K, V loads
+    // Warp LOAD_WARP: K, the next: V.
     if (lane == 0) {
-      int g = 0, k_issued = 0, v_issued = 0;
+      const bool is_k = warp == LOAD_WARP;
+      const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+      uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+      const uint32_t ring = smem_u32(smem + (is_k ? C::OFF_K : C::OFF_V));
+      int g = 0;
       bool ok = true;
       Walk wk(pl, a);
       Item it;
       while (ok && wk.next(it, a)) {
         for (int j = it.j0; j < it.j1; ++j, ++g) {
           const int st = g % NST;
-          int z[4];  // the tile's boxes, looked up before the waits
+          int z[4];  // the tile's boxes, looked up before the wait
 #pragma unroll
           for (int i = 0; i < 4; ++i) z[i] = i * box < BN ? page_head(it, j * BN + i * box) : beyond;
           const int slot = (j * BN) & pmask;  // 0 unless pages are larger than a tile
-          if (g >= NST && !mbar_wait(smem_u32(&k_empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
-          const uint32_t kf = smem_u32(&k_full[st]), vf = smem_u32(&v_full[st]);
-          mbar_arrive_expect_tx(kf, TILE_KV);
-          const uint32_t kb = smem_u32(smem + C::OFF_K + st * TILE_KV);
+          if (g >= NST && !mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
+          const uint32_t bar = smem_u32(&full[st]), dst = ring + st * TILE_KV;
+          mbar_arrive_expect_tx(bar, TILE_KV);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (i * box < BN) {
-              tma_load_4d(kb + i * box * 128, &tm_k, 0, slot, z[i], 0, kf);
-              tma_load_4d(kb + HALF_KV + i * box * 128, &tm_k, 0, slot, z[i], 1, kf);
+              tma_load_4d(dst + i * box * 128, map, 0, slot, z[i], 0, bar);
+              tma_load_4d(dst + HALF_KV + i * box * 128, map, 0, slot, z[i], 1, bar);
             }
-          k_issued = g + 1;
-          if (g >= NST && !mbar_wait(smem_u32(&v_empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
-          mbar_arrive_expect_tx(vf, TILE_KV);
-          const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i * box < BN) {
-              tma_load_4d(vb + i * box * 128, &tm_v, 0, slot, z[i], 0, vf);
-              tma_load_4d(vb + HALF_KV + i * box * 128, &tm_v, 0, slot, z[i], 1, vf);
-            }
-          v_issued = g + 1;
         }
       }
       if (ab.raised()) {
         // Let this thread's own copies land before the CTA exits.
-        for (int gg = max(0, k_issued - NST); gg < k_issued; ++gg)
-          mbar_wait_drain(smem_u32(&k_full[gg % NST]), (gg / NST) & 1);
-        for (int gg = max(0, v_issued - NST); gg < v_issued; ++gg)
-          mbar_wait_drain(smem_u32(&v_full[gg % NST]), (gg / NST) & 1);
+        for (int gg = max(0, g - NST); gg < g; ++gg)
+          mbar_wait_drain(smem_u32(&full[gg % NST]), (gg / NST) & 1);
       }
     }
   } else {
-    // ------------------------------------------------------------ e4m3: loads and conversion
-    const int cw = warp - LOAD_WARP;
-    // Loads of raw tile gl (warp LOAD_WARP, lane 0): up to NRAW tiles in flight.
-    Walk lw(pl, a);
-    Item lit;
-    int lj = 0, gl = 0;
-    bool more = cw == 0 && lw.next(lit, a);
-    if (more) lj = lit.j0;
-    auto load_one = [&]() -> bool {  // by lane 0 of warp LOAD_WARP
-      const int st = gl % NRAW;
-      int z[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = i * box < BN ? page_head(lit, lj * BN + i * box) : beyond;
-      const int slot = (lj * BN) & pmask;
-      if (gl >= NRAW && (!mbar_wait(smem_u32(&rk_empty[st]), ((gl / NRAW) - 1) & 1, ab) ||
-                         !mbar_wait(smem_u32(&rv_empty[st]), ((gl / NRAW) - 1) & 1, ab)))
-        return false;
-      const uint32_t kf = smem_u32(&rk_full[st]), vf = smem_u32(&rv_full[st]);
-      const uint32_t kb = smem_u32(smem + C::OFF_RAW + st * 2 * RAW), vb = kb + RAW;
-      mbar_arrive_expect_tx(kf, RAW);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i * box < BN) tma_load_3d(kb + i * box * 128, &tm_k, 0, slot, z[i], kf);
-      mbar_arrive_expect_tx(vf, RAW);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i * box < BN) tma_load_3d(vb + i * box * 128, &tm_v, 0, slot, z[i], vf);
-      return true;
-    };
-    auto load_ahead = [&](int upto) {  // issue the tiles below upto; false if a wait ran out
-      bool ok = true;
-      while (ok && more && gl < upto) {
-        ok = load_one();
-        if (!ok) break;
-        ++gl;
-        if (++lj == lit.j1) {
-          more = lw.next(lit, a);
-          if (more) lj = lit.j0;
-        }
-      }
-      return ok;
-    };
-    if (cw == 0 && lane == 0) load_ahead(NRAW);
+    // ------------------------------------------------------------ e4m3: conversion
     // A warp converts 16 of the tile's rows; a thread four 16-byte pieces of K
-    // and of V: rows r and r + 8, pieces c and c ^ 4. Lanes of odd rows start
+    // and of V: rows r and r + 8, pieces c0 and c0 ^ 4. Lanes of odd rows start
     // in the other half of the row, which keeps both the reads and the
     // swizzled writes free of bank conflicts.
     const int odd = (lane >> 2) & 1;
-    const int r = cw * 16 + 2 * (lane >> 3) + odd, c0 = (lane & 3) + 4 * odd;
+    const int r = (warp - LOAD_WARP) * 16 + 2 * (lane >> 3) + odd, c0 = (lane & 3) + 4 * odd;
+    uint32_t from[2], to[2][2];  // offsets of the pieces of row r in a raw and in a bf16 tile
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 ^ (4 * h);
+      from[h] = r * 128 + (c << 4);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        to[h][e] = (c >> 2) * HALF_KV + r * 128 + (((2 * (c & 3) + e) ^ (r & 7)) << 4);
+    }
     int g = 0;
     bool ok = true;
     Walk wk(pl, a);
     Item it;
     while (ok && wk.next(it, a)) {
       const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-      // Scale bytes of the thread's rows of a tile (0: a row that is not there).
-      auto scales_of = [&](int j, uint32_t (&e)[4]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int key = j * BN + r + 8 * i;
-          e[i] = e[2 + i] = 0u;
-          if (j < it.j1 && key < it.s.len) {
-            const int page = table[key >> shift];
-            if (page >= 0 && page < a.c.num_pages) {
-              const long long at = ((static_cast<long long>(page) * a.c.Hkv + it.kvh) << shift) + (key & pmask);
-              e[i] = a.c.kscale[at];
-              e[2 + i] = a.c.vscale[at];
-            }
-          }
+      const int len = it.s.len, kvh = it.kvh, j1 = it.j1;
+      // The page of the warp's rows of a tile (16 rows never cross one), and
+      // from it the scale bytes of rows r and r + 8 (0: a row that is not there):
+      // looked up two tiles and one tile ahead.
+      auto page_of = [&](int j) {
+        const int key = j * BN + (r & ~15);
+        return j < j1 && key < len ? table[key >> shift] : -1;
+      };
+      auto scales_of = [&](int j, int page, uint32_t (&e)[4]) {
+        e[0] = e[1] = e[2] = e[3] = 0u;
+        if (page < 0 || page >= a.c.num_pages) return;
+        const int key = j * BN + r;
+        const long long at = ((static_cast<long long>(page) * a.c.Hkv + kvh) << shift) + (key & pmask);
+        if (key < len) {
+          e[0] = a.c.kscale[at];
+          e[2] = a.c.vscale[at];
+        }
+        if (key + 8 < len) {
+          e[1] = a.c.kscale[at + 8];
+          e[3] = a.c.vscale[at + 8];
         }
       };
       uint32_t e_next[4];
-      scales_of(it.j0, e_next);
-      for (int j = it.j0; j < it.j1; ++j, ++g) {
-        if (cw == 0) {
-          if (lane == 0) load_ahead(g + NRAW);  // a wait that ran out shows below
-          __syncwarp();
-        }
+      scales_of(it.j0, page_of(it.j0), e_next);
+      int page_next = page_of(it.j0 + 1);
+      for (int j = it.j0; j < j1; ++j, ++g) {
         const uint32_t e4[4] = {e_next[0], e_next[1], e_next[2], e_next[3]};
-        scales_of(j + 1, e_next);
+        scales_of(j + 1, page_next, e_next);
+        page_next = page_of(j + 2);
         const int rs = g % NRAW, st = g % NST;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           ok = mbar_wait(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
-          if (ok && g >= NST) ok = mbar_wait(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           const uint8_t *raw = smem + C::OFF_RAW + (rs * 2 + kv) * RAW;
-          const uint32_t dst = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K) + st * TILE_KV);
           uint4 x[2][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              x[i][h] = *reinterpret_cast<const uint4 *>(raw + (r + 8 * i) * 128 + ((c0 ^ (4 * h)) << 4));
+            for (int h = 0; h < 2; ++h) x[i][h] = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * i);
+          if (ok && g >= NST) ok = mbar_wait(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          const uint32_t dst = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K) + st * TILE_KV);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
             // need a second factor. E = 0: no row, zeros.
             const int E = static_cast<int>(e4[2 * kv + i]);
             const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
-            const uint32_t f2x = f1 | (f1 << 16);
+            const uint32_t ff = f1 | (f1 << 16);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t w[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), f2x);
-                y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), f2x);
+                y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), ff);
+                y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), ff);
               }
               if (E > 134) {
-                const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f3x = f3 | (f3 << 16);
+                const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f4 = f3 | (f3 << 16);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f3x);
+                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f4);
               }
-              const int c = c0 ^ (4 * h), row = r + 8 * i;
-              const uint32_t at = dst + (c >> 2) * HALF_KV + row * 128;
-              st_shared_v4(at + (((2 * (c & 3)) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
-              st_shared_v4(at + (((2 * (c & 3) + 1) ^ (row & 7)) << 4), y[4], y[5], y[6], y[7]);
+              st_shared_v4(dst + to[h][0] + 1024 * i, y[0], y[1], y[2], y[3]);
+              st_shared_v4(dst + to[h][1] + 1024 * i, y[4], y[5], y[6], y[7]);
             }
           }
           fence_proxy_async_smem();
@@ -853,13 +902,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           }
         }
         if (!ok) break;
-      }
-    }
-    if (cw == 0 && lane == 0) {
-      // Let this thread's own copies land before the CTA exits.
-      for (int gg = max(0, gl - NRAW); gg < gl; ++gg) {
-        mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
-        mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
       }
     }
   }
