@@ -16,7 +16,7 @@
 //     keys. A CTA whose share starts or ends inside an item writes that part's
 //     raw O1, O2, m, l, sigma (fp32) to the workspace, and a second kernel
 //     merges the parts. Lengths live on the device, so each CTA finds its share
-//     itself: the tiles of the first t row tiles of a chunk are a sum of
+//     itself: the key tiles of the first t row tiles of a chunk are a sum of
 //     floor((a + i TQ) / 64), evaluated in closed form.
 //   - Pages. A key tile is 64 / page_size boxes (one for larger pages). Slots
 //     behind the last key may hold anything: S and T are masked by selection,
@@ -67,7 +67,8 @@ struct Cfg {
   static constexpr int OFF_STAT = OFF_RAW + (FP8 ? NRAW * 2 * RAW : 0);
   static constexpr int OFF_OST = OFF_STAT + 2 * 3 * BM * 4;  // per epilogue warp: 32 rows x 64 bytes
   static constexpr int OFF_PLAN = OFF_OST + 4 * 2048;
-  static constexpr int OFF_BAR = OFF_PLAN + 64;
+  static constexpr int OFF_WALK = OFF_PLAN + 64;  // one per warp, one more for the raw loads
+  static constexpr int OFF_BAR = OFF_WALK + 17 * 112;
   static constexpr int NBAR = 2 + 4 * NST + 2 + 4 + 2 + 4 + 1 + 2 + 4 + (FP8 ? 4 * NRAW : 0);
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -81,9 +82,11 @@ struct Args {
   float *parts;  // [2 grid][PART floats]
   int *table;    // [grid][4] the item that CTA c starts and does not finish
   long long ots, ohs;
-  int T, Hq, G, TQ, min_units;
+  int T, Hq, G, TQ;
   float scale_log2;
 };
+// A CTA's share is at least this many key tiles.
+constexpr int kMinTiles = 4;
 // A part: [64][128 rows] float4 (O1's 128 columns, then O2's), then m, l, sigma.
 constexpr int PART = 2 * D * BM + 3 * BM;
 
@@ -91,7 +94,7 @@ constexpr int PART = 2 * D * BM + 3 * BM;
 struct Seq {
   int len, first, n, nq;  // keys, first packed row, new tokens, row tiles
 };
-__device__ __forceinline__ Seq seq_of(const Args &a, int b) {
+__device__ __noinline__ Seq seq_of(const Args &a, int b) {
   Seq s;
   s.len = cache_len(a.c, a.seqlens, b);
   s.first = a.cu[b];
@@ -110,24 +113,21 @@ __device__ __forceinline__ int tiles_of(const Seq &s, int t, int TQ) {
   const int seen = s.len - s.n + static_cast<int>(min(static_cast<long long>(t + 1) * TQ, static_cast<long long>(s.n)));
   return max(1, (seen + BN - 1) / BN);
 }
-// sum over i < n of floor((b + i a) / m), all >= 0, m <= 2^16 (the Euclid-like
-// recursion of lattice-point counting).
-__device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t a, long long b) {
-  long long ans = 0;
-  while (n > 0) {
-    ans += (n - 1) * n / 2 * (a / m);
-    a %= m;
-    ans += n * (b / m);
-    const uint32_t r = static_cast<uint32_t>(b % m);
-    const long long y = static_cast<long long>(a) * n + r;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
+// sum over i < n of floor((b + i TQ) / 64), b >= 0. With per = 64 / gcd(TQ, 64)
+// the term of i = q per + r is q (TQ per / 64) + floor((b + r TQ) / 64), so one
+// period's terms and the sum over q give the rest; no divisions.
+__device__ __forceinline__ long long tile_sum(long long n, int TQ, long long b) {
+  const int lg = max(0, 6 - (__ffs(TQ) - 1));  // per = 1 << lg
+  const long long q = n >> lg, inc = (static_cast<long long>(TQ) << lg) >> 6;
+  const int rest = static_cast<int>(n & ((1 << lg) - 1)), most = q > 0 ? 1 << lg : rest;
+  long long all = 0, some = 0;  // the terms of a period, and those below rest
+#pragma unroll 1
+  for (int r = 0; r < most; ++r) {
+    const long long f = (b + r * TQ) >> 6;
+    all += f;
+    if (r < rest) some += f;
   }
-  return ans;
+  return ((inc << lg) * (q * (q - 1) / 2)) + q * all + rest * q * inc + some;
 }
 // Key tiles of the first t row tiles (t <= nq).
 __device__ __noinline__ long long tiles_before(const Seq &s, int t, int TQ) {
@@ -137,7 +137,7 @@ __device__ __noinline__ long long tiles_before(const Seq &s, int t, int TQ) {
   // Row tiles i < i0 see at most BN keys: one key tile each.
   const long long base = static_cast<long long>(s.len) - s.n + TQ + BN - 1;  // i = 0's numerator
   const long long i0 = base >= 2 * BN ? 0 : min(static_cast<long long>(t), (2 * BN - base + TQ - 1) / TQ);
-  return extra + i0 + floor_sum(t - i0, BN, static_cast<uint32_t>(TQ), max(0ll, base + i0 * TQ));
+  return extra + i0 + tile_sum(t - i0, TQ, max(0ll, base + i0 * TQ));
 }
 
 struct Plan {
@@ -146,52 +146,87 @@ struct Plan {
   int b, kvh, t, j;   // where the share starts
 };
 
+// A part of an item: key tiles [j0, j1) of its nt.
 struct Item {
-  Seq s;
-  int b, kvh, t, j0, j1, nt;
+  int b, kvh, t, len;  // sequence, kv head, row tile; keys of the sequence
+  int row0, ntok;      // first packed row; tokens of the chunk from there on
+  int pos0;            // position of the first token
+  int j0, j1, nt;
 };
 
-// The walk keeps little across an item (the softmax warps have no registers to
-// spare): the sequence is looked up again for every item.
+// A role's place in the CTA's share, in shared memory: the softmax warps have
+// no registers to spare for it, and a step must cost the issuing threads little.
 struct Walk {
-  long long left;
-  int b, kvh, t, j;  // t, j: of the next item
-  __device__ __forceinline__ Walk(const Plan &p, const Args &a)
-      : left(p.e - p.s), b(p.b), kvh(p.kvh), t(p.t), j(p.j) {}
-  __device__ __noinline__ bool next(Item &it, const Args &a) {
-    if (left <= 0) return false;  // more tiles left: another item follows, so b stays below B
-    it.s = seq_of(a, b);
-    if (t == it.s.nq) {
-      t = 0;
-      if (++kvh == a.c.Hkv) {
-        kvh = 0;
-        do it.s = seq_of(a, ++b);
-        while (it.s.nq == 0);
-      }
-    }
-    it.b = b;
-    it.kvh = kvh;
-    it.t = t++;
-    it.nt = tiles_of(it.s, it.t, a.TQ);
-    it.j0 = j;
-    j = 0;
-    it.j1 = static_cast<int>(min(static_cast<long long>(it.nt), it.j0 + left));
-    left -= it.j1 - it.j0;
-    return true;
+  long long left;  // key tiles
+  int b, kvh, t, j;
+  Seq s;
+  Item it;
+  int more;
+  __device__ __forceinline__ void begin(const Plan &p, const Args &a) {
+    left = p.e - p.s;
+    b = p.b;
+    kvh = p.kvh;
+    t = p.t;
+    j = p.j;
+    s = seq_of(a, b);
   }
 };
+
+// The next item into w->it, by a role's one thread (WARP = false) or by its warp.
+template <bool WARP>
+__device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
+  if (WARP) __syncwarp();  // every lane has read the item before
+  if (!WARP || (threadIdx.x & 31) == 0) {
+    const bool more = w->left > 0;  // then another item follows, and b stays below B
+    if (more) {
+      Seq s = w->s;
+      int t = w->t, kvh = w->kvh, b = w->b;
+      if (t == s.nq) {
+        t = 0;
+        if (++kvh == a.c.Hkv) {
+          kvh = 0;
+          do s = seq_of(a, ++b);
+          while (s.nq == 0);
+          w->s = s;
+          w->b = b;
+        }
+        w->kvh = kvh;
+      }
+      w->t = t + 1;
+      Item it;
+      it.b = b;
+      it.kvh = kvh;
+      it.t = t;
+      it.len = s.len;
+      it.row0 = s.first + t * a.TQ;
+      it.ntok = s.n - t * a.TQ;
+      it.pos0 = s.len - s.n + t * a.TQ;
+      it.nt = tiles_of(s, t, a.TQ);
+      it.j0 = w->j;
+      w->j = 0;
+      it.j1 = static_cast<int>(min(static_cast<long long>(it.nt), it.j0 + w->left));
+      w->left -= it.j1 - it.j0;
+      w->it = it;
+    }
+    w->more = more;
+  }
+  if (WARP) __syncwarp();
+  return w->more != 0;
+}
 
 // One warp: the CTA's share and where it starts.
 __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   const int c = blockIdx.x;
-  long long U = 0;
+  long long U = 0, u0 = 0;  // u0: sequence `lane`
   for (int i = lane; i < a.c.B; i += 32) {
     const Seq s = seq_of(a, i);
-    U += tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+    const long long u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+    if (i < 32) u0 = u;
+    U += u;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
-  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), U / a.min_units));
+  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), U / kMinTiles));
   Plan p;
   p.U = U;
   p.n = static_cast<int>(n);
@@ -202,10 +237,13 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
     long long base = 0;
     for (int i0 = 0; i0 < a.c.B; i0 += 32) {
       const int i = i0 + lane;
-      long long u = 0;
-      if (i < a.c.B) {
-        const Seq s = seq_of(a, i);
-        u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+      long long u = u0;
+      if (i0 > 0) {
+        u = 0;
+        if (i < a.c.B) {
+          const Seq s = seq_of(a, i);
+          u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+        }
       }
       long long inc = u;
 #pragma unroll
@@ -258,6 +296,15 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const A
   }
 }
 
+// Waits as calls, not copies: see mbar_poll.
+__device__ __noinline__ bool wait_one(uint32_t bar, uint32_t parity, const Abort &ab) {
+  return mbar_wait(bar, parity, ab);
+}
+// By a whole warp; the same answer in every lane.
+__device__ __noinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+}
+
 // 4-D tiled load (box and swizzle come from the tensor map).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
                                             int w, uint32_t bar) {
@@ -285,14 +332,16 @@ template <bool FP8>
 __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_r,
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const Args a) {
+                         const __grid_constant__ Args a) {
   using C = Cfg<FP8>;
   constexpr int NST = C::NST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   float *stat = reinterpret_cast<float *>(smem + C::OFF_STAT);  // [item parity][m, l, sigma][row]
+  static_assert(sizeof(Plan) <= 64 && sizeof(Walk) <= 112, "shared memory layout");
   Plan *plan = reinterpret_cast<Plan *>(smem + C::OFF_PLAN);
+  Walk *walks = reinterpret_cast<Walk *>(smem + C::OFF_WALK);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *q_full = bars;             // Q and R of the item loaded
   uint64_t *q_empty = bars + 1;        // the item's last S and T UMMAs done (count 2)
@@ -364,6 +413,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  if (threadIdx.x < 17) walks[threadIdx.x].begin(pl, a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -374,15 +424,17 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
 
   // Row (page, kv head) of the tensor maps of a key of the item; `beyond` for
   // keys behind its last one and for pages that do not exist (reported).
-  auto page_head = [&](const Item &it, int key) -> int {
-    if (key >= it.s.len) return beyond;
-    const int page = a.c.table[static_cast<long long>(it.b) * a.c.max_pages + (key >> shift)];
+  auto page_head = [&](const int *table, int key, int len, int kvh) -> int {
+    if (key >= len) return beyond;
+    const int page = table[key >> shift];
     if (page < 0 || page >= a.c.num_pages) {
       if (a.c.err) atomicOr(a.c.err, kErrBadInput);
       return beyond;
     }
-    return page * a.c.Hkv + it.kvh;
+    return page * a.c.Hkv + kvh;
   };
+  Walk *wk = &walks[warp];
+  const Item &it = wk->it;
   const int box = min(1 << shift, BN);  // keys of a box, as in the maps
 
   if (warp < 4) {
@@ -393,43 +445,55 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     const int rtok = row / a.G;
     int g = 0;
     bool ok = true;
-    Walk wk(pl, a);
-    Item it;
-    for (int k = 0; ok && wk.next(it, a); ++k) {
-      const int pos0 = it.s.len - it.s.n + it.t * a.TQ;  // position of the tile's first token
-      const int pos = pos0 + rtok;                       // the last key that this row sees
+    for (int k = 0; ok && walk_next<true>(wk, a); ++k) {
       float m_used = -INFINITY, l = 0.f, sg = 0.f;
-      // One key tile; the mask is a compile-time choice, so that the tiles
-      // below the diagonal run straight through. lim: keys of the tile that
-      // the row sees, valid: that exist.
-      auto tile = [&](auto mask_tag, int gg, int lim, int valid) -> bool {
-        constexpr bool MASK = decltype(mask_tag)::value;
-        const int x = gg & 1;
-        if (MASK && !FP8 && valid < BN) {
-          // The last tile: zero the V rows behind the last key.
-          const int st = gg % NST;
-          bool ok = mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab);
-          if (!__all_sync(0xffffffffu, ok)) return false;
-          const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
-          for (int i = max(valid, 0) * 8 + row; i < BN * 8; i += BM) {
-            st_shared_v4(vb + i * 16, 0u, 0u, 0u, 0u);
-            st_shared_v4(vb + HALF_KV + i * 16, 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        const bool ok = mbar_wait(smem_u32(&st_full[x]), (gg >> 1) & 1, ab);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        tc_fence_after();
+      const int n = it.j1 - it.j0;
+      for (int j = 0; ok && j < n; ++j) {
+        const int gg = g + j, x = gg & 1;
+        const int key0 = (it.j0 + j) * BN;
         const uint32_t cs = tl + (x ? COL_S1 : COL_S0);
+        ok = wait_all(smem_u32(&st_full[x]), (gg >> 1) & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        if (key0 + BN - 1 > it.pos0) {
+          // Some row does not see the whole tile: -inf into its S, in tensor
+          // memory, so that the code below is the same for all tiles (a
+          // second copy of it, specialised on the mask, held every SM at the
+          // instruction cache it shares). In a sequence's last tile T gets
+          // zeros behind the last key, where the pages may hold NaN, and so
+          // does V (bf16; converted tiles have them).
+          const int lim = it.pos0 + rtok - key0, valid = it.len - key0;
+#pragma unroll 1
+          for (int qq = 0; qq < 8; ++qq) {
+            if (qq >= 4 && valid >= BN) break;
+            const uint32_t col = cs + (qq < 4 ? 0 : COL_T - BN) + 16 * qq;
+            const int last = qq < 4 ? lim : valid - 1 + BN;
+            const float fill = qq < 4 ? -INFINITY : 0.f;
+            float s16[16];
+            tmem_ld16(col, s16);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s16[e] = 16 * qq + e <= last ? s16[e] : fill;
+            tmem_st16(col, *reinterpret_cast<uint32_t(*)[16]>(s16));
+          }
+          tmem_wait_st();
+          if (!FP8 && valid < BN) {
+            const int st = gg % NST;
+            ok = wait_all(smem_u32(&v_full[st]), (gg / NST) & 1, ab);
+            if (!ok) break;
+            const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
+#pragma unroll 1
+            for (int i = max(valid, 0) * 8 + row; i < BN * 8; i += BM) {
+              st_shared_v4(vb + i * 16, 0u, 0u, 0u, 0u);
+              st_shared_v4(vb + HALF_KV + i * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
         float s[64];
         tmem_ld32(cs, *reinterpret_cast<float(*)[32]>(&s[0]));
         tmem_ld32(cs + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
         tmem_wait_ld();
-        if (MASK) {
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (e >= lim) s[e] = -INFINITY;
-        }
         float mx8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(s[2 * e], s[2 * e + 1]);
@@ -445,9 +509,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           sg *= alpha;
           m_used = mt;
         }
-        if (gg > g && __any_sync(0xffffffffu, need)) {
-          bool ok = mbar_wait(smem_u32(&pv_done[(gg - 1) & 1]), ((gg - 1) >> 1) & 1, ab);
-          if (!__all_sync(0xffffffffu, ok)) return false;
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          ok = wait_all(smem_u32(&pv_done[(gg - 1) & 1]), ((gg - 1) >> 1) & 1, ab);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
           for (int part = 0; part < 8; ++part) {
@@ -469,12 +533,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           float t[16];
           tmem_ld16(cs + COL_T + 16 * qq, t);
           tmem_wait_ld();
-          if (MASK) {
-            // p = 0 there, but t may be NaN (slots behind the last key).
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (16 * qq + e >= lim) t[e] = 0.f;
-          }
           uint32_t pk[8], ptk[8];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
@@ -503,29 +561,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * x + 1]));
-        return true;
-      };
-      // Tiles that every row of the item sees whole, then the others.
-      const int n = it.j1 - it.j0, whole = min(n, max(0, (pos0 + 1) / BN - it.j0));
-      int j = 0;
-      for (; ok && j < whole; ++j) ok = tile(std::false_type{}, g + j, BN, BN);
-      for (; ok && j < n; ++j) {
-        const int key0 = (it.j0 + j) * BN;
-        ok = tile(std::true_type{}, g + j, pos - key0 + 1, it.s.len - key0);
       }
       // The epilogue must have read item k - 2's statistics before its buffer
       // is written again. It has once it released item k - 1's O, which the
       // item's own value UMMAs wait for too. (Items of one or two tiles would
       // otherwise let the softmax run two items ahead of a busy epilogue.)
-      if (ok && k > 0) ok = mbar_wait(smem_u32(o_free), (k - 1) & 1, ab);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (ok && k > 0) ok = wait_all(smem_u32(o_free), (k - 1) & 1, ab);
+      if (!ok) break;
       float *st = stat + (k & 1) * 3 * BM;
       st[row] = m_used;
       st[BM + row] = l;
       st[2 * BM + row] = sg;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&stat_full[k & 1]));
-      g += it.j1 - it.j0;
+      g += n;
     }
   } else if (warp < EP_WARP + 4) {
     // ------------------------------------------------------------ epilogue
@@ -533,16 +582,25 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     const int row = qw * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(qw * 32) << 16);
     const uint32_t stage = smem_u32(smem + C::OFF_OST + qw * 2048);
+    // Row `row` is token rtok and head rh of the group; a lane writes 16 bytes
+    // of rows qw * 32 + 8 i + lane / 4.
+    const int rtok = row / a.G, rh = row - rtok * a.G;
+    int otok[4];
+    long long ooff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int orow = qw * 32 + 8 * i + (lane >> 2), ot = orow / a.G;
+      otok[i] = ot < a.TQ ? ot : 0x7fffffff;
+      ooff[i] = ot * a.ots + (orow - ot * a.G) * a.ohs + (lane & 3) * 8;
+    }
     int g = 0;
     bool cut = false;  // the share ends inside an item that starts in it
-    Walk wk(pl, a);
-    Item it;
-    for (int k = 0; wk.next(it, a); ++k) {
+    for (int k = 0; walk_next<true>(wk, a); ++k) {
       const int glast = g + it.j1 - it.j0 - 1;
       g = glast + 1;
-      bool ok = mbar_wait(smem_u32(&stat_full[k & 1]), (k >> 1) & 1, ab);
-      ok = ok && mbar_wait(smem_u32(&pv_done[glast & 1]), (glast >> 1) & 1, ab);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!wait_all(smem_u32(&stat_full[k & 1]), (k >> 1) & 1, ab) ||
+          !wait_all(smem_u32(&pv_done[glast & 1]), (glast >> 1) & 1, ab))
+        break;
       tc_fence_after();
       const float *st = stat + (k & 1) * 3 * BM;
       const float m_used = st[row], l = st[BM + row], sg = st[2 * BM + row];
@@ -588,6 +646,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const float g1 = (1.f + sg * inv) * inv;
       // Output rows: 32 dims at a time through shared memory, so that four
       // lanes write 64 contiguous bytes of a row.
+      __nv_bfloat16 *base = a.out + it.row0 * a.ots + it.kvh * a.G * a.ohs;
+      const int ntok = it.ntok;
 #pragma unroll 1
       for (int part = 0; part < 4; ++part) {
         float o1[32], o2[32];
@@ -609,18 +669,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2), orow = qw * 32 + rr, ch = lane & 3;
+          const int rr = i * 8 + (lane >> 2);
           const uint4 v = *reinterpret_cast<const uint4 *>(smem + C::OFF_OST + qw * 2048 + rr * 64 +
-                                                          ((ch ^ ((rr >> 1) & 3)) << 4));
-          const int ot = orow / a.G, tok = it.t * a.TQ + ot;
-          if (ot < a.TQ && tok < it.s.n)
-            *reinterpret_cast<uint4 *>(a.out + (it.s.first + tok) * a.ots +
-                                       (it.kvh * a.G + orow - ot * a.G) * a.ohs + part * 32 + ch * 8) = v;
+                                                          (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          if (otok[i] < ntok) *reinterpret_cast<uint4 *>(base + ooff[i] + part * 32) = v;
         }
       }
-      const int ot = row / a.G, tok = it.t * a.TQ + ot;
-      if (a.lse != nullptr && ot < a.TQ && tok < it.s.n)
-        a.lse[static_cast<long long>(it.s.first + tok) * a.Hq + it.kvh * a.G + row - ot * a.G] =
+      if (a.lse != nullptr && rtok < a.TQ && rtok < it.ntok)
+        a.lse[static_cast<long long>(it.row0 + rtok) * a.Hq + it.kvh * a.G + rh] =
             l > 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
     if (!cut && warp == EP_WARP && lane == 0) a.table[4 * blockIdx.x] = -1;
@@ -635,14 +691,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t dout = tbase + (is_o1 ? COL_O1 : COL_O2);
       int g = 0;
       bool ok = true;
-      Walk wk(pl, a);
-      Item it;
-      for (int k = 0; ok && wk.next(it, a); ++k) {
+      for (int k = 0; ok && walk_next<false>(wk, a); ++k) {
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
           if (j == 0 && k > 0 && !mbar_poll(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
-          if (!mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (!wait_one(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
           if (!mbar_poll(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
@@ -680,16 +734,16 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       // page numbers are fetched when the one before it is issued. Its stage
       // held tile gl - NRAW, whose V all converter warps have left by the time
       // that the K of the tile after it is converted, so there is no wait.
-      Walk lw(pl, a);
-      Item lit;
+      Walk *lw = &walks[16];
+      const Item &lit = lw->it;
       int lj = 0, gl = 0, page[4];
-      bool more = FP8 && !is_s && lw.next(lit, a);
+      bool more = FP8 && !is_s && walk_next<false>(lw, a);
       auto fetch_pages = [&] {
         const int *table = a.c.table + static_cast<long long>(lit.b) * a.c.max_pages;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = lj * BN + i * box;
-          page[i] = i * box < BN && key < lit.s.len ? table[key >> shift] : a.c.num_pages;
+          page[i] = i * box < BN && key < lit.len ? table[key >> shift] : a.c.num_pages;
         }
       };
       if (more) {
@@ -707,43 +761,41 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if (i * box >= BN) continue;
           int z = beyond;
           if (page[i] >= 0 && page[i] < a.c.num_pages) z = page[i] * a.c.Hkv + lit.kvh;
-          else if (page[i] != a.c.num_pages || lj * BN + i * box < lit.s.len)
+          else if (page[i] != a.c.num_pages || lj * BN + i * box < lit.len)
             if (a.c.err) atomicOr(a.c.err, kErrBadInput);
           tma_load_3d(kb + i * box * 128, &tm_k, 0, slot, z, kf);
           tma_load_3d(vb + i * box * 128, &tm_v, 0, slot, z, vf);
         }
         ++gl;
         if (++lj == lit.j1) {
-          more = lw.next(lit, a);
+          more = walk_next<false>(lw, a);
           if (!more) return;
           lj = lit.j0;
         }
         fetch_pages();
       };
       while (more && gl < NRAW - 1) load_raw();
-      Walk wk(pl, a);
-      Item it;
-      for (int k = 0; ok && wk.next(it, a); ++k) {
+      for (int k = 0; ok && walk_next<false>(wk, a); ++k) {
         if (is_s) {
           // Q and R of the previous item are dead once its last S and T finish.
-          if (k > 0 && !mbar_wait(smem_u32(q_empty), (k - 1) & 1, ab)) break;
+          if (k > 0 && !wait_one(smem_u32(q_empty), (k - 1) & 1, ab)) break;
           mbar_arrive_expect_tx(qb, 4 * a.G * a.TQ * 128);
-          const int h0 = it.kvh * a.G, t0 = it.s.first + it.t * a.TQ;
+          const int h0 = it.kvh * a.G, t0 = it.row0;
           tma_load_3d(smem_u32(smem), &tm_q, 0, h0, t0, qb);
           tma_load_3d(smem_u32(smem + HALF_Q), &tm_q, 64, h0, t0, qb);
           tma_load_3d(smem_u32(smem + C::OFF_R), &tm_r, 0, h0, t0, qb);
           tma_load_3d(smem_u32(smem + C::OFF_R + HALF_Q), &tm_r, 64, h0, t0, qb);
           q_issued = k + 1;
         }
-        if (!mbar_wait(qb, k & 1, ab)) break;
+        if (!wait_one(qb, k & 1, ab)) break;
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
-          if (!mbar_wait(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (!wait_one(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
           if (FP8 && more) {  // (S: never)
             const int rs = gl % NRAW, par = ((gl / NRAW) - 1) & 1;
-            if (gl >= NRAW && (!mbar_wait(smem_u32(&rk_empty[rs]), par, ab) ||
-                               !mbar_wait(smem_u32(&rv_empty[rs]), par, ab))) { ok = false; break; }
+            if (gl >= NRAW && (!wait_one(smem_u32(&rk_empty[rs]), par, ab) ||
+                               !wait_one(smem_u32(&rv_empty[rs]), par, ab))) { ok = false; break; }
             load_raw();
           }
           if (gg >= 2 && !mbar_poll(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
@@ -778,24 +830,24 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t ring = smem_u32(smem + (is_k ? C::OFF_K : C::OFF_V));
       int g = 0;
       bool ok = true;
-      Walk wk(pl, a);
-      Item it;
-      while (ok && wk.next(it, a)) {
-        for (int j = it.j0; j < it.j1; ++j, ++g) {
+      while (ok && walk_next<false>(wk, a)) {
+        const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+        const int len = it.len, kvh = it.kvh, j1 = it.j1;
+        for (int j = it.j0; j < j1; ++j, ++g) {
           const int st = g % NST;
-          int z[4];  // the tile's boxes, looked up before the wait
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = i * box < BN ? page_head(it, j * BN + i * box) : beyond;
           const int slot = (j * BN) & pmask;  // 0 unless pages are larger than a tile
-          if (g >= NST && !mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
+          int z = page_head(table, j * BN, len, kvh);
+          if (g >= NST && !wait_one(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
           const uint32_t bar = smem_u32(&full[st]), dst = ring + st * TILE_KV;
           mbar_arrive_expect_tx(bar, TILE_KV);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i * box < BN) {
-              tma_load_4d(dst + i * box * 128, map, 0, slot, z[i], 0, bar);
-              tma_load_4d(dst + HALF_KV + i * box * 128, map, 0, slot, z[i], 1, bar);
-            }
+#pragma unroll 1
+          for (int i = 0;;) {
+            tma_load_4d(dst + i * 128, map, 0, slot, z, 0, bar);
+            tma_load_4d(dst + HALF_KV + i * 128, map, 0, slot, z, 1, bar);
+            i += box;
+            if (i >= BN) break;
+            z = page_head(table, j * BN + i, len, kvh);
+          }
         }
       }
       if (ab.raised()) {
@@ -823,11 +875,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     }
     int g = 0;
     bool ok = true;
-    Walk wk(pl, a);
-    Item it;
-    while (ok && wk.next(it, a)) {
+    while (ok && walk_next<true>(wk, a)) {
       const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-      const int len = it.s.len, kvh = it.kvh, j1 = it.j1;
+      const int len = it.len, kvh = it.kvh, j1 = it.j1;
       // The page of the warp's rows of a tile (16 rows never cross one), and
       // from it the scale bytes of rows r and r + 8 (0: a row that is not there):
       // looked up two tiles and one tile ahead.
@@ -857,23 +907,23 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         scales_of(j + 1, page_next, e_next);
         page_next = page_of(j + 2);
         const int rs = g % NRAW, st = g % NST;
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          ok = mbar_wait(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
+          ok = wait_all(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
           const uint8_t *raw = smem + C::OFF_RAW + (rs * 2 + kv) * RAW;
           uint4 x[2][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[i][h] = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * i);
-          if (ok && g >= NST) ok = mbar_wait(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          if (ok && g >= NST) ok = wait_all(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
+          if (!ok) break;
           const uint32_t dst = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K) + st * TILE_KV);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
             // need a second factor. E = 0: no row, zeros.
-            const int E = static_cast<int>(e4[2 * kv + i]);
+            const int E = static_cast<int>(kv ? e4[2 + i] : e4[i]);
             const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
             const uint32_t ff = f1 | (f1 << 16);
 #pragma unroll
@@ -1043,7 +1093,6 @@ cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void 
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.TQ = BM / a.G;
-  a.min_units = 4;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const int grid = sm_count();
   a.table = static_cast<int *>(workspace);
