@@ -296,7 +296,7 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const A
   }
 }
 
-// Waits as calls, not copies: see mbar_poll.
+// Waits off the tiles' critical path as calls, not copies: see mbar_poll.
 __device__ __noinline__ bool wait_one(uint32_t bar, uint32_t parity, const Abort &ab) {
   return mbar_wait(bar, parity, ab);
 }
@@ -447,22 +447,22 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     bool ok = true;
     for (int k = 0; ok && walk_next<true>(wk, a); ++k) {
       float m_used = -INFINITY, l = 0.f, sg = 0.f;
-      const int n = it.j1 - it.j0;
+      // From tile `whole` on, some row does not see all keys of a tile.
+      const int n = it.j1 - it.j0, whole = max(0, (it.pos0 + 1) / BN - it.j0);
       for (int j = 0; ok && j < n; ++j) {
         const int gg = g + j, x = gg & 1;
-        const int key0 = (it.j0 + j) * BN;
         const uint32_t cs = tl + (x ? COL_S1 : COL_S0);
-        ok = wait_all(smem_u32(&st_full[x]), (gg >> 1) & 1, ab);
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&st_full[x]), (gg >> 1) & 1, ab));
         if (!ok) break;
         tc_fence_after();
-        if (key0 + BN - 1 > it.pos0) {
-          // Some row does not see the whole tile: -inf into its S, in tensor
+        if (j >= whole) {
+          // -inf into the S of keys that a row does not see, in tensor
           // memory, so that the code below is the same for all tiles (a
           // second copy of it, specialised on the mask, held every SM at the
           // instruction cache it shares). In a sequence's last tile T gets
           // zeros behind the last key, where the pages may hold NaN, and so
           // does V (bf16; converted tiles have them).
-          const int lim = it.pos0 + rtok - key0, valid = it.len - key0;
+          const int key0 = (it.j0 + j) * BN, lim = it.pos0 + rtok - key0, valid = it.len - key0;
 #pragma unroll 1
           for (int qq = 0; qq < 8; ++qq) {
             if (qq >= 4 && valid >= BN) break;
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
           if (j == 0 && k > 0 && !mbar_poll(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
-          if (!wait_one(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
           if (!mbar_poll(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
-          if (!wait_one(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
           if (FP8 && more) {  // (S: never)
             const int rs = gl % NRAW, par = ((gl / NRAW) - 1) & 1;
             if (gl >= NRAW && (!wait_one(smem_u32(&rk_empty[rs]), par, ab) ||
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           const int st = g % NST;
           const int slot = (j * BN) & pmask;  // 0 unless pages are larger than a tile
           int z = page_head(table, j * BN, len, kvh);
-          if (g >= NST && !wait_one(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
+          if (g >= NST && !mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
           const uint32_t bar = smem_u32(&full[st]), dst = ring + st * TILE_KV;
           mbar_arrive_expect_tx(bar, TILE_KV);
 #pragma unroll 1
@@ -909,14 +909,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         const int rs = g % NRAW, st = g % NST;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          ok = wait_all(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
+          ok = mbar_wait(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
           const uint8_t *raw = smem + C::OFF_RAW + (rs * 2 + kv) * RAW;
           uint4 x[2][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[i][h] = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * i);
-          if (ok && g >= NST) ok = wait_all(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
+          if (ok && g >= NST) ok = mbar_wait(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t dst = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K) + st * TILE_KV);
 #pragma unroll
