@@ -144,7 +144,16 @@ struct Plan {
   long long U, s, e;  // key tiles of the batch; this CTA's share [s, e)
   int n;              // CTAs with work
   int b, kvh, t, j;   // where the share starts
+  // Rounds of whole items (> 0) instead of shares. When all sequences are alike
+  // and there are at least kRoundItems items a CTA, whole items, longest first
+  // and dealt in snake order, even out by themselves, and the CTAs of a round
+  // read the same keys at the same time (from the L2 of their own die, and
+  // without parts to merge). Measured on GB300: 1 x 16384 tokens 1618 us in
+  // shares, 1533 in rounds, 4 x 4096 457 and 419; with 1.7 items a CTA (2048
+  // tokens over 32768 keys) rounds would idle CTAs for 16% of the time.
+  int items;
 };
+constexpr int kRoundItems = 6;
 
 // A part of an item: key tiles [j0, j1) of its nt.
 struct Item {
@@ -158,12 +167,15 @@ struct Item {
 // no registers to spare for it, and a step must cost the issuing threads little.
 struct Walk {
   long long left;  // key tiles
+  int items, n;    // of the plan
   int b, kvh, t, j;
   Seq s;
   Item it;
   int more;
   __device__ __forceinline__ void begin(const Plan &p, const Args &a) {
     left = p.e - p.s;
+    items = p.items;
+    n = p.n;
     b = p.b;
     kvh = p.kvh;
     t = p.t;
@@ -177,11 +189,21 @@ template <bool WARP>
 __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
   if (WARP) __syncwarp();  // every lane has read the item before
   if (!WARP || (threadIdx.x & 31) == 0) {
-    const bool more = w->left > 0;  // then another item follows, and b stays below B
+    bool more = w->left > 0;  // then another item follows, and b stays below B
+    Seq s = w->s;
+    int t = w->t, kvh = w->kvh, b = w->b;
+    if (w->items > 0) {
+      // Round t of whole items.
+      const int c = blockIdx.x, o = t * w->n + ((t & 1) ? w->n - 1 - c : c), heads = a.c.B * a.c.Hkv;
+      more = o < w->items;
+      w->t = t + 1;
+      t = s.nq - 1 - o / heads;
+      b = (o % heads) / a.c.Hkv;
+      kvh = o % a.c.Hkv;
+      s.first = b * s.n;
+    }
     if (more) {
-      Seq s = w->s;
-      int t = w->t, kvh = w->kvh, b = w->b;
-      if (t == s.nq) {
+      if (w->items == 0 && t == s.nq) {
         t = 0;
         if (++kvh == a.c.Hkv) {
           kvh = 0;
@@ -192,7 +214,7 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
         }
         w->kvh = kvh;
       }
-      w->t = t + 1;
+      if (w->items == 0) w->t = t + 1;
       Item it;
       it.b = b;
       it.kvh = kvh;
@@ -204,8 +226,11 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
       it.nt = tiles_of(s, t, a.TQ);
       it.j0 = w->j;
       w->j = 0;
-      it.j1 = static_cast<int>(min(static_cast<long long>(it.nt), it.j0 + w->left));
-      w->left -= it.j1 - it.j0;
+      it.j1 = it.nt;
+      if (w->items == 0) {
+        it.j1 = static_cast<int>(min(static_cast<long long>(it.nt), it.j0 + w->left));
+        w->left -= it.j1 - it.j0;
+      }
       w->it = it;
     }
     w->more = more;
@@ -218,12 +243,16 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
 __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   const int c = blockIdx.x;
   long long U = 0, u0 = 0;  // u0: sequence `lane`
+  const Seq s0 = seq_of(a, 0);
+  bool alike = s0.nq > 0;
   for (int i = lane; i < a.c.B; i += 32) {
     const Seq s = seq_of(a, i);
     const long long u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
     if (i < 32) u0 = u;
     U += u;
+    alike = alike && s.n == s0.n && s.len == s0.len && s.first == i * s0.n;
   }
+  alike = __all_sync(0xffffffffu, alike);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
   const long long n = max(1ll, min(static_cast<long long>(gridDim.x), U / kMinTiles));
@@ -232,8 +261,12 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   p.n = static_cast<int>(n);
   p.s = c < n ? c * U / n : 0;
   p.e = c < n ? (c + 1) * U / n : 0;
-  p.b = p.kvh = p.t = p.j = 0;
-  if (p.s < p.e) {
+  p.b = p.kvh = p.t = p.j = p.items = 0;
+  const long long items = static_cast<long long>(s0.nq) * a.c.Hkv * a.c.B;
+  if (alike && items >= kRoundItems * static_cast<long long>(gridDim.x)) {
+    p.items = static_cast<int>(items);
+    p.n = gridDim.x;
+  } else if (p.s < p.e) {
     long long base = 0;
     for (int i0 = 0; i0 < a.c.B; i0 += 32) {
       const int i = i0 + lane;
@@ -313,6 +346,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// The box of a tiled load into L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // Codes 0, 1 (lo) and 2, 3 (hi) of a word as bf16 pairs, times 2^-120.
@@ -405,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Plan pl = *plan;
-  if (pl.s >= pl.e) {  // no share
+  if (pl.items == 0 && pl.s >= pl.e) {  // no share
     if (threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
     return;
   }
@@ -691,7 +732,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t dout = tbase + (is_o1 ? COL_O1 : COL_O2);
       int g = 0;
       bool ok = true;
-      for (int k = 0; ok && walk_next<false>(wk, a); ++k) {
+      bool more = walk_next<false>(wk, a);
+      for (int k = 0; ok && more; ++k) {
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
@@ -711,6 +753,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           umma_commit(smem_u32(&v_empty[st]));
           tc_fence_before();
           mbar_arrive(smem_u32(&pv_issued[2 * x + (is_o1 ? 0 : 1)]));
+          if (j == 0) more = walk_next<false>(wk, a);  // off the item boundary's path
         }
         g += nt;
       }
@@ -775,7 +818,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         fetch_pages();
       };
       while (more && gl < NRAW - 1) load_raw();
-      for (int k = 0; ok && walk_next<false>(wk, a); ++k) {
+      bool next = walk_next<false>(wk, a);
+      for (int k = 0; ok && next; ++k) {
+        const int nt = it.j1 - it.j0;
         if (is_s) {
           // Q and R of the previous item are dead once its last S and T finish.
           if (k > 0 && !wait_one(smem_u32(q_empty), (k - 1) & 1, ab)) break;
@@ -788,7 +833,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           q_issued = k + 1;
         }
         if (!wait_one(qb, k & 1, ab)) break;
-        const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NST;
           if (!mbar_wait(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
@@ -808,6 +852,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
                     kdesc + (ks >> 2) * (HALF_KV >> 4) + (ks & 3) * 2, idesc_st, ks > 0);
           umma_commit(smem_u32(&st_full[x]));
           umma_commit(smem_u32(&k_empty[st]));
+          if (j == 0) {
+            // The next item, off the item boundary's path, and its Q and R into
+            // L2: the boundary waits for their load.
+            next = walk_next<false>(wk, a);
+            if (is_s && next) {
+              const int h0 = it.kvh * a.G, t0 = it.row0;
+              tma_prefetch_3d(&tm_q, 0, h0, t0);
+              tma_prefetch_3d(&tm_q, 64, h0, t0);
+              tma_prefetch_3d(&tm_r, 0, h0, t0);
+              tma_prefetch_3d(&tm_r, 64, h0, t0);
+            }
+          }
         }
         if (ok) umma_commit(smem_u32(q_empty));  // Q / R of this item no longer read
         g += nt;
