@@ -6,8 +6,12 @@
 // a = 2^(x - 127) (1 + m / 128) in bf16, so E = x - 8, plus one if the
 // mantissa m is above 448 / 256 = 1.75's (96): integer arithmetic on the bits,
 // and the product with a power of two is exact, so a code has one rounding.
-// Both kernels only move memory: half a warp takes one row (16 lanes of 16
-// bytes of bf16), a warp the K and the V row of one (token, kv head).
+// Both kernels only move memory. A warp takes N consecutive packed rows of one
+// kv head, half of it K and half V (16 lanes of 16 bytes of bf16 a row): lane
+// n looks row n up (sequence, position, page), then all N loads are issued
+// before the first result is used. Consecutive rows of a head are contiguous in
+// their page, and the Hkv warps of a row group together read or write whole
+// contiguous rows on the other side.
 #include <string.h>
 
 #include "plx_paged.cuh"
@@ -27,42 +31,62 @@ struct AppendArgs {
   int T;
 };
 
-template <bool FP8>
+// Rows a warp handles: one when there are too few warps to fill the GPU twice
+// with more (a decode step's rows: latency), else eight (bytes in flight).
+// GB300: 34660 tokens x 8 heads to e4m3 %APP1% us with one, %APP8% with eight; 64
+// tokens %SM1% and %SM8%.
+int rows_per_warp(long long rows) { return rows < 16ll * WARPS * sm_count() ? 1 : 8; }
+
+template <bool FP8, int N>
 __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs a) {
   const int lane = threadIdx.x & 31, half = lane >> 4, sub = lane & 15;
-  const long long i = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  if (i >= static_cast<long long>(a.T) * a.c.Hkv) return;
-  const int t = static_cast<int>(i / a.c.Hkv), h = static_cast<int>(i - static_cast<long long>(t) * a.c.Hkv);
-  const int b = row_sequence(a.cu_q, a.c.B, t);
-  if (b < 0) return;
-  const int first = a.cu_q ? a.cu_q[b] : b, end = a.cu_q ? a.cu_q[b + 1] : b + 1;
-  const int pos = cache_len(a.c, a.seqlens, b) - end + t;
-  (void)first;
-  if (pos < 0) return;  // more new tokens than the cache is to hold: padding
-  const long long row = page_row(a.c, b, h, pos);
-  if (row < 0) return;
-  const __nv_bfloat16 *src = (half ? a.v : a.k) + t * a.token_stride + h * a.head_stride;
-  const uint4 x = *reinterpret_cast<const uint4 *>(src + sub * 8);
-  if (!FP8) {
-    *reinterpret_cast<uint4 *>((half ? a.vpages : a.kpages) + row * (2 * D) + sub * 16) = x;
-    return;
+  const long long w = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  const int h = static_cast<int>(w % a.c.Hkv);
+  const long long t0 = w / a.c.Hkv * N;
+  if (t0 >= a.T) return;
+  long long my_row = -1;
+  if (lane < N && t0 + lane < a.T) {
+    const int t = static_cast<int>(t0) + lane;
+    const int b = row_sequence(a.cu_q, a.c.B, t);
+    if (b >= 0) {
+      const int end = a.cu_q ? a.cu_q[b + 1] : b + 1;
+      const int pos = cache_len(a.c, a.seqlens, b) - end + t;
+      if (pos >= 0) my_row = page_row(a.c, b, h, pos);  // else padding
+    }
   }
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m2 = 0;
+  const __nv_bfloat16 *src = (half ? a.v : a.k) + t0 * a.token_stride + h * a.head_stride + sub * 8;
+  uint4 x[N];
+  long long row[N];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, w[e] & 0x7fff7fffu);
-  uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  for (int n = 0; n < N; ++n) {
+    row[n] = __shfl_sync(0xffffffffu, my_row, n);
+    x[n] = row[n] >= 0 ? *reinterpret_cast<const uint4 *>(src + n * a.token_stride) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint8_t *pages = half ? a.vpages : a.kpages;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m >= 0x7f80u && sub == 0 && a.c.err) atomicOr(a.c.err, kErrBadInput);  // inf or NaN
-  const int E = max(1, static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0));
-  const float f = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);  // 2^(127 - E)
-  uint32_t c[4];
+  for (int n = 0; n < N; ++n) {
+    if (!FP8) {
+      if (row[n] >= 0) *reinterpret_cast<uint4 *>(pages + row[n] * (2 * D) + sub * 16) = x[n];
+      continue;
+    }
+    const uint32_t wd[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+    uint32_t m2 = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = float2_to_e4m3x2(bf16lo(w[e]) * f, bf16hi(w[e]) * f);
-  *reinterpret_cast<uint2 *>((half ? a.vpages : a.kpages) + row * D + sub * 8) =
-      make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  if (sub == 0) (half ? a.vscale : a.kscale)[row] = static_cast<uint8_t>(E);
+    for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, wd[e] & 0x7fff7fffu);
+    uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m >= 0x7f80u && sub == 0 && a.c.err) atomicOr(a.c.err, kErrBadInput);  // inf or NaN
+    const int E = max(1, static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0));
+    const float f = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);  // 2^(127 - E)
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = float2_to_e4m3x2(bf16lo(wd[e]) * f, bf16hi(wd[e]) * f);
+    if (row[n] < 0) continue;
+    *reinterpret_cast<uint2 *>(pages + row[n] * D + sub * 8) =
+        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    if (sub == 0) (half ? a.vscale : a.kscale)[row[n]] = static_cast<uint8_t>(E);
+  }
 }
 
 struct ReadArgs {
@@ -72,38 +96,71 @@ struct ReadArgs {
   int T;
 };
 
-template <bool FP8>
+template <bool FP8, int N>
 __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
   const int lane = threadIdx.x & 31, half = lane >> 4, sub = lane & 15;
-  const long long i = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  if (i >= static_cast<long long>(a.T) * a.c.Hkv) return;
-  const int t = static_cast<int>(i / a.c.Hkv), h = static_cast<int>(i - static_cast<long long>(t) * a.c.Hkv);
-  const int b = row_sequence(a.cu_k, a.c.B, t);
-  if (b < 0) return;
-  const int pos = t - a.cu_k[b];
-  if (pos >= (static_cast<long long>(a.c.max_pages) << a.c.page_shift)) {
-    if (a.c.err) atomicOr(a.c.err, kErrBadInput);
-    return;
-  }
-  const long long row = page_row(a.c, b, h, pos);
-  if (row < 0) return;
-  const uint8_t *pages = static_cast<const uint8_t *>(half ? a.c.v : a.c.k);
-  uint4 x;
-  if (FP8) {
-    const uint2 c = *reinterpret_cast<const uint2 *>(pages + row * D + sub * 8);
-    const float f = scale_of((half ? a.c.vscale : a.c.kscale)[row]);
-    const uint32_t two[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 y = e4m3x2_to_float2(two[e]);
-      w[e] = pack_bf16x2(y.x * f, y.y * f);
+  const long long w = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  const int h = static_cast<int>(w % a.c.Hkv);
+  const long long t0 = w / a.c.Hkv * N;
+  if (t0 >= a.T) return;
+  long long my_row = -1;
+  if (lane < N && t0 + lane < a.T) {
+    const int t = static_cast<int>(t0) + lane;
+    const int b = row_sequence(a.cu_k, a.c.B, t);
+    if (b >= 0) {
+      const int pos = t - a.cu_k[b];
+      if (pos < (static_cast<long long>(a.c.max_pages) << a.c.page_shift)) my_row = page_row(a.c, b, h, pos);
+      else if (a.c.err) atomicOr(a.c.err, kErrBadInput);
     }
-    x = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    x = *reinterpret_cast<const uint4 *>(pages + row * (2 * D) + sub * 16);
   }
-  *reinterpret_cast<uint4 *>((half ? a.v : a.k) + i * D + sub * 8) = x;
+  const uint8_t *pages = static_cast<const uint8_t *>(half ? a.c.v : a.c.k);
+  const uint8_t *scales = half ? a.c.vscale : a.c.kscale;
+  uint4 x[N];
+  uint32_t E[N];
+  long long row[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    row[n] = __shfl_sync(0xffffffffu, my_row, n);
+    x[n] = make_uint4(0u, 0u, 0u, 0u);
+    E[n] = 0u;
+    if (row[n] < 0) continue;
+    if (FP8) {
+      const uint2 c = *reinterpret_cast<const uint2 *>(pages + row[n] * D + sub * 8);
+      x[n].x = c.x;
+      x[n].y = c.y;
+      E[n] = scales[row[n]];
+    } else {
+      x[n] = *reinterpret_cast<const uint4 *>(pages + row[n] * (2 * D) + sub * 16);
+    }
+  }
+  __nv_bfloat16 *out = (half ? a.v : a.k) + (t0 * a.c.Hkv + h) * D + sub * 8;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (row[n] < 0) continue;
+    if (FP8) {
+      const float f = scale_of(E[n]);
+      const uint32_t two[4] = {x[n].x & 0xffffu, x[n].x >> 16, x[n].y & 0xffffu, x[n].y >> 16};
+      uint32_t wd[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = e4m3x2_to_float2(two[e]);
+        wd[e] = pack_bf16x2(y.x * f, y.y * f);
+      }
+      x[n] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+    }
+    *reinterpret_cast<uint4 *>(out + static_cast<long long>(n) * a.c.Hkv * D) = x[n];
+  }
+}
+
+template <bool FP8, int N>
+void append(const AppendArgs &a, cudaStream_t stream) {
+  const long long warps = (static_cast<long long>(a.T) + N - 1) / N * a.c.Hkv;
+  kv_append_kernel<FP8, N><<<static_cast<unsigned>((warps + WARPS - 1) / WARPS), 32 * WARPS, 0, stream>>>(a);
+}
+template <bool FP8, int N>
+void read(const ReadArgs &a, cudaStream_t stream) {
+  const long long warps = (static_cast<long long>(a.T) + N - 1) / N * a.c.Hkv;
+  kv_read_kernel<FP8, N><<<static_cast<unsigned>((warps + WARPS - 1) / WARPS), 32 * WARPS, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -124,10 +181,9 @@ cudaError_t launch_kv_append(const PagedCache &c, const void *k, const void *v,
   a.seqlens = seqlens;
   a.cu_q = cu_q;
   a.T = T;
-  const long long rows = static_cast<long long>(T) * c.Hkv;
-  const unsigned grid = static_cast<unsigned>((rows + WARPS - 1) / WARPS);
-  if (c.kscale != nullptr) kv_append_kernel<true><<<grid, 32 * WARPS, 0, stream>>>(a);
-  else kv_append_kernel<false><<<grid, 32 * WARPS, 0, stream>>>(a);
+  const bool one = rows_per_warp(static_cast<long long>(T) * c.Hkv) == 1;
+  if (c.kscale != nullptr) one ? append<true, 1>(a, stream) : append<true, 8>(a, stream);
+  else one ? append<false, 1>(a, stream) : append<false, 8>(a, stream);
   return cudaGetLastError();
 }
 
@@ -139,10 +195,9 @@ cudaError_t launch_kv_read(const PagedCache &c, const int *cu_k, void *k, void *
   a.k = static_cast<__nv_bfloat16 *>(k);
   a.v = static_cast<__nv_bfloat16 *>(v);
   a.T = T;
-  const long long rows = static_cast<long long>(T) * c.Hkv;
-  const unsigned grid = static_cast<unsigned>((rows + WARPS - 1) / WARPS);
-  if (c.kscale != nullptr) kv_read_kernel<true><<<grid, 32 * WARPS, 0, stream>>>(a);
-  else kv_read_kernel<false><<<grid, 32 * WARPS, 0, stream>>>(a);
+  const bool one = rows_per_warp(static_cast<long long>(T) * c.Hkv) == 1;
+  if (c.kscale != nullptr) one ? read<true, 1>(a, stream) : read<true, 8>(a, stream);
+  else one ? read<false, 1>(a, stream) : read<false, 8>(a, stream);
   return cudaGetLastError();
 }
 

@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int OFF_STAT = OFF_RAW + (FP8 ? NRAW * 2 * RAW : 0);
   static constexpr int OFF_OST = OFF_STAT + 2 * 3 * BM * 4;  // per epilogue warp: 32 rows x 64 bytes
   static constexpr int OFF_PLAN = OFF_OST + 4 * 2048;
-  static constexpr int OFF_WALK = OFF_PLAN + 64;  // one per warp, one more for the raw loads
+  static constexpr int OFF_WALK = OFF_PLAN + 80;  // one per warp, one more for the raw loads
   static constexpr int OFF_BAR = OFF_WALK + 17 * 112;
   static constexpr int NBAR = 2 + 4 * NST + 2 + 4 + 2 + 4 + 1 + 2 + 4 + (FP8 ? 4 * NRAW : 0);
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
@@ -144,6 +144,7 @@ struct Plan {
   long long U, s, e;  // key tiles of the batch; this CTA's share [s, e)
   int n;              // CTAs with work
   int b, kvh, t, j;   // where the share starts
+  Seq first;          // sequence b
   // Rounds of whole items (> 0) instead of shares. When all sequences are alike
   // and there are at least kRoundItems items a CTA, whole items, longest first
   // and dealt in snake order, even out by themselves, and the CTAs of a round
@@ -172,7 +173,7 @@ struct Walk {
   Seq s;
   Item it;
   int more;
-  __device__ __forceinline__ void begin(const Plan &p, const Args &a) {
+  __device__ __forceinline__ void begin(const Plan &p) {
     left = p.e - p.s;
     items = p.items;
     n = p.n;
@@ -180,7 +181,7 @@ struct Walk {
     kvh = p.kvh;
     t = p.t;
     j = p.j;
-    s = seq_of(a, b);
+    s = p.first;
   }
 };
 
@@ -239,32 +240,51 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
   return w->more != 0;
 }
 
+// Lane l's sequence in every lane.
+__device__ __forceinline__ Seq seq_from(const Seq &s, int l) {
+  return Seq{__shfl_sync(0xffffffffu, s.len, l), __shfl_sync(0xffffffffu, s.first, l),
+             __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.nq, l)};
+}
 // One warp: the CTA's share and where it starts.
 __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   const int c = blockIdx.x;
-  long long U = 0, u0 = 0;  // u0: sequence `lane`
-  const Seq s0 = seq_of(a, 0);
-  bool alike = s0.nq > 0;
-  for (int i = lane; i < a.c.B; i += 32) {
-    const Seq s = seq_of(a, i);
-    const long long u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
-    if (i < 32) u0 = u;
-    U += u;
-    alike = alike && s.n == s0.n && s.len == s0.len && s.first == i * s0.n;
+  long long U = 0, u0 = 0;  // mine, u0: sequence `lane`
+  int items = 0;
+  Seq mine = {}, s0 = {};
+  bool alike = true;
+  for (int i0 = 0; i0 < a.c.B; i0 += 32) {
+    const int i = i0 + lane;
+    Seq s = {};
+    if (i < a.c.B) s = seq_of(a, i);
+    if (i0 == 0) s0 = seq_from(s, 0);
+    if (i < a.c.B) {
+      const long long u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+      if (i0 == 0) {
+        u0 = u;
+        mine = s;
+      }
+      U += u;
+      items += s.nq * a.c.Hkv;
+      alike = alike && s.n == s0.n && s.len == s0.len && s.first == i * s0.n;
+    }
   }
-  alike = __all_sync(0xffffffffu, alike);
+  alike = __all_sync(0xffffffffu, alike) && s0.nq > 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
-  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), U / kMinTiles));
+  // Shares of kMinTiles tiles at least, or of whole items where they are shorter.
+  const long long least = max(1ll, min(static_cast<long long>(kMinTiles), U / max(items, 1)));
+  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), U / least));
   Plan p;
   p.U = U;
   p.n = static_cast<int>(n);
   p.s = c < n ? c * U / n : 0;
   p.e = c < n ? (c + 1) * U / n : 0;
   p.b = p.kvh = p.t = p.j = p.items = 0;
-  const long long items = static_cast<long long>(s0.nq) * a.c.Hkv * a.c.B;
-  if (alike && items >= kRoundItems * static_cast<long long>(gridDim.x)) {
-    p.items = static_cast<int>(items);
+  p.first = s0;
+  if (alike && items >= kRoundItems * static_cast<int>(gridDim.x)) {
+    p.items = items;
     p.n = gridDim.x;
   } else if (p.s < p.e) {
     long long base = 0;
@@ -289,11 +309,12 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
         const int l = __ffs(hit) - 1;
         p.b = i0 + l;
         base += __shfl_sync(0xffffffffu, inc - u, l);
+        p.first = i0 == 0 ? seq_from(mine, l) : seq_of(a, p.b);
         break;
       }
       base += __shfl_sync(0xffffffffu, inc, 31);
     }
-    const Seq s = seq_of(a, p.b);
+    const Seq s = p.first;
     const long long head = tiles_before(s, s.nq, a.TQ), off = p.s - base;
     p.kvh = static_cast<int>(off / head);
     const long long in = off - p.kvh * head;
@@ -380,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   float *stat = reinterpret_cast<float *>(smem + C::OFF_STAT);  // [item parity][m, l, sigma][row]
-  static_assert(sizeof(Plan) <= 64 && sizeof(Walk) <= 112, "shared memory layout");
+  static_assert(sizeof(Plan) <= 80 && sizeof(Walk) <= 112, "shared memory layout");
   Plan *plan = reinterpret_cast<Plan *>(smem + C::OFF_PLAN);
   Walk *walks = reinterpret_cast<Walk *>(smem + C::OFF_WALK);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -443,22 +464,26 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       st_shared_v4(smem_u32(smem) + i * 16, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
-  __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Plan pl = *plan;
-  if (pl.items == 0 && pl.s >= pl.e) {  // no share
-    if (threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
-    return;
-  }
   if (warp == O1_WARP) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (threadIdx.x < 17) walks[threadIdx.x].begin(pl, a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Plan pl = *plan;
   const uint32_t tbase = *tmem_slot;
+  if (pl.items == 0 && pl.s >= pl.e) {  // no share
+    if (threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
+    if (warp == O1_WARP) tmem_dealloc(tbase, 512);
+    return;
+  }
+  if (lane == 0) {
+    walks[warp].begin(pl);
+    if (warp == S_WARP + 1) walks[16].begin(pl);
+  }
+  __syncwarp();
   const Abort ab{abort_flag, a.c.err};
   const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
   const int beyond = a.c.num_pages * a.c.Hkv;  // a box there reads nothing: zero fill
