@@ -50,26 +50,26 @@ constexpr int HALF_Q = BM * 64 * 2;
 constexpr int HALF_KV = BN * 64 * 2;
 constexpr int TILE_KV = 2 * HALF_KV;  // 16 KB: a bf16 K or V tile
 constexpr int RAW = BN * D;           // 8 KB: an e4m3 K or V tile
-constexpr int NRAW = 3;
+constexpr int NRAW = 4;               // raw stages (K and V together)
 constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_T = 64, COL_O1 = 256, COL_O2 = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int EP_WARP = 4, O1_WARP = 8, S_WARP = 10, LOAD_WARP = 12;
 
 template <bool FP8>
 struct Cfg {
-  static constexpr int NST = FP8 ? 3 : 4;  // bf16 K and V stages
+  static constexpr int NSK = FP8 ? 2 : 4, NSV = FP8 ? 3 : 4;  // bf16 K and V stages
   static constexpr int WARPS = FP8 ? 16 : 14;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int OFF_R = 2 * HALF_Q;
   static constexpr int OFF_K = 4 * HALF_Q;
-  static constexpr int OFF_V = OFF_K + NST * TILE_KV;
-  static constexpr int OFF_RAW = OFF_V + NST * TILE_KV;  // [NRAW][K, V]
+  static constexpr int OFF_V = OFF_K + NSK * TILE_KV;
+  static constexpr int OFF_RAW = OFF_V + NSV * TILE_KV;  // [NRAW][K, V]
   static constexpr int OFF_STAT = OFF_RAW + (FP8 ? NRAW * 2 * RAW : 0);
   static constexpr int OFF_OST = OFF_STAT + 2 * 3 * BM * 4;  // per epilogue warp: 32 rows x 64 bytes
   static constexpr int OFF_PLAN = OFF_OST + 4 * 2048;
   static constexpr int OFF_WALK = OFF_PLAN + 80;  // one per warp, one more for the raw loads
   static constexpr int OFF_BAR = OFF_WALK + 17 * 112;
-  static constexpr int NBAR = 2 + 4 * NST + 2 + 4 + 2 + 4 + 1 + 2 + 4 + (FP8 ? 4 * NRAW : 0);
+  static constexpr int NBAR = 2 + 2 * NSK + 2 * NSV + 2 + 4 + 2 + 4 + 1 + 2 + 4 + (FP8 ? 4 * NRAW : 0);
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ Args a) {
   using C = Cfg<FP8>;
-  constexpr int NST = C::NST;
+  constexpr int NSK = C::NSK, NSV = C::NSV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -407,11 +407,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *q_full = bars;             // Q and R of the item loaded
   uint64_t *q_empty = bars + 1;        // the item's last S and T UMMAs done (count 2)
-  uint64_t *k_full = bars + 2;         // bf16: TMA bytes; e4m3: count 4 (a lane per converter warp)
-  uint64_t *k_empty = k_full + NST;    // count 2 (S and T)
-  uint64_t *v_full = k_empty + NST;
-  uint64_t *v_empty = v_full + NST;    // count 2 (O1 and O2)
-  uint64_t *st_full = v_empty + NST;   // [2] count 2
+  uint64_t *k_full = bars + 2;         // bf16: TMA bytes; e4m3: count 2 (a lane per converter warp)
+  uint64_t *k_empty = k_full + NSK;    // count 2 (S and T)
+  uint64_t *v_full = k_empty + NSK;
+  uint64_t *v_empty = v_full + NSV;    // count 2 (O1 and O2)
+  uint64_t *st_full = v_empty + NSV;   // [2] count 2
   uint64_t *p_full = st_full + 2;      // [2][2] count 4: P of keys [32 h, 32 h + 32) of buffer x
   uint64_t *pv_done = p_full + 4;      // [2] count 2
   uint64_t *pv_issued = pv_done + 2;   // [2][2]
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   uint64_t *stat_full = o_free + 1;    // [2] count 4
   uint64_t *drain = stat_full + 2;     // [4]
   uint64_t *rk_full = drain + 4;       // e4m3: [NRAW] raw K loaded
-  uint64_t *rk_empty = rk_full + NRAW; // count 4
+  uint64_t *rk_empty = rk_full + NRAW; // count 2
   uint64_t *rv_full = rk_empty + NRAW;
   uint64_t *rv_empty = rv_full + NRAW;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::NBAR);
@@ -431,10 +431,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   if (threadIdx.x == 32) {
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 2);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(smem_u32(&k_full[s]), FP8 ? 4 : 1);
+    for (int s = 0; s < NSK; ++s) {
+      mbar_init(smem_u32(&k_full[s]), FP8 ? 2 : 1);
       mbar_init(smem_u32(&k_empty[s]), 2);
-      mbar_init(smem_u32(&v_full[s]), FP8 ? 4 : 1);
+    }
+    for (int s = 0; s < NSV; ++s) {
+      mbar_init(smem_u32(&v_full[s]), FP8 ? 2 : 1);
       mbar_init(smem_u32(&v_empty[s]), 2);
     }
     for (int x = 0; x < 2; ++x) {
@@ -451,9 +453,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     if (FP8)
       for (int s = 0; s < NRAW; ++s) {
         mbar_init(smem_u32(&rk_full[s]), 1);
-        mbar_init(smem_u32(&rk_empty[s]), 4);
+        mbar_init(smem_u32(&rk_empty[s]), 2);
         mbar_init(smem_u32(&rv_full[s]), 1);
-        mbar_init(smem_u32(&rv_empty[s]), 4);
+        mbar_init(smem_u32(&rv_empty[s]), 2);
       }
     *abort_flag = 0;
     fence_mbar_init();
@@ -544,8 +546,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           }
           tmem_wait_st();
           if (!FP8 && valid < BN) {
-            const int st = gg % NST;
-            ok = wait_all(smem_u32(&v_full[st]), (gg / NST) & 1, ab);
+            const int st = gg % NSV;
+            ok = wait_all(smem_u32(&v_full[st]), (gg / NSV) & 1, ab);
             if (!ok) break;
             const uint32_t vb = smem_u32(smem + C::OFF_V + st * TILE_KV);
 #pragma unroll 1
@@ -761,9 +763,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       for (int k = 0; ok && more; ++k) {
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
-          const int gg = g + j, x = gg & 1, st = gg % NST;
+          const int gg = g + j, x = gg & 1, st = gg % NSV;
           if (j == 0 && k > 0 && !mbar_poll(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
-          if (!mbar_wait(smem_u32(&v_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&v_full[st]), (gg / NSV) & 1, ab)) { ok = false; break; }
           if (!mbar_poll(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
@@ -798,14 +800,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t qb = smem_u32(q_full);
       int g = 0, q_issued = 0;
       bool ok = true;
-      // e4m3, T: the next raw tile to load is gl, key tile lj of item lit; its
-      // page numbers are fetched when the one before it is issued. Its stage
-      // held tile gl - NRAW, whose V all converter warps have left by the time
-      // that the K of the tile after it is converted, so there is no wait.
+      // e4m3, T: raw K of tile gl, key tile lj of item lit, is the next to load;
+      // raw V follows one tile behind, because V leaves the raw ring later.
+      // Page numbers are fetched when the tile before is issued. At tile gg
+      // this thread loads K of tile gg + NRAW - 1 and V of tile gg + NRAW - 2.
       Walk *lw = &walks[16];
       const Item &lit = lw->it;
-      int lj = 0, gl = 0, page[4];
-      bool more = FP8 && !is_s && walk_next<false>(lw, a);
+      int lj = 0, gl = 0, page[4], zv[4], vslot = 0;
+      bool more = FP8 && !is_s && walk_next<false>(lw, a), v_due = false;
       auto fetch_pages = [&] {
         const int *table = a.c.table + static_cast<long long>(lit.b) * a.c.max_pages;
 #pragma unroll
@@ -818,31 +820,44 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         lj = lit.j0;
         fetch_pages();
       }
-      auto load_raw = [&] {
-        const int st = gl % NRAW, slot = (lj * BN) & pmask;
-        const uint32_t kf = smem_u32(&rk_full[st]), vf = smem_u32(&rv_full[st]);
-        const uint32_t kb = smem_u32(smem + C::OFF_RAW + st * 2 * RAW), vb = kb + RAW;
-        mbar_arrive_expect_tx(kf, RAW);
-        mbar_arrive_expect_tx(vf, RAW);
+      auto load_v = [&]() -> bool {  // V of tile gl - 1
+        const int gv = gl - 1, st = gv % NRAW;
+        v_due = false;
+        if (gv >= NRAW && !mbar_wait(smem_u32(&rv_empty[st]), ((gv / NRAW) - 1) & 1, ab)) return false;
+        const uint32_t bar = smem_u32(&rv_full[st]), dst = smem_u32(smem + C::OFF_RAW + st * 2 * RAW + RAW);
+        mbar_arrive_expect_tx(bar, RAW);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i * box < BN) tma_load_3d(dst + i * box * 128, &tm_v, 0, vslot, zv[i], bar);
+        return true;
+      };
+      auto load_k = [&]() -> bool {  // K of tile gl
+        const int st = gl % NRAW;
+        if (gl >= NRAW && !mbar_wait(smem_u32(&rk_empty[st]), ((gl / NRAW) - 1) & 1, ab)) return false;
+        const uint32_t bar = smem_u32(&rk_full[st]), dst = smem_u32(smem + C::OFF_RAW + st * 2 * RAW);
+        vslot = (lj * BN) & pmask;
+        mbar_arrive_expect_tx(bar, RAW);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (i * box >= BN) continue;
-          int z = beyond;
-          if (page[i] >= 0 && page[i] < a.c.num_pages) z = page[i] * a.c.Hkv + lit.kvh;
+          zv[i] = beyond;
+          if (page[i] >= 0 && page[i] < a.c.num_pages) zv[i] = page[i] * a.c.Hkv + lit.kvh;
           else if (page[i] != a.c.num_pages || lj * BN + i * box < lit.len)
             if (a.c.err) atomicOr(a.c.err, kErrBadInput);
-          tma_load_3d(kb + i * box * 128, &tm_k, 0, slot, z, kf);
-          tma_load_3d(vb + i * box * 128, &tm_v, 0, slot, z, vf);
+          tma_load_3d(dst + i * box * 128, &tm_k, 0, vslot, zv[i], bar);
         }
         ++gl;
+        v_due = true;
         if (++lj == lit.j1) {
           more = walk_next<false>(lw, a);
-          if (!more) return;
+          if (!more) return true;
           lj = lit.j0;
         }
         fetch_pages();
+        return true;
       };
-      while (more && gl < NRAW - 1) load_raw();
+      auto load_step = [&]() -> bool { return (!v_due || load_v()) && (!more || load_k()); };
+      while (ok && more && gl < NRAW - 1) ok = load_step();
       bool next = walk_next<false>(wk, a);
       for (int k = 0; ok && next; ++k) {
         const int nt = it.j1 - it.j0;
@@ -859,14 +874,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         }
         if (!wait_one(qb, k & 1, ab)) break;
         for (int j = 0; j < nt; ++j) {
-          const int gg = g + j, x = gg & 1, st = gg % NST;
-          if (!mbar_wait(smem_u32(&k_full[st]), (gg / NST) & 1, ab)) { ok = false; break; }
-          if (FP8 && more) {  // (S: never)
-            const int rs = gl % NRAW, par = ((gl / NRAW) - 1) & 1;
-            if (gl >= NRAW && (!wait_one(smem_u32(&rk_empty[rs]), par, ab) ||
-                               !wait_one(smem_u32(&rv_empty[rs]), par, ab))) { ok = false; break; }
-            load_raw();
-          }
+          const int gg = g + j, x = gg & 1, st = gg % NSK;
+          if (!mbar_wait(smem_u32(&k_full[st]), (gg / NSK) & 1, ab)) { ok = false; break; }
+          if (FP8 && !is_s && !load_step()) { ok = false; break; }
           if (gg >= 2 && !mbar_poll(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t kdesc = kdesc0 + st * (TILE_KV >> 4);
@@ -898,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       if (q_issued > 0) mbar_wait_drain(qb, (q_issued - 1) & 1);  // this thread's own copies
       for (int gg = max(0, gl - NRAW); gg < gl; ++gg) {
         mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
-        mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
+        if (gg < gl - 1 || !v_due) mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
       }
     }
   } else if (!FP8) {
@@ -907,6 +917,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     if (lane == 0) {
       const bool is_k = warp == LOAD_WARP;
       const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+      static_assert(FP8 || NSK == NSV, "one loop for both rings");
       uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
       const uint32_t ring = smem_u32(smem + (is_k ? C::OFF_K : C::OFF_V));
       int g = 0;
@@ -915,10 +926,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
         const int len = it.len, kvh = it.kvh, j1 = it.j1;
         for (int j = it.j0; j < j1; ++j, ++g) {
-          const int st = g % NST;
+          const int st = g % NSK;
           const int slot = (j * BN) & pmask;  // 0 unless pages are larger than a tile
           int z = page_head(table, j * BN, len, kvh);
-          if (g >= NST && !mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab)) { ok = false; break; }
+          if (g >= NSK && !mbar_wait(smem_u32(&empty[st]), ((g / NSK) - 1) & 1, ab)) { ok = false; break; }
           const uint32_t bar = smem_u32(&full[st]), dst = ring + st * TILE_KV;
           mbar_arrive_expect_tx(bar, TILE_KV);
 #pragma unroll 1
@@ -933,107 +944,98 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       }
       if (ab.raised()) {
         // Let this thread's own copies land before the CTA exits.
-        for (int gg = max(0, g - NST); gg < g; ++gg)
-          mbar_wait_drain(smem_u32(&full[gg % NST]), (gg / NST) & 1);
+        for (int gg = max(0, g - NSK); gg < g; ++gg)
+          mbar_wait_drain(smem_u32(&full[gg % NSK]), (gg / NSK) & 1);
       }
     }
   } else {
     // ------------------------------------------------------------ e4m3: conversion
-    // A warp converts 16 of the tile's rows; a thread four 16-byte pieces of K
-    // and of V: rows r and r + 8, pieces c0 and c0 ^ 4. Lanes of odd rows start
-    // in the other half of the row, which keeps both the reads and the
-    // swizzled writes free of bank conflicts.
-    const int odd = (lane >> 2) & 1;
-    const int r = (warp - LOAD_WARP) * 16 + 2 * (lane >> 3) + odd, c0 = (lane & 3) + 4 * odd;
+    // Two warps convert K, two V, so that neither waits for the other's ring:
+    // a warp 32 of a tile's rows, a thread eight 16-byte pieces: of rows
+    // r + 8 i, i < 4, pieces c0 and c0 ^ 4. Lanes of odd rows start in the other
+    // half of the row, which keeps both the reads and the swizzled writes free
+    // of bank conflicts.
+    const int kv = warp & 1, odd = (lane >> 2) & 1, part = (warp - LOAD_WARP) >> 1;
+    const int r = part * 32 + 2 * (lane >> 3) + odd, c0 = (lane & 3) + 4 * odd;
     uint32_t from[2], to[2][2];  // offsets of the pieces of row r in a raw and in a bf16 tile
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = c0 ^ (4 * h);
-      from[h] = r * 128 + (c << 4);
+      from[h] = r * 128 + (c << 4) + kv * RAW;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         to[h][e] = (c >> 2) * HALF_KV + r * 128 + (((2 * (c & 3) + e) ^ (r & 7)) << 4);
     }
-    int g = 0;
+    const uint8_t *scales = kv ? a.c.vscale : a.c.kscale;
+    uint64_t *rfull = kv ? rv_full : rk_full, *rempty = kv ? rv_empty : rk_empty;
+    uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
+    const uint32_t ring = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K));
+    const int stages = kv ? NSV : NSK;
+    int g = 0, st = 0, turn = 0;  // tile, its stage, times round the ring
     bool ok = true;
     while (ok && walk_next<true>(wk, a)) {
       const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
       const int len = it.len, kvh = it.kvh, j1 = it.j1;
-      // The page of the warp's rows of a tile (16 rows never cross one), and
-      // from it the scale bytes of rows r and r + 8 (0: a row that is not there):
-      // looked up two tiles and one tile ahead.
+      // Lane l looks up the scale of row part 32 + l of a tile (0: a row that
+      // is not there), the page two tiles and the byte one tile ahead.
+      const int mine = part * 32 + lane;
       auto page_of = [&](int j) {
-        const int key = j * BN + (r & ~15);
+        const int key = j * BN + mine;
         return j < j1 && key < len ? table[key >> shift] : -1;
       };
-      auto scales_of = [&](int j, int page, uint32_t (&e)[4]) {
-        e[0] = e[1] = e[2] = e[3] = 0u;
-        if (page < 0 || page >= a.c.num_pages) return;
-        const int key = j * BN + r;
-        const long long at = ((static_cast<long long>(page) * a.c.Hkv + kvh) << shift) + (key & pmask);
-        if (key < len) {
-          e[0] = a.c.kscale[at];
-          e[2] = a.c.vscale[at];
-        }
-        if (key + 8 < len) {
-          e[1] = a.c.kscale[at + 8];
-          e[3] = a.c.vscale[at + 8];
-        }
+      auto scale_byte = [&](int j, int page) -> uint32_t {
+        if (page < 0 || page >= a.c.num_pages) return 0u;
+        return scales[((static_cast<long long>(page) * a.c.Hkv + kvh) << shift) + ((j * BN + mine) & pmask)];
       };
-      uint32_t e_next[4];
-      scales_of(it.j0, page_of(it.j0), e_next);
+      uint32_t e_next = scale_byte(it.j0, page_of(it.j0));
       int page_next = page_of(it.j0 + 1);
       for (int j = it.j0; j < j1; ++j, ++g) {
-        const uint32_t e4[4] = {e_next[0], e_next[1], e_next[2], e_next[3]};
-        scales_of(j + 1, page_next, e_next);
+        const uint32_t e_mine = e_next;
+        e_next = scale_byte(j + 1, page_next);
         page_next = page_of(j + 2);
-        const int rs = g % NRAW, st = g % NST;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = mbar_wait(smem_u32(kv ? &rv_full[rs] : &rk_full[rs]), (g / NRAW) & 1, ab);
-          const uint8_t *raw = smem + C::OFF_RAW + (rs * 2 + kv) * RAW;
-          uint4 x[2][2];
+        const int rs = g % NRAW;
+        ok = mbar_wait(smem_u32(&rfull[rs]), (g / NRAW) & 1, ab);
+        if (ok && turn > 0) ok = mbar_wait(smem_u32(&empty[st]), (turn - 1) & 1, ab);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t *raw = smem + C::OFF_RAW + rs * 2 * RAW;
+        const uint32_t dst = ring + st * TILE_KV;
+#pragma unroll 2
+        for (int i = 0; i < 4; ++i) {
+          // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
+          // need a second factor. E = 0: no row, zeros.
+          const int E = static_cast<int>(__shfl_sync(0xffffffffu, e_mine, 8 * i + (r & 7)));
+          const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
+          const uint32_t ff = f1 | (f1 << 16);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * i);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) x[i][h] = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * i);
-          if (ok && g >= NST) ok = mbar_wait(smem_u32(kv ? &v_empty[st] : &k_empty[st]), ((g / NST) - 1) & 1, ab);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint32_t dst = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K) + st * TILE_KV);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
-            // need a second factor. E = 0: no row, zeros.
-            const int E = static_cast<int>(kv ? e4[2 + i] : e4[i]);
-            const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
-            const uint32_t ff = f1 | (f1 << 16);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), ff);
-                y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), ff);
-              }
-              if (E > 134) {
-                const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f4 = f3 | (f3 << 16);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f4);
-              }
-              st_shared_v4(dst + to[h][0] + 1024 * i, y[0], y[1], y[2], y[3]);
-              st_shared_v4(dst + to[h][1] + 1024 * i, y[4], y[5], y[6], y[7]);
+            for (int e = 0; e < 4; ++e) {
+              y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), ff);
+              y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), ff);
             }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(kv ? &rv_empty[rs] : &rk_empty[rs]));
-            mbar_arrive(smem_u32(kv ? &v_full[st] : &k_full[st]));
+            if (E > 134) {
+              const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f4 = f3 | (f3 << 16);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f4);
+            }
+            st_shared_v4(dst + to[h][0] + 1024 * i, y[0], y[1], y[2], y[3]);
+            st_shared_v4(dst + to[h][1] + 1024 * i, y[4], y[5], y[6], y[7]);
           }
         }
-        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&full[st]));
+          mbar_arrive(smem_u32(&rempty[rs]));
+        }
+        if (++st == stages) {
+          st = 0;
+          ++turn;
+        }
       }
     }
   }
