@@ -29,10 +29,10 @@
 //     it the stored value, exactly.
 //
 // Warps: 0..3 softmax, 4..7 epilogue, 8 O1, 9 O2, 10 S (and the Q, R loads),
-// 11 T; bf16: 12 loads K, 13 loads V; e4m3: 12..15 convert, and the T thread
-// issues the raw loads (16 warps are what 128 registers a thread allow; a
-// converter warp that also loaded held the others up). Tensor memory as in
-// prefill_tc.cu.
+// 11 T; bf16: 12 loads K, 13 loads V; e4m3: 8 O1 and O2, 9 the raw loads,
+// 12..15 convert (16 warps are what 128 registers a thread allow; a converter
+// warp or the T thread that also loaded held the others up by about as long
+// as a tile takes). Tensor memory as in prefill_tc.cu.
 #include <math.h>
 #include <string.h>
 
@@ -67,8 +67,8 @@ struct Cfg {
   static constexpr int OFF_STAT = OFF_RAW + (FP8 ? NRAW * 2 * RAW : 0);
   static constexpr int OFF_OST = OFF_STAT + 2 * 3 * BM * 4;  // per epilogue warp: 32 rows x 64 bytes
   static constexpr int OFF_PLAN = OFF_OST + 4 * 2048;
-  static constexpr int OFF_WALK = OFF_PLAN + 80;  // one per warp, one more for the raw loads
-  static constexpr int OFF_BAR = OFF_WALK + 17 * 112;
+  static constexpr int OFF_WALK = OFF_PLAN + 80;  // one per warp
+  static constexpr int OFF_BAR = OFF_WALK + 16 * 112;
   static constexpr int NBAR = 2 + 2 * NSK + 2 * NSV + 2 + 4 + 2 + 4 + 1 + 2 + 4 + (FP8 ? 4 * NRAW : 0);
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -410,10 +410,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   uint64_t *k_full = bars + 2;         // bf16: TMA bytes; e4m3: count 2 (a lane per converter warp)
   uint64_t *k_empty = k_full + NSK;    // count 2 (S and T)
   uint64_t *v_full = k_empty + NSK;
-  uint64_t *v_empty = v_full + NSV;    // count 2 (O1 and O2)
+  uint64_t *v_empty = v_full + NSV;    // count 2 (O1 and O2; e4m3: one thread)
   uint64_t *st_full = v_empty + NSV;   // [2] count 2
   uint64_t *p_full = st_full + 2;      // [2][2] count 4: P of keys [32 h, 32 h + 32) of buffer x
-  uint64_t *pv_done = p_full + 4;      // [2] count 2
+  uint64_t *pv_done = p_full + 4;      // [2] as v_empty
   uint64_t *pv_issued = pv_done + 2;   // [2][2]
   uint64_t *o_free = pv_issued + 4;    // count 4: the epilogue has read O1 and O2
   uint64_t *stat_full = o_free + 1;    // [2] count 4
@@ -437,13 +437,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     }
     for (int s = 0; s < NSV; ++s) {
       mbar_init(smem_u32(&v_full[s]), FP8 ? 2 : 1);
-      mbar_init(smem_u32(&v_empty[s]), 2);
+      mbar_init(smem_u32(&v_empty[s]), FP8 ? 1 : 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&st_full[x]), 2);
       mbar_init(smem_u32(&p_full[2 * x]), 4);
       mbar_init(smem_u32(&p_full[2 * x + 1]), 4);
-      mbar_init(smem_u32(&pv_done[x]), 2);
+      mbar_init(smem_u32(&pv_done[x]), FP8 ? 1 : 2);
       mbar_init(smem_u32(&pv_issued[2 * x]), 1);
       mbar_init(smem_u32(&pv_issued[2 * x + 1]), 1);
       mbar_init(smem_u32(&stat_full[x]), 4);
@@ -483,7 +483,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   }
   if (lane == 0) {
     walks[warp].begin(pl);
-    if (warp == S_WARP + 1) walks[16].begin(pl);
   }
   __syncwarp();
   const Abort ab{abort_flag, a.c.err};
@@ -750,13 +749,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     if (!cut && warp == EP_WARP && lane == 0) a.table[4 * blockIdx.x] = -1;
   } else if (warp < S_WARP) {
     // ------------------------------------------------------------ value UMMAs
-    // Warp O1_WARP: O1 += P V (P over S); the next: O2 += (P o T) V (over T).
-    if (lane == 0) {
-      const bool is_o1 = warp == O1_WARP;
+    // O1 += P V (P over S) and O2 += (P o T) V (over T): bf16 by a thread each,
+    // e4m3 both by warp O1_WARP's, while the next warp's loads the raw tiles.
+    if (lane == 0 && !(FP8 && warp != O1_WARP)) {
+      const int first = FP8 ? 0 : warp - O1_WARP, count = FP8 ? 2 : 1;
       constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 1);
       const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), HALF_KV, 1024);
-      const uint32_t col_off = is_o1 ? 0u : COL_T;
-      const uint32_t dout = tbase + (is_o1 ? COL_O1 : COL_O2);
       int g = 0;
       bool ok = true;
       bool more = walk_next<false>(wk, a);
@@ -766,27 +764,71 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           const int gg = g + j, x = gg & 1, st = gg % NSV;
           if (j == 0 && k > 0 && !mbar_poll(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
           if (!mbar_wait(smem_u32(&v_full[st]), (gg / NSV) & 1, ab)) { ok = false; break; }
-          if (!mbar_poll(smem_u32(&p_full[2 * x]), (gg >> 1) & 1, ab)) { ok = false; break; }
-          tc_fence_after();
           const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
-          const uint32_t ap = tbase + (x ? COL_S1 : COL_S0) + col_off;
+          const uint32_t ap = tbase + (x ? COL_S1 : COL_S0);
 #pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks) {
-            if (ks == 2 && !mbar_poll(smem_u32(&p_full[2 * x + 1]), (gg >> 1) & 1, ab)) { ok = false; break; }
-            umma_ts(dout, ap + ks * 8, vdesc + ks * (2048 >> 4), idesc_pv, (j > 0 || ks > 0));
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_poll(smem_u32(&p_full[2 * x + h]), (gg >> 1) & 1, ab)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < count; ++c) {
+              const int which = first + c;
+              const uint32_t dout = tbase + (which ? COL_O2 : COL_O1), src = ap + (which ? COL_T : 0);
+#pragma unroll
+              for (int ks = 2 * h; ks < 2 * h + 2; ++ks)
+                umma_ts(dout, src + ks * 8, vdesc + ks * (2048 >> 4), idesc_pv, (j > 0 || ks > 0));
+            }
           }
           if (!ok) break;
           umma_commit(smem_u32(&pv_done[x]));
           umma_commit(smem_u32(&v_empty[st]));
           tc_fence_before();
-          mbar_arrive(smem_u32(&pv_issued[2 * x + (is_o1 ? 0 : 1)]));
+          mbar_arrive(smem_u32(&pv_issued[2 * x + first]));
+          if (FP8) mbar_arrive(smem_u32(&pv_issued[2 * x + 1]));
           if (j == 0) more = walk_next<false>(wk, a);  // off the item boundary's path
         }
         g += nt;
       }
       // Every UMMA this thread issued must finish before TMEM is released.
-      umma_commit(smem_u32(&drain[is_o1 ? 0 : 1]));
-      mbar_wait_drain(smem_u32(&drain[is_o1 ? 0 : 1]), 0);
+      umma_commit(smem_u32(&drain[first]));
+      mbar_wait_drain(smem_u32(&drain[first]), 0);
+    } else if (FP8 && warp != O1_WARP && lane == 0) {
+      // ---------------------------------------------------------- raw loads
+      int g = 0, issued[2] = {0, 0};  // tiles of K and V
+      bool ok = true;
+      while (ok && walk_next<false>(wk, a)) {
+        const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+        const int len = it.len, kvh = it.kvh, j1 = it.j1;
+        for (int j = it.j0; j < j1; ++j, ++g) {
+          const int st = g % NRAW, slot = (j * BN) & pmask;
+          int z[4];  // the tile's boxes, looked up before the waits
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = i * box < BN ? page_head(table, j * BN + i * box, len, kvh) : beyond;
+          uint32_t dst = smem_u32(smem + C::OFF_RAW + st * 2 * RAW);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t bar = smem_u32(kv ? &rv_full[st] : &rk_full[st]);
+            if (g >= NRAW && !mbar_wait(smem_u32(kv ? &rv_empty[st] : &rk_empty[st]), ((g / NRAW) - 1) & 1, ab)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar, RAW);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i * box < BN) tma_load_3d(dst + i * box * 128, kv ? &tm_v : &tm_k, 0, slot, z[i], bar);
+            dst += RAW;
+            kv ? ++issued[1] : ++issued[0];
+          }
+          if (!ok) break;
+        }
+      }
+      if (ab.raised()) {
+        // Let this thread's own copies land before the CTA exits.
+        for (int gg = max(0, issued[0] - NRAW); gg < issued[0]; ++gg)
+          mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
+        for (int gg = max(0, issued[1] - NRAW); gg < issued[1]; ++gg)
+          mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
+      }
     }
   } else if (warp < LOAD_WARP) {
     // ------------------------------------------------------------ score UMMAs
@@ -800,64 +842,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t qb = smem_u32(q_full);
       int g = 0, q_issued = 0;
       bool ok = true;
-      // e4m3, T: raw K of tile gl, key tile lj of item lit, is the next to load;
-      // raw V follows one tile behind, because V leaves the raw ring later.
-      // Page numbers are fetched when the tile before is issued. At tile gg
-      // this thread loads K of tile gg + NRAW - 1 and V of tile gg + NRAW - 2.
-      Walk *lw = &walks[16];
-      const Item &lit = lw->it;
-      int lj = 0, gl = 0, page[4], zv[4], vslot = 0;
-      bool more = FP8 && !is_s && walk_next<false>(lw, a), v_due = false;
-      auto fetch_pages = [&] {
-        const int *table = a.c.table + static_cast<long long>(lit.b) * a.c.max_pages;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = lj * BN + i * box;
-          page[i] = i * box < BN && key < lit.len ? table[key >> shift] : a.c.num_pages;
-        }
-      };
-      if (more) {
-        lj = lit.j0;
-        fetch_pages();
-      }
-      auto load_v = [&]() -> bool {  // V of tile gl - 1
-        const int gv = gl - 1, st = gv % NRAW;
-        v_due = false;
-        if (gv >= NRAW && !mbar_wait(smem_u32(&rv_empty[st]), ((gv / NRAW) - 1) & 1, ab)) return false;
-        const uint32_t bar = smem_u32(&rv_full[st]), dst = smem_u32(smem + C::OFF_RAW + st * 2 * RAW + RAW);
-        mbar_arrive_expect_tx(bar, RAW);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i * box < BN) tma_load_3d(dst + i * box * 128, &tm_v, 0, vslot, zv[i], bar);
-        return true;
-      };
-      auto load_k = [&]() -> bool {  // K of tile gl
-        const int st = gl % NRAW;
-        if (gl >= NRAW && !mbar_wait(smem_u32(&rk_empty[st]), ((gl / NRAW) - 1) & 1, ab)) return false;
-        const uint32_t bar = smem_u32(&rk_full[st]), dst = smem_u32(smem + C::OFF_RAW + st * 2 * RAW);
-        vslot = (lj * BN) & pmask;
-        mbar_arrive_expect_tx(bar, RAW);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i * box >= BN) continue;
-          zv[i] = beyond;
-          if (page[i] >= 0 && page[i] < a.c.num_pages) zv[i] = page[i] * a.c.Hkv + lit.kvh;
-          else if (page[i] != a.c.num_pages || lj * BN + i * box < lit.len)
-            if (a.c.err) atomicOr(a.c.err, kErrBadInput);
-          tma_load_3d(dst + i * box * 128, &tm_k, 0, vslot, zv[i], bar);
-        }
-        ++gl;
-        v_due = true;
-        if (++lj == lit.j1) {
-          more = walk_next<false>(lw, a);
-          if (!more) return true;
-          lj = lit.j0;
-        }
-        fetch_pages();
-        return true;
-      };
-      auto load_step = [&]() -> bool { return (!v_due || load_v()) && (!more || load_k()); };
-      while (ok && more && gl < NRAW - 1) ok = load_step();
       bool next = walk_next<false>(wk, a);
       for (int k = 0; ok && next; ++k) {
         const int nt = it.j1 - it.j0;
@@ -876,7 +860,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NSK;
           if (!mbar_wait(smem_u32(&k_full[st]), (gg / NSK) & 1, ab)) { ok = false; break; }
-          if (FP8 && !is_s && !load_step()) { ok = false; break; }
           if (gg >= 2 && !mbar_poll(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t kdesc = kdesc0 + st * (TILE_KV >> 4);
@@ -906,10 +889,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       umma_commit(smem_u32(&drain[is_s ? 2 : 3]));
       mbar_wait_drain(smem_u32(&drain[is_s ? 2 : 3]), 0);
       if (q_issued > 0) mbar_wait_drain(qb, (q_issued - 1) & 1);  // this thread's own copies
-      for (int gg = max(0, gl - NRAW); gg < gl; ++gg) {
-        mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
-        if (gg < gl - 1 || !v_due) mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
-      }
     }
   } else if (!FP8) {
     // ------------------------------------------------------------ K, V loads
@@ -969,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     const uint8_t *scales = kv ? a.c.vscale : a.c.kscale;
     uint64_t *rfull = kv ? rv_full : rk_full, *rempty = kv ? rv_empty : rk_empty;
     uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
-    const uint32_t ring = smem_u32(smem + (kv ? C::OFF_V : C::OFF_K));
+    uint8_t *ring = smem + (kv ? C::OFF_V : C::OFF_K);
     const int stages = kv ? NSV : NSK;
     int g = 0, st = 0, turn = 0;  // tile, its stage, times round the ring
     bool ok = true;
@@ -999,31 +978,40 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint8_t *raw = smem + C::OFF_RAW + rs * 2 * RAW;
-        const uint32_t dst = ring + st * TILE_KV;
-#pragma unroll 2
-        for (int i = 0; i < 4; ++i) {
-          // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
-          // need a second factor. E = 0: no row, zeros.
-          const int E = static_cast<int>(__shfl_sync(0xffffffffu, e_mine, 8 * i + (r & 7)));
-          const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
-          const uint32_t ff = f1 | (f1 << 16);
+        uint8_t *tile = ring + st * TILE_KV;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 4; i0 += 2) {  // four pieces in flight
+          uint4 x[2][2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * i);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), ff);
-              y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), ff);
+            for (int h = 0; h < 2; ++h)
+              x[i][h] = *reinterpret_cast<const uint4 *>(raw + from[h] + 1024 * (i0 + i));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // 2^(E - 7) as a bf16 pair; rows with E > 134 (values above 57344)
+            // need a second factor. E = 0: no row, zeros.
+            const int E = static_cast<int>(__shfl_sync(0xffffffffu, e_mine, 8 * (i0 + i) + (r & 7)));
+            const uint32_t f1 = E == 0 ? 0u : static_cast<uint32_t>(min(E + 120, 254)) << 7;
+            const uint32_t ff = f1 | (f1 << 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[2 * e] = mul_bf16x2(codes_bf16<0x9180>(w[e]), ff);
+                y[2 * e + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[e]), ff);
+              }
+              if (E > 134) {
+                const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f4 = f3 | (f3 << 16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f4);
+              }
+              uint8_t *at = tile + 1024 * (i0 + i);
+              *reinterpret_cast<uint4 *>(at + to[h][0]) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4 *>(at + to[h][1]) = make_uint4(y[4], y[5], y[6], y[7]);
             }
-            if (E > 134) {
-              const uint32_t f3 = static_cast<uint32_t>(127 + E - 134) << 7, f4 = f3 | (f3 << 16);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f4);
-            }
-            st_shared_v4(dst + to[h][0] + 1024 * i, y[0], y[1], y[2], y[3]);
-            st_shared_v4(dst + to[h][1] + 1024 * i, y[4], y[5], y[6], y[7]);
           }
         }
         fence_proxy_async_smem();
