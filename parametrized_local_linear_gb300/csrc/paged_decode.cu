@@ -53,23 +53,25 @@ constexpr int NCW = 4;          // consumer warps
 constexpr int GMAX = 8;         // query rows of a group
 constexpr int NST = 2 * NCW;    // ring stages; tile i goes to warp i % NCW and stage i % NST
 constexpr int THREADS = 32 * (NCW + 1);
-constexpr int RS = D + 8;       // floats of a row of partials in shared memory (bank spread)
 constexpr int REC = 2 * D + 2;  // floats of a record: O1 / l, O2 / l, sigma / l, log2-sum-exp
 constexpr float k2p56 = 72057594037927936.f;  // 2^56 = 2^120 / 2^64
 
 // Shared memory. The stages (K rows and V rows of a tile, 4 KB each) come
-// first: the 128-byte-swizzled boxes need 1024-byte alignment.
+// first: the 128-byte-swizzled boxes need 1024-byte alignment. An item's
+// partial sums are merged through the stages of its warps' last tiles, which
+// are released only then: 8 rows x 256 floats are just a stage.
 constexpr int TILE = 4096;
-constexpr int OFF_MLS = NST * 2 * TILE;
-constexpr int OFF_BAR = OFF_MLS + NCW * GMAX * 3 * 4;
-constexpr int OFF_FLAG = OFF_BAR + 2 * NST * 8;
-constexpr int OFF_PLAN = OFF_FLAG + 16;
-constexpr int OFF_RED = OFF_PLAN + 64;
+constexpr int OFF_QB = NST * 2 * TILE;               // two blocks of columns: the item's query fragments
+constexpr int qb_bytes(int nb) { return nb == 2 ? 2 * 8 * 32 * 8 : 0; }
+constexpr int mls_off(int nb) { return OFF_QB + qb_bytes(nb); }  // [NCW][GMAX] m, l, sigma, weight
+constexpr int bar_off(int nb) { return mls_off(nb) + NCW * GMAX * 16; }
+constexpr int flag_off(int nb) { return bar_off(nb) + 2 * NST * 8; }
+constexpr int plan_off(int nb) { return flag_off(nb) + 16; }
+constexpr int held_off(int nb) { return plan_off(nb) + 64; }     // [NCW] stage that holds a warp's sums
+constexpr size_t rows_smem(int nb) { return held_off(nb) + 16 + 1024; }
 static_assert(NST % NCW == 0, "each stage must belong to one consumer warp");
-constexpr size_t rows_smem(int gs) { return OFF_RED + size_t(NCW) * gs * RS * 4 + 1024; }
-// CTAs of an SM: with one block of columns three fit its registers (128 a
-// thread) and shared memory, with two blocks two.
-constexpr int ctas_per_sm(int nb) { return nb == 1 ? 3 : 2; }
+static_assert(2 * TILE == GMAX * 2 * D * 4, "a stage holds a warp's sums");
+constexpr int kCtasPerSm = 3;  // 128 registers a thread, 72 KB of shared memory
 
 struct RowsArgs {
   PagedCache c;
@@ -226,17 +228,17 @@ __device__ __forceinline__ int row_shift(float m) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 template <bool FP8, int NB>
-__global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
+__global__ void __launch_bounds__(THREADS, kCtasPerSm)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const RowsArgs a) {
   constexpr int KT = FP8 ? 32 : 16;  // keys of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + bar_off(NB));
   uint64_t *empty = full + NST;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_FLAG);
-  Plan *plan = reinterpret_cast<Plan *>(smem + OFF_PLAN);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + flag_off(NB));
+  Plan *plan = reinterpret_cast<Plan *>(smem + plan_off(NB));
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -405,8 +407,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
   const int g = lane >> 2, tq = lane & 3;
   const int gs = a.gs;
   constexpr int MT = KT / 16;  // m tiles of 16 keys
-  float *red = reinterpret_cast<float *>(smem + OFF_RED);  // [NCW][gs][RS]
-  float *mls = reinterpret_cast<float *>(smem + OFF_MLS);  // [NCW][GMAX][3]
+  float *mls = reinterpret_cast<float *>(smem + mls_off(NB));
+  volatile int *held = reinterpret_cast<volatile int *>(smem + held_off(NB));
+  uint2 *qsm = reinterpret_cast<uint2 *>(smem + OFF_QB);  // [nb][kk][lane]
   Walk<KT> wk(pl, a);
   Item it;
   int gt = 0;  // tiles of the previous items
@@ -428,37 +431,52 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
                             (key & ((1 << a.c.page_shift) - 1));
       return a.c.kscale[row] | (static_cast<uint32_t>(a.c.vscale[row]) << 8);
     };
-    uint32_t sc_next = 0u;
-    int page_next = -1;
+    // In the order that overlaps their latencies: page numbers, query rows,
+    // scale bytes.
+    int page_first = -1, page_next = -1;
     if constexpr (FP8) {
-      sc_next = scales_of(t_first, page_of(t_first));
+      page_first = page_of(t_first);
       page_next = page_of(t_first + NCW);
     }
     // Column g of block nb is q (even g) or r (odd g) of row 4 nb + g / 2;
     // this thread's scores are those of row 4 nb + tq.
-    uint32_t qb[NB][8][2];
+    // With two blocks of columns the fragments live in shared memory, each
+    // warp writing two of the eight steps.
+    uint32_t qb[NB == 1 ? 8 : 1][2];
     float fs[NB], ft[NB];  // what the scores and the probe products still lack
     int last[NB];          // the last key that row 4 nb + tq sees (< 0: none)
     const int all_see = it.s.len - it.s.n + r0 / a.G;  // keys up to here are seen by all rows
+    uint2 xq[NB][8];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = 4 * nb + (g >> 1);
       const bool live = row < nr;
       const int tok = (r0 + (live ? row : 0)) / a.G, h = it.kvh * a.G + (r0 + (live ? row : 0)) % a.G;
       const __nv_bfloat16 *src = ((g & 1) ? a.r : a.q) + (it.s.first + tok) * a.qts + h * a.qhs;
+      // e4m3: slots 2 tq, 2 tq + 1 hold dims 4 tq, 4 tq + 1 and slots + 8 dims
+      // 4 tq + 2, 4 tq + 3 of the 16, as the codes' words do.
+      const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        if (!live) xq[nb][kk] = make_uint2(0u, 0u);
+        else if (FP8) xq[nb][kk] = *reinterpret_cast<const uint2 *>(src + 16 * kk + 4 * tq);
+        else xq[nb][kk] = make_uint2(w[8 * kk + tq], w[8 * kk + 4 + tq]);
+      }
+      const int mine = 4 * nb + tq;
+      last[nb] = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
+    }
+    uint32_t sc_next = 0u;
+    if constexpr (FP8) sc_next = scales_of(t_first, page_first);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
       fs[nb] = a.scale_log2;
       ft[nb] = 1.f;
       if constexpr (FP8) {
-        // Slots 2 tq, 2 tq + 1 hold dims 4 tq, 4 tq + 1 and slots + 8 dims
-        // 4 tq + 2, 4 tq + 3 of the 16, as the codes' words do.
-        uint2 x[8];
         float mx = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          x[kk] = live ? *reinterpret_cast<const uint2 *>(src + 16 * kk + 4 * tq) : make_uint2(0u, 0u);
-          mx = fmax3(mx, fmaxf(fabsf(bf16lo(x[kk].x)), fabsf(bf16hi(x[kk].x))),
-                     fmaxf(fabsf(bf16lo(x[kk].y)), fabsf(bf16hi(x[kk].y))));
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          mx = fmax3(mx, fmaxf(fabsf(bf16lo(xq[nb][kk].x)), fabsf(bf16hi(xq[nb][kk].x))),
+                     fmaxf(fabsf(bf16lo(xq[nb][kk].y)), fabsf(bf16hi(xq[nb][kk].y))));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int up = row_shift(mx);
@@ -466,21 +484,25 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
         fs[nb] *= __shfl_sync(0xffffffffu, back, 8 * tq);      // column 2 tq
         ft[nb] *= __shfl_sync(0xffffffffu, back, 8 * tq + 4);  // column 2 tq + 1
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          qb[nb][kk][0] = pack_f16x2(bf16lo(x[kk].x) * u, bf16hi(x[kk].x) * u);
-          qb[nb][kk][1] = pack_f16x2(bf16lo(x[kk].y) * u, bf16hi(x[kk].y) * u);
-        }
-      } else {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
+        for (int kk = 0; kk < 8; ++kk)
+          xq[nb][kk] = make_uint2(pack_f16x2(bf16lo(xq[nb][kk].x) * u, bf16hi(xq[nb][kk].x) * u),
+                                  pack_f16x2(bf16lo(xq[nb][kk].y) * u, bf16hi(xq[nb][kk].y) * u));
+      }
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          qb[nb][kk][0] = live ? w[8 * kk + tq] : 0u;
-          qb[nb][kk][1] = live ? w[8 * kk + 4 + tq] : 0u;
+      for (int kk = 0; kk < 8; ++kk) {
+        if constexpr (NB == 1) {
+          qb[kk][0] = xq[nb][kk].x;
+          qb[kk][1] = xq[nb][kk].y;
+        } else if ((kk >> 1) == warp) {
+          qsm[(nb * 8 + kk) * 32 + lane] = xq[nb][kk];
         }
       }
-      const int mine = 4 * nb + tq;
-      last[nb] = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
     }
+    if constexpr (NB == 2) consumer_sync();
+    auto query = [&](int nb, int kk) -> uint2 {
+      if constexpr (NB == 1) return make_uint2(qb[kk][0], qb[kk][1]);
+      else return qsm[(nb * 8 + kk) * 32 + lane];
+    };
     // acc[nb][c]: O1, O2 of row 4 nb + tq at the chunk's dims g and g + 8
     // (e4m3: 2 g and 2 g + 1).
     float acc[NB][8][4], m[NB], l[NB], sg[NB];
@@ -491,6 +513,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
     }
+    int hold = -1;
     for (int t = t_first; t < nt; t += NCW) {
       const int gi = gt + t, st = gi % NST;
       const uint32_t sc = sc_next;
@@ -524,8 +547,10 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
               const uint32_t a0 = w[mt][2 * e], a1 = w[mt][2 * e + 1];
               const uint32_t af[4] = {codes_f16(a0), codes_f16(a1), codes_f16(a0 >> 16), codes_f16(a1 >> 16)};
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma_f16_16816(cc[nb][mt], af, qb[nb][2 * cp + e][0], qb[nb][2 * cp + e][1]);
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint2 b = query(nb, 2 * cp + e);
+                mma_f16_16816(cc[nb][mt], af, b.x, b.y);
+              }
             }
         }
 #pragma unroll
@@ -552,7 +577,10 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
           uint32_t af[4];
           ldsm_x4(kb + swz(arow, 2 * kk + acol), af[0], af[1], af[2], af[3]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(c2[nb][kk & 1], af, qb[nb][kk][0], qb[nb][kk][1]);
+          for (int nb = 0; nb < NB; ++nb) {
+            const uint2 b = query(nb, kk);
+            mma_bf16_16816(c2[nb][kk & 1], af, b.x, b.y);
+          }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -662,7 +690,11 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+      if (t + NCW < nt) {
+        if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+      } else {
+        hold = st;  // the warp's last tile of the item: its sums go there
+      }
     }
     gt += nt;
 #pragma unroll
@@ -674,59 +706,74 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NB))
       }
 
     // ---------------------------------------------------------- merge warps
-    // O1 first, then O2 through the same shared memory.
+    if (lane == 0) held[warp] = hold;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = 4 * nb + tq;
       if (g == 0 && row < nr) {
-        mls[(warp * GMAX + row) * 3 + 0] = m[nb];
-        mls[(warp * GMAX + row) * 3 + 1] = l[nb];
-        mls[(warp * GMAX + row) * 3 + 2] = sg[nb];
+        float *s = mls + (warp * GMAX + row) * 4;
+        s[0] = m[nb];
+        s[1] = l[nb];
+        s[2] = sg[nb];
+      }
+      if (hold < 0 || row >= nr) continue;
+      // Rows rotated by 8 floats each, which spreads the four over the banks.
+      float *o = reinterpret_cast<float *>(smem + hold * 2 * TILE) + row * 2 * D;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d0 = (16 * i + (FP8 ? 2 * g : g) + 8 * tq) & (D - 1);
+        const int d1 = (16 * i + (FP8 ? 2 * g + 1 : g + 8) + 8 * tq) & (D - 1);
+        o[d0] = acc[nb][i][0];
+        o[D + d0] = acc[nb][i][1];
+        o[d1] = acc[nb][i][2];
+        o[D + d1] = acc[nb][i][3];
       }
     }
+    consumer_sync();
     const int dim = threadIdx.x;
     const float down = FP8 ? k2p56 : 1.f;
+    float *recs = a.recs + (c + it.vrow) * gs * REC;
+    if (dim < nr) {  // a thread per row: the warps' weights, sigma, log-sum-exp
+      float M = -INFINITY, L = 0.f, S = 0.f;
 #pragma unroll
-    for (int ph = 0; ph < 2; ++ph) {
+      for (int w = 0; w < NCW; ++w) M = fmaxf(M, mls[(w * GMAX + dim) * 4]);
+      const bool none = M == -INFINITY || ab.raised();
+      float f[NCW];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int row = 4 * nb + tq;
-        if (row < nr) {
-          float *o = red + (warp * gs + row) * RS;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[16 * i + (FP8 ? 2 * g : g)] = acc[nb][i][ph];
-            o[16 * i + (FP8 ? 2 * g + 1 : g + 8)] = acc[nb][i][2 + ph];
-          }
-        }
+      for (int w = 0; w < NCW; ++w) {
+        const float *s = mls + (w * GMAX + dim) * 4;
+        f[w] = none ? 0.f : fast_exp2(s[0] - M);
+        L = fmaf(f[w], s[1], L);
+        S = fmaf(f[w], s[2], S);
       }
-      consumer_sync();
-      const bool aborted = ab.raised();
-      {
-        for (int gh = 0; gh < nr; ++gh) {
-          float M = -INFINITY;
+      const float inv = none ? 0.f : 1.f / L;
 #pragma unroll
-          for (int w = 0; w < NCW; ++w) M = fmaxf(M, mls[(w * GMAX + gh) * 3]);
-          float *rec = a.recs + ((c + it.vrow) * gs + gh) * REC;
-          if (M == -INFINITY || aborted) {
-            rec[ph * D + dim] = 0.f;
-            if (dim == 0) rec[2 * D + ph] = ph == 0 ? 0.f : -INFINITY;
-            continue;
-          }
-          float L = 0.f, S = 0.f, O = 0.f;
+      for (int w = 0; w < NCW; ++w) mls[(w * GMAX + dim) * 4 + 3] = f[w] * inv * down;
+      recs[dim * REC + 2 * D] = S * inv;
+      recs[dim * REC + 2 * D + 1] = none ? -INFINITY : M + log2f(L);
+    }
+    consumer_sync();
+    const float *sums[NCW];
 #pragma unroll
-          for (int w = 0; w < NCW; ++w) {
-            const float f = fast_exp2(mls[(w * GMAX + gh) * 3] - M);
-            L = fmaf(f, mls[(w * GMAX + gh) * 3 + 1], L);
-            S = fmaf(f, mls[(w * GMAX + gh) * 3 + 2], S);
-            O = fmaf(f, red[(w * gs + gh) * RS + dim], O);
-          }
-          const float inv = 1.f / L;
-          rec[ph * D + dim] = O * inv * down;
-          if (dim == 0) rec[2 * D + ph] = ph == 0 ? S * inv : M + log2f(L);
-        }
+    for (int w = 0; w < NCW; ++w) sums[w] = held[w] < 0 ? nullptr : reinterpret_cast<const float *>(smem + held[w] * 2 * TILE);
+#pragma unroll 4
+    for (int row = 0; row < nr; ++row) {
+      const int at = row * 2 * D + ((dim + 8 * (row & 3)) & (D - 1));
+      float o1 = 0.f, o2 = 0.f;
+#pragma unroll
+      for (int w = 0; w < NCW; ++w) {
+        if (sums[w] == nullptr) continue;  // the warp had no tile of the item
+        const float f = mls[(w * GMAX + row) * 4 + 3];
+        o1 = fmaf(f, sums[w][at], o1);
+        o2 = fmaf(f, sums[w][at + D], o2);
       }
-      consumer_sync();  // the next partials overwrite red (and mls)
+      recs[row * REC + dim] = o1;
+      recs[row * REC + D + dim] = o2;
+    }
+    consumer_sync();  // the sums have been read: the stages may be loaded again
+    if (hold >= 0 && lane == 0) {
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&empty[hold]));
     }
     if (it.t0 == 0 && dim == 0) {
       // This CTA holds the row's first tile, so it is the first of the CTAs
@@ -847,17 +894,17 @@ cudaError_t launch_rows(const RowsArgs &a, const CUtensorMap &mk, const CUtensor
   if (ctx == 0 || configured_ctx != ctx) {
     cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, NB>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(rows_smem(4 * NB)));
+                                         static_cast<int>(rows_smem(NB)));
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  paged_rows_kernel<FP8, NB><<<a.nshare, THREADS, rows_smem(a.gs), stream>>>(mk, mv, a);
+  paged_rows_kernel<FP8, NB><<<a.nshare, THREADS, rows_smem(NB), stream>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int paged_rows_shares(int slot) { return ctas_per_sm(slot > 4 ? 2 : 1) * sm_count(); }
+int paged_rows_shares() { return kCtasPerSm * sm_count(); }
 
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
                               long long qhs, const int *seqlens, const int *cu_q, void *out,
@@ -881,7 +928,7 @@ cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r,
   a.G = Hq / c.Hkv;
   a.T = T;
   a.gs = paged_rows_slot(a.G, cu_q != nullptr);
-  a.nshare = paged_rows_shares(a.gs);
+  a.nshare = paged_rows_shares();
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const long long vrows = paged_rows_vrows(T, c.B, a.G, c.Hkv);
   a.meta = static_cast<int2 *>(workspace);

@@ -108,7 +108,7 @@ cudaError_t launch_kv_read(const PagedCache &c, const int *cu_k, void *k, void *
 // (sequence, kv head, group of 8 query rows), padded to 256 bytes, then
 // (shares + virtual rows) slots of `slot` records of 2 d + 2 floats. CTA c
 // writes its part of virtual row v to slot c + v.
-int paged_rows_shares(int slot);  // CTAs of the split kernel
+int paged_rows_shares();  // CTAs of the split kernel
 inline int paged_rows_slot(int G, bool many) { return many || G > 8 ? 8 : G; }
 inline long long paged_rows_vrows(int T, int B, int G, int Hkv) {
   return (static_cast<long long>(T) * G / 8 + B) * Hkv;
@@ -118,7 +118,7 @@ inline size_t paged_rows_workspace_bytes(int T, int B, int G, int Hkv, int d, bo
   const long long vrows = paged_rows_vrows(T, B, G, Hkv);
   const int slot = paged_rows_slot(G, many);
   return paged_rows_meta_bytes(vrows) +
-         size_t(paged_rows_shares(slot) + vrows) * slot * (2 * size_t(d) + 2) * sizeof(float);
+         size_t(paged_rows_shares() + vrows) * slot * (2 * size_t(d) + 2) * sizeof(float);
 }
 // lse ([T, Hq] fp32) may be null; cu_q null: one new token a sequence.
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
