@@ -414,74 +414,100 @@ def plx_decode_default_nsplit(B, Hkv) -> int:
     return int(lib().plx_decode_default_nsplit(B, Hkv))
 
 
+def _like(t, name, dtype, shape, dev):
+    """_need with the whole shape, in the fewest attribute reads (the paged
+    calls check up to ten tensors, and a decode step waits for them)."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _need(t, name, dtype, len(shape), dev)
+
+
 def _pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
     """Checks of a paged cache and of the int32 [B] lengths (or None) that go
     with it; returns the pointers (kpages, vpages, kscale, vscale, block_table)
     and the sizes (B, Hkv, d, num_pages, page_size, max_pages)."""
-    fp8 = kscale is not None or vscale is not None
-    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
-    if kpages.dim() != 4:
-        raise ValueError("kpages must be [num_pages, Hkv, page_size, d], got shape "
-                         f"{tuple(kpages.shape)}")
     shape = kpages.shape
-    if vpages.shape != shape:
-        raise ValueError(f"vpages has shape {tuple(vpages.shape)}, expected {tuple(shape)}")
+    if len(shape) != 4:
+        raise ValueError(f"kpages must be [num_pages, Hkv, page_size, d], got shape {tuple(shape)}")
     if block_table.dim() != 2 or block_table.shape[0] < 1:
         raise ValueError(f"block_table must be [B, max_pages], got shape {tuple(block_table.shape)}")
     B, width = block_table.shape
-    if seqlens is not None and tuple(seqlens.shape) != (B,):
-        raise ValueError(f"seqlens must have shape ({B},), got {tuple(seqlens.shape)}")
-    for name, t in (("kscale", kscale), ("vscale", vscale)):
-        if fp8 and (t is None or t.shape != shape[:3]):
-            raise ValueError(f"{name} must be given with shape {tuple(shape[:3])}")
-    _need(kpages, "kpages", dtype, 4, dev)
-    _need(vpages, "vpages", dtype, 4, dev)
+    fp8 = kscale is not None or vscale is not None
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    n, Hkv, page, d = shape
     if fp8:
-        _need(kscale, "kscale", torch.uint8, 3, dev)
-        _need(vscale, "vscale", torch.uint8, 3, dev)
-    _need(block_table, "block_table", torch.int32, 2, dev)
+        for name, t in (("kscale", kscale), ("vscale", vscale)):
+            if t is None or t.shape != shape[:3]:
+                raise ValueError(f"{name} must be given with shape {tuple(shape[:3])}")
+    if vpages.shape != shape:
+        raise ValueError(f"vpages has shape {tuple(vpages.shape)}, expected {tuple(shape)}")
+    if seqlens is not None and seqlens.shape != (B,):
+        raise ValueError(f"seqlens must have shape ({B},), got {tuple(seqlens.shape)}")
+    if kpages.dtype is not dtype or vpages.dtype is not dtype:
+        name, t = ("kpages", kpages) if kpages.dtype is not dtype else ("vpages", vpages)
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dev.type != "cuda":
+        raise ValueError("kpages must be a CUDA tensor" if kpages.device.type != "cuda" else
+                         "all tensors must be CUDA tensors")
+    _like(kpages, "kpages", dtype, shape, dev)
+    _like(vpages, "vpages", dtype, shape, dev)
+    _like(block_table, "block_table", torch.int32, (B, width), dev)
     if seqlens is not None:
-        _need(seqlens, "seqlens", torch.int32, 1, dev)
-    ptrs = (kpages.data_ptr(), vpages.data_ptr(), kscale.data_ptr() if fp8 else None,
-            vscale.data_ptr() if fp8 else None, block_table.data_ptr())
-    return ptrs, (B, shape[1], shape[3], shape[0], shape[2], width)
-
-
-def _cu(cu, name, B, dev):
-    if tuple(cu.shape) != (B + 1,):
-        raise ValueError(f"{name} must have shape ({B + 1},), got {tuple(cu.shape)}")
-    _need(cu, name, torch.int32, 1, dev)
+        _like(seqlens, "seqlens", torch.int32, (B,), dev)
+    if not fp8:
+        return (kpages.data_ptr(), vpages.data_ptr(), None, None, block_table.data_ptr()), (
+            B, Hkv, d, n, page, width)
+    _like(kscale, "kscale", torch.uint8, shape[:3], dev)
+    _like(vscale, "vscale", torch.uint8, shape[:3], dev)
+    return (kpages.data_ptr(), vpages.data_ptr(), kscale.data_ptr(), vscale.data_ptr(),
+            block_table.data_ptr()), (B, Hkv, d, n, page, width)
 
 
 def _packed(t, name, heads, d, dev):
     """(token, head) strides of packed rows [T, heads, d]; only a row's d
     values must be contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [T, {heads if heads is not None else 'heads'}, {d}], got "
-                         f"shape {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev is not None and t.device != dev:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or shape[1] != heads:
+        raise ValueError(f"{name} must be [T, {heads}, {d}], got shape {tuple(shape)}")
+    if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     ts, hs, ds = t.stride()
     if ds != 1 and d != 1:
         raise ValueError(f"{name} must have its last dimension contiguous")
     # A dimension of size one has no stride of its own.
-    hs = hs if t.shape[1] > 1 else d
-    ts = ts if t.shape[0] > 1 else max(d, hs * t.shape[1])
+    if heads == 1:
+        hs = d
+    if shape[0] == 1:
+        ts = max(d, hs * heads)
     return ts, hs
 
 
-def _workspace(workspace, need, stream, dev):
-    """(tensor, pointer, bytes) of the caller's workspace, or of one of `need`
-    bytes from torch's caching allocator, in the order of the call's stream (a
+def _launch(fn, dev, stream, args):
+    """fn(*args, stream) on the device of the tensors; raises on a bad status."""
+    if torch.cuda.current_device() == dev.index:
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream, dev)))
+
+
+def _workspace(workspace, sizer, sizes, stream, dev):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one of the
+    needed size from torch's caching allocator, in the order of the call's stream (a
     stream-ordered allocation by the library would give its memory back to the
     driver whenever the GPU idles: 200 us for a call after a synchronize)."""
     if workspace is None:
+        if torch.cuda.current_device() == dev.index:  # the size goes by the device's SM count
+            need = getattr(lib(), sizer)(*sizes)
+        else:
+            with torch.cuda.device(dev):
+                need = getattr(lib(), sizer)(*sizes)
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
@@ -514,14 +540,12 @@ def plx_kv_append(k, v, kpages, vpages, block_table, seqlens, cu_q=None, kscale=
         raise ValueError("k and v must have the same strides")
     T = k.shape[0]
     if cu_q is not None:
-        _cu(cu_q, "cu_q", B, dev)
+        _like(cu_q, "cu_q", torch.int32, (B + 1,), dev)
     elif T != B:
         raise ValueError(f"without cu_q, k must have one row for each of the {B} sequences, got {T}")
-    with torch.cuda.device(dev):
-        st = lib().plx_kv_append(k.data_ptr(), v.data_ptr(), *strides, *ptrs, seqlens.data_ptr(),
-                                 cu_q.data_ptr() if cu_q is not None else None, T, B, Hkv, d, n,
-                                 page, width, _stream(stream, dev))
-    _check(st)
+    _launch(lib().plx_kv_append, dev, stream,
+            (k.data_ptr(), v.data_ptr(), *strides, *ptrs, seqlens.data_ptr(),
+             cu_q.data_ptr() if cu_q is not None else None, T, B, Hkv, d, n, page, width))
     return kpages, vpages
 
 
@@ -535,17 +559,17 @@ def plx_kv_read(kpages, vpages, block_table, cu_k, T, kscale=None, vscale=None, 
     if T < 0:
         raise ValueError(f"T must be >= 0, got {T}")
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, None, dev)
-    _cu(cu_k, "cu_k", B, dev)
-    k = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev) if v is None else v
-    for name, t in (("k", k), ("v", v)):
-        _need(t, name, torch.bfloat16, 3, dev)
-        if tuple(t.shape) != (T, Hkv, d):
-            raise ValueError(f"{name} must be ({T}, {Hkv}, {d}), got {tuple(t.shape)}")
-    with torch.cuda.device(dev):
-        st = lib().plx_kv_read(*ptrs, cu_k.data_ptr(), k.data_ptr(), v.data_ptr(), T, B, Hkv, d, n,
-                               page, width, _stream(stream, dev))
-    _check(st)
+    _like(cu_k, "cu_k", torch.int32, (B + 1,), dev)
+    if k is None:
+        k = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _like(k, "k", torch.bfloat16, (T, Hkv, d), dev)
+    if v is None:
+        v = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _like(v, "v", torch.bfloat16, (T, Hkv, d), dev)
+    _launch(lib().plx_kv_read, dev, stream,
+            (*ptrs, cu_k.data_ptr(), k.data_ptr(), v.data_ptr(), T, B, Hkv, d, n, page, width))
     return k, v
 
 
@@ -556,24 +580,26 @@ def plx_decode_fwd_paged(q, r, kpages, vpages, block_table, seqlens, kscale=None
     if q.dim() != 3:
         raise ValueError(f"q must be [B, Hq, d], got shape {tuple(q.shape)}")
     dev = q.device
-    Hq = q.shape[1]
-    out = torch.empty_like(q) if out is None else out
-    rows = (("q", q), ("r", r), ("out", out))
-    for name, t in rows:
-        if tuple(t.shape) != (block_table.shape[0], Hq, kpages.shape[-1]):
-            raise ValueError(f"{name} must be ({block_table.shape[0]}, {Hq}, {kpages.shape[-1]}), got "
-                             f"shape {tuple(t.shape)}")
+    B, Hq, d = shape = q.shape
+    if B != block_table.shape[0] or d != kpages.shape[-1]:
+        raise ValueError(f"q must be ({block_table.shape[0]}, {Hq}, {kpages.shape[-1]}), got shape "
+                         f"{tuple(shape)}")
+    for name, t in (("r", r), ("out", out)):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
-    for name, t in rows:
-        _need(t, name, torch.bfloat16, 3, dev)
-    ws, ws_ptr, ws_bytes = _workspace(workspace, plx_decode_paged_workspace_bytes(B, Hq, Hkv, d),
+    _like(q, "q", torch.bfloat16, shape, dev)
+    _like(r, "r", torch.bfloat16, shape, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _like(out, "out", torch.bfloat16, shape, dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_decode_paged_workspace_bytes", (B, Hq, Hkv, d),
                                       stream, dev)
-    with torch.cuda.device(dev):
-        st = lib().plx_decode_fwd_paged(q.data_ptr(), r.data_ptr(), *ptrs, seqlens.data_ptr(),
-                                        out.data_ptr(), B, Hq, Hkv, d, n, page, width, ws_ptr,
-                                        ws_bytes, _stream(stream, dev))
-    _check(st)
+    _launch(lib().plx_decode_fwd_paged, dev, stream,
+            (q.data_ptr(), r.data_ptr(), *ptrs, seqlens.data_ptr(), out.data_ptr(), B, Hq, Hkv, d, n,
+             page, width, ws_ptr, ws_bytes))
     return out
 
 
@@ -593,25 +619,20 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
     strides = _packed(q, "q", Hq, d, dev)
     if _packed(r, "r", Hq, d, dev) != strides:
         raise ValueError("q and r must have the same strides")
-    _cu(cu_q, "cu_q", B, dev)
+    _like(cu_q, "cu_q", torch.int32, (B + 1,), dev)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
     if out.shape != q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
     out_strides = _packed(out, "out", Hq, d, dev)
     if lse is not None:
-        _need(lse, "lse", torch.float32, 2, dev)
-        if tuple(lse.shape) != (T, Hq):
-            raise ValueError(f"lse must be ({T}, {Hq}), got {tuple(lse.shape)}")
-    ws, ws_ptr, ws_bytes = _workspace(workspace, plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d),
-                                      stream, dev)
-    with torch.cuda.device(dev):
-        st = lib().plx_prefill_fwd_paged(q.data_ptr(), r.data_ptr(), *strides, *ptrs,
-                                         seqlens.data_ptr(), cu_q.data_ptr(), out.data_ptr(),
-                                         *out_strides, lse.data_ptr() if lse is not None else None,
-                                         T, B, Hq, Hkv, d, n, page, width, ws_ptr, ws_bytes,
-                                         _stream(stream, dev))
-    _check(st)
+        _like(lse, "lse", torch.float32, (T, Hq), dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_prefill_paged_workspace_bytes",
+                                      (T, B, Hq, Hkv, d), stream, dev)
+    _launch(lib().plx_prefill_fwd_paged, dev, stream,
+            (q.data_ptr(), r.data_ptr(), *strides, *ptrs, seqlens.data_ptr(), cu_q.data_ptr(),
+             out.data_ptr(), *out_strides, lse.data_ptr() if lse is not None else None, T, B, Hq, Hkv,
+             d, n, page, width, ws_ptr, ws_bytes))
     return out, lse
 
 

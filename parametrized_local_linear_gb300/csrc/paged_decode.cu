@@ -6,17 +6,18 @@
 // The streaming form is decode.cu's: s = q.k and t = r.k of a key from the same
 // products, P = exp(s) and P o T against the same value rows, one running max.
 // Here the KEYS are the M rows of the m16n8k16 products and the query rows the
-// N columns, column 2 h the query q_h and 2 h + 1 its probe r_h (NB blocks of
-// four query rows): S^T = K [q r], then O^T = V^T [P, P o T], whose
-// operand is S^T's own registers after one 8x8 transpose. Compared with the
-// queries as rows this halves the products, the accumulators and the softmax
-// work for the usual one to four query heads a kv head, whose rows would
-// leave most of an M of 16 idle; that is what lets e4m3 pages, at twice the
-// keys a byte, keep up with the memory.
+// N columns, column 2 h the query q_h and 2 h + 1 its probe r_h: S^T =
+// K [q r], then O^T = V^T [P, P o T], whose operand is S^T's own registers
+// after one 8x8 transpose. Compared with the queries as rows this halves the
+// products, the accumulators and the softmax work for the usual one to four
+// query heads a kv head, whose rows would leave most of an M of 16 idle; that is
+// what lets e4m3 pages, at twice the keys a byte, keep up with the memory.
 //   - Query rows. The n_b G rows (token, query head of the group) of a sequence
-//     and kv head are taken eight at a time as row groups; each group streams
-//     the keys for itself (the groups of a kv head run side by side and share
-//     its keys in L2). A group is masked causally where it needs to be.
+//     and kv head are taken in groups of 4 R; with R = 2 the four consumer
+//     warps are two pairs, each tile going to both warps of a pair, four rows
+//     each (eight columns more in one warp cost registers: 2 CTAs an SM or
+//     spills, 330 us against 269 for 64 x 8192 e4m3 keys and 8 query heads a kv
+//     head). A group is masked causally where it needs to be.
 //   - Pages. The stream is counted in tiles of KT keys, which never cross a
 //     page of a multiple of KT keys (page_size 16 gives two boxes a tile of 32).
 //     A (page, kv head) block is contiguous, so a tile is one 4 KB TMA box of
@@ -50,8 +51,8 @@ namespace {
 
 constexpr int D = 128;
 constexpr int NCW = 4;          // consumer warps
-constexpr int GMAX = 8;         // query rows of a group
-constexpr int NST = 2 * NCW;    // ring stages; tile i goes to warp i % NCW and stage i % NST
+constexpr int RW = 4;           // query rows of a warp: half the eight columns of a product
+constexpr int NST = 2 * NCW;    // ring stages; tile i goes to warp row i % (NCW / R) and stage i % NST
 constexpr int THREADS = 32 * (NCW + 1);
 constexpr int REC = 2 * D + 2;  // floats of a record: O1 / l, O2 / l, sigma / l, log2-sum-exp
 constexpr float k2p56 = 72057594037927936.f;  // 2^56 = 2^120 / 2^64
@@ -59,18 +60,15 @@ constexpr float k2p56 = 72057594037927936.f;  // 2^56 = 2^120 / 2^64
 // Shared memory. The stages (K rows and V rows of a tile, 4 KB each) come
 // first: the 128-byte-swizzled boxes need 1024-byte alignment. An item's
 // partial sums are merged through the stages of its warps' last tiles, which
-// are released only then: 8 rows x 256 floats are just a stage.
+// are released only then: 4 R rows x 256 floats fit a stage.
 constexpr int TILE = 4096;
-constexpr int OFF_QB = NST * 2 * TILE;               // two blocks of columns: the item's query fragments
-constexpr int qb_bytes(int nb) { return nb == 2 ? 2 * 8 * 32 * 8 : 0; }
-constexpr int mls_off(int nb) { return OFF_QB + qb_bytes(nb); }  // [NCW][GMAX] m, l, sigma, weight
-constexpr int bar_off(int nb) { return mls_off(nb) + NCW * GMAX * 16; }
-constexpr int flag_off(int nb) { return bar_off(nb) + 2 * NST * 8; }
-constexpr int plan_off(int nb) { return flag_off(nb) + 16; }
-constexpr int held_off(int nb) { return plan_off(nb) + 64; }     // [NCW] stage that holds a warp's sums
-constexpr size_t rows_smem(int nb) { return held_off(nb) + 16 + 1024; }
-static_assert(NST % NCW == 0, "each stage must belong to one consumer warp");
-static_assert(2 * TILE == GMAX * 2 * D * 4, "a stage holds a warp's sums");
+constexpr int OFF_MLS = NST * 2 * TILE;  // [NCW][RW] m, l, sigma, weight
+constexpr int OFF_BAR = OFF_MLS + NCW * RW * 16;
+constexpr int OFF_FLAG = OFF_BAR + 2 * NST * 8;
+constexpr int OFF_PLAN = OFF_FLAG + 16;
+constexpr int OFF_HELD = OFF_PLAN + 64;  // [NCW] stage that holds a warp's sums
+constexpr size_t ROWS_SMEM = OFF_HELD + 16 + 1024;
+static_assert(2 * TILE == 2 * RW * 2 * D * 4, "a stage holds the sums of two warps");
 constexpr int kCtasPerSm = 3;  // 128 registers a thread, 72 KB of shared memory
 
 struct RowsArgs {
@@ -94,7 +92,7 @@ struct Plan {
 struct Seq {
   int len, tiles, first, n, ng;
 };
-template <int KT>
+template <int KT, int GS>
 __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
   Seq s;
   s.len = cache_len(a.c, a.seqlens, b);
@@ -110,13 +108,13 @@ __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
       s.first = s.n = 0;
     }
   }
-  s.ng = (s.n * a.G + GMAX - 1) / GMAX;
+  s.ng = (s.n * a.G + GS - 1) / GS;
   return s;
 }
 // Row groups in front of sequence b, counted so that no scan is needed:
-// ceil(n G / 8) <= floor((c + n) G / 8) - floor(c G / 8) + 1.
-__device__ __forceinline__ long long groups_before(int first, int b, int G) {
-  return static_cast<long long>(first) * G / GMAX + b;
+// ceil(n G / gs) <= floor((c + n) G / gs) - floor(c G / gs) + 1.
+__device__ __forceinline__ long long groups_before(int first, int b, int G, int gs) {
+  return static_cast<long long>(first) * G / gs + b;
 }
 
 // One item: tiles [t0, t1) of row group grp of kv head kvh of sequence b.
@@ -126,13 +124,13 @@ struct Item {
   long long vrow;  // the item's row of records
 };
 
-template <int KT>
+template <int KT, int GS>
 struct Walk {
   long long pos, e, base;
   int b;
   Seq s;
   __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a)
-      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT>(a, p.b0)) {}
+      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS>(a, p.b0)) {}
   __device__ __forceinline__ bool next(Item &it, const RowsArgs &a) {
     if (pos >= e) return false;
     // Positions below W all lie in some sequence, so b stays below B here.
@@ -140,7 +138,7 @@ struct Walk {
       const long long end = base + static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
       if (pos < end) break;
       base = end;
-      s = seq_of<KT>(a, ++b);
+      s = seq_of<KT, GS>(a, ++b);
     }
     const long long off = pos - base;
     const int vh = static_cast<int>(off / s.tiles);
@@ -150,7 +148,7 @@ struct Walk {
     it.grp = vh - it.kvh * s.ng;
     it.t0 = static_cast<int>(off - static_cast<long long>(vh) * s.tiles);
     it.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), it.t0 + (e - pos)));
-    it.vrow = groups_before(s.first, b, a.G) * a.c.Hkv + vh;
+    it.vrow = groups_before(s.first, b, a.G, GS) * a.c.Hkv + vh;
     pos += it.t1 - it.t0;
     return true;
   }
@@ -227,18 +225,20 @@ __device__ __forceinline__ int row_shift(float m) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-template <bool FP8, int NB>
+template <bool FP8, int R>
 __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const RowsArgs a) {
   constexpr int KT = FP8 ? 32 : 16;  // keys of a tile
+  constexpr int GS = RW * R;         // query rows of a group
+  constexpr int NL = NCW / R;        // warp rows: tiles in work at a time
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + bar_off(NB));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
   uint64_t *empty = full + NST;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + flag_off(NB));
-  Plan *plan = reinterpret_cast<Plan *>(smem + plan_off(NB));
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_FLAG);
+  Plan *plan = reinterpret_cast<Plan *>(smem + OFF_PLAN);
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     long long W = 0;
     int rows = 0, lmin = 0x7fffffff, lmax = 0;  // rows of records and lengths of sequences with keys
     for (int i = lane; i < a.c.B; i += 32) {
-      const Seq s = seq_of<KT>(a, i);
+      const Seq s = seq_of<KT, GS>(a, i);
       const long long u = static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
       W += u;
       if (u > 0) {
@@ -269,14 +269,14 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     if (rows > 0 && lmin == lmax) {
       // Rows of one length: cut them all alike, or give every share whole rows,
       // if that keeps 80% of the CTAs (decode.cu's rule).
-      const long long R = rows, floor_n = (4 * n + 4) / 5;
+      const long long all = rows, floor_n = (4 * n + 4) / 5;
       long long best = 0;
-      if (R <= n) {
-        best = R * (n / R);
+      if (all <= n) {
+        best = all * (n / all);
       } else {
-        for (long long m = (R + n - 1) / n, m_end = m + 64; m < m_end && R / m >= floor_n; ++m)
-          if (R % m == 0) {
-            best = R / m;
+        for (long long m = (all + n - 1) / n, m_end = m + 64; m < m_end && all / m >= floor_n; ++m)
+          if (all % m == 0) {
+            best = all / m;
             break;
           }
       }
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         const int i = i0 + lane;
         long long u = 0;
         if (i < a.c.B) {
-          const Seq q = seq_of<KT>(a, i);
+          const Seq q = seq_of<KT, GS>(a, i);
           u = static_cast<long long>(q.tiles) * q.ng * a.c.Hkv;
         }
         long long inc = u;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   if (threadIdx.x == 0) {
     for (int st = 0; st < NST; ++st) {
       mbar_init(smem_u32(&full[st]), 1);
-      mbar_init(smem_u32(&empty[st]), 1);
+      mbar_init(smem_u32(&empty[st]), R);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       const int shift = a.c.page_shift, mask = (1 << shift) - 1;
       const int per = KT > mask + 1 ? 16 : KT;  // keys of a box, as in the map
       const int beyond = a.c.num_pages * a.c.Hkv;
-      Walk<KT> wk(pl, a);
+      Walk<KT, GS> wk(pl, a);
       Item it;
       int g = 0;
       bool ok = true;
@@ -405,18 +405,18 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   // Every consumer warp takes part in every item's merge (both barriers), also
   // after an abort, so the named barrier is always complete.
   const int g = lane >> 2, tq = lane & 3;
+  const int blk = warp % R, line = warp / R;  // rows RW blk .. of a group; tiles line, line + NL, ...
   const int gs = a.gs;
   constexpr int MT = KT / 16;  // m tiles of 16 keys
-  float *mls = reinterpret_cast<float *>(smem + mls_off(NB));
-  volatile int *held = reinterpret_cast<volatile int *>(smem + held_off(NB));
-  uint2 *qsm = reinterpret_cast<uint2 *>(smem + OFF_QB);  // [nb][kk][lane]
-  Walk<KT> wk(pl, a);
+  float *mls = reinterpret_cast<float *>(smem + OFF_MLS);
+  volatile int *held = reinterpret_cast<volatile int *>(smem + OFF_HELD);
+  Walk<KT, GS> wk(pl, a);
   Item it;
   int gt = 0;  // tiles of the previous items
   while (wk.next(it, a)) {
     const int nt = it.t1 - it.t0;
-    const int r0 = it.grp * GMAX, nr = min(GMAX, it.s.n * a.G - r0);  // this group's rows
-    const int t_first = (warp - gt % NCW + NCW) % NCW;
+    const int r0 = it.grp * GS, nr = min(GS, it.s.n * a.G - r0);  // this group's rows
+    const int t_first = (line - gt % NL + NL) % NL;
     // The scale bytes of key `lane` of the warp's tiles, one tile ahead, and
     // the page number of the tile after it.
     const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
@@ -436,20 +436,14 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     int page_first = -1, page_next = -1;
     if constexpr (FP8) {
       page_first = page_of(t_first);
-      page_next = page_of(t_first + NCW);
+      page_next = page_of(t_first + NL);
     }
-    // Column g of block nb is q (even g) or r (odd g) of row 4 nb + g / 2;
-    // this thread's scores are those of row 4 nb + tq.
-    // With two blocks of columns the fragments live in shared memory, each
-    // warp writing two of the eight steps.
-    uint32_t qb[NB == 1 ? 8 : 1][2];
-    float fs[NB], ft[NB];  // what the scores and the probe products still lack
-    int last[NB];          // the last key that row 4 nb + tq sees (< 0: none)
-    const int all_see = it.s.len - it.s.n + r0 / a.G;  // keys up to here are seen by all rows
-    uint2 xq[NB][8];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int row = 4 * nb + (g >> 1);
+    // Column g is q (even g) or r (odd g) of the warp's row g / 2; this
+    // thread's scores are those of its row tq.
+    uint2 qb[8];
+    float fs = a.scale_log2, ft = 1.f;  // what the scores and the probe products still lack
+    {
+      const int row = RW * blk + (g >> 1);
       const bool live = row < nr;
       const int tok = (r0 + (live ? row : 0)) / a.G, h = it.kvh * a.G + (r0 + (live ? row : 0)) % a.G;
       const __nv_bfloat16 *src = ((g & 1) ? a.r : a.q) + (it.s.first + tok) * a.qts + h * a.qhs;
@@ -458,82 +452,58 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        if (!live) xq[nb][kk] = make_uint2(0u, 0u);
-        else if (FP8) xq[nb][kk] = *reinterpret_cast<const uint2 *>(src + 16 * kk + 4 * tq);
-        else xq[nb][kk] = make_uint2(w[8 * kk + tq], w[8 * kk + 4 + tq]);
+        if (!live) qb[kk] = make_uint2(0u, 0u);
+        else if (FP8) qb[kk] = *reinterpret_cast<const uint2 *>(src + 16 * kk + 4 * tq);
+        else qb[kk] = make_uint2(w[8 * kk + tq], w[8 * kk + 4 + tq]);
       }
-      const int mine = 4 * nb + tq;
-      last[nb] = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
     }
+    const int mine = RW * blk + tq;
+    // The last key that row tq sees (< 0: none), and that all rows see.
+    const int last = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
+    const int all_see = it.s.len - it.s.n + r0 / a.G;
     uint32_t sc_next = 0u;
-    if constexpr (FP8) sc_next = scales_of(t_first, page_first);
+    if constexpr (FP8) {
+      sc_next = scales_of(t_first, page_first);
+      float mx = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      fs[nb] = a.scale_log2;
-      ft[nb] = 1.f;
-      if constexpr (FP8) {
-        float mx = 0.f;
+      for (int kk = 0; kk < 8; ++kk)
+        mx = fmax3(mx, fmaxf(fabsf(bf16lo(qb[kk].x)), fabsf(bf16hi(qb[kk].x))),
+                   fmaxf(fabsf(bf16lo(qb[kk].y)), fabsf(bf16hi(qb[kk].y))));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int up = row_shift(mx);
+      const float u = pow2(up), back = pow2(-up);
+      fs *= __shfl_sync(0xffffffffu, back, 8 * tq);      // column 2 tq
+      ft *= __shfl_sync(0xffffffffu, back, 8 * tq + 4);  // column 2 tq + 1
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mx = fmax3(mx, fmaxf(fabsf(bf16lo(xq[nb][kk].x)), fabsf(bf16hi(xq[nb][kk].x))),
-                     fmaxf(fabsf(bf16lo(xq[nb][kk].y)), fabsf(bf16hi(xq[nb][kk].y))));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int up = row_shift(mx);
-        const float u = pow2(up), back = pow2(-up);
-        fs[nb] *= __shfl_sync(0xffffffffu, back, 8 * tq);      // column 2 tq
-        ft[nb] *= __shfl_sync(0xffffffffu, back, 8 * tq + 4);  // column 2 tq + 1
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          xq[nb][kk] = make_uint2(pack_f16x2(bf16lo(xq[nb][kk].x) * u, bf16hi(xq[nb][kk].x) * u),
-                                  pack_f16x2(bf16lo(xq[nb][kk].y) * u, bf16hi(xq[nb][kk].y) * u));
-      }
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        if constexpr (NB == 1) {
-          qb[kk][0] = xq[nb][kk].x;
-          qb[kk][1] = xq[nb][kk].y;
-        } else if ((kk >> 1) == warp) {
-          qsm[(nb * 8 + kk) * 32 + lane] = xq[nb][kk];
-        }
-      }
+      for (int kk = 0; kk < 8; ++kk)
+        qb[kk] = make_uint2(pack_f16x2(bf16lo(qb[kk].x) * u, bf16hi(qb[kk].x) * u),
+                            pack_f16x2(bf16lo(qb[kk].y) * u, bf16hi(qb[kk].y) * u));
     }
-    if constexpr (NB == 2) consumer_sync();
-    auto query = [&](int nb, int kk) -> uint2 {
-      if constexpr (NB == 1) return make_uint2(qb[kk][0], qb[kk][1]);
-      else return qsm[(nb * 8 + kk) * 32 + lane];
-    };
-    // acc[nb][c]: O1, O2 of row 4 nb + tq at the chunk's dims g and g + 8
-    // (e4m3: 2 g and 2 g + 1).
-    float acc[NB][8][4], m[NB], l[NB], sg[NB];
+    // acc[c]: O1, O2 of row tq at the chunk's dims g and g + 8 (e4m3: 2 g and
+    // 2 g + 1).
+    float acc[8][4], m = -INFINITY, l = 0.f, sg = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      m[nb] = -INFINITY;
-      l[nb] = sg[nb] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
-    }
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     int hold = -1;
-    for (int t = t_first; t < nt; t += NCW) {
+    for (int t = t_first; t < nt; t += NL) {
       const int gi = gt + t, st = gi % NST;
       const uint32_t sc = sc_next;
       if constexpr (FP8) {
-        sc_next = scales_of(t + NCW, page_next);
-        page_next = page_of(t + 2 * NCW);
+        sc_next = scales_of(t + NL, page_next);
+        page_next = page_of(t + 2 * NL);
       }
       bool ok = false;
       if (lane == 0) ok = !ab.raised() && mbar_wait(smem_u32(&full[st]), (gi / NST) & 1, ab);
       if (!__shfl_sync(0xffffffffu, ok, 0)) continue;  // aborting: skip the tile
       const uint32_t kb = smem_u32(smem + st * 2 * TILE), vb = kb + TILE;
       const int key0 = (it.t0 + t) * KT;
-      // cc[nb][mt][0..1]: s and t of key 16 mt + g, [2..3]: of key 16 mt + 8 + g.
-      float cc[NB][MT][4];
+      // cc[mt][0..1]: s and t of key 16 mt + g, [2..3]: of key 16 mt + 8 + g.
+      float cc[MT][4];
       const int arow = (lane & 7) + 8 * ((lane >> 3) & 1), acol = lane >> 4;
       if constexpr (FP8) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) cc[nb][mt][0] = cc[nb][mt][1] = cc[nb][mt][2] = cc[nb][mt][3] = 0.f;
+        for (int mt = 0; mt < MT; ++mt) cc[mt][0] = cc[mt][1] = cc[mt][2] = cc[mt][3] = 0.f;
 #pragma unroll
         for (int cp = 0; cp < 4; ++cp) {  // two chunks of 16 dims
           uint32_t w[MT][4];
@@ -546,11 +516,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
             for (int mt = 0; mt < MT; ++mt) {
               const uint32_t a0 = w[mt][2 * e], a1 = w[mt][2 * e + 1];
               const uint32_t af[4] = {codes_f16(a0), codes_f16(a1), codes_f16(a0 >> 16), codes_f16(a1 >> 16)};
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const uint2 b = query(nb, 2 * cp + e);
-                mma_f16_16816(cc[nb][mt], af, b.x, b.y);
-              }
+              mma_f16_16816(cc[mt], af, qb[2 * cp + e].x, qb[2 * cp + e].y);
             }
         }
 #pragma unroll
@@ -559,97 +525,70 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           for (int e = 0; e < 2; ++e) {
             const uint32_t two = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * e + g);
             const float f = scale_of(two & 0xffu);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              cc[nb][mt][2 * e] *= fs[nb] * f;
-              cc[nb][mt][2 * e + 1] *= ft[nb] * f;
-            }
+            cc[mt][2 * e] *= fs * f;
+            cc[mt][2 * e + 1] *= ft * f;
           }
       } else {
         // Two sums over the even and the odd steps, added at the end.
-        float c2[NB][2][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) c2[nb][i][0] = c2[nb][i][1] = c2[nb][i][2] = c2[nb][i][3] = 0.f;
+        float c2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           uint32_t af[4];
           ldsm_x4(kb + swz(arow, 2 * kk + acol), af[0], af[1], af[2], af[3]);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const uint2 b = query(nb, kk);
-            mma_bf16_16816(c2[nb][kk & 1], af, b.x, b.y);
-          }
+          mma_bf16_16816(c2[kk & 1], af, qb[kk].x, qb[kk].y);
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          cc[nb][0][0] = (c2[nb][0][0] + c2[nb][1][0]) * fs[nb];
-          cc[nb][0][1] = c2[nb][0][1] + c2[nb][1][1];
-          cc[nb][0][2] = (c2[nb][0][2] + c2[nb][1][2]) * fs[nb];
-          cc[nb][0][3] = c2[nb][0][3] + c2[nb][1][3];
-        }
+        cc[0][0] = (c2[0][0] + c2[1][0]) * fs;
+        cc[0][1] = c2[0][1] + c2[1][1];
+        cc[0][2] = (c2[0][2] + c2[1][2]) * fs;
+        cc[0][3] = c2[0][3] + c2[1][3];
       }
       if (key0 + KT - 1 > all_see) {
         // Some row does not see all of the tile. Slots behind the sequence's
         // end, which no row sees, may hold anything: select, do not multiply.
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool see = key0 + 16 * mt + 8 * e + g <= last[nb];
-              cc[nb][mt][2 * e] = see ? cc[nb][mt][2 * e] : -INFINITY;
-              cc[nb][mt][2 * e + 1] = see ? cc[nb][mt][2 * e + 1] : 0.f;
-            }
-      }
-      float alpha[NB];
-      bool moved = false;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float mx = fmax3(m[nb], cc[nb][0][0], cc[nb][0][2]);
-        if (MT > 1) mx = fmax3(mx, cc[nb][MT - 1][0], cc[nb][MT - 1][2]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        alpha[nb] = mx == -INFINITY ? 1.f : fast_exp2(m[nb] - mx);  // m = -inf: 0
-        moved = moved || alpha[nb] != 1.f;
-        m[nb] = mx;
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          l[nb] *= alpha[nb];
-          sg[nb] *= alpha[nb];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[nb][i][0] *= alpha[nb];
-            acc[nb][i][1] *= alpha[nb];
-            acc[nb][i][2] *= alpha[nb];
-            acc[nb][i][3] *= alpha[nb];
+          for (int e = 0; e < 2; ++e) {
+            const bool see = key0 + 16 * mt + 8 * e + g <= last;
+            cc[mt][2 * e] = see ? cc[mt][2 * e] : -INFINITY;
+            cc[mt][2 * e + 1] = see ? cc[mt][2 * e + 1] : 0.f;
           }
+      }
+      float mx = fmax3(m, cc[0][0], cc[0][2]);
+      if (MT > 1) mx = fmax3(mx, cc[MT - 1][0], cc[MT - 1][2]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float alpha = mx == -INFINITY ? 1.f : fast_exp2(m - mx);  // m = -inf: 0
+      m = mx;
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        l *= alpha;
+        sg *= alpha;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[i][0] *= alpha;
+          acc[i][1] *= alpha;
+          acc[i][2] *= alpha;
+          acc[i][3] *= alpha;
         }
       }
       // The weights as B operands: (p, p t) of a key side by side, transposed
       // to pairs of keys for the column.
-      uint32_t pb[NB][MT][2];
+      const float msub = m == -INFINITY ? 0.f : m;
+      uint32_t pb[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float fv = 1.f;  // e4m3: 2^(E_v - 127 + 64)
+          const float p = fast_exp2(cc[mt][2 * e] - msub), pt = p * cc[mt][2 * e + 1];
+          l += p;
+          sg += pt;
           if constexpr (FP8) {
             const uint32_t two = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * e + g);
-            fv = __uint_as_float(((two >> 8) + 64u) << 23);
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const float msub = m[nb] == -INFINITY ? 0.f : m[nb];
-            const float p = fast_exp2(cc[nb][mt][2 * e] - msub), pt = p * cc[nb][mt][2 * e + 1];
-            l[nb] += p;
-            sg[nb] += pt;
-            pb[nb][mt][e] = transpose_8x8(FP8 ? pack_bf16x2(p * fv, pt * fv) : pack_bf16x2(p, pt));
+            const float fv = __uint_as_float(((two >> 8) + 64u) << 23);  // 2^(E_v - 127 + 64)
+            pb[mt][e] = transpose_8x8(pack_bf16x2(p * fv, pt * fv));
+          } else {
+            pb[mt][e] = transpose_8x8(pack_bf16x2(p, pt));
           }
         }
       if constexpr (FP8) {
@@ -663,9 +602,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
             for (int e = 0; e < 2; ++e) {
               const uint32_t af[4] = {codes_even(w[2 * e]), codes_odd(w[2 * e]), codes_even(w[2 * e + 1]),
                                       codes_odd(w[2 * e + 1])};
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma_bf16_16816(acc[nb][2 * cp + e], af, pb[nb][mt][0], pb[nb][mt][1]);
+              mma_bf16_16816(acc[2 * cp + e], af, pb[mt][0], pb[mt][1]);
             }
           }
       } else {
@@ -685,12 +622,11 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           af[1] &= k0;
           af[2] &= k1;
           af[3] &= k1;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(acc[nb][i], af, pb[nb][0][0], pb[nb][0][1]);
+          mma_bf16_16816(acc[i], af, pb[0][0], pb[0][1]);
         }
       }
       __syncwarp();
-      if (t + NCW < nt) {
+      if (t + NL < nt) {
         if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
       } else {
         hold = st;  // the warp's last tile of the item: its sums go there
@@ -698,72 +634,72 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     }
     gt += nt;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) {
-        l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], o);
-        sg[nb] += __shfl_xor_sync(0xffffffffu, sg[nb], o);
-      }
+    for (int o = 4; o <= 16; o <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
 
     // ---------------------------------------------------------- merge warps
+    // A stage that holds sums is shared by the R warps of its row: all of them
+    // must be done with the tile before it is overwritten.
+    if (R > 1) consumer_sync();
     if (lane == 0) held[warp] = hold;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int row = 4 * nb + tq;
-      if (g == 0 && row < nr) {
-        float *s = mls + (warp * GMAX + row) * 4;
-        s[0] = m[nb];
-        s[1] = l[nb];
-        s[2] = sg[nb];
-      }
-      if (hold < 0 || row >= nr) continue;
+    if (g == 0) {
+      float *s = mls + (warp * RW + tq) * 4;
+      s[0] = m;
+      s[1] = l;
+      s[2] = sg;
+    }
+    if (hold >= 0) {
       // Rows rotated by 8 floats each, which spreads the four over the banks.
-      float *o = reinterpret_cast<float *>(smem + hold * 2 * TILE) + row * 2 * D;
+      float *o = reinterpret_cast<float *>(smem + hold * 2 * TILE) + (RW * blk + tq) * 2 * D;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int d0 = (16 * i + (FP8 ? 2 * g : g) + 8 * tq) & (D - 1);
         const int d1 = (16 * i + (FP8 ? 2 * g + 1 : g + 8) + 8 * tq) & (D - 1);
-        o[d0] = acc[nb][i][0];
-        o[D + d0] = acc[nb][i][1];
-        o[d1] = acc[nb][i][2];
-        o[D + d1] = acc[nb][i][3];
+        o[d0] = acc[i][0];
+        o[D + d0] = acc[i][1];
+        o[d1] = acc[i][2];
+        o[D + d1] = acc[i][3];
       }
     }
     consumer_sync();
     const int dim = threadIdx.x;
     const float down = FP8 ? k2p56 : 1.f;
     float *recs = a.recs + (c + it.vrow) * gs * REC;
+    // Row `row` is row row % RW of the warps line R + row / RW.
+    auto stat = [&](int ln, int row) { return mls + ((ln * R + row / RW) * RW + row % RW) * 4; };
     if (dim < nr) {  // a thread per row: the warps' weights, sigma, log-sum-exp
-      float M = -INFINITY, L = 0.f, S = 0.f;
+      float M = -INFINITY, L = 0.f, S = 0.f, f[NL];
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) M = fmaxf(M, mls[(w * GMAX + dim) * 4]);
+      for (int w = 0; w < NL; ++w) M = fmaxf(M, stat(w, dim)[0]);
       const bool none = M == -INFINITY || ab.raised();
-      float f[NCW];
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) {
-        const float *s = mls + (w * GMAX + dim) * 4;
+      for (int w = 0; w < NL; ++w) {
+        const float *s = stat(w, dim);
         f[w] = none ? 0.f : fast_exp2(s[0] - M);
         L = fmaf(f[w], s[1], L);
         S = fmaf(f[w], s[2], S);
       }
       const float inv = none ? 0.f : 1.f / L;
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) mls[(w * GMAX + dim) * 4 + 3] = f[w] * inv * down;
+      for (int w = 0; w < NL; ++w) stat(w, dim)[3] = f[w] * inv * down;
       recs[dim * REC + 2 * D] = S * inv;
       recs[dim * REC + 2 * D + 1] = none ? -INFINITY : M + log2f(L);
     }
     consumer_sync();
-    const float *sums[NCW];
+    const float *sums[NL];
 #pragma unroll
-    for (int w = 0; w < NCW; ++w) sums[w] = held[w] < 0 ? nullptr : reinterpret_cast<const float *>(smem + held[w] * 2 * TILE);
+    for (int w = 0; w < NL; ++w)
+      sums[w] = held[w * R] < 0 ? nullptr : reinterpret_cast<const float *>(smem + held[w * R] * 2 * TILE);
 #pragma unroll 4
     for (int row = 0; row < nr; ++row) {
-      const int at = row * 2 * D + ((dim + 8 * (row & 3)) & (D - 1));
+      const int at = row * 2 * D + ((dim + 8 * (row % RW)) & (D - 1));
       float o1 = 0.f, o2 = 0.f;
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) {
-        if (sums[w] == nullptr) continue;  // the warp had no tile of the item
-        const float f = mls[(w * GMAX + row) * 4 + 3];
+      for (int w = 0; w < NL; ++w) {
+        if (sums[w] == nullptr) continue;  // the warps had no tile of the item
+        const float f = stat(w, row)[3];
         o1 = fmaf(f, sums[w][at], o1);
         o2 = fmaf(f, sums[w][at + D], o2);
       }
@@ -797,10 +733,11 @@ struct CombineArgs {
   __nv_bfloat16 *out;
   float *lse;
   long long ots, ohs, nslots;
-  int Hq, G, T, gs;
+  int Hq, G, T, gs, group;  // records of a slot, rows of a group
 };
 
 constexpr int CCH = 512;
+constexpr int kFewRecs = 32;
 
 __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
   __shared__ float wsig[2][CCH];
@@ -816,26 +753,57 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
   const bool bad = a.cu != nullptr && (first < 0 || end > a.T);
   float o = 0.f, lse2 = -INFINITY;
   if (!bad && len - n + (t - first) >= 0 && len > 0) {
-    const int kvh = h / a.G, ng = (n * a.G + GMAX - 1) / GMAX;
+    const int kvh = h / a.G, ng = (n * a.G + a.group - 1) / a.group;
     const int row = (t - first) * a.G + (h - kvh * a.G);
-    const int2 mt =
-        a.meta[(static_cast<long long>(first) * a.G / GMAX + b) * a.c.Hkv + static_cast<long long>(kvh) * ng + row / GMAX];
+    const int2 mt = a.meta[groups_before(first, b, a.G, a.group) * a.c.Hkv + static_cast<long long>(kvh) * ng +
+                           row / a.group];
     // An entry outside the records (left by an earlier call when this one
     // did no work) is not followed.
     const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
     const int nrec = inside ? mt.y : 0;
     const size_t stride = static_cast<size_t>(a.gs) * REC;
-    const float *rec = a.recs + (inside ? mt.x : 0) * stride + static_cast<size_t>(row % GMAX) * REC;
-    float M = -INFINITY;
-    for (int s = dim; s < nrec; s += D) M = fmaxf(M, rec[s * stride + 2 * D + 1]);
+    const float *rec = a.recs + (inside ? mt.x : 0) * stride + static_cast<size_t>(row % a.group) * REC;
+    float M = -INFINITY, W = 0.f, o1 = 0.f, o2 = 0.f, sf = 0.f;
+    if (nrec <= kFewRecs) {
+      // Few records: every thread reads them all at once, in one latency, and
+      // keeps a running maximum.
+      for (int base = 0; base < nrec; base += 8) {
+        float e[8], sr[8], x1[8], x2[8], mx = M;
 #pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-    if ((dim & 31) == 0) slot[dim >> 5] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(slot[0], slot[1]), fmaxf(slot[2], slot[3]));
-    if (M != -INFINITY) {
-      float W = 0.f, o1 = 0.f, o2 = 0.f, sf = 0.f;
-      for (int base = 0; base < nrec; base += CCH) {
+        for (int i = 0; i < 8; ++i) {
+          const float *r = rec + (base + i) * stride;
+          const bool in = base + i < nrec;
+          e[i] = in ? r[2 * D + 1] : -INFINITY;
+          sr[i] = in ? r[2 * D] : 0.f;
+          x1[i] = in ? r[dim] : 0.f;
+          x2[i] = in ? r[D + dim] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, e[i]);
+        if (mx == -INFINITY) continue;
+        const float back = exp2f(M - mx);
+        W *= back;
+        sf *= back;
+        o1 *= back;
+        o2 *= back;
+        M = mx;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float w = exp2f(e[i] - M);
+          W += w;
+          sf = fmaf(w, sr[i], sf);
+          o1 = fmaf(w, x1[i], o1);
+          o2 = fmaf(w, x2[i], o2);
+        }
+      }
+    } else {
+      for (int s = dim; s < nrec; s += D) M = fmaxf(M, rec[s * stride + 2 * D + 1]);
+#pragma unroll
+      for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+      if ((dim & 31) == 0) slot[dim >> 5] = M;
+      __syncthreads();
+      M = fmaxf(fmaxf(slot[0], slot[1]), fmaxf(slot[2], slot[3]));
+      for (int base = 0; M != -INFINITY && base < nrec; base += CCH) {
         const int cnt = min(CCH, nrec - base);
         const float *rb = rec + static_cast<size_t>(base) * stride;
         __syncthreads();  // the previous chunk's weights are consumed
@@ -854,6 +822,8 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
           o2 = fmaf(w, rb[i * stride + D + dim], o2);
         }
       }
+    }
+    if (M != -INFINITY) {
       const float inv = 1.f / W;
       o1 *= inv;
       o2 *= inv;
@@ -886,25 +856,32 @@ bool make_page_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, con
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8, int NB>
+template <bool FP8, int R>
 cudaError_t launch_rows(const RowsArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                         cudaStream_t stream) {
   static thread_local unsigned long long configured_ctx = 0;
   const unsigned long long ctx = context_id();
   if (ctx == 0 || configured_ctx != ctx) {
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, NB>,
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(rows_smem(NB)));
+                                         static_cast<int>(ROWS_SMEM));
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  paged_rows_kernel<FP8, NB><<<a.nshare, THREADS, rows_smem(NB), stream>>>(mk, mv, a);
+  paged_rows_kernel<FP8, R><<<a.nshare, THREADS, ROWS_SMEM, stream>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 int paged_rows_shares() { return kCtasPerSm * sm_count(); }
+
+// Rows of a group: eight once a sequence has more than four query rows a kv
+// head on average. GB300, GPU time of four and of eight: one new token x 2 heads
+// 173 and 258 us (64 x 8192 e4m3 keys, a pair of warps half idle); 4 tokens x
+// 2 heads 51 and 38 us (16 sequences of 500 to 6000 e4m3 keys); 8 heads 334 and
+// 269 us (e4m3), 625 and 337 us (bf16): a second group reads the keys again.
+int paged_rows_group(int T, int B, int G) { return static_cast<long long>(T) * G > RW * static_cast<long long>(B) ? 2 * RW : RW; }
 
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
                               long long qhs, const int *seqlens, const int *cu_q, void *out,
@@ -927,14 +904,15 @@ cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r,
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.T = T;
-  a.gs = paged_rows_slot(a.G, cu_q != nullptr);
+  const int group = paged_rows_group(T, c.B, a.G);
+  a.gs = paged_rows_slot(group, a.G, cu_q != nullptr);
   a.nshare = paged_rows_shares();
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  const long long vrows = paged_rows_vrows(T, c.B, a.G, c.Hkv);
+  const long long vrows = paged_rows_vrows(T, c.B, a.G, c.Hkv, group);
   a.meta = static_cast<int2 *>(workspace);
   a.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + paged_rows_meta_bytes(vrows));
   cudaError_t e;
-  if (a.gs <= 4) e = fp8 ? launch_rows<true, 1>(a, mk, mv, stream) : launch_rows<false, 1>(a, mk, mv, stream);
+  if (group == 4) e = fp8 ? launch_rows<true, 1>(a, mk, mv, stream) : launch_rows<false, 1>(a, mk, mv, stream);
   else e = fp8 ? launch_rows<true, 2>(a, mk, mv, stream) : launch_rows<false, 2>(a, mk, mv, stream);
   if (e != cudaSuccess) return e;
   CombineArgs k;
@@ -952,6 +930,7 @@ cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r,
   k.G = a.G;
   k.T = T;
   k.gs = a.gs;
+  k.group = group;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(T) * Hq);
   cfg.blockDim = dim3(D);

@@ -105,20 +105,21 @@ cudaError_t launch_kv_read(const PagedCache &c, const int *cu_k, void *k, void *
                            cudaStream_t stream);
 // Few new tokens a sequence (decode: one): split over equal shares of the key
 // stream and combined. Workspace: {first record slot, slots} per virtual row
-// (sequence, kv head, group of 8 query rows), padded to 256 bytes, then
+// (sequence, kv head, group of 4 or 8 query rows), padded to 256 bytes, then
 // (shares + virtual rows) slots of `slot` records of 2 d + 2 floats. CTA c
 // writes its part of virtual row v to slot c + v.
 int paged_rows_shares();  // CTAs of the split kernel
-inline int paged_rows_slot(int G, bool many) { return many || G > 8 ? 8 : G; }
-inline long long paged_rows_vrows(int T, int B, int G, int Hkv) {
-  return (static_cast<long long>(T) * G / 8 + B) * Hkv;
+int paged_rows_group(int T, int B, int G);
+inline int paged_rows_slot(int group, int G, bool many) { return many || G > group ? group : G; }
+inline long long paged_rows_vrows(int T, int B, int G, int Hkv, int group) {
+  return (static_cast<long long>(T) * G / group + B) * Hkv;
 }
 inline size_t paged_rows_meta_bytes(long long vrows) { return (size_t(vrows) * 8 + 255) / 256 * 256; }
 inline size_t paged_rows_workspace_bytes(int T, int B, int G, int Hkv, int d, bool many) {
-  const long long vrows = paged_rows_vrows(T, B, G, Hkv);
-  const int slot = paged_rows_slot(G, many);
-  return paged_rows_meta_bytes(vrows) +
-         size_t(paged_rows_shares() + vrows) * slot * (2 * size_t(d) + 2) * sizeof(float);
+  const int group = paged_rows_group(T, B, G);
+  const long long vrows = paged_rows_vrows(T, B, G, Hkv, group);
+  return paged_rows_meta_bytes(vrows) + size_t(paged_rows_shares() + vrows) * paged_rows_slot(group, G, many) *
+                                            (2 * size_t(d) + 2) * sizeof(float);
 }
 // lse ([T, Hq] fp32) may be null; cu_q null: one new token a sequence.
 cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
