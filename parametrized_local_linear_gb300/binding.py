@@ -68,6 +68,8 @@ _lock = threading.Lock()
 def lib():
     """Load libplx.so (built by ``build.build()``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -489,9 +491,12 @@ def _packed(t, name, heads, d, dev):
 def _launch(fn, dev, stream, args):
     """fn(*args, stream) on the device of the tensors; raises on a bad status."""
     if torch.cuda.current_device() == dev.index:
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        _check(fn(*args, stream.cuda_stream))
+        # The raw handle of the current stream: torch.cuda.current_stream builds
+        # a Stream object around it, which costs 2 us of a 17 us call.
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+                    else stream.cuda_stream)
+        if status != PLX_OK:
+            _check(status)
     else:
         with torch.cuda.device(dev):
             _check(fn(*args, _stream(stream, dev)))

@@ -94,19 +94,16 @@ struct Seq {
 };
 template <int KT, int GS>
 __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
+  // All loads first: they share one latency.
+  const int n = a.seqlens[b], first = a.cu != nullptr ? a.cu[b] : b, end = a.cu != nullptr ? a.cu[b + 1] : b + 1;
   Seq s;
-  s.len = cache_len(a.c, a.seqlens, b);
+  s.len = checked_len(a.c, n);
   s.tiles = (s.len + KT - 1) / KT;
-  s.first = b;
-  s.n = 1;
-  if (a.cu != nullptr) {
-    s.first = a.cu[b];
-    const int end = a.cu[b + 1];
-    s.n = end - s.first;
-    if (s.first < 0 || end > a.T || s.n < 0) {
-      if (a.c.err) atomicOr(a.c.err, kErrBadInput);
-      s.first = s.n = 0;
-    }
+  s.first = first;
+  s.n = end - first;
+  if (first < 0 || end > a.T || s.n < 0) {
+    if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+    s.first = s.n = 0;
   }
   s.ng = (s.n * a.G + GS - 1) / GS;
   return s;

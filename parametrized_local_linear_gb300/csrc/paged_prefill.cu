@@ -95,12 +95,13 @@ struct Seq {
   int len, first, n, nq;  // keys, first packed row, new tokens, row tiles
 };
 __device__ __noinline__ Seq seq_of(const Args &a, int b) {
+  // All loads first: they share one latency.
+  const int n = a.seqlens[b], first = a.cu[b], end = a.cu[b + 1];
   Seq s;
-  s.len = cache_len(a.c, a.seqlens, b);
-  s.first = a.cu[b];
-  const int end = a.cu[b + 1];
-  s.n = end - s.first;
-  if (s.first < 0 || end > a.T || s.n < 0) {
+  s.len = checked_len(a.c, n);
+  s.first = first;
+  s.n = end - first;
+  if (first < 0 || end > a.T || s.n < 0) {
     if (a.c.err) atomicOr(a.c.err, kErrBadInput);
     s.first = s.n = 0;
   }

@@ -34,15 +34,17 @@ __device__ __forceinline__ long long page_row(const PagedCache &c, int b, int h,
   return ((static_cast<long long>(page) * c.Hkv + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
-// Keys of sequence b; 0 (and the device error word set) for a length that the
-// block table cannot hold.
-__device__ __forceinline__ int cache_len(const PagedCache &c, const int *seqlens, int b) {
-  const int n = max(seqlens[b], 0);
+// Keys of a sequence of `n`; 0 (and the device error word set) for a length
+// that the block table cannot hold.
+__device__ __forceinline__ int checked_len(const PagedCache &c, int n) {
   if (n > (static_cast<long long>(c.max_pages) << c.page_shift)) {
     if (c.err) atomicOr(c.err, kErrBadInput);
     return 0;
   }
-  return n;
+  return max(n, 0);
+}
+__device__ __forceinline__ int cache_len(const PagedCache &c, const int *seqlens, int b) {
+  return checked_len(c, seqlens[b]);
 }
 
 // The sequence that packed row t belongs to: the last b with cu[b] <= t, if
