@@ -33,8 +33,8 @@ struct AppendArgs {
 
 // Rows a warp handles: one when there are too few warps to fill the GPU twice
 // with more (a decode step's rows: latency), else eight (bytes in flight).
-// GB300: 34660 tokens x 8 heads to e4m3 %APP1% us with one, %APP8% with eight; 64
-// tokens %SM1% and %SM8%.
+// GB300, one and eight: append of 34660 tokens x 8 heads to e4m3 79 and 40 us,
+// of 64 tokens 3.0 and 4.3; read back of 195089 e4m3 tokens 335 and 180 us.
 int rows_per_warp(long long rows) { return rows < 16ll * WARPS * sm_count() ? 1 : 8; }
 
 template <bool FP8, int N>

@@ -333,25 +333,10 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   if (lane == 0) *plan = p;
 }
 
-// mbar_wait_spin with a loop that stays a loop: unrolled, the four issuing
-// threads' polls alone are tens of KB of code, which take instruction cache
-// from the softmax warps.
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const Abort &ab) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_test_wait(bar, parity)) return true;
-    if (ab.raised()) return false;
-    if (clock64() - t0 > kSpinLimitCycles) {
-      ab.raise(kErrTimeout);
-      return false;
-    }
-  }
-}
-
-// Waits off the tiles' critical path as calls, not copies: see mbar_poll.
+// The issuing threads suspend in their waits: with polls (prefill_tc.cu's) the
+// softmax warps on the same schedulers lose issue slots; 2048 tokens over 32768
+// keys took 705 us against 689. Waits off the tiles' critical path are
+// calls, not copies: code is instruction cache, which is what bounds short items.
 __device__ __noinline__ bool wait_one(uint32_t bar, uint32_t parity, const Abort &ab) {
   return mbar_wait(bar, parity, ab);
 }
@@ -763,13 +748,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NSV;
-          if (j == 0 && k > 0 && !mbar_poll(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
+          if (j == 0 && k > 0 && !mbar_wait(smem_u32(o_free), (k - 1) & 1, ab)) { ok = false; break; }
           if (!mbar_wait(smem_u32(&v_full[st]), (gg / NSV) & 1, ab)) { ok = false; break; }
           const uint64_t vdesc = vdesc0 + st * (TILE_KV >> 4);
           const uint32_t ap = tbase + (x ? COL_S1 : COL_S0);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!mbar_poll(smem_u32(&p_full[2 * x + h]), (gg >> 1) & 1, ab)) { ok = false; break; }
+            if (!mbar_wait(smem_u32(&p_full[2 * x + h]), (gg >> 1) & 1, ab)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < count; ++c) {
@@ -861,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         for (int j = 0; j < nt; ++j) {
           const int gg = g + j, x = gg & 1, st = gg % NSK;
           if (!mbar_wait(smem_u32(&k_full[st]), (gg / NSK) & 1, ab)) { ok = false; break; }
-          if (gg >= 2 && !mbar_poll(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
+          if (gg >= 2 && !mbar_wait(smem_u32(&pv_issued[2 * x + (is_s ? 0 : 1)]), ((gg - 2) >> 1) & 1, ab)) { ok = false; break; }
           tc_fence_after();
           const uint64_t kdesc = kdesc0 + st * (TILE_KV >> 4);
           const uint32_t d = tbase + (x ? COL_S1 : COL_S0) + col_off;
