@@ -50,14 +50,14 @@ constexpr int HALF_Q = BM * 64 * 2;
 constexpr int HALF_KV = BN * 64 * 2;
 constexpr int TILE_KV = 2 * HALF_KV;  // 16 KB: a bf16 K or V tile
 constexpr int RAW = BN * D;           // 8 KB: an e4m3 K or V tile
-constexpr int NRAW = 4;               // raw stages (K and V together)
+constexpr int NRAW = 3;               // raw stages (K and V together)
 constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_T = 64, COL_O1 = 256, COL_O2 = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int EP_WARP = 4, O1_WARP = 8, S_WARP = 10, LOAD_WARP = 12;
 
 template <bool FP8>
 struct Cfg {
-  static constexpr int NSK = FP8 ? 2 : 4, NSV = FP8 ? 3 : 4;  // bf16 K and V stages
+  static constexpr int NSK = FP8 ? 3 : 4, NSV = NSK;  // bf16 K and V stages
   static constexpr int WARPS = FP8 ? 16 : 14;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int OFF_R = 2 * HALF_Q;
@@ -944,7 +944,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     bool ok = true;
     while (ok && walk_next<true>(wk, a)) {
       const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-      const int len = it.len, kvh = it.kvh, j1 = it.j1;
+      const int len = it.len, j1 = it.j1;
+      const uint8_t *head = scales + (static_cast<long long>(it.kvh) << shift);
+      const long long page_step = static_cast<long long>(a.c.Hkv) << shift;
       // Lane l looks up the scale of row part 32 + l of a tile (0: a row that
       // is not there), the page two tiles and the byte one tile ahead.
       const int mine = part * 32 + lane;
@@ -953,8 +955,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         return j < j1 && key < len ? table[key >> shift] : -1;
       };
       auto scale_byte = [&](int j, int page) -> uint32_t {
-        if (page < 0 || page >= a.c.num_pages) return 0u;
-        return scales[((static_cast<long long>(page) * a.c.Hkv + kvh) << shift) + ((j * BN + mine) & pmask)];
+        return page >= 0 && page < a.c.num_pages ? head[page * page_step + ((j * BN + mine) & pmask)] : 0u;
       };
       uint32_t e_next = scale_byte(it.j0, page_of(it.j0));
       int page_next = page_of(it.j0 + 1);
