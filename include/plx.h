@@ -286,9 +286,12 @@ int plx_decode_default_nsplit(int B, int Hkv);
  * key). Whatever the pages hold behind seqlens[b], NaN included, does not reach
  * any result. Packed rows have strides in elements, for the token and the head;
  * a row's d values are contiguous. Strides are multiples of 8 and at least d,
- * pointers 16-byte aligned (4 bytes for int32 and fp32). A page number outside 0 .. num_pages - 1 or a length beyond
- * max_pages * page_size is not followed: the row's results are undefined and
- * plx_check_device_error reports PLX_ERR_INVALID_ARG.
+ * pointers 16-byte aligned (4 bytes for int32 and fp32). A page number outside
+ * 0 .. num_pages - 1, a length beyond max_pages * page_size or a cu_q that
+ * decreases or passes T is not followed: the sequence's results are undefined
+ * and plx_check_device_error reports PLX_ERR_INVALID_ARG; nothing outside the
+ * arguments is read or written. Lengths below zero count as zero. No atomics:
+ * given arguments and lengths give the same bits on one GPU model.
  */
 
 /*

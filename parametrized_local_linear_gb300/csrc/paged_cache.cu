@@ -51,7 +51,11 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs 
     if (b >= 0) {
       const int end = a.cu_q ? a.cu_q[b + 1] : b + 1;
       const int pos = cache_len(a.c, a.seqlens, b) - end + t;
-      if (pos >= 0) my_row = page_row(a.c, b, h, pos);  // else padding
+      if (end > a.T) {
+        if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+      } else if (pos >= 0) {  // else padding
+        my_row = page_row(a.c, b, h, pos);
+      }
     }
   }
   const __nv_bfloat16 *src = (half ? a.v : a.k) + t0 * a.token_stride + h * a.head_stride + sub * 8;

@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     // ------------------------------------------------------------ plan
     long long W = 0;
     int rows = 0, lmin = 0x7fffffff, lmax = 0;  // rows of records and lengths of sequences with keys
+#pragma unroll 4
     for (int i = lane; i < a.c.B; i += 32) {
       const Seq s = seq_of<KT, GS>(a, i);
       const long long u = static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;

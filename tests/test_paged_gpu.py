@@ -515,6 +515,110 @@ def test_prefill_replays_in_a_graph_with_other_lengths():
     plx_check_device_error()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_short_sequences(fp8):
+    """More sequences than the plans' warp has lanes, empty ones among them."""
+    dev = device()
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 70, 150).tolist()
+    lens[3:40] = [0] * 37
+    counts = [int(rng.integers(0, n + 1)) if rng.random() < 0.5 else min(n, 1) for n in lens]
+    pool = ref.filled_pool(lens, 2, 16, fp8, 14)
+    kw = dict(seqlens=pool.seqlens.to(dev), **pool.to(dev))
+    for many in (counts, [min(n, 1) for n in lens], [min(n, 1 + b % 3) for b, n in enumerate(lens)]):
+        T = sum(many)
+        q, r = ref.normal_rows(T, 4, 1), ref.normal_rows(T, 4, 2, 0.05)
+        o, _, bound = ref.reference(pool, q, r, many)
+        out, _ = plx_prefill_fwd_paged(q.to(dev), r.to(dev), cu_q=ends(many).to(dev), **kw)
+        plx_check_device_error()
+        ref.assert_within(out, o, bound, "prefill")
+    q, r = ref.normal_rows(150, 4, 3), ref.normal_rows(150, 4, 4, 0.05)
+    o, _, bound = ref.reference(pool, q, r, [1] * 150)
+    out = plx_decode_fwd_paged(q.to(dev), r.to(dev), **kw)
+    plx_check_device_error()
+    ref.assert_within(out, o, bound, "decode")
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (6, 1)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_batches_of_alike_sequences(fp8, Hq, Hkv):
+    """Batches of one shape with many row tiles (dealt to the CTAs in rounds
+    of whole items), against the same rows of a batch that is not."""
+    dev = device()
+    B, n, L = 24 * (3 - Hkv), 1300, 1400
+    pool = ref.filled_pool([L] * 2 + [40], Hkv, 64, fp8, 15)
+    table = pool.table[[b % 2 for b in range(B)] + [2]].contiguous().to(dev)  # shared pages
+    sl = torch.tensor([L] * B + [40], dtype=I32, device=dev)
+    T = B * n + 7
+    q, r = ref.normal_rows(T, Hq, 1).to(dev), ref.normal_rows(T, Hq, 2, 0.05).to(dev)
+    kw = pool.to(dev)
+    kw.pop("block_table")
+    lse, lse2 = torch.empty(T, Hq, device=dev), torch.empty(B * n, Hq, device=dev)
+    mixed, _ = plx_prefill_fwd_paged(q, r, block_table=table, seqlens=sl, cu_q=ends([n] * B + [7]).to(dev),
+                                     lse=lse, **kw)
+    alike, _ = plx_prefill_fwd_paged(q[:B * n], r[:B * n], block_table=table[:B], seqlens=sl[:B],
+                                     cu_q=ends([n] * B).to(dev), lse=lse2, **kw)
+    plx_check_device_error()
+    assert_bf16_close(alike.double().cpu().numpy(), mixed[:B * n].double().cpu().numpy())
+    assert (lse[:B * n] - lse2).abs().max() <= LSE_ABS
+    rows = [0, 1, 63, 64, 128, n - 1]
+    for b in (0, 11, B - 1):
+        K, V = pool.get(b % 2, L)
+        for h in range(Hq):
+            i = torch.tensor([b * n + x for x in rows], device=dev)
+            g = h // (Hq // Hkv)
+            o, _, bound = ref.attend(q[i, h].double().cpu().numpy(), r[i, h].double().cpu().numpy(), K[:, g],
+                                     V[:, g], np.array(rows) + L - n + 1)
+            ref.assert_within(alike[i, h], o, bound, "alike")
+
+
+def test_no_new_tokens():
+    dev = device()
+    pool = ref.filled_pool([40, 7], 2, 16, True, 3)
+    kw = pool.to(dev)
+    none = torch.empty(0, 4, 128, dtype=torch.bfloat16, device=dev)
+    zero = torch.zeros(3, dtype=I32, device=dev)
+    out, _ = plx_prefill_fwd_paged(none, none, seqlens=pool.seqlens.to(dev), cu_q=zero, **kw)
+    assert out.shape == (0, 4, 128)
+    plx_kv_append(none[:, :2], none[:, :2], seqlens=pool.seqlens.to(dev), cu_q=zero, **kw)
+    assert plx_kv_read(**kw, cu_k=zero, T=0)[0].shape == (0, 2, 128)
+    # rows that belong to no sequence
+    for rows in (9, 200):
+        q = ref.normal_rows(rows, 4, 1).to(dev)
+        out = torch.full_like(q, 2.0)
+        plx_prefill_fwd_paged(q, q, seqlens=pool.seqlens.to(dev), cu_q=zero, out=out, **kw)
+        k = q[:, :2].contiguous()
+        plx_kv_append(k, k, seqlens=pool.seqlens.to(dev), cu_q=zero, **kw)
+        plx_check_device_error()
+        assert torch.all(out == 2.0) and same_bits(kw["kpages"], pool.k)
+
+
+def test_c_calls_allocate_their_own_workspace():
+    """workspace = NULL at the C boundary: the same results."""
+    import ctypes
+    dev = device()
+    L = binding.lib()
+    p = lambda t: ctypes.c_void_p(t.data_ptr()) if t is not None else None  # noqa: E731
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for fp8 in (False, True):
+        (q, r), kw = _problem(dev, fp8, (300, 80), (100, 80))
+        pages = [kw[k] for k in ("kpages", "vpages", "kscale", "vscale", "block_table", "seqlens", "cu_q")]
+        n, Hkv, page, d = kw["kpages"].shape
+        sizes = (2, 4, Hkv, d, n, page, kw["block_table"].shape[1])
+        out = torch.empty_like(q)
+        s = L.plx_prefill_fwd_paged(p(q), p(r), 512, 128, *map(p, pages), p(out), 512, 128, None, q.shape[0],
+                                    *sizes, None, 0, st)
+        assert s == binding.PLX_OK, L.plx_last_error_message()
+        want, _ = plx_prefill_fwd_paged(q, r, **kw)
+        dec = torch.empty_like(q[:2])
+        s = L.plx_decode_fwd_paged(p(q), p(r), *map(p, pages[:6]), p(dec), *sizes, None, 0, st)
+        assert s == binding.PLX_OK, L.plx_last_error_message()
+        kw.pop("cu_q")
+        want_dec = plx_decode_fwd_paged(q[:2].contiguous(), r[:2].contiguous(), **kw)
+        plx_check_device_error()
+        assert torch.equal(out, want) and torch.equal(dec, want_dec)
+
+
 # ------------------------------------------------------------ beyond 32 bits
 @pytest.mark.parametrize("fp8", [False, True])
 def test_pages_past_32_bit_offsets(fp8):
@@ -601,3 +705,48 @@ def test_bad_pages_and_lengths_are_reported(fp8, bad):
         cu = torch.tensor([0, kw["block_table"].shape[1] * 16 + 5, kw["block_table"].shape[1] * 16 + 8], dtype=I32)
         plx_kv_read(**kw, cu_k=cu.to(dev), T=int(cu[-1]))
         reported()
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 60], [0, 70, 6], [-2, 3, 6], [0, 6, 3]])
+@pytest.mark.parametrize("rows", [6, 40])
+def test_bad_row_offsets_are_reported(cu, rows):
+    """cu_q that passes T, decreases or starts below 0 (6 rows: the kernel for
+    few rows, 40: the tile kernel): reported, and the rows beside the output
+    are not written."""
+    dev = device()
+    pool = ref.filled_pool([100, 60], 2, 16, True, 3)
+    kw = pool.to(dev)
+    sl = pool.seqlens.to(dev)
+    guard = torch.full((rows + 100, 4, 128), 3.0, dtype=torch.bfloat16, device=dev)
+    q = ref.normal_rows(rows, 4, 1).to(dev)
+    bad = torch.tensor(cu, dtype=I32, device=dev)
+    plx_prefill_fwd_paged(q, q, seqlens=sl, cu_q=bad, out=guard[50:50 + rows], **kw)
+    with pytest.raises(PlxError) as e:
+        plx_check_device_error()
+    assert e.value.status == binding.PLX_ERR_INVALID_ARG
+    assert torch.all(guard[:50] == 3.0) and torch.all(guard[50 + rows:] == 3.0)
+    k = q[:, :2].contiguous()
+    plx_kv_append(k, k, seqlens=sl, cu_q=bad, **kw)  # rows go to a place of a sequence or nowhere
+    try:
+        plx_check_device_error()
+    except PlxError as err:
+        assert err.status == binding.PLX_ERR_INVALID_ARG
+
+
+def test_negative_lengths_count_as_zero():
+    dev = device()
+    pool = ref.filled_pool([40, 30], 2, 16, False, 3)
+    kw = pool.to(dev)
+    sl = torch.tensor([-5, 30], dtype=I32, device=dev)
+    pool.lens[0] = 0
+    q, r = ref.normal_rows(2, 4, 1), ref.normal_rows(2, 4, 2, 0.05)
+    o, _, bound = ref.reference(pool, q, r, [1, 1])
+    out = plx_decode_fwd_paged(q.to(dev), r.to(dev), seqlens=sl, **kw)
+    ref.assert_within(out, o, bound, "decode")
+    out, _ = plx_prefill_fwd_paged(q.to(dev), r.to(dev), seqlens=sl, cu_q=ends([1, 1]).to(dev), **kw)
+    ref.assert_within(out, o, bound, "prefill")
+    k = q[:, :2].contiguous()
+    plx_kv_append(k.to(dev), k.to(dev), seqlens=sl, **kw)
+    plx_check_device_error()
+    pool.put(1, 29, k[1:].double().numpy(), k[1:].double().numpy())
+    assert same_bits(kw["kpages"], pool.k) and same_bits(kw["vpages"], pool.v)
