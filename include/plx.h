@@ -269,14 +269,15 @@ int plx_decode_default_nsplit(int B, int Hkv);
  *   kscale, vscale : uint8 [num_pages, Hkv, page_size], both or neither. A row
  *                    of codes stands for code * 2^(E - 127), E its byte in
  *                    1 .. 254 (E = 0 only for rows of zeros). Attention over e4m3
- *                    pages wants |v| < 2^70.
+ *                    pages wants |v| and |v (r.k)| below 2^70.
  *   block_table    : int32 [B, max_pages] on the device. Position p of sequence
  *                    b is in slot p % page_size of page
  *                    block_table[b, p / page_size]. Entries behind a sequence's
  *                    last page are not read, and pages may be shared between
  *                    sequences that only read them.
  *   seqlens        : int32 [B] on the device: the keys of each sequence, the
- *                    call's new tokens included; at most max_pages * page_size.
+ *                    call's new tokens included; at most max_pages * page_size
+ *                    (which is at most 2^30).
  *   cu_q           : int32 [B + 1] on the device, non-decreasing from
  *                    cu_q[0] = 0: the n_b = cu_q[b + 1] - cu_q[b] >= 0 new
  *                    tokens of sequence b are rows cu_q[b] .. of the T packed
@@ -284,13 +285,15 @@ int plx_decode_default_nsplit(int B, int Hkv);
  * New token i (0 .. n_b - 1) of sequence b has position seqlens[b] - n_b + i; a
  * negative one marks padding (a row that has no place in the cache and sees no
  * key). Whatever the pages hold behind seqlens[b], NaN included, does not reach
- * any result. Packed rows have strides in elements, for the token and the head;
+ * any result. Values in front of it must be finite: the products of a tile of
+ * keys give a value that a token does not see yet the weight zero. Packed rows have strides in elements, for the token and the head;
  * a row's d values are contiguous. Strides are multiples of 8 and at least d,
  * pointers 16-byte aligned (4 bytes for int32 and fp32). A page number outside
  * 0 .. num_pages - 1, a length beyond max_pages * page_size or a cu_q that
- * decreases or passes T is not followed: the sequence's results are undefined
- * and plx_check_device_error reports PLX_ERR_INVALID_ARG; nothing outside the
- * arguments is read or written. Lengths below zero count as zero. No atomics:
+ * decreases, starts below 0 or passes T is not followed: the sequence's results
+ * are undefined and plx_check_device_error reports PLX_ERR_INVALID_ARG (append
+ * and read: where one of their rows meets it); nothing outside the arguments is
+ * read or written. Lengths below zero count as zero. No atomics:
  * given arguments and lengths give the same bits on one GPU model.
  */
 

@@ -449,9 +449,9 @@ plx_status paged_cache(const char *fn, plx::PagedCache *c, const void *kpages, c
   if (!aligned16(kscale) || !aligned16(vscale))
     return fail(PLX_ERR_INVALID_ARG, "%s: kscale and vscale must be 16-byte aligned", fn);
   if (static_cast<long long>(num_pages) * Hkv > 0x7fffffffLL ||
-      static_cast<long long>(max_pages) * page_size > 0x7fffffffLL)
-    return fail(PLX_ERR_UNSUPPORTED, "%s: num_pages * Hkv and max_pages * page_size must be < 2^31",
-                fn);
+      static_cast<long long>(max_pages) * page_size > 1LL << 30)
+    return fail(PLX_ERR_UNSUPPORTED,
+                "%s: num_pages * Hkv must be < 2^31 and max_pages * page_size at most 2^30", fn);
   c->k = kpages;
   c->v = vpages;
   c->kscale = kscale;

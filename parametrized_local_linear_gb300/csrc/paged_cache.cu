@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs 
     const int t = static_cast<int>(t0) + lane;
     const int b = row_sequence(a.cu_q, a.c.B, t);
     if (b >= 0) {
-      const int end = a.cu_q ? a.cu_q[b + 1] : b + 1;
+      const int first = a.cu_q ? a.cu_q[b] : b, end = a.cu_q ? a.cu_q[b + 1] : b + 1;
       const int pos = cache_len(a.c, a.seqlens, b) - end + t;
-      if (end > a.T) {
+      if (first < 0 || end > a.T) {
         if (a.c.err) atomicOr(a.c.err, kErrBadInput);
       } else if (pos >= 0) {  // else padding
         my_row = page_row(a.c, b, h, pos);
@@ -112,8 +112,10 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
     const int t = static_cast<int>(t0) + lane;
     const int b = row_sequence(a.cu_k, a.c.B, t);
     if (b >= 0) {
-      const int pos = t - a.cu_k[b];
-      if (pos < (static_cast<long long>(a.c.max_pages) << a.c.page_shift)) my_row = page_row(a.c, b, h, pos);
+      const int first = a.cu_k[b], pos = t - first;  // first <= t
+      const bool in = first >= 0 && a.cu_k[b + 1] <= a.T &&
+                      pos < (static_cast<long long>(a.c.max_pages) << a.c.page_shift);
+      if (in) my_row = page_row(a.c, b, h, pos);
       else if (a.c.err) atomicOr(a.c.err, kErrBadInput);
     }
   }

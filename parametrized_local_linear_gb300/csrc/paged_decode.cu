@@ -100,10 +100,12 @@ __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
   s.len = checked_len(a.c, n);
   s.tiles = (s.len + KT - 1) / KT;
   s.first = first;
-  s.n = end - first;
-  if (first < 0 || end > a.T || s.n < 0) {
+  s.n = 0;
+  if (first < 0 || end > a.T || end < first) {
     if (a.c.err) atomicOr(a.c.err, kErrBadInput);
-    s.first = s.n = 0;
+    s.first = 0;
+  } else {
+    s.n = end - first;
   }
   s.ng = (s.n * a.G + GS - 1) / GS;
   return s;

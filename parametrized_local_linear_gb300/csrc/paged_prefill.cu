@@ -100,10 +100,12 @@ __device__ __noinline__ Seq seq_of(const Args &a, int b) {
   Seq s;
   s.len = checked_len(a.c, n);
   s.first = first;
-  s.n = end - first;
-  if (first < 0 || end > a.T || s.n < 0) {
+  s.n = 0;
+  if (first < 0 || end > a.T || end < first) {
     if (a.c.err) atomicOr(a.c.err, kErrBadInput);
-    s.first = s.n = 0;
+    s.first = 0;
+  } else {
+    s.n = end - first;
   }
   s.nq = (s.n + a.TQ - 1) / a.TQ;
   return s;

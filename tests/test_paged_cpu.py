@@ -242,3 +242,10 @@ def test_row_shapes_are_rejected():
         _py("prefill", a, r=torch.zeros(5, 3, 128, dtype=bf))
     with pytest.raises(ValueError, match="T must be"):
         _py("read", a, T=-1)
+
+
+@pytest.mark.parametrize("call", sorted(CALLS))
+def test_a_table_past_2_to_30_positions_is_rejected(lib, call):
+    """Positions plus a tile stay inside 32 bits."""
+    assert CALLS[call](lib, width=(1 << 26) + 1) == UNS  # 2^30 + 16 positions
+    assert b"2^30" in lib.plx_last_error_message()

@@ -750,3 +750,89 @@ def test_negative_lengths_count_as_zero():
     plx_check_device_error()
     pool.put(1, 29, k[1:].double().numpy(), k[1:].double().numpy())
     assert same_bits(kw["kpages"], pool.k) and same_bits(kw["vpages"], pool.v)
+
+
+@pytest.mark.parametrize("cu", [[-2**31, 3], [2, -2**31], [-1, 3], [0, 50]])
+@pytest.mark.parametrize("rows", [4, 40])
+def test_offsets_whose_difference_overflows_are_reported(cu, rows):
+    """Offsets are compared before they are subtracted."""
+    dev = device()
+    pool = ref.filled_pool([100], 2, 16, False, 3)
+    kw = pool.to(dev)
+    q = ref.normal_rows(rows, 4, 1).to(dev)
+    k = q[:, :2].contiguous()
+    bad = torch.tensor(cu, dtype=I32, device=dev)
+    guard = torch.full((rows + 100, 4, 128), 3.0, dtype=torch.bfloat16, device=dev)
+
+    def reported(met):
+        if not met:
+            return plx_check_device_error()
+        with pytest.raises(PlxError) as e:
+            plx_check_device_error()
+        assert e.value.status == binding.PLX_ERR_INVALID_ARG
+
+    plx_prefill_fwd_paged(q, q, seqlens=pool.seqlens.to(dev), cu_q=bad, out=guard[50:50 + rows], **kw)
+    reported(True)
+    assert torch.all(guard[:50] == 3.0) and torch.all(guard[50 + rows:] == 3.0)
+    met = cu != [2, -2**31]  # no row lies between such offsets
+    plx_kv_append(k, k, seqlens=pool.seqlens.to(dev), cu_q=bad, **kw)
+    reported(met)
+    assert same_bits(kw["kpages"], pool.k) and same_bits(kw["vpages"], pool.v)
+    gk = torch.full((rows, 2, 128), 3.0, dtype=torch.bfloat16, device=dev)
+    gv = gk.clone()
+    plx_kv_read(**kw, cu_k=bad, T=rows, k=gk, v=gv)
+    reported(met)
+    assert torch.all(gk == 3.0) and torch.all(gv == 3.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_debug_build_gives_the_same_bits(fp8, monkeypatch):
+    dev = device()
+    dbg = binding.load_debug_lib()
+
+    def run():
+        (q, r), kw = _problem(dev, fp8)
+        k, v = q[:, :2].contiguous(), r[:, 2:].contiguous()
+        plx_kv_append(k, v, **kw)
+        out, lse = plx_prefill_fwd_paged(q, r, lse=torch.empty(q.shape[:2], device=dev), **kw)
+        few, _ = plx_prefill_fwd_paged(q[:3], r[:3], **dict(kw, cu_q=ends([2, 0, 1]).to(dev)))
+        kw.pop("cu_q")
+        sl = kw.pop("seqlens")
+        step = plx_decode_fwd_paged(q[:3].contiguous(), r[:3].contiguous(), seqlens=sl, **kw)
+        back = plx_kv_read(cu_k=ends(sl.tolist()).to(dev), T=int(sl.sum()), **kw)
+        plx_check_device_error()
+        return [out, lse.view(torch.int16), few, step, *back]
+
+    release = run()
+    monkeypatch.setattr(binding, "lib", lambda: dbg)
+    assert all(same_bits(a, b) for a, b in zip(release, run()))
+
+
+def test_calls_from_two_host_threads():
+    """Each thread with its own stream and cache, calls overlapping."""
+    import threading
+    dev = device()
+    problems = [_problem(dev, True, (900, 300), (200, 300), 5), _problem(dev, False, (700, 64), (33, 64), 6)]
+    want = [plx_prefill_fwd_paged(*rows, **kw)[0] for rows, kw in problems]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                rows, kw = problems[i]
+                for _ in range(20):
+                    got[i].append(plx_prefill_fwd_paged(*rows, **kw)[0])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 - raised again by the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    plx_check_device_error()
+    assert not errors
+    for i in range(2):
+        assert len(got[i]) == 20 and all(torch.equal(x, want[i]) for x in got[i])
