@@ -416,20 +416,26 @@ def plx_decode_default_nsplit(B, Hkv) -> int:
     return int(lib().plx_decode_default_nsplit(B, Hkv))
 
 
+def _is(t, dtype, shape, index):
+    """Whether t is a contiguous tensor of this type and shape on CUDA device
+    `index`. The paged calls check up to ten tensors, and a decode step waits
+    for them: this reads the fewest attributes, and only a tensor that fails it
+    goes through the checks that say why."""
+    return (t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
+
+
 def _like(t, name, dtype, shape, dev):
-    """_need with the whole shape, in the fewest attribute reads (the paged
-    calls check up to ten tensors, and a decode step waits for them)."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    """_need with the whole shape."""
+    if _is(t, dtype, shape, dev.index):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     _need(t, name, dtype, len(shape), dev)
 
 
-def _pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
-    """Checks of a paged cache and of the int32 [B] lengths (or None) that go
-    with it; returns the pointers (kpages, vpages, kscale, vscale, block_table)
-    and the sizes (B, Hkv, d, num_pages, page_size, max_pages)."""
+def _check_pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
+    """Raises for what is wrong with the tensors of a paged cache."""
     shape = kpages.shape
     if len(shape) != 4:
         raise ValueError(f"kpages must be [num_pages, Hkv, page_size, d], got shape {tuple(shape)}")
@@ -438,7 +444,6 @@ def _pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
     B, width = block_table.shape
     fp8 = kscale is not None or vscale is not None
     dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
-    n, Hkv, page, d = shape
     if fp8:
         for name, t in (("kscale", kscale), ("vscale", vscale)):
             if t is None or t.shape != shape[:3]:
@@ -458,13 +463,30 @@ def _pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
     _like(block_table, "block_table", torch.int32, (B, width), dev)
     if seqlens is not None:
         _like(seqlens, "seqlens", torch.int32, (B,), dev)
-    if not fp8:
-        return (kpages.data_ptr(), vpages.data_ptr(), None, None, block_table.data_ptr()), (
-            B, Hkv, d, n, page, width)
-    _like(kscale, "kscale", torch.uint8, shape[:3], dev)
-    _like(vscale, "vscale", torch.uint8, shape[:3], dev)
-    return (kpages.data_ptr(), vpages.data_ptr(), kscale.data_ptr(), vscale.data_ptr(),
-            block_table.data_ptr()), (B, Hkv, d, n, page, width)
+    if fp8:
+        _like(kscale, "kscale", torch.uint8, shape[:3], dev)
+        _like(vscale, "vscale", torch.uint8, shape[:3], dev)
+
+
+def _pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
+    """Checks of a paged cache and of the int32 [B] lengths (or None) that go
+    with it; returns the pointers (kpages, vpages, kscale, vscale, block_table)
+    and the sizes (B, Hkv, d, num_pages, page_size, max_pages)."""
+    shape, entries, index = kpages.shape, block_table.shape, dev.index
+    fp8 = kscale is not None and vscale is not None
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    if not (len(shape) == 4 and len(entries) == 2 and entries[0] >= 1
+            and (fp8 or kscale is vscale)
+            and _is(kpages, dtype, shape, index) and _is(vpages, dtype, shape, index)
+            and _is(block_table, torch.int32, entries, index)
+            and (seqlens is None or _is(seqlens, torch.int32, entries[:1], index))
+            and (not fp8 or (_is(kscale, torch.uint8, shape[:3], index)
+                             and _is(vscale, torch.uint8, shape[:3], index)))):
+        _check_pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev)
+    B, width = entries
+    n, Hkv, page, d = shape
+    return (kpages.data_ptr(), vpages.data_ptr(), kscale.data_ptr() if fp8 else None,
+            vscale.data_ptr() if fp8 else None, block_table.data_ptr()), (B, Hkv, d, n, page, width)
 
 
 def _packed(t, name, heads, d, dev):
@@ -475,7 +497,7 @@ def _packed(t, name, heads, d, dev):
     shape = t.shape
     if len(shape) != 3 or shape[2] != d or shape[1] != heads:
         raise ValueError(f"{name} must be [T, {heads}, {d}], got shape {tuple(shape)}")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     ts, hs, ds = t.stride()
     if ds != 1 and d != 1:
@@ -490,7 +512,7 @@ def _packed(t, name, heads, d, dev):
 
 def _launch(fn, dev, stream, args):
     """fn(*args, stream) on the device of the tensors; raises on a bad status."""
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         # The raw handle of the current stream: torch.cuda.current_stream builds
         # a Stream object around it, which costs 2 us of a 17 us call.
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
@@ -508,7 +530,7 @@ def _workspace(workspace, sizer, sizes, stream, dev):
     stream-ordered allocation by the library would give its memory back to the
     driver whenever the GPU idles: 200 us for a call after a synchronize)."""
     if workspace is None:
-        if torch.cuda.current_device() == dev.index:  # the size goes by the device's SM count
+        if torch._C._cuda_getDevice() == dev.index:  # the size goes by the device's SM count
             need = getattr(lib(), sizer)(*sizes)
         else:
             with torch.cuda.device(dev):
@@ -589,17 +611,19 @@ def plx_decode_fwd_paged(q, r, kpages, vpages, block_table, seqlens, kscale=None
     if B != block_table.shape[0] or d != kpages.shape[-1]:
         raise ValueError(f"q must be ({block_table.shape[0]}, {Hq}, {kpages.shape[-1]}), got shape "
                          f"{tuple(shape)}")
-    for name, t in (("r", r), ("out", out)):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
+    rows = [("q", q), ("r", r)] + ([("out", out)] if out is not None else [])
+    good = all([_is(t, torch.bfloat16, shape, dev.index) for _, t in rows])
+    if not good:
+        for name, t in rows:
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
-    _like(q, "q", torch.bfloat16, shape, dev)
-    _like(r, "r", torch.bfloat16, shape, dev)
+    if not good:
+        for name, t in rows:
+            _like(t, name, torch.bfloat16, shape, dev)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _like(out, "out", torch.bfloat16, shape, dev)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_decode_paged_workspace_bytes", (B, Hq, Hkv, d),
                                       stream, dev)
     _launch(lib().plx_decode_fwd_paged, dev, stream,
@@ -626,10 +650,11 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
         raise ValueError("q and r must have the same strides")
     _like(cu_q, "cu_q", torch.int32, (B + 1,), dev)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-    if out.shape != q.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    out_strides = _packed(out, "out", Hq, d, dev)
+        out, out_strides = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev), (Hq * d, d)
+    else:
+        if out.shape != q.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+        out_strides = _packed(out, "out", Hq, d, dev)
     if lse is not None:
         _like(lse, "lse", torch.float32, (T, Hq), dev)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_prefill_paged_workspace_bytes",
