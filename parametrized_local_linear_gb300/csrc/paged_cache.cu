@@ -12,6 +12,10 @@
 // before the first result is used. Consecutive rows of a head are contiguous in
 // their page, and the Hkv warps of a row group together read or write whole
 // contiguous rows on the other side.
+// The bound is memory. GB300: append of 34660 tokens x 8 heads to e4m3 40 us
+// (5.3 TB/s of the 6.8 that a copy reaches; the byte of a scale costs a 32-byte
+// sector), of 16425 tokens to bf16 21.9 us (6.1 TB/s); read back of 195089 e4m3 tokens 180 us (6.7 TB/s); one token a sequence, 64 of them: 2.9
+// us, the launch.
 #include <string.h>
 
 #include "plx_paged.cuh"
