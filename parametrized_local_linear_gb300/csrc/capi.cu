@@ -480,14 +480,51 @@ plx_status check_strides(const char *fn, const char *what, long long token, long
   return PLX_OK;
 }
 
-// Whether a prefill call has so few query rows a sequence and kv head (eight on
-// average) that the kernel that streams keys for eight rows at a time takes it.
-// The tile kernel's products always have 128 rows, the other reads the keys once
-// for every eight. GB300, GPU time of it and of the tile kernel, 64 sequences x
-// 8192 keys x 8 kv heads, 8 rows: bf16 347 and 439 us, e4m3 293 and 576; 16 rows:
-// bf16 673 and 442, e4m3 564 and 576. 16 sequences of 500 to 6000 keys, 8 rows:
-// 50 and 65, 42 and 78; 16 rows: 69 and 65, 69 and 78.
-bool few_rows(int T, int B, int G) { return static_cast<long long>(T) * G <= 8ll * B; }
+// Which kernels a prefill call launches. The tile kernel's products always have
+// 128 rows; the other reads a sequence's keys once for every eight (token, query
+// head) rows. GB300, GPU time of the latter and of the tile kernel, 64 sequences
+// x 8192 keys x 8 kv heads, 8 rows: bf16 347 and 439 us, e4m3 293 and 576; 16
+// rows: bf16 673 and 442, e4m3 564 and 576. 16 sequences of 500 to 6000 keys, 8
+// rows: 50 and 65, 42 and 78; 16 rows: 69 and 65, 69 and 78. Lengths live on the
+// device, so each kernel can be told to take the sequences of at most, or of more
+// than, some number of rows:
+//   - at most eight rows a sequence on average: those of up to 16 go to the rows
+//     kernel and longer ones to the tile kernel, which is left out if no sequence
+//     can have more than 128 rows. 255 tokens over 500 keys each and a chunk of
+//     512 over 32768: 330 and 341 us (bf16, e4m3) against 2038 and 1998 in the rows
+//     kernel alone; 64 sequences of 4 tokens over 4096 keys, which need no tile
+//     kernel: 190 and 156 against 186 and 150.
+//   - more, up to kMixedRows on average, in kMixedSeqs sequences or more: decodes
+//     with chunks among them. Those of one group of rows go to the rows kernel.
+//     Against the tile kernel alone: 63 tokens and a chunk of 512 over 4096 keys
+//     each 214 and 148 us against 234 and 284, 31 tokens and a chunk of 2048 over
+//     8192 keys 342 and 298 against 367 and 451; 16 chunks of 128 over 2048 keys,
+//     none of them short, 82 and 92 against 79 and 83.
+//   - more still, fewer sequences, or more than eight query heads a kv head: the
+//     tile kernel alone (two launches fewer: 12 us of host time).
+constexpr int kMixedRows = 256, kMixedSeqs = 8;
+struct PrefillPlan {
+  bool rows, tiles;
+  plx::RowsPlan p;
+  size_t rows_bytes, bytes;
+};
+PrefillPlan prefill_plan(int T, int B, int Hq, int Hkv, int d) {
+  const int G = Hq / Hkv;
+  const long long n = static_cast<long long>(T) * G;
+  PrefillPlan x = {false, true, {0, 0}, 0, 0};
+  if (n <= 8ll * B) {
+    x.rows = true;
+    x.tiles = n > 128;
+    x.p = {plx::paged_rows_group(T, B, G), x.tiles ? 16 : 0};
+  } else if (B >= kMixedSeqs && G <= 8 && n <= static_cast<long long>(kMixedRows) * B) {
+    x.rows = true;
+    x.p.group = x.p.most = G <= 4 ? 4 : 8;
+  }
+  if (x.tiles && (G > x.p.most || static_cast<long long>(B) * Hq > (1LL << 24))) x.rows = false;
+  if (x.rows) x.rows_bytes = (plx::paged_rows_workspace_bytes(x.p, T, B, G, Hkv, d, true) + 255) / 256 * 256;
+  x.bytes = x.rows_bytes + (x.tiles ? plx::paged_prefill_workspace_bytes() : 0);
+  return x;
+}
 
 plx_status check_heads(const char *fn, int Hq, int Hkv) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
@@ -550,7 +587,8 @@ plx_status plx_kv_read(const void *kpages, const void *vpages, const unsigned ch
 
 size_t plx_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
-  return plx::paged_rows_workspace_bytes(B, B, Hq / Hkv, Hkv, d, false);
+  const int G = Hq / Hkv;
+  return plx::paged_rows_workspace_bytes({plx::paged_rows_group(B, B, G), 0}, B, B, G, Hkv, d, false);
 }
 
 plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages,
@@ -580,15 +618,15 @@ plx_status plx_decode_fwd_paged(const void *q, const void *r, const void *kpages
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_workspace(fn, workspace, plx_decode_paged_workspace_bytes(B, Hq, Hkv, d), st,
                         [&](void *ws) {
-                          return plx::launch_paged_rows(c, q, r, row, d, seqlens, nullptr, out, row,
-                                                        d, nullptr, B, Hq, ws, st);
+                          return plx::launch_paged_rows({plx::paged_rows_group(B, B, Hq / Hkv), 0}, c, q,
+                                                        r, row, d, seqlens, nullptr, out, row, d,
+                                                        nullptr, B, Hq, ws, st);
                         });
 }
 
 size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d) {
   if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
-  return few_rows(T, B, Hq / Hkv) ? plx::paged_rows_workspace_bytes(T, B, Hq / Hkv, Hkv, d, true)
-                                  : plx::paged_prefill_workspace_bytes();
+  return prefill_plan(T, B, Hq, Hkv, d).bytes;
 }
 
 plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_token_stride,
@@ -624,17 +662,18 @@ plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_toke
     return fail(PLX_ERR_UNSUPPORTED, "%s: problem too large for one launch", fn);
   c.err = plx::device_error_word();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return with_workspace(fn, workspace, plx_prefill_paged_workspace_bytes(T, B, Hq, Hkv, d), st,
-                        [&](void *ws) {
-                          return few_rows(T, B, Hq / Hkv)
-                                     ? plx::launch_paged_rows(c, q, r, qr_token_stride, qr_head_stride,
-                                                              seqlens, cu_q, out, out_token_stride,
-                                                              out_head_stride, lse, T, Hq, ws, st)
-                                     : plx::launch_paged_prefill(c, q, r, qr_token_stride,
-                                                                 qr_head_stride, seqlens, cu_q, out,
-                                                                 out_token_stride, out_head_stride,
-                                                                 lse, T, Hq, ws, st);
-                        });
+  const PrefillPlan x = prefill_plan(T, B, Hq, Hkv, d);
+  return with_workspace(fn, workspace, x.bytes, st, [&](void *ws) {
+    cudaError_t e = cudaSuccess;
+    if (x.rows)
+      e = plx::launch_paged_rows(x.p, c, q, r, qr_token_stride, qr_head_stride, seqlens, cu_q, out,
+                                 out_token_stride, out_head_stride, lse, T, Hq, ws, st);
+    if (e == cudaSuccess && x.tiles)
+      e = plx::launch_paged_prefill(c, q, r, qr_token_stride, qr_head_stride, seqlens, cu_q, out,
+                                    out_token_stride, out_head_stride, lse, T, Hq,
+                                    x.rows ? x.p.most : 0, static_cast<char *>(ws) + x.rows_bytes, st);
+    return e;
+  });
 }
 
 plx_status plx_check_device_error(void *stream) {

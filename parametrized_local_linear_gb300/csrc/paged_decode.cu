@@ -84,6 +84,7 @@ struct RowsArgs {
   float *recs;
   int2 *meta;
   int Hq, G, T, nshare, gs;  // gs: records of a slot (rows of the largest group)
+  int most;                  // as in RowsPlan
   float scale_log2;
 };
 
@@ -112,13 +113,15 @@ __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
   } else {
     s.n = end - first;
   }
-  s.ng = (s.n * a.G + GS - 1) / GS;
+  const long long rows = static_cast<long long>(s.n) * a.G;
+  s.ng = a.most > 0 && rows > a.most ? 0 : static_cast<int>((rows + GS - 1) / GS);
   return s;
 }
-// Row groups in front of sequence b, counted so that no scan is needed:
+// Places for the row groups in front of sequence b, counted so that no scan is
+// needed: most / gs for each, or, without a limit, by
 // ceil(n G / gs) <= floor((c + n) G / gs) - floor(c G / gs) + 1.
-__device__ __forceinline__ long long groups_before(int first, int b, int G, int gs) {
-  return static_cast<long long>(first) * G / gs + b;
+__device__ __forceinline__ long long groups_before(int first, int b, int G, int gs, int most) {
+  return most > 0 ? static_cast<long long>(b) * (most / gs) : static_cast<long long>(first) * G / gs + b;
 }
 
 // One item: tiles [t0, t1) of row group grp of kv head kvh of sequence b.
@@ -152,7 +155,7 @@ struct Walk {
     it.grp = vh - it.kvh * s.ng;
     it.t0 = static_cast<int>(off - static_cast<long long>(vh) * s.tiles);
     it.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), it.t0 + (e - pos)));
-    it.vrow = groups_before(s.first, b, a.G, GS) * a.c.Hkv + vh;
+    it.vrow = groups_before(s.first, b, a.G, GS, a.most) * a.c.Hkv + vh;
     pos += it.t1 - it.t0;
     return true;
   }
@@ -727,7 +730,8 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   }
 }
 
-// One block of D threads per (packed row, query head): merge the row's records
+// One block of D threads per (packed row, query head), or, if that is fewer, per
+// (sequence, token below the limit of rows, query head): merge the row's records
 // and form o = O1 - O2 + O1 s (combining final outputs would be wrong: O1 s
 // is bilinear in the partial sums).
 struct CombineArgs {
@@ -738,7 +742,8 @@ struct CombineArgs {
   __nv_bfloat16 *out;
   float *lse;
   long long ots, ohs, nslots;
-  int Hq, G, T, gs, group;  // records of a slot, rows of a group
+  int Hq, G, T, gs, group, most;  // records of a slot, rows of a group
+  int tokens;                     // blocks of a sequence and query head; 0: blocks go by packed rows
 };
 
 constexpr int CCH = 512;
@@ -747,12 +752,25 @@ constexpr int kFewRecs = 32;
 __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
   __shared__ float wsig[2][CCH];
   __shared__ float slot[D / 32];
-  const int t = blockIdx.x / a.Hq, h = blockIdx.x - t * a.Hq, dim = threadIdx.x;
-  const int b = row_sequence(a.cu, a.c.B, t);
-  // Wait for the split kernel to complete before any record is read (and
-  // before this block leaves, so that what follows comes after both).
+  const int at = blockIdx.x / a.Hq, h = blockIdx.x - at * a.Hq, dim = threadIdx.x;
+  int t = at, b;
+  if (a.tokens > 0) {
+    b = at / a.tokens;
+    const int s0 = a.cu[b], s1 = a.cu[b + 1], i = at - b * a.tokens;
+    t = s0;
+    if (s0 < 0 || s1 > a.T || s1 < s0 || s1 - s0 > a.tokens || i >= s1 - s0) b = -1;
+    else t += i;
+  } else {
+    b = row_sequence(a.cu, a.c.B, t);
+    if (a.most > 0 && b >= 0 && (a.cu[b] < 0 || (static_cast<long long>(a.cu[b + 1]) - a.cu[b]) * a.G > a.most)) b = -1;
+  }
+  // The tile kernel of the same call, if one follows, may start (it does not
+  // read what this one writes). Then wait for the split kernel to complete before
+  // any record is read (and before this block leaves, so that what follows comes
+  // after both).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (b < 0) return;  // behind the last sequence
+  if (b < 0) return;  // behind the last sequence, or not of these rows
   const int first = a.cu ? a.cu[b] : b, end = a.cu ? a.cu[b + 1] : b + 1;
   const int len = cache_len(a.c, a.seqlens, b), n = end - first;
   const bool bad = a.cu != nullptr && (first < 0 || end > a.T);
@@ -760,8 +778,8 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
   if (!bad && len - n + (t - first) >= 0 && len > 0) {
     const int kvh = h / a.G, ng = (n * a.G + a.group - 1) / a.group;
     const int row = (t - first) * a.G + (h - kvh * a.G);
-    const int2 mt = a.meta[groups_before(first, b, a.G, a.group) * a.c.Hkv + static_cast<long long>(kvh) * ng +
-                           row / a.group];
+    const int2 mt = a.meta[groups_before(first, b, a.G, a.group, a.most) * a.c.Hkv +
+                           static_cast<long long>(kvh) * ng + row / a.group];
     // An entry outside the records (left by an earlier call when this one
     // did no work) is not followed.
     const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
@@ -837,7 +855,7 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
     }
   }
   a.out[t * a.ots + h * a.ohs + dim] = __float2bfloat16_rn(o);
-  if (a.lse != nullptr && dim == 0) a.lse[blockIdx.x] = lse2 * 0.6931471805599453f;
+  if (a.lse != nullptr && dim == 0) a.lse[static_cast<long long>(t) * a.Hq + h] = lse2 * 0.6931471805599453f;
 }
 
 // Map of one page tensor. bf16: {64, page, pages Hkv, 2 halves}, boxes of 16
@@ -888,9 +906,9 @@ int paged_rows_shares() { return kCtasPerSm * sm_count(); }
 // 269 us (e4m3), 625 and 337 us (bf16): a second group reads the keys again.
 int paged_rows_group(int T, int B, int G) { return static_cast<long long>(T) * G > RW * static_cast<long long>(B) ? 2 * RW : RW; }
 
-cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
-                              long long qhs, const int *seqlens, const int *cu_q, void *out,
-                              long long ots, long long ohs, float *lse, int T, int Hq,
+cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void *q, const void *r,
+                              long long qts, long long qhs, const int *seqlens, const int *cu_q,
+                              void *out, long long ots, long long ohs, float *lse, int T, int Hq,
                               void *workspace, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return cudaErrorInvalidValue;
@@ -909,11 +927,12 @@ cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r,
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.T = T;
-  const int group = paged_rows_group(T, c.B, a.G);
+  const int group = p.group;
+  a.most = p.most;
   a.gs = paged_rows_slot(group, a.G, cu_q != nullptr);
   a.nshare = paged_rows_shares();
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  const long long vrows = paged_rows_vrows(T, c.B, a.G, c.Hkv, group);
+  const long long vrows = paged_rows_vrows(p, T, c.B, a.G, c.Hkv);
   a.meta = static_cast<int2 *>(workspace);
   a.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + paged_rows_meta_bytes(vrows));
   cudaError_t e;
@@ -936,8 +955,10 @@ cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r,
   k.T = T;
   k.gs = a.gs;
   k.group = group;
+  k.most = p.most;
+  k.tokens = p.most > 0 && static_cast<long long>(c.B) * (p.most / a.G) < T ? p.most / a.G : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(T) * Hq);
+  cfg.gridDim = dim3(static_cast<unsigned>(k.tokens > 0 ? c.B * k.tokens : T) * Hq);
   cfg.blockDim = dim3(D);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

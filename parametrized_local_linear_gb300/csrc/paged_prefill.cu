@@ -90,6 +90,7 @@ struct Args {
   int *table;    // [grid][4] the item that CTA c starts and does not finish
   long long ots, ohs;
   int T, Hq, G, TQ;
+  int few;  // sequences of at most so many new tokens are not this kernel's
   float scale_log2;
 };
 // A CTA's share is at least this many key tiles.
@@ -114,7 +115,7 @@ __device__ __noinline__ Seq seq_of(const Args &a, int b) {
   } else {
     s.n = end - first;
   }
-  s.nq = (s.n + a.TQ - 1) / a.TQ;
+  s.nq = s.n <= a.few ? 0 : (s.n + a.TQ - 1) / a.TQ;
   return s;
 }
 // Key tiles of row tile t: up to the last key that its last token sees, at
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   if (pl.items == 0 && pl.s >= pl.e) {  // no share
     if (threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
     if (warp == O1_WARP) tmem_dealloc(tbase, 512);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   if (lane == 0) {
@@ -1043,6 +1045,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+  // After the call's other kernels, if it has any: they ran beside this one (they
+  // share no result), and what follows waits for this grid only.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Merge of the items that several CTAs share: block (c, i) forms dims
@@ -1142,8 +1147,17 @@ cudaError_t launch_tiles(const Args &a, int grid, const CUtensorMap (&m)[4], cud
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  paged_prefill_kernel<FP8><<<grid, Cfg<FP8>::THREADS, Cfg<FP8>::SMEM, stream>>>(m[0], m[1], m[2], m[3], a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Cfg<FP8>::THREADS);
+  cfg.dynamicSmemBytes = Cfg<FP8>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.few > 0 ? 1 : 0;  // behind the call's other kernels
+  return cudaLaunchKernelEx(&cfg, paged_prefill_kernel<FP8>, m[0], m[1], m[2], m[3], a);
 }
 
 constexpr size_t table_bytes(int grid) { return (size_t(grid) * 16 + 255) / 256 * 256; }
@@ -1157,7 +1171,7 @@ size_t paged_prefill_workspace_bytes() {
 
 cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void *r, long long qts,
                                  long long qhs, const int *seqlens, const int *cu_q, void *out,
-                                 long long ots, long long ohs, float *lse, int T, int Hq,
+                                 long long ots, long long ohs, float *lse, int T, int Hq, int few,
                                  void *workspace, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return cudaErrorInvalidValue;
@@ -1174,6 +1188,7 @@ cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void 
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.TQ = BM / a.G;
+  a.few = few / a.G;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const int grid = sm_count();
   a.table = static_cast<int *>(workspace);

@@ -104,34 +104,42 @@ cudaError_t launch_kv_append(const PagedCache &c, const void *k, const void *v,
 cudaError_t launch_kv_read(const PagedCache &c, const int *cu_k, void *k, void *v, int T,
                            cudaStream_t stream);
 // Few new tokens a sequence (decode: one): split over equal shares of the key
-// stream and combined. Workspace: {first record slot, slots} per virtual row
-// (sequence, kv head, group of 4 or 8 query rows), padded to 256 bytes, then
-// (shares + virtual rows) slots of `slot` records of 2 d + 2 floats. CTA c
-// writes its part of virtual row v to slot c + v.
-int paged_rows_shares();  // CTAs of the split kernel
+// stream and combined. Query rows (token, query head) of a sequence and kv head
+// are taken in groups of 4 or 8. With most > 0 only sequences of at most `most`
+// rows a kv head are; the others are left as they were.
+struct RowsPlan {
+  int group, most;
+};
 int paged_rows_group(int T, int B, int G);
+int paged_rows_shares();  // CTAs of the split kernel
+// Workspace: {first record slot, slots} per virtual row (sequence, kv head,
+// group), padded to 256 bytes, then (shares + virtual rows) slots of `slot`
+// records of 2 d + 2 floats. CTA c writes its part of virtual row v to slot
+// c + v.
 inline int paged_rows_slot(int group, int G, bool many) { return many || G > group ? group : G; }
-inline long long paged_rows_vrows(int T, int B, int G, int Hkv, int group) {
-  return (static_cast<long long>(T) * G / group + B) * Hkv;
+inline long long paged_rows_vrows(const RowsPlan &p, int T, int B, int G, int Hkv) {
+  const long long groups = p.most > 0 ? static_cast<long long>(B) * (p.most / p.group)
+                                      : static_cast<long long>(T) * G / p.group + B;
+  return groups * Hkv;
 }
 inline size_t paged_rows_meta_bytes(long long vrows) { return (size_t(vrows) * 8 + 255) / 256 * 256; }
-inline size_t paged_rows_workspace_bytes(int T, int B, int G, int Hkv, int d, bool many) {
-  const int group = paged_rows_group(T, B, G);
-  const long long vrows = paged_rows_vrows(T, B, G, Hkv, group);
-  return paged_rows_meta_bytes(vrows) + size_t(paged_rows_shares() + vrows) * paged_rows_slot(group, G, many) *
+inline size_t paged_rows_workspace_bytes(const RowsPlan &p, int T, int B, int G, int Hkv, int d, bool many) {
+  const long long vrows = paged_rows_vrows(p, T, B, G, Hkv);
+  return paged_rows_meta_bytes(vrows) + size_t(paged_rows_shares() + vrows) * paged_rows_slot(p.group, G, many) *
                                             (2 * size_t(d) + 2) * sizeof(float);
 }
 // lse ([T, Hq] fp32) may be null; cu_q null: one new token a sequence.
-cudaError_t launch_paged_rows(const PagedCache &c, const void *q, const void *r, long long qts,
-                              long long qhs, const int *seqlens, const int *cu_q, void *out,
-                              long long ots, long long ohs, float *lse, int T, int Hq,
+cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void *q, const void *r,
+                              long long qts, long long qhs, const int *seqlens, const int *cu_q,
+                              void *out, long long ots, long long ohs, float *lse, int T, int Hq,
                               void *workspace, cudaStream_t stream);
 
-// Chunks of any length (tcgen05). lse ([T, Hq] fp32) may be null.
+// Chunks of any length (tcgen05). lse ([T, Hq] fp32) may be null. Sequences of at
+// most `few` rows a kv head are left as they were.
 size_t paged_prefill_workspace_bytes();
 cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void *r, long long qts,
                                  long long qhs, const int *seqlens, const int *cu_q, void *out,
-                                 long long ots, long long ohs, float *lse, int T, int Hq,
+                                 long long ots, long long ohs, float *lse, int T, int Hq, int few,
                                  void *workspace, cudaStream_t stream);
 
 cudaError_t launch_timeout_probe(long long limit_cycles, unsigned *err, cudaStream_t stream);

@@ -836,3 +836,58 @@ def test_calls_from_two_host_threads():
     assert not errors
     for i in range(2):
         assert len(got[i]) == 20 and all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("counts,Hq,Hkv,page,behind", [
+    ([1, 200, 2, 0, 3, 17, 1], 4, 2, 16, 0),          # decodes with chunks among them: both kernels
+    ([2, 1, 90, 5, 4, 1], 2, 2, 64, 3),               # one query head a kv head: up to four tokens
+    ([1, 150, 1, 2, 1], 16, 2, 32, 1),                # eight: one token
+    ([1, 1, 40], 12, 2, 128, 0),                      # six
+    ([1] * 17 + [60, 0, 2], 4, 2, 16, 0),             # few rows on average, one long chunk
+    ([8, 9, 8, 7] + [3] * 20, 4, 2, 16, 2),           # two groups of eight rows, and just above
+    ([1] * 15 + [30] + [0] * 24, 18, 2, 64, 0),       # nine query heads a kv head
+    ([0] * 30 + [100], 4, 2, 16, 0),                  # a long chunk alone among idle sequences
+    ([1, 700, 1], 4, 2, 32, 0),                       # mostly chunk: the tile kernel alone
+])
+def test_mixed_chunk_lengths(fp8, counts, Hq, Hkv, page, behind):
+    """Short and long chunks of one call, some with padding rows in front."""
+    dev = device()
+    lens = [(37 * b) % 300 + (c if b % 4 else max(c - 2, 0)) for b, c in enumerate(counts)]
+    pool = ref.filled_pool(lens, Hkv, page, fp8, 11)
+    T = sum(counts) + behind
+    q, r = ref.normal_rows(T, Hq, 1), ref.normal_rows(T, Hq, 2, 0.05)
+    o, lse_want, bound = ref.reference(pool, q, r, counts, behind)
+    out = torch.full((T, Hq, 128), 3.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((T, Hq), 3.0, device=dev)
+    ws = torch.full((plx_prefill_paged_workspace_bytes(T, len(counts), Hq, Hkv, 128),), 255,
+                    dtype=torch.uint8, device=dev)
+    plx_prefill_fwd_paged(q.to(dev), r.to(dev), seqlens=pool.seqlens.to(dev), cu_q=ends(counts).to(dev),
+                          out=out, lse=lse, workspace=ws, **pool.to(dev))
+    plx_check_device_error()
+    n = sum(counts)
+    assert torch.all(out[n:] == 3.0) and torch.all(lse[n:] == 3.0)
+    ref.assert_within(out[:n], o[:n], bound[:n])
+    got, want = lse[:n].double().cpu().numpy(), lse_want[:n]
+    empty = np.isneginf(want)
+    assert np.array_equal(np.isneginf(got), empty)
+    assert np.all(np.abs(got[~empty] - want[~empty]) <= LSE_ABS)
+
+
+def test_bad_row_offsets_among_mixed_chunks():
+    """cu_q whose entries pass T or fall back, in a call that both kernels work on."""
+    dev = device()
+    pool = ref.filled_pool([100, 60, 40, 30], 2, 16, False, 3)
+    kw = pool.to(dev)
+    rows = 100
+    guard = torch.full((rows + 200, 4, 128), 3.0, dtype=torch.bfloat16, device=dev)
+    q = ref.normal_rows(rows, 4, 1).to(dev)
+    top = 2**31 - 1
+    for cu in ([0, top, 1, 2, 3], [0, 1, top, 2, rows], [0, -2**31, 1, 2, 3], [top - 1, top, 2, 3, rows],
+               [0, 1, rows + 2, 3, 4], [-5, 1, 2, 3, rows]):
+        bad = torch.tensor(cu, dtype=I32, device=dev)
+        plx_prefill_fwd_paged(q, q, seqlens=pool.seqlens.to(dev), cu_q=bad, out=guard[100:100 + rows], **kw)
+        with pytest.raises(PlxError) as e:
+            plx_check_device_error()
+        assert e.value.status == binding.PLX_ERR_INVALID_ARG
+        assert torch.all(guard[:100] == 3.0) and torch.all(guard[100 + rows:] == 3.0)
