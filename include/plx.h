@@ -265,7 +265,8 @@ int plx_decode_default_nsplit(int B, int Hkv);
  * above. Arguments shared by them:
  *   kpages, vpages : [num_pages, Hkv, page_size, d], bf16, or e4m3 codes (one
  *                    byte each) if kscale and vscale are given. page_size is
- *                    16, 32, 64, 128 or 256; d must be 128.
+ *                    16, 32, 64, 128 or 256; d must be 128; there are fewer than
+ *                    2^31 rows, num_pages * Hkv * page_size.
  *   kscale, vscale : uint8 [num_pages, Hkv, page_size], both or neither. A row
  *                    of codes stands for code * 2^(E - 127), E its byte in
  *                    1 .. 254 (E = 0 only for rows of zeros). Attention over e4m3

@@ -449,10 +449,12 @@ plx_status paged_cache(const char *fn, plx::PagedCache *c, const void *kpages, c
     return fail(PLX_ERR_INVALID_ARG, "%s: page pointers must be 16-byte aligned", fn);
   if (!aligned16(kscale) || !aligned16(vscale))
     return fail(PLX_ERR_INVALID_ARG, "%s: kscale and vscale must be 16-byte aligned", fn);
-  if (static_cast<long long>(num_pages) * Hkv > 0x7fffffffLL ||
+  if (static_cast<long long>(num_pages) * Hkv > 0x7fffffffLL / page_size ||
       static_cast<long long>(max_pages) * page_size > 1LL << 30)
     return fail(PLX_ERR_UNSUPPORTED,
-                "%s: num_pages * Hkv must be < 2^31 and max_pages * page_size at most 2^30", fn);
+                "%s: num_pages * Hkv * page_size must be < 2^31 (256 GB of codes) and "
+                "max_pages * page_size at most 2^30",
+                fn);
   c->k = kpages;
   c->v = vpages;
   c->kscale = kscale;

@@ -12,9 +12,10 @@
 // before the first result is used. Consecutive rows of a head are contiguous in
 // their page, and the Hkv warps of a row group together read or write whole
 // contiguous rows on the other side.
-// The bound is memory. GB300: append of 34660 tokens x 8 heads to e4m3 40 us
-// (5.3 TB/s of the 6.8 that a copy reaches; the byte of a scale costs a 32-byte
-// sector), of 16425 tokens to bf16 21.9 us (6.1 TB/s); read back of 195089 e4m3 tokens 180 us (6.7 TB/s); one token a sequence, 64 of them: 2.9
+// The bound is memory, for e4m3 with the ALU close behind (70% busy: maxima,
+// unpacking, conversion). GB300: append of 34660 tokens x 8 heads to e4m3 35 us
+// (6.1 TB/s of the 6.8 that a copy reaches; 40 with a maximum over 16 lanes and an
+// exponent for each row by itself), of 16425 tokens to bf16 21.9 us (6.1 TB/s); read back of 195089 e4m3 tokens 180 us (6.7 TB/s); one token a sequence, 64 of them: 2.9
 // us, the launch.
 #include <string.h>
 
@@ -37,7 +38,7 @@ struct AppendArgs {
 
 // Rows a warp handles: one when there are too few warps to fill the GPU twice
 // with more (a decode step's rows: latency), else eight (bytes in flight).
-// GB300, one and eight: append of 34660 tokens x 8 heads to e4m3 79 and 40 us,
+// GB300, one and eight: append of 34660 tokens x 8 heads to e4m3 79 and 35 us,
 // of 64 tokens 3.0 and 4.3; read back of 195089 e4m3 tokens 335 and 180 us.
 int rows_per_warp(long long rows) { return rows < 16ll * WARPS * sm_count() ? 1 : 8; }
 
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs 
   const int h = static_cast<int>(w % a.c.Hkv);
   const long long t0 = w / a.c.Hkv * N;
   if (t0 >= a.T) return;
-  long long my_row = -1;
+  int my_row = -1;
   if (lane < N && t0 + lane < a.T) {
     const int t = static_cast<int>(t0) + lane;
     const int b = row_sequence(a.cu_q, a.c.B, t);
@@ -58,42 +59,70 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs 
       if (first < 0 || end > a.T) {
         if (a.c.err) atomicOr(a.c.err, kErrBadInput);
       } else if (pos >= 0) {  // else padding
-        my_row = page_row(a.c, b, h, pos);
+        my_row = static_cast<int>(page_row(a.c, b, h, pos));
       }
     }
   }
   const __nv_bfloat16 *src = (half ? a.v : a.k) + t0 * a.token_stride + h * a.head_stride + sub * 8;
   uint4 x[N];
-  long long row[N];
+  int row[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     row[n] = __shfl_sync(0xffffffffu, my_row, n);
     x[n] = row[n] >= 0 ? *reinterpret_cast<const uint4 *>(src + n * a.token_stride) : make_uint4(0u, 0u, 0u, 0u);
   }
   uint8_t *pages = half ? a.vpages : a.kpages;
+  if constexpr (!FP8) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    if (!FP8) {
-      if (row[n] >= 0) *reinterpret_cast<uint4 *>(pages + row[n] * (2 * D) + sub * 16) = x[n];
-      continue;
+    for (int n = 0; n < N; ++n)
+      if (row[n] >= 0) *reinterpret_cast<uint4 *>(pages + row[n] * (2ll * D) + sub * 16) = x[n];
+  } else {
+    // Magnitude bits of a row's largest element, of this lane's eight.
+    uint32_t m[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t m2 = __vmaxu2(__vmaxu2(x[n].x & 0x7fff7fffu, x[n].y & 0x7fff7fffu),
+                                   __vmaxu2(x[n].z & 0x7fff7fffu, x[n].w & 0x7fff7fffu));
+      m[n] = max(m2 & 0xffffu, m2 >> 16);
     }
-    const uint32_t wd[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-    uint32_t m2 = 0;
+    // Over the 16 lanes of a row. Eight rows: in each step a lane keeps half of its
+    // rows and gives the other half to the lane that keeps those, so it ends with
+    // row sub / 2's and works out one exponent instead of eight.
+    if constexpr (N == 8) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, wd[e] & 0x7fff7fffu);
-    uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+      for (int w = 4; w > 0; w >>= 1) {
+        const bool high = (sub & (2 * w)) != 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m >= 0x7f80u && sub == 0 && a.c.err) atomicOr(a.c.err, kErrBadInput);  // inf or NaN
-    const int E = max(1, static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0));
-    const float f = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);  // 2^(127 - E)
-    uint32_t c[4];
+        for (int n = 0; n < w; ++n) {
+          const uint32_t give = high ? m[n] : m[n + w], keep = high ? m[n + w] : m[n];
+          m[n] = max(keep, __shfl_xor_sync(0xffffffffu, give, 2 * w));
+        }
+      }
+      m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = float2_to_e4m3x2(bf16lo(wd[e]) * f, bf16hi(wd[e]) * f);
-    if (row[n] < 0) continue;
-    *reinterpret_cast<uint2 *>(pages + row[n] * D + sub * 8) =
-        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-    if (sub == 0) (half ? a.vscale : a.kscale)[row[n]] = static_cast<uint8_t>(E);
+      for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    }
+    constexpr int LPR = N == 8 ? 2 : 16;  // lanes that hold a row's maximum
+    if (m[0] >= 0x7f80u && sub % LPR == 0 && a.c.err) atomicOr(a.c.err, kErrBadInput);  // inf or NaN
+    const int mine = max(1, static_cast<int>(m[0] >> 7) - 8 + ((m[0] & 0x7fu) > 0x60u ? 1 : 0));
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int E = __shfl_sync(0xffffffffu, mine, (lane & 16) + n * LPR);
+      if (row[n] < 0) continue;
+      const float f = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);  // 2^(127 - E)
+      const uint64_t f2x = f2(f, f);
+      const uint32_t wd[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      uint32_t c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t y = fmul2(f2(bf16lo(wd[e]), bf16hi(wd[e])), f2x);
+        c[e] = float2_to_e4m3x2(f2lo(y), f2hi(y));
+      }
+      *reinterpret_cast<uint2 *>(pages + row[n] * static_cast<long long>(D) + sub * 8) =
+          make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+      if (sub == 0) (half ? a.vscale : a.kscale)[row[n]] = static_cast<uint8_t>(E);
+    }
   }
 }
 
@@ -111,7 +140,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
   const int h = static_cast<int>(w % a.c.Hkv);
   const long long t0 = w / a.c.Hkv * N;
   if (t0 >= a.T) return;
-  long long my_row = -1;
+  int my_row = -1;
   if (lane < N && t0 + lane < a.T) {
     const int t = static_cast<int>(t0) + lane;
     const int b = row_sequence(a.cu_k, a.c.B, t);
@@ -119,7 +148,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
       const int first = a.cu_k[b], pos = t - first;  // first <= t
       const bool in = first >= 0 && a.cu_k[b + 1] <= a.T &&
                       pos < (static_cast<long long>(a.c.max_pages) << a.c.page_shift);
-      if (in) my_row = page_row(a.c, b, h, pos);
+      if (in) my_row = static_cast<int>(page_row(a.c, b, h, pos));
       else if (a.c.err) atomicOr(a.c.err, kErrBadInput);
     }
   }
@@ -127,7 +156,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
   const uint8_t *scales = half ? a.c.vscale : a.c.kscale;
   uint4 x[N];
   uint32_t E[N];
-  long long row[N];
+  int row[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     row[n] = __shfl_sync(0xffffffffu, my_row, n);
@@ -135,12 +164,12 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
     E[n] = 0u;
     if (row[n] < 0) continue;
     if (FP8) {
-      const uint2 c = *reinterpret_cast<const uint2 *>(pages + row[n] * D + sub * 8);
+      const uint2 c = *reinterpret_cast<const uint2 *>(pages + row[n] * static_cast<long long>(D) + sub * 8);
       x[n].x = c.x;
       x[n].y = c.y;
       E[n] = scales[row[n]];
     } else {
-      x[n] = *reinterpret_cast<const uint4 *>(pages + row[n] * (2 * D) + sub * 16);
+      x[n] = *reinterpret_cast<const uint4 *>(pages + row[n] * (2ll * D) + sub * 16);
     }
   }
   __nv_bfloat16 *out = (half ? a.v : a.k) + (t0 * a.c.Hkv + h) * D + sub * 8;

@@ -249,3 +249,10 @@ def test_a_table_past_2_to_30_positions_is_rejected(lib, call):
     """Positions plus a tile stay inside 32 bits."""
     assert CALLS[call](lib, width=(1 << 26) + 1) == UNS  # 2^30 + 16 positions
     assert b"2^30" in lib.plx_last_error_message()
+
+
+@pytest.mark.parametrize("call", sorted(CALLS))
+def test_2_to_31_rows_of_pages_are_rejected(lib, call):
+    """Rows of a page tensor are counted in 32 bits."""
+    assert CALLS[call](lib, n=1 << 26) == UNS  # 2^26 pages x 2 heads x 16 slots
+    assert b"2^31" in lib.plx_last_error_message()
