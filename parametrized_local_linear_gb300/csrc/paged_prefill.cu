@@ -814,11 +814,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(bar, RAW);
-#pragma unroll 1
-            for (int i = 0; i * box < BN; ++i) {
-              const int zi = __shfl_sync(0xffffffffu, z, i);
-              if (lane == 0) tma_load_3d(dst + i * box * 128, kv ? &tm_v : &tm_k, 0, slot, zi, bar);
-            }
+            __syncwarp();
+            if (lane * box < BN) tma_load_3d(dst + lane * box * 128, kv ? &tm_v : &tm_k, 0, slot, z, bar);
             kv ? ++issued[1] : ++issued[0];
           }
           if (!ok) break;
@@ -913,13 +910,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         if (!ok) break;
         const uint32_t bar = smem_u32(&full[st]), dst = ring + st * TILE_KV;
         if (lane == 0) mbar_arrive_expect_tx(bar, TILE_KV);
-#pragma unroll 1
-        for (int i = 0; i * box < BN; ++i) {
-          const int zi = __shfl_sync(0xffffffffu, z, i);
-          if (lane == 0) {
-            tma_load_4d(dst + i * box * 128, map, 0, slot, zi, 0, bar);
-            tma_load_4d(dst + HALF_KV + i * box * 128, map, 0, slot, zi, 1, bar);
-          }
+        __syncwarp();
+        if (lane * box < BN) {
+          tma_load_4d(dst + lane * box * 128, map, 0, slot, z, 0, bar);
+          tma_load_4d(dst + HALF_KV + lane * box * 128, map, 0, slot, z, 1, bar);
         }
       }
     }
