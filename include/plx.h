@@ -286,8 +286,9 @@ int plx_decode_default_nsplit(int B, int Hkv);
  * New token i (0 .. n_b - 1) of sequence b has position seqlens[b] - n_b + i; a
  * negative one marks padding (a row that has no place in the cache and sees no
  * key). Whatever the pages hold behind seqlens[b], NaN included, does not reach
- * any result. Values in front of it must be finite: the products of a tile of
- * keys give a value that a token does not see yet the weight zero. Packed rows have strides in elements, for the token and the head;
+ * any result. Keys and values in front of it must be finite: in a tile of keys
+ * the ones that a token does not see yet have the weight zero in its sums, not no
+ * part in them. Packed rows have strides in elements, for the token and the head;
  * a row's d values are contiguous. Strides are multiples of 8 and at least d,
  * pointers 16-byte aligned (4 bytes for int32 and fp32). A page number outside
  * 0 .. num_pages - 1, a length beyond max_pages * page_size or a cu_q that
