@@ -891,3 +891,34 @@ def test_bad_row_offsets_among_mixed_chunks():
             plx_check_device_error()
         assert e.value.status == binding.PLX_ERR_INVALID_ARG
         assert torch.all(guard[:100] == 3.0) and torch.all(guard[100 + rows:] == 3.0)
+
+
+@pytest.mark.parametrize("counts", [[3, 60, 1, 40, 2], [1] * 5, [2, 70, 1, 1, 30, 1, 2, 1, 9]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_sequence_that_is_not_finite_leaves_the_others_alone(counts, bad):
+    """One sequence's keys, values and queries hold NaN or infinities; every
+    other sequence's results are the same bits as without them."""
+    dev = device()
+    lens = [80 + 37 * b for b in range(len(counts))]
+    pool = ref.filled_pool(lens, 2, 16, False, 3)
+    T, sick = sum(counts), 1
+    q, r = ref.normal_rows(T, 4, 1).to(dev), ref.normal_rows(T, 4, 2, 0.05).to(dev)
+    kw, sl, cu = pool.to(dev), pool.seqlens.to(dev), ends(counts).to(dev)
+    first = [row.contiguous() for row in (q[cu[1:].long() - 1], r[cu[1:].long() - 1])]
+
+    def run():
+        return [plx_prefill_fwd_paged(q, r, seqlens=sl, cu_q=cu, **kw)[0],
+                plx_decode_fwd_paged(*first, seqlens=sl, **kw)]
+
+    clean = run()
+    for pages in (kw["kpages"], kw["vpages"]):
+        for page in pool.table[sick, :(lens[sick] + 15) // 16].tolist():
+            pages[page, :, ::3, ::5] = bad
+    q[ends(counts)[sick]:ends(counts)[sick + 1], :, ::7] = bad
+    dirty = run()
+    plx_check_device_error()
+    rows = torch.ones(T, dtype=torch.bool)
+    rows[ends(counts)[sick]:ends(counts)[sick + 1]] = False
+    assert same_bits(clean[0][rows.to(dev)], dirty[0][rows.to(dev)])
+    others = [b for b in range(len(counts)) if b != sick]
+    assert same_bits(clean[1][others], dirty[1][others])
