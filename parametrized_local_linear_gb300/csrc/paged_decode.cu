@@ -175,6 +175,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// The sector of an address into L2.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // Byte offset of 16-byte chunk c of row `row`: bf16 tiles are two halves of
 // 16 rows x 128 bytes, e4m3 tiles 32 rows x 128 bytes, both 128-byte swizzled.
 __device__ __forceinline__ uint32_t swz(int row, int c) {
@@ -432,6 +437,16 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
             if constexpr (FP8) {
               tma_load_3d(dst, &tm_k, 0, slot, z, bar);
               tma_load_3d(dst + TILE, &tm_v, 0, slot, z, bar);
+              // The consumers load the scale bytes a tile ahead, this a ring
+              // ahead. With two warps a tile, who both load them, 256 us against
+              // 275 for 64 x 8192 keys and 8 query heads a kv head (two tiles
+              // ahead in the consumers: 280); no change with one, and slower
+              // where a tile is two boxes and sequences are short.
+              if (R == 2 && per == KT && z != beyond) {
+                const long long row = (static_cast<long long>(z) << shift) + slot;
+                prefetch_l2(a.c.kscale + row);
+                prefetch_l2(a.c.vscale + row);
+              }
             } else {
               tma_load_4d(dst, &tm_k, 0, slot, z, 0, bar);
               tma_load_4d(dst + TILE, &tm_v, 0, slot, z, 0, bar);
@@ -943,7 +958,7 @@ int paged_rows_shares() { return kCtasPerSm * sm_count(); }
 // head on average. GB300, GPU time of four and of eight: one new token x 2 heads
 // 173 and 258 us (64 x 8192 e4m3 keys, a pair of warps half idle); 4 tokens x
 // 2 heads 51 and 38 us (16 sequences of 500 to 6000 e4m3 keys); 8 heads 334 and
-// 269 us (e4m3), 625 and 337 us (bf16): a second group reads the keys again.
+// 256 us (e4m3), 625 and 337 us (bf16): a second group reads the keys again.
 int paged_rows_group(int T, int B, int G) { return static_cast<long long>(T) * G > RW * static_cast<long long>(B) ? 2 * RW : RW; }
 
 cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void *q, const void *r,
