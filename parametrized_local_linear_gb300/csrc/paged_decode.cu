@@ -643,16 +643,17 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float p = fast_exp2(cc[mt][2 * e] - msub), pt = p * cc[mt][2 * e + 1];
+          const float p = fast_exp2(cc[mt][2 * e] - msub);
+          uint32_t w = pack_bf16x2(p, p * cc[mt][2 * e + 1]);
+          // sigma is the sum of the p t as rounded: their errors cancel in
+          // O1 s - O2 as the values do (one key: o = v whatever t is).
           l += p;
-          sg += pt;
+          sg += bf16hi(w);
           if constexpr (FP8) {
             const uint32_t two = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * e + g);
-            const float fv = __uint_as_float(((two >> 8) + 64u) << 23);  // 2^(E_v - 127 + 64)
-            pb[mt][e] = transpose_8x8(pack_bf16x2(p * fv, pt * fv));
-          } else {
-            pb[mt][e] = transpose_8x8(pack_bf16x2(p, pt));
+            w = mul_bf16x2(w, ((two >> 8) + 64u) * 0x00800080u);  // 2^(E_v - 127 + 64)
           }
+          pb[mt][e] = transpose_8x8(w);
         }
       if constexpr (FP8) {
 #pragma unroll

@@ -383,11 +383,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "n"(SEL));
   return (r << 4) & 0x87f087f0u;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
 
 template <bool FP8>
 __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)

@@ -133,8 +133,10 @@ def attend(Q, R, K, V, nkeys):
     nkeys[i] of K, V. Returns (o, lse, bound): bound [m, d] on |o_gpu - o| of
     a kernel that rounds the weights p_j and the products p_j t_j to bf16 once
     before the value products, and the output once:
-      2^-8 ((1 + |s|) sum_j w_j |v_j| + sum_j w_j |t_j| |v_j| + |o|)
-    since o = O1 (1 + s) - O2 and s and the denominator use unrounded p."""
+      2^-8 ((1 + |s|) sum_j w_j |v_j| + sum_j w_j |t_j| (|v_j| + |O1|) + |o|)
+    since o = O1 (1 + s) - O2, the denominator uses unrounded p, and s unrounded
+    p_j t_j (long chunks) or those of O2 (few rows): a p_j t_j that is off by e
+    enters o as -e v_j or as e (O1 - v_j)."""
     Q, R, K, V = (torch.as_tensor(np.asarray(x, dtype=np.float64)) for x in (Q, R, K, V))
     nkeys = torch.as_tensor(nkeys)
     m = Q.shape[0]
@@ -150,7 +152,8 @@ def attend(Q, R, K, V, nkeys):
     c = w * (t - (R * mean_k).sum(1, keepdim=True))
     o = mean_v - (c @ V - c.sum(1, keepdim=True) * mean_v)
     s = (w * t).sum(1, keepdim=True)
-    bound = BF16_HALF * ((1 + s.abs()) * (w @ V.abs()) + (w * t.abs()) @ V.abs() + o.abs())
+    bound = BF16_HALF * ((1 + s.abs()) * (w @ V.abs()) + (w * t.abs()) @ V.abs()
+                         + mean_v.abs() * (w * t.abs()).sum(1, keepdim=True) + o.abs())
     return o.numpy(), lse.numpy(), bound.numpy() + 1e-6
 
 

@@ -922,3 +922,25 @@ def test_a_sequence_that_is_not_finite_leaves_the_others_alone(counts, bad):
     assert same_bits(clean[0][rows.to(dev)], dirty[0][rows.to(dev)])
     others = [b for b in range(len(counts)) if b != sick]
     assert same_bits(clean[1][others], dirty[1][others])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("counts,Hq,Hkv", [([1] * 6, 16, 2), ([1] * 6, 4, 2), ([3, 1, 1, 1, 1, 2], 4, 2)])
+def test_a_token_that_sees_one_key_gives_its_value(counts, Hq, Hkv, fp8):
+    """Few rows: o = v whatever the probe says: w = 1, and O2 and O1 s cancel,
+    exactly up to fp32 rounding (each first token of a sequence, |t| up to a few
+    tens)."""
+    dev = device()
+    pool = ref.filled_pool(counts, Hkv, 16, fp8, 9)
+    T, starts = sum(counts), ends(counts)[:-1].long()
+    q, r = ref.normal_rows(T, Hq, 1), ref.normal_rows(T, Hq, 2, 1.0)
+    out, _ = plx_prefill_fwd_paged(q.to(dev), r.to(dev), seqlens=pool.seqlens.to(dev),
+                                   cu_q=ends(counts).to(dev), **pool.to(dev))
+    got = out.cpu()[starts].double().numpy()
+    plx_check_device_error()
+    # p, 1 / l, s and the two products of the result are off by a few 2^-23
+    # relative to (1 + |t|) |v|; with |t| < 64 that is below 2^-9 |v|, half a step
+    # of the smallest distance of a bf16 value from its neighbours.
+    for b in range(len(counts)):
+        v = np.repeat(pool.get(b, 1)[1][0], Hq // Hkv, axis=0)
+        assert np.array_equal(got[b], v), b
