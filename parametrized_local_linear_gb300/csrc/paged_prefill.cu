@@ -708,8 +708,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         }
         continue;
       }
+      // The token at position 0 sees one key: the covariance is zero and o = v. Its
+      // O1 s and O2 differ by the rounding of P o T, so they are left out.
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float g1 = (1.f + sg * inv) * inv;
+      const bool one = it.pos0 + rtok == 0;
+      const float g1 = one ? inv : (1.f + sg * inv) * inv, g2 = one ? 0.f : inv;
       // Output rows: 32 dims at a time through shared memory, so that four
       // lanes write 64 contiguous bytes of a row.
       __nv_bfloat16 *base = a.out + it.row0 * a.ots + it.kvh * a.G * a.ohs;
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float x0 = fmaf(o1[e], g1, -o2[e] * inv), x1 = fmaf(o1[e + 1], g1, -o2[e + 1] * inv);
+          const float x0 = fmaf(o1[e], g1, -o2[e] * g2), x1 = fmaf(o1[e + 1], g1, -o2[e + 1] * g2);
           pk[e >> 1] = l > 0.f ? pack_bf16x2(x0, x1) : 0u;
         }
         __syncwarp();  // the previous part has been read
@@ -1081,10 +1084,11 @@ __global__ void __launch_bounds__(BM) paged_prefill_merge_kernel(const Args a) {
   const int h = kvh * a.G + row - ot * a.G;
   uint32_t pk[4] = {};
   if (L > 0.f) {
-    const float inv = 1.f / L, g1 = (1.f + S * inv) * inv;
+    const bool one = s.len - s.n + tok == 0;  // as in the epilogue
+    const float inv = 1.f / L, g1 = one ? inv : (1.f + S * inv) * inv, g2 = one ? 0.f : inv;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      pk[e] = pack_bf16x2(fmaf(o1[2 * e], g1, -o2[2 * e] * inv), fmaf(o1[2 * e + 1], g1, -o2[2 * e + 1] * inv));
+      pk[e] = pack_bf16x2(fmaf(o1[2 * e], g1, -o2[2 * e] * g2), fmaf(o1[2 * e + 1], g1, -o2[2 * e + 1] * g2));
   }
   *reinterpret_cast<uint4 *>(a.out + (s.first + tok) * a.ots + h * a.ohs + 8 * i) =
       make_uint4(pk[0], pk[1], pk[2], pk[3]);

@@ -925,11 +925,11 @@ def test_a_sequence_that_is_not_finite_leaves_the_others_alone(counts, bad):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("counts,Hq,Hkv", [([1] * 6, 16, 2), ([1] * 6, 4, 2), ([3, 1, 1, 1, 1, 2], 4, 2)])
+@pytest.mark.parametrize("counts,Hq,Hkv", [([1] * 6, 16, 2), ([1] * 6, 4, 2), ([3, 1, 1, 1, 1, 2], 4, 2),
+                                           ([2, 1, 1, 30, 40, 2], 16, 1), ([70, 50], 4, 2), ([300] * 3, 2, 2)])
 def test_a_token_that_sees_one_key_gives_its_value(counts, Hq, Hkv, fp8):
-    """Few rows: o = v whatever the probe says: w = 1, and O2 and O1 s cancel,
-    exactly up to fp32 rounding (each first token of a sequence, |t| up to a few
-    tens)."""
+    """o = v whatever the probe says: w = 1, and O2 and O1 s cancel (each first
+    token of a sequence, |t| up to a few tens)."""
     dev = device()
     pool = ref.filled_pool(counts, Hkv, 16, fp8, 9)
     T, starts = sum(counts), ends(counts)[:-1].long()
