@@ -103,6 +103,12 @@ struct PrefillArgs {
   unsigned *err;
 };
 
+// A wait by a whole warp, off the tiles' path: a call, since code in line costs
+// the tile loop instruction cache (4 x 4096 tokens 388 us in line, 383 so).
+__device__ __noinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+}
+
 struct Item {
   int q0, ntiles, zq, zk;
 };
@@ -433,8 +439,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * x + 1]));
       }
-      if (!ok) break;
       // Hand the row statistics to the epilogue and move on to the next item.
+      // The epilogue must have read item k - 2's before their buffer is written
+      // again. With two or more tiles an item it has: the scores of item k's last
+      // tile were issued behind value UMMAs of item k - 1, which waited for the
+      // epilogue to have read item k - 2's O. With one tile each (at most BN keys)
+      // they were only behind item k - 2's, so wait for item k - 1's O to have
+      // been read.
+      if (n == 1 && ok && k > 0) ok = wait_all(smem_u32(o_free), (k - 1) & 1, ab);
+      if (!ok) break;
       float *st = stat + (k & 1) * 3 * BM;
       st[row] = m_used;
       st[BM + row] = l;

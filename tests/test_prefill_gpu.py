@@ -60,6 +60,24 @@ def test_bf16_small_matches_oracle_every_row(B, Hq, Hkv, L):
     np.testing.assert_allclose(lse.double().numpy(), ref_lse, rtol=0, atol=LSE_ABS)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,Lk", [(20, 64, 8, 64, 64), (37, 32, 32, 33, 33), (40, 48, 2, 1, 1),
+                                            (30, 40, 8, 5, 50)])
+def test_bf16_many_items_of_one_key_tile_match_oracle_every_row(B, Hq, Hkv, Lq, Lk):
+    """Seven or more items a CTA, each of one key tile: the softmax must not run
+    into the row statistics of items that the epilogue has yet to read."""
+    from parametrized_local_linear_gb300 import plx_prefill_fwd_chunk
+    q, k, v, r = inputs.prefill_inputs(B, Hq, Hkv, Lk, 128, torch.bfloat16, 0.05, 29)
+    q, r = q[:, :, Lk - Lq:].contiguous(), r[:, :, Lk - Lq:].contiguous()
+    ref, ref_lse = oracle.prefill(q, k, v, r)
+    dev = device()
+    for _ in range(5):
+        lse = torch.full(q.shape[:3], float("nan"), device=dev)
+        out, _ = plx_prefill_fwd_chunk(*(t.to(dev) for t in (q, k, v, r)), lse=lse)
+        plx_check_device_error()
+        assert_bf16_close(out.double().cpu().numpy(), ref)
+        assert np.max(np.abs(lse.double().cpu().numpy() - ref_lse)) <= LSE_ABS
+
+
 def test_bf16_large_probe_and_values():
     """Larger probe (|r| ~ 0.5) and shifted values make the correction dominate."""
     q, k, v, r = inputs.prefill_inputs(1, 2, 1, 320, 128, torch.bfloat16, 0.5, 99)
