@@ -270,7 +270,8 @@ int plx_decode_default_nsplit(int B, int Hkv);
  *   kscale, vscale : uint8 [num_pages, Hkv, page_size], both or neither. A row
  *                    of codes stands for code * 2^(E - 127), E its byte in
  *                    1 .. 254 (E = 0 only for rows of zeros). Attention over e4m3
- *                    pages wants |v| and |v (r.k)| below 2^70.
+ *                    pages wants |r.k| below 2^63; weighted values w |v| below
+ *                    2^-70 may count as zero there.
  *   block_table    : int32 [B, max_pages] on the device. Position p of sequence
  *                    b is in slot p % page_size of page
  *                    block_table[b, p / page_size]. Entries behind a sequence's

@@ -37,8 +37,9 @@
 //     (sign, then the 7 magnitude bits over exponent and mantissa) are its
 //     value times 2^-120, exactly, subnormals included, in three integer
 //     instructions for two codes; the weights carry 2^64 and the records the
-//     other 2^56. The limit that follows, |v| < 2^70, is far outside any
-//     network's values. ldmatrix moves pairs of bytes: dims pair up differently
+//     other 2^56. Rows with E above 127 (values above 448) would take a weight
+//     out of bf16's range: the rest of their scale goes onto their codes, in a
+//     second copy of the value products that a tile with such a row takes. ldmatrix moves pairs of bytes: dims pair up differently
 //     than for bf16, and the query fragments and output rows are permuted to
 //     match.
 // The bound is memory for whole batches, the latency of a CTA's first loads, its
@@ -48,6 +49,8 @@
 // 1777 keys 9.6 us, of which the combine takes 3.
 #include <math.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "plx_paged.cuh"
 
@@ -60,6 +63,9 @@ constexpr int RW = 4;           // query rows of a warp: half the eight columns 
 constexpr int NST = 2 * NCW;    // ring stages; tile i goes to warp row i % (NCW / R) and stage i % NST
 constexpr int THREADS = 32 * (NCW + 1);
 constexpr int REC = 2 * D + 2;  // floats of a record: O1 / l, O2 / l, sigma / l, log2-sum-exp
+// The largest exponent byte of a value row whose scale the weights take whole:
+// they reach p t 2^64 then, and bf16 ends at 2^128.
+constexpr uint32_t kMaxWeightE = 127;
 constexpr float k2p56 = 72057594037927936.f;  // 2^56 = 2^120 / 2^64
 
 // Shared memory. The stages (K rows and V rows of a tile, 4 KB each) come
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     const int r0 = it.grp * GS, nr = min(GS, it.s.n * a.G - r0);  // this group's rows
     const int t_first = (line - gt % NL + NL) % NL;
     // The scale bytes of key `lane` of the warp's tiles, one tile ahead, and
-    // the page number of the tile after it.
+    // the page number of the tile after it. Byte 0 is K's, byte 1 V's.
     const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
     auto page_of = [&](int t) {
       const int key = (it.t0 + t) * KT + lane;
@@ -556,6 +562,10 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         sc_next = scales_of(t + NL, page_next);
         page_next = page_of(t + 2 * NL);
       }
+      // sc >> 8 > kMaxWeightE in some lane
+      const bool big = FP8 && __any_sync(0xffffffffu, sc > 0x7fffu);
+      // 2^(E_v - 127 + 64), or its part that the weights take, as a bf16 pair
+      const uint32_t scv = (min(sc >> 8, kMaxWeightE) + 64u) * 0x00800080u;
       bool ok = false;
       if (lane == 0) ok = !ab.raised() && mbar_wait(smem_u32(&full[st]), (gi / NST) & 1, ab);
       if (!__shfl_sync(0xffffffffu, ok, 0)) continue;  // aborting: skip the tile
@@ -650,25 +660,42 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           l += p;
           sg += bf16hi(w);
           if constexpr (FP8) {
-            const uint32_t two = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * e + g);
-            w = mul_bf16x2(w, ((two >> 8) + 64u) * 0x00800080u);  // 2^(E_v - 127 + 64)
+            w = mul_bf16x2(w, __shfl_sync(0xffffffffu, scv, 16 * mt + 8 * e + g));  // 2^(E_v - 127 + 64)
           }
           pb[mt][e] = transpose_8x8(w);
         }
       if constexpr (FP8) {
+        auto products = [&](auto extra) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t up[2];  // 2^(E_v - kMaxWeightE) of this thread's keys, at least 1
+            if constexpr (decltype(extra)::value) {
 #pragma unroll
-          for (int cp = 0; cp < 4; ++cp) {
-            uint32_t w[4];  // chunk 2 cp: keys 0-7, 8-15; chunk 2 cp + 1: the same
-            ldsm_x4_t(vb + swz(16 * mt + arow, 2 * cp + acol), w[0], w[1], w[2], w[3]);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t e0 = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * h + 2 * tq);
+                const uint32_t e1 = __shfl_sync(0xffffffffu, sc, 16 * mt + 8 * h + 2 * tq + 1);
+                up[h] = (max(e0 >> 8, kMaxWeightE) << 7) | (max(e1 >> 8, kMaxWeightE) << 23);
+              }
+            }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t af[4] = {codes_even(w[2 * e]), codes_odd(w[2 * e]), codes_even(w[2 * e + 1]),
-                                      codes_odd(w[2 * e + 1])};
-              mma_bf16_16816(acc[2 * cp + e], af, pb[mt][0], pb[mt][1]);
+            for (int cp = 0; cp < 4; ++cp) {
+              uint32_t w[4];  // chunk 2 cp: keys 0-7, 8-15; chunk 2 cp + 1: the same
+              ldsm_x4_t(vb + swz(16 * mt + arow, 2 * cp + acol), w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t af[4] = {codes_even(w[2 * e]), codes_odd(w[2 * e]), codes_even(w[2 * e + 1]),
+                                  codes_odd(w[2 * e + 1])};
+                if constexpr (decltype(extra)::value) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) af[i] = mul_bf16x2(af[i], up[i >> 1]);
+                }
+                mma_bf16_16816(acc[2 * cp + e], af, pb[mt][0], pb[mt][1]);
+              }
             }
           }
+        };
+        if (__builtin_expect(big, 0)) products(std::true_type{});
+        else products(std::false_type{});
       } else {
         const int vrow = (lane & 7) + 8 * (lane >> 4), vcol = (lane >> 3) & 1;
         const int valid = it.s.len - key0;  // rows of the tile that hold keys
