@@ -524,6 +524,15 @@ def _launch(fn, dev, stream, args):
             _check(fn(*args, _stream(stream, dev)))
 
 
+def _empty(shape, dtype, dev, stream):
+    """Memory for a result, in the order of the call's stream: from the current
+    stream's pool, another stream would write what work queued here may still use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _workspace(workspace, sizer, sizes, stream, dev):
     """(tensor, pointer, bytes) of the caller's workspace, or of one of the
     needed size from torch's caching allocator, in the order of the call's stream (a
@@ -535,11 +544,7 @@ def _workspace(workspace, sizer, sizes, stream, dev):
         else:
             with torch.cuda.device(dev):
                 need = getattr(lib(), sizer)(*sizes)
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != dev:
         raise ValueError("workspace must be on the device of q")
@@ -588,11 +593,11 @@ def plx_kv_read(kpages, vpages, block_table, cu_k, T, kscale=None, vscale=None, 
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, None, dev)
     _like(cu_k, "cu_k", torch.int32, (B + 1,), dev)
     if k is None:
-        k = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+        k = _empty((T, Hkv, d), torch.bfloat16, dev, stream)
     else:
         _like(k, "k", torch.bfloat16, (T, Hkv, d), dev)
     if v is None:
-        v = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+        v = _empty((T, Hkv, d), torch.bfloat16, dev, stream)
     else:
         _like(v, "v", torch.bfloat16, (T, Hkv, d), dev)
     _launch(lib().plx_kv_read, dev, stream,
@@ -623,7 +628,7 @@ def plx_decode_fwd_paged(q, r, kpages, vpages, block_table, seqlens, kscale=None
         for name, t in rows:
             _like(t, name, torch.bfloat16, shape, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(shape, torch.bfloat16, dev, stream)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_decode_paged_workspace_bytes", (B, Hq, Hkv, d),
                                       stream, dev)
     _launch(lib().plx_decode_fwd_paged, dev, stream,
@@ -650,7 +655,7 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
         raise ValueError("q and r must have the same strides")
     _like(cu_q, "cu_q", torch.int32, (B + 1,), dev)
     if out is None:
-        out, out_strides = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev), (Hq * d, d)
+        out, out_strides = _empty((T, Hq, d), torch.bfloat16, dev, stream), (Hq * d, d)
     else:
         if out.shape != q.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")

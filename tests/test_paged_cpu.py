@@ -256,3 +256,30 @@ def test_2_to_31_rows_of_pages_are_rejected(lib, call):
     """Rows of a page tensor are counted in 32 bits."""
     assert CALLS[call](lib, n=1 << 26) == UNS  # 2^26 pages x 2 heads x 16 slots
     assert b"2^31" in lib.plx_last_error_message()
+
+
+# ------------------------------------------------------------ memory of results
+def test_results_are_allocated_in_the_order_of_the_calls_stream(monkeypatch):
+    import inspect
+    order = []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            order.append(self.stream)
+
+        def __exit__(self, *exc):
+            order.append(None)
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: order.append("empty") or empty(*a, **kw))
+    t = binding._empty((3, 2), torch.bfloat16, torch.device("cpu"), "another")
+    assert order == ["another", "empty", None] and t.shape == (3, 2) and t.dtype is torch.bfloat16
+    binding._empty((3, 2), torch.bfloat16, torch.device("cpu"), None)
+    assert order[3:] == ["empty"]
+    for fn in (binding.plx_decode_fwd_paged, binding.plx_prefill_fwd_paged, binding.plx_kv_read,
+               binding._workspace):
+        assert "torch.empty" not in inspect.getsource(fn)
