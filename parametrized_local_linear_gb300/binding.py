@@ -5,7 +5,10 @@ include/plx.h) and does nothing but check tensor shapes/dtypes/devices, pass
 ``data_ptr()`` values and the current CUDA stream, and turn a non-OK status
 into an exception. All arithmetic runs in the library's kernels; there is no
 fallback: if libplx.so is missing or fails to load, every call raises.
-PyTorch supplies device memory and streams only.
+PyTorch supplies device memory and streams only. What a call allocates itself
+(results not given, workspaces) comes in the order of its stream, as under
+``torch.cuda.stream``: with ``stream=`` given, use a result on another stream
+as one made there.
 """
 from __future__ import annotations
 
@@ -109,6 +112,15 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, dev, stream):
+    """Memory for a result, in the order of the call's stream: from the current
+    stream's pool, another stream would write what work queued here may still use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _need(t, name, dtype, ndim, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -136,7 +148,7 @@ def _prefill(fn, dtype, q, k, v, r, out, lse, stream):
     if tuple(k.shape) != (B, Hkv, L, d) or tuple(v.shape) != (B, Hkv, L, d):
         raise ValueError("k and v must be [B, Hkv, L, d] matching q")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, dev, stream)
     _need(out, "out", dtype, 4, dev)
     if tuple(out.shape) != tuple(q.shape):
         raise ValueError("out must have the shape of q")
@@ -169,7 +181,7 @@ def plx_prefill_fwd_cor(q, k, v, r, out=None, lse=None, cor=None, stream=None):
     |Sigma rho| / |o| per row (see include/plx.h). ``cor`` is fp32
     [B, Hq, Lq] (allocated if None). Returns (out, lse, cor)."""
     if cor is None:
-        cor = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        cor = _empty(q.shape[:3], torch.float32, q.device, stream)
     return _prefill_chunk(q, k, v, r, out, lse, cor, stream)
 
 
@@ -185,7 +197,7 @@ def _prefill_chunk(q, k, v, r, out, lse, cor, stream):
     if tuple(k.shape) != (B, Hkv, Lk, d) or tuple(v.shape) != (B, Hkv, Lk, d):
         raise ValueError("k and v must be [B, Hkv, Lk, d] matching q")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, dev, stream)
     _need(out, "out", torch.bfloat16, 4, dev)
     if tuple(out.shape) != tuple(q.shape):
         raise ValueError("out must have the shape of q")
@@ -219,10 +231,10 @@ def plx_prefill_fwd_train(q, k, v, r, out=None, lse=None, o1=None, sbar=None, st
     Hkv = k.shape[1]
     if tuple(r.shape) != tuple(q.shape) or tuple(k.shape) != (B, Hkv, L, d) or v.shape != k.shape:
         raise ValueError("r must match q; k and v must be [B, Hkv, L, d]")
-    out = torch.empty_like(q) if out is None else out
-    o1 = torch.empty_like(q) if o1 is None else o1
-    lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev) if lse is None else lse
-    sbar = torch.empty((B, Hq, L), dtype=torch.float32, device=dev) if sbar is None else sbar
+    out = _empty(q.shape, q.dtype, dev, stream) if out is None else out
+    o1 = _empty(q.shape, q.dtype, dev, stream) if o1 is None else o1
+    lse = _empty((B, Hq, L), torch.float32, dev, stream) if lse is None else lse
+    sbar = _empty((B, Hq, L), torch.float32, dev, stream) if sbar is None else sbar
     for name, t in (("out", out), ("o1", o1)):
         _need(t, name, torch.bfloat16, 4, dev)
         if tuple(t.shape) != tuple(q.shape):
@@ -251,10 +263,10 @@ def plx_prefill_bwd(q, k, v, r, out, o1, lse, sbar, dout, dq=None, dk=None, dv=N
         _need(t, name, torch.bfloat16, 4, dev)
         if tuple(t.shape) != (B, Hkv, L, d):
             raise ValueError(f"{name} must be [B, Hkv, L, d]")
-    dq = torch.empty_like(q) if dq is None else dq
-    dr = torch.empty_like(q) if dr is None else dr
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, dev, stream) if dq is None else dq
+    dr = _empty(q.shape, q.dtype, dev, stream) if dr is None else dr
+    dk = _empty(k.shape, k.dtype, dev, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, dev, stream) if dv is None else dv
     for name, t, like in (("r", r, q), ("out", out, q), ("o1", o1, q), ("dout", dout, q),
                           ("dq", dq, q), ("dr", dr, q), ("dk", dk, k), ("dv", dv, k)):
         _need(t, name, torch.bfloat16, 4, dev)
@@ -287,7 +299,7 @@ def plx_qkvr_proj(x, w, B, L, Hq, Hkv, d=128, q=None, k=None, v=None, r=None, st
     outs = {}
     for name, t in (("q", q), ("k", k), ("v", v), ("r", r)):
         if t is None:
-            t = torch.empty(shapes[name], dtype=torch.bfloat16, device=dev)
+            t = _empty(shapes[name], torch.bfloat16, dev, stream)
         _need(t, name, torch.bfloat16, 4, dev)
         if tuple(t.shape) != shapes[name]:
             raise ValueError(f"{name} must be {shapes[name]}")
@@ -353,7 +365,7 @@ def plx_decode_fwd(q, r, kcache, vcache, seqlens, out=None, nsplit=0, workspace=
     B, Hq, d = q.shape
     Hkv = kcache.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, dev, stream)
     L = lib()
     with torch.cuda.device(dev):
         s = _stream(stream, dev)
@@ -396,9 +408,9 @@ def plx_decode_fwd_cor(q, r, kcache, vcache, seqlens, out=None, cor=None, stream
     dev = _decode_tensors(q, r, kcache, vcache, seqlens, out, cor)
     B, Hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, dev, stream)
     if cor is None:
-        cor = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        cor = _empty((B, Hq), torch.float32, dev, stream)
     with torch.cuda.device(dev):
         st = lib().plx_decode_fwd_cor(q.data_ptr(), r.data_ptr(), kcache.data_ptr(),
                                       vcache.data_ptr(), seqlens.data_ptr(), out.data_ptr(),
@@ -522,15 +534,6 @@ def _launch(fn, dev, stream, args):
     else:
         with torch.cuda.device(dev):
             _check(fn(*args, _stream(stream, dev)))
-
-
-def _empty(shape, dtype, dev, stream):
-    """Memory for a result, in the order of the call's stream: from the current
-    stream's pool, another stream would write what work queued here may still use."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _workspace(workspace, sizer, sizes, stream, dev):

@@ -66,3 +66,13 @@ def test_decode_host_tensors_are_rejected(call):
     before any launch."""
     with pytest.raises(ValueError, match="CUDA"):
         _calls()[call](*_decode_args())
+
+
+def test_only_one_place_allocates_results():
+    """Every result that a call allocates comes in the order of the call's
+    stream: no call asks torch for memory by itself."""
+    import inspect
+
+    from parametrized_local_linear_gb300 import binding
+    rest = inspect.getsource(binding).replace(inspect.getsource(binding._empty), "")
+    assert "torch.empty" not in rest and "torch.zeros" not in rest
