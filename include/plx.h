@@ -379,8 +379,10 @@ size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
  * libplx_debug.so with this same interface) check, before each TMA copy and
  * each indexed global store, that the coordinates or index lie inside the
  * buffer: the tensor-map coordinates of every prefill, backward and
- * projection box, every decode box against its sequence's tokens, and the
- * decode's query rows and record slots. A failed check skips the access,
+ * projection box, every decode box against its sequence's tokens, the
+ * decode's query rows and record slots, and over a paged cache every page box,
+ * the rows of pages and results, records, parts and the tables that say where
+ * they are. A failed check skips the access,
  * stops the CTA as a timed-out wait does and sets the bit that this call
  * reports as PLX_ERR_BOUNDS; nothing traps. Outputs of a call that passed
  * every check equal the release library's bit for bit. */

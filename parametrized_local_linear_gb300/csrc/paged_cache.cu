@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs 
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     row[n] = __shfl_sync(0xffffffffu, my_row, n);
+    if (row[n] >= 0 && !PLX_IN_BOUNDS(row_inside(a.c, row[n]) && t0 + n < a.T, ErrWord{a.c.err})) row[n] = -1;
     x[n] = row[n] >= 0 ? *reinterpret_cast<const uint4 *>(src + n * a.token_stride) : make_uint4(0u, 0u, 0u, 0u);
   }
   uint8_t *pages = half ? a.vpages : a.kpages;
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const ReadArgs a) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     row[n] = __shfl_sync(0xffffffffu, my_row, n);
+    if (row[n] >= 0 && !PLX_IN_BOUNDS(row_inside(a.c, row[n]) && t0 + n < a.T, ErrWord{a.c.err})) row[n] = -1;
     x[n] = make_uint4(0u, 0u, 0u, 0u);
     E[n] = 0u;
     if (row[n] < 0) continue;

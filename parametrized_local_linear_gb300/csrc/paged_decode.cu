@@ -90,6 +90,7 @@ struct RowsArgs {
   float *recs;
   int2 *meta;
   int Hq, G, T, nshare, gs;  // gs: records of a slot (rows of the largest group)
+  long long vrows;           // places of meta; recs has nshare more
   int most;                  // as in RowsPlan
   float scale_log2;
 };
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           const int st = g % NST;
           const uint32_t bar = smem_u32(&full[st]);
           if (g >= NST) ok = mbar_wait(smem_u32(&empty[st]), ((g / NST) - 1) & 1, ab);
+          ok = ok && PLX_IN_BOUNDS(box_inside(a.c, z, 0, 16), ab);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(bar, 2 * TILE);
@@ -396,8 +398,9 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           if (active) tma_load_3d(smem_u32(smem + st * 2 * TILE) + at, map, 0, 0, z, bar);
         }
       }
-      if (!ok && lane == 0) {
-        // Let the warp's own copies (tiles g - NST .. g - 1) land first.
+      if (lane == 0) {
+        // The warp's own copies (tiles g - NST .. g - 1) land before it leaves:
+        // after an abort no consumer waits for them.
         for (int t = max(0, g - NST); t < g; ++t)
           mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
       }
@@ -440,9 +443,13 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
               }
             }
             const uint32_t dst = kb + y * 128;
+            // A box that fails the check goes where nothing is read: the stage
+            // still gets its bytes, which the drain below waits for.
+            const bool in = PLX_IN_BOUNDS(box_inside(a.c, z, slot, per), ab);
+            const int by = in ? slot : 0, bz = in ? z : beyond;
             if constexpr (FP8) {
-              tma_load_3d(dst, &tm_k, 0, slot, z, bar);
-              tma_load_3d(dst + TILE, &tm_v, 0, slot, z, bar);
+              tma_load_3d(dst, &tm_k, 0, by, bz, bar);
+              tma_load_3d(dst + TILE, &tm_v, 0, by, bz, bar);
               // The consumers load the scale bytes a tile ahead, this a ring
               // ahead. With two warps a tile, who both load them, 256 us against
               // 275 for 64 x 8192 keys and 8 query heads a kv head (two tiles
@@ -454,18 +461,15 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
                 prefetch_l2(a.c.vscale + row);
               }
             } else {
-              tma_load_4d(dst, &tm_k, 0, slot, z, 0, bar);
-              tma_load_4d(dst + TILE, &tm_v, 0, slot, z, 0, bar);
+              tma_load_4d(dst, &tm_k, 0, by, bz, 0, bar);
+              tma_load_4d(dst + TILE, &tm_v, 0, by, bz, 0, bar);
             }
           }
           ++g;
         }
       }
-      if (!ok) {
-        // Let this thread's own copies (tiles g - NST .. g - 1) land first.
-        for (int t = max(0, g - NST); t < g; ++t)
-          mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
-      }
+      for (int t = max(0, g - NST); t < g; ++t)  // as above
+        mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
     }
     return;
   }
@@ -486,6 +490,11 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     const int nt = it.t1 - it.t0;
     const int r0 = it.grp * GS, nr = min(GS, it.s.n * a.G - r0);  // this group's rows
     const int t_first = (line - gt % NL + NL) % NL;
+    // The item's query rows, records and place in meta lie inside theirs.
+    const bool item_ok = PLX_IN_BOUNDS(
+        it.b < a.c.B && it.kvh < a.c.Hkv && it.vrow >= 0 && it.vrow < a.vrows && nr >= 1 && nr <= gs &&
+            it.s.first >= 0 && it.s.first + (r0 + nr - 1) / a.G < a.T && it.t1 <= it.s.tiles,
+        ab);
     // The scale bytes of key `lane` of the warp's tiles, one tile ahead, and
     // the page number of the tile after it. Byte 0 is K's, byte 1 V's.
     const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
@@ -513,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     float fs = a.scale_log2, ft = 1.f;  // what the scores and the probe products still lack
     {
       const int row = RW * blk + (g >> 1);
-      const bool live = row < nr;
+      const bool live = row < nr && item_ok;
       const int tok = (r0 + (live ? row : 0)) / a.G, h = it.kvh * a.G + (r0 + (live ? row : 0)) % a.G;
       const __nv_bfloat16 *src = ((g & 1) ? a.r : a.q) + (it.s.first + tok) * a.qts + h * a.qhs;
       // e4m3: slots 2 tq, 2 tq + 1 hold dims 4 tq, 4 tq + 1 and slots + 8 dims
@@ -775,8 +784,10 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       const float inv = none ? 0.f : 1.f / L;
 #pragma unroll
       for (int w = 0; w < NL; ++w) stat(w, dim)[3] = f[w] * inv * down;
-      recs[dim * REC + 2 * D] = S * inv;
-      recs[dim * REC + 2 * D + 1] = none ? -INFINITY : M + log2f(L);
+      if (item_ok) {
+        recs[dim * REC + 2 * D] = S * inv;
+        recs[dim * REC + 2 * D + 1] = none ? -INFINITY : M + log2f(L);
+      }
     }
     consumer_sync();
     const float *sums[NL];
@@ -794,6 +805,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         o1 = fmaf(f, sums[w][at], o1);
         o2 = fmaf(f, sums[w][at + D], o2);
       }
+      if (!item_ok) continue;
       recs[row * REC + dim] = o1;
       recs[row * REC + D + dim] = o2;
     }
@@ -802,7 +814,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&empty[hold]));
     }
-    if (it.t0 == 0 && dim == 0) {
+    if (it.t0 == 0 && dim == 0 && item_ok) {
       // This CTA holds the row's first tile, so it is the first of the CTAs
       // that hold the row; the last one holds its last tile x, CTA
       // floor(((x + 1) n - 1) / W). CTA c' writes to slot c' + vrow.
@@ -824,7 +836,7 @@ struct CombineArgs {
   const int *seqlens, *cu;
   __nv_bfloat16 *out;
   float *lse;
-  long long ots, ohs, nslots;
+  long long ots, ohs, nslots, vrows;
   int Hq, G, T, gs, group, most;  // records of a slot, rows of a group
   int tokens;                     // blocks of a sequence and query head; 0: blocks go by packed rows
 };
@@ -861,8 +873,10 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
   if (!bad && len - n + (t - first) >= 0 && len > 0) {
     const int kvh = h / a.G, ng = (n * a.G + a.group - 1) / a.group;
     const int row = (t - first) * a.G + (h - kvh * a.G);
-    const int2 mt = a.meta[groups_before(first, b, a.G, a.group, a.most) * a.c.Hkv +
-                           static_cast<long long>(kvh) * ng + row / a.group];
+    const long long place = groups_before(first, b, a.G, a.group, a.most) * a.c.Hkv +
+                            static_cast<long long>(kvh) * ng + row / a.group;
+    if (!PLX_IN_BOUNDS(place >= 0 && place < a.vrows && t < a.T && row % a.group < a.gs, ErrWord{a.c.err})) return;
+    const int2 mt = a.meta[place];
     // An entry outside the records (left by an earlier call when this one
     // did no work) is not followed.
     const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
@@ -1016,6 +1030,7 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
   a.nshare = paged_rows_shares();
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const long long vrows = paged_rows_vrows(p, T, c.B, a.G, c.Hkv);
+  a.vrows = vrows;
   a.meta = static_cast<int2 *>(workspace);
   a.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + paged_rows_meta_bytes(vrows));
   cudaError_t e;
@@ -1033,6 +1048,7 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
   k.ots = ots;
   k.ohs = ohs;
   k.nslots = a.nshare + vrows;
+  k.vrows = vrows;
   k.Hq = Hq;
   k.G = a.G;
   k.T = T;

@@ -670,6 +670,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       tc_fence_after();
       const float *st = stat + (k & 1) * 3 * BM;
       const float m_used = st[row], l = st[BM + row], sg = st[2 * BM + row];
+      // Rows of the output; at most two parts a share, its first item's and its last's.
+      const bool item_ok = PLX_IN_BOUNDS(
+          it.b < a.c.B && it.kvh >= 0 && it.kvh < a.c.Hkv && it.row0 >= 0 && it.ntok >= 1 &&
+              min(it.ntok, a.TQ) <= a.T - it.row0 && ((it.j0 == 0 && it.j1 == it.nt) || k == 0 || (it.j0 == 0 && !cut)),
+          ab);
       auto o_read = [&] {  // O has been read: the next item's value UMMAs may overwrite it
         tc_fence_before();
         __syncwarp();
@@ -688,13 +693,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if (part == 7) o_read();
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            p4[(part * 8 + e) * BM + row] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            if (item_ok) p4[(part * 8 + e) * BM + row] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
         float *ps = reinterpret_cast<float *>(p4) + 2 * D * BM;
-        ps[row] = m_used;
-        ps[BM + row] = l;
-        ps[2 * BM + row] = sg;
-        if (it.j0 == 0) {
+        if (item_ok) {
+          ps[row] = m_used;
+          ps[BM + row] = l;
+          ps[2 * BM + row] = sg;
+        }
+        if (it.j0 == 0 && item_ok) {
           cut = true;
           if (warp == EP_WARP && lane == 0) {
             int *te = a.table + 4 * blockIdx.x;
@@ -716,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       // Output rows: 32 dims at a time through shared memory, so that four
       // lanes write 64 contiguous bytes of a row.
       __nv_bfloat16 *base = a.out + it.row0 * a.ots + it.kvh * a.G * a.ohs;
-      const int ntok = it.ntok;
+      const int ntok = item_ok ? it.ntok : 0;
 #pragma unroll 1
       for (int part = 0; part < 4; ++part) {
         float o1[32], o2[32];
@@ -744,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if (otok[i] < ntok) *reinterpret_cast<uint4 *>(base + ooff[i] + part * 32) = v;
         }
       }
-      if (a.lse != nullptr && rtok < a.TQ && rtok < it.ntok)
+      if (a.lse != nullptr && rtok < a.TQ && rtok < ntok)
         a.lse[static_cast<long long>(it.row0 + rtok) * a.Hq + it.kvh * a.G + rh] =
             l > 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
@@ -809,6 +816,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
             const uint32_t bar = smem_u32(kv ? &rv_full[st] : &rk_full[st]);
             const uint32_t dst = smem_u32(smem + C::OFF_RAW + (st * 2 + kv) * RAW);
             if (g >= NRAW) ok = mbar_wait(smem_u32(kv ? &rv_empty[st] : &rk_empty[st]), ((g / NRAW) - 1) & 1, ab);
+            ok = ok && PLX_IN_BOUNDS(lane * box >= BN || box_inside(a.c, z, slot, box), ab);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(bar, RAW);
@@ -819,13 +827,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if (!ok) break;
         }
       }
-      if (ab.raised()) {
-        // Let this warp's own copies land before the CTA exits.
-        for (int gg = max(0, issued[0] - NRAW); gg < issued[0]; ++gg)
-          mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
-        for (int gg = max(0, issued[1] - NRAW); gg < issued[1]; ++gg)
-          mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
-      }
+      // This warp's own copies land before the CTA exits: after an abort no
+      // other warp waits for them.
+      for (int gg = max(0, issued[0] - NRAW); gg < issued[0]; ++gg)
+        mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
+      for (int gg = max(0, issued[1] - NRAW); gg < issued[1]; ++gg)
+        mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
     }
   } else if (warp < LOAD_WARP) {
     // ------------------------------------------------------------ score UMMAs
@@ -845,8 +852,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         if (is_s) {
           // Q and R of the previous item are dead once its last S and T finish.
           if (k > 0 && !wait_one(smem_u32(q_empty), (k - 1) & 1, ab)) break;
-          mbar_arrive_expect_tx(qb, 4 * a.G * a.TQ * 128);
           const int h0 = it.kvh * a.G, t0 = it.row0;
+          if (!PLX_IN_BOUNDS(t0 >= 0 && t0 < a.T && h0 >= 0 && h0 + a.G <= a.Hq, ab)) break;
+          mbar_arrive_expect_tx(qb, 4 * a.G * a.TQ * 128);
           tma_load_3d(smem_u32(smem), &tm_q, 0, h0, t0, qb);
           tma_load_3d(smem_u32(smem + HALF_Q), &tm_q, 64, h0, t0, qb);
           tma_load_3d(smem_u32(smem + C::OFF_R), &tm_r, 0, h0, t0, qb);
@@ -904,6 +912,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         const int st = g % NSK, slot = (j * BN) & pmask, z = z_next;  // slot: 0 unless pages are larger than a tile
         z_next = boxes_of(it, j + 1);
         if (g >= NSK) ok = mbar_wait(smem_u32(&empty[st]), ((g / NSK) - 1) & 1, ab);
+        ok = ok && PLX_IN_BOUNDS(lane * box >= BN || box_inside(a.c, z, slot, box), ab);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t bar = smem_u32(&full[st]), dst = ring + st * TILE_KV;
@@ -915,11 +924,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         }
       }
     }
-    if (ab.raised()) {
-      // Let this warp's own copies land before the CTA exits.
-      for (int gg = max(0, g - NSK); gg < g; ++gg)
-        mbar_wait_drain(smem_u32(&full[gg % NSK]), (gg / NSK) & 1);
-    }
+    // This warp's own copies land before the CTA exits: after an abort no other
+    // warp waits for them.
+    for (int gg = max(0, g - NSK); gg < g; ++gg)
+      mbar_wait_drain(smem_u32(&full[gg % NSK]), (gg / NSK) & 1);
   } else {
     // ------------------------------------------------------------ e4m3: conversion
     // Two warps convert K, two V, so that neither waits for the other's ring:
@@ -1051,9 +1059,12 @@ __global__ void __launch_bounds__(BM) paged_prefill_merge_kernel(const Args a) {
   const int b = te[0];
   if (b < 0) return;
   const int kvh = te[1], t = te[2], last = te[3] >> 1, slot = te[3] & 1;
+  if (!PLX_IN_BOUNDS(b < a.c.B && kvh >= 0 && kvh < a.c.Hkv && t >= 0 && last >= c && last < static_cast<int>(gridDim.x),
+                     ErrWord{a.c.err}))
+    return;
   const Seq s = seq_of(a, b);
   const int ot = row / a.G, tok = t * a.TQ + ot;
-  if (ot >= a.TQ || tok >= s.n) return;
+  if (ot >= a.TQ || tok >= s.n || !PLX_IN_BOUNDS(s.first + tok < a.T, ErrWord{a.c.err})) return;
   // Parts: CTA c's, then slot 0 of the CTAs up to the last.
   auto part = [&](int p) { return a.parts + (p == c ? 2ll * c + slot : 2ll * p) * PART; };
   float M = -INFINITY;

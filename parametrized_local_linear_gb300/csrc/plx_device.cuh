@@ -97,6 +97,14 @@ struct Abort {
   }
 };
 
+// In place of an Abort in kernels that wait for nothing: only the error word.
+struct ErrWord {
+  unsigned *err;  // may be null
+  __device__ __forceinline__ void raise(unsigned code) const {
+    if (err) atomicOr(err, code);
+  }
+};
+
 // Wait for phase `parity` of `bar`; false if the wait ran out or the CTA is
 // aborting.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Abort &ab,

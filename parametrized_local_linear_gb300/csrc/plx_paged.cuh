@@ -34,6 +34,16 @@ __device__ __forceinline__ long long page_row(const PagedCache &c, int b, int h,
   return ((static_cast<long long>(page) * c.Hkv + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
+// Whether the box of `keys` rows from slot `slot` of (page, kv head) block z lies
+// in the pages, or wholly behind them (z = num_pages Hkv: TMA zero fill).
+__device__ __forceinline__ bool box_inside(const PagedCache &c, int z, int slot, int keys) {
+  return z >= 0 && z <= c.num_pages * c.Hkv && slot >= 0 && slot + keys <= 1 << c.page_shift;
+}
+// Whether `row` is one of the pages' rows.
+__device__ __forceinline__ bool row_inside(const PagedCache &c, long long row) {
+  return row >= 0 && row < (static_cast<long long>(c.num_pages) * c.Hkv) << c.page_shift;
+}
+
 // Keys of a sequence of `n`; 0 (and the device error word set) for a length
 // that the block table cannot hold.
 __device__ __forceinline__ int checked_len(const PagedCache &c, int n) {

@@ -283,3 +283,14 @@ def test_results_are_allocated_in_the_order_of_the_calls_stream(monkeypatch):
     for fn in (binding.plx_decode_fwd_paged, binding.plx_prefill_fwd_paged, binding.plx_kv_read,
                binding._workspace):
         assert "torch.empty" not in inspect.getsource(fn)
+
+
+# ------------------------------------------------------------ debug build
+@pytest.mark.parametrize("name,at_least", [("paged_cache.cu", 2), ("paged_decode.cu", 4), ("paged_prefill.cu", 6)])
+def test_the_debug_build_checks_the_paged_kernels(name, at_least):
+    """The header promises a check before each TMA copy and each indexed store:
+    page boxes, rows of pages and results, records, parts and their tables."""
+    import os
+    from parametrized_local_linear_gb300 import build
+    with open(os.path.join(build.CSRC, name)) as f:
+        assert f.read().count("PLX_IN_BOUNDS(") >= at_least

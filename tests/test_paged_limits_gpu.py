@@ -1,10 +1,11 @@
 """The paged calls at the edges of what they take: values of every size that
-the e4m3 cache holds."""
+the e4m3 cache holds; the debug build's checks."""
 import numpy as np
 import pytest
 import torch
 
-from parametrized_local_linear_gb300 import plx_check_device_error, plx_decode_fwd_paged, plx_prefill_fwd_paged
+from parametrized_local_linear_gb300 import (binding, plx_check_device_error, plx_decode_fwd_paged, plx_kv_append,
+                                             plx_kv_read, plx_prefill_fwd_paged)
 
 import paged_ref as ref
 from helpers import device
@@ -40,3 +41,40 @@ def test_e4m3_values_of_every_size(Hq, Hkv, page, low, high):
             out = plx_decode_fwd_paged(q.to(dev), r.to(dev), **kw)
             plx_check_device_error()
             ref.assert_within(out, o, bound, "decode")
+
+
+# ------------------------------------------------------------ debug build
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,counts,Hq,Hkv,page,behind", [
+    ([1], [1], 2, 2, 16, 0), ([100, 70, 9, 0, 64], [3, 64, 0, 0, 1], 4, 2, 16, 2), ([5, 3], [9, 3], 4, 2, 16, 0),
+    ([40, 33], [7, 33], 128, 1, 16, 0), ([50], [9], 65, 1, 32, 0), ([2000, 50, 1030], [4, 1, 300], 16, 8, 64, 0),
+    ([6000], [130], 2, 1, 256, 0), ([300, 20, 40] + [90] * 9, [100, 2, 3] + [1] * 9, 4, 2, 16, 1),
+    ([260] * 4, [256] * 4, 64, 32, 128, 0), ([500] * 17, [1] * 16 + [300], 4, 2, 16, 0)])
+def test_debug_build_passes_its_checks(fp8, lens, counts, Hq, Hkv, page, behind, monkeypatch):
+    """Valid calls of every form (few rows, tiles, both, rounds of whole items,
+    split items): no check fails, and the bits are the release library's."""
+    dev = device()
+    pool = ref.filled_pool(lens, Hkv, page, fp8, 5)
+    T, B = sum(counts) + behind, len(lens)
+    q, r = ref.normal_rows(T, Hq, 1).to(dev), ref.normal_rows(T, Hq, 2, 0.05).to(dev)
+    qd, rd = ref.normal_rows(B, Hq, 3).to(dev), ref.normal_rows(B, Hq, 4, 0.05).to(dev)
+    k, v = ref.normal_rows(T, Hkv, 5).to(dev), ref.normal_rows(T, Hkv, 6).to(dev)
+    sl, cu = pool.seqlens.to(dev), ends(counts).to(dev)
+    cu_k = ends([max(n, 0) for n in lens]).to(dev)
+
+    def run():
+        kw = pool.to(dev)
+        plx_kv_append(k, v, seqlens=sl, cu_q=cu, **kw)
+        out, lse = torch.zeros_like(q), torch.zeros(T, Hq, device=dev)
+        plx_prefill_fwd_paged(q, r, seqlens=sl, cu_q=cu, out=out, lse=lse, **kw)
+        step = plx_decode_fwd_paged(qd, rd, seqlens=sl, **kw)
+        back = plx_kv_read(cu_k=cu_k, T=int(cu_k[-1]), **kw)
+        plx_check_device_error()
+        return [out, lse.view(torch.int16), step, *back, kw["kpages"], kw["vpages"]]
+
+    release = run()
+    dbg = binding.load_debug_lib()
+    monkeypatch.setattr(binding, "lib", lambda: dbg)
+    for a, b in zip(release, run()):
+        kind = torch.int16 if a.element_size() == 2 else torch.uint8
+        assert torch.equal(a.view(kind), b.view(kind))
