@@ -284,19 +284,21 @@ int plx_decode_default_nsplit(int B, int Hkv);
  *                    cu_q[0] = 0: the n_b = cu_q[b + 1] - cu_q[b] >= 0 new
  *                    tokens of sequence b are rows cu_q[b] .. of the T packed
  *                    rows. Rows behind cu_q[B] belong to no sequence.
- * New token i (0 .. n_b - 1) of sequence b has position seqlens[b] - n_b + i; a
- * negative one marks padding (a row that has no place in the cache and sees no
- * key). Whatever the pages hold behind seqlens[b], NaN included, does not reach
- * any result. Keys and values in front of it must be finite: in a tile of keys
- * the ones that a token does not see yet have the weight zero in its sums, not no
- * part in them. Packed rows have strides in elements, for the token and the head;
- * a row's d values are contiguous. Strides are multiples of 8 and at least d,
- * pointers 16-byte aligned (4 bytes for int32 and fp32). A page number outside
- * 0 .. num_pages - 1, a length beyond max_pages * page_size or a cu_q that
- * decreases, starts below 0 or passes T is not followed: the sequence's results
- * are undefined and plx_check_device_error reports PLX_ERR_INVALID_ARG (append
- * and read: where one of their rows meets it); nothing outside the arguments is
- * read or written. Lengths below zero count as zero. No atomics:
+ * New token i (0 .. n_b - 1) of sequence b has position seqlens[b] - n_b + i;
+ * a negative one marks padding (a row that has no place in the cache and sees
+ * no key). Whatever the pages hold behind seqlens[b], NaN included, does not
+ * reach any result. Keys and values in front of it must be finite: in a tile
+ * of keys the ones that a token does not see yet have the weight zero in its
+ * sums, not no part in them. A query or probe row that is not finite reaches
+ * its own results only: they are NaN where the sums are. Packed rows have
+ * strides in elements, for the token and the head; a row's d values are
+ * contiguous. Strides are multiples of 8 and at least d, pointers 16-byte
+ * aligned (4 bytes for int32 and fp32). A page number outside 0 .. num_pages -
+ * 1, a length beyond max_pages * page_size or a cu_q that decreases, starts
+ * below 0 or passes T is not followed: the sequence's results are undefined
+ * and plx_check_device_error reports PLX_ERR_INVALID_ARG (append and read:
+ * where one of their rows meets it); nothing outside the arguments is read or
+ * written. Lengths below zero count as zero. No atomics:
  * given arguments and lengths give the same bits on one GPU model.
  */
 

@@ -773,14 +773,17 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       float M = -INFINITY, L = 0.f, S = 0.f, f[NL];
 #pragma unroll
       for (int w = 0; w < NL; ++w) M = fmaxf(M, stat(w, dim)[0]);
-      const bool none = M == -INFINITY || ab.raised();
+      const float msub = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int w = 0; w < NL; ++w) {
         const float *s = stat(w, dim);
-        f[w] = none ? 0.f : fast_exp2(s[0] - M);
+        f[w] = fast_exp2(s[0] - msub);
         L = fmaf(f[w], s[1], L);
         S = fmaf(f[w], s[2], S);
       }
+      // L = 0: the row sees no key here. A query that is not a number has L = NaN
+      // (and M = -inf): its records and its output get NaN.
+      const bool none = L == 0.f || ab.raised();
       const float inv = none ? 0.f : 1.f / L;
 #pragma unroll
       for (int w = 0; w < NL; ++w) stat(w, dim)[3] = f[w] * inv * down;
@@ -900,8 +903,7 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx = fmaxf(mx, e[i]);
-        if (mx == -INFINITY) continue;
-        const float back = exp2f(M - mx);
+        const float msub = mx == -INFINITY ? 0.f : mx, back = exp2f(M - msub);
         W *= back;
         sf *= back;
         o1 *= back;
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
         M = mx;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float w = exp2f(e[i] - M);
+          const float w = exp2f(e[i] - msub);
           W += w;
           sf = fmaf(w, sr[i], sf);
           o1 = fmaf(w, x1[i], o1);
@@ -923,12 +925,13 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
       if ((dim & 31) == 0) slot[dim >> 5] = M;
       __syncthreads();
       M = fmaxf(fmaxf(slot[0], slot[1]), fmaxf(slot[2], slot[3]));
-      for (int base = 0; M != -INFINITY && base < nrec; base += CCH) {
+      const float msub = M == -INFINITY ? 0.f : M;
+      for (int base = 0; base < nrec; base += CCH) {
         const int cnt = min(CCH, nrec - base);
         const float *rb = rec + static_cast<size_t>(base) * stride;
         __syncthreads();  // the previous chunk's weights are consumed
         for (int i = dim; i < cnt; i += D) {
-          const float w = exp2f(rb[i * stride + 2 * D + 1] - M);
+          const float w = exp2f(rb[i * stride + 2 * D + 1] - msub);
           wsig[0][i] = w;
           wsig[1][i] = w * rb[i * stride + 2 * D];
         }
@@ -943,7 +946,7 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
         }
       }
     }
-    if (M != -INFINITY) {
+    if (W != 0.f) {  // NaN, for a query that is not a number, goes on
       const float inv = 1.f / W;
       o1 *= inv;
       o2 *= inv;

@@ -358,6 +358,13 @@ __device__ __noinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
 }
 
+// The loads into a ring's last stages, of `issued` tiles in all, land before the
+// loading warp leaves: after an abort no other warp waits for them.
+__device__ __noinline__ void drain_ring(uint64_t *full, int issued, int stages) {
+  for (int g = max(0, issued - stages); g < issued; ++g)
+    mbar_wait_drain(smem_u32(&full[g % stages]), (g / stages) & 1);
+}
+
 // 4-D tiled load (box and swizzle come from the tensor map).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
                                             int w, uint32_t bar) {
@@ -717,7 +724,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       }
       // The token at position 0 sees one key: the covariance is zero and o = v. Its
       // O1 s and O2 differ by the rounding of P o T, so they are left out.
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // l = 0: the row sees no key. A query that is not a number has l = NaN.
+      const float inv = l != 0.f ? 1.f / l : 0.f;
       const bool one = it.pos0 + rtok == 0;
       const float g1 = one ? inv : (1.f + sg * inv) * inv, g2 = one ? 0.f : inv;
       // Output rows: 32 dims at a time through shared memory, so that four
@@ -735,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const float x0 = fmaf(o1[e], g1, -o2[e] * g2), x1 = fmaf(o1[e + 1], g1, -o2[e + 1] * g2);
-          pk[e >> 1] = l > 0.f ? pack_bf16x2(x0, x1) : 0u;
+          pk[e >> 1] = l != 0.f ? pack_bf16x2(x0, x1) : 0u;
         }
         __syncwarp();  // the previous part has been read
 #pragma unroll
@@ -753,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       }
       if (a.lse != nullptr && rtok < a.TQ && rtok < ntok)
         a.lse[static_cast<long long>(it.row0 + rtok) * a.Hq + it.kvh * a.G + rh] =
-            l > 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            l != 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
     if (!cut && warp == EP_WARP && lane == 0) a.table[4 * blockIdx.x] = -1;
   } else if (warp < S_WARP) {
@@ -827,12 +835,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if (!ok) break;
         }
       }
-      // This warp's own copies land before the CTA exits: after an abort no
-      // other warp waits for them.
-      for (int gg = max(0, issued[0] - NRAW); gg < issued[0]; ++gg)
-        mbar_wait_drain(smem_u32(&rk_full[gg % NRAW]), (gg / NRAW) & 1);
-      for (int gg = max(0, issued[1] - NRAW); gg < issued[1]; ++gg)
-        mbar_wait_drain(smem_u32(&rv_full[gg % NRAW]), (gg / NRAW) & 1);
+      drain_ring(rk_full, issued[0], NRAW);
+      drain_ring(rv_full, issued[1], NRAW);
     }
   } else if (warp < LOAD_WARP) {
     // ------------------------------------------------------------ score UMMAs
@@ -924,10 +928,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         }
       }
     }
-    // This warp's own copies land before the CTA exits: after an abort no other
-    // warp waits for them.
-    for (int gg = max(0, g - NSK); gg < g; ++gg)
-      mbar_wait_drain(smem_u32(&full[gg % NSK]), (gg / NSK) & 1);
+    drain_ring(full, g, NSK);
   } else {
     // ------------------------------------------------------------ e4m3: conversion
     // Two warps convert K, two V, so that neither waits for the other's ring:
@@ -1070,31 +1071,30 @@ __global__ void __launch_bounds__(BM) paged_prefill_merge_kernel(const Args a) {
   float M = -INFINITY;
   for (int p = c; p <= last; ++p) M = fmaxf(M, part(p)[2 * D * BM + row]);
   float L = 0.f, S = 0.f, o1[8] = {}, o2[8] = {};
-  if (M != -INFINITY) {
+  const float msub = M == -INFINITY ? 0.f : M;
 #pragma unroll 2
-    for (int p = c; p <= last; ++p) {
-      const float *st = part(p) + 2 * D * BM;
-      const float f = fast_exp2(st[row] - M);
-      L = fmaf(f, st[BM + row], L);
-      S = fmaf(f, st[2 * BM + row], S);
-      const float4 *p4 = reinterpret_cast<const float4 *>(part(p));
+  for (int p = c; p <= last; ++p) {
+    const float *st = part(p) + 2 * D * BM;
+    const float f = fast_exp2(st[row] - msub);
+    L = fmaf(f, st[BM + row], L);
+    S = fmaf(f, st[2 * BM + row], S);
+    const float4 *p4 = reinterpret_cast<const float4 *>(part(p));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 x = p4[(2 * i + h) * BM + row], y = p4[(32 + 2 * i + h) * BM + row];
-        o1[4 * h] = fmaf(f, x.x, o1[4 * h]);
-        o1[4 * h + 1] = fmaf(f, x.y, o1[4 * h + 1]);
-        o1[4 * h + 2] = fmaf(f, x.z, o1[4 * h + 2]);
-        o1[4 * h + 3] = fmaf(f, x.w, o1[4 * h + 3]);
-        o2[4 * h] = fmaf(f, y.x, o2[4 * h]);
-        o2[4 * h + 1] = fmaf(f, y.y, o2[4 * h + 1]);
-        o2[4 * h + 2] = fmaf(f, y.z, o2[4 * h + 2]);
-        o2[4 * h + 3] = fmaf(f, y.w, o2[4 * h + 3]);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const float4 x = p4[(2 * i + h) * BM + row], y = p4[(32 + 2 * i + h) * BM + row];
+      o1[4 * h] = fmaf(f, x.x, o1[4 * h]);
+      o1[4 * h + 1] = fmaf(f, x.y, o1[4 * h + 1]);
+      o1[4 * h + 2] = fmaf(f, x.z, o1[4 * h + 2]);
+      o1[4 * h + 3] = fmaf(f, x.w, o1[4 * h + 3]);
+      o2[4 * h] = fmaf(f, y.x, o2[4 * h]);
+      o2[4 * h + 1] = fmaf(f, y.y, o2[4 * h + 1]);
+      o2[4 * h + 2] = fmaf(f, y.z, o2[4 * h + 2]);
+      o2[4 * h + 3] = fmaf(f, y.w, o2[4 * h + 3]);
     }
   }
   const int h = kvh * a.G + row - ot * a.G;
   uint32_t pk[4] = {};
-  if (L > 0.f) {
+  if (L != 0.f) {  // as in the epilogue
     const bool one = s.len - s.n + tok == 0;  // as in the epilogue
     const float inv = 1.f / L, g1 = one ? inv : (1.f + S * inv) * inv, g2 = one ? 0.f : inv;
 #pragma unroll
@@ -1105,7 +1105,7 @@ __global__ void __launch_bounds__(BM) paged_prefill_merge_kernel(const Args a) {
       make_uint4(pk[0], pk[1], pk[2], pk[3]);
   if (i == 0 && a.lse != nullptr)
     a.lse[static_cast<long long>(s.first + tok) * a.Hq + h] =
-        L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Q, R: [T, Hq, 128] with any strides, boxes of 64 dims x G heads x TQ tokens.

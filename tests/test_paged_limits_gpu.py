@@ -1,5 +1,5 @@
 """The paged calls at the edges of what they take: values of every size that
-the e4m3 cache holds; the debug build's checks."""
+the e4m3 cache holds, queries that are not numbers; the debug build's checks."""
 import numpy as np
 import pytest
 import torch
@@ -41,6 +41,41 @@ def test_e4m3_values_of_every_size(Hq, Hkv, page, low, high):
             out = plx_decode_fwd_paged(q.to(dev), r.to(dev), **kw)
             plx_check_device_error()
             ref.assert_within(out, o, bound, "decode")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("counts,lens,Hq,Hkv", [([1, 1, 1], [40, 500, 33], 4, 2), ([1, 1], [500, 33], 8, 1),
+                                                ([3, 2], [70, 300], 4, 2), ([130, 5], [6000, 64], 4, 2),
+                                                ([1] * 9 + [300], [90] * 9 + [2000], 4, 2), ([1], [60000], 2, 1)])
+@pytest.mark.parametrize("where", ["q", "r"])
+def test_a_query_that_is_not_a_number_gives_nan(counts, lens, Hq, Hkv, fp8, where):
+    """In its own row and nowhere else, not the zeros and -inf of a row that sees
+    no key: in one kernel or two, and where the sums of several CTAs are joined."""
+    dev = device()
+    pool = ref.filled_pool(lens, Hkv, 32, fp8, 3)
+    T = sum(counts)
+    q, r = ref.normal_rows(T, Hq, 1).to(dev), ref.normal_rows(T, Hq, 2, 0.05).to(dev)
+    kw = dict(seqlens=pool.seqlens.to(dev), **pool.to(dev))
+
+    def run():
+        lse = torch.empty(T, Hq, device=dev)
+        out, _ = plx_prefill_fwd_paged(q, r, cu_q=ends(counts).to(dev), lse=lse, **kw)
+        got = [out, lse]
+        if counts == [1] * len(counts):
+            got.append(plx_decode_fwd_paged(q, r, **kw))
+        plx_check_device_error()
+        return got
+
+    clean = run()
+    sick = torch.zeros(T, Hq, dtype=torch.bool, device=dev)
+    for t, h in ((0, 1), (T - 1, 0)):
+        sick[t, h] = True
+        (q if where == "q" else r)[t, h, 17] = float("nan")
+    dirty = run()
+    for c, d in zip(clean, dirty):
+        if d.dim() == 3 or where == "q":
+            assert torch.isnan(d[sick]).all()
+        assert torch.equal(c[~sick], d[~sick])
 
 
 # ------------------------------------------------------------ debug build
