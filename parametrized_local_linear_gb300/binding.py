@@ -446,6 +446,12 @@ def _like(t, name, dtype, shape, dev):
     _need(t, name, dtype, len(shape), dev)
 
 
+def _given(name, t):
+    """For tensors that only some of the paged calls can do without."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+
+
 def _check_pages(kpages, vpages, kscale, vscale, block_table, seqlens, dev):
     """Raises for what is wrong with the tensors of a paged cache."""
     shape = kpages.shape
@@ -551,8 +557,8 @@ def _workspace(workspace, sizer, sizes, stream, dev):
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != dev:
         raise ValueError("workspace must be on the device of q")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    if not workspace.is_contiguous() or workspace.numel() == 0:
+        raise ValueError("workspace must be contiguous and not empty")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -567,6 +573,7 @@ def plx_kv_append(k, v, kpages, vpages, block_table, seqlens, cu_q=None, kscale=
         raise ValueError(f"k must be [T, Hkv, d], got shape {tuple(k.shape)}")
     if v.shape != k.shape:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected the shape of k {tuple(k.shape)}")
+    _given("seqlens", seqlens)
     dev = k.device
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
@@ -589,6 +596,7 @@ def plx_kv_read(kpages, vpages, block_table, cu_k, T, kscale=None, vscale=None, 
     """Read sequences of a paged KV cache back (see include/plx.h): the first
     cu_k[b + 1] - cu_k[b] tokens of sequence b at rows cu_k[b] .. of bf16
     [T, Hkv, d], the packed cache of plx_decode_fwd. Returns (k, v)."""
+    _given("cu_k", cu_k)
     dev = kpages.device
     T = int(T)
     if T < 0:
@@ -614,6 +622,7 @@ def plx_decode_fwd_paged(q, r, kpages, vpages, block_table, seqlens, kscale=None
     Returns out."""
     if q.dim() != 3:
         raise ValueError(f"q must be [B, Hq, d], got shape {tuple(q.shape)}")
+    _given("seqlens", seqlens)
     dev = q.device
     B, Hq, d = shape = q.shape
     if B != block_table.shape[0] or d != kpages.shape[-1]:
@@ -649,6 +658,8 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
         raise ValueError(f"q must be [T, Hq, d], got shape {tuple(q.shape)}")
     if r.shape != q.shape:
         raise ValueError(f"r has shape {tuple(r.shape)}, expected the shape of q {tuple(q.shape)}")
+    _given("seqlens", seqlens)
+    _given("cu_q", cu_q)
     dev = q.device
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)

@@ -258,6 +258,13 @@ def test_2_to_31_rows_of_pages_are_rejected(lib, call):
     assert b"2^31" in lib.plx_last_error_message()
 
 
+@pytest.mark.parametrize("call,name", [("append", "seqlens"), ("decode", "seqlens"), ("prefill", "seqlens"),
+                                       ("prefill", "cu_q"), ("read", "cu_k")])
+def test_missing_lengths_and_offsets_are_rejected(call, name):
+    with pytest.raises(TypeError, match=name):
+        _py(call, _args(), **{name: None})
+
+
 # ------------------------------------------------------------ memory of results
 def test_results_are_allocated_in_the_order_of_the_calls_stream(monkeypatch):
     import inspect

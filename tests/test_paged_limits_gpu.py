@@ -1,5 +1,6 @@
 """The paged calls at the edges of what they take: values of every size that
-the e4m3 cache holds, queries that are not numbers; the debug build's checks."""
+the e4m3 cache holds, queries that are not numbers, refusals; the debug build's
+checks."""
 import numpy as np
 import pytest
 import torch
@@ -76,6 +77,19 @@ def test_a_query_that_is_not_a_number_gives_nan(counts, lens, Hq, Hkv, fp8, wher
         if d.dim() == 3 or where == "q":
             assert torch.isnan(d[sick]).all()
         assert torch.equal(c[~sick], d[~sick])
+
+
+# ------------------------------------------------------------ refusals
+def test_an_empty_workspace_is_refused():
+    """Its pointer is null, which at the C boundary asks for an allocation."""
+    dev = device()
+    pool = ref.filled_pool([40, 7], 2, 16, True, 3)
+    kw = dict(seqlens=pool.seqlens.to(dev), workspace=torch.empty(0, dtype=torch.uint8, device=dev), **pool.to(dev))
+    q = ref.normal_rows(2, 4, 1).to(dev)
+    with pytest.raises(ValueError, match="workspace"):
+        plx_decode_fwd_paged(q, q, **kw)
+    with pytest.raises(ValueError, match="workspace"):
+        plx_prefill_fwd_paged(q, q, cu_q=ends([1, 1]).to(dev), **kw)
 
 
 # ------------------------------------------------------------ debug build
