@@ -1,12 +1,12 @@
 """The paged calls at the edges of what they take: values of every size that
-the e4m3 cache holds, queries that are not numbers, refusals; the debug build's
-checks."""
+the e4m3 cache holds, queries that are not numbers, refusals, bad metadata; the
+debug build's checks."""
 import numpy as np
 import pytest
 import torch
 
-from parametrized_local_linear_gb300 import (binding, plx_check_device_error, plx_decode_fwd_paged, plx_kv_append,
-                                             plx_kv_read, plx_prefill_fwd_paged)
+from parametrized_local_linear_gb300 import (PlxError, binding, plx_check_device_error, plx_decode_fwd_paged,
+                                             plx_kv_append, plx_kv_read, plx_prefill_fwd_paged)
 
 import paged_ref as ref
 from helpers import device
@@ -90,6 +90,104 @@ def test_an_empty_workspace_is_refused():
         plx_decode_fwd_paged(q, q, **kw)
     with pytest.raises(ValueError, match="workspace"):
         plx_prefill_fwd_paged(q, q, cu_q=ends([1, 1]).to(dev), **kw)
+
+
+# ------------------------------------------------------------ bad metadata
+def same_pages(kw, pool):
+    pairs = [(kw["kpages"], pool.k), (kw["vpages"], pool.v)]
+    if pool.fp8:
+        pairs += [(kw["kscale"], pool.ks), (kw["vscale"], pool.vs)]
+    kind = [torch.uint8 if a.element_size() == 1 else torch.int16 for a, _ in pairs]
+    return all(torch.equal(a.cpu().view(t), b.view(t)) for (a, b), t in zip(pairs, kind))
+
+
+def reported(yes=True):
+    if not yes:
+        return plx_check_device_error()
+    with pytest.raises(PlxError) as e:
+        plx_check_device_error()
+    assert e.value.status == binding.PLX_ERR_INVALID_ARG
+    plx_check_device_error()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("entry", [-1, 1 << 30])
+def test_append_leaves_the_page_alone_whose_entry_is_bad(fp8, entry):
+    """The page that the table should have named keeps its bytes, and so does
+    every other one that no new token goes to."""
+    dev = device()
+    lens = [100, 60]
+    pool = ref.filled_pool(lens, 2, 16, fp8, 3)
+    kw = pool.to(dev)
+    kw["block_table"][0, 2] = entry
+    new = ref.normal_rows(160, 2, 9)
+    plx_kv_append(new.to(dev), new.to(dev), seqlens=pool.seqlens.to(dev), cu_q=ends(lens).to(dev), **kw)
+    reported()
+    page = pool.table[0, 2].item()
+    tensors = [t for t in (pool.k, pool.v, pool.ks, pool.vs) if t is not None]
+    before = [t.view(torch.uint8)[page].clone() for t in tensors]
+    for b, at in ((0, 0), (1, 100)):
+        x = new[at:at + lens[b]].double().numpy()
+        pool.put(b, 0, x, x)
+    for t, old in zip(tensors, before):
+        assert not torch.equal(t.view(torch.uint8)[page], old)  # the tokens would have shown
+        t.view(torch.uint8)[page] = old
+    assert same_pages(kw, pool)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [6, 40])
+@pytest.mark.parametrize("cu,met,stored", [
+    ([0, 3, 60], True, [(0, 97, 0, 3)]),    # the second sequence passes T
+    ([0, 70, 6], True, []),                 # the first does
+    ([-2, 3, 6], True, [(1, 57, 3, 6)]),    # the first starts below 0
+    ([0, 6, 3], False, [(0, 94, 0, 6)]),    # the second falls back: no row lies between its offsets
+])
+def test_append_with_bad_offsets_writes_only_the_good_sequences(fp8, rows, cu, met, stored):
+    dev = device()
+    pool = ref.filled_pool([100, 60], 2, 16, fp8, 3)
+    kw = pool.to(dev)
+    k, v = ref.normal_rows(rows, 2, 1), ref.normal_rows(rows, 2, 2)
+    plx_kv_append(k.to(dev), v.to(dev), seqlens=pool.seqlens.to(dev),
+                  cu_q=torch.tensor(cu, dtype=I32, device=dev), **kw)
+    reported(met)
+    for b, pos, i0, i1 in stored:
+        pool.put(b, pos, k[i0:i1].double().numpy(), v[i0:i1].double().numpy())
+    assert same_pages(kw, pool)
+
+
+@pytest.mark.parametrize("counts", [[3, 60, 1, 40, 2], [1] * 5, [2, 70, 1, 1, 30, 1, 2, 1, 9]])
+@pytest.mark.parametrize("code,E", [(0x7F, 120), (0xFF, 255), (0x7E, 254)])
+def test_an_e4m3_sequence_that_is_not_finite_leaves_the_others_alone(counts, code, E):
+    """One sequence's pages hold NaN codes or scales that overflow, its queries
+    NaN; every other sequence's results are the same bits as without them."""
+    dev = device()
+    lens = [80 + 37 * b for b in range(len(counts))]
+    pool = ref.filled_pool(lens, 2, 16, True, 3)
+    T, sick = sum(counts), 1
+    q, r = ref.normal_rows(T, 4, 1).to(dev), ref.normal_rows(T, 4, 2, 0.05).to(dev)
+    kw, sl, cu = pool.to(dev), pool.seqlens.to(dev), ends(counts).to(dev)
+    first = [row.contiguous() for row in (q[cu[1:].long() - 1], r[cu[1:].long() - 1])]
+
+    def run():
+        return [plx_prefill_fwd_paged(q, r, seqlens=sl, cu_q=cu, **kw)[0],
+                plx_decode_fwd_paged(*first, seqlens=sl, **kw)]
+
+    clean = run()
+    for pages, scales in ((kw["kpages"], kw["kscale"]), (kw["vpages"], kw["vscale"])):
+        for page in pool.table[sick, :(lens[sick] + 15) // 16].tolist():
+            pages.view(torch.uint8)[page, :, ::3, ::5] = code
+            scales[page, :, ::3] = E
+    rows = slice(sum(counts[:sick]), sum(counts[:sick + 1]))
+    q[rows, :, ::7] = float("nan")
+    dirty = run()
+    plx_check_device_error()
+    others = torch.ones(T, dtype=torch.bool)
+    others[rows] = False
+    bits = lambda x: x.view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(clean[0][others.to(dev)]), bits(dirty[0][others.to(dev)]))
+    keep = [b for b in range(len(counts)) if b != sick]
+    assert torch.equal(bits(clean[1][keep]), bits(dirty[1][keep]))
 
 
 # ------------------------------------------------------------ debug build
