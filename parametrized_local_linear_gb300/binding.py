@@ -28,6 +28,13 @@ PLX_ERR_CUDA = 3
 PLX_ERR_DEVICE_TIMEOUT = 4
 PLX_ERR_BOUNDS = 5
 
+# Current device and raw handle of its current stream. torch.cuda.current_stream
+# builds a Stream object around the handle, which costs 2 us of a 17 us call; it
+# serves where a torch version lacks the inner names.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 # Every symbol the header declares, with its ctypes signature.
 _vp, _i, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
 SIGNATURES = {
@@ -530,11 +537,8 @@ def _packed(t, name, heads, d, dev):
 
 def _launch(fn, dev, stream, args):
     """fn(*args, stream) on the device of the tensors; raises on a bad status."""
-    if torch._C._cuda_getDevice() == dev.index:
-        # The raw handle of the current stream: torch.cuda.current_stream builds
-        # a Stream object around it, which costs 2 us of a 17 us call.
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
-                    else stream.cuda_stream)
+    if _current_device() == dev.index:
+        status = fn(*args, _raw_stream(dev.index) if stream is None else stream.cuda_stream)
         if status != PLX_OK:
             _check(status)
     else:
@@ -548,7 +552,7 @@ def _workspace(workspace, sizer, sizes, stream, dev):
     stream-ordered allocation by the library would give its memory back to the
     driver whenever the GPU idles: 200 us for a call after a synchronize)."""
     if workspace is None:
-        if torch._C._cuda_getDevice() == dev.index:  # the size goes by the device's SM count
+        if _current_device() == dev.index:  # the size goes by the device's SM count
             need = getattr(lib(), sizer)(*sizes)
         else:
             with torch.cuda.device(dev):

@@ -76,3 +76,22 @@ def test_only_one_place_allocates_results():
     from parametrized_local_linear_gb300 import binding
     rest = inspect.getsource(binding).replace(inspect.getsource(binding._empty), "")
     assert "torch.empty" not in rest and "torch.zeros" not in rest
+
+
+@pytest.mark.parametrize("missing", [False, True])
+def test_stream_and_device_names_of_torch_have_a_fallback(monkeypatch, missing):
+    import importlib.util
+
+    from parametrized_local_linear_gb300 import binding
+    if missing:
+        monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("binding_again", binding.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert callable(again._current_device) and callable(again._raw_stream)
+    if missing:
+        assert again._current_device is torch.cuda.current_device
+        monkeypatch.setattr(torch.cuda, "current_stream",
+                            lambda i: type("S", (), dict(cuda_stream=1000 + i)))
+        assert again._raw_stream(3) == 1003
