@@ -15,8 +15,9 @@
 // The bound is memory, for e4m3 with the ALU close behind (70% busy: maxima,
 // unpacking, conversion). GB300: append of 34660 tokens x 8 heads to e4m3 35 us
 // (6.1 TB/s of the 6.8 that a copy reaches; 40 with a maximum over 16 lanes and an
-// exponent for each row by itself), of 16425 tokens to bf16 21.9 us (6.1 TB/s); read back of 195089 e4m3 tokens 180 us (6.7 TB/s); one token a sequence, 64 of them: 2.9
-// us, the launch.
+// exponent for each row by itself), of 16425 tokens to bf16 21.9 us (6.1 TB/s);
+// read back of 195089 e4m3 tokens 180 us (6.7 TB/s); one token a sequence, 64 of
+// them: 2.9 us, the launch.
 #include <string.h>
 
 #include "plx_paged.cuh"
@@ -36,11 +37,13 @@ struct AppendArgs {
   int T;
 };
 
-// Rows a warp handles: one when there are too few warps to fill the GPU twice
-// with more (a decode step's rows: latency), else eight (bytes in flight).
-// GB300, one and eight: append of 34660 tokens x 8 heads to e4m3 79 and 35 us,
-// of 64 tokens 3.0 and 4.3; read back of 195089 e4m3 tokens 335 and 180 us.
-int rows_per_warp(long long rows) { return rows < 16ll * WARPS * sm_count() ? 1 : 8; }
+// Rows a warp handles: one while eight would not give every SM a block (a decode
+// step's rows: latency), else eight (bytes in flight). GB300, one and eight, 8
+// heads, replays of a graph of one call: append to e4m3 of 64 tokens 4.1 and 6.2 us, 600 and
+// 1200 (just below the switch) 6.2 both, 1800 8.2 and 6.2, 4800 14.4 and 8.3, 20000
+// 45 and 25; to bf16 and read back likewise (1800 tokens 8.0 and 6.2, read back
+// 6.2 both; 2400 8.2 and 6.2).
+int rows_per_warp(long long rows) { return rows < 8ll * WARPS * sm_count() ? 1 : 8; }
 
 template <bool FP8, int N>
 __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendArgs a) {
