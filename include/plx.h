@@ -335,6 +335,9 @@ plx_status plx_kv_read(const void *kpages, const void *vpages, const unsigned ch
  * plx_decode_fwd over a paged cache: one new query per sequence, which sees all
  * seqlens[b] keys (its own, appended before, included).
  *   q, r, out : bf16 [B, Hq, d], contiguous. A sequence of length 0 gets zeros.
+ * The cache is read once for every eight query heads of a kv head: with more than
+ * eight, plx_prefill_fwd_paged with one token a sequence reads it once and is
+ * faster (bf16 from 9 heads on, e4m3 from 17).
  * workspace: at least plx_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes on
  * the device, 16-byte aligned, or NULL to allocate them in stream order
  * (cudaMallocAsync / cudaFreeAsync on `stream`). Calls that may overlap on the

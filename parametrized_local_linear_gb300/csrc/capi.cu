@@ -485,25 +485,29 @@ plx_status check_strides(const char *fn, const char *what, long long token, long
 // Which kernels a prefill call launches. The tile kernel's products always have
 // 128 rows; the other reads a sequence's keys once for every eight (token, query
 // head) rows. GB300, GPU time of the latter and of the tile kernel, 64 sequences
-// x 8192 keys x 8 kv heads, 8 rows: bf16 347 and 439 us, e4m3 293 and 576; 16
-// rows: bf16 673 and 442, e4m3 564 and 576. 16 sequences of 500 to 6000 keys, 8
-// rows: 50 and 65, 42 and 78; 16 rows: 69 and 65, 69 and 78. Lengths live on the
+// x 8192 keys x 8 kv heads, 8 rows: bf16 344 and 390 us, e4m3 255 and 490; 16
+// rows: bf16 675 and 393, e4m3 496 and 489. 16 sequences of 500 to 6000 keys, 8
+// rows: 46 and 64, 39 and 70; 16 rows: 67 and 64, 67 and 70. Lengths live on the
 // device, so each kernel can be told to take the sequences of at most, or of more
 // than, some number of rows:
 //   - at most eight rows a sequence on average: those of up to 16 go to the rows
 //     kernel and longer ones to the tile kernel, which is left out if no sequence
 //     can have more than 128 rows. 255 tokens over 500 keys each and a chunk of
-//     512 over 32768: 330 and 341 us (bf16, e4m3) against 2038 and 1998 in the rows
+//     512 over 32768: 327 and 339 us (bf16, e4m3) against 1858 and 1911 in the rows
 //     kernel alone; 64 sequences of 4 tokens over 4096 keys, which need no tile
-//     kernel: 190 and 156 against 186 and 150.
+//     kernel: 193 and 149 against 190 and 144.
 //   - more, up to kMixedRows on average, in kMixedSeqs sequences or more: decodes
 //     with chunks among them. Those of one group of rows go to the rows kernel.
 //     Against the tile kernel alone: 63 tokens and a chunk of 512 over 4096 keys
-//     each 214 and 148 us against 234 and 284, 31 tokens and a chunk of 2048 over
-//     8192 keys 342 and 298 against 367 and 451; 16 chunks of 128 over 2048 keys,
-//     none of them short, 82 and 92 against 79 and 83.
+//     each 217 and 153 us against 231 and 285, 31 tokens and a chunk of 2048 over
+//     8192 keys 350 and 303 against 354 and 454; 16 chunks of 128 over 2048 keys,
+//     none of them short, 83 and 91 against 78 and 84.
 //   - more still, fewer sequences, or more than eight query heads a kv head: the
 //     tile kernel alone (two launches fewer: 12 us of host time).
+// Decode always takes the rows kernel: the tile kernel wants cu_q. Above eight query
+// heads a kv head a call of one token a sequence is faster as a prefill (bf16; e4m3
+// from 16 on): 16 heads 669 and 393 us (e4m3 491 and 488), 32 heads 1318 and 395
+// (970 and 490).
 constexpr int kMixedRows = 256, kMixedSeqs = 8;
 struct PrefillPlan {
   bool rows, tiles;

@@ -16,8 +16,9 @@
 //     and kv head are taken in groups of 4 R; with R = 2 the four consumer
 //     warps are two pairs, each tile going to both warps of a pair, four rows
 //     each (eight columns more in one warp cost registers: 2 CTAs an SM or
-//     spills, 330 us against 269 for 64 x 8192 e4m3 keys and 8 query heads a kv
-//     head). A group is masked causally where it needs to be.
+//     spills, 330 us for 64 x 8192 e4m3 keys and 8 query heads a kv head, where the
+//     pair then took 269 and takes 252 now). A group is masked causally where it
+//     needs to be.
 //   - Pages. The stream is counted in tiles of KT keys, which never cross a
 //     page of a multiple of KT keys (page_size 16 gives two boxes a tile of 32).
 //     A (page, kv head) block is contiguous, so a tile is one 4 KB TMA box of
@@ -44,9 +45,9 @@
 //     match.
 // The bound is memory for whole batches, the latency of a CTA's first loads, its
 // last tile and the combine for small ones. GB300: 64 sequences x 8192 keys x 8
-// kv heads x 2 query heads, e4m3 171 us (6.3 TB/s of the 6.8 that a copy
-// reaches); 8 ragged sequences of 450987 bf16 keys 277 us (6.7 TB/s); one sequence of
-// 1777 keys 9.6 us, of which the combine takes 3.
+// kv heads x 2 query heads, e4m3 172 us (6.3 TB/s of the 6.8 that a copy
+// reaches); 8 ragged sequences of 450987 bf16 keys 277 us (6.7 TB/s); one sequence
+// of 1777 keys 10 us, of which the combine takes 3.
 #include <math.h>
 #include <string.h>
 

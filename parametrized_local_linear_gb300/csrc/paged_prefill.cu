@@ -37,9 +37,11 @@
 // What bounds it: bf16 as prefill_tc.cu, the tile's chain of hand-overs and the
 // shared-memory operands of its products (tensor pipe 63% busy); e4m3 the
 // softmax warps' issue slots, which four converter warps share (57% of all slots
-// used, tensor pipe 54%). GB300, 16 query and 8 kv heads: 2048 tokens over 32768
-// keys bf16 690 us (1543 TFLOP/s), e4m3 807; 12 chunks of 5531 tokens in all over
-// 1000 to 16000 e4m3 keys each 820 us (1050).
+// used, tensor pipe 54%). GB300, 16 query and 8 kv heads, GPU time of replays on
+// the same inputs: 2048 tokens over 32768 keys bf16 687 us (1550 TFLOP/s), e4m3
+// 807; 12 chunks of 5531 tokens in all over 1000 to 16000 e4m3 keys each 812 us
+// (1060). Calls on changing inputs, under the power limit for longer: 756 us (1409)
+// and 828 (1040).
 #include <math.h>
 #include <string.h>
 
@@ -612,6 +614,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
             const int col = 16 * qq + e;
             const uint64_t xx = ffma2(f2(s[col], s[col + 1]), c2, nm2);
             const uint64_t p = f2(fast_exp2(f2lo(xx)), fast_exp2(f2hi(xx)));
+            // The value products take p and p t in bf16, whose roundings average
+            // out over a row's keys (relative error of outputs 0.0023, 0.0017 of
+            // it the output's own rounding). l and sigma are sums of the unrounded
+            // ones; sigma from the rounded ones would serve rows whose weight is on
+            // a few keys better, and costs 1-4% of the time here (unpacking).
             const uint64_t pt = fmul2(p, f2(t[e], t[e + 1]));
             lp[(e >> 1) & 1] = fadd2(lp[(e >> 1) & 1], p);
             sp[(e >> 1) & 1] = fadd2(sp[(e >> 1) & 1], pt);
