@@ -173,16 +173,6 @@ __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory");
 }
 
-// 4-D tiled load (box and swizzle come from the tensor map).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                            int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-
 // The sector of an address into L2.
 __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
@@ -194,22 +184,6 @@ __device__ __forceinline__ uint32_t swz(int row, int c) {
   return (c >> 3) * 2048 + row * 128 + ((((c & 7) ^ (row & 7))) << 4);
 }
 
-// Bytes of w by the selector's nibbles; a nibble's top bit takes the sign.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t prmt(uint32_t w) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "n"(SEL));
-  return r;
-}
-// Codes 0, 2 (even) and 1, 3 (odd) of a word as bf16 pairs, times 2^-120: each
-// byte sign-extended to 16 bits, shifted to put the magnitude over the low
-// exponent and the high mantissa bits; the mask drops the sign's copies.
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-  return (prmt<0xa280>(w) << 4) & 0x87f087f0u;
-}
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
-  return (prmt<0xb391>(w) << 4) & 0x87f087f0u;
-}
 // The two codes of a half word as fp16.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t two) {
   uint32_t h;
@@ -693,8 +667,8 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
               ldsm_x4_t(vb + swz(16 * mt + arow, 2 * cp + acol), w[0], w[1], w[2], w[3]);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                uint32_t af[4] = {codes_even(w[2 * e]), codes_odd(w[2 * e]), codes_even(w[2 * e + 1]),
-                                  codes_odd(w[2 * e + 1])};
+                uint32_t af[4] = {codes_bf16<0xa280>(w[2 * e]), codes_bf16<0xb391>(w[2 * e]),
+                                  codes_bf16<0xa280>(w[2 * e + 1]), codes_bf16<0xb391>(w[2 * e + 1])};
                 if constexpr (decltype(extra)::value) {
 #pragma unroll
                   for (int i = 0; i < 4; ++i) af[i] = mul_bf16x2(af[i], up[i >> 1]);

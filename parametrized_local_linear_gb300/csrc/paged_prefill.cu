@@ -367,30 +367,12 @@ __device__ __noinline__ void drain_ring(uint64_t *full, int issued, int stages) 
     mbar_wait_drain(smem_u32(&full[g % stages]), (g / stages) & 1);
 }
 
-// 4-D tiled load (box and swizzle come from the tensor map).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                            int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-
 // The box of a tiled load into L2.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y), "r"(z)
                : "memory");
-}
-
-// Codes 0, 1 (lo) and 2, 3 (hi) of a word as bf16 pairs, times 2^-120.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "n"(SEL));
-  return (r << 4) & 0x87f087f0u;
 }
 
 template <bool FP8>

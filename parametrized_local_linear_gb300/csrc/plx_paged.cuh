@@ -89,6 +89,18 @@ __device__ __forceinline__ uint32_t float2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two codes of a word as a bf16 pair, times 2^-120 (subnormals included): the
+// selector's nibbles take each byte sign-extended to 16 bits, shifted to put the
+// magnitude over the low exponent and the high mantissa bits; the mask drops the
+// sign's copies. 0x9180 takes codes 0, 1; 0xb3a2 codes 2, 3; 0xa280 codes 0, 2;
+// 0xb391 codes 1, 3.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "n"(SEL));
+  return (r << 4) & 0x87f087f0u;
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
@@ -96,5 +108,15 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
 }
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 4-D tiled load (box and swizzle come from the tensor map).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 
 }  // namespace plx
