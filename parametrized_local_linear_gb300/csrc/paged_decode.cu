@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           if (active) tma_load_3d(smem_u32(smem + st * 2 * TILE) + at, map, 0, 0, z, bar);
         }
       }
-      if (lane == 0) {
+      if ((kStopsAtOnce || !ok) && lane == 0) {
         // The warp's own copies (tiles g - NST .. g - 1) land before it leaves:
         // after an abort no consumer waits for them.
         for (int t = max(0, g - NST); t < g; ++t)
@@ -443,8 +443,10 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           ++g;
         }
       }
-      for (int t = max(0, g - NST); t < g; ++t)  // as above
-        mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
+      if (kStopsAtOnce || !ok) {
+        for (int t = max(0, g - NST); t < g; ++t)  // as above
+          mbar_wait_drain(smem_u32(&full[t % NST]), (t / NST) & 1);
+      }
     }
     return;
   }

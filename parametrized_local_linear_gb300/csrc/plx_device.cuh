@@ -38,6 +38,13 @@ constexpr unsigned kErrLayout = 8u;
 #else
 #define PLX_IN_BOUNDS(cond, ab) true
 #endif
+// Whether a check may stop a CTA at once, while other warps' copies are in flight.
+// (A timed-out wait stops it seconds after they landed.)
+#ifdef PLX_DEBUG_BOUNDS
+constexpr bool kStopsAtOnce = true;
+#else
+constexpr bool kStopsAtOnce = false;
+#endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
