@@ -39,10 +39,10 @@ struct AppendArgs {
 
 // Rows a warp handles: one while eight would not give every SM a block (a decode
 // step's rows: latency), else eight (bytes in flight). GB300, one and eight, 8
-// heads, replays of a graph of one call: append to e4m3 of 64 tokens 4.1 and 6.2 us, 600 and
-// 1200 (just below the switch) 6.2 both, 1800 8.2 and 6.2, 4800 14.4 and 8.3, 20000
-// 45 and 25; to bf16 and read back likewise (1800 tokens 8.0 and 6.2, read back
-// 6.2 both; 2400 8.2 and 6.2).
+// heads, replays of a graph of one call: append to e4m3 of 64 tokens 4.1 and 6.2
+// us, 600 and 1200 (just below the switch) 6.2 both, 1800 8.2 and 6.2, 4800 14.4
+// and 8.3, 20000 45 and 25; to bf16 and read back likewise (1800 tokens 8.0 and
+// 6.2, read back 6.2 both; 2400 8.2 and 6.2).
 int rows_per_warp(long long rows) { return rows < 8ll * WARPS * sm_count() ? 1 : 8; }
 
 template <bool FP8, int N>

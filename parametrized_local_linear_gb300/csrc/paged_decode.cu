@@ -38,11 +38,11 @@
 //     (sign, then the 7 magnitude bits over exponent and mantissa) are its
 //     value times 2^-120, exactly, subnormals included, in three integer
 //     instructions for two codes; the weights carry 2^64 and the records the
-//     other 2^56. Rows with E above 127 (values above 448) would take a weight
-//     out of bf16's range: the rest of their scale goes onto their codes, in a
-//     second copy of the value products that a tile with such a row takes. ldmatrix moves pairs of bytes: dims pair up differently
-//     than for bf16, and the query fragments and output rows are permuted to
-//     match.
+//     other 2^56. Rows with E above 127 (values above 448) would take a weight out
+//     of bf16's range: the rest of their scale goes onto their codes, in a second
+//     copy of the value products that a tile with such a row takes. ldmatrix moves
+//     pairs of bytes: dims pair up differently than for bf16, and the query
+//     fragments and output rows are permuted to match.
 // The bound is memory for whole batches, the latency of a CTA's first loads, its
 // last tile and the combine for small ones. GB300: 64 sequences x 8192 keys x 8
 // kv heads x 2 query heads, e4m3 172 us (6.3 TB/s of the 6.8 that a copy

@@ -92,6 +92,46 @@ def test_an_empty_workspace_is_refused():
         plx_prefill_fwd_paged(q, q, cu_q=ends([1, 1]).to(dev), **kw)
 
 
+# ------------------------------------------------------------ eight rows a warp
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_append_and_read_back_with_eight_rows_a_warp(fp8, heads_first):
+    """Enough rows for eight a warp: chunks that start, end and change sequence
+    inside a warp's eight, padding in front, rows behind, a short last group."""
+    dev = device()
+    lens, counts, behind = [1500, 0, 3, 901, 7, 300], [1301, 0, 9, 601, 1, 2], 5
+    pool = ref.Pool(lens, 8, 32, fp8, 7)
+    T = sum(counts) + behind
+    assert T % 8 and T * 8 > 8 * 8 * 152
+    k, v = ref.normal_rows(T, 8, 1), ref.normal_rows(T, 8, 2, 30.0)
+    kw = pool.to(dev)
+    kd, vd = (x.transpose(0, 1).contiguous().to(dev).transpose(0, 1) if heads_first else x.to(dev) for x in (k, v))
+    plx_kv_append(kd, vd, seqlens=pool.seqlens.to(dev), cu_q=ends(counts).to(dev), **kw)
+    plx_check_device_error()
+    at = 0
+    for b, n in enumerate(counts):
+        skip = max(0, n - lens[b])  # padding
+        if n > skip:
+            pool.put(b, lens[b] - n + skip, k[at + skip:at + n].double().numpy(),
+                     v[at + skip:at + n].double().numpy())
+        at += n
+    same = lambda a, b: torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    assert same(kw["kpages"], pool.k) and same(kw["vpages"], pool.v)
+    assert not fp8 or same(kw["kscale"], pool.ks) and same(kw["vscale"], pool.vs)
+    for b, n in enumerate(lens):
+        if n:
+            pool.put(b, 0, ref.normal_rows(n, 8, b + 10).double().numpy(), ref.normal_rows(n, 8, b + 20).double().numpy())
+    kw, take = pool.to(dev), [1499, 0, 3, 900, 0, 299]
+    T = sum(take) + behind
+    outs = [torch.full((T, 8, 128), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    plx_kv_read(**kw, cu_k=ends(take).to(dev), T=T, k=outs[0], v=outs[1])
+    plx_check_device_error()
+    want = [pool.get(b, n) for b, n in enumerate(take)]
+    for i, got in enumerate(outs):
+        w = np.concatenate([x[i] for x in want] + [np.full((behind, 8, 128), 7.0)])
+        assert np.array_equal(got.double().cpu().numpy(), w)
+
+
 # ------------------------------------------------------------ bad metadata
 def same_pages(kw, pool):
     pairs = [(kw["kpages"], pool.k), (kw["vpages"], pool.v)]
