@@ -371,6 +371,157 @@ plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_toke
                                  size_t workspace_bytes, void *stream);
 size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
 
+/*
+ * Decode for sequences that share prefixes (several continuations of one prompt,
+ * users behind one instruction): plx_decode_fwd_paged whose sequences come in
+ * groups, the first keys of a group's sequences being the same. They are read once
+ * for all of them, through the pages of the group's first sequence.
+ *   cu_g        : int32 [ngroups + 1] on the device, non-decreasing from cu_g[0] =
+ *                 0: group g is the sequences cu_g[g] .. cu_g[g + 1] - 1 (it may be
+ *                 empty). Sequences behind cu_g[ngroups] are in no group.
+ *   prefix_lens : int32 [ngroups] on the device: keys that the group's sequences
+ *                 share (below zero counts as zero); not more than the first one's
+ *                 seqlens. A sequence with fewer keys, or none, sees those it has.
+ * Position p >= the prefix's length of a sequence is in its own pages; of its block
+ * table, entries in front of the one with the prefix's length are not read (but for
+ * the group's first sequence). The result is plx_decode_fwd_paged's up to rounding:
+ * the weights of a sequence meet in one softmax. A prefix that is longer than the
+ * group's first sequence is taken for none, and ends of groups that decrease or pass
+ * B as no group; plx_check_device_error reports PLX_ERR_INVALID_ARG for both.
+ * ngroups >= 1. workspace as for plx_decode_fwd_paged, of
+ * plx_decode_shared_workspace_bytes(B, Hq, Hkv, d).
+ */
+plx_status plx_decode_fwd_shared(const void *q, const void *r, const void *kpages,
+                                 const void *vpages, const unsigned char *kscale,
+                                 const unsigned char *vscale, const int *block_table,
+                                 const int *seqlens, const int *cu_g, const int *prefix_lens,
+                                 void *out, int ngroups, int B, int Hq, int Hkv, int d,
+                                 int num_pages, int page_size, int max_pages, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+size_t plx_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d);
+
+/*
+ * Between two steps of a server: the rows of a paged cache's block table take over
+ * pages from each other (forks, a reordered batch), are cut, grown or emptied.
+ * Every page has a reference count, 0 for a free one.
+ *   page_refs : int32 [num_pages] on the device: the times that rows use each page
+ *               (more, for pages that something else holds too)
+ *   src       : int32 [B] on the device: the row whose tokens row b takes over, or
+ *               -1 for none; the same row may be taken by many. NULL: its own
+ *   lens      : int32 [B] on the device: the tokens that row b has afterwards (below
+ *               zero counts as zero), at most max_pages * page_size
+ * Row b of block_table_out holds the first kept = min(lens[b], seqlens[src[b]])
+ * tokens of old row src[b], all rows as they were before the call, and then pages
+ * for the others, whose slots are for plx_kv_append to fill:
+ *   - whole pages among the kept tokens are shared: one reference more;
+ *   - a page of which only the first slots are kept stays with the first row that
+ *     keeps it so if no row has the whole of it, and is copied for every other (the
+ *     kept slots; the others of the copy are left as they were), so that rows write
+ *     to pages of their own only;
+ *   - what rows no longer use loses its references, and can be taken in this call;
+ *   - fresh pages, for a copy and for growing, are the lowest free ones, in the
+ *     order of the rows. Once a row needs more than are left, neither it nor any
+ *     row behind it gets any: it ends with its kept tokens, without those of a page
+ *     that it would have had to copy. seqlens_out[b] < lens[b] says so.
+ * Written: block_table_out [B, max_pages] (the entries of a row's pages; those
+ * behind them are left as they were), seqlens_out [B], page_refs_out [num_pages],
+ * and the copied pages. All three may be the inputs (in place), or none of them.
+ * A row whose src or lens is out of range stays as it was; pages that do not exist
+ * are kept as entries and not followed; plx_check_device_error reports
+ * PLX_ERR_INVALID_ARG for each. Counts that do not cover the rows' use give
+ * undefined tables, but nothing outside the arguments is read or written.
+ * workspace: at least plx_kv_update_workspace_bytes(B, num_pages, max_pages) bytes
+ * on the device, 16-byte aligned, or NULL to allocate them in stream order. Calls
+ * that may overlap on the GPU must not share one.
+ */
+plx_status plx_kv_update(void *kpages, void *vpages, unsigned char *kscale, unsigned char *vscale,
+                         const int *block_table, const int *seqlens, const int *page_refs,
+                         const int *src, const int *lens, int *block_table_out, int *seqlens_out,
+                         int *page_refs_out, int B, int Hkv, int d, int num_pages, int page_size,
+                         int max_pages, void *workspace, size_t workspace_bytes, void *stream);
+size_t plx_kv_update_workspace_bytes(int B, int num_pages, int max_pages);
+
+/*
+ * Compaction of a paged cache: with U pages in use (page_refs above zero), those
+ * with numbers from U on move to the free ones below U, in ascending order, so that
+ * the first U pages are the used ones and the rest of the pool is free.
+ *   page_map : int32 [num_pages] on the device, written: the new number of every
+ *              used page, -1 for a free one (for what holds pages beside the table)
+ *   used     : int32 [1] on the device, written: U
+ * block_table_out and page_refs_out as for plx_kv_update (both in place, or
+ * neither); lengths do not change. Moved pages are copied whole; what they leave
+ * stays in the pool's free part. A page in use whose count says free stays an entry
+ * as it is and is reported as PLX_ERR_INVALID_ARG by plx_check_device_error, as is a
+ * page that does not exist. workspace as for plx_kv_update, of
+ * plx_kv_compact_workspace_bytes(num_pages).
+ */
+plx_status plx_kv_compact(void *kpages, void *vpages, unsigned char *kscale, unsigned char *vscale,
+                          const int *block_table, const int *seqlens, const int *page_refs,
+                          int *block_table_out, int *page_refs_out, int *page_map, int *used, int B,
+                          int Hkv, int d, int num_pages, int page_size, int max_pages,
+                          void *workspace, size_t workspace_bytes, void *stream);
+size_t plx_kv_compact_workspace_bytes(int num_pages);
+
+/*
+ * Rotary positions: pairs of the first rotary_dim = R values of every row of q, k and
+ * r are turned by the angle position * inv_freq[i], i < R / 2:
+ *   y0 = scale (x0 cos a - x1 sin a),   y1 = scale (x1 cos a + x0 sin a)
+ * in fp32 from angles that are exact to 2^-33 of a turn, rounded once. The pairs are
+ * (x[i], x[i + R / 2]), or with interleaved != 0 (x[2 i], x[2 i + 1]). Values from R
+ * on are copied. plx_rotary_bwd takes the gradients of the outputs and gives those of
+ * the inputs (the angles negated, the same scale). The probe r meets the rotated keys:
+ * rotated like q, r.k depends on the distance of the positions, as q.k does; without
+ * r (NULL), it is left to the caller.
+ *   q, k, r : [B, H, L, d] in any order of the three outer dimensions, H = Hq for q
+ *             and r, Hkv for k; dtype PLX_BF16 or PLX_F32; each may be NULL, not all.
+ *             Packed rows [T, H, d] are B = 1, L = T.
+ *   q_out.. : where the results go, NULL with its input. An output is its input (in
+ *             place, the same strides) or overlaps no input.
+ *   strides : 18 numbers on the HOST, in elements: those of the sequence, the token and
+ *             the head for q, k, r, q_out, k_out, r_out in turn; multiples of 8, at
+ *             least d where the dimension is larger than 1.
+ *   positions : int32 [B, L] on the device, or NULL
+ *   seqlens   : with positions NULL, B = 1: int32 [nseq] on the device, and cu_q int32
+ *               [nseq + 1] or NULL for one token each: rows are new tokens of nseq
+ *               sequences with the positions of plx_kv_append; padding rows and rows
+ *               behind the last sequence are left as they were. Both NULL: row t of
+ *               each sequence has position t.
+ *   inv_freq  : fp64 [R / 2] on the device, finite, radians a position
+ * d is 64 or 128, R even, 2 .. d; pointers 16-byte aligned.
+ */
+#define PLX_BF16 0
+#define PLX_F32 1
+plx_status plx_rotary_fwd(const void *q, const void *k, const void *r, void *q_out, void *k_out,
+                          void *r_out, const long long *strides, const int *positions,
+                          const int *seqlens, const int *cu_q, const double *inv_freq, double scale,
+                          int nseq, int B, int L, int Hq, int Hkv, int d, int rotary_dim,
+                          int interleaved, int dtype, void *stream);
+plx_status plx_rotary_bwd(const void *dq, const void *dk, const void *dr, void *dq_out,
+                          void *dk_out, void *dr_out, const long long *strides,
+                          const int *positions, const int *seqlens, const int *cu_q,
+                          const double *inv_freq, double scale, int nseq, int B, int L, int Hq,
+                          int Hkv, int d, int rotary_dim, int interleaved, int dtype, void *stream);
+
+/*
+ * The frequencies of plx_rotary_fwd, on the host: inv_freq[i] = base^(-2 i / R), i <
+ * R / 2, fp64, and *scale. For contexts `factor` times as long as those trained on:
+ *   PLX_ROTARY_PLAIN    as they are; scale 1
+ *   PLX_ROTARY_LINEAR   divided by factor; scale 1
+ *   PLX_ROTARY_BASE     base * factor^(R / (R - 2)) in place of base (the slowest pair
+ *                       is then linear's, the fastest plain's; R > 2); scale 1
+ *   PLX_ROTARY_BY_PARTS with n = original_len * inv_freq / (2 pi) turns over the
+ *                       trained length: plain for n >= beta_fast, linear for n <=
+ *                       beta_slow, between them mixed by (n - beta_slow) / (beta_fast -
+ *                       beta_slow); scale 0.1 ln(factor) + 1 for factor > 1
+ * base > 0, factor >= 1; by parts also original_len > 0 and beta_fast > beta_slow.
+ */
+#define PLX_ROTARY_PLAIN 0
+#define PLX_ROTARY_LINEAR 1
+#define PLX_ROTARY_BASE 2
+#define PLX_ROTARY_BY_PARTS 3
+plx_status plx_rotary_freqs(double *inv_freq, double *scale, int rotary_dim, double base, int kind,
+                            double factor, double original_len, double beta_slow, double beta_fast);
+
 /* Synchronises `stream`, then reads and clears the device error word.
  * PLX_ERR_DEVICE_TIMEOUT if a bounded wait ran out since the last check,
  * PLX_ERR_INVALID_ARG if a kernel found its device-side inputs out of range

@@ -58,6 +58,15 @@ SIGNATURES = {
     "plx_prefill_fwd_paged": (_i, [_vp] * 2 + [_ll] * 2 + [_vp] * 8 + [_ll] * 2 + [_vp] + [_i] * 8
                               + [_vp, _sz, _vp]),
     "plx_prefill_paged_workspace_bytes": (_sz, [_i] * 5),
+    "plx_decode_fwd_shared": (_i, [_vp] * 11 + [_i] * 8 + [_vp, _sz, _vp]),
+    "plx_decode_shared_workspace_bytes": (_sz, [_i] * 4),
+    "plx_kv_update": (_i, [_vp] * 12 + [_i] * 6 + [_vp, _sz, _vp]),
+    "plx_kv_update_workspace_bytes": (_sz, [_i] * 3),
+    "plx_kv_compact": (_i, [_vp] * 11 + [_i] * 6 + [_vp, _sz, _vp]),
+    "plx_kv_compact_workspace_bytes": (_sz, [_i]),
+    "plx_rotary_fwd": (_i, [_vp] * 11 + [ctypes.c_double] + [_i] * 9 + [_vp]),
+    "plx_rotary_bwd": (_i, [_vp] * 11 + [ctypes.c_double] + [_i] * 9 + [_vp]),
+    "plx_rotary_freqs": (_i, [_vp] * 2 + [_i, ctypes.c_double, _i] + [ctypes.c_double] * 4),
     "plx_check_device_error": (_i, [_vp]),
     "plx_debug_timeout_probe": (_i, [_ll, _vp]),
     "plx_status_string": (ctypes.c_char_p, [_i]),
@@ -687,6 +696,235 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
              out.data_ptr(), *out_strides, lse.data_ptr() if lse is not None else None, T, B, Hq, Hkv,
              d, n, page, width, ws_ptr, ws_bytes))
     return out, lse
+
+
+def plx_decode_fwd_shared(q, r, kpages, vpages, block_table, seqlens, cu_g, prefix_lens, kscale=None,
+                          vscale=None, out=None, workspace=None, stream=None):
+    """Decode over a paged KV cache for groups of sequences that share their first
+    keys (see include/plx.h): q, r bf16 [B, Hq, d]; group g is the sequences
+    cu_g[g] .. cu_g[g + 1] - 1, whose first prefix_lens[g] keys are read once, through
+    the first one's pages. Returns out."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [B, Hq, d], got shape {tuple(q.shape)}")
+    for name, t in (("seqlens", seqlens), ("cu_g", cu_g), ("prefix_lens", prefix_lens)):
+        _given(name, t)
+    dev = q.device
+    B, Hq, d = shape = q.shape
+    if B != block_table.shape[0] or d != kpages.shape[-1]:
+        raise ValueError(f"q must be ({block_table.shape[0]}, {Hq}, {kpages.shape[-1]}), got shape "
+                         f"{tuple(shape)}")
+    if prefix_lens.dim() != 1 or prefix_lens.shape[0] < 1:
+        raise ValueError(f"prefix_lens must be [ngroups], got shape {tuple(prefix_lens.shape)}")
+    groups = prefix_lens.shape[0]
+    for name, t in (("r", r), ("out", out)):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
+    if cu_g.shape != (groups + 1,):
+        raise ValueError(f"cu_g must have shape ({groups + 1},), got {tuple(cu_g.shape)}")
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
+                                               dev)
+    _like(q, "q", torch.bfloat16, shape, dev)
+    _like(r, "r", torch.bfloat16, shape, dev)
+    _like(cu_g, "cu_g", torch.int32, (groups + 1,), dev)
+    _like(prefix_lens, "prefix_lens", torch.int32, (groups,), dev)
+    if out is None:
+        out = _empty(shape, torch.bfloat16, dev, stream)
+    else:
+        _like(out, "out", torch.bfloat16, shape, dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_decode_shared_workspace_bytes",
+                                      (B, Hq, Hkv, d), stream, dev)
+    _launch(lib().plx_decode_fwd_shared, dev, stream,
+            (q.data_ptr(), r.data_ptr(), *ptrs, seqlens.data_ptr(), cu_g.data_ptr(),
+             prefix_lens.data_ptr(), out.data_ptr(), groups, B, Hq, Hkv, d, n, page, width, ws_ptr,
+             ws_bytes))
+    return out
+
+
+def plx_kv_update(kpages, vpages, block_table, seqlens, page_refs, lens, src=None, kscale=None,
+                  vscale=None, block_table_out=None, seqlens_out=None, page_refs_out=None,
+                  workspace=None, stream=None):
+    """Forks, reorders, cuts, grows and empties the rows of a paged KV cache's block
+    table (see include/plx.h): row b takes over the first min(lens[b], its length)
+    tokens of old row src[b] (its own without ``src``, none for -1) and gets pages for
+    lens[b]. int32 tensors: seqlens, lens, src [B], page_refs [num_pages]. In place, or
+    into all three of ``block_table_out``, ``seqlens_out``, ``page_refs_out``. Returns
+    (block_table, seqlens, page_refs) as they are afterwards."""
+    outs = (block_table_out, seqlens_out, page_refs_out)
+    for name, t in (("seqlens", seqlens), ("page_refs", page_refs), ("lens", lens)):
+        _given(name, t)
+    dev = kpages.device
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
+                                               dev)
+    if any(t is None for t in outs):
+        if not all(t is None for t in outs):
+            raise ValueError("block_table_out, seqlens_out and page_refs_out must be given all or none")
+        outs = block_table, seqlens, page_refs
+    _like(page_refs, "page_refs", torch.int32, (n,), dev)
+    _like(lens, "lens", torch.int32, (B,), dev)
+    if src is not None:
+        _like(src, "src", torch.int32, (B,), dev)
+    _like(outs[0], "block_table_out", torch.int32, (B, width), dev)
+    _like(outs[1], "seqlens_out", torch.int32, (B,), dev)
+    _like(outs[2], "page_refs_out", torch.int32, (n,), dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_kv_update_workspace_bytes", (B, n, width),
+                                      stream, dev)
+    _launch(lib().plx_kv_update, dev, stream,
+            (*ptrs, seqlens.data_ptr(), page_refs.data_ptr(),
+             src.data_ptr() if src is not None else None, lens.data_ptr(),
+             *(t.data_ptr() for t in outs), B, Hkv, d, n, page, width, ws_ptr, ws_bytes))
+    return outs
+
+
+def plx_kv_compact(kpages, vpages, block_table, seqlens, page_refs, kscale=None, vscale=None,
+                   block_table_out=None, page_refs_out=None, page_map=None, used=None,
+                   workspace=None, stream=None):
+    """Moves the used pages of a paged KV cache to the front of the pool (see
+    include/plx.h), in place or into ``block_table_out`` and ``page_refs_out``. Returns
+    (block_table, page_refs, page_map, used): ``page_map`` int32 [num_pages] has every
+    used page's new number, -1 for a free one, ``used`` int32 [1] how many are used."""
+    outs = (block_table_out, page_refs_out)
+    for name, t in (("seqlens", seqlens), ("page_refs", page_refs)):
+        _given(name, t)
+    dev = kpages.device
+    ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
+                                               dev)
+    if any(t is None for t in outs):
+        if not all(t is None for t in outs):
+            raise ValueError("block_table_out and page_refs_out must be given both or neither")
+        outs = block_table, page_refs
+    _like(page_refs, "page_refs", torch.int32, (n,), dev)
+    _like(outs[0], "block_table_out", torch.int32, (B, width), dev)
+    _like(outs[1], "page_refs_out", torch.int32, (n,), dev)
+    if page_map is None:
+        page_map = _empty((n,), torch.int32, dev, stream)
+    else:
+        _like(page_map, "page_map", torch.int32, (n,), dev)
+    if used is None:
+        used = _empty((1,), torch.int32, dev, stream)
+    else:
+        _like(used, "used", torch.int32, (1,), dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_kv_compact_workspace_bytes", (n,), stream, dev)
+    _launch(lib().plx_kv_compact, dev, stream,
+            (*ptrs, seqlens.data_ptr(), page_refs.data_ptr(), *(t.data_ptr() for t in outs),
+             page_map.data_ptr(), used.data_ptr(), B, Hkv, d, n, page, width, ws_ptr, ws_bytes))
+    return (*outs, page_map, used)
+
+
+_ROTARY_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_ROTARY_KINDS = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def plx_rotary_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=0,
+                     beta_slow=1.0, beta_fast=32.0, device=None):
+    """Frequencies of rotary positions (see include/plx.h), for a context ``factor``
+    times as long with ``scaling`` "linear", "base" or "parts". Returns (inv_freq fp64
+    [rotary_dim / 2] on ``device``, scale)."""
+    if scaling not in _ROTARY_KINDS:
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
+    freqs, scale = (ctypes.c_double * (max(int(rotary_dim), 2) // 2))(), ctypes.c_double()
+    _check(lib().plx_rotary_freqs(ctypes.addressof(freqs), ctypes.addressof(scale), int(rotary_dim), base,
+                                  _ROTARY_KINDS[scaling], factor, original_len, beta_slow, beta_fast))
+    return torch.tensor(list(freqs), dtype=torch.float64, device=device), scale.value
+
+
+def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale, outs, stream):
+    given = [(name, t, o) for name, t, o in zip("qkr", (q, k, r), outs) if t is not None]
+    if not given:
+        raise ValueError("q, k and r are all None")
+    x = given[0][1]
+    dev, dtype, dims = x.device, x.dtype, x.dim()
+    if dtype not in _ROTARY_DTYPES:
+        raise TypeError(f"{given[0][0]} must be torch.bfloat16 or torch.float32, got {dtype}")
+    if dims not in (3, 4):
+        raise ValueError(f"{given[0][0]} must be [T, H, d] or [B, H, L, d], got shape {tuple(x.shape)}")
+    packed = dims == 3
+    B, L, d = (1, x.shape[0], x.shape[2]) if packed else (x.shape[0], x.shape[2], x.shape[3])
+    heads, results = {}, [None] * 3
+    strides, ptrs = [0] * 18, [None] * 6
+    for name, t, o in given:
+        H = t.shape[1] if t.dim() == dims else 0
+        shape = (L, H, d) if packed else (B, H, L, d)
+        if t.shape != shape or heads.setdefault(name == "k", H) != H:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with {given[0][0]}'s "
+                             f"{tuple(x.shape)}")
+        if o is not None and o.shape != shape:
+            raise ValueError(f"{name}_out has shape {tuple(o.shape)}, expected {tuple(shape)}")
+    for name, t, o in given:
+        at = "qkr".index(name)
+        if dev.type == "cuda" and o is None:
+            o = _empty(t.shape, dtype, dev, stream)
+        for what, y, place in ((name, t, at), (name + "_out", o, at + 3)):
+            if dev.type != "cuda" or y.get_device() != dev.index:
+                raise ValueError(f"{what} must be a CUDA tensor on the device of {given[0][0]} ({dev})")
+            if y.dtype is not dtype:
+                raise TypeError(f"{what} must be {dtype}, got {y.dtype}")
+            st = y.stride()
+            if st[-1] != 1 and y.numel() > 0:
+                raise ValueError(f"{what} must have its last dimension contiguous")
+            # (sequence, token, head)
+            strides[3 * place:3 * place + 3] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
+            ptrs[place] = y.data_ptr()
+        results[at] = o
+    half = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    _like(inv_freq, "inv_freq", torch.float64, (half,), dev)
+    if positions is not None:
+        if seqlens is not None or cu_q is not None:
+            raise ValueError("positions and seqlens / cu_q exclude each other")
+        _like(positions, "positions", torch.int32, (L,) if packed else (B, L), dev)
+    elif seqlens is None and packed:
+        raise ValueError("packed rows need positions, or seqlens (and cu_q)")
+    nseq = 0
+    if seqlens is not None:
+        if not packed:
+            raise ValueError("seqlens goes with packed rows [T, H, d]")
+        nseq = seqlens.shape[0] if seqlens.dim() == 1 else 0
+        _like(seqlens, "seqlens", torch.int32, (nseq,), dev)
+        if cu_q is not None:
+            _like(cu_q, "cu_q", torch.int32, (nseq + 1,), dev)
+    elif cu_q is not None:
+        raise ValueError("cu_q without seqlens")
+    if B > 0 and L > 0:
+        _launch(fn, dev, stream,
+                (*ptrs, (_ll * 18)(*strides),
+                 positions.data_ptr() if positions is not None else None,
+                 seqlens.data_ptr() if seqlens is not None else None,
+                 cu_q.data_ptr() if cu_q is not None else None, inv_freq.data_ptr(), scale, nseq, B,
+                 L, heads.get(False, 1), heads.get(True, 1), d, 2 * half, int(bool(interleaved)),
+                 _ROTARY_DTYPES[dtype]))
+    return tuple(results)
+
+
+def plx_rotary_fwd(q, k, inv_freq, r=None, positions=None, seqlens=None, cu_q=None,
+                   interleaved=False, scale=1.0, q_out=None, k_out=None, r_out=None, stream=None):
+    """Rotary positions (see include/plx.h): q, r [B, Hq, L, d] and k [B, Hkv, L, d], or
+    packed rows [T, H, d], bf16 or fp32 with any strides of the outer dimensions; the
+    first 2 * len(inv_freq) values of each row are turned. Positions: int32
+    ``positions`` [B, L] or [T], or those of plx_kv_append's new tokens from ``seqlens``
+    and ``cu_q`` (packed), or 0 .. L - 1. q, k or r may be None; ``q_out=q`` works in
+    place. Returns (q, k, r) turned."""
+    return _rotary(lib().plx_rotary_fwd, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved,
+                   scale, (q_out, k_out, r_out), stream)
+
+
+def plx_rotary_bwd(dq, dk, inv_freq, dr=None, positions=None, seqlens=None, cu_q=None,
+                   interleaved=False, scale=1.0, dq_out=None, dk_out=None, dr_out=None,
+                   stream=None):
+    """Backward of plx_rotary_fwd (see include/plx.h): from the gradients of its outputs
+    those of its inputs, with its other arguments. Returns (dq, dk, dr)."""
+    return _rotary(lib().plx_rotary_bwd, dq, dk, dr, inv_freq, positions, seqlens, cu_q, interleaved,
+                   scale, (dq_out, dk_out, dr_out), stream)
+
+
+def plx_decode_shared_workspace_bytes(B, Hq, Hkv, d) -> int:
+    return int(lib().plx_decode_shared_workspace_bytes(B, Hq, Hkv, d))
+
+
+def plx_kv_update_workspace_bytes(B, num_pages, max_pages) -> int:
+    return int(lib().plx_kv_update_workspace_bytes(B, num_pages, max_pages))
+
+
+def plx_kv_compact_workspace_bytes(num_pages) -> int:
+    return int(lib().plx_kv_compact_workspace_bytes(num_pages))
 
 
 def plx_decode_paged_workspace_bytes(B, Hq, Hkv, d) -> int:

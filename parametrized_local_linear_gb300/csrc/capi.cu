@@ -1,14 +1,15 @@
 // C ABI of libplx.so: argument validation, per-device set-up, the decode
 // workspace, device error reporting. The operations themselves are defined
 // in include/plx.h; the kernels live in prefill_tc.cu, prefill_bwd.cu,
-// prefill_f32.cu, proj.cu, decode.cu, and for the paged cache in paged_cache.cu,
-// paged_decode.cu and paged_prefill.cu.
+// prefill_f32.cu, proj.cu, decode.cu, rotary.cu, and for the paged cache in
+// paged_cache.cu, paged_decode.cu, paged_prefill.cu and paged_moves.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdarg.h>
 #include <stdio.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "../../include/plx.h"
@@ -680,6 +681,231 @@ plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_toke
                                     x.rows ? x.p.most : 0, static_cast<char *>(ws) + x.rows_bytes, st);
     return e;
   });
+}
+
+size_t plx_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  const size_t rows = plx_decode_paged_workspace_bytes(B, Hq, Hkv, d);
+  return rows == 0 ? 0 : (rows + 255) / 256 * 256 + plx::shared_parts_bytes(B, Hq, Hkv);
+}
+
+plx_status plx_decode_fwd_shared(const void *q, const void *r, const void *kpages,
+                                 const void *vpages, const unsigned char *kscale,
+                                 const unsigned char *vscale, const int *block_table,
+                                 const int *seqlens, const int *cu_g, const int *prefix_lens,
+                                 void *out, int ngroups, int B, int Hq, int Hkv, int d,
+                                 int num_pages, int page_size, int max_pages, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  const char *fn = "plx_decode_fwd_shared";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  s = check_heads(fn, Hq, Hkv);
+  if (s) return s;
+  if (!q || !r || !out || !seqlens) return fail(PLX_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (ngroups < 1) return fail(PLX_ERR_INVALID_ARG, "%s: ngroups (%d) must be >= 1", fn, ngroups);
+  if (!cu_g || !prefix_lens) return fail(PLX_ERR_INVALID_ARG, "%s: null cu_g or prefix_lens", fn);
+  if (!aligned16(q) || !aligned16(r) || !aligned16(out))
+    return fail(PLX_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", fn);
+  if (static_cast<long long>(B) * Hq > (1LL << 24) || Hkv > 65535)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: B * Hq must be <= 2^24 and Hkv <= 65535", fn);
+  const size_t rows = (plx_decode_paged_workspace_bytes(B, Hq, Hkv, d) + 255) / 256 * 256;
+  const size_t need = plx_decode_shared_workspace_bytes(B, Hq, Hkv, d);
+  if (workspace && workspace_bytes < need)
+    return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  c.err = plx::device_error_word();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const plx::SharedGroups g = {cu_g, prefix_lens, ngroups};
+  return with_workspace(fn, workspace, need, st, [&](void *ws) {
+    const plx::SharedParts parts = plx::shared_parts(static_cast<char *>(ws) + rows, B, Hq, Hkv);
+    cudaError_t e = plx::launch_shared_rows(c, g, q, r, seqlens, Hq, ws, st);
+    if (e == cudaSuccess) e = plx::launch_shared_prefix(c, g, q, r, seqlens, Hq, parts, st);
+    if (e == cudaSuccess) e = plx::launch_shared_combine(c, g, seqlens, Hq, ws, parts, out, st);
+    return e;
+  });
+}
+
+size_t plx_kv_update_workspace_bytes(int B, int num_pages, int max_pages) {
+  if (B < 1 || num_pages < 1 || max_pages < 1) return 0;
+  return plx::kv_update_workspace_bytes(B, num_pages, max_pages);
+}
+
+plx_status plx_kv_update(void *kpages, void *vpages, unsigned char *kscale, unsigned char *vscale,
+                         const int *block_table, const int *seqlens, const int *page_refs,
+                         const int *src, const int *lens, int *block_table_out, int *seqlens_out,
+                         int *page_refs_out, int B, int Hkv, int d, int num_pages, int page_size,
+                         int max_pages, void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "plx_kv_update";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  if (!seqlens || !page_refs || !lens || !block_table_out || !seqlens_out || !page_refs_out)
+    return fail(PLX_ERR_INVALID_ARG, "%s: null lengths, counts or outputs", fn);
+  const int in_place = (block_table_out == block_table) + (seqlens_out == seqlens) + (page_refs_out == page_refs);
+  if (in_place != 0 && in_place != 3)
+    return fail(PLX_ERR_INVALID_ARG, "%s: either all of the outputs are the inputs, or none", fn);
+  if (B > (1 << 20) || (static_cast<long long>(Hkv) + 1) * B > 0x7fffffffLL)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: B at most 2^20 and B * (Hkv + 1) below 2^31", fn);
+  const size_t need = plx_kv_update_workspace_bytes(B, num_pages, max_pages);
+  if (workspace && workspace_bytes < need)
+    return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  c.err = plx::device_error_word();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_workspace(fn, workspace, need, st, [&](void *ws) {
+    return plx::launch_kv_update(c, seqlens, page_refs, src, lens, block_table_out, seqlens_out,
+                                 page_refs_out, ws, st);
+  });
+}
+
+size_t plx_kv_compact_workspace_bytes(int num_pages) {
+  return num_pages < 1 ? 0 : plx::kv_compact_workspace_bytes(num_pages);
+}
+
+plx_status plx_kv_compact(void *kpages, void *vpages, unsigned char *kscale, unsigned char *vscale,
+                          const int *block_table, const int *seqlens, const int *page_refs,
+                          int *block_table_out, int *page_refs_out, int *page_map, int *used, int B,
+                          int Hkv, int d, int num_pages, int page_size, int max_pages,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "plx_kv_compact";
+  plx::PagedCache c;
+  plx_status s = paged_cache(fn, &c, kpages, vpages, kscale, vscale, block_table, B, Hkv, d,
+                             num_pages, page_size, max_pages);
+  if (s) return s;
+  if (!seqlens || !page_refs || !block_table_out || !page_refs_out || !page_map || !used)
+    return fail(PLX_ERR_INVALID_ARG, "%s: null lengths, counts or outputs", fn);
+  if ((block_table_out == block_table) != (page_refs_out == page_refs))
+    return fail(PLX_ERR_INVALID_ARG, "%s: either both of the outputs are the inputs, or none", fn);
+  const size_t need = plx_kv_compact_workspace_bytes(num_pages);
+  if (workspace && workspace_bytes < need)
+    return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  c.err = plx::device_error_word();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_workspace(fn, workspace, need, st, [&](void *ws) {
+    return plx::launch_kv_compact(c, seqlens, page_refs, block_table_out, page_refs_out, page_map,
+                                  used, ws, st);
+  });
+}
+
+namespace {
+
+plx_status rotary(const char *fn, bool backward, const void *const (&in)[3], void *const (&out)[3],
+                  const long long *strides, const int *positions, const int *seqlens,
+                  const int *cu_q, const double *inv_freq, double scale, int nseq, int B, int L,
+                  int Hq, int Hkv, int d, int rotary_dim, int interleaved, int dtype, void *stream) {
+  const char names[] = "qkr";
+  if (!strides || !inv_freq) return fail(PLX_ERR_INVALID_ARG, "%s: null strides or inv_freq", fn);
+  if (B < 0 || L < 0 || Hq < 1 || Hkv < 1)
+    return fail(PLX_ERR_INVALID_ARG, "%s: sizes must be >= 1 (B=%d L=%d Hq=%d Hkv=%d)", fn, B, L, Hq, Hkv);
+  if (d != 64 && d != 128) return fail(PLX_ERR_UNSUPPORTED, "%s: head dim %d (64 or 128)", fn, d);
+  if (rotary_dim < 2 || rotary_dim > d || rotary_dim % 2 != 0)
+    return fail(PLX_ERR_INVALID_ARG, "%s: rotary_dim %d must be even and in 2 .. %d", fn, rotary_dim, d);
+  if (dtype != PLX_BF16 && dtype != PLX_F32)
+    return fail(PLX_ERR_INVALID_ARG, "%s: dtype %d (PLX_BF16 or PLX_F32)", fn, dtype);
+  if (positions && (seqlens || cu_q))
+    return fail(PLX_ERR_INVALID_ARG, "%s: positions and seqlens / cu_q exclude each other", fn);
+  if (cu_q && !seqlens) return fail(PLX_ERR_INVALID_ARG, "%s: cu_q without seqlens", fn);
+  if (seqlens && (B != 1 || nseq < 1))
+    return fail(PLX_ERR_INVALID_ARG, "%s: with seqlens, rows are packed (B = 1) and nseq >= 1", fn);
+  if (seqlens && !cu_q && nseq != L)
+    return fail(PLX_ERR_INVALID_ARG, "%s: without cu_q, there must be one row for each of the %d sequences, got %d",
+                fn, nseq, L);
+  if (!in[0] && !in[1] && !in[2]) return fail(PLX_ERR_INVALID_ARG, "%s: q, k and r are all null", fn);
+  if (static_cast<long long>(B) * L > 0x7fffffffLL || Hq > (1 << 20) || Hkv > (1 << 20))
+    return fail(PLX_ERR_UNSUPPORTED, "%s: B * L must be below 2^31 and heads at most 2^20", fn);
+  plx::RotaryTensor t[3] = {};
+  int heads[3] = {};
+  const long long most = 1LL << 40;
+  for (int i = 0; i < 3; ++i) {
+    if ((in[i] == nullptr) != (out[i] == nullptr))
+      return fail(PLX_ERR_INVALID_ARG, "%s: %c and its output must be given both or neither", fn, names[i]);
+    if (in[i] == nullptr) continue;
+    heads[i] = i == 1 ? Hkv : Hq;
+    if (!aligned16(in[i]) || !aligned16(out[i]))
+      return fail(PLX_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", fn);
+    const long long *si = strides + 3 * i, *so = strides + 9 + 3 * i;
+    const long long size[3] = {B, L, heads[i]};
+    for (int k = 0; k < 3; ++k)
+      for (const long long *p : {si, so})
+        if (size[k] > 1 && (p[k] < d || p[k] > most || p[k] % 8 != 0))
+          return fail(PLX_ERR_INVALID_ARG, "%s: %c strides must be multiples of 8, at least %d and at most 2^40",
+                      fn, names[i], d);
+    // Rows of an output must be apart: from the smallest stride on, each one
+    // passes what those in front of it reach.
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return so[x] < so[y]; });
+    long long reach = d;
+    for (int k : order) {
+      if (size[k] <= 1) continue;
+      if (so[k] < reach) return fail(PLX_ERR_INVALID_ARG, "%s: rows of %c's output overlap", fn, names[i]);
+      reach += (size[k] - 1) * so[k];
+    }
+    for (int k = 0; k < 3; ++k)
+      if (in[i] == out[i] && size[k] > 1 && si[k] != so[k])
+        return fail(PLX_ERR_INVALID_ARG, "%s: %c in place needs the same strides", fn, names[i]);
+    t[i] = {in[i], out[i], B > 1 ? si[0] : 0, L > 1 ? si[1] : 0, heads[i] > 1 ? si[2] : 0,
+            B > 1 ? so[0] : 0, L > 1 ? so[1] : 0, heads[i] > 1 ? so[2] : 0};
+  }
+  if (B == 0 || L == 0) return PLX_OK;
+  return finish_launch(
+      plx::launch_rotary(t, heads, positions, seqlens, cu_q, nseq, inv_freq, static_cast<float>(scale), backward, B,
+                         L, d, rotary_dim, interleaved != 0, dtype == PLX_F32, plx::device_error_word(),
+                         static_cast<cudaStream_t>(stream)),
+      fn);
+}
+
+}  // namespace
+
+plx_status plx_rotary_fwd(const void *q, const void *k, const void *r, void *q_out, void *k_out,
+                          void *r_out, const long long *strides, const int *positions,
+                          const int *seqlens, const int *cu_q, const double *inv_freq, double scale,
+                          int nseq, int B, int L, int Hq, int Hkv, int d, int rotary_dim,
+                          int interleaved, int dtype, void *stream) {
+  return rotary("plx_rotary_fwd", false, {q, k, r}, {q_out, k_out, r_out}, strides, positions, seqlens, cu_q,
+                inv_freq, scale, nseq, B, L, Hq, Hkv, d, rotary_dim, interleaved, dtype, stream);
+}
+
+plx_status plx_rotary_bwd(const void *dq, const void *dk, const void *dr, void *dq_out,
+                          void *dk_out, void *dr_out, const long long *strides,
+                          const int *positions, const int *seqlens, const int *cu_q,
+                          const double *inv_freq, double scale, int nseq, int B, int L, int Hq,
+                          int Hkv, int d, int rotary_dim, int interleaved, int dtype, void *stream) {
+  return rotary("plx_rotary_bwd", true, {dq, dk, dr}, {dq_out, dk_out, dr_out}, strides, positions, seqlens,
+                cu_q, inv_freq, scale, nseq, B, L, Hq, Hkv, d, rotary_dim, interleaved, dtype, stream);
+}
+
+plx_status plx_rotary_freqs(double *inv_freq, double *scale, int rotary_dim, double base, int kind,
+                            double factor, double original_len, double beta_slow, double beta_fast) {
+  const char *fn = "plx_rotary_freqs";
+  if (!inv_freq || !scale) return fail(PLX_ERR_INVALID_ARG, "%s: null inv_freq or scale", fn);
+  if (rotary_dim < 2 || rotary_dim % 2 != 0)
+    return fail(PLX_ERR_INVALID_ARG, "%s: rotary_dim %d must be even and at least 2", fn, rotary_dim);
+  if (kind < PLX_ROTARY_PLAIN || kind > PLX_ROTARY_BY_PARTS)
+    return fail(PLX_ERR_INVALID_ARG, "%s: unknown kind %d", fn, kind);
+  if (!(base > 0) || !std::isfinite(base) || (kind != PLX_ROTARY_PLAIN && (!(factor >= 1) || !std::isfinite(factor))))
+    return fail(PLX_ERR_INVALID_ARG, "%s: base must be above 0 and factor at least 1", fn);
+  if (kind == PLX_ROTARY_BASE && rotary_dim == 2)
+    return fail(PLX_ERR_INVALID_ARG, "%s: a scaled base needs rotary_dim above 2", fn);
+  if (kind == PLX_ROTARY_BY_PARTS &&
+      (!(original_len > 0) || !std::isfinite(original_len) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast - beta_slow)))
+    return fail(PLX_ERR_INVALID_ARG, "%s: by parts needs original_len above 0 and beta_fast above beta_slow", fn);
+  const double R = rotary_dim;
+  if (kind == PLX_ROTARY_BASE) base *= std::pow(factor, R / (R - 2));
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2 * i / R);
+    double keep = 1;  // the share of the plain frequency
+    if (kind == PLX_ROTARY_LINEAR) keep = 0;
+    if (kind == PLX_ROTARY_BY_PARTS) {
+      const double turns = original_len * f / 6.283185307179586477;  // 2 pi
+      keep = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+    }
+    inv_freq[i] = keep == 1 ? f : f * keep + f / factor * (1 - keep);
+  }
+  *scale = kind == PLX_ROTARY_BY_PARTS ? 0.1 * std::log(factor) + 1 : 1;
+  return PLX_OK;
 }
 
 plx_status plx_check_device_error(void *stream) {

@@ -94,6 +94,7 @@ struct RowsArgs {
   long long vrows;           // places of meta; recs has nshare more
   int most;                  // as in RowsPlan
   float scale_log2;
+  SharedGroups groups;       // SUFFIX: keys that a group shares are left out
 };
 
 struct Plan {
@@ -105,14 +106,20 @@ struct Plan {
 // Keys, tiles, new tokens and row groups of sequence b.
 struct Seq {
   int len, tiles, first, n, ng;
+  int start;  // SUFFIX: the first key; its tile is the sequence's first
 };
-template <int KT, int GS>
+template <int KT, int GS, bool SUFFIX>
 __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
   // All loads first: they share one latency.
   const int n = a.seqlens[b], first = a.cu != nullptr ? a.cu[b] : b, end = a.cu != nullptr ? a.cu[b + 1] : b + 1;
   Seq s;
   s.len = checked_len(a.c, n);
   s.tiles = (s.len + KT - 1) / KT;
+  s.start = 0;
+  if constexpr (SUFFIX) {
+    s.start = min(group_with(a.c, a.groups, a.seqlens, b).prefix, s.len);
+    s.tiles = s.start < s.len ? s.tiles - s.start / KT : 0;
+  }
   s.first = first;
   s.n = 0;
   if (first < 0 || end > a.T || end < first) {
@@ -132,20 +139,21 @@ __device__ __forceinline__ long long groups_before(int first, int b, int G, int 
   return most > 0 ? static_cast<long long>(b) * (most / gs) : static_cast<long long>(first) * G / gs + b;
 }
 
-// One item: tiles [t0, t1) of row group grp of kv head kvh of sequence b.
+// One item: tiles [t0, t1) (of those from `start` on) of row group grp of kv head kvh of
+// sequence b.
 struct Item {
   Seq s;
   int b, kvh, grp, t0, t1;
   long long vrow;  // the item's row of records
 };
 
-template <int KT, int GS>
+template <int KT, int GS, bool SUFFIX>
 struct Walk {
   long long pos, e, base;
   int b;
   Seq s;
   __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a)
-      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS>(a, p.b0)) {}
+      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, SUFFIX>(a, p.b0)) {}
   __device__ __forceinline__ bool next(Item &it, const RowsArgs &a) {
     if (pos >= e) return false;
     // Positions below W all lie in some sequence, so b stays below B here.
@@ -153,7 +161,7 @@ struct Walk {
       const long long end = base + static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
       if (pos < end) break;
       base = end;
-      s = seq_of<KT, GS>(a, ++b);
+      s = seq_of<KT, GS, SUFFIX>(a, ++b);
     }
     const long long off = pos - base;
     const int vh = static_cast<int>(off / s.tiles);
@@ -168,6 +176,12 @@ struct Walk {
     return true;
   }
 };
+
+// The first key of tile t of an item's sequence.
+template <int KT, bool SUFFIX>
+__device__ __forceinline__ int tile_key(const Item &it, int t) {
+  return SUFFIX ? (it.s.start / KT + t) * KT : t * KT;
+}
 
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory");
@@ -219,7 +233,7 @@ __device__ __forceinline__ int row_shift(float m) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-template <bool FP8, int R>
+template <bool FP8, int R, bool SUFFIX>
 __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const RowsArgs a) {
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     int rows = 0, lmin = 0x7fffffff, lmax = 0;  // rows of records and lengths of sequences with keys
 #pragma unroll 4
     for (int i = lane; i < a.c.B; i += 32) {
-      const Seq s = seq_of<KT, GS>(a, i);
+      const Seq s = seq_of<KT, GS, SUFFIX>(a, i);
       const long long u = static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
       W += u;
       if (u > 0) {
@@ -286,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         const int i = i0 + lane;
         long long u = 0;
         if (i < a.c.B) {
-          const Seq q = seq_of<KT, GS>(a, i);
+          const Seq q = seq_of<KT, GS, SUFFIX>(a, i);
           u = static_cast<long long>(q.tiles) * q.ng * a.c.Hkv;
         }
         long long inc = u;
@@ -346,18 +360,18 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       const uint32_t at = (lane & 1) * TILE + first_key * 128;  // in a stage
       const bool active = lane < 2 * (KT / 16);
       const CUtensorMap *map = (lane & 1) ? &tm_v : &tm_k;
-      Walk<KT, GS> wk(pl, a);
+      Walk<KT, GS, SUFFIX> wk(pl, a);
       Item it;
       int g = 0;
       bool ok = true;
       while (ok && wk.next(it, a)) {
         const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-        const int end = min(it.t1 * KT, it.s.len);
-        int key = it.t0 * KT + first_key;
+        const int end = min(tile_key<KT, SUFFIX>(it, it.t1), it.s.len);
+        int key = tile_key<KT, SUFFIX>(it, it.t0) + first_key;
         int page = active && key < end ? table[key >> 4] : 0;
         for (int t = it.t0; t < it.t1; ++t, key += KT, ++g) {
           int z = beyond;
-          if (key < end) {
+          if (key < end && !(SUFFIX && key + 16 <= it.s.start)) {
             if (page >= 0 && page < a.c.num_pages) z = page * a.c.Hkv + it.kvh;
             else if (a.c.err) atomicOr(a.c.err, kErrBadInput);
           }
@@ -384,14 +398,14 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       prefetch_tensormap(&tm_v);
       const int shift = a.c.page_shift, mask = (1 << shift) - 1;
       const int per = KT > mask + 1 ? 16 : KT;  // keys of a box, as in the map
-      Walk<KT, GS> wk(pl, a);
+      Walk<KT, GS, SUFFIX> wk(pl, a);
       Item it;
       int g = 0;
       bool ok = true;
       while (ok && wk.next(it, a)) {
         const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-        int key = it.t0 * KT;
-        const int end = it.t1 * KT;
+        int key = tile_key<KT, SUFFIX>(it, it.t0);
+        const int end = tile_key<KT, SUFFIX>(it, it.t1);
         int next = table[key >> shift];  // t0's tile holds a key
         int z = beyond;
         bool fresh = true;
@@ -411,8 +425,13 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
               fresh = false;
               z = beyond;
               if (key < it.s.len) {
-                if (next >= 0 && next < a.c.num_pages) z = next * a.c.Hkv + it.kvh;
-                else if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+                if (SUFFIX && key + per <= it.s.start) {
+                  // A box of shared keys in front of the sequence's own: zeros.
+                } else if (next >= 0 && next < a.c.num_pages) {
+                  z = next * a.c.Hkv + it.kvh;
+                } else if (a.c.err) {
+                  atomicOr(a.c.err, kErrBadInput);
+                }
                 const int ahead = (key | mask) + 1;
                 if (ahead < min(end, it.s.len)) next = table[ahead >> shift];
               }
@@ -460,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   constexpr int MT = KT / 16;  // m tiles of 16 keys
   float *mls = reinterpret_cast<float *>(smem + OFF_MLS);
   volatile int *held = reinterpret_cast<volatile int *>(smem + OFF_HELD);
-  Walk<KT, GS> wk(pl, a);
+  Walk<KT, GS, SUFFIX> wk(pl, a);
   Item it;
   int gt = 0;  // tiles of the previous items
   while (wk.next(it, a)) {
@@ -476,12 +495,12 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     // the page number of the tile after it. Byte 0 is K's, byte 1 V's.
     const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
     auto page_of = [&](int t) {
-      const int key = (it.t0 + t) * KT + lane;
+      const int key = tile_key<KT, SUFFIX>(it, it.t0 + t) + lane;
       return t < nt && key < it.s.len ? table[key >> a.c.page_shift] : -1;
     };
     auto scales_of = [&](int t, int page) -> uint32_t {
       if (page < 0 || page >= a.c.num_pages) return 0u;
-      const int key = (it.t0 + t) * KT + lane;
+      const int key = tile_key<KT, SUFFIX>(it, it.t0 + t) + lane;
       const long long row = ((static_cast<long long>(page) * a.c.Hkv + it.kvh) << a.c.page_shift) +
                             (key & ((1 << a.c.page_shift) - 1));
       return a.c.kscale[row] | (static_cast<uint32_t>(a.c.vscale[row]) << 8);
@@ -556,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       if (lane == 0) ok = !ab.raised() && mbar_wait(smem_u32(&full[st]), (gi / NST) & 1, ab);
       if (!__shfl_sync(0xffffffffu, ok, 0)) continue;  // aborting: skip the tile
       const uint32_t kb = smem_u32(smem + st * 2 * TILE), vb = kb + TILE;
-      const int key0 = (it.t0 + t) * KT;
+      const int key0 = tile_key<KT, SUFFIX>(it, it.t0 + t);
       // cc[mt][0..1]: s and t of key 16 mt + g, [2..3]: of key 16 mt + 8 + g.
       float cc[MT][4];
       const int arow = (lane & 7) + 8 * ((lane >> 3) & 1), acol = lane >> 4;
@@ -601,14 +620,15 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         cc[0][2] = (c2[0][2] + c2[1][2]) * fs;
         cc[0][3] = c2[0][3] + c2[1][3];
       }
-      if (key0 + KT - 1 > all_see) {
+      if (key0 + KT - 1 > all_see || (SUFFIX && key0 < it.s.start)) {
         // Some row does not see all of the tile. Slots behind the sequence's
         // end, which no row sees, may hold anything: select, do not multiply.
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const bool see = key0 + 16 * mt + 8 * e + g <= last;
+            const int key = key0 + 16 * mt + 8 * e + g;
+            const bool see = key <= last && !(SUFFIX && key < it.s.start);
             cc[mt][2 * e] = see ? cc[mt][2 * e] : -INFINITY;
             cc[mt][2 * e + 1] = see ? cc[mt][2 * e + 1] : 0.f;
           }
@@ -690,6 +710,11 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         if (valid < KT) {
           k0 = 2 * tq < valid ? (2 * tq + 1 < valid ? 0xffffffffu : 0xffffu) : 0u;
           k1 = 2 * tq + 8 < valid ? (2 * tq + 9 < valid ? 0xffffffffu : 0xffffu) : 0u;
+        }
+        if (SUFFIX && key0 < it.s.start) {
+          const int lost = it.s.start - key0;  // rows in front of the first key
+          k0 &= 2 * tq >= lost ? 0xffffffffu : 2 * tq + 1 >= lost ? 0xffff0000u : 0u;
+          k1 &= 2 * tq + 8 >= lost ? 0xffffffffu : 2 * tq + 9 >= lost ? 0xffff0000u : 0u;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -935,6 +960,144 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
   if (a.lse != nullptr && dim == 0) a.lse[static_cast<long long>(t) * a.Hq + h] = lse2 * 0.6931471805599453f;
 }
 
+// The last sums of decode with shared prefixes: thread = (sequence, query head of the
+// group), block = 128 of them of a kv head and four dims, so that the raw sums of
+// the prefix ([dims / 4][row] float4) are read in whole lines.
+struct SharedArgs {
+  PagedCache c;
+  SharedGroups groups;
+  SharedParts parts;
+  const float *recs;
+  const int2 *meta;
+  const int *seqlens;
+  __nv_bfloat16 *out;
+  long long nslots, vrows;
+  int Hq, G, TQ, gs, group, ctas;
+};
+
+// Sums of records under a running maximum.
+struct Running {
+  float M, W, s, o1[4], o2[4];
+};
+template <int N>
+__device__ __forceinline__ void add_records(Running &x, const float (&m)[N], const float (&w)[N], const float (&s)[N],
+                                            const float4 (&o1)[N], const float4 (&o2)[N]) {
+  float mx = x.M;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mx = fmaxf(mx, m[i]);
+  const float msub = mx == -INFINITY ? 0.f : mx, back = exp2f(x.M - msub);
+  x.M = mx;
+  x.W *= back;
+  x.s *= back;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    x.o1[d] *= back;
+    x.o2[d] *= back;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float f = exp2f(m[i] - msub);
+    x.W = fmaf(f, w[i], x.W);
+    x.s = fmaf(f, s[i], x.s);
+    const float a[4] = {o1[i].x, o1[i].y, o1[i].z, o1[i].w}, b[4] = {o2[i].x, o2[i].y, o2[i].z, o2[i].w};
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      x.o1[d] = fmaf(f, a[d], x.o1[d]);
+      x.o2[d] = fmaf(f, b[d], x.o2[d]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(D) shared_combine_kernel(const SharedArgs a) {
+  constexpr int N = 4, RAW = 2 * D * 128 + 3 * 128;  // floats of a raw part
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int at = blockIdx.x * D + threadIdx.x, kvh = blockIdx.y, c4 = blockIdx.z;
+  const int b = at / a.G, gh = at - b * a.G, h = kvh * a.G + gh;
+  if (b >= a.c.B) return;
+  const int len = cache_len(a.c, a.seqlens, b);
+  const Group g = group_with(a.c, a.groups, a.seqlens, b);
+  const int start = min(g.prefix, len);
+  Running x = {-INFINITY, 0.f, 0.f, {}, {}};
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (start > 0) {
+    const int tile = (b - g.first) / a.TQ * a.TQ + g.first, row = (b - tile) * a.G + gh;
+    const int2 pt = a.parts.parts[static_cast<long long>(tile) * a.c.Hkv + kvh];
+    if (pt.x < 0) {
+      const float *r = a.parts.recs + (static_cast<long long>(b) * a.Hq + h) * kSharedRec;
+      const float4 st = *reinterpret_cast<const float4 *>(r + 2 * D);
+      const float m[1] = {st.y}, w[1] = {1.f}, s[1] = {st.x};
+      const float4 o1[1] = {*reinterpret_cast<const float4 *>(r + 4 * c4)};
+      const float4 o2[1] = {*reinterpret_cast<const float4 *>(r + D + 4 * c4)};
+      add_records<1>(x, m, w, s, o1, o2);
+    } else {
+      const int last = min(pt.y >> 1, a.ctas - 1);
+      for (int p0 = pt.x; p0 <= last; p0 += N) {
+        float m[N], w[N], s[N];
+        float4 o1[N], o2[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int p = p0 + i;
+          const bool in = p <= last;
+          const float *raw = a.parts.raw + (2ll * p + (p == pt.x ? pt.y & 1 : 0)) * RAW;
+          m[i] = in ? raw[2 * D * 128 + row] : -INFINITY;
+          w[i] = in ? raw[2 * D * 128 + 128 + row] : 0.f;
+          s[i] = in ? raw[2 * D * 128 + 256 + row] : 0.f;
+          o1[i] = in ? reinterpret_cast<const float4 *>(raw)[c4 * 128 + row] : zero;
+          o2[i] = in ? reinterpret_cast<const float4 *>(raw)[(D / 4 + c4) * 128 + row] : zero;
+        }
+        add_records<N>(x, m, w, s, o1, o2);
+      }
+    }
+  }
+  if (start < len) {
+    const int ng = (a.G + a.group - 1) / a.group;
+    const long long place = groups_before(b, b, a.G, a.group, 0) * a.c.Hkv + static_cast<long long>(kvh) * ng + gh / a.group;
+    if (!PLX_IN_BOUNDS(place >= 0 && place < a.vrows, ErrWord{a.c.err})) return;
+    const int2 mt = a.meta[place];
+    const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
+    const int n = inside ? mt.y : 0;
+    const size_t stride = static_cast<size_t>(a.gs) * REC;
+    const float *rec = a.recs + (inside ? mt.x : 0) * stride + static_cast<size_t>(gh % a.group) * REC;
+    for (int r0 = 0; r0 < n; r0 += N) {
+      float m[N], w[N], s[N];
+      float4 o1[N], o2[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool in = r0 + i < n;
+        const float2 *r = reinterpret_cast<const float2 *>(rec + (r0 + i) * stride);
+        const float2 st = in ? r[D] : make_float2(0.f, -INFINITY);
+        s[i] = st.x;
+        m[i] = st.y;
+        w[i] = in ? 1.f : 0.f;
+        float2 y[4] = {};
+        if (in) {
+          y[0] = r[2 * c4];
+          y[1] = r[2 * c4 + 1];
+          y[2] = r[D / 2 + 2 * c4];
+          y[3] = r[D / 2 + 2 * c4 + 1];
+        }
+        o1[i] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+        o2[i] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+      }
+      add_records<N>(x, m, w, s, o1, o2);
+    }
+  }
+  float o[4] = {};
+  if (x.W != 0.f) {  // NaN, for a query that is not a number, goes on
+    const float inv = 1.f / x.W, sg = x.s * inv;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const float p = x.o1[d] * inv;
+      // One key: the covariance is zero and o = v, whatever O2's rounding.
+      o[d] = len == 1 ? p : p - (x.o2[d] * inv - p * sg);
+    }
+  }
+  uint2 w;
+  w.x = pack_bf16x2(o[0], o[1]);
+  w.y = pack_bf16x2(o[2], o[3]);
+  *reinterpret_cast<uint2 *>(a.out + (static_cast<long long>(b) * a.Hq + h) * D + 4 * c4) = w;
+}
+
 // Map of one page tensor. bf16: {64, page, pages Hkv, 2 halves}, boxes of 16
 // rows of both halves; e4m3: {128, page, pages Hkv}, boxes of up to 32 rows.
 bool make_page_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, const void *ptr, bool fp8) {
@@ -956,19 +1119,19 @@ bool make_page_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, con
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8, int R>
+template <bool FP8, int R, bool SUFFIX>
 cudaError_t launch_rows(const RowsArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                         cudaStream_t stream) {
   static thread_local unsigned long long configured_ctx = 0;
   const unsigned long long ctx = context_id();
   if (ctx == 0 || configured_ctx != ctx) {
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, R>,
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, R, SUFFIX>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(ROWS_SMEM));
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  paged_rows_kernel<FP8, R><<<a.nshare, THREADS, ROWS_SMEM, stream>>>(mk, mv, a);
+  paged_rows_kernel<FP8, R, SUFFIX><<<a.nshare, THREADS, ROWS_SMEM, stream>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
@@ -983,18 +1146,21 @@ int paged_rows_shares() { return kCtasPerSm * sm_count(); }
 // 256 us (e4m3), 625 and 337 us (bf16): a second group reads the keys again.
 int paged_rows_group(int T, int B, int G) { return static_cast<long long>(T) * G > RW * static_cast<long long>(B) ? 2 * RW : RW; }
 
-cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void *q, const void *r,
-                              long long qts, long long qhs, const int *seqlens, const int *cu_q,
-                              void *out, long long ots, long long ohs, float *lse, int T, int Hq,
-                              void *workspace, cudaStream_t stream) {
+namespace {
+
+// The split kernel of a call; `a` as it was launched.
+template <bool SUFFIX>
+cudaError_t launch_split(const RowsPlan &p, const PagedCache &c, const void *q, const void *r, long long qts,
+                         long long qhs, const int *seqlens, const int *cu_q, int T, int Hq,
+                         const SharedGroups &groups, void *workspace, RowsArgs &a, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return cudaErrorInvalidValue;
   const bool fp8 = c.kscale != nullptr;
   CUtensorMap mk, mv;
   if (!make_page_map(enc, &mk, c, c.k, fp8) || !make_page_map(enc, &mv, c, c.v, fp8))
     return cudaErrorInvalidValue;
-  RowsArgs a;
   a.c = c;
+  a.groups = groups;
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.r = static_cast<const __nv_bfloat16 *>(r);
   a.qts = qts;
@@ -1013,10 +1179,21 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
   a.vrows = vrows;
   a.meta = static_cast<int2 *>(workspace);
   a.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + paged_rows_meta_bytes(vrows));
-  cudaError_t e;
-  if (group == 4) e = fp8 ? launch_rows<true, 1>(a, mk, mv, stream) : launch_rows<false, 1>(a, mk, mv, stream);
-  else e = fp8 ? launch_rows<true, 2>(a, mk, mv, stream) : launch_rows<false, 2>(a, mk, mv, stream);
+  if (group == 4)
+    return fp8 ? launch_rows<true, 1, SUFFIX>(a, mk, mv, stream) : launch_rows<false, 1, SUFFIX>(a, mk, mv, stream);
+  return fp8 ? launch_rows<true, 2, SUFFIX>(a, mk, mv, stream) : launch_rows<false, 2, SUFFIX>(a, mk, mv, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void *q, const void *r,
+                              long long qts, long long qhs, const int *seqlens, const int *cu_q,
+                              void *out, long long ots, long long ohs, float *lse, int T, int Hq,
+                              void *workspace, cudaStream_t stream) {
+  RowsArgs a;
+  cudaError_t e = launch_split<false>(p, c, q, r, qts, qhs, seqlens, cu_q, T, Hq, SharedGroups{}, workspace, a, stream);
   if (e != cudaSuccess) return e;
+  const long long vrows = a.vrows;
   CombineArgs k;
   k.c = c;
   k.recs = a.recs;
@@ -1033,7 +1210,7 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
   k.G = a.G;
   k.T = T;
   k.gs = a.gs;
-  k.group = group;
+  k.group = p.group;
   k.most = p.most;
   k.tokens = p.most > 0 && static_cast<long long>(c.B) * (p.most / a.G) < T ? p.most / a.G : 0;
   cudaLaunchConfig_t cfg = {};
@@ -1048,6 +1225,49 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
   e = cudaLaunchKernelEx(&cfg, paged_combine_kernel, k);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+namespace {
+RowsPlan shared_rows_plan(int B, int G) { return {paged_rows_group(B, B, G), 0}; }
+}  // namespace
+
+cudaError_t launch_shared_rows(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
+                               const int *seqlens, int Hq, void *workspace, cudaStream_t stream) {
+  RowsArgs a;
+  return launch_split<true>(shared_rows_plan(c.B, Hq / c.Hkv), c, q, r, static_cast<long long>(Hq) * D, D, seqlens,
+                            nullptr, c.B, Hq, g, workspace, a, stream);
+}
+
+cudaError_t launch_shared_combine(const PagedCache &c, const SharedGroups &g, const int *seqlens, int Hq,
+                                  const void *rows_workspace, const SharedParts &parts, void *out,
+                                  cudaStream_t stream) {
+  SharedArgs a;
+  a.c = c;
+  a.groups = g;
+  a.parts = parts;
+  a.seqlens = seqlens;
+  a.out = static_cast<__nv_bfloat16 *>(out);
+  a.Hq = Hq;
+  a.G = Hq / c.Hkv;
+  a.TQ = 128 / a.G;
+  const RowsPlan p = shared_rows_plan(c.B, a.G);
+  a.group = p.group;
+  a.gs = paged_rows_slot(p.group, a.G, false);
+  a.vrows = paged_rows_vrows(p, c.B, c.B, a.G, c.Hkv);
+  a.nslots = paged_rows_shares() + a.vrows;
+  a.ctas = sm_count();
+  a.meta = static_cast<const int2 *>(rows_workspace);
+  a.recs = reinterpret_cast<const float *>(static_cast<const uint8_t *>(rows_workspace) + paged_rows_meta_bytes(a.vrows));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((c.B * a.G + D - 1) / D, c.Hkv, D / 4);
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_combine_kernel, a);
 }
 
 }  // namespace plx

@@ -94,6 +94,10 @@ struct Args {
   int T, Hq, G, TQ;
   int few;  // sequences of at most so many new tokens are not this kernel's
   float scale_log2;
+  // SHARED: the kernel's sequences are groups, their tokens the group's sequences,
+  // each of which sees the same keys (as many of them as it has).
+  SharedGroups groups;
+  SharedParts shared;
 };
 // A CTA's share is at least this many key tiles.
 constexpr int kMinTiles = 4;
@@ -104,7 +108,12 @@ constexpr int PART = 2 * D * BM + 3 * BM;
 struct Seq {
   int len, first, n, nq;  // keys, first packed row, new tokens, row tiles
 };
+template <bool SHARED>
 __device__ __noinline__ Seq seq_of(const Args &a, int b) {
+  if constexpr (SHARED) {
+    const Group g = group_of(a.c, a.groups, a.seqlens, b);
+    return Seq{g.prefix, g.first, g.n, g.prefix > 0 ? (g.n + a.TQ - 1) / a.TQ : 0};
+  }
   // All loads first: they share one latency.
   const int n = a.seqlens[b], first = a.cu[b], end = a.cu[b + 1];
   Seq s;
@@ -122,7 +131,9 @@ __device__ __noinline__ Seq seq_of(const Args &a, int b) {
 }
 // Key tiles of row tile t: up to the last key that its last token sees, at
 // least one (a row tile of padding still writes its zeros).
+template <bool SHARED>
 __device__ __forceinline__ int tiles_of(const Seq &s, int t, int TQ) {
+  if constexpr (SHARED) return (s.len + BN - 1) / BN;
   const int seen = s.len - s.n + static_cast<int>(min(static_cast<long long>(t + 1) * TQ, static_cast<long long>(s.n)));
   return max(1, (seen + BN - 1) / BN);
 }
@@ -146,10 +157,12 @@ __device__ __forceinline__ long long tile_sum(long long n, int TQ, long long b) 
   return ((inc << lg) * (q * (q - 1) / 2)) + q * all + rest * q * inc + some;
 }
 // Key tiles of the first t row tiles (t <= nq).
+template <bool SHARED>
 __device__ __noinline__ long long tiles_before(const Seq &s, int t, int TQ) {
+  if constexpr (SHARED) return static_cast<long long>(t) * tiles_of<true>(s, 0, TQ);
   if (t <= 0) return 0;
   long long extra = 0;
-  if (t == s.nq) extra = tiles_of(s, --t, TQ);  // the last row tile may be short
+  if (t == s.nq) extra = tiles_of<false>(s, --t, TQ);  // the last row tile may be short
   // Row tiles i < i0 see at most BN keys: one key tile each.
   const long long base = static_cast<long long>(s.len) - s.n + TQ + BN - 1;  // i = 0's numerator
   const long long i0 = base >= 2 * BN ? 0 : min(static_cast<long long>(t), (2 * BN - base + TQ - 1) / TQ);
@@ -178,6 +191,7 @@ struct Item {
   int row0, ntok;      // first packed row; tokens of the chunk from there on
   int pos0;            // position of the first token
   int j0, j1, nt;
+  int table;           // SHARED: the row of the block table
 };
 
 // A role's place in the CTA's share, in shared memory: the softmax warps have
@@ -202,7 +216,7 @@ struct Walk {
 };
 
 // The next item into w->it, by a role's one thread (WARP = false) or by its warp.
-template <bool WARP>
+template <bool WARP, bool SHARED>
 __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
   if (WARP) __syncwarp();  // every lane has read the item before
   if (!WARP || (threadIdx.x & 31) == 0) {
@@ -211,7 +225,7 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
     int t = w->t, kvh = w->kvh, b = w->b;
     if (w->items > 0) {
       // Round t of whole items.
-      const int c = blockIdx.x, o = t * w->n + ((t & 1) ? w->n - 1 - c : c), heads = a.c.B * a.c.Hkv;
+      const int c = blockIdx.x, o = t * w->n + ((t & 1) ? w->n - 1 - c : c), heads = (SHARED ? a.groups.n : a.c.B) * a.c.Hkv;
       more = o < w->items;
       w->t = t + 1;
       t = s.nq - 1 - o / heads;
@@ -224,7 +238,7 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
         t = 0;
         if (++kvh == a.c.Hkv) {
           kvh = 0;
-          do s = seq_of(a, ++b);
+          do s = seq_of<SHARED>(a, ++b);
           while (s.nq == 0);
           w->s = s;
           w->b = b;
@@ -240,7 +254,8 @@ __device__ __noinline__ bool walk_next(Walk *w, const Args &a) {
       it.row0 = s.first + t * a.TQ;
       it.ntok = s.n - t * a.TQ;
       it.pos0 = s.len - s.n + t * a.TQ;
-      it.nt = tiles_of(s, t, a.TQ);
+      it.nt = tiles_of<SHARED>(s, t, a.TQ);
+      if constexpr (SHARED) it.table = s.first;
       it.j0 = w->j;
       w->j = 0;
       it.j1 = it.nt;
@@ -262,19 +277,20 @@ __device__ __forceinline__ Seq seq_from(const Seq &s, int l) {
              __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.nq, l)};
 }
 // One warp: the CTA's share and where it starts.
+template <bool SHARED>
 __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, count = SHARED ? a.groups.n : a.c.B;
   long long U = 0, u0 = 0;  // mine, u0: sequence `lane`
   int items = 0;
   Seq mine = {}, s0 = {};
   bool alike = true;
-  for (int i0 = 0; i0 < a.c.B; i0 += 32) {
+  for (int i0 = 0; i0 < count; i0 += 32) {
     const int i = i0 + lane;
     Seq s = {};
-    if (i < a.c.B) s = seq_of(a, i);
+    if (i < count) s = seq_of<SHARED>(a, i);
     if (i0 == 0) s0 = seq_from(s, 0);
-    if (i < a.c.B) {
-      const long long u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+    if (i < count) {
+      const long long u = tiles_before<SHARED>(s, s.nq, a.TQ) * a.c.Hkv;
       if (i0 == 0) {
         u0 = u;
         mine = s;
@@ -304,14 +320,14 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
     p.n = gridDim.x;
   } else if (p.s < p.e) {
     long long base = 0;
-    for (int i0 = 0; i0 < a.c.B; i0 += 32) {
+    for (int i0 = 0; i0 < count; i0 += 32) {
       const int i = i0 + lane;
       long long u = u0;
       if (i0 > 0) {
         u = 0;
-        if (i < a.c.B) {
-          const Seq s = seq_of(a, i);
-          u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
+        if (i < count) {
+          const Seq s = seq_of<SHARED>(a, i);
+          u = tiles_before<SHARED>(s, s.nq, a.TQ) * a.c.Hkv;
         }
       }
       long long inc = u;
@@ -320,18 +336,18 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
         const long long v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, i < a.c.B && base + inc > p.s);
+      const unsigned hit = __ballot_sync(0xffffffffu, i < count && base + inc > p.s);
       if (hit != 0u) {
         const int l = __ffs(hit) - 1;
         p.b = i0 + l;
         base += __shfl_sync(0xffffffffu, inc - u, l);
-        p.first = i0 == 0 ? seq_from(mine, l) : seq_of(a, p.b);
+        p.first = i0 == 0 ? seq_from(mine, l) : seq_of<SHARED>(a, p.b);
         break;
       }
       base += __shfl_sync(0xffffffffu, inc, 31);
     }
     const Seq s = p.first;
-    const long long head = tiles_before(s, s.nq, a.TQ), off = p.s - base;
+    const long long head = tiles_before<SHARED>(s, s.nq, a.TQ), off = p.s - base;
     p.kvh = static_cast<int>(div64(off, head));
     const long long in = off - p.kvh * head;
     // The last t with tiles_before(t) <= in: 32 candidates a round.
@@ -339,11 +355,11 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
     while (step > 1) {
       step = (step + 31) / 32;
       const long long cand = lo + static_cast<long long>(step) * lane;
-      const bool below = cand < s.nq && tiles_before(s, static_cast<int>(cand), a.TQ) <= in;
+      const bool below = cand < s.nq && tiles_before<SHARED>(s, static_cast<int>(cand), a.TQ) <= in;
       lo += step * (31 - __clz(__ballot_sync(0xffffffffu, below)));
     }
     p.t = lo;
-    p.j = static_cast<int>(in - tiles_before(s, lo, a.TQ));
+    p.j = static_cast<int>(in - tiles_before<SHARED>(s, lo, a.TQ));
   }
   if (lane == 0) *plan = p;
 }
@@ -376,7 +392,7 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, i
                : "memory");
 }
 
-template <bool FP8>
+template <bool FP8, bool SHARED>
 __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_r,
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (warp == 0) make_plan(a, plan, lane);
+  if (warp == 0) make_plan<SHARED>(a, plan, lane);
   if (threadIdx.x == 32) {
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 2);
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   const Plan pl = *plan;
   const uint32_t tbase = *tmem_slot;
   if (pl.items == 0 && pl.s >= pl.e) {  // no share
-    if (threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
+    if (!SHARED && threadIdx.x == 0) a.table[4 * blockIdx.x] = -1;
     if (warp == O1_WARP) tmem_dealloc(tbase, 512);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -485,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   auto boxes_of = [&](const Item &item, int j) -> int {
     const int key = j * BN + lane * box;
     if (j >= item.j1 || lane * box >= BN || key >= item.len) return beyond;
-    const int page = a.c.table[static_cast<long long>(item.b) * a.c.max_pages + (key >> shift)];
+    const int page = a.c.table[static_cast<long long>(SHARED ? item.table : item.b) * a.c.max_pages + (key >> shift)];
     if (page < 0 || page >= a.c.num_pages) {
       if (a.c.err) atomicOr(a.c.err, kErrBadInput);
       return beyond;
@@ -503,10 +519,17 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     const int rtok = row / a.G;
     int g = 0;
     bool ok = true;
-    for (int k = 0; ok && walk_next<true>(wk, a); ++k) {
+    for (int k = 0; ok && walk_next<true, SHARED>(wk, a); ++k) {
       float m_used = -INFINITY, l = 0.f, sg = 0.f;
-      // From tile `whole` on, some row does not see all keys of a tile.
-      const int n = it.j1 - it.j0, whole = max(0, (it.pos0 + 1) / BN - it.j0);
+      // SHARED: the last key that the row sees. From tile `whole` on, some row (of the warp)
+      // does not see all keys of a tile.
+      int seen = 0, whole_seen = it.pos0;
+      if constexpr (SHARED) {
+        const bool there = rtok < min(it.ntok, a.TQ);
+        seen = there ? min(it.len, cache_len(a.c, a.seqlens, it.row0 + rtok)) - 1 : it.len - 1;
+        whole_seen = __reduce_min_sync(0xffffffffu, seen);
+      }
+      const int n = it.j1 - it.j0, whole = max(0, (whole_seen + 1) / BN - it.j0);
       for (int j = 0; ok && j < n; ++j) {
         const int gg = g + j, x = gg & 1;
         const uint32_t cs = tl + (x ? COL_S1 : COL_S0);
@@ -520,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           // instruction cache it shares). In a sequence's last tile T gets
           // zeros behind the last key, where the pages may hold NaN, and so
           // does V (bf16; converted tiles have them).
-          const int key0 = (it.j0 + j) * BN, lim = it.pos0 + rtok - key0, valid = it.len - key0;
+          const int key0 = (it.j0 + j) * BN, lim = (SHARED ? seen : it.pos0 + rtok) - key0, valid = it.len - key0;
 #pragma unroll 1
           for (int qq = 0; qq < 8; ++qq) {
             if (qq >= 4 && valid >= BN) break;
@@ -658,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     }
     int g = 0;
     bool cut = false;  // the share ends inside an item that starts in it
-    for (int k = 0; walk_next<true>(wk, a); ++k) {
+    for (int k = 0; walk_next<true, SHARED>(wk, a); ++k) {
       const int glast = g + it.j1 - it.j0 - 1;
       g = glast + 1;
       if (!wait_all(smem_u32(&stat_full[k & 1]), (k >> 1) & 1, ab) ||
@@ -670,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       // Rows of the output; at most two parts a share, its first item's and its last's.
       const bool item_ok = PLX_IN_BOUNDS(
           it.b < a.c.B && it.kvh >= 0 && it.kvh < a.c.Hkv && it.row0 >= 0 && it.ntok >= 1 &&
-              min(it.ntok, a.TQ) <= a.T - it.row0 && ((it.j0 == 0 && it.j1 == it.nt) || k == 0 || (it.j0 == 0 && !cut)),
+              min(it.ntok, a.TQ) <= a.T - it.row0 && (!SHARED || it.table < a.c.B) && ((it.j0 == 0 && it.j1 == it.nt) || k == 0 || (it.j0 == 0 && !cut)),
           ab);
       auto o_read = [&] {  // O has been read: the next item's value UMMAs may overwrite it
         tc_fence_before();
@@ -678,10 +701,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         if (lane == 0) mbar_arrive(smem_u32(o_free));
       };
       if (it.j0 != 0 || it.j1 != it.nt) {
-        // A part of an item: raw sums for the merge. The share's first item
+        // A part of an item: raw sums for the merge (SHARED: for the last sums). The share's first item
         // goes to slot 0, a later one (its last) to slot 1.
         const int slot = k == 0 ? 0 : 1;
-        float4 *p4 = reinterpret_cast<float4 *>(a.parts + (2ll * blockIdx.x + slot) * PART);
+        float4 *p4 = reinterpret_cast<float4 *>((SHARED ? a.shared.raw : a.parts) + (2ll * blockIdx.x + slot) * PART);
 #pragma unroll 1
         for (int part = 0; part < 8; ++part) {
           float o[32];
@@ -701,15 +724,43 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         if (it.j0 == 0 && item_ok) {
           cut = true;
           if (warp == EP_WARP && lane == 0) {
-            int *te = a.table + 4 * blockIdx.x;
-            te[0] = it.b;
-            te[1] = it.kvh;
-            te[2] = it.t;
             // The CTA that holds the item's last tile.
             const long long x = pl.e + (it.nt - it.j1) - 1;
-            te[3] = static_cast<int>(div64((x + 1) * pl.n - 1, pl.U)) * 2 + slot;
+            const int last = static_cast<int>(div64((x + 1) * pl.n - 1, pl.U)) * 2 + slot;
+            if constexpr (SHARED) {
+              a.shared.parts[static_cast<long long>(it.row0) * a.c.Hkv + it.kvh] = make_int2(blockIdx.x, last);
+            } else {
+              int *te = a.table + 4 * blockIdx.x;
+              te[0] = it.b;
+              te[1] = it.kvh;
+              te[2] = it.t;
+              te[3] = last;
+            }
           }
         }
+        continue;
+      }
+      if constexpr (SHARED) {
+        // The whole prefix: normalised records, a row each.
+        const bool there = item_ok && rtok < min(it.ntok, a.TQ);
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        float *rec = a.shared.recs + (static_cast<long long>(it.row0 + rtok) * a.Hq + it.kvh * a.G + rh) * kSharedRec;
+#pragma unroll 1
+        for (int part = 0; part < 8; ++part) {
+          float o[32];
+          tmem_ld32(tl + (part < 4 ? COL_O1 : COL_O2) + (part & 3) * 32, o);
+          tmem_wait_ld();
+          if (part == 7) o_read();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (there)
+              reinterpret_cast<float4 *>(rec)[part * 8 + e] =
+                  make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+        }
+        if (there)
+          *reinterpret_cast<float4 *>(rec + 2 * D) = make_float4(sg * inv, l != 0.f ? m_used + log2f(l) : -INFINITY, 0.f, 0.f);
+        if (warp == EP_WARP && lane == 0 && item_ok)
+          a.shared.parts[static_cast<long long>(it.row0) * a.c.Hkv + it.kvh] = make_int2(-1, 0);
         continue;
       }
       // The token at position 0 sees one key: the covariance is zero and o = v. Its
@@ -753,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         a.lse[static_cast<long long>(it.row0 + rtok) * a.Hq + it.kvh * a.G + rh] =
             l != 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
-    if (!cut && warp == EP_WARP && lane == 0) a.table[4 * blockIdx.x] = -1;
+    if (!SHARED && !cut && warp == EP_WARP && lane == 0) a.table[4 * blockIdx.x] = -1;
   } else if (warp < S_WARP) {
     // ------------------------------------------------------------ value UMMAs
     // O1 += P V (P over S) and O2 += (P o T) V (over T): bf16 by a thread each,
@@ -764,7 +815,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), HALF_KV, 1024);
       int g = 0;
       bool ok = true;
-      bool more = walk_next<false>(wk, a);
+      bool more = walk_next<false, SHARED>(wk, a);
       for (int k = 0; ok && more; ++k) {
         const int nt = it.j1 - it.j0;
         for (int j = 0; j < nt; ++j) {
@@ -792,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           tc_fence_before();
           mbar_arrive(smem_u32(&pv_issued[2 * x + first]));
           if (FP8) mbar_arrive(smem_u32(&pv_issued[2 * x + 1]));
-          if (j == 0) more = walk_next<false>(wk, a);  // off the item boundary's path
+          if (j == 0) more = walk_next<false, SHARED>(wk, a);  // off the item boundary's path
         }
         g += nt;
       }
@@ -803,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       // ---------------------------------------------------------- raw loads
       int g = 0, issued[2] = {0, 0};  // tiles of K and V
       bool ok = true;
-      while (ok && walk_next<true>(wk, a)) {
+      while (ok && walk_next<true, SHARED>(wk, a)) {
         const int j1 = it.j1;
         int z_next = boxes_of(it, it.j0);
         for (int j = it.j0; j < j1; ++j, ++g) {
@@ -842,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const uint32_t qb = smem_u32(q_full);
       int g = 0, q_issued = 0;
       bool ok = true;
-      bool next = walk_next<false>(wk, a);
+      bool next = walk_next<false, SHARED>(wk, a);
       for (int k = 0; ok && next; ++k) {
         const int nt = it.j1 - it.j0;
         if (is_s) {
@@ -874,7 +925,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if (j == 0) {
             // The next item, off the item boundary's path, and its Q and R into
             // L2: the boundary waits for their load.
-            next = walk_next<false>(wk, a);
+            next = walk_next<false, SHARED>(wk, a);
             if (is_s && next) {
               const int h0 = it.kvh * a.G, t0 = it.row0;
               tma_prefetch_3d(&tm_q, 0, h0, t0);
@@ -901,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     const uint32_t ring = smem_u32(smem + (is_k ? C::OFF_K : C::OFF_V));
     int g = 0;
     bool ok = true;
-    while (ok && walk_next<true>(wk, a)) {
+    while (ok && walk_next<true, SHARED>(wk, a)) {
       const int j1 = it.j1;
       int z_next = boxes_of(it, it.j0);
       for (int j = it.j0; j < j1; ++j, ++g) {
@@ -946,8 +997,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     const int stages = kv ? NSV : NSK;
     int g = 0, st = 0, turn = 0;  // tile, its stage, times round the ring
     bool ok = true;
-    while (ok && walk_next<true>(wk, a)) {
-      const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+    while (ok && walk_next<true, SHARED>(wk, a)) {
+      const int *table = a.c.table + static_cast<long long>(SHARED ? it.table : it.b) * a.c.max_pages;
       const int len = it.len, j1 = it.j1;
       const uint8_t *head = scales + (static_cast<long long>(it.kvh) << shift);
       const long long page_step = static_cast<long long>(a.c.Hkv) << shift;
@@ -1055,7 +1106,7 @@ __global__ void __launch_bounds__(BM) paged_prefill_merge_kernel(const Args a) {
   if (!PLX_IN_BOUNDS(b < a.c.B && kvh >= 0 && kvh < a.c.Hkv && t >= 0 && last >= c && last < static_cast<int>(gridDim.x),
                      ErrWord{a.c.err}))
     return;
-  const Seq s = seq_of(a, b);
+  const Seq s = seq_of<false>(a, b);
   const int ot = row / a.G, tok = t * a.TQ + ot;
   if (ot >= a.TQ || tok >= s.n || !PLX_IN_BOUNDS(s.first + tok < a.T, ErrWord{a.c.err})) return;
   // Parts: CTA c's, then slot 0 of the CTAs up to the last.
@@ -1133,12 +1184,12 @@ bool make_tile_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, con
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
+template <bool FP8, bool SHARED>
 cudaError_t launch_tiles(const Args &a, int grid, const CUtensorMap (&m)[4], cudaStream_t stream) {
   static thread_local unsigned long long configured_ctx = 0;
   const unsigned long long ctx = context_id();
   if (ctx == 0 || configured_ctx != ctx) {
-    cudaError_t e = cudaFuncSetAttribute(paged_prefill_kernel<FP8>,
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_kernel<FP8, SHARED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::SMEM);
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
@@ -1152,8 +1203,8 @@ cudaError_t launch_tiles(const Args &a, int grid, const CUtensorMap (&m)[4], cud
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.few > 0 ? 1 : 0;  // behind the call's other kernels
-  return cudaLaunchKernelEx(&cfg, paged_prefill_kernel<FP8>, m[0], m[1], m[2], m[3], a);
+  cfg.numAttrs = SHARED || a.few > 0 ? 1 : 0;  // behind the call's other kernels
+  return cudaLaunchKernelEx(&cfg, paged_prefill_kernel<FP8, SHARED>, m[0], m[1], m[2], m[3], a);
 }
 
 constexpr size_t table_bytes(int grid) { return (size_t(grid) * 16 + 255) / 256 * 256; }
@@ -1194,7 +1245,7 @@ cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void 
       !make_rows_map(enc, &m[1], r, T, Hq, a.G, a.TQ, qts, qhs) ||
       !make_tile_map(enc, &m[2], c, c.k, fp8) || !make_tile_map(enc, &m[3], c, c.v, fp8))
     return cudaErrorInvalidValue;
-  cudaError_t e = fp8 ? launch_tiles<true>(a, grid, m, stream) : launch_tiles<false>(a, grid, m, stream);
+  cudaError_t e = fp8 ? launch_tiles<true, false>(a, grid, m, stream) : launch_tiles<false, false>(a, grid, m, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, D / 8);
@@ -1208,6 +1259,47 @@ cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void 
   e = cudaLaunchKernelEx(&cfg, paged_prefill_merge_kernel, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+namespace {
+size_t places_bytes(int B, int Hkv) { return (size_t(B) * Hkv * sizeof(int2) + 255) / 256 * 256; }
+size_t records_bytes(int B, int Hq) { return (size_t(B) * Hq * kSharedRec * sizeof(float) + 255) / 256 * 256; }
+}  // namespace
+
+size_t shared_parts_bytes(int B, int Hq, int Hkv) {
+  return places_bytes(B, Hkv) + records_bytes(B, Hq) + size_t(2 * sm_count()) * PART * sizeof(float);
+}
+SharedParts shared_parts(void *workspace, int B, int Hq, int Hkv) {
+  char *ws = static_cast<char *>(workspace);
+  SharedParts p;
+  p.parts = reinterpret_cast<int2 *>(ws);
+  p.recs = reinterpret_cast<float *>(ws + places_bytes(B, Hkv));
+  p.raw = reinterpret_cast<float *>(ws + places_bytes(B, Hkv) + records_bytes(B, Hq));
+  return p;
+}
+
+cudaError_t launch_shared_prefix(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
+                                 const int *seqlens, int Hq, const SharedParts &parts, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return cudaErrorInvalidValue;
+  const bool fp8 = c.kscale != nullptr;
+  Args a = {};
+  a.c = c;
+  a.seqlens = seqlens;
+  a.groups = g;
+  a.shared = parts;
+  a.T = c.B;
+  a.Hq = Hq;
+  a.G = Hq / c.Hkv;
+  a.TQ = BM / a.G;
+  a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+  CUtensorMap m[4];
+  const long long row = static_cast<long long>(Hq) * D;
+  if (!make_rows_map(enc, &m[0], q, c.B, Hq, a.G, a.TQ, row, D) ||
+      !make_rows_map(enc, &m[1], r, c.B, Hq, a.G, a.TQ, row, D) ||
+      !make_tile_map(enc, &m[2], c, c.k, fp8) || !make_tile_map(enc, &m[3], c, c.v, fp8))
+    return cudaErrorInvalidValue;
+  return fp8 ? launch_tiles<true, true>(a, sm_count(), m, stream) : launch_tiles<false, true>(a, sm_count(), m, stream);
 }
 
 }  // namespace plx

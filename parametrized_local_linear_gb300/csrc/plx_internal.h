@@ -134,6 +134,41 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
                               void *out, long long ots, long long ohs, float *lse, int T, int Hq,
                               void *workspace, cudaStream_t stream);
 
+// Groups of sequences whose first prefix[g] keys are the same: sequences cu[g] ..
+// cu[g + 1] - 1, the pages those of the first one.
+struct SharedGroups {
+  const int *cu, *prefix;
+  int n;
+};
+// What the tile kernel leaves of a group's prefix for the final sums: for the row
+// tile that starts at sequence b, and kv head h, parts[b Hkv + h] = {first CTA, 2 last
+// CTA + slot of the first} where CTAs share it (their raw sums in `raw`), or {-1, 0}
+// (normalised records [B, Hq][kSharedRec] in `recs`).
+struct SharedParts {
+  int2 *parts;
+  float *recs, *raw;
+};
+constexpr int kSharedRec = 260;  // O1 / l, O2 / l, sigma / l, log2-sum-exp, padding
+size_t shared_parts_bytes(int B, int Hq, int Hkv);
+SharedParts shared_parts(void *workspace, int B, int Hq, int Hkv);
+// Keys of the groups' prefixes (tile kernel), then those behind them and the sum.
+cudaError_t launch_shared_prefix(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
+                                 const int *seqlens, int Hq, const SharedParts &parts, cudaStream_t stream);
+cudaError_t launch_shared_rows(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
+                               const int *seqlens, int Hq, void *workspace, cudaStream_t stream);
+cudaError_t launch_shared_combine(const PagedCache &c, const SharedGroups &g, const int *seqlens, int Hq,
+                                  const void *rows_workspace, const SharedParts &parts, void *out,
+                                  cudaStream_t stream);
+
+// The bookkeeping of pages between two steps, and their compaction.
+size_t kv_update_workspace_bytes(int B, int num_pages, int max_pages);
+cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int *refs, const int *src,
+                             const int *lens, int *table_out, int *seqlens_out, int *refs_out,
+                             void *workspace, cudaStream_t stream);
+size_t kv_compact_workspace_bytes(int num_pages);
+cudaError_t launch_kv_compact(const PagedCache &c, const int *seqlens, const int *refs, int *table_out,
+                              int *refs_out, int *map, int *used, void *workspace, cudaStream_t stream);
+
 // Chunks of any length (tcgen05). lse ([T, Hq] fp32) may be null. Sequences of at
 // most `few` rows a kv head are left as they were.
 size_t paged_prefill_workspace_bytes();
@@ -141,6 +176,18 @@ cudaError_t launch_paged_prefill(const PagedCache &c, const void *q, const void 
                                  long long qhs, const int *seqlens, const int *cu_q, void *out,
                                  long long ots, long long ohs, float *lse, int T, int Hq, int few,
                                  void *workspace, cudaStream_t stream);
+
+// Rotary positions. heads[i] = 0: tensor i (q, k, r) is not there. Strides in
+// elements; near: pairs of neighbours, else of halves.
+struct RotaryTensor {
+  const void *in;
+  void *out;
+  long long in_seq, in_token, in_head, out_seq, out_token, out_head;
+};
+cudaError_t launch_rotary(const RotaryTensor (&t)[3], const int (&heads)[3], const int *positions,
+                          const int *seqlens, const int *cu_q, int nseq, const double *freq, float scale,
+                          bool backward, int B, int L, int d, int rotary_dim, bool near, bool f32,
+                          unsigned *err, cudaStream_t stream);
 
 cudaError_t launch_timeout_probe(long long limit_cycles, unsigned *err, cudaStream_t stream);
 

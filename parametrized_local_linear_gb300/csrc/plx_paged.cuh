@@ -71,6 +71,31 @@ __device__ __forceinline__ int row_sequence(const int *cu, int B, int t) {
   return cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
 }
 
+// Group `g`: its first sequence, sequences, and the keys that they share: none where
+// the first sequence does not have them (reported), no sequences where the ends do
+// not make sense.
+struct Group {
+  int first, n, prefix;
+};
+__device__ __forceinline__ Group group_of(const PagedCache &c, const SharedGroups &g, const int *seqlens, int i) {
+  const int first = g.cu[i], end = g.cu[i + 1], want = g.prefix[i];
+  if (first < 0 || end > c.B || end < first) {
+    if (c.err) atomicOr(c.err, kErrBadInput);
+    return Group{0, 0, 0};
+  }
+  Group r = {first, end - first, max(want, 0)};
+  if (r.n > 0 && r.prefix > cache_len(c, seqlens, first)) {
+    if (c.err) atomicOr(c.err, kErrBadInput);
+    r.prefix = 0;
+  }
+  return r;
+}
+// The group of sequence b; no sequences if it is in none.
+__device__ __forceinline__ Group group_with(const PagedCache &c, const SharedGroups &g, const int *seqlens, int b) {
+  const int i = row_sequence(g.cu, g.n, b);
+  return i < 0 ? Group{b, 0, 0} : group_of(c, g, seqlens, i);
+}
+
 // 2^(E - 127), 1 <= E <= 254.
 __device__ __forceinline__ float scale_of(uint32_t E) { return __uint_as_float(E << 23); }
 
