@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -827,54 +828,47 @@ def plx_rotary_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, origina
     return torch.tensor(list(freqs), dtype=torch.float64, device=device), scale.value
 
 
-def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale, outs, stream):
+_strides = struct.Struct("18q").pack
+
+
+def _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, outs):
+    """Raises for what is wrong with the tensors of a rotary call."""
     given = [(name, t, o) for name, t, o in zip("qkr", (q, k, r), outs) if t is not None]
     if not given:
         raise ValueError("q, k and r are all None")
-    x = given[0][1]
+    first, x = given[0][:2]
     dev, dtype, dims = x.device, x.dtype, x.dim()
     if dtype not in _ROTARY_DTYPES:
-        raise TypeError(f"{given[0][0]} must be torch.bfloat16 or torch.float32, got {dtype}")
+        raise TypeError(f"{first} must be torch.bfloat16 or torch.float32, got {dtype}")
     if dims not in (3, 4):
-        raise ValueError(f"{given[0][0]} must be [T, H, d] or [B, H, L, d], got shape {tuple(x.shape)}")
+        raise ValueError(f"{first} must be [T, H, d] or [B, H, L, d], got shape {tuple(x.shape)}")
     packed = dims == 3
     B, L, d = (1, x.shape[0], x.shape[2]) if packed else (x.shape[0], x.shape[2], x.shape[3])
-    heads, results = {}, [None] * 3
-    strides, ptrs = [0] * 18, [None] * 6
+    heads = {}
     for name, t, o in given:
         H = t.shape[1] if t.dim() == dims else 0
         shape = (L, H, d) if packed else (B, H, L, d)
         if t.shape != shape or heads.setdefault(name == "k", H) != H:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with {given[0][0]}'s "
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with {first}'s "
                              f"{tuple(x.shape)}")
         if o is not None and o.shape != shape:
             raise ValueError(f"{name}_out has shape {tuple(o.shape)}, expected {tuple(shape)}")
     for name, t, o in given:
-        at = "qkr".index(name)
-        if dev.type == "cuda" and o is None:
-            o = _empty(t.shape, dtype, dev, stream)
-        for what, y, place in ((name, t, at), (name + "_out", o, at + 3)):
+        for what, y in ((name, t), (name + "_out", o)):
+            if y is None:
+                continue
             if dev.type != "cuda" or y.get_device() != dev.index:
-                raise ValueError(f"{what} must be a CUDA tensor on the device of {given[0][0]} ({dev})")
+                raise ValueError(f"{what} must be a CUDA tensor on the device of {first} ({dev})")
             if y.dtype is not dtype:
                 raise TypeError(f"{what} must be {dtype}, got {y.dtype}")
-            st = y.stride()
-            if st[-1] != 1 and y.numel() > 0:
+            if y.stride()[-1] != 1 and y.numel() > 0:
                 raise ValueError(f"{what} must have its last dimension contiguous")
-            # (sequence, token, head)
-            strides[3 * place:3 * place + 3] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
-            ptrs[place] = y.data_ptr()
-        results[at] = o
-    half = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
-    _like(inv_freq, "inv_freq", torch.float64, (half,), dev)
+    _like(inv_freq, "inv_freq", torch.float64, (inv_freq.shape[0] if inv_freq.dim() == 1 else 0,), dev)
     if positions is not None:
         if seqlens is not None or cu_q is not None:
             raise ValueError("positions and seqlens / cu_q exclude each other")
         _like(positions, "positions", torch.int32, (L,) if packed else (B, L), dev)
-    elif seqlens is None and packed:
-        raise ValueError("packed rows need positions, or seqlens (and cu_q)")
-    nseq = 0
-    if seqlens is not None:
+    elif seqlens is not None:
         if not packed:
             raise ValueError("seqlens goes with packed rows [T, H, d]")
         nseq = seqlens.shape[0] if seqlens.dim() == 1 else 0
@@ -883,13 +877,76 @@ def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale,
             _like(cu_q, "cu_q", torch.int32, (nseq + 1,), dev)
     elif cu_q is not None:
         raise ValueError("cu_q without seqlens")
+    elif packed:
+        raise ValueError("packed rows need positions, or seqlens (and cu_q)")
+
+
+def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale, q_out, k_out, r_out,
+            stream):
+    # As for the paged calls: one lean pass over the tensors, and the checks that
+    # say why only where it finds something.
+    x = q if q is not None else k if k is not None else r
+    if x is None:
+        _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, (q_out, k_out, r_out))
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    packed = len(shape) == 3
+    good = index >= 0 and dtype in _ROTARY_DTYPES and (packed or len(shape) == 4)
+    if good:
+        B, L, d = (1, shape[0], shape[2]) if packed else (shape[0], shape[2], shape[3])
+        Hq = Hkv = 0
+        ptrs, strides, results = [None] * 6, [0] * 18, [None] * 3
+        for at, t, o in ((0, q, q_out), (1, k, k_out), (2, r, r_out)):
+            if t is None:
+                continue
+            ts = t.shape
+            if len(ts) != len(shape):
+                good = False
+                break
+            H = ts[1]
+            if at == 1:
+                Hkv = H
+            else:
+                good = good and (Hq == 0 or H == Hq)
+                Hq = H
+            st = t.stride()
+            good = (good and t.dtype is dtype and t.get_device() == index and st[-1] == 1
+                    and ts == ((L, H, d) if packed else (B, H, L, d)))
+            # (sequence, token, head)
+            strides[3 * at:3 * at + 3] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
+            if o is None:
+                strides[9 + 3 * at:12 + 3 * at] = (0, H * d, d) if packed else (H * L * d, d, L * d)
+            else:
+                st = o.stride()
+                good = (good and o.shape == ts and o.dtype is dtype and o.get_device() == index
+                        and st[-1] == 1)
+                strides[9 + 3 * at:12 + 3 * at] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
+            ptrs[at] = t.data_ptr()
+    nseq = 0
+    good = (good and inv_freq.dtype is torch.float64 and inv_freq.get_device() == index
+            and inv_freq.dim() == 1 and inv_freq.is_contiguous())
+    if positions is not None:
+        good = (good and seqlens is None and cu_q is None
+                and _is(positions, torch.int32, (L,) if packed else (B, L), index))
+    elif seqlens is not None:
+        if good:
+            nseq = seqlens.numel()
+            good = (packed and _is(seqlens, torch.int32, (nseq,), index)
+                    and (cu_q is None or _is(cu_q, torch.int32, (nseq + 1,), index)))
+    else:
+        good = good and cu_q is None and not packed
+    dev = x.device
+    if not good:
+        _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, (q_out, k_out, r_out))
+    for at, t, o in ((0, q, q_out), (1, k, k_out), (2, r, r_out)):
+        if t is not None:
+            results[at] = o = _empty(t.shape, dtype, dev, stream) if o is None else o
+            ptrs[3 + at] = o.data_ptr()
     if B > 0 and L > 0:
         _launch(fn, dev, stream,
-                (*ptrs, (_ll * 18)(*strides),
-                 positions.data_ptr() if positions is not None else None,
-                 seqlens.data_ptr() if seqlens is not None else None,
-                 cu_q.data_ptr() if cu_q is not None else None, inv_freq.data_ptr(), scale, nseq, B,
-                 L, heads.get(False, 1), heads.get(True, 1), d, 2 * half, int(bool(interleaved)),
+                (*ptrs, _strides(*strides), None if positions is None else positions.data_ptr(),
+                 None if seqlens is None else seqlens.data_ptr(),
+                 None if cu_q is None else cu_q.data_ptr(), inv_freq.data_ptr(), scale, nseq, B, L,
+                 Hq or 1, Hkv or 1, d, 2 * inv_freq.shape[0], 1 if interleaved else 0,
                  _ROTARY_DTYPES[dtype]))
     return tuple(results)
 
@@ -903,7 +960,7 @@ def plx_rotary_fwd(q, k, inv_freq, r=None, positions=None, seqlens=None, cu_q=No
     and ``cu_q`` (packed), or 0 .. L - 1. q, k or r may be None; ``q_out=q`` works in
     place. Returns (q, k, r) turned."""
     return _rotary(lib().plx_rotary_fwd, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved,
-                   scale, (q_out, k_out, r_out), stream)
+                   scale, q_out, k_out, r_out, stream)
 
 
 def plx_rotary_bwd(dq, dk, inv_freq, dr=None, positions=None, seqlens=None, cu_q=None,
@@ -912,7 +969,7 @@ def plx_rotary_bwd(dq, dk, inv_freq, dr=None, positions=None, seqlens=None, cu_q
     """Backward of plx_rotary_fwd (see include/plx.h): from the gradients of its outputs
     those of its inputs, with its other arguments. Returns (dq, dk, dr)."""
     return _rotary(lib().plx_rotary_bwd, dq, dk, dr, inv_freq, positions, seqlens, cu_q, interleaved,
-                   scale, (dq_out, dk_out, dr_out), stream)
+                   scale, dq_out, dk_out, dr_out, stream)
 
 
 def plx_decode_shared_workspace_bytes(B, Hq, Hkv, d) -> int:

@@ -25,33 +25,90 @@
 namespace plx {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int MAXR = 128;  // most rotated values of a row
 
 struct RotaryArgs {
-  RotaryTensor t[3];  // those that are there
-  int n0, n1, heads;  // heads of the first, of the first two, of all
+  RotaryTensor t[3];
+  int heads[3], blocks[3];  // heads of a tensor; blocks (of hpt heads) up to and with it
   const int *positions, *seqlens, *cu;
   const double *freq;
   float scale;
   int negate;  // backward
   int nseq, L, half, units, hpt;
   long long rows;
-  PagedCache c;  // err and the limit of lengths, for the lookup of positions
+  unsigned *err;
 };
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T x[V];
 };
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f32(float &y, float x) { y = x; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16 &y, float x) { y = __float2bfloat16_rn(x); }
+
+// The pairs of two vectors turned. bf16 halves: as packed pairs of pairs, half the
+// instructions; else one by one (NEAR: pair i is values 2 i, 2 i + 1 of both vectors
+// together).
+template <int V, bool NEAR>
+__device__ __forceinline__ void turn_pairs(Vec<float, V> &x0, Vec<float, V> &x1, const float (&co)[V],
+                                           const float (&si)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float &e0 = !NEAR ? x0.x[i] : 2 * i < V ? x0.x[(2 * i) % V] : x1.x[(2 * i) % V];
+    float &e1 = !NEAR ? x1.x[i] : 2 * i + 1 < V ? x0.x[(2 * i + 1) % V] : x1.x[(2 * i + 1) % V];
+    const float p = e0, q = e1;
+    e0 = p * co[i] - q * si[i];
+    e1 = q * co[i] + p * si[i];
+  }
+}
+template <int V, bool NEAR>
+__device__ __forceinline__ void turn_pairs(Vec<__nv_bfloat16, V> &x0, Vec<__nv_bfloat16, V> &x1, const float (&co)[V],
+                                           const float (&si)[V]) {
+  if constexpr (V == 1) {
+    Vec<float, 1> y0 = {__bfloat162float(x0.x[0])}, y1 = {__bfloat162float(x1.x[0])};
+    turn_pairs<1, NEAR>(y0, y1, co, si);
+    x0.x[0] = __float2bfloat16_rn(y0.x[0]);
+    x1.x[0] = __float2bfloat16_rn(y1.x[0]);
+  } else {
+    uint32_t w0[V / 2], w1[V / 2];
+    memcpy(w0, &x0, sizeof(w0));
+    memcpy(w1, &x1, sizeof(w1));
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if constexpr (!NEAR) {
+        const uint64_t p = f2(bf16lo(w0[i]), bf16hi(w0[i])), q = f2(bf16lo(w1[i]), bf16hi(w1[i]));
+        const uint64_t c = f2(co[2 * i], co[2 * i + 1]), s = f2(si[2 * i], si[2 * i + 1]);
+        const uint64_t n = f2(-si[2 * i], -si[2 * i + 1]);
+        w0[i] = pack_bf16x2(ffma2(q, n, fmul2(p, c)));
+        w1[i] = pack_bf16x2(ffma2(p, s, fmul2(q, c)));
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t &w = h ? w1[i] : w0[i];
+          const float p = bf16lo(w), q = bf16hi(w), c = co[h * (V / 2) + i], s = si[h * (V / 2) + i];
+          w = pack_bf16x2(p * c - q * s, q * c + p * s);
+        }
+      }
+    }
+    memcpy(&x0, w0, sizeof(w0));
+    memcpy(&x1, w1, sizeof(w1));
+  }
+}
+
+// A store that does not stay in L2 before others.
+template <typename T, int V>
+__device__ __forceinline__ void store_once(T *to, const Vec<T, V> &x) {
+  if constexpr (sizeof(x) == 16) {
+    uint4 w;
+    memcpy(&w, &x, 16);
+    __stcs(reinterpret_cast<uint4 *>(to), w);
+  } else {
+    *reinterpret_cast<Vec<T, V> *>(to) = x;
+  }
+}
 
 // T: element; V: values of a vector, at most 16 bytes; NEAR: neighbours are pairs.
 template <typename T, int V, bool NEAR>
-__global__ void __launch_bounds__(THREADS) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(THREADS, 8) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   __shared__ unsigned long long turns[MAXR / 2];
   for (int i = threadIdx.x; i < a.half; i += THREADS) {
     double t = a.freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
@@ -63,23 +120,51 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const __grid_constant__
   const long long row = g / a.units;
   const int u = static_cast<int>(g - row * a.units);
   if (row >= a.rows) return;
-  long long pos;
+  long long b = 0, t = row, pos;
+  if (a.L < a.rows) {
+    b = row / a.L;
+    t = row - b * a.L;
+  }
   if (a.positions != nullptr) {
     pos = a.positions[row];
   } else if (a.seqlens != nullptr) {
-    const int t = static_cast<int>(row), b = row_sequence(a.cu, a.nseq, t);
-    if (b < 0) return;  // behind the last sequence
-    const int first = a.cu ? a.cu[b] : b, end = a.cu ? a.cu[b + 1] : b + 1;
+    const int r = static_cast<int>(row), sq = row_sequence(a.cu, a.nseq, r);
+    if (sq < 0) return;  // behind the last sequence
+    const int first = a.cu ? a.cu[sq] : sq, end = a.cu ? a.cu[sq + 1] : sq + 1;
     if (first < 0 || end > a.rows) {
-      if (a.c.err) atomicOr(a.c.err, kErrBadInput);
+      if (a.err) atomicOr(a.err, kErrBadInput);
       return;
     }
-    pos = static_cast<long long>(max(a.seqlens[b], 0)) - end + t;
+    pos = static_cast<long long>(max(a.seqlens[sq], 0)) - end + r;
     if (pos < 0) return;  // padding
   } else {
-    pos = row % a.L;
+    pos = t;
   }
+  // This block's tensor and heads.
+  const int y = blockIdx.y, which = (y >= a.blocks[0]) + (y >= a.blocks[1]);
+  const RotaryTensor &w = a.t[which];
+  const int h0 = (y - (which == 0 ? 0 : a.blocks[which - 1])) * a.hpt, n = min(a.hpt, a.heads[which] - h0);
+  const T *in = static_cast<const T *>(w.in) + b * w.in_seq + t * w.in_token + h0 * w.in_head;
+  T *out = static_cast<T *>(w.out) + b * w.out_seq + t * w.out_token + h0 * w.out_head;
   const bool turn = u * V < a.half;
+  if (!turn && out == in) return;  // in place: values behind R stay
+  // Where this thread's two vectors are in a row.
+  const int at0 = turn && !NEAR ? u * V : turn ? 2 * u * V : 2 * a.half + 2 * (u - a.half / V) * V;
+  const int at1 = turn && !NEAR ? a.half + u * V : at0 + V;
+  in += at0;
+  out += at0;
+  const int apart = at1 - at0;
+  constexpr int N = 2;
+  Vec<T, V> x0[N], x1[N];
+  auto load = [&](int left) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) {
+        x0[i] = *reinterpret_cast<const Vec<T, V> *>(in + i * w.in_head);
+        x1[i] = *reinterpret_cast<const Vec<T, V> *>(in + i * w.in_head + apart);
+      }
+  };
+  load(n);  // on their way while the angles are worked out
   float co[V], si[V];
   if (turn) {
     const unsigned long long p = static_cast<unsigned long long>(a.negate ? -pos : pos);
@@ -89,58 +174,28 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const __grid_constant__
       const uint32_t quarter = (f + 0x20000000u) >> 30;
       float s, c;
       sincospif(static_cast<float>(static_cast<int>(f - (quarter << 30))) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-      const float x = (quarter & 1) ? s : c, y = (quarter & 1) ? c : s;
+      const float x = (quarter & 1) ? s : c, z = (quarter & 1) ? c : s;
       co[i] = (((quarter + 1) & 2) ? -x : x) * a.scale;
-      si[i] = ((quarter & 2) ? -y : y) * a.scale;
+      si[i] = ((quarter & 2) ? -z : z) * a.scale;
     }
   }
-  // Where this thread's two vectors are in a row.
-  const int at0 = turn && !NEAR ? u * V : turn ? 2 * u * V : 2 * a.half + 2 * (u - a.half / V) * V;
-  const int at1 = turn && !NEAR ? a.half + u * V : at0 + V;
-  const long long b = row / a.L, t = row - b * a.L;
-  const int h0 = blockIdx.y * a.hpt, h1 = min(h0 + a.hpt, a.heads);
-  constexpr int N = 4;
-  for (int h = h0; h < h1; h += N) {
-    Vec<T, V> x0[N], x1[N];
-    T *out[N];
+  for (int h = 0; h < n; h += N) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int hh = h + n;
-      out[n] = nullptr;
-      if (hh >= h1) continue;
-      const int which = (hh >= a.n0) + (hh >= a.n1), head = hh - (which == 0 ? 0 : which == 1 ? a.n0 : a.n1);
-      const RotaryTensor &w = a.t[which];
-      const T *in = static_cast<const T *>(w.in) + b * w.in_seq + t * w.in_token + head * w.in_head;
-      T *o = static_cast<T *>(w.out) + b * w.out_seq + t * w.out_token + head * w.out_head;
-      if (!turn && o == in) continue;  // in place: values behind R stay
-      out[n] = o;
-      x0[n] = *reinterpret_cast<const Vec<T, V> *>(in + at0);
-      x1[n] = *reinterpret_cast<const Vec<T, V> *>(in + at1);
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (out[n] == nullptr) continue;
-      if (turn) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          // NEAR: pair i is values 2 i, 2 i + 1 of the two vectors together.
-          T &e0 = !NEAR ? x0[n].x[i] : 2 * i < V ? x0[n].x[(2 * i) % V] : x1[n].x[(2 * i) % V];
-          T &e1 = !NEAR ? x1[n].x[i] : 2 * i + 1 < V ? x0[n].x[(2 * i + 1) % V] : x1[n].x[(2 * i + 1) % V];
-          const float p = to_f32(e0), q = to_f32(e1);
-          from_f32(e0, p * co[i] - q * si[i]);
-          from_f32(e1, q * co[i] + p * si[i]);
-        }
+    for (int i = 0; i < N; ++i)
+      if (h + i < n) {
+        if (turn) turn_pairs<V, NEAR>(x0[i], x1[i], co, si);
+        store_once(out + i * w.out_head, x0[i]);
+        store_once(out + i * w.out_head + apart, x1[i]);
       }
-      *reinterpret_cast<Vec<T, V> *>(out[n] + at0) = x0[n];
-      *reinterpret_cast<Vec<T, V> *>(out[n] + at1) = x1[n];
-    }
+    in += N * w.in_head;
+    out += N * w.out_head;
+    load(n - h - N);
   }
 }
 
 template <typename T, int V>
 cudaError_t launch(const RotaryArgs &a, bool near, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((a.rows * a.units + THREADS - 1) / THREADS),
-                  static_cast<unsigned>((a.heads + a.hpt - 1) / a.hpt));
+  const dim3 grid(static_cast<unsigned>((a.rows * a.units + THREADS - 1) / THREADS), static_cast<unsigned>(a.blocks[2]));
   if (near) rotary_kernel<T, V, true><<<grid, THREADS, 0, stream>>>(a);
   else rotary_kernel<T, V, false><<<grid, THREADS, 0, stream>>>(a);
   return cudaGetLastError();
@@ -153,16 +208,6 @@ cudaError_t launch_rotary(const RotaryTensor (&t)[3], const int (&heads)[3], con
                           bool backward, int B, int L, int d, int rotary_dim, bool near, bool f32,
                           unsigned *err, cudaStream_t stream) {
   RotaryArgs a = {};
-  int n = 0, ends[3] = {};
-  for (int i = 0; i < 3; ++i) {
-    if (heads[i] == 0) continue;
-    a.t[n] = t[i];
-    ends[n] = (n ? ends[n - 1] : 0) + heads[i];
-    ++n;
-  }
-  a.heads = ends[n - 1];
-  a.n0 = ends[0];
-  a.n1 = n > 1 ? ends[1] : a.heads;
   a.positions = positions;
   a.seqlens = seqlens;
   a.cu = cu_q;
@@ -173,18 +218,24 @@ cudaError_t launch_rotary(const RotaryTensor (&t)[3], const int (&heads)[3], con
   a.L = L;
   a.half = rotary_dim / 2;
   a.rows = static_cast<long long>(B) * L;
-  a.c.err = err;
+  a.err = err;
   // The widest vectors that the pairs' places allow (halves start at R / 2).
   int V = f32 ? 4 : 8;
   while (a.half % V != 0) V /= 2;
   a.units = d / (2 * V);
   // Heads a thread: one while that leaves SMs without threads (latency), up to
   // eight, which share their sines and cosines.
-  const long long items = a.rows * a.units * a.heads;
+  const int all = heads[0] + heads[1] + heads[2];
+  const long long items = a.rows * a.units * all;
   long long hpt = items / (static_cast<long long>(sm_count()) * 1024);
   hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
-  while ((a.heads + hpt - 1) / hpt > 65535) hpt *= 2;
+  while (all / hpt > 65000) hpt *= 2;
   a.hpt = static_cast<int>(hpt);
+  for (int i = 0, n = 0; i < 3; ++i) {
+    a.t[i] = t[i];
+    a.heads[i] = heads[i];
+    a.blocks[i] = n += (heads[i] + a.hpt - 1) / a.hpt;
+  }
   if (f32) {
     if (V == 4) return launch<float, 4>(a, near, stream);
     if (V == 2) return launch<float, 2>(a, near, stream);
