@@ -13,6 +13,7 @@ as one made there.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -556,17 +557,20 @@ def _launch(fn, dev, stream, args):
             _check(fn(*args, _stream(stream, dev)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(sizer, sizes, index):
+    """What the library's size function says on that device (it goes by its SM count)."""
+    with torch.cuda.device(index):
+        return getattr(lib(), sizer)(*sizes)
+
+
 def _workspace(workspace, sizer, sizes, stream, dev):
     """(tensor, pointer, bytes) of the caller's workspace, or of one of the
     needed size from torch's caching allocator, in the order of the call's stream (a
     stream-ordered allocation by the library would give its memory back to the
     driver whenever the GPU idles: 200 us for a call after a synchronize)."""
     if workspace is None:
-        if _current_device() == dev.index:  # the size goes by the device's SM count
-            need = getattr(lib(), sizer)(*sizes)
-        else:
-            with torch.cuda.device(dev):
-                need = getattr(lib(), sizer)(*sizes)
+        need = _workspace_bytes(sizer, sizes, dev.index)
         workspace = _empty(need, torch.uint8, dev, stream)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != dev:
@@ -717,21 +721,26 @@ def plx_decode_fwd_shared(q, r, kpages, vpages, block_table, seqlens, cu_g, pref
     if prefix_lens.dim() != 1 or prefix_lens.shape[0] < 1:
         raise ValueError(f"prefix_lens must be [ngroups], got shape {tuple(prefix_lens.shape)}")
     groups = prefix_lens.shape[0]
-    for name, t in (("r", r), ("out", out)):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
-    if cu_g.shape != (groups + 1,):
-        raise ValueError(f"cu_g must have shape ({groups + 1},), got {tuple(cu_g.shape)}")
+    index, bf16 = dev.index, torch.bfloat16
+    good = (_is(q, bf16, shape, index) and _is(r, bf16, shape, index)
+            and (out is None or _is(out, bf16, shape, index))
+            and _is(cu_g, torch.int32, (groups + 1,), index)
+            and _is(prefix_lens, torch.int32, (groups,), index))
+    if not good:
+        for name, t in (("r", r), ("out", out)):
+            if t is not None and t.shape != shape:
+                raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
+        if cu_g.shape != (groups + 1,):
+            raise ValueError(f"cu_g must have shape ({groups + 1},), got {tuple(cu_g.shape)}")
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
-    _like(q, "q", torch.bfloat16, shape, dev)
-    _like(r, "r", torch.bfloat16, shape, dev)
-    _like(cu_g, "cu_g", torch.int32, (groups + 1,), dev)
-    _like(prefix_lens, "prefix_lens", torch.int32, (groups,), dev)
+    if not good:
+        for name, t in (("q", q), ("r", r)) + ((("out", out),) if out is not None else ()):
+            _like(t, name, bf16, shape, dev)
+        _like(cu_g, "cu_g", torch.int32, (groups + 1,), dev)
+        _like(prefix_lens, "prefix_lens", torch.int32, (groups,), dev)
     if out is None:
-        out = _empty(shape, torch.bfloat16, dev, stream)
-    else:
-        _like(out, "out", torch.bfloat16, shape, dev)
+        out = _empty(shape, bf16, dev, stream)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_decode_shared_workspace_bytes",
                                       (B, Hq, Hkv, d), stream, dev)
     _launch(lib().plx_decode_fwd_shared, dev, stream,
@@ -756,23 +765,27 @@ def plx_kv_update(kpages, vpages, block_table, seqlens, page_refs, lens, src=Non
     dev = kpages.device
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
-    if any(t is None for t in outs):
-        if not all(t is None for t in outs):
+    if block_table_out is None or seqlens_out is None or page_refs_out is None:
+        if not (block_table_out is None and seqlens_out is None and page_refs_out is None):
             raise ValueError("block_table_out, seqlens_out and page_refs_out must be given all or none")
         outs = block_table, seqlens, page_refs
-    _like(page_refs, "page_refs", torch.int32, (n,), dev)
-    _like(lens, "lens", torch.int32, (B,), dev)
-    if src is not None:
-        _like(src, "src", torch.int32, (B,), dev)
-    _like(outs[0], "block_table_out", torch.int32, (B, width), dev)
-    _like(outs[1], "seqlens_out", torch.int32, (B,), dev)
-    _like(outs[2], "page_refs_out", torch.int32, (n,), dev)
+    i32, index = torch.int32, dev.index
+    if not (_is(page_refs, i32, (n,), index) and _is(lens, i32, (B,), index)
+            and (src is None or _is(src, i32, (B,), index)) and _is(outs[0], i32, (B, width), index)
+            and _is(outs[1], i32, (B,), index) and _is(outs[2], i32, (n,), index)):
+        _like(page_refs, "page_refs", i32, (n,), dev)
+        _like(lens, "lens", i32, (B,), dev)
+        if src is not None:
+            _like(src, "src", i32, (B,), dev)
+        _like(outs[0], "block_table_out", i32, (B, width), dev)
+        _like(outs[1], "seqlens_out", i32, (B,), dev)
+        _like(outs[2], "page_refs_out", i32, (n,), dev)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_kv_update_workspace_bytes", (B, n, width),
                                       stream, dev)
     _launch(lib().plx_kv_update, dev, stream,
             (*ptrs, seqlens.data_ptr(), page_refs.data_ptr(),
-             src.data_ptr() if src is not None else None, lens.data_ptr(),
-             *(t.data_ptr() for t in outs), B, Hkv, d, n, page, width, ws_ptr, ws_bytes))
+             src.data_ptr() if src is not None else None, lens.data_ptr(), outs[0].data_ptr(),
+             outs[1].data_ptr(), outs[2].data_ptr(), B, Hkv, d, n, page, width, ws_ptr, ws_bytes))
     return outs
 
 
@@ -789,24 +802,28 @@ def plx_kv_compact(kpages, vpages, block_table, seqlens, page_refs, kscale=None,
     dev = kpages.device
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
-    if any(t is None for t in outs):
-        if not all(t is None for t in outs):
+    if block_table_out is None or page_refs_out is None:
+        if not (block_table_out is None and page_refs_out is None):
             raise ValueError("block_table_out and page_refs_out must be given both or neither")
         outs = block_table, page_refs
-    _like(page_refs, "page_refs", torch.int32, (n,), dev)
-    _like(outs[0], "block_table_out", torch.int32, (B, width), dev)
-    _like(outs[1], "page_refs_out", torch.int32, (n,), dev)
+    i32, index = torch.int32, dev.index
+    if not (_is(page_refs, i32, (n,), index) and _is(outs[0], i32, (B, width), index)
+            and _is(outs[1], i32, (n,), index) and (page_map is None or _is(page_map, i32, (n,), index))
+            and (used is None or _is(used, i32, (1,), index))):
+        _like(page_refs, "page_refs", i32, (n,), dev)
+        _like(outs[0], "block_table_out", i32, (B, width), dev)
+        _like(outs[1], "page_refs_out", i32, (n,), dev)
+        if page_map is not None:
+            _like(page_map, "page_map", i32, (n,), dev)
+        if used is not None:
+            _like(used, "used", i32, (1,), dev)
     if page_map is None:
-        page_map = _empty((n,), torch.int32, dev, stream)
-    else:
-        _like(page_map, "page_map", torch.int32, (n,), dev)
+        page_map = _empty((n,), i32, dev, stream)
     if used is None:
-        used = _empty((1,), torch.int32, dev, stream)
-    else:
-        _like(used, "used", torch.int32, (1,), dev)
+        used = _empty((1,), i32, dev, stream)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_kv_compact_workspace_bytes", (n,), stream, dev)
     _launch(lib().plx_kv_compact, dev, stream,
-            (*ptrs, seqlens.data_ptr(), page_refs.data_ptr(), *(t.data_ptr() for t in outs),
+            (*ptrs, seqlens.data_ptr(), page_refs.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
              page_map.data_ptr(), used.data_ptr(), B, Hkv, d, n, page, width, ws_ptr, ws_bytes))
     return (*outs, page_map, used)
 

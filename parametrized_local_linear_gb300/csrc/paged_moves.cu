@@ -26,6 +26,7 @@ struct UpdateArgs {
   int *table_out, *seqlens_out, *refs_out;
   Row *rows;
   int *free_list;
+  int *counts;  // free pages of every block's segment
   int *stage;  // old entries of the rows when the tables are updated in place, else null
 };
 
@@ -35,45 +36,19 @@ __device__ __forceinline__ bool good_page(const PagedCache &c, int page) {
   return false;
 }
 
-// A block for each row: what it keeps, and the reference counts without partial
-// last pages.
-__global__ void __launch_bounds__(THREADS) update_count_kernel(const UpdateArgs a) {
-  const int b = blockIdx.x, P = 1 << a.c.page_shift;
-  const int old = cache_len(a.c, a.seqlens, b);
-  int s = a.src != nullptr ? a.src[b] : b, want = max(a.lens[b], 0);
-  if (s < -1 || s >= a.c.B || want > (static_cast<long long>(a.c.max_pages) << a.c.page_shift)) {
-    if (threadIdx.x == 0 && a.c.err) atomicOr(a.c.err, kErrBadInput);
-    s = b;
-    want = old;
-  }
-  const int have = s >= 0 ? cache_len(a.c, a.seqlens, s) : 0;
-  const int kept = min(want, have), full = kept >> a.c.page_shift;
-  int part = kept & (P - 1);
-  const int *mine = a.c.table + static_cast<long long>(b) * a.c.max_pages;
-  const int *from = a.c.table + static_cast<long long>(max(s, 0)) * a.c.max_pages;
-  const int before = (old + P - 1) >> a.c.page_shift;
-  for (int j = (s == b ? full : 0) + threadIdx.x; j < before; j += THREADS)
-    if (good_page(a.c, mine[j])) atomicSub(&a.refs_out[mine[j]], 1);
-  if (s != b)
-    for (int j = threadIdx.x; j < full; j += THREADS)
-      if (good_page(a.c, from[j])) atomicAdd(&a.refs_out[from[j]], 1);
-  if (a.stage != nullptr && s != b)
-    for (int j = threadIdx.x; j < full; j += THREADS)
-      a.stage[static_cast<long long>(b) * a.c.max_pages + j] = from[j];
-  if (threadIdx.x == 0) {
-    int tail = part > 0 ? from[full] : -1;
-    if (part > 0 && !good_page(a.c, tail)) part = 0, tail = -1;
-    Row r = {s, full, part, tail, 0, 0, want, 0};
-    a.rows[b] = r;
-  }
+// A cluster works out both plans: their phases are a few hundred nanoseconds each,
+// and a barrier between them costs less than a launch.
+constexpr int CL = 8, PLAN = 1024;
+
+// The cluster's blocks are the grid's.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int PLAN = 1024;
-
-// Exclusive prefix sum of x over the block, and its total.
+// Exclusive prefix sum of x over a block of PLAN threads, and its total.
 template <typename T>
 __device__ __forceinline__ T block_scan(T x, T *total) {
-  __shared__ T sums[PLAN / 32];
+  __shared__ T sums[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   T inc = x;
 #pragma unroll
@@ -84,71 +59,197 @@ __device__ __forceinline__ T block_scan(T x, T *total) {
   __syncthreads();  // an earlier call's sums have been read
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  T before = 0, all = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
+  T all = sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T v = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += v;
   }
-  *total = all;
-  return before + inc - x;
+  *total = __shfl_sync(0xffffffffu, all, 31);
+  const T before = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
+  return (warp > 0 ? before : T(0)) + inc - x;
 }
 
-// One block: which rows keep their partial last page (the first row of those that
-// have it, if no row has all of it), how many fresh pages each needs, and which.
-__global__ void __launch_bounds__(PLAN) update_plan_kernel(const UpdateArgs a) {
-  const int P = 1 << a.c.page_shift, B = a.c.B;
-  for (int b = threadIdx.x; b < B; b += PLAN) {
-    const int tail = a.rows[b].tail;
+// Four flags of a thread, those of places k PLAN + thread (k < 4), as prefix sums over
+// the places in their order: at[k], and the sum of all.
+__device__ __forceinline__ int flags_scan(const bool (&flag)[4], int (&at)[4]) {
+  unsigned long long x = 0, all;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x |= static_cast<unsigned long long>(flag[k]) << (16 * k);  // at most PLAN in each field
+  const unsigned long long before = block_scan<unsigned long long>(x, &all);
+  int sum = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    at[k] = sum + static_cast<int>((before >> (16 * k)) & 0xffffu);
+    sum += static_cast<int>((all >> (16 * k)) & 0xffffu);
+  }
+  return sum;
+}
+
+// The block's pages of all of them: [*p0, returned).
+__device__ __forceinline__ int segment(int pages, int *p0) {
+  const long long each = (static_cast<long long>(pages) + CL * PLAN - 1) / (CL * PLAN) * PLAN;
+  *p0 = static_cast<int>(min(each * blockIdx.x, static_cast<long long>(pages)));
+  return static_cast<int>(min(each * (blockIdx.x + 1), static_cast<long long>(pages)));
+}
+
+// A part of row b: what it keeps, and the reference counts without partial last pages.
+__device__ __forceinline__ void count_row(const UpdateArgs &a, int b, int part_of, int parts) {
+  const int P = 1 << a.c.page_shift, lane = threadIdx.x & 31;
+  const int own = a.seqlens[b], wanted = a.lens[b];
+  int s = a.src != nullptr ? a.src[b] : b, want = max(wanted, 0);
+  const int old = checked_len(a.c, own);
+  if (s < -1 || s >= a.c.B || want > (static_cast<long long>(a.c.max_pages) << a.c.page_shift)) {
+    if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrBadInput);
+    s = b;
+    want = old;
+  }
+  const int have = s == b ? old : s >= 0 ? cache_len(a.c, a.seqlens, s) : 0;
+  const int kept = min(want, have), full = kept >> a.c.page_shift;
+  int part = kept & (P - 1);
+  const int *mine = a.c.table + static_cast<long long>(b) * a.c.max_pages;
+  const int *from = a.c.table + static_cast<long long>(max(s, 0)) * a.c.max_pages;
+  const int before = (old + P - 1) >> a.c.page_shift, first = 32 * part_of + lane, step = 32 * parts;
+#pragma unroll 4
+  for (int j = (s == b ? full : 0) + first; j < before; j += step) {
+    const int p = mine[j];
+    if (good_page(a.c, p)) atomicSub(&a.refs_out[p], 1);
+  }
+  if (s != b) {
+    int *stage = a.stage != nullptr ? a.stage + static_cast<long long>(b) * a.c.max_pages : nullptr;
+#pragma unroll 4
+    for (int j = first; j < full; j += step) {
+      const int p = from[j];
+      if (good_page(a.c, p)) atomicAdd(&a.refs_out[p], 1);
+      if (stage != nullptr) stage[j] = p;
+    }
+  }
+  if (first == 0) {
+    int tail = part > 0 ? from[full] : -1;
+    if (part > 0 && !good_page(a.c, tail)) part = 0, tail = -1;
+    const Row r = {s, full, part, tail, 0, 0, want, 0};
+    a.rows[b] = r;
+  }
+}
+
+// What another block of the cluster wrote: from L2.
+__device__ __forceinline__ Row load_row(const Row *r) {
+  Row x;
+  const int4 lo = __ldcg(reinterpret_cast<const int4 *>(r)), hi = __ldcg(reinterpret_cast<const int4 *>(r) + 1);
+  memcpy(&x, &lo, 16);
+  memcpy(reinterpret_cast<char *>(&x) + 16, &hi, 16);
+  return x;
+}
+
+// One cluster: reference counts; which rows keep their partial last page (the first
+// row of those that have it, if no row has all of it: the rows claim it by their
+// number, in place of the count 0); how many fresh pages each needs, and which.
+__global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kernel(const UpdateArgs a) {
+  const int P = 1 << a.c.page_shift, B = a.c.B, rank = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.refs != a.refs_out) {
+    for (int p = rank * PLAN + threadIdx.x; p < a.c.num_pages; p += CL * PLAN) a.refs_out[p] = a.refs[p];
+    cluster_sync();
+  }
+  constexpr int WARPS = CL * PLAN / 32;
+  const int parts = max(1, WARPS / B);
+  for (int task = rank * (PLAN / 32) + (threadIdx.x >> 5); task < B * parts; task += WARPS)
+    count_row(a, task / parts, task % parts, parts);
+  cluster_sync();
+  for (int b = rank * PLAN + threadIdx.x; b < B; b += CL * PLAN) {
+    const int tail = __ldcg(&a.rows[b].tail);
     if (tail < 0) continue;
     const int v = __ldcg(&a.refs_out[tail]);
     if (v == 0 || v < INT_MIN / 2) atomicMin(&a.refs_out[tail], INT_MIN + b);
   }
-  __syncthreads();
+  cluster_sync();
+  // Every block sums the rows' needs; the first writes them down.
   long long total = 0;
   for (int b0 = 0; b0 < B; b0 += PLAN) {
     const int b = b0 + threadIdx.x;
     int need = 0;
+    Row r;
     if (b < B) {
-      Row r = a.rows[b];
+      r = load_row(&a.rows[b]);
       r.keep = r.tail >= 0 && __ldcg(&a.refs_out[r.tail]) == INT_MIN + b;
       r.copies = r.tail >= 0 && !r.keep;
       need = ((r.new_len + P - 1) >> a.c.page_shift) - r.full - r.keep;
-      a.rows[b] = r;
     }
     long long all;
     const long long at = total + block_scan<long long>(need, &all);
-    if (b < B) a.rows[b].start = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
+    if (b < B && rank == 0) {
+      r.start = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
+      a.rows[b] = r;
+    }
     total += all;
   }
-  __syncthreads();
-  // The lowest free pages, as many as are needed.
-  int found = 0;
-  for (int p0 = 0; p0 < a.c.num_pages && found < total; p0 += PLAN) {
-    const int p = p0 + threadIdx.x;
-    const bool is_free = p < a.c.num_pages && __ldcg(&a.refs_out[p]) == 0;
+  int p0, found = 0;
+  const int p1 = segment(a.c.num_pages, &p0);
+  if (total > 0) {
+    int mine = 0;
+    for (int p = p0 + threadIdx.x; p < p1; p += PLAN) mine += __ldcg(&a.refs_out[p]) == 0;
     int all;
-    const int at = found + block_scan<int>(is_free, &all);
-    if (is_free) a.free_list[at] = p;
-    found += all;
-  }
-  __syncthreads();
-  for (int b = threadIdx.x; b < B; b += PLAN) {
-    Row r = a.rows[b];
-    const int need = ((r.new_len + P - 1) >> a.c.page_shift) - r.full - r.keep;
-    if (need > 0 && static_cast<long long>(r.start) + need > found) {  // no pages for it
-      r.new_len = (r.full << a.c.page_shift) + (r.keep ? r.part : 0);
-      r.copies = 0;
-      a.rows[b] = r;
-    } else {
-      for (int i = 0; i < need; ++i) a.refs_out[a.free_list[r.start + i]] = 1;
+    block_scan<int>(mine, &all);
+    if (threadIdx.x == 0) a.counts[rank] = all;
+    cluster_sync();
+    int below = 0;
+    for (int i = 0; i < CL; ++i) {
+      const int n = __ldcg(&a.counts[i]);
+      if (i < rank) below += n;
+      found += n;
     }
-    if (r.keep) a.refs_out[r.tail] = 1;
+    // Where the free pages do not do: the rows from the first one that they do not serve on.
+    long long granted = total;
+    if (total > found) {
+      __shared__ int least;
+      if (threadIdx.x == 0) least = found;
+      __syncthreads();
+      for (int b = threadIdx.x; b < B; b += PLAN) {
+        const Row r = load_row(&a.rows[b]);
+        const int need = ((r.new_len + P - 1) >> a.c.page_shift) - r.full - r.keep;
+        if (need > 0 && static_cast<long long>(r.start) + need > found) atomicMin(&least, r.start);
+      }
+      __syncthreads();
+      granted = least;
+    }
+    // The lowest free pages, as many as are granted.
+    for (int q0 = p0; q0 < p1 && below < granted; q0 += 4 * PLAN) {
+      bool is_free[4];
+      int at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int p = q0 + k * PLAN + threadIdx.x;
+        is_free[k] = p < p1 && __ldcg(&a.refs_out[p]) == 0;
+      }
+      const int n = flags_scan(is_free, at);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (is_free[k] && below + at[k] < granted) {
+          const int p = q0 + k * PLAN + threadIdx.x;
+          a.free_list[below + at[k]] = p;
+          a.refs_out[p] = 1;
+        }
+      below += n;
+    }
+  }
+  // The first block's rows: without pages where there are none.
+  if (rank == 0) {
+    for (int b = threadIdx.x; b < B; b += PLAN) {
+      const Row r = a.rows[b];  // this thread's
+      const int need = ((r.new_len + P - 1) >> a.c.page_shift) - r.full - r.keep;
+      if (need > 0 && static_cast<long long>(r.start) + need > found) {
+        a.rows[b].new_len = (r.full << a.c.page_shift) + (r.keep ? r.part : 0);
+        a.rows[b].copies = 0;
+      }
+      if (r.keep) a.refs_out[r.tail] = 1;
+    }
   }
 }
 
 // Blocks of a row: one writes its entries, one a kv head copies its partial page.
 __global__ void __launch_bounds__(THREADS) update_move_kernel(const UpdateArgs a) {
   const int b = blockIdx.x / (a.c.Hkv + 1), job = blockIdx.x - b * (a.c.Hkv + 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Row r = a.rows[b];
   const int shift = a.c.page_shift;
   if (job == 0) {
@@ -173,7 +274,15 @@ __global__ void __launch_bounds__(THREADS) update_move_kernel(const UpdateArgs a
     uint8_t *pages = const_cast<uint8_t *>(static_cast<const uint8_t *>(kv ? a.c.v : a.c.k));
     const uint4 *x = reinterpret_cast<const uint4 *>(pages + src * bytes);
     uint4 *y = reinterpret_cast<uint4 *>(pages + dst * bytes);
-    for (int i = threadIdx.x; i < n; i += THREADS) y[i] = x[i];
+    for (int i = threadIdx.x; i < n; i += 4 * THREADS) {
+      uint4 w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * THREADS < n) w[k] = x[i + k * THREADS];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * THREADS < n) y[i + k * THREADS] = w[k];
+    }
     if (a.c.kscale != nullptr) {
       uint8_t *scale = const_cast<uint8_t *>(kv ? a.c.vscale : a.c.kscale);
       for (int i = threadIdx.x; i < r.part; i += THREADS) scale[dst + i] = scale[src + i];
@@ -182,73 +291,59 @@ __global__ void __launch_bounds__(THREADS) update_move_kernel(const UpdateArgs a
 }
 
 // ---------------------------------------------------------------- compaction
-constexpr int CHUNK = 4096;  // pages of a block
-
 struct CompactArgs {
   PagedCache c;
   const int *seqlens, *refs;
   int *table_out, *refs_out, *map, *used;
-  int *counts;   // used pages of every chunk
+  int *counts;   // used pages of every block's segment, then:
   int *base;     // used pages below page number U = used[0]: the moves are its others
   int *holes;    // free pages below U, ascending
   int *by_rank;  // used page of a rank, from U on
   int *rank;     // used pages in front of a used page (-1: free)
-  int chunks;
 };
 
-__device__ __forceinline__ int block_sum(int x) {
-  __shared__ int sums[THREADS / 32];
-  x = __reduce_add_sync(0xffffffffu, x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) all += sums[w];
-  return all;
-}
-
-__global__ void __launch_bounds__(THREADS) compact_count_kernel(const CompactArgs a) {
-  int n = 0;
-  const int p0 = blockIdx.x * CHUNK;
-#pragma unroll
-  for (int i = 0; i < CHUNK / THREADS; ++i) {
-    const int p = p0 + i * THREADS + threadIdx.x;
-    n += p < a.c.num_pages && a.refs[p] > 0;
-  }
-  n = block_sum(n);
-  if (threadIdx.x == 0) a.counts[blockIdx.x] = n;
-}
-
-__global__ void __launch_bounds__(THREADS) compact_rank_kernel(const CompactArgs a) {
-  int below = 0, all = 0;
-  for (int i = threadIdx.x; i < a.chunks; i += THREADS) {
-    const int n = a.counts[i];
-    all += n;
+__global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) compact_plan_kernel(const CompactArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int p0, mine = 0, all;
+  const int p1 = segment(a.c.num_pages, &p0);
+  for (int p = p0 + threadIdx.x; p < p1; p += PLAN) mine += a.refs[p] > 0;
+  block_scan<int>(mine, &all);
+  if (threadIdx.x == 0) a.counts[blockIdx.x] = all;
+  cluster_sync();
+  int below = 0, U = 0;
+  for (int i = 0; i < CL; ++i) {
+    const int n = __ldcg(&a.counts[i]);
     if (i < static_cast<int>(blockIdx.x)) below += n;
+    U += n;
   }
-  below = block_sum(below);
-  const int U = block_sum(all);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.used[0] = U;
     if (U == a.c.num_pages) *a.base = U;
   }
-  const int p0 = blockIdx.x * CHUNK;
-  for (int i = 0; i < CHUNK / THREADS; ++i) {
-    const int p = p0 + i * THREADS + threadIdx.x;
-    const bool is_used = p < a.c.num_pages && a.refs[p] > 0;
-    int n;
-    const int rank = below + block_scan<int>(is_used, &n);
+  for (int q0 = p0; q0 < p1; q0 += 4 * PLAN) {
+    bool is_used[4];
+    int at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = q0 + k * PLAN + threadIdx.x;
+      is_used[k] = p < p1 && a.refs[p] > 0;
+    }
+    const int n = flags_scan(is_used, at);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = q0 + k * PLAN + threadIdx.x, rank = below + at[k];
+      if (p >= p1) continue;
+      if (p == U) *a.base = rank;
+      a.rank[p] = is_used[k] ? rank : -1;
+      if (p < U && !is_used[k]) a.holes[p - rank] = p;
+      if (p >= U && is_used[k]) a.by_rank[rank] = p;
+    }
     below += n;
-    if (p >= a.c.num_pages) continue;
-    if (p == U) *a.base = rank;
-    a.rank[p] = is_used ? rank : -1;
-    if (p < U && !is_used) a.holes[p - rank] = p;
-    if (p >= U && is_used) a.by_rank[rank] = p;
   }
 }
 
 __global__ void __launch_bounds__(THREADS) compact_move_kernel(const CompactArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int U = a.used[0], base = *a.base, moves = U - base;
   const long long step = static_cast<long long>(gridDim.x) * THREADS;
   const long long first = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
@@ -302,10 +397,26 @@ __global__ void __launch_bounds__(THREADS) compact_move_kernel(const CompactArgs
 
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// A kernel that waits by itself for the one in front of it.
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), unsigned grid, const Args &a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 }  // namespace
 
 size_t kv_update_workspace_bytes(int B, int num_pages, int max_pages) {
-  return round256(size_t(B) * sizeof(Row)) + round256(size_t(num_pages) * 4) + size_t(B) * max_pages * 4;
+  return round256(size_t(B) * sizeof(Row)) + round256(CL * 4) + round256(size_t(num_pages) * 4) +
+         size_t(B) * max_pages * 4;
 }
 
 cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int *refs, const int *src,
@@ -323,22 +434,18 @@ cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int 
   char *ws = static_cast<char *>(workspace);
   a.rows = reinterpret_cast<Row *>(ws);
   ws += round256(size_t(c.B) * sizeof(Row));
+  a.counts = reinterpret_cast<int *>(ws);
+  ws += round256(CL * 4);
   a.free_list = reinterpret_cast<int *>(ws);
   ws += round256(size_t(c.num_pages) * 4);
   a.stage = table_out == c.table ? reinterpret_cast<int *>(ws) : nullptr;
-  if (refs_out != refs) {
-    cudaError_t e = cudaMemcpyAsync(refs_out, refs, size_t(c.num_pages) * 4, cudaMemcpyDeviceToDevice, stream);
-    if (e != cudaSuccess) return e;
-  }
-  update_count_kernel<<<c.B, THREADS, 0, stream>>>(a);
-  update_plan_kernel<<<1, PLAN, 0, stream>>>(a);
-  update_move_kernel<<<c.B * (c.Hkv + 1), THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  update_plan_kernel<<<CL, PLAN, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_after(update_move_kernel, static_cast<unsigned>(c.B) * (c.Hkv + 1), a, stream);
 }
 
 size_t kv_compact_workspace_bytes(int num_pages) {
-  const size_t chunks = (size_t(num_pages) + CHUNK - 1) / CHUNK;
-  return round256((chunks + 1) * 4) + 3 * round256(size_t(num_pages) * 4);
+  return round256((CL + 1) * 4) + 3 * round256(size_t(num_pages) * 4);
 }
 
 cudaError_t launch_kv_compact(const PagedCache &c, const int *seqlens, const int *refs, int *table_out,
@@ -351,20 +458,18 @@ cudaError_t launch_kv_compact(const PagedCache &c, const int *seqlens, const int
   a.refs_out = refs_out;
   a.map = map;
   a.used = used;
-  a.chunks = (c.num_pages + CHUNK - 1) / CHUNK;
   char *ws = static_cast<char *>(workspace);
   a.counts = reinterpret_cast<int *>(ws);
-  a.base = a.counts + a.chunks;
-  ws += round256(size_t(a.chunks + 1) * 4);
+  a.base = a.counts + CL;
+  ws += round256((CL + 1) * 4);
   a.holes = reinterpret_cast<int *>(ws);
   ws += round256(size_t(c.num_pages) * 4);
   a.by_rank = reinterpret_cast<int *>(ws);
   ws += round256(size_t(c.num_pages) * 4);
   a.rank = reinterpret_cast<int *>(ws);
-  compact_count_kernel<<<a.chunks, THREADS, 0, stream>>>(a);
-  compact_rank_kernel<<<a.chunks, THREADS, 0, stream>>>(a);
-  compact_move_kernel<<<8 * sm_count(), THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  compact_plan_kernel<<<CL, PLAN, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_after(compact_move_kernel, 8u * sm_count(), a, stream);
 }
 
 }  // namespace plx
