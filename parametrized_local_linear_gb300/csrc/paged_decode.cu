@@ -79,7 +79,12 @@ constexpr int OFF_BAR = OFF_MLS + NCW * RW * 16;
 constexpr int OFF_FLAG = OFF_BAR + 2 * NST * 8;
 constexpr int OFF_PLAN = OFF_FLAG + 16;
 constexpr int OFF_HELD = OFF_PLAN + 64;  // [NCW] stage that holds a warp's sums
-constexpr size_t ROWS_SMEM = OFF_HELD + 16 + 1024;
+// SUFFIX: keys and first own key of the first sequences, looked up by all threads at
+// once (what goes over the sequences, plan and walks, finds them here).
+constexpr int OFF_KNOWN = OFF_HELD + 16;
+constexpr int KNOWN = 512;
+template <bool SUFFIX>
+constexpr size_t ROWS_SMEM = OFF_KNOWN + (SUFFIX ? KNOWN * 8 : 0) + 1024;
 static_assert(2 * TILE == 2 * RW * 2 * D * 4, "a stage holds the sums of two warps");
 constexpr int kCtasPerSm = 3;  // 128 registers a thread, 72 KB of shared memory
 
@@ -108,18 +113,24 @@ struct Seq {
   int len, tiles, first, n, ng;
   int start;  // SUFFIX: the first key; its tile is the sequence's first
 };
+// Keys of sequence b, and the first that its group does not share.
+__device__ __forceinline__ int2 own_keys(const RowsArgs &a, int b) {
+  const int len = cache_len(a.c, a.seqlens, b);
+  return make_int2(len, min(group_with(a.c, a.groups, a.seqlens, b).prefix, len));
+}
 template <int KT, int GS, bool SUFFIX>
-__device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b) {
+__device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b, const int2 *known) {
+  if constexpr (SUFFIX) {  // one token each
+    const int2 x = b < KNOWN ? known[b] : own_keys(a, b);
+    const int tiles = x.y < x.x ? (x.x + KT - 1) / KT - x.y / KT : 0;
+    return Seq{x.x, tiles, b, 1, (a.G + GS - 1) / GS, x.y};
+  }
   // All loads first: they share one latency.
   const int n = a.seqlens[b], first = a.cu != nullptr ? a.cu[b] : b, end = a.cu != nullptr ? a.cu[b + 1] : b + 1;
   Seq s;
   s.len = checked_len(a.c, n);
   s.tiles = (s.len + KT - 1) / KT;
   s.start = 0;
-  if constexpr (SUFFIX) {
-    s.start = min(group_with(a.c, a.groups, a.seqlens, b).prefix, s.len);
-    s.tiles = s.start < s.len ? s.tiles - s.start / KT : 0;
-  }
   s.first = first;
   s.n = 0;
   if (first < 0 || end > a.T || end < first) {
@@ -139,6 +150,17 @@ __device__ __forceinline__ long long groups_before(int first, int b, int G, int 
   return most > 0 ? static_cast<long long>(b) * (most / gs) : static_cast<long long>(first) * G / gs + b;
 }
 
+// What an item costs besides its tiles (its queries, its merge, its records), in
+// tiles: a row of a sequence counts as so many more where sequences may be short
+// (SUFFIX), so that a share of many short rows is not the last to end.
+template <bool SUFFIX>
+constexpr int kRowCost = SUFFIX ? 8 : 0;
+// A sequence's part of the stream that is cut into shares.
+template <bool SUFFIX>
+__device__ __forceinline__ long long units(const Seq &s, const RowsArgs &a) {
+  return s.tiles > 0 ? static_cast<long long>(s.tiles + kRowCost<SUFFIX>) * s.ng * a.c.Hkv : 0;
+}
+
 // One item: tiles [t0, t1) (of those from `start` on) of row group grp of kv head kvh of
 // sequence b.
 struct Item {
@@ -152,27 +174,34 @@ struct Walk {
   long long pos, e, base;
   int b;
   Seq s;
-  __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a)
-      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, SUFFIX>(a, p.b0)) {}
+  const int2 *known;
+  __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a, const int2 *known_)
+      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, SUFFIX>(a, p.b0, known_)), known(known_) {}
   __device__ __forceinline__ bool next(Item &it, const RowsArgs &a) {
-    if (pos >= e) return false;
-    // Positions below W all lie in some sequence, so b stays below B here.
-    while (true) {
-      const long long end = base + static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
-      if (pos < end) break;
-      base = end;
-      s = seq_of<KT, GS, SUFFIX>(a, ++b);
-    }
-    const long long off = pos - base;
-    const int vh = static_cast<int>(off / s.tiles);
+    constexpr int X = kRowCost<SUFFIX>;
+    int vh, t0, t1;
+    do {
+      if (pos >= e) return false;
+      // Positions below W all lie in some sequence, so b stays below B here.
+      while (true) {
+        const long long end = base + units<SUFFIX>(s, a);
+        if (pos < end) break;
+        base = end;
+        s = seq_of<KT, GS, SUFFIX>(a, ++b, known);
+      }
+      const long long off = pos - base;
+      vh = static_cast<int>(off / (s.tiles + X));
+      t0 = static_cast<int>(off - static_cast<long long>(vh) * (s.tiles + X)) - X;
+      t1 = static_cast<int>(min(static_cast<long long>(s.tiles), t0 + (e - pos)));
+      pos += t1 - t0;
+    } while (SUFFIX && t1 <= 0);  // no tile: only of what stands for the row's fixed cost
     it.s = s;
     it.b = b;
     it.kvh = vh / s.ng;
     it.grp = vh - it.kvh * s.ng;
-    it.t0 = static_cast<int>(off - static_cast<long long>(vh) * s.tiles);
-    it.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), it.t0 + (e - pos)));
+    it.t0 = SUFFIX ? max(t0, 0) : t0;
+    it.t1 = t1;
     it.vrow = groups_before(s.first, b, a.G, GS, a.most) * a.c.Hkv + vh;
-    pos += it.t1 - it.t0;
     return true;
   }
 };
@@ -249,6 +278,12 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   Plan *plan = reinterpret_cast<Plan *>(smem + OFF_PLAN);
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int2 *known = reinterpret_cast<const int2 *>(smem + OFF_KNOWN);
+  if constexpr (SUFFIX) {
+    int2 *to = reinterpret_cast<int2 *>(smem + OFF_KNOWN);
+    for (int i = threadIdx.x; i < min(a.c.B, KNOWN); i += THREADS) to[i] = own_keys(a, i);
+    __syncthreads();
+  }
 
   if (warp == NCW) {
     // ------------------------------------------------------------ plan
@@ -256,8 +291,8 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     int rows = 0, lmin = 0x7fffffff, lmax = 0;  // rows of records and lengths of sequences with keys
 #pragma unroll 4
     for (int i = lane; i < a.c.B; i += 32) {
-      const Seq s = seq_of<KT, GS, SUFFIX>(a, i);
-      const long long u = static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
+      const Seq s = seq_of<KT, GS, SUFFIX>(a, i, known);
+      const long long u = units<SUFFIX>(s, a);
       W += u;
       if (u > 0) {
         rows += s.ng * a.c.Hkv;
@@ -300,8 +335,8 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
         const int i = i0 + lane;
         long long u = 0;
         if (i < a.c.B) {
-          const Seq q = seq_of<KT, GS, SUFFIX>(a, i);
-          u = static_cast<long long>(q.tiles) * q.ng * a.c.Hkv;
+          const Seq q = seq_of<KT, GS, SUFFIX>(a, i, known);
+          u = units<SUFFIX>(q, a);
         }
         long long inc = u;
 #pragma unroll
@@ -360,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       const uint32_t at = (lane & 1) * TILE + first_key * 128;  // in a stage
       const bool active = lane < 2 * (KT / 16);
       const CUtensorMap *map = (lane & 1) ? &tm_v : &tm_k;
-      Walk<KT, GS, SUFFIX> wk(pl, a);
+      Walk<KT, GS, SUFFIX> wk(pl, a, known);
       Item it;
       int g = 0;
       bool ok = true;
@@ -398,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       prefetch_tensormap(&tm_v);
       const int shift = a.c.page_shift, mask = (1 << shift) - 1;
       const int per = KT > mask + 1 ? 16 : KT;  // keys of a box, as in the map
-      Walk<KT, GS, SUFFIX> wk(pl, a);
+      Walk<KT, GS, SUFFIX> wk(pl, a, known);
       Item it;
       int g = 0;
       bool ok = true;
@@ -479,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   constexpr int MT = KT / 16;  // m tiles of 16 keys
   float *mls = reinterpret_cast<float *>(smem + OFF_MLS);
   volatile int *held = reinterpret_cast<volatile int *>(smem + OFF_HELD);
-  Walk<KT, GS, SUFFIX> wk(pl, a);
+  Walk<KT, GS, SUFFIX> wk(pl, a, known);
   Item it;
   int gt = 0;  // tiles of the previous items
   while (wk.next(it, a)) {
@@ -962,7 +997,9 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
 
 // The last sums of decode with shared prefixes: thread = (sequence, query head of the
 // group), block = 128 of them of a kv head and four dims, so that the raw sums of
-// the prefix ([dims / 4][row] float4) are read in whole lines.
+// the prefix ([dims / 4][row] float4) are read in whole lines. Four threads share a
+// row's parts, so that all of them are on their way in one latency or two; places
+// are looked up before the kernels in front are done.
 struct SharedArgs {
   PagedCache c;
   SharedGroups groups;
@@ -1008,80 +1045,115 @@ __device__ __forceinline__ void add_records(Running &x, const float (&m)[N], con
   }
 }
 
-__global__ void __launch_bounds__(D) shared_combine_kernel(const SharedArgs a) {
-  constexpr int N = 4, RAW = 2 * D * 128 + 3 * 128;  // floats of a raw part
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int at = blockIdx.x * D + threadIdx.x, kvh = blockIdx.y, c4 = blockIdx.z;
+constexpr int CSL = 4;  // slices of a block: each takes every fourth part and record
+
+__global__ void __launch_bounds__(CSL * D) shared_combine_kernel(const SharedArgs a) {
+  constexpr int N = 5, RAW = 2 * D * 128 + 3 * 128;  // N: loads in flight; floats of a raw part
+  __shared__ float sums[CSL - 1][11][D];
+  const int lane = threadIdx.x & (D - 1), slice = threadIdx.x / D;
+  const int at = blockIdx.x * D + lane, kvh = blockIdx.y, c4 = blockIdx.z;
   const int b = at / a.G, gh = at - b * a.G, h = kvh * a.G + gh;
-  if (b >= a.c.B) return;
-  const int len = cache_len(a.c, a.seqlens, b);
-  const Group g = group_with(a.c, a.groups, a.seqlens, b);
+  const bool there = b < a.c.B;
+  int len = 0;
+  Group g = {};
+  if (there) {
+    len = cache_len(a.c, a.seqlens, b);
+    g = group_with(a.c, a.groups, a.seqlens, b);
+  }
   const int start = min(g.prefix, len);
+  const int tile = there ? (b - g.first) / a.TQ * a.TQ + g.first : 0, row = (b - tile) * a.G + gh;
+  const int ng = (a.G + a.group - 1) / a.group;
+  const long long place = groups_before(b, b, a.G, a.group, 0) * a.c.Hkv + static_cast<long long>(kvh) * ng + gh / a.group;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int2 pt = make_int2(0, -1), mt = make_int2(0, 0);
+  if (start > 0) pt = a.parts.parts[static_cast<long long>(tile) * a.c.Hkv + kvh];
+  if (start < len && PLX_IN_BOUNDS(place >= 0 && place < a.vrows, ErrWord{a.c.err})) mt = a.meta[place];
   Running x = {-INFINITY, 0.f, 0.f, {}, {}};
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (start > 0) {
-    const int tile = (b - g.first) / a.TQ * a.TQ + g.first, row = (b - tile) * a.G + gh;
-    const int2 pt = a.parts.parts[static_cast<long long>(tile) * a.c.Hkv + kvh];
-    if (pt.x < 0) {
+  if (start > 0 && pt.x < 0) {
+    if (slice == 0) {
       const float *r = a.parts.recs + (static_cast<long long>(b) * a.Hq + h) * kSharedRec;
       const float4 st = *reinterpret_cast<const float4 *>(r + 2 * D);
       const float m[1] = {st.y}, w[1] = {1.f}, s[1] = {st.x};
       const float4 o1[1] = {*reinterpret_cast<const float4 *>(r + 4 * c4)};
       const float4 o2[1] = {*reinterpret_cast<const float4 *>(r + D + 4 * c4)};
       add_records<1>(x, m, w, s, o1, o2);
-    } else {
-      const int last = min(pt.y >> 1, a.ctas - 1);
-      for (int p0 = pt.x; p0 <= last; p0 += N) {
-        float m[N], w[N], s[N];
-        float4 o1[N], o2[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int p = p0 + i;
-          const bool in = p <= last;
-          const float *raw = a.parts.raw + (2ll * p + (p == pt.x ? pt.y & 1 : 0)) * RAW;
-          m[i] = in ? raw[2 * D * 128 + row] : -INFINITY;
-          w[i] = in ? raw[2 * D * 128 + 128 + row] : 0.f;
-          s[i] = in ? raw[2 * D * 128 + 256 + row] : 0.f;
-          o1[i] = in ? reinterpret_cast<const float4 *>(raw)[c4 * 128 + row] : zero;
-          o2[i] = in ? reinterpret_cast<const float4 *>(raw)[(D / 4 + c4) * 128 + row] : zero;
-        }
-        add_records<N>(x, m, w, s, o1, o2);
-      }
     }
-  }
-  if (start < len) {
-    const int ng = (a.G + a.group - 1) / a.group;
-    const long long place = groups_before(b, b, a.G, a.group, 0) * a.c.Hkv + static_cast<long long>(kvh) * ng + gh / a.group;
-    if (!PLX_IN_BOUNDS(place >= 0 && place < a.vrows, ErrWord{a.c.err})) return;
-    const int2 mt = a.meta[place];
-    const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
-    const int n = inside ? mt.y : 0;
-    const size_t stride = static_cast<size_t>(a.gs) * REC;
-    const float *rec = a.recs + (inside ? mt.x : 0) * stride + static_cast<size_t>(gh % a.group) * REC;
-    for (int r0 = 0; r0 < n; r0 += N) {
+  } else if (start > 0) {
+    const int last = min(pt.y >> 1, a.ctas - 1);
+    for (int p0 = pt.x + slice; p0 <= last; p0 += N * CSL) {
       float m[N], w[N], s[N];
       float4 o1[N], o2[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const bool in = r0 + i < n;
-        const float2 *r = reinterpret_cast<const float2 *>(rec + (r0 + i) * stride);
-        const float2 st = in ? r[D] : make_float2(0.f, -INFINITY);
-        s[i] = st.x;
-        m[i] = st.y;
-        w[i] = in ? 1.f : 0.f;
-        float2 y[4] = {};
+        const int p = p0 + i * CSL;
+        const bool in = p <= last;
+        const float *raw = a.parts.raw + (2ll * p + (p == pt.x ? pt.y & 1 : 0)) * RAW;
+        m[i] = in ? raw[2 * D * 128 + row] : -INFINITY;
+        w[i] = in ? raw[2 * D * 128 + 128 + row] : 0.f;
+        s[i] = in ? raw[2 * D * 128 + 256 + row] : 0.f;
+        o1[i] = in ? reinterpret_cast<const float4 *>(raw)[c4 * 128 + row] : zero;
+        o2[i] = in ? reinterpret_cast<const float4 *>(raw)[(D / 4 + c4) * 128 + row] : zero;
+      }
+      add_records<N>(x, m, w, s, o1, o2);
+    }
+  }
+  {
+    // An entry outside the records (left by an earlier call when this one did no
+    // work) is not followed.
+    const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
+    const int n = inside ? mt.y : 0;
+    const size_t stride = static_cast<size_t>(a.gs) * REC;
+    const float *rec = a.recs + (inside ? mt.x : 0) * stride + static_cast<size_t>(gh % a.group) * REC;
+    constexpr int M = 2;
+    for (int r0 = CSL - 1 - slice; r0 < n; r0 += M * CSL) {  // the last slices have the fewer parts
+      float m[M], w[M], s[M];
+      float4 o1[M], o2[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        const bool in = r0 + i * CSL < n;
+        const float2 *r = reinterpret_cast<const float2 *>(rec + (r0 + i * CSL) * stride);
+        float2 st = make_float2(0.f, -INFINITY), y[4] = {};
         if (in) {
+          st = r[D];
           y[0] = r[2 * c4];
           y[1] = r[2 * c4 + 1];
           y[2] = r[D / 2 + 2 * c4];
           y[3] = r[D / 2 + 2 * c4 + 1];
         }
+        s[i] = st.x;
+        m[i] = st.y;
+        w[i] = in ? 1.f : 0.f;
         o1[i] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
         o2[i] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
       }
-      add_records<N>(x, m, w, s, o1, o2);
+      add_records<M>(x, m, w, s, o1, o2);
     }
   }
+  if (slice > 0) {
+    float(*z)[D] = sums[slice - 1];
+    z[0][lane] = x.M;
+    z[1][lane] = x.W;
+    z[2][lane] = x.s;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      z[3 + d][lane] = x.o1[d];
+      z[7 + d][lane] = x.o2[d];
+    }
+  }
+  __syncthreads();
+  if (slice > 0 || !there) return;
+  float m[CSL - 1], w[CSL - 1], s[CSL - 1];
+  float4 o1[CSL - 1], o2[CSL - 1];
+#pragma unroll
+  for (int i = 0; i < CSL - 1; ++i) {
+    m[i] = sums[i][0][lane];
+    w[i] = sums[i][1][lane];
+    s[i] = sums[i][2][lane];
+    o1[i] = make_float4(sums[i][3][lane], sums[i][4][lane], sums[i][5][lane], sums[i][6][lane]);
+    o2[i] = make_float4(sums[i][7][lane], sums[i][8][lane], sums[i][9][lane], sums[i][10][lane]);
+  }
+  add_records<CSL - 1>(x, m, w, s, o1, o2);
   float o[4] = {};
   if (x.W != 0.f) {  // NaN, for a query that is not a number, goes on
     const float inv = 1.f / x.W, sg = x.s * inv;
@@ -1092,10 +1164,10 @@ __global__ void __launch_bounds__(D) shared_combine_kernel(const SharedArgs a) {
       o[d] = len == 1 ? p : p - (x.o2[d] * inv - p * sg);
     }
   }
-  uint2 w;
-  w.x = pack_bf16x2(o[0], o[1]);
-  w.y = pack_bf16x2(o[2], o[3]);
-  *reinterpret_cast<uint2 *>(a.out + (static_cast<long long>(b) * a.Hq + h) * D + 4 * c4) = w;
+  uint2 out;
+  out.x = pack_bf16x2(o[0], o[1]);
+  out.y = pack_bf16x2(o[2], o[3]);
+  *reinterpret_cast<uint2 *>(a.out + (static_cast<long long>(b) * a.Hq + h) * D + 4 * c4) = out;
 }
 
 // Map of one page tensor. bf16: {64, page, pages Hkv, 2 halves}, boxes of 16
@@ -1127,11 +1199,11 @@ cudaError_t launch_rows(const RowsArgs &a, const CUtensorMap &mk, const CUtensor
   if (ctx == 0 || configured_ctx != ctx) {
     cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, R, SUFFIX>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(ROWS_SMEM));
+                                         static_cast<int>(ROWS_SMEM<SUFFIX>));
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  paged_rows_kernel<FP8, R, SUFFIX><<<a.nshare, THREADS, ROWS_SMEM, stream>>>(mk, mv, a);
+  paged_rows_kernel<FP8, R, SUFFIX><<<a.nshare, THREADS, ROWS_SMEM<SUFFIX>, stream>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
@@ -1260,7 +1332,7 @@ cudaError_t launch_shared_combine(const PagedCache &c, const SharedGroups &g, co
   a.recs = reinterpret_cast<const float *>(static_cast<const uint8_t *>(rows_workspace) + paged_rows_meta_bytes(a.vrows));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((c.B * a.G + D - 1) / D, c.Hkv, D / 4);
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(CSL * D);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
