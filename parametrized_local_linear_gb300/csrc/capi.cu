@@ -683,9 +683,55 @@ plx_status plx_prefill_fwd_paged(const void *q, const void *r, long long qr_toke
   });
 }
 
+namespace {
+
+// Which kernels a shared decode launches: the rows kernel always, for the keys behind
+// the prefixes. A prefix is read once for every 128 rows (sequence, query head) of a
+// kv head by the tile kernel, or once for every eight by the rows kernel, which needs
+// no second launch and has no deep pipeline to fill. GB300, GPU time of the latter and
+// of the tile kernel, 200 own keys at most:
+//   - 8 rows a group: 1 prefix of 4000 keys x 8 kv heads 16.4 and 26.8 us (bf16; e4m3
+//     16.9 and 30.0), 16 of 8000 109 and 124 (93 and 154), 1 of 32000 x 1 23.2 and 27.5;
+//   - 16 rows: 1 of 4000 x 8 19.1 and 28.0 (19.1 and 31.9), 16 of 2000 70 and 73 (77
+//     and 84), 16 of 8000 194 and 135 (165 and 164);
+//   - 32 rows: 1 of 4000 x 8 24.8 and 29.4 (25.0 and 31.5), 1 of 32000 76 and 50.
+// So the rows kernel takes the prefixes where groups have at most eight rows on
+// average, or more as long as its further passes are short (over at most kMorePasses
+// key rows, by the block table's width: lengths live on the device). It then takes the
+// groups of up to `most` rows, and the tile kernel the others, if there can be any.
+// (Only up to kFewPlaces sequences x kv heads: the records of both have places.)
+constexpr int kFewPlaces = 4096;
+constexpr long long kMorePasses = 1 << 17;
+struct SharedPlan {
+  plx::RowsPlan rows;
+  bool tiles;
+};
+SharedPlan shared_plan(int ngroups, int B, int Hq, int Hkv, long long table_keys) {
+  const int G = Hq / Hkv;
+  const long long n = static_cast<long long>(B) * G, passes = (n + 8ll * ngroups - 1) / (8ll * ngroups);
+  SharedPlan x = {{plx::paged_rows_group(B, B, G), 0}, true};
+  if (G <= 8 && static_cast<long long>(B) * Hkv <= kFewPlaces && passes <= 4 &&
+      (passes - 1) * ngroups * Hkv <= kMorePasses / table_keys) {
+    x.rows = {n > 4ll * ngroups ? 8 : 4, std::max(16, static_cast<int>(8 * passes))};
+    x.tiles = n > x.rows.most;
+  }
+  return x;
+}
+// For any groups and lengths.
+size_t shared_rows_bytes(int B, int Hq, int Hkv, int d) {
+  const int G = Hq / Hkv;
+  size_t most = plx::shared_rows_workspace_bytes({plx::paged_rows_group(B, B, G), 0}, B, G, Hkv, d);
+  if (G <= 8 && static_cast<long long>(B) * Hkv <= kFewPlaces)
+    for (int group : {4, 8})
+      most = std::max(most, plx::shared_rows_workspace_bytes({group, 16}, B, G, Hkv, d));
+  return (most + 255) / 256 * 256;
+}
+
+}  // namespace
+
 size_t plx_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d) {
-  const size_t rows = plx_decode_paged_workspace_bytes(B, Hq, Hkv, d);
-  return rows == 0 ? 0 : (rows + 255) / 256 * 256 + plx::shared_parts_bytes(B, Hq, Hkv);
+  if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
+  return shared_rows_bytes(B, Hq, Hkv, d) + plx::shared_parts_bytes(B, Hq, Hkv);
 }
 
 plx_status plx_decode_fwd_shared(const void *q, const void *r, const void *kpages,
@@ -709,19 +755,21 @@ plx_status plx_decode_fwd_shared(const void *q, const void *r, const void *kpage
     return fail(PLX_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", fn);
   if (static_cast<long long>(B) * Hq > (1LL << 24) || Hkv > 65535)
     return fail(PLX_ERR_UNSUPPORTED, "%s: B * Hq must be <= 2^24 and Hkv <= 65535", fn);
-  const size_t rows = (plx_decode_paged_workspace_bytes(B, Hq, Hkv, d) + 255) / 256 * 256;
-  const size_t need = plx_decode_shared_workspace_bytes(B, Hq, Hkv, d);
+  const size_t rows = shared_rows_bytes(B, Hq, Hkv, d), need = rows + plx::shared_parts_bytes(B, Hq, Hkv);
   if (workspace && workspace_bytes < need)
     return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);
   if (!aligned16(workspace)) return fail(PLX_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
   c.err = plx::device_error_word();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const plx::SharedGroups g = {cu_g, prefix_lens, ngroups};
+  const SharedPlan x = shared_plan(ngroups, B, Hq, Hkv, static_cast<long long>(max_pages) * page_size);
   return with_workspace(fn, workspace, need, st, [&](void *ws) {
     const plx::SharedParts parts = plx::shared_parts(static_cast<char *>(ws) + rows, B, Hq, Hkv);
-    cudaError_t e = plx::launch_shared_rows(c, g, q, r, seqlens, Hq, ws, st);
-    if (e == cudaSuccess) e = plx::launch_shared_prefix(c, g, q, r, seqlens, Hq, parts, st);
-    if (e == cudaSuccess) e = plx::launch_shared_combine(c, g, seqlens, Hq, ws, parts, out, st);
+    cudaError_t e = plx::launch_shared_rows(x.rows, c, g, q, r, seqlens, Hq, ws, st);
+    if (e == cudaSuccess && x.tiles)
+      e = plx::launch_shared_prefix(c, g, q, r, seqlens, Hq, x.rows.most / (Hq / Hkv), parts, st);
+    if (e == cudaSuccess)
+      e = plx::launch_shared_combine(x.rows, c, g, seqlens, Hq, ws, parts, out, st);
     return e;
   });
 }
@@ -852,7 +900,8 @@ plx_status rotary(const char *fn, bool backward, const void *const (&in)[3], voi
   if (B == 0 || L == 0) return PLX_OK;
   return finish_launch(
       plx::launch_rotary(t, heads, positions, seqlens, cu_q, nseq, inv_freq, static_cast<float>(scale), backward, B,
-                         L, d, rotary_dim, interleaved != 0, dtype == PLX_F32, plx::device_error_word(),
+                         L, d, rotary_dim, interleaved != 0, dtype == PLX_F32,
+                         seqlens ? plx::device_error_word() : nullptr,
                          static_cast<cudaStream_t>(stream)),
       fn);
 }

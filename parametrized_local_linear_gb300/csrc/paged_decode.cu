@@ -79,12 +79,12 @@ constexpr int OFF_BAR = OFF_MLS + NCW * RW * 16;
 constexpr int OFF_FLAG = OFF_BAR + 2 * NST * 8;
 constexpr int OFF_PLAN = OFF_FLAG + 16;
 constexpr int OFF_HELD = OFF_PLAN + 64;  // [NCW] stage that holds a warp's sums
-// SUFFIX: keys and first own key of the first sequences, looked up by all threads at
+// kOwn, kAll: keys and first own key of the first sequences, looked up by all threads at
 // once (what goes over the sequences, plan and walks, finds them here).
 constexpr int OFF_KNOWN = OFF_HELD + 16;
 constexpr int KNOWN = 512;
-template <bool SUFFIX>
-constexpr size_t ROWS_SMEM = OFF_KNOWN + (SUFFIX ? KNOWN * 8 : 0) + 1024;
+template <int KEYS>
+constexpr size_t ROWS_SMEM = OFF_KNOWN + (KEYS > 0 ? KNOWN * 8 : 0) + 1024;
 static_assert(2 * TILE == 2 * RW * 2 * D * 4, "a stage holds the sums of two warps");
 constexpr int kCtasPerSm = 3;  // 128 registers a thread, 72 KB of shared memory
 
@@ -99,8 +99,14 @@ struct RowsArgs {
   long long vrows;           // places of meta; recs has nshare more
   int most;                  // as in RowsPlan
   float scale_log2;
-  SharedGroups groups;       // SUFFIX: keys that a group shares are left out
+  SharedGroups groups;       // kOwn, kAll
+  int places;                // kAll: places of the groups' prefixes, in front of the sequences'
 };
+// What the kernel goes over: sequences; the keys of sequences behind those that
+// their group shares (one token each); the shared keys of groups (of at most `most`
+// rows a kv head), whose sequences are the tokens and see as many of them as they
+// have, and then the keys behind them.
+enum Keys { kWhole, kOwn, kAll };
 
 struct Plan {
   long long W, s, e;  // tiles of the batch; this CTA's share [s, e)
@@ -111,16 +117,23 @@ struct Plan {
 // Keys, tiles, new tokens and row groups of sequence b.
 struct Seq {
   int len, tiles, first, n, ng;
-  int start;  // SUFFIX: the first key; its tile is the sequence's first
+  int start;  // the first key; its tile is the sequence's first
 };
 // Keys of sequence b, and the first that its group does not share.
 __device__ __forceinline__ int2 own_keys(const RowsArgs &a, int b) {
   const int len = cache_len(a.c, a.seqlens, b);
   return make_int2(len, min(group_with(a.c, a.groups, a.seqlens, b).prefix, len));
 }
-template <int KT, int GS, bool SUFFIX>
+template <int KT, int GS, int KEYS>
 __device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b, const int2 *known) {
-  if constexpr (SUFFIX) {  // one token each
+  if constexpr (KEYS > 0) {
+    if (KEYS == kAll && b < a.groups.n) {
+      const Group g = group_of(a.c, a.groups, a.seqlens, b);
+      const long long rows = static_cast<long long>(g.n) * a.G;
+      const bool take = g.n > 0 && rows <= a.most;
+      return Seq{g.prefix, take ? (g.prefix + KT - 1) / KT : 0, g.first, g.n, take ? static_cast<int>((rows + GS - 1) / GS) : 0, 0};
+    }
+    if (KEYS == kAll) b -= a.groups.n;
     const int2 x = b < KNOWN ? known[b] : own_keys(a, b);
     const int tiles = x.y < x.x ? (x.x + KT - 1) / KT - x.y / KT : 0;
     return Seq{x.x, tiles, b, 1, (a.G + GS - 1) / GS, x.y};
@@ -151,14 +164,15 @@ __device__ __forceinline__ long long groups_before(int first, int b, int G, int 
 }
 
 // What an item costs besides its tiles (its queries, its merge, its records), in
-// tiles: a row of a sequence counts as so many more where sequences may be short
-// (SUFFIX), so that a share of many short rows is not the last to end.
-template <bool SUFFIX>
-constexpr int kRowCost = SUFFIX ? 8 : 0;
+// tiles: a row counts as so many more where most may be short (behind shared keys), so
+// that a share of many short rows is not the last to end: 64 sequences with 1 to 1024
+// keys behind 32768 91 us with none, 79 with 4, 74 with 8 and with 16.
+template <int KEYS>
+constexpr int kRowCost = KEYS > 0 ? 8 : 0;
 // A sequence's part of the stream that is cut into shares.
-template <bool SUFFIX>
+template <int KEYS>
 __device__ __forceinline__ long long units(const Seq &s, const RowsArgs &a) {
-  return s.tiles > 0 ? static_cast<long long>(s.tiles + kRowCost<SUFFIX>) * s.ng * a.c.Hkv : 0;
+  return s.tiles > 0 ? static_cast<long long>(s.tiles + kRowCost<KEYS>) * s.ng * a.c.Hkv : 0;
 }
 
 // One item: tiles [t0, t1) (of those from `start` on) of row group grp of kv head kvh of
@@ -169,47 +183,53 @@ struct Item {
   long long vrow;  // the item's row of records
 };
 
-template <int KT, int GS, bool SUFFIX>
+template <int KT, int GS, int KEYS>
 struct Walk {
   long long pos, e, base;
   int b;
   Seq s;
   const int2 *known;
   __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a, const int2 *known_)
-      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, SUFFIX>(a, p.b0, known_)), known(known_) {}
+      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, KEYS>(a, p.b0, known_)), known(known_) {}
   __device__ __forceinline__ bool next(Item &it, const RowsArgs &a) {
-    constexpr int X = kRowCost<SUFFIX>;
+    constexpr int X = kRowCost<KEYS>;
     int vh, t0, t1;
     do {
       if (pos >= e) return false;
       // Positions below W all lie in some sequence, so b stays below B here.
       while (true) {
-        const long long end = base + units<SUFFIX>(s, a);
+        const long long end = base + units<KEYS>(s, a);
         if (pos < end) break;
         base = end;
-        s = seq_of<KT, GS, SUFFIX>(a, ++b, known);
+        s = seq_of<KT, GS, KEYS>(a, ++b, known);
       }
       const long long off = pos - base;
       vh = static_cast<int>(off / (s.tiles + X));
       t0 = static_cast<int>(off - static_cast<long long>(vh) * (s.tiles + X)) - X;
       t1 = static_cast<int>(min(static_cast<long long>(s.tiles), t0 + (e - pos)));
       pos += t1 - t0;
-    } while (SUFFIX && t1 <= 0);  // no tile: only of what stands for the row's fixed cost
+    } while (KEYS > 0 && t1 <= 0);  // no tile: only of what stands for the row's fixed cost
     it.s = s;
     it.b = b;
     it.kvh = vh / s.ng;
     it.grp = vh - it.kvh * s.ng;
-    it.t0 = SUFFIX ? max(t0, 0) : t0;
+    it.t0 = KEYS > 0 ? max(t0, 0) : t0;
     it.t1 = t1;
-    it.vrow = groups_before(s.first, b, a.G, GS, a.most) * a.c.Hkv + vh;
+    if constexpr (KEYS == kWhole) {
+      it.vrow = groups_before(s.first, b, a.G, GS, a.most) * a.c.Hkv + vh;
+    } else {
+      // In front of a group or sequence there are at most as many others as sequences.
+      const int places = KEYS == kAll && b >= a.groups.n ? a.places : 0;
+      it.vrow = (places + groups_before(s.first, s.first, a.G, GS, 0)) * a.c.Hkv + vh;
+    }
     return true;
   }
 };
 
 // The first key of tile t of an item's sequence.
-template <int KT, bool SUFFIX>
+template <int KT, int KEYS>
 __device__ __forceinline__ int tile_key(const Item &it, int t) {
-  return SUFFIX ? (it.s.start / KT + t) * KT : t * KT;
+  return KEYS > 0 ? (it.s.start / KT + t) * KT : t * KT;
 }
 
 __device__ __forceinline__ void consumer_sync() {
@@ -262,13 +282,14 @@ __device__ __forceinline__ int row_shift(float m) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-template <bool FP8, int R, bool SUFFIX>
+template <bool FP8, int R, int KEYS>
 __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const RowsArgs a) {
   constexpr int KT = FP8 ? 32 : 16;  // keys of a tile
   constexpr int GS = RW * R;         // query rows of a group
   constexpr int NL = NCW / R;        // warp rows: tiles in work at a time
+  constexpr bool SUFFIX = KEYS > 0;  // sequences whose first key need not be 0
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -287,12 +308,13 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
 
   if (warp == NCW) {
     // ------------------------------------------------------------ plan
+    const int count = a.c.B + (KEYS == kAll ? a.groups.n : 0);
     long long W = 0;
     int rows = 0, lmin = 0x7fffffff, lmax = 0;  // rows of records and lengths of sequences with keys
 #pragma unroll 4
-    for (int i = lane; i < a.c.B; i += 32) {
-      const Seq s = seq_of<KT, GS, SUFFIX>(a, i, known);
-      const long long u = units<SUFFIX>(s, a);
+    for (int i = lane; i < count; i += 32) {
+      const Seq s = seq_of<KT, GS, KEYS>(a, i, known);
+      const long long u = units<KEYS>(s, a);
       W += u;
       if (u > 0) {
         rows += s.ng * a.c.Hkv;
@@ -331,12 +353,12 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     long long base0 = 0;
     if (c < n && s < e) {
       long long base = 0;  // the first sequence whose end lies past s
-      for (int i0 = 0; i0 < a.c.B; i0 += 32) {
+      for (int i0 = 0; i0 < count; i0 += 32) {
         const int i = i0 + lane;
         long long u = 0;
-        if (i < a.c.B) {
-          const Seq q = seq_of<KT, GS, SUFFIX>(a, i, known);
-          u = units<SUFFIX>(q, a);
+        if (i < count) {
+          const Seq q = seq_of<KT, GS, KEYS>(a, i, known);
+          u = units<KEYS>(q, a);
         }
         long long inc = u;
 #pragma unroll
@@ -344,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
           const long long v = __shfl_up_sync(0xffffffffu, inc, o);
           if (lane >= o) inc += v;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, i < a.c.B && base + inc > s);
+        const unsigned hit = __ballot_sync(0xffffffffu, i < count && base + inc > s);
         if (hit != 0u) {
           const int l = __ffs(hit) - 1;
           b0 = i0 + l;
@@ -395,14 +417,14 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       const uint32_t at = (lane & 1) * TILE + first_key * 128;  // in a stage
       const bool active = lane < 2 * (KT / 16);
       const CUtensorMap *map = (lane & 1) ? &tm_v : &tm_k;
-      Walk<KT, GS, SUFFIX> wk(pl, a, known);
+      Walk<KT, GS, KEYS> wk(pl, a, known);
       Item it;
       int g = 0;
       bool ok = true;
       while (ok && wk.next(it, a)) {
-        const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-        const int end = min(tile_key<KT, SUFFIX>(it, it.t1), it.s.len);
-        int key = tile_key<KT, SUFFIX>(it, it.t0) + first_key;
+        const int *table = a.c.table + static_cast<long long>(SUFFIX ? it.s.first : it.b) * a.c.max_pages;
+        const int end = min(tile_key<KT, KEYS>(it, it.t1), it.s.len);
+        int key = tile_key<KT, KEYS>(it, it.t0) + first_key;
         int page = active && key < end ? table[key >> 4] : 0;
         for (int t = it.t0; t < it.t1; ++t, key += KT, ++g) {
           int z = beyond;
@@ -433,14 +455,14 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       prefetch_tensormap(&tm_v);
       const int shift = a.c.page_shift, mask = (1 << shift) - 1;
       const int per = KT > mask + 1 ? 16 : KT;  // keys of a box, as in the map
-      Walk<KT, GS, SUFFIX> wk(pl, a, known);
+      Walk<KT, GS, KEYS> wk(pl, a, known);
       Item it;
       int g = 0;
       bool ok = true;
       while (ok && wk.next(it, a)) {
-        const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
-        int key = tile_key<KT, SUFFIX>(it, it.t0);
-        const int end = tile_key<KT, SUFFIX>(it, it.t1);
+        const int *table = a.c.table + static_cast<long long>(SUFFIX ? it.s.first : it.b) * a.c.max_pages;
+        int key = tile_key<KT, KEYS>(it, it.t0);
+        const int end = tile_key<KT, KEYS>(it, it.t1);
         int next = table[key >> shift];  // t0's tile holds a key
         int z = beyond;
         bool fresh = true;
@@ -514,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   constexpr int MT = KT / 16;  // m tiles of 16 keys
   float *mls = reinterpret_cast<float *>(smem + OFF_MLS);
   volatile int *held = reinterpret_cast<volatile int *>(smem + OFF_HELD);
-  Walk<KT, GS, SUFFIX> wk(pl, a, known);
+  Walk<KT, GS, KEYS> wk(pl, a, known);
   Item it;
   int gt = 0;  // tiles of the previous items
   while (wk.next(it, a)) {
@@ -523,19 +545,19 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     const int t_first = (line - gt % NL + NL) % NL;
     // The item's query rows, records and place in meta lie inside theirs.
     const bool item_ok = PLX_IN_BOUNDS(
-        it.b < a.c.B && it.kvh < a.c.Hkv && it.vrow >= 0 && it.vrow < a.vrows && nr >= 1 && nr <= gs &&
+        (SUFFIX ? it.s.first : it.b) < a.c.B && it.kvh < a.c.Hkv && it.vrow >= 0 && it.vrow < a.vrows && nr >= 1 && nr <= gs &&
             it.s.first >= 0 && it.s.first + (r0 + nr - 1) / a.G < a.T && it.t1 <= it.s.tiles,
         ab);
     // The scale bytes of key `lane` of the warp's tiles, one tile ahead, and
     // the page number of the tile after it. Byte 0 is K's, byte 1 V's.
-    const int *table = a.c.table + static_cast<long long>(it.b) * a.c.max_pages;
+    const int *table = a.c.table + static_cast<long long>(SUFFIX ? it.s.first : it.b) * a.c.max_pages;
     auto page_of = [&](int t) {
-      const int key = tile_key<KT, SUFFIX>(it, it.t0 + t) + lane;
+      const int key = tile_key<KT, KEYS>(it, it.t0 + t) + lane;
       return t < nt && key < it.s.len ? table[key >> a.c.page_shift] : -1;
     };
     auto scales_of = [&](int t, int page) -> uint32_t {
       if (page < 0 || page >= a.c.num_pages) return 0u;
-      const int key = tile_key<KT, SUFFIX>(it, it.t0 + t) + lane;
+      const int key = tile_key<KT, KEYS>(it, it.t0 + t) + lane;
       const long long row = ((static_cast<long long>(page) * a.c.Hkv + it.kvh) << a.c.page_shift) +
                             (key & ((1 << a.c.page_shift) - 1));
       return a.c.kscale[row] | (static_cast<uint32_t>(a.c.vscale[row]) << 8);
@@ -568,8 +590,15 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     }
     const int mine = RW * blk + tq;
     // The last key that row tq sees (< 0: none), and that all rows see.
-    const int last = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
-    const int all_see = it.s.len - it.s.n + r0 / a.G;
+    int last = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
+    int all_see = it.s.len - it.s.n + r0 / a.G;
+    if (KEYS == kAll && it.b < a.groups.n) {
+      if (mine < nr) {
+        const int m = it.s.first + (r0 + mine) / a.G;
+        last = min(it.s.len, m < KNOWN ? known[m].x : cache_len(a.c, a.seqlens, m)) - 1;
+      }
+      all_see = __reduce_min_sync(0xffffffffu, mine < nr ? last : it.s.len - 1);
+    }
     uint32_t sc_next = 0u;
     if constexpr (FP8) {
       sc_next = scales_of(t_first, page_first);
@@ -610,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       if (lane == 0) ok = !ab.raised() && mbar_wait(smem_u32(&full[st]), (gi / NST) & 1, ab);
       if (!__shfl_sync(0xffffffffu, ok, 0)) continue;  // aborting: skip the tile
       const uint32_t kb = smem_u32(smem + st * 2 * TILE), vb = kb + TILE;
-      const int key0 = tile_key<KT, SUFFIX>(it, it.t0 + t);
+      const int key0 = tile_key<KT, KEYS>(it, it.t0 + t);
       // cc[mt][0..1]: s and t of key 16 mt + g, [2..3]: of key 16 mt + 8 + g.
       float cc[MT][4];
       const int arow = (lane & 7) + 8 * ((lane >> 3) & 1), acol = lane >> 4;
@@ -1010,6 +1039,7 @@ struct SharedArgs {
   __nv_bfloat16 *out;
   long long nslots, vrows;
   int Hq, G, TQ, gs, group, ctas;
+  int most, places;  // groups of at most so many rows a kv head are among the records too
 };
 
 // Sums of records under a running maximum.
@@ -1062,12 +1092,22 @@ __global__ void __launch_bounds__(CSL * D) shared_combine_kernel(const SharedArg
   }
   const int start = min(g.prefix, len);
   const int tile = there ? (b - g.first) / a.TQ * a.TQ + g.first : 0, row = (b - tile) * a.G + gh;
-  const int ng = (a.G + a.group - 1) / a.group;
-  const long long place = groups_before(b, b, a.G, a.group, 0) * a.c.Hkv + static_cast<long long>(kvh) * ng + gh / a.group;
+  // Places of the records of the shared keys (of few rows) and of the own ones.
+  const int grow = (b - g.first) * a.G + gh;
+  const bool few = static_cast<long long>(g.n) * a.G <= a.most;
+  auto place_of = [&](int first, int rows, int r) {
+    return groups_before(first, first, a.G, a.group, 0) * a.c.Hkv + static_cast<long long>(kvh) * ((rows + a.group - 1) / a.group) + r / a.group;
+  };
+  const long long shared_place = few ? place_of(g.first, g.n * a.G, grow) : 0;
+  const long long own_place = static_cast<long long>(a.places) * a.c.Hkv + place_of(b, a.G, gh);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int2 pt = make_int2(0, -1), mt = make_int2(0, 0);
-  if (start > 0) pt = a.parts.parts[static_cast<long long>(tile) * a.c.Hkv + kvh];
-  if (start < len && PLX_IN_BOUNDS(place >= 0 && place < a.vrows, ErrWord{a.c.err})) mt = a.meta[place];
+  int2 pt = make_int2(0, -1), mt[2] = {make_int2(0, 0), make_int2(0, 0)};
+  if (start > 0 && few) {
+    if (PLX_IN_BOUNDS(shared_place >= 0 && shared_place < a.vrows, ErrWord{a.c.err})) mt[0] = a.meta[shared_place];
+  } else if (start > 0) {
+    pt = a.parts.parts[static_cast<long long>(tile) * a.c.Hkv + kvh];
+  }
+  if (start < len && PLX_IN_BOUNDS(own_place >= 0 && own_place < a.vrows, ErrWord{a.c.err})) mt[1] = a.meta[own_place];
   Running x = {-INFINITY, 0.f, 0.f, {}, {}};
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   if (start > 0 && pt.x < 0) {
@@ -1098,15 +1138,16 @@ __global__ void __launch_bounds__(CSL * D) shared_combine_kernel(const SharedArg
       add_records<N>(x, m, w, s, o1, o2);
     }
   }
-  {
+#pragma unroll
+  for (int own = 0; own < 2; ++own) {
     // An entry outside the records (left by an earlier call when this one did no
     // work) is not followed.
-    const bool inside = mt.x >= 0 && mt.y >= 1 && static_cast<long long>(mt.x) + mt.y <= a.nslots;
-    const int n = inside ? mt.y : 0;
+    const bool inside = mt[own].x >= 0 && mt[own].y >= 1 && static_cast<long long>(mt[own].x) + mt[own].y <= a.nslots;
+    const int n = inside ? mt[own].y : 0;
     const size_t stride = static_cast<size_t>(a.gs) * REC;
-    const float *rec = a.recs + (inside ? mt.x : 0) * stride + static_cast<size_t>(gh % a.group) * REC;
+    const float *rec = a.recs + (inside ? mt[own].x : 0) * stride + static_cast<size_t>((own ? gh : grow) % a.group) * REC;
     constexpr int M = 2;
-    for (int r0 = CSL - 1 - slice; r0 < n; r0 += M * CSL) {  // the last slices have the fewer parts
+    for (int r0 = own ? CSL - 1 - slice : slice; r0 < n; r0 += M * CSL) {  // the last slices have the fewer parts
       float m[M], w[M], s[M];
       float4 o1[M], o2[M];
 #pragma unroll
@@ -1191,19 +1232,19 @@ bool make_page_map(EncodeTiledFn enc, CUtensorMap *map, const PagedCache &c, con
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8, int R, bool SUFFIX>
+template <bool FP8, int R, int KEYS>
 cudaError_t launch_rows(const RowsArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                         cudaStream_t stream) {
   static thread_local unsigned long long configured_ctx = 0;
   const unsigned long long ctx = context_id();
   if (ctx == 0 || configured_ctx != ctx) {
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, R, SUFFIX>,
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<FP8, R, KEYS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(ROWS_SMEM<SUFFIX>));
+                                         static_cast<int>(ROWS_SMEM<KEYS>));
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  paged_rows_kernel<FP8, R, SUFFIX><<<a.nshare, THREADS, ROWS_SMEM<SUFFIX>, stream>>>(mk, mv, a);
+  paged_rows_kernel<FP8, R, KEYS><<<a.nshare, THREADS, ROWS_SMEM<KEYS>, stream>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
@@ -1221,7 +1262,7 @@ int paged_rows_group(int T, int B, int G) { return static_cast<long long>(T) * G
 namespace {
 
 // The split kernel of a call; `a` as it was launched.
-template <bool SUFFIX>
+template <int KEYS>
 cudaError_t launch_split(const RowsPlan &p, const PagedCache &c, const void *q, const void *r, long long qts,
                          long long qhs, const int *seqlens, const int *cu_q, int T, int Hq,
                          const SharedGroups &groups, void *workspace, RowsArgs &a, cudaStream_t stream) {
@@ -1244,16 +1285,17 @@ cudaError_t launch_split(const RowsPlan &p, const PagedCache &c, const void *q, 
   a.T = T;
   const int group = p.group;
   a.most = p.most;
-  a.gs = paged_rows_slot(group, a.G, cu_q != nullptr);
+  a.gs = paged_rows_slot(group, a.G, cu_q != nullptr || KEYS == kAll);
   a.nshare = paged_rows_shares();
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  const long long vrows = paged_rows_vrows(p, T, c.B, a.G, c.Hkv);
+  const long long vrows = KEYS == kWhole ? paged_rows_vrows(p, T, c.B, a.G, c.Hkv) : shared_rows_vrows(p, c.B, a.G, c.Hkv);
+  a.places = static_cast<int>(shared_rows_places(p, c.B, a.G));
   a.vrows = vrows;
   a.meta = static_cast<int2 *>(workspace);
   a.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + paged_rows_meta_bytes(vrows));
   if (group == 4)
-    return fp8 ? launch_rows<true, 1, SUFFIX>(a, mk, mv, stream) : launch_rows<false, 1, SUFFIX>(a, mk, mv, stream);
-  return fp8 ? launch_rows<true, 2, SUFFIX>(a, mk, mv, stream) : launch_rows<false, 2, SUFFIX>(a, mk, mv, stream);
+    return fp8 ? launch_rows<true, 1, KEYS>(a, mk, mv, stream) : launch_rows<false, 1, KEYS>(a, mk, mv, stream);
+  return fp8 ? launch_rows<true, 2, KEYS>(a, mk, mv, stream) : launch_rows<false, 2, KEYS>(a, mk, mv, stream);
 }
 
 }  // namespace
@@ -1263,7 +1305,7 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
                               void *out, long long ots, long long ohs, float *lse, int T, int Hq,
                               void *workspace, cudaStream_t stream) {
   RowsArgs a;
-  cudaError_t e = launch_split<false>(p, c, q, r, qts, qhs, seqlens, cu_q, T, Hq, SharedGroups{}, workspace, a, stream);
+  cudaError_t e = launch_split<kWhole>(p, c, q, r, qts, qhs, seqlens, cu_q, T, Hq, SharedGroups{}, workspace, a, stream);
   if (e != cudaSuccess) return e;
   const long long vrows = a.vrows;
   CombineArgs k;
@@ -1299,19 +1341,16 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
   return cudaGetLastError();
 }
 
-namespace {
-RowsPlan shared_rows_plan(int B, int G) { return {paged_rows_group(B, B, G), 0}; }
-}  // namespace
-
-cudaError_t launch_shared_rows(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
-                               const int *seqlens, int Hq, void *workspace, cudaStream_t stream) {
+cudaError_t launch_shared_rows(const RowsPlan &p, const PagedCache &c, const SharedGroups &g, const void *q,
+                               const void *r, const int *seqlens, int Hq, void *workspace, cudaStream_t stream) {
   RowsArgs a;
-  return launch_split<true>(shared_rows_plan(c.B, Hq / c.Hkv), c, q, r, static_cast<long long>(Hq) * D, D, seqlens,
-                            nullptr, c.B, Hq, g, workspace, a, stream);
+  const long long row = static_cast<long long>(Hq) * D;
+  return p.most > 0 ? launch_split<kAll>(p, c, q, r, row, D, seqlens, nullptr, c.B, Hq, g, workspace, a, stream)
+                    : launch_split<kOwn>(p, c, q, r, row, D, seqlens, nullptr, c.B, Hq, g, workspace, a, stream);
 }
 
-cudaError_t launch_shared_combine(const PagedCache &c, const SharedGroups &g, const int *seqlens, int Hq,
-                                  const void *rows_workspace, const SharedParts &parts, void *out,
+cudaError_t launch_shared_combine(const RowsPlan &p, const PagedCache &c, const SharedGroups &g, const int *seqlens,
+                                  int Hq, const void *rows_workspace, const SharedParts &parts, void *out,
                                   cudaStream_t stream) {
   SharedArgs a;
   a.c = c;
@@ -1322,10 +1361,11 @@ cudaError_t launch_shared_combine(const PagedCache &c, const SharedGroups &g, co
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.TQ = 128 / a.G;
-  const RowsPlan p = shared_rows_plan(c.B, a.G);
+  a.most = p.most;
+  a.places = static_cast<int>(shared_rows_places(p, c.B, a.G));
   a.group = p.group;
-  a.gs = paged_rows_slot(p.group, a.G, false);
-  a.vrows = paged_rows_vrows(p, c.B, c.B, a.G, c.Hkv);
+  a.gs = paged_rows_slot(p.group, a.G, p.most > 0);
+  a.vrows = shared_rows_vrows(p, c.B, a.G, c.Hkv);
   a.nslots = paged_rows_shares() + a.vrows;
   a.ctas = sm_count();
   a.meta = static_cast<const int2 *>(rows_workspace);

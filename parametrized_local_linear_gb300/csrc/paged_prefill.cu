@@ -112,7 +112,7 @@ template <bool SHARED>
 __device__ __noinline__ Seq seq_of(const Args &a, int b) {
   if constexpr (SHARED) {
     const Group g = group_of(a.c, a.groups, a.seqlens, b);
-    return Seq{g.prefix, g.first, g.n, g.prefix > 0 ? (g.n + a.TQ - 1) / a.TQ : 0};
+    return Seq{g.prefix, g.first, g.n, g.prefix > 0 && g.n > a.few ? (g.n + a.TQ - 1) / a.TQ : 0};
   }
   // All loads first: they share one latency.
   const int n = a.seqlens[b], first = a.cu[b], end = a.cu[b + 1];
@@ -429,6 +429,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (SHARED && threadIdx.x == 64) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_r);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
   if (warp == 0) make_plan<SHARED>(a, plan, lane);
   if (threadIdx.x == 32) {
     mbar_init(smem_u32(q_full), 1);
@@ -1279,7 +1285,7 @@ SharedParts shared_parts(void *workspace, int B, int Hq, int Hkv) {
 }
 
 cudaError_t launch_shared_prefix(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
-                                 const int *seqlens, int Hq, const SharedParts &parts, cudaStream_t stream) {
+                                 const int *seqlens, int Hq, int few, const SharedParts &parts, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return cudaErrorInvalidValue;
   const bool fp8 = c.kscale != nullptr;
@@ -1288,6 +1294,7 @@ cudaError_t launch_shared_prefix(const PagedCache &c, const SharedGroups &g, con
   a.seqlens = seqlens;
   a.groups = g;
   a.shared = parts;
+  a.few = few;
   a.T = c.B;
   a.Hq = Hq;
   a.G = Hq / c.Hkv;

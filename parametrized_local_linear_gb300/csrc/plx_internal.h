@@ -134,6 +134,15 @@ cudaError_t launch_paged_rows(const RowsPlan &p, const PagedCache &c, const void
                               void *out, long long ots, long long ohs, float *lse, int T, int Hq,
                               void *workspace, cudaStream_t stream);
 
+// The bookkeeping of pages between two steps, and their compaction.
+size_t kv_update_workspace_bytes(int B, int num_pages, int max_pages);
+cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int *refs, const int *src,
+                             const int *lens, int *table_out, int *seqlens_out, int *refs_out,
+                             void *workspace, cudaStream_t stream);
+size_t kv_compact_workspace_bytes(int num_pages);
+cudaError_t launch_kv_compact(const PagedCache &c, const int *seqlens, const int *refs, int *table_out,
+                              int *refs_out, int *map, int *used, void *workspace, cudaStream_t stream);
+
 // Groups of sequences whose first prefix[g] keys are the same: sequences cu[g] ..
 // cu[g + 1] - 1, the pages those of the first one.
 struct SharedGroups {
@@ -151,23 +160,29 @@ struct SharedParts {
 constexpr int kSharedRec = 260;  // O1 / l, O2 / l, sigma / l, log2-sum-exp, padding
 size_t shared_parts_bytes(int B, int Hq, int Hkv);
 SharedParts shared_parts(void *workspace, int B, int Hq, int Hkv);
-// Keys of the groups' prefixes (tile kernel), then those behind them and the sum.
+// The rows kernel's part: the keys behind the shared ones, and, where p.most > 0, the
+// shared keys of groups of at most so many rows a kv head. Records as for
+// paged_rows_workspace_bytes, virtual rows those of the groups' prefixes, then the
+// sequences'.
+inline long long shared_rows_places(const RowsPlan &p, int B, int G) {
+  return p.most > 0 ? static_cast<long long>(B) * G / p.group + B : 0;
+}
+inline long long shared_rows_vrows(const RowsPlan &p, int B, int G, int Hkv) {
+  return (shared_rows_places(p, B, G) + static_cast<long long>(B) * G / p.group + B) * Hkv;
+}
+inline size_t shared_rows_workspace_bytes(const RowsPlan &p, int B, int G, int Hkv, int d) {
+  const long long vrows = shared_rows_vrows(p, B, G, Hkv);
+  return paged_rows_meta_bytes(vrows) + size_t(paged_rows_shares() + vrows) * paged_rows_slot(p.group, G, p.most > 0) *
+                                            (2 * size_t(d) + 2) * sizeof(float);
+}
+cudaError_t launch_shared_rows(const RowsPlan &p, const PagedCache &c, const SharedGroups &g, const void *q,
+                               const void *r, const int *seqlens, int Hq, void *workspace, cudaStream_t stream);
+// The tile kernel's part: the prefixes of groups of more than `few` sequences.
 cudaError_t launch_shared_prefix(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
-                                 const int *seqlens, int Hq, const SharedParts &parts, cudaStream_t stream);
-cudaError_t launch_shared_rows(const PagedCache &c, const SharedGroups &g, const void *q, const void *r,
-                               const int *seqlens, int Hq, void *workspace, cudaStream_t stream);
-cudaError_t launch_shared_combine(const PagedCache &c, const SharedGroups &g, const int *seqlens, int Hq,
-                                  const void *rows_workspace, const SharedParts &parts, void *out,
+                                 const int *seqlens, int Hq, int few, const SharedParts &parts, cudaStream_t stream);
+cudaError_t launch_shared_combine(const RowsPlan &p, const PagedCache &c, const SharedGroups &g, const int *seqlens,
+                                  int Hq, const void *rows_workspace, const SharedParts &parts, void *out,
                                   cudaStream_t stream);
-
-// The bookkeeping of pages between two steps, and their compaction.
-size_t kv_update_workspace_bytes(int B, int num_pages, int max_pages);
-cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int *refs, const int *src,
-                             const int *lens, int *table_out, int *seqlens_out, int *refs_out,
-                             void *workspace, cudaStream_t stream);
-size_t kv_compact_workspace_bytes(int num_pages);
-cudaError_t launch_kv_compact(const PagedCache &c, const int *seqlens, const int *refs, int *table_out,
-                              int *refs_out, int *map, int *used, void *workspace, cudaStream_t stream);
 
 // Chunks of any length (tcgen05). lse ([T, Hq] fp32) may be null. Sequences of at
 // most `few` rows a kv head are left as they were.

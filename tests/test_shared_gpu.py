@@ -26,7 +26,7 @@ def ints(x):
     return torch.tensor(x, dtype=I32, device="cuda")
 
 
-def problem(sizes, prefix, lens, Hq, Hkv, page, fp8, seed=3, hide=True):
+def cache(sizes, prefix, lens, Hq, Hkv, page, fp8, seed=3, hide=True):
     """A pool in which every group's sequences begin with the same keys, each with its
     own pages: the whole ones in front of a sequence's own keys are then taken out of
     its table (hide), but for the first of a group."""
@@ -41,7 +41,6 @@ def problem(sizes, prefix, lens, Hq, Hkv, page, fp8, seed=3, hide=True):
         b += n
     B = len(lens)
     q, r = ref.normal_rows(B, Hq, seed + 1), ref.normal_rows(B, Hq, seed + 2, 0.05)
-    want = ref.reference(pool, q, r, [1] * B)
     kw = pool.to("cuda")
     b = 0
     for n, p in zip(sizes, prefix):
@@ -50,7 +49,13 @@ def problem(sizes, prefix, lens, Hq, Hkv, page, fp8, seed=3, hide=True):
                 kw["block_table"][i, :max(0, p) // page] = -7
         b += n
     kw.update(seqlens=pool.seqlens.cuda(), cu_g=ends(sizes), prefix_lens=ints(prefix))
-    return q.cuda(), r.cuda(), kw, want
+    return pool, q.cuda(), r.cuda(), kw
+
+
+def problem(*args, **kw):
+    """Queries, probes and arguments of a call, and what it gives in fp64."""
+    pool, q, r, args = cache(*args, **kw)
+    return q, r, args, ref.reference(pool, q.cpu(), r.cpu(), [1] * len(pool.lens))
 
 
 CASES = [
@@ -69,6 +74,10 @@ CASES = [
     ([3, 2], [64, 64], [64, 64, 64, 64, 64], 4, 2, 64),         # no keys behind any prefix
     ([2], [300], [301, 320], 128, 1, 32),                       # a whole tile of query heads
     ([2], [300], [301, 320], 96, 1, 32),                        # heads that do not fill one
+    ([1] * 8 + [20] + [2] * 3, [100] * 8 + [333] + [50] * 3, [101] * 8 + [340] * 20 + [60] * 6, 4, 2, 16),  # both kernels
+    ([9] * 5, [90, 90, 90, 64, 1], [100] * 45, 4, 2, 32),       # row tiles that few sequences fill
+    ([12, 9], [130, 70], [131, 20, 0, 129, 130] + [150] * 7 + [70] * 9, 4, 2, 16),  # shorter than the prefix there
+    ([40], [4000], [4001 + i for i in range(40)], 8, 1, 64),    # split, and several row tiles
 ]
 
 
@@ -87,6 +96,56 @@ def test_shared_decode_matches_fp64(sizes, prefix, lens, Hq, Hkv, page, fp8):
     assert torch.equal(out, again)
 
 
+def some_rows(out, q, r, pool, bs):
+    """Rows `bs` of a decode against fp64."""
+    G = q.shape[1] // pool.Hkv
+    for b in bs:
+        n = pool.lens[b]
+        K, V = pool.get(b, n)
+        for h in range(q.shape[1]):
+            o, _, bound = ref.attend(q[b:b + 1, h].double().cpu().numpy(), r[b:b + 1, h].double().cpu().numpy(),
+                                     K[:, h // G], V[:, h // G], [n])
+            assert np.all(np.abs(out[b, h].double().cpu().numpy() - o[0]) <= bound[0]), (b, h)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_alike_groups(fp8):
+    """So many row tiles that the CTAs take whole ones in rounds; shared pages."""
+    device()
+    n, groups, page = 33, 58, 16
+    B = n * groups
+    pool = ref.Pool([70] * B, 16, page, fp8, 3)
+    g = torch.Generator().manual_seed(4)
+    for name in ("k", "v"):
+        x = getattr(pool, name)
+        if fp8:  # codes of up to 15 (0x57), scales 2^-3 and 2^-4
+            codes = torch.randint(0, 0x58, x.shape, generator=g, dtype=torch.uint8)
+            setattr(pool, name, (codes + 128 * torch.randint(0, 2, x.shape, generator=g, dtype=torch.uint8)
+                                 ).view(torch.float8_e4m3fn))
+            setattr(pool, name + "s", torch.randint(123, 125, x.shape[:3], generator=g, dtype=torch.uint8))
+        else:
+            x.copy_(torch.randn(x.shape, generator=g))
+    for b in range(B):
+        pool.table[b, :4] = pool.table[b - b % n, :4]
+    q, r = ref.normal_rows(B, 16, 5).cuda(), ref.normal_rows(B, 16, 6, 0.05).cuda()
+    out = plx_decode_fwd_shared(q, r, seqlens=pool.seqlens.cuda(), cu_g=ends([n] * groups),
+                                prefix_lens=ints([64] * groups), **pool.to("cuda"))
+    plx_check_device_error()
+    some_rows(out, q, r, pool, random.Random(1).sample(range(B), 40))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_more_sequences_than_are_looked_up_ahead(fp8):
+    """600 sequences in groups of two, and some in none."""
+    device()
+    sizes, prefix = [2] * 290, [20 + b % 40 for b in range(290)]
+    lens = [p + 1 + b % 7 for b, p in enumerate(prefix) for _ in range(2)] + [5] * 20
+    pool, q, r, kw = cache(sizes, prefix, lens, 2, 1, 16, fp8)
+    out = plx_decode_fwd_shared(q, r, **kw)
+    plx_check_device_error()
+    some_rows(out, q, r, pool, range(len(lens)))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_random_groups(fp8):
     """Sizes of all kinds, some sequences in no group."""
@@ -94,7 +153,7 @@ def test_random_groups(fp8):
     for seed in range(8):
         rng = random.Random(seed)
         page, (Hq, Hkv) = rng.choice([16, 32, 64, 128, 256]), rng.choice([(4, 2), (8, 1), (6, 2), (3, 3), (20, 2)])
-        sizes = [rng.choice([0, 1, 2, 3, 8]) for _ in range(rng.randint(1, 6))]
+        sizes = [rng.choice([0, 1, 2, 3, 8] if seed % 2 else [0, 9, 20, 33]) for _ in range(rng.randint(1, 6))]
         prefix, lens = [], []
         for n in sizes:
             p = rng.choice([0, 1, rng.randint(1, 700)])
@@ -228,7 +287,7 @@ def test_two_streams_at_once():
 @pytest.mark.parametrize("fp8", [False, True])
 def test_debug_build_gives_the_same_bits(fp8, monkeypatch):
     device()
-    cases = [problem(*c, fp8) for c in CASES[1:10]]
+    cases = [problem(*c, fp8) for c in CASES[1:]]
     want = [plx_decode_fwd_shared(q, r, **kw) for q, r, kw, _ in cases]
     plx_check_device_error()
     monkeypatch.setattr(binding, "_lib", binding.load_debug_lib())
