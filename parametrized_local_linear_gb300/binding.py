@@ -868,6 +868,8 @@ def _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, outs):
         if t.shape != shape or heads.setdefault(name == "k", H) != H:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with {first}'s "
                              f"{tuple(x.shape)}")
+        if H == 0:
+            raise ValueError(f"{name} has no heads")
         if o is not None and o.shape != shape:
             raise ValueError(f"{name}_out has shape {tuple(o.shape)}, expected {tuple(shape)}")
     for name, t, o in given:
@@ -926,7 +928,7 @@ def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale,
                 good = good and (Hq == 0 or H == Hq)
                 Hq = H
             st = t.stride()
-            good = (good and t.dtype is dtype and t.get_device() == index and st[-1] == 1
+            good = (good and H > 0 and t.dtype is dtype and t.get_device() == index and st[-1] == 1
                     and ts == ((L, H, d) if packed else (B, H, L, d)))
             # (sequence, token, head)
             strides[3 * at:3 * at + 3] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])

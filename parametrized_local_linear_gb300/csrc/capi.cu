@@ -750,6 +750,7 @@ plx_status plx_decode_fwd_shared(const void *q, const void *r, const void *kpage
   if (s) return s;
   if (!q || !r || !out || !seqlens) return fail(PLX_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (ngroups < 1) return fail(PLX_ERR_INVALID_ARG, "%s: ngroups (%d) must be >= 1", fn, ngroups);
+  if (ngroups > 1 << 24) return fail(PLX_ERR_UNSUPPORTED, "%s: ngroups (%d) must be <= 2^24", fn, ngroups);
   if (!cu_g || !prefix_lens) return fail(PLX_ERR_INVALID_ARG, "%s: null cu_g or prefix_lens", fn);
   if (!aligned16(q) || !aligned16(r) || !aligned16(out))
     return fail(PLX_ERR_INVALID_ARG, "%s: tensor pointers must be 16-byte aligned", fn);
@@ -897,6 +898,10 @@ plx_status rotary(const char *fn, bool backward, const void *const (&in)[3], voi
     t[i] = {in[i], out[i], B > 1 ? si[0] : 0, L > 1 ? si[1] : 0, heads[i] > 1 ? si[2] : 0,
             B > 1 ? so[0] : 0, L > 1 ? so[1] : 0, heads[i] > 1 ? so[2] : 0};
   }
+  for (int i = 0; i < 3; ++i)
+    for (int k = 0; k < 3; ++k)
+      if (i != k && out[i] && (out[i] == in[k] || out[i] == out[k]))
+        return fail(PLX_ERR_INVALID_ARG, "%s: %c's output is %c or its output", fn, names[i], names[k]);
   if (B == 0 || L == 0) return PLX_OK;
   return finish_launch(
       plx::launch_rotary(t, heads, positions, seqlens, cu_q, nseq, inv_freq, static_cast<float>(scale), backward, B,

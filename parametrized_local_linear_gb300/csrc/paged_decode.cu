@@ -172,6 +172,7 @@ constexpr int kRowCost = KEYS > 0 ? 8 : 0;
 // A sequence's part of the stream that is cut into shares.
 template <int KEYS>
 __device__ __forceinline__ long long units(const Seq &s, const RowsArgs &a) {
+  if constexpr (KEYS == kWhole) return static_cast<long long>(s.tiles) * s.ng * a.c.Hkv;
   return s.tiles > 0 ? static_cast<long long>(s.tiles + kRowCost<KEYS>) * s.ng * a.c.Hkv : 0;
 }
 
@@ -188,10 +189,9 @@ struct Walk {
   long long pos, e, base;
   int b;
   Seq s;
-  const int2 *known;
-  __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a, const int2 *known_)
-      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, KEYS>(a, p.b0, known_)), known(known_) {}
-  __device__ __forceinline__ bool next(Item &it, const RowsArgs &a) {
+  __device__ __forceinline__ Walk(const Plan &p, const RowsArgs &a, const int2 *known)
+      : pos(p.s), e(p.e), base(p.base), b(p.b0), s(seq_of<KT, GS, KEYS>(a, p.b0, known)) {}
+  __device__ __forceinline__ bool next(Item &it, const RowsArgs &a, const int2 *known) {
     constexpr int X = kRowCost<KEYS>;
     int vh, t0, t1;
     do {
@@ -208,7 +208,7 @@ struct Walk {
       t0 = static_cast<int>(off - static_cast<long long>(vh) * (s.tiles + X)) - X;
       t1 = static_cast<int>(min(static_cast<long long>(s.tiles), t0 + (e - pos)));
       pos += t1 - t0;
-    } while (KEYS > 0 && t1 <= 0);  // no tile: only of what stands for the row's fixed cost
+    } while (KEYS != kWhole && t1 <= 0);  // no tile: only of what stands for the row's fixed cost
     it.s = s;
     it.b = b;
     it.kvh = vh / s.ng;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   Plan *plan = reinterpret_cast<Plan *>(smem + OFF_PLAN);
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int2 *known = reinterpret_cast<const int2 *>(smem + OFF_KNOWN);
+  const int2 *known = SUFFIX ? reinterpret_cast<const int2 *>(smem + OFF_KNOWN) : nullptr;
   if constexpr (SUFFIX) {
     int2 *to = reinterpret_cast<int2 *>(smem + OFF_KNOWN);
     for (int i = threadIdx.x; i < min(a.c.B, KNOWN); i += THREADS) to[i] = own_keys(a, i);
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       Item it;
       int g = 0;
       bool ok = true;
-      while (ok && wk.next(it, a)) {
+      while (ok && wk.next(it, a, known)) {
         const int *table = a.c.table + static_cast<long long>(SUFFIX ? it.s.first : it.b) * a.c.max_pages;
         const int end = min(tile_key<KT, KEYS>(it, it.t1), it.s.len);
         int key = tile_key<KT, KEYS>(it, it.t0) + first_key;
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
       Item it;
       int g = 0;
       bool ok = true;
-      while (ok && wk.next(it, a)) {
+      while (ok && wk.next(it, a, known)) {
         const int *table = a.c.table + static_cast<long long>(SUFFIX ? it.s.first : it.b) * a.c.max_pages;
         int key = tile_key<KT, KEYS>(it, it.t0);
         const int end = tile_key<KT, KEYS>(it, it.t1);
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   Walk<KT, GS, KEYS> wk(pl, a, known);
   Item it;
   int gt = 0;  // tiles of the previous items
-  while (wk.next(it, a)) {
+  while (wk.next(it, a, known)) {
     const int nt = it.t1 - it.t0;
     const int r0 = it.grp * GS, nr = min(GS, it.s.n * a.G - r0);  // this group's rows
     const int t_first = (line - gt % NL + NL) % NL;
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     // The last key that row tq sees (< 0: none), and that all rows see.
     int last = mine < nr ? it.s.len - it.s.n + (r0 + mine) / a.G : -1;
     int all_see = it.s.len - it.s.n + r0 / a.G;
-    if (KEYS == kAll && it.b < a.groups.n) {
+    if (KEYS == kAll && it.b < a.groups.n) {  // as many of the shared keys as it has
       if (mine < nr) {
         const int m = it.s.first + (r0 + mine) / a.G;
         last = min(it.s.len, m < KNOWN ? known[m].x : cache_len(a.c, a.seqlens, m)) - 1;

@@ -67,7 +67,7 @@ def test_cache_arguments_are_checked(lib, call, kw, status, word):
 
 @pytest.mark.parametrize("kw,status,word", [
     (dict(q=None), INV, b"null"), (dict(out=None), INV, b"null"), (dict(cu=None), INV, b"cu_g"),
-    (dict(pre=None), INV, b"prefix_lens"), (dict(ng=0), INV, b"ngroups"), (dict(Hq=3), INV, b"multiple"),
+    (dict(pre=None), INV, b"prefix_lens"), (dict(ng=0), INV, b"ngroups"), (dict(ng=(1 << 24) + 1), UNS, b"2^24"), (dict(Hq=3), INV, b"multiple"),
     (dict(Hq=512), UNS, b"at most 128"), (dict(r=ODD), INV, b"aligned"), (dict(B=1 << 23), UNS, b"2^24"),
 ])
 def test_shared_arguments_are_checked(lib, kw, status, word):
@@ -97,7 +97,8 @@ def test_compact_arguments_are_checked(lib, kw, status, word):
 def _turn(lib, fn="plx_rotary_fwd", st=None, **kw):
     # sequence, token, head of q, k, r, q_out, k_out, r_out
     strides = [2 * 4 * 128, 128, 2 * 128] * 6 if st is None else st
-    a = dict(q=P, k=P, r=P, qo=Q, ko=Q, ro=Q, strides=(ctypes.c_longlong * 18)(*strides), pos=None, sl=None, cu=None,
+    V = [ctypes.c_void_p(4096 * i) for i in range(1, 7)]
+    a = dict(q=V[0], k=V[1], r=V[2], qo=V[3], ko=V[4], ro=V[5], strides=(ctypes.c_longlong * 18)(*strides), pos=None, sl=None, cu=None,
              freq=P, scale=1.0, nseq=0, B=3, L=2, Hq=4, Hkv=4, d=128, R=128, near=0, dtype=0)
     a.update(kw)
     return getattr(lib, fn)(*a.values(), None)
@@ -113,6 +114,7 @@ def _turn(lib, fn="plx_rotary_fwd", st=None, **kw):
     (dict(q=None, k=None, r=None, qo=None, ko=None, ro=None), INV, b"all null"),
     (dict(qo=None), INV, b"both"), (dict(k=None), INV, b"both"), (dict(r=ODD), INV, b"aligned"),
     (dict(B=1 << 20, L=1 << 12), UNS, b"2^31"), (dict(qo=P, st=[1024, 128, 256] * 3 + [2048, 128, 256] * 3), INV, b"same strides"),
+    (dict(ko=P), INV, b"output is q"), (dict(qo=Q, k=Q, ko=Q), INV, b"output is k"), (dict(ro=ctypes.c_void_p(5 * 4096)), INV, b"output is"),
     (dict(st=[1024, 128, 0] * 6), INV, b"multiples"), (dict(st=[1024, 132, 256] * 6), INV, b"multiples"),
     (dict(st=[1024, 128, 256] * 3 + [1024, 128, 128] * 3), INV, b"overlap"),
     (dict(st=[1024, 128, 256] * 3 + [512, 128, 256] * 3), INV, b"overlap"),
@@ -232,6 +234,7 @@ def _rot(**kw):
     (dict(k=torch.zeros(2, 2, 8, 128, dtype=BF)), ValueError, "k has shape"),
     (dict(r=torch.zeros(2, 3, 9, 128, dtype=BF)), ValueError, "r has shape"),
     (dict(q_out=torch.zeros(2, 4, 9, 64, dtype=BF)), ValueError, "q_out has shape"),
+    (dict(k=torch.zeros(2, 0, 9, 128, dtype=BF)), ValueError, "no heads"),
 ])
 def test_rotary_tensors_are_checked(kw, error, word):
     with pytest.raises(error, match=word):
