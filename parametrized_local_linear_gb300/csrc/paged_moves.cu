@@ -141,12 +141,57 @@ __device__ __forceinline__ Row load_row(const Row *r) {
   return x;
 }
 
+// Job `job` of row b's Hkv + 1, by THREADS threads: its entries, or the slots of one kv
+// head of its copied page.
+__device__ __forceinline__ void move_row(const UpdateArgs &a, const Row &r, int b, int job, int thread) {
+  const int shift = a.c.page_shift;
+  if (job == 0) {
+    const long long base = static_cast<long long>(b) * a.c.max_pages;
+    const int *from = a.stage != nullptr ? a.stage + base : a.c.table + static_cast<long long>(max(r.src, 0)) * a.c.max_pages;
+    const int pages = (r.new_len + (1 << shift) - 1) >> shift, kept = r.full + r.keep;
+    const bool stays = a.stage != nullptr && r.src == b;  // in place: its old entries are there
+    for (int j = (stays ? kept : 0) + thread; j < pages; j += THREADS)
+      a.table_out[base + j] = j < r.full ? from[j] : j < kept ? r.tail : __ldcg(&a.free_list[r.start + j - kept]);
+    if (thread == 0) a.seqlens_out[b] = r.new_len;
+    return;
+  }
+  if (!r.copies) return;
+  const int to = __ldcg(&a.free_list[r.start]);
+  const long long src = (static_cast<long long>(r.tail) * a.c.Hkv + job - 1) << shift;
+  const long long dst = (static_cast<long long>(to) * a.c.Hkv + job - 1) << shift;
+  if (!PLX_IN_BOUNDS(row_inside(a.c, src + r.part - 1) && row_inside(a.c, dst + r.part - 1), ErrWord{a.c.err})) return;
+  const int bytes = a.c.kscale != nullptr ? D : 2 * D;  // of a slot
+  const int n = r.part * bytes / 16;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    uint8_t *pages = const_cast<uint8_t *>(static_cast<const uint8_t *>(kv ? a.c.v : a.c.k));
+    const uint4 *x = reinterpret_cast<const uint4 *>(pages + src * bytes);
+    uint4 *y = reinterpret_cast<uint4 *>(pages + dst * bytes);
+    for (int i = thread; i < n; i += 4 * THREADS) {
+      uint4 w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * THREADS < n) w[k] = x[i + k * THREADS];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * THREADS < n) y[i + k * THREADS] = w[k];
+    }
+    if (a.c.kscale != nullptr) {
+      uint8_t *scale = const_cast<uint8_t *>(kv ? a.c.vscale : a.c.kscale);
+      for (int i = thread; i < r.part; i += THREADS) scale[dst + i] = scale[src + i];
+    }
+  }
+}
+
 // One cluster: reference counts; which rows keep their partial last page (the first
 // row of those that have it, if no row has all of it: the rows claim it by their
-// number, in place of the count 0); how many fresh pages each needs, and which.
+// number, in place of the count 0); how many fresh pages each needs, and which. With
+// MOVES it writes the rows too: where every row keeps its own tokens few pages are
+// copied, and a second launch would cost more (of a step's 23 us of host time 4).
+template <bool MOVES>
 __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kernel(const UpdateArgs a) {
   const int P = 1 << a.c.page_shift, B = a.c.B, rank = blockIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!MOVES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.refs != a.refs_out) {
     for (int p = rank * PLAN + threadIdx.x; p < a.c.num_pages; p += CL * PLAN) a.refs_out[p] = a.refs[p];
     cluster_sync();
@@ -244,50 +289,20 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
       if (r.keep) a.refs_out[r.tail] = 1;
     }
   }
+  if constexpr (MOVES) {
+    cluster_sync();
+    constexpr int PER = PLAN / THREADS;
+    for (int b = rank * PER + threadIdx.x / THREADS; b < B; b += CL * PER) {
+      const Row r = load_row(&a.rows[b]);
+      for (int job = 0; job <= (r.copies ? a.c.Hkv : 0); ++job) move_row(a, r, b, job, threadIdx.x % THREADS);
+    }
+  }
 }
 
-// Blocks of a row: one writes its entries, one a kv head copies its partial page.
 __global__ void __launch_bounds__(THREADS) update_move_kernel(const UpdateArgs a) {
-  const int b = blockIdx.x / (a.c.Hkv + 1), job = blockIdx.x - b * (a.c.Hkv + 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Row r = a.rows[b];
-  const int shift = a.c.page_shift;
-  if (job == 0) {
-    const long long base = static_cast<long long>(b) * a.c.max_pages;
-    const int *from = a.stage != nullptr ? a.stage + base : a.c.table + static_cast<long long>(max(r.src, 0)) * a.c.max_pages;
-    const int pages = (r.new_len + (1 << shift) - 1) >> shift, kept = r.full + r.keep;
-    const bool stays = a.stage != nullptr && r.src == b;  // in place: its old entries are there
-    for (int j = (stays ? kept : 0) + threadIdx.x; j < pages; j += THREADS)
-      a.table_out[base + j] = j < r.full ? from[j] : j < kept ? r.tail : a.free_list[r.start + j - kept];
-    if (threadIdx.x == 0) a.seqlens_out[b] = r.new_len;
-    return;
-  }
-  if (!r.copies) return;
-  const int to = a.free_list[r.start];
-  const long long src = (static_cast<long long>(r.tail) * a.c.Hkv + job - 1) << shift;
-  const long long dst = (static_cast<long long>(to) * a.c.Hkv + job - 1) << shift;
-  if (!PLX_IN_BOUNDS(row_inside(a.c, src + r.part - 1) && row_inside(a.c, dst + r.part - 1), ErrWord{a.c.err})) return;
-  const int bytes = a.c.kscale != nullptr ? D : 2 * D;  // of a row
-  const int n = r.part * bytes / 16;
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    uint8_t *pages = const_cast<uint8_t *>(static_cast<const uint8_t *>(kv ? a.c.v : a.c.k));
-    const uint4 *x = reinterpret_cast<const uint4 *>(pages + src * bytes);
-    uint4 *y = reinterpret_cast<uint4 *>(pages + dst * bytes);
-    for (int i = threadIdx.x; i < n; i += 4 * THREADS) {
-      uint4 w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k * THREADS < n) w[k] = x[i + k * THREADS];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k * THREADS < n) y[i + k * THREADS] = w[k];
-    }
-    if (a.c.kscale != nullptr) {
-      uint8_t *scale = const_cast<uint8_t *>(kv ? a.c.vscale : a.c.kscale);
-      for (int i = threadIdx.x; i < r.part; i += THREADS) scale[dst + i] = scale[src + i];
-    }
-  }
+  const int b = blockIdx.x / (a.c.Hkv + 1);
+  move_row(a, load_row(&a.rows[b]), b, blockIdx.x - b * (a.c.Hkv + 1), threadIdx.x);
 }
 
 // ---------------------------------------------------------------- compaction
@@ -439,7 +454,11 @@ cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int 
   a.free_list = reinterpret_cast<int *>(ws);
   ws += round256(size_t(c.num_pages) * 4);
   a.stage = table_out == c.table ? reinterpret_cast<int *>(ws) : nullptr;
-  update_plan_kernel<<<CL, PLAN, 0, stream>>>(a);
+  if (src == nullptr) {
+    update_plan_kernel<true><<<CL, PLAN, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  update_plan_kernel<false><<<CL, PLAN, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_after(update_move_kernel, static_cast<unsigned>(c.B) * (c.Hkv + 1), a, stream);
 }
