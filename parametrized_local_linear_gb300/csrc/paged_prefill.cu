@@ -62,6 +62,7 @@ constexpr int RAW = BN * D;           // 8 KB: an e4m3 K or V tile
 constexpr int NRAW = 3;               // raw stages (K and V together)
 constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_T = 64, COL_O1 = 256, COL_O2 = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kIdle = -2;
 constexpr int EP_WARP = 4, O1_WARP = 8, S_WARP = 10, LOAD_WARP = 12;
 
 template <bool FP8>
@@ -527,12 +528,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     bool ok = true;
     for (int k = 0; ok && walk_next<true, SHARED>(wk, a); ++k) {
       float m_used = -INFINITY, l = 0.f, sg = 0.f;
-      // SHARED: the last key that the row sees. From tile `whole` on, some row (of the warp)
+      // SHARED: the last key that the row sees, or kIdle in a warp whose rows the item
+      // does not have (groups of few sequences), which only hands over. From tile `whole` on, some row (of the warp)
       // does not see all keys of a tile.
       int seen = 0, whole_seen = it.pos0;
       if constexpr (SHARED) {
-        const bool there = rtok < min(it.ntok, a.TQ);
-        seen = there ? min(it.len, cache_len(a.c, a.seqlens, it.row0 + rtok)) - 1 : it.len - 1;
+        const int ntok = min(it.ntok, a.TQ);
+        seen = rtok < ntok ? min(it.len, cache_len(a.c, a.seqlens, it.row0 + rtok)) - 1 : it.len - 1;
+        if (warp * 32 >= ntok * a.G) seen = kIdle;
         whole_seen = __reduce_min_sync(0xffffffffu, seen);
       }
       const int n = it.j1 - it.j0, whole = max(0, (whole_seen + 1) / BN - it.j0);
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           // does V (bf16; converted tiles have them).
           const int key0 = (it.j0 + j) * BN, lim = (SHARED ? seen : it.pos0 + rtok) - key0, valid = it.len - key0;
 #pragma unroll 1
-          for (int qq = 0; qq < 8; ++qq) {
+          for (int qq = SHARED && seen == kIdle ? 8 : 0; qq < 8; ++qq) {
             if (qq >= 4 && valid >= BN) break;
             const uint32_t col = cs + (qq < 4 ? 0 : COL_T - BN) + 16 * qq;
             const int last = qq < 4 ? lim : valid - 1 + BN;
@@ -576,6 +579,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
             }
             fence_proxy_async_smem();
           }
+        }
+        if (SHARED && seen == kIdle) {
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&p_full[2 * x]));
+            mbar_arrive(smem_u32(&p_full[2 * x + 1]));
+          }
+          continue;
         }
         float s[64];
         tmem_ld32(cs, *reinterpret_cast<float(*)[32]>(&s[0]));
@@ -710,9 +721,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         // A part of an item: raw sums for the merge (SHARED: for the last sums). The share's first item
         // goes to slot 0, a later one (its last) to slot 1.
         const int slot = k == 0 ? 0 : 1;
+        const bool idle = SHARED && qw * 32 >= min(it.ntok, a.TQ) * a.G;  // no rows of the item
+        if (idle) o_read();
         float4 *p4 = reinterpret_cast<float4 *>((SHARED ? a.shared.raw : a.parts) + (2ll * blockIdx.x + slot) * PART);
 #pragma unroll 1
-        for (int part = 0; part < 8; ++part) {
+        for (int part = idle ? 8 : 0; part < 8; ++part) {
           float o[32];
           tmem_ld32(tl + (part < 4 ? COL_O1 : COL_O2) + (part & 3) * 32, o);
           tmem_wait_ld();
