@@ -26,8 +26,8 @@ struct UpdateArgs {
   int *table_out, *seqlens_out, *refs_out;
   Row *rows;
   int *free_list;
-  int *counts;  // free pages of every block's segment
-  int *stage;  // old entries of the rows when the tables are updated in place, else null
+  int *counts;  // free pages of every block's segment, then the pages that rows need
+  int *stage;   // old entries of the rows when the tables are updated in place, else null
 };
 
 __device__ __forceinline__ bool good_page(const PagedCache &c, int page) {
@@ -208,43 +208,52 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
     if (v == 0 || v < INT_MIN / 2) atomicMin(&a.refs_out[tail], INT_MIN + b);
   }
   cluster_sync();
-  // Every block sums the rows' needs; the first writes them down.
-  long long total = 0;
-  for (int b0 = 0; b0 < B; b0 += PLAN) {
-    const int b = b0 + threadIdx.x;
-    int need = 0;
-    Row r;
-    if (b < B) {
-      r = load_row(&a.rows[b]);
-      r.keep = r.tail >= 0 && __ldcg(&a.refs_out[r.tail]) == INT_MIN + b;
-      r.copies = r.tail >= 0 && !r.keep;
-      need = ((r.new_len + P - 1) >> a.c.page_shift) - r.full - r.keep;
-    }
-    long long all;
-    const long long at = total + block_scan<long long>(need, &all);
-    if (b < B && rank == 0) {
-      r.start = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
-      a.rows[b] = r;
-    }
-    total += all;
-  }
-  int p0, found = 0;
+  // The free pages of every block's segment; the first block also sums the rows' needs.
+  // (No barrier of the cluster is behind a condition on data: blocks that saw
+  // different data, as a call that overlaps another on the same cache could, would
+  // wait for ever.)
+  int p0, mine = 0, all_free;
   const int p1 = segment(a.c.num_pages, &p0);
-  if (total > 0) {
-    int mine = 0;
-    for (int p = p0 + threadIdx.x; p < p1; p += PLAN) mine += __ldcg(&a.refs_out[p]) == 0;
-    int all;
-    block_scan<int>(mine, &all);
-    if (threadIdx.x == 0) a.counts[rank] = all;
-    cluster_sync();
+  for (int p = p0 + threadIdx.x; p < p1; p += PLAN) mine += __ldcg(&a.refs_out[p]) == 0;
+  block_scan<int>(mine, &all_free);
+  if (threadIdx.x == 0) a.counts[rank] = all_free;
+  if (rank == 0) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < B; b0 += PLAN) {
+      const int b = b0 + threadIdx.x;
+      int need = 0;
+      Row r;
+      if (b < B) {
+        r = load_row(&a.rows[b]);
+        r.keep = r.tail >= 0 && __ldcg(&a.refs_out[r.tail]) == INT_MIN + b;
+        r.copies = r.tail >= 0 && !r.keep;
+        need = ((r.new_len + P - 1) >> a.c.page_shift) - r.full - r.keep;
+      }
+      long long all;
+      const long long at = sum + block_scan<long long>(need, &all);
+      if (b < B) {
+        r.start = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
+        a.rows[b] = r;
+      }
+      sum += all;
+    }
+    if (threadIdx.x == 0) a.counts[CL] = static_cast<int>(min(sum, static_cast<long long>(INT_MAX)));
+  }
+  cluster_sync();
+  __shared__ int counts[CL + 1];
+  if (threadIdx.x <= CL) counts[threadIdx.x] = __ldcg(&a.counts[threadIdx.x]);
+  __syncthreads();
+  const int total = counts[CL];
+  int found = 0;
+  {
     int below = 0;
     for (int i = 0; i < CL; ++i) {
-      const int n = __ldcg(&a.counts[i]);
-      if (i < rank) below += n;
-      found += n;
+      if (i < rank) below += counts[i];
+      found += counts[i];
     }
+    found = min(found, a.c.num_pages);
     // Where the free pages do not do: the rows from the first one that they do not serve on.
-    long long granted = total;
+    int granted = min(total, found);
     if (total > found) {
       __shared__ int least;
       if (threadIdx.x == 0) least = found;
@@ -277,7 +286,9 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
       below += n;
     }
   }
-  // The first block's rows: without pages where there are none.
+  // The first block's rows: without pages where there are none, once all blocks have
+  // read their needs.
+  cluster_sync();
   if (rank == 0) {
     for (int b = threadIdx.x; b < B; b += PLAN) {
       const Row r = a.rows[b];  // this thread's
@@ -430,7 +441,7 @@ cudaError_t launch_after(void (*kernel)(Args), unsigned grid, const Args &a, cud
 }  // namespace
 
 size_t kv_update_workspace_bytes(int B, int num_pages, int max_pages) {
-  return round256(size_t(B) * sizeof(Row)) + round256(CL * 4) + round256(size_t(num_pages) * 4) +
+  return round256(size_t(B) * sizeof(Row)) + round256((CL + 1) * 4) + round256(size_t(num_pages) * 4) +
          size_t(B) * max_pages * 4;
 }
 
@@ -450,7 +461,7 @@ cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int 
   a.rows = reinterpret_cast<Row *>(ws);
   ws += round256(size_t(c.B) * sizeof(Row));
   a.counts = reinterpret_cast<int *>(ws);
-  ws += round256(CL * 4);
+  ws += round256((CL + 1) * 4);
   a.free_list = reinterpret_cast<int *>(ws);
   ws += round256(size_t(c.num_pages) * 4);
   a.stage = table_out == c.table ? reinterpret_cast<int *>(ws) : nullptr;

@@ -221,6 +221,23 @@ def test_pools_of_all_sizes(n, free):
     c.check()
 
 
+@pytest.mark.parametrize("B", [3, 64, 700])
+def test_steps_that_need_nothing_or_too_much(B):
+    """Back to back on one stream: rows that keep partial pages and need no other,
+    and rows of which most find none."""
+    device()
+    c = Cache(B, 4, 2 * B, 16, 1, True, seed=B)
+    c.update([1 + b % 30 for b in range(B)])
+    for i in range(60):
+        same = list(c.lens)
+        if i % 3 == 2:
+            same = [min(64, n + 20) for n in same]
+        c.update(same, [b for b in range(B)] if i % 2 else None)
+        if i % 3 == 2:
+            c.update([max(1, n - 25 - b % 7) if n else 0 for b, n in enumerate(c.lens)])
+    c.check()
+
+
 def test_many_rows():
     """More rows than the planning block has threads."""
     device()
