@@ -34,6 +34,13 @@
 // warp or the T thread that also loaded held the others up by about as long
 // as a tile takes). Tensor memory as in prefill_tc.cu.
 //
+// Shared prefixes (SHARED): the sequences are groups, their tokens the group's
+// sequences (decode's queries), which all see the group's keys (as many as they
+// have). An item's sums are not results yet: parts as above, records of whole items;
+// a warp without rows of an item (groups of few sequences) only hands over. 128
+// rows over 32768 keys of 8 kv heads: 21 us of tiles (5.8 TB/s of keys and values), and
+// about 12 around them: the plan, the way to the first tile, the raw sums.
+//
 // What bounds it: bf16 as prefill_tc.cu, the tile's chain of hand-overs and the
 // shared-memory operands of its products (tensor pipe 63% busy); e4m3 the
 // softmax warps' issue slots, which four converter warps share (57% of all slots
