@@ -165,9 +165,7 @@ __device__ __forceinline__ long long tile_sum(long long n, int TQ, long long b) 
   return ((inc << lg) * (q * (q - 1) / 2)) + q * all + rest * q * inc + some;
 }
 // Key tiles of the first t row tiles (t <= nq).
-template <bool SHARED>
 __device__ __noinline__ long long tiles_before(const Seq &s, int t, int TQ) {
-  if constexpr (SHARED) return static_cast<long long>(t) * tiles_of<true>(s, 0, TQ);
   if (t <= 0) return 0;
   long long extra = 0;
   if (t == s.nq) extra = tiles_of<false>(s, --t, TQ);  // the last row tile may be short
@@ -285,9 +283,8 @@ __device__ __forceinline__ Seq seq_from(const Seq &s, int l) {
              __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.nq, l)};
 }
 // One warp: the CTA's share and where it starts.
-template <bool SHARED>
 __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
-  const int c = blockIdx.x, count = SHARED ? a.groups.n : a.c.B;
+  const int c = blockIdx.x, count = a.c.B;
   long long U = 0, u0 = 0;  // mine, u0: sequence `lane`
   int items = 0;
   Seq mine = {}, s0 = {};
@@ -295,10 +292,10 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
   for (int i0 = 0; i0 < count; i0 += 32) {
     const int i = i0 + lane;
     Seq s = {};
-    if (i < count) s = seq_of<SHARED>(a, i);
+    if (i < count) s = seq_of<false>(a, i);
     if (i0 == 0) s0 = seq_from(s, 0);
     if (i < count) {
-      const long long u = tiles_before<SHARED>(s, s.nq, a.TQ) * a.c.Hkv;
+      const long long u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
       if (i0 == 0) {
         u0 = u;
         mine = s;
@@ -334,8 +331,8 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
       if (i0 > 0) {
         u = 0;
         if (i < count) {
-          const Seq s = seq_of<SHARED>(a, i);
-          u = tiles_before<SHARED>(s, s.nq, a.TQ) * a.c.Hkv;
+          const Seq s = seq_of<false>(a, i);
+          u = tiles_before(s, s.nq, a.TQ) * a.c.Hkv;
         }
       }
       long long inc = u;
@@ -349,13 +346,13 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
         const int l = __ffs(hit) - 1;
         p.b = i0 + l;
         base += __shfl_sync(0xffffffffu, inc - u, l);
-        p.first = i0 == 0 ? seq_from(mine, l) : seq_of<SHARED>(a, p.b);
+        p.first = i0 == 0 ? seq_from(mine, l) : seq_of<false>(a, p.b);
         break;
       }
       base += __shfl_sync(0xffffffffu, inc, 31);
     }
     const Seq s = p.first;
-    const long long head = tiles_before<SHARED>(s, s.nq, a.TQ), off = p.s - base;
+    const long long head = tiles_before(s, s.nq, a.TQ), off = p.s - base;
     p.kvh = static_cast<int>(div64(off, head));
     const long long in = off - p.kvh * head;
     // The last t with tiles_before(t) <= in: 32 candidates a round.
@@ -363,11 +360,96 @@ __device__ __noinline__ void make_plan(const Args &a, Plan *plan, int lane) {
     while (step > 1) {
       step = (step + 31) / 32;
       const long long cand = lo + static_cast<long long>(step) * lane;
-      const bool below = cand < s.nq && tiles_before<SHARED>(s, static_cast<int>(cand), a.TQ) <= in;
+      const bool below = cand < s.nq && tiles_before(s, static_cast<int>(cand), a.TQ) <= in;
       lo += step * (31 - __clz(__ballot_sync(0xffffffffu, below)));
     }
     p.t = lo;
-    p.j = static_cast<int>(in - tiles_before<SHARED>(s, lo, a.TQ));
+    p.j = static_cast<int>(in - tiles_before(s, lo, a.TQ));
+  }
+  if (lane == 0) *plan = p;
+}
+
+// a / b; a 64-bit division only where it takes one.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return div64(a, b);
+}
+// make_plan for groups, whose row tiles all have the same key tiles: fewer steps and
+// less code in front of the first load (a CTA starts when another kernel's leave its
+// SM, and its code is not in the caches).
+__device__ __forceinline__ void make_shared_plan(const Args &a, Plan *plan, int lane) {
+  const int c = blockIdx.x, count = a.groups.n;
+  auto group_seq = [&](int i) {
+    const Group g = group_of(a.c, a.groups, a.seqlens, i);
+    return Seq{g.prefix, g.first, g.n, g.prefix > 0 && g.n > a.few ? (g.n + a.TQ - 1) / a.TQ : 0};
+  };
+  auto units = [&](const Seq &s) { return static_cast<long long>(s.nq) * a.c.Hkv * ((s.len + BN - 1) / BN); };
+  long long U = 0;
+  int items = 0;
+  Seq mine = {}, s0 = {};  // mine: group `lane`
+  bool alike = true;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int i = i0 + lane;
+    Seq s = {};
+    if (i < count) s = group_seq(i);
+    if (i0 == 0) {
+      mine = s;
+      s0 = seq_from(s, 0);
+    }
+    if (i < count) {
+      U += units(s);
+      items += s.nq * a.c.Hkv;
+      alike = alike && s.n == s0.n && s.len == s0.len && s.first == i * s0.n;
+    }
+  }
+  alike = __all_sync(0xffffffffu, alike) && s0.nq > 0;
+  items = __reduce_add_sync(0xffffffffu, items);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+  const long long least = max(1ll, min(static_cast<long long>(kMinTiles), quotient(U, max(items, 1))));
+  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), quotient(U, least)));
+  Plan p;
+  p.U = U;
+  p.n = static_cast<int>(n);
+  p.s = c < n ? quotient(c * U, n) : 0;
+  p.e = c < n ? quotient((c + 1) * U, n) : 0;
+  p.b = p.kvh = p.t = p.j = p.items = 0;
+  p.first = s0;
+  if (alike && items >= kRoundItems * static_cast<int>(gridDim.x)) {
+    p.items = items;
+    p.n = gridDim.x;
+  } else if (p.s < p.e) {
+    long long base = 0;
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      const int i = i0 + lane;
+      Seq s = mine;
+      if (i0 > 0) {
+        s = Seq{};
+        if (i < count) s = group_seq(i);
+      }
+      const long long u = units(s);
+      long long inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, i < count && base + inc > p.s);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        p.b = i0 + l;
+        base += __shfl_sync(0xffffffffu, inc - u, l);
+        p.first = seq_from(s, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const Seq s = p.first;
+    const int tiles = (s.len + BN - 1) / BN;
+    const long long off = p.s - base, row_tile = quotient(off, tiles);
+    p.j = static_cast<int>(off - row_tile * tiles);
+    p.kvh = static_cast<int>(quotient(row_tile, s.nq));
+    p.t = static_cast<int>(row_tile - static_cast<long long>(p.kvh) * s.nq);
   }
   if (lane == 0) *plan = p;
 }
@@ -443,7 +525,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == 0) make_plan<SHARED>(a, plan, lane);
+  if (warp == 0) {
+    if constexpr (SHARED) make_shared_plan(a, plan, lane);
+    else make_plan(a, plan, lane);
+  }
   if (threadIdx.x == 32) {
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 2);
