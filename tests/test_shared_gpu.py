@@ -284,6 +284,76 @@ def test_two_streams_at_once():
     plx_check_device_error()
 
 
+def test_pages_past_32_bit_offsets():
+    """A prefix and own keys behind 4 GB of the pool, in both kernels."""
+    device()
+    for sizes, Hq in (([3], 8), ([6, 3], 32)):  # few rows; 24 and 12 rows a kv head
+        n, Hkv, page, B = 9000, 8, 256, sum(sizes)
+        kp = torch.zeros(n, Hkv, page, 128, dtype=torch.bfloat16, device="cuda")
+        vp = torch.zeros_like(kp)
+        kp[n - 40:], vp[n - 40:] = torch.randn(2, 40, Hkv, page, 128, device="cuda").to(torch.bfloat16)
+        first = [sum(sizes[:g]) for g in range(len(sizes))]
+        table = torch.zeros(B, 2, dtype=I32, device="cuda")
+        for g, b in enumerate(first):
+            table[b:b + sizes[g], 0] = n - 1 - g
+        table[:, 1] = torch.arange(n - 20, n - 20 + B, device="cuda")
+        lens = ints([260 + b for b in range(B)])
+        q, r = (ref.normal_rows(B, Hq, 3, x).cuda() for x in (1.0, 0.05))
+        out = plx_decode_fwd_shared(q, r, kp, vp, table, lens, ends(sizes), ints([256] * len(sizes)))
+        plx_check_device_error()
+        for b in range(B):
+            K, V = (torch.cat([x[table[b, 0].item()], x[table[b, 1].item()]], 1)[:, :260 + b].double().cpu().numpy()
+                    for x in (kp, vp))
+            for h in range(Hq):
+                o, _, bound = ref.attend(q[b:b + 1, h].double().cpu().numpy(), r[b:b + 1, h].double().cpu().numpy(),
+                                         K[h // (Hq // Hkv)], V[h // (Hq // Hkv)], [260 + b])
+                assert np.all(np.abs(out[b, h].double().cpu().numpy() - o[0]) <= bound[0]), (b, h)
+        del kp, vp
+
+
+def test_calls_from_two_host_threads():
+    """Each with a stream, a cache and queries of its own: rotate, update, decode."""
+    import threading
+    device()
+    freq, _ = plx_rotary_freqs(128, device="cuda")
+    jobs = []
+    for seed in (3, 4):
+        q, r, kw, (o, _, bound) = problem([3, 40], [300, 70], [301, 320, 5] + [90] * 40, 4, 2, 32, seed == 4, seed)
+        x = ref.normal_rows(64, 4, seed).cuda()
+        pos = torch.arange(64, dtype=I32, device="cuda") * seed
+        want = plx_rotary_fwd(x, None, freq, positions=pos)[0]
+        jobs.append((q, r, kw, o, bound, x, pos, want))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(job):
+        q, r, kw, o, bound, x, pos, want = job
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                table = torch.zeros(4, 4, dtype=I32, device="cuda")
+                lens, refs = (torch.zeros(k, dtype=I32, device="cuda") for k in (4, 12))
+                pages = torch.zeros(2, 12, 1, 16, 128, dtype=torch.bfloat16, device="cuda")
+                for i in range(20):
+                    out = plx_decode_fwd_shared(q, r, **kw)
+                    y = plx_rotary_fwd(x, None, freq, positions=pos)[0]
+                    grown = min(40, 2 * i + 2)
+                    plx_kv_update(pages[0], pages[1], table, lens, refs, ints([grown, grown, 0, 0]),
+                                  src=ints([0, 0, -1, -1]))
+                torch.cuda.current_stream().synchronize()
+                ref.assert_within(out, o, bound, "thread")
+                assert torch.equal(y, want) and lens.tolist() == [40, 40, 0, 0]
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    plx_check_device_error()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_debug_build_gives_the_same_bits(fp8, monkeypatch):
     device()
