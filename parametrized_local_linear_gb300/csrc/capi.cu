@@ -795,8 +795,8 @@ plx_status plx_kv_update(void *kpages, void *vpages, unsigned char *kscale, unsi
   const int in_place = (block_table_out == block_table) + (seqlens_out == seqlens) + (page_refs_out == page_refs);
   if (in_place != 0 && in_place != 3)
     return fail(PLX_ERR_INVALID_ARG, "%s: either all of the outputs are the inputs, or none", fn);
-  if (B > (1 << 20) || (static_cast<long long>(Hkv) + 1) * B > 0x7fffffffLL)
-    return fail(PLX_ERR_UNSUPPORTED, "%s: B at most 2^20 and B * (Hkv + 1) below 2^31", fn);
+  if (B > (1 << 20) || (static_cast<long long>(Hkv) + 64) * B > 0x7fffffffLL)
+    return fail(PLX_ERR_UNSUPPORTED, "%s: B at most 2^20 and B * (Hkv + 64) below 2^31", fn);
   const size_t need = plx_kv_update_workspace_bytes(B, num_pages, max_pages);
   if (workspace && workspace_bytes < need)
     return fail(PLX_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);

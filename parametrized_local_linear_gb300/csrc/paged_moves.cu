@@ -12,12 +12,14 @@
 //     free pages of a block's segment and the rows' needs, the lowest free pages.
 //     The moves copy the used slots of copied pages and write the rows' entries.
 //     GB300, replays of a graph: 64 rows of 190 pages in a pool of 12773 that grow by a
-//     token 13.0 us; 64 rows that take over others of 32 to 130 pages 12.7.
+//     token 12.6 us (a cluster of four 14.7, one block 26.7); 64 rows that take over
+//     others of 32 to 130 pages 13.6 (13.7, 16.4); in a pool of 4 million pages 30 us
+//     in place and 143 with tables of 3.6 million entries written elsewhere.
 //   compact: used pages of a segment, then their ranks: a used page from U on goes to
 //     the free one below U of its rank among the moves. The moves are one copy of
 //     every moved page, 16 bytes a thread and four at a time: 417 MB there and back
-//     in 122 us, 6.8 TB/s, the rate of a copy (135 us with the plan); 48 pages of 33 KB
-//     7.5 us.
+//     in 122 us, 6.8 TB/s, the rate of a copy (132 us with the plan); 48 pages of 33 KB
+//     7.5 us; the plan and 3.6 million entries of a pool of 4 million pages 136 us.
 #include <limits.h>
 #include <string.h>
 
@@ -28,6 +30,7 @@ namespace {
 
 constexpr int D = 128;
 constexpr int THREADS = 256;
+constexpr int ENTRIES = 4 * THREADS;  // block table entries of a block
 
 // ---------------------------------------------------------------- update
 // What a row of the new table is made of.
@@ -44,6 +47,7 @@ struct UpdateArgs {
   Row *rows;
   int *free_list;
   int *counts;  // free pages of every block's segment, the pages that rows need, the free ones
+  int chunks;   // blocks for a row's entries
   int *stage;   // old entries of the rows when the tables are updated in place, else null
 };
 
@@ -87,27 +91,57 @@ __device__ __forceinline__ T block_scan(T x, T *total) {
   return (warp > 0 ? before : T(0)) + inc - x;
 }
 
-// Four flags of a thread, those of places k PLAN + thread (k < 4), as prefix sums over
-// the places in their order: at[k], and the sum of all.
-__device__ __forceinline__ int flags_scan(const bool (&flag)[4], int (&at)[4]) {
-  unsigned long long x = 0, all;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x |= static_cast<unsigned long long>(flag[k]) << (16 * k);  // at most PLAN in each field
-  const unsigned long long before = block_scan<unsigned long long>(x, &all);
-  int sum = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    at[k] = sum + static_cast<int>((before >> (16 * k)) & 0xffffu);
-    sum += static_cast<int>((all >> (16 * k)) & 0xffffu);
-  }
-  return sum;
-}
-
 // The block's pages of all of them: [*p0, returned).
 __device__ __forceinline__ int segment(int pages, int *p0) {
   const long long each = (static_cast<long long>(pages) + CL * PLAN - 1) / (CL * PLAN) * PLAN;
   *p0 = static_cast<int>(min(each * blockIdx.x, static_cast<long long>(pages)));
   return static_cast<int>(min(each * (blockIdx.x + 1), static_cast<long long>(pages)));
+}
+
+// A warp's pages of its block's: [*lo, returned). Counted and listed warp by warp,
+// eight loads in flight, with one scan of the warps' counts.
+__device__ __forceinline__ int warp_range(int p0, int p1, int *lo) {
+  const int each = ((p1 - p0 + 31) / 32 + 31) / 32 * 32, warp = threadIdx.x >> 5;
+  *lo = min(p0 + warp * each, p1);
+  return min(*lo + each, p1);
+}
+constexpr int U8 = 8;
+// Pages of [lo, hi) for which flag(page) holds, in every lane.
+template <typename Flag>
+__device__ __forceinline__ int count_pages(int lo, int hi, Flag flag) {
+  int n = 0;
+  for (int p = lo + (threadIdx.x & 31); p < hi; p += 32 * U8) {
+#pragma unroll
+    for (int k = 0; k < U8; ++k) n += flag(min(p + 32 * k, hi - 1)) & (p + 32 * k < hi);  // no branch: loads together
+  }
+  return __reduce_add_sync(0xffffffffu, n);
+}
+// emit(page, holds, pages of the range in front of it for which it holds, plus run) for
+// the pages of [lo, hi), until run reaches `stop`.
+template <typename Flag, typename Emit>
+__device__ __forceinline__ void list_pages(int lo, int hi, int run, int stop, Flag flag, Emit emit) {
+  const int lane = threadIdx.x & 31;
+  for (int p = lo; p < hi && run < stop; p += 32 * U8) {
+    bool holds[U8];
+#pragma unroll
+    for (int k = 0; k < U8; ++k) holds[k] = flag(min(p + 32 * k + lane, hi - 1)) & (p + 32 * k + lane < hi);
+#pragma unroll
+    for (int k = 0; k < U8; ++k) {
+      const unsigned m = __ballot_sync(0xffffffffu, holds[k]);
+      if (p + 32 * k + lane < hi) emit(p + 32 * k + lane, holds[k], run + __popc(m & ((1u << lane) - 1)));
+      run += __popc(m);
+    }
+  }
+}
+// The block's count from its warps', and (*before) those of the warps in front.
+__device__ __forceinline__ int block_count(int n, int *before) {
+  __shared__ int counts[PLAN / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) counts[warp] = n;
+  __syncthreads();
+  const int x = counts[lane];
+  *before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+  return __reduce_add_sync(0xffffffffu, x);
 }
 
 // A part of row b: what it keeps, and the reference counts without partial last pages.
@@ -173,24 +207,25 @@ __device__ __forceinline__ Row final_row(const UpdateArgs &a, int b, int found) 
   return r;
 }
 
-// Job `job` of row b's Hkv + 1, by THREADS threads: its entries, or the slots of one kv
-// head of its copied page.
-__device__ __forceinline__ void move_row(const UpdateArgs &a, const Row &r, int b, int job, int thread) {
+// Entries [j0, j1) of row b, by THREADS threads.
+__device__ __forceinline__ void write_entries(const UpdateArgs &a, const Row &r, int b, int j0, int j1, int thread) {
   const int shift = a.c.page_shift;
-  if (job == 0) {
-    const long long base = static_cast<long long>(b) * a.c.max_pages;
-    const int *from = a.stage != nullptr ? a.stage + base : a.c.table + static_cast<long long>(max(r.src, 0)) * a.c.max_pages;
-    const int pages = (r.new_len + (1 << shift) - 1) >> shift, kept = r.full + r.keep;
-    const bool stays = a.stage != nullptr && r.src == b;  // in place: its old entries are there
-    for (int j = (stays ? kept : 0) + thread; j < pages; j += THREADS)
-      a.table_out[base + j] = j < r.full ? from[j] : j < kept ? r.tail : __ldcg(&a.free_list[r.start + j - kept]);
-    if (thread == 0) a.seqlens_out[b] = r.new_len;
-    return;
-  }
+  const long long base = static_cast<long long>(b) * a.c.max_pages;
+  const int *from = a.stage != nullptr ? a.stage + base : a.c.table + static_cast<long long>(max(r.src, 0)) * a.c.max_pages;
+  const int pages = (r.new_len + (1 << shift) - 1) >> shift, kept = r.full + r.keep;
+  const bool stays = a.stage != nullptr && r.src == b;  // in place: its old entries are there
+#pragma unroll 4
+  for (int j = (stays ? max(kept, j0) : j0) + thread; j < min(pages, j1); j += THREADS)
+    a.table_out[base + j] = j < r.full ? from[j] : j < kept ? r.tail : __ldcg(&a.free_list[r.start + j - kept]);
+  if (j0 == 0 && thread == 0) a.seqlens_out[b] = r.new_len;
+}
+// The slots of one kv head of a row's copied page, by THREADS threads.
+__device__ __forceinline__ void copy_slots(const UpdateArgs &a, const Row &r, int head, int thread) {
+  const int shift = a.c.page_shift;
   if (!r.copies) return;
   const int to = __ldcg(&a.free_list[r.start]);
-  const long long src = (static_cast<long long>(r.tail) * a.c.Hkv + job - 1) << shift;
-  const long long dst = (static_cast<long long>(to) * a.c.Hkv + job - 1) << shift;
+  const long long src = (static_cast<long long>(r.tail) * a.c.Hkv + head) << shift;
+  const long long dst = (static_cast<long long>(to) * a.c.Hkv + head) << shift;
   if (!PLX_IN_BOUNDS(row_inside(a.c, src + r.part - 1) && row_inside(a.c, dst + r.part - 1), ErrWord{a.c.err})) return;
   const int bytes = a.c.kscale != nullptr ? D : 2 * D;  // of a slot
   const int n = r.part * bytes / 16;
@@ -225,7 +260,15 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
   const int B = a.c.B, rank = blockIdx.x;
   if (!MOVES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.refs != a.refs_out) {
-    for (int p = rank * PLAN + threadIdx.x; p < a.c.num_pages; p += CL * PLAN) a.refs_out[p] = a.refs[p];
+    for (long long p = rank * PLAN + threadIdx.x; p < a.c.num_pages; p += U8 * CL * PLAN) {
+      int n[U8];
+#pragma unroll
+      for (int k = 0; k < U8; ++k)
+        if (p + k * CL * PLAN < a.c.num_pages) n[k] = a.refs[p + k * CL * PLAN];
+#pragma unroll
+      for (int k = 0; k < U8; ++k)
+        if (p + k * CL * PLAN < a.c.num_pages) a.refs_out[p + k * CL * PLAN] = n[k];
+    }
     cluster_sync();
   }
   constexpr int WARPS = CL * PLAN / 32;
@@ -244,10 +287,10 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
   // (No barrier of the cluster is behind a condition on data: blocks that saw
   // different data, as a call that overlaps another on the same cache could, would
   // wait for ever.)
-  int p0, mine = 0, all_free;
-  const int p1 = segment(a.c.num_pages, &p0);
-  for (int p = p0 + threadIdx.x; p < p1; p += PLAN) mine += __ldcg(&a.refs_out[p]) == 0;
-  block_scan<int>(mine, &all_free);
+  int p0, lo, in_block;
+  const int p1 = segment(a.c.num_pages, &p0), hi = warp_range(p0, p1, &lo);
+  auto is_free = [&](int p) { return __ldcg(&a.refs_out[p]) == 0; };
+  const int all_free = block_count(count_pages(lo, hi, is_free), &in_block);
   if (threadIdx.x == 0) a.counts[rank] = all_free;
   if (rank == 0) {
     long long sum = 0;
@@ -306,39 +349,33 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
       granted = least;
     }
     // The lowest free pages, as many as are granted.
-    for (int q0 = p0; q0 < p1 && below < granted; q0 += 4 * PLAN) {
-      bool is_free[4];
-      int at[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int p = q0 + k * PLAN + threadIdx.x;
-        is_free[k] = p < p1 && __ldcg(&a.refs_out[p]) == 0;
-      }
-      const int n = flags_scan(is_free, at);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (is_free[k] && below + at[k] < granted) {
-          const int p = q0 + k * PLAN + threadIdx.x;
-          a.free_list[below + at[k]] = p;
-          a.refs_out[p] = 1;
-        }
-      below += n;
-    }
+    list_pages(lo, hi, below + in_block, granted, is_free, [&](int p, bool holds, int at) {
+      if (!holds || at >= granted) return;
+      a.free_list[at] = p;
+      a.refs_out[p] = 1;
+    });
   }
   if constexpr (MOVES) {
     cluster_sync();
     constexpr int PER = PLAN / THREADS;
     for (int b = rank * PER + threadIdx.x / THREADS; b < B; b += CL * PER) {
       const Row r = final_row(a, b, found);
-      for (int job = 0; job <= (r.copies ? a.c.Hkv : 0); ++job) move_row(a, r, b, job, threadIdx.x % THREADS);
+      write_entries(a, r, b, 0, a.c.max_pages, threadIdx.x % THREADS);
+      for (int head = 0; head < (r.copies ? a.c.Hkv : 0); ++head) copy_slots(a, r, head, threadIdx.x % THREADS);
     }
   }
 }
 
 __global__ void __launch_bounds__(THREADS) update_move_kernel(const UpdateArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.x / (a.c.Hkv + 1);
-  move_row(a, final_row(a, b, __ldcg(&a.counts[CL + 1])), b, blockIdx.x - b * (a.c.Hkv + 1), threadIdx.x);
+  const int jobs = a.c.Hkv + a.chunks, b = blockIdx.x / jobs, job = blockIdx.x - b * jobs;
+  const Row r = final_row(a, b, __ldcg(&a.counts[CL + 1]));
+  if (job >= a.chunks) {
+    copy_slots(a, r, job - a.chunks, threadIdx.x);
+  } else {
+    for (long long j0 = static_cast<long long>(job) * ENTRIES; j0 < a.c.max_pages; j0 += static_cast<long long>(a.chunks) * ENTRIES)
+      write_entries(a, r, b, static_cast<int>(j0), static_cast<int>(j0) + ENTRIES, threadIdx.x);
+  }
 }
 
 // ---------------------------------------------------------------- compaction
@@ -355,10 +392,10 @@ struct CompactArgs {
 
 __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) compact_plan_kernel(const CompactArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int p0, mine = 0, all;
-  const int p1 = segment(a.c.num_pages, &p0);
-  for (int p = p0 + threadIdx.x; p < p1; p += PLAN) mine += a.refs[p] > 0;
-  block_scan<int>(mine, &all);
+  int p0, lo, in_block;
+  const int p1 = segment(a.c.num_pages, &p0), hi = warp_range(p0, p1, &lo);
+  auto is_used = [&](int p) { return a.refs[p] > 0; };
+  const int all = block_count(count_pages(lo, hi, is_used), &in_block);
   if (threadIdx.x == 0) a.counts[blockIdx.x] = all;
   cluster_sync();
   int below = 0, U = 0;
@@ -371,26 +408,12 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) compact_plan_ker
     a.used[0] = U;
     if (U == a.c.num_pages) *a.base = U;
   }
-  for (int q0 = p0; q0 < p1; q0 += 4 * PLAN) {
-    bool is_used[4];
-    int at[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int p = q0 + k * PLAN + threadIdx.x;
-      is_used[k] = p < p1 && a.refs[p] > 0;
-    }
-    const int n = flags_scan(is_used, at);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int p = q0 + k * PLAN + threadIdx.x, rank = below + at[k];
-      if (p >= p1) continue;
-      if (p == U) *a.base = rank;
-      a.rank[p] = is_used[k] ? rank : -1;
-      if (p < U && !is_used[k]) a.holes[p - rank] = p;
-      if (p >= U && is_used[k]) a.by_rank[rank] = p;
-    }
-    below += n;
-  }
+  list_pages(lo, hi, below + in_block, INT_MAX, is_used, [&](int p, bool holds, int rank) {
+    if (p == U) *a.base = rank;
+    a.rank[p] = holds ? rank : -1;
+    if (p < U && !holds) a.holes[p - rank] = p;
+    if (p >= U && holds) a.by_rank[rank] = p;
+  });
 }
 
 __global__ void __launch_bounds__(THREADS) compact_move_kernel(const CompactArgs a) {
@@ -408,10 +431,13 @@ __global__ void __launch_bounds__(THREADS) compact_move_kernel(const CompactArgs
     if (p >= U) a.refs_out[p] = 0;
   }
   const int shift = a.c.page_shift;
-  for (int b = blockIdx.x; b < a.c.B; b += gridDim.x) {
-    const int pages = (cache_len(a.c, a.seqlens, b) + (1 << shift) - 1) >> shift;
+  const int chunks = (a.c.max_pages + ENTRIES - 1) / ENTRIES;
+  for (long long w = blockIdx.x; w < static_cast<long long>(a.c.B) * chunks; w += gridDim.x) {
+    const int b = static_cast<int>(w / chunks), j0 = static_cast<int>(w - static_cast<long long>(b) * chunks) * ENTRIES;
+    const int pages = min((cache_len(a.c, a.seqlens, b) + (1 << shift) - 1) >> shift, j0 + ENTRIES);
     const long long row = static_cast<long long>(b) * a.c.max_pages;
-    for (int j = threadIdx.x; j < pages; j += THREADS) {
+#pragma unroll 4
+    for (int j = j0 + threadIdx.x; j < pages; j += THREADS) {
       int p = a.c.table[row + j];
       if (good_page(a.c, p)) {
         const int rank = a.rank[p];
@@ -490,13 +516,17 @@ cudaError_t launch_kv_update(const PagedCache &c, const int *seqlens, const int 
   a.free_list = reinterpret_cast<int *>(ws);
   ws += round256(size_t(c.num_pages) * 4);
   a.stage = table_out == c.table ? reinterpret_cast<int *>(ws) : nullptr;
-  if (src == nullptr) {
+  a.chunks = (c.max_pages + ENTRIES - 1) / ENTRIES;
+  a.chunks = a.chunks < 64 ? a.chunks : 64;
+  // One launch where there is little to write: each row keeps its own tokens, and the
+  // tables are updated in place or small (eight blocks copy 60000 entries in 3 us).
+  if (src == nullptr && (a.stage != nullptr || static_cast<long long>(c.B) * c.max_pages <= 65536)) {
     update_plan_kernel<true><<<CL, PLAN, 0, stream>>>(a);
     return cudaGetLastError();
   }
   update_plan_kernel<false><<<CL, PLAN, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_after(update_move_kernel, static_cast<unsigned>(c.B) * (c.Hkv + 1), a, stream);
+  return e != cudaSuccess ? e : launch_after(update_move_kernel, static_cast<unsigned>(c.B) * (c.Hkv + a.chunks), a, stream);
 }
 
 size_t kv_compact_workspace_bytes(int num_pages) {
