@@ -388,8 +388,8 @@ size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
  * the weights of a sequence meet in one softmax. A prefix that is longer than the
  * group's first sequence is taken for none, and ends of groups that decrease or pass
  * B as no group; plx_check_device_error reports PLX_ERR_INVALID_ARG for both.
- * ngroups >= 1. workspace as for plx_decode_fwd_paged, of
- * plx_decode_shared_workspace_bytes(B, Hq, Hkv, d).
+ * ngroups is 1 .. 2^24, B * Hq at most 2^24. workspace as for plx_decode_fwd_paged, of
+ * plx_decode_shared_workspace_bytes(B, Hq, Hkv, d) (for any ngroups).
  */
 plx_status plx_decode_fwd_shared(const void *q, const void *r, const void *kpages,
                                  const void *vpages, const unsigned char *kscale,
@@ -428,7 +428,7 @@ size_t plx_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d);
  * and the copied pages. All three may be the inputs (in place), or none of them.
  * A row whose src or lens is out of range stays as it was; pages that do not exist
  * are kept as entries and not followed; plx_check_device_error reports
- * PLX_ERR_INVALID_ARG for each. Counts that do not cover the rows' use give
+ * PLX_ERR_INVALID_ARG for each. B is at most 2^20. Counts that do not cover the rows' use give
  * undefined tables, but nothing outside the arguments is read or written.
  * workspace: at least plx_kv_update_workspace_bytes(B, num_pages, max_pages) bytes
  * on the device, 16-byte aligned, or NULL to allocate them in stream order. Calls
@@ -487,7 +487,7 @@ size_t plx_kv_compact_workspace_bytes(int num_pages);
  *               behind the last sequence are left as they were. Both NULL: row t of
  *               each sequence has position t.
  *   inv_freq  : fp64 [R / 2] on the device, finite, radians a position
- * d is 64 or 128, R even, 2 .. d; pointers 16-byte aligned.
+ * d is 64 or 128, R even, 2 .. d; pointers 16-byte aligned. B, L may be 0.
  */
 #define PLX_BF16 0
 #define PLX_F32 1

@@ -703,17 +703,12 @@ def plx_prefill_fwd_paged(q, r, kpages, vpages, block_table, seqlens, cu_q, ksca
     return out, lse
 
 
-def plx_decode_fwd_shared(q, r, kpages, vpages, block_table, seqlens, cu_g, prefix_lens, kscale=None,
-                          vscale=None, out=None, workspace=None, stream=None):
-    """Decode over a paged KV cache for groups of sequences that share their first
-    keys (see include/plx.h): q, r bf16 [B, Hq, d]; group g is the sequences
-    cu_g[g] .. cu_g[g + 1] - 1, whose first prefix_lens[g] keys are read once, through
-    the first one's pages. Returns out."""
+def _shared_checks(q, r, kpages, block_table, seqlens, cu_g, prefix_lens, out):
+    """Raises for what is wrong with the shapes of a shared decode; returns its groups."""
     if q.dim() != 3:
         raise ValueError(f"q must be [B, Hq, d], got shape {tuple(q.shape)}")
     for name, t in (("seqlens", seqlens), ("cu_g", cu_g), ("prefix_lens", prefix_lens)):
         _given(name, t)
-    dev = q.device
     B, Hq, d = shape = q.shape
     if B != block_table.shape[0] or d != kpages.shape[-1]:
         raise ValueError(f"q must be ({block_table.shape[0]}, {Hq}, {kpages.shape[-1]}), got shape "
@@ -721,24 +716,41 @@ def plx_decode_fwd_shared(q, r, kpages, vpages, block_table, seqlens, cu_g, pref
     if prefix_lens.dim() != 1 or prefix_lens.shape[0] < 1:
         raise ValueError(f"prefix_lens must be [ngroups], got shape {tuple(prefix_lens.shape)}")
     groups = prefix_lens.shape[0]
-    index, bf16 = dev.index, torch.bfloat16
-    good = (_is(q, bf16, shape, index) and _is(r, bf16, shape, index)
-            and (out is None or _is(out, bf16, shape, index))
-            and _is(cu_g, torch.int32, (groups + 1,), index)
-            and _is(prefix_lens, torch.int32, (groups,), index))
+    for name, t in (("r", r), ("out", out)):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
+    if cu_g.shape != (groups + 1,):
+        raise ValueError(f"cu_g must have shape ({groups + 1},), got {tuple(cu_g.shape)}")
+    return groups
+
+
+def plx_decode_fwd_shared(q, r, kpages, vpages, block_table, seqlens, cu_g, prefix_lens, kscale=None,
+                          vscale=None, out=None, workspace=None, stream=None):
+    """Decode over a paged KV cache for groups of sequences that share their first
+    keys (see include/plx.h): q, r bf16 [B, Hq, d]; group g is the sequences
+    cu_g[g] .. cu_g[g + 1] - 1, whose first prefix_lens[g] keys are read once, through
+    the first one's pages. Returns out."""
+    dev, shape, bf16, i32 = q.device, q.shape, torch.bfloat16, torch.int32
+    index = dev.index
+    good = (seqlens is not None and cu_g is not None and prefix_lens is not None
+            and len(shape) == 3 and shape[0] == block_table.shape[0]
+            and shape[2] == kpages.shape[-1] and len(prefix_lens.shape) == 1
+            and prefix_lens.shape[0] >= 1)
+    if good:
+        groups = prefix_lens.shape[0]
+        good = (_is(q, bf16, shape, index) and _is(r, bf16, shape, index)
+                and (out is None or _is(out, bf16, shape, index))
+                and _is(cu_g, i32, (groups + 1,), index) and _is(prefix_lens, i32, (groups,), index))
     if not good:
-        for name, t in (("r", r), ("out", out)):
-            if t is not None and t.shape != shape:
-                raise ValueError(f"{name} must be {tuple(shape)}, got shape {tuple(t.shape)}")
-        if cu_g.shape != (groups + 1,):
-            raise ValueError(f"cu_g must have shape ({groups + 1},), got {tuple(cu_g.shape)}")
+        groups = _shared_checks(q, r, kpages, block_table, seqlens, cu_g, prefix_lens, out)
+    Hq = shape[1]
     ptrs, (B, Hkv, d, n, page, width) = _pages(kpages, vpages, kscale, vscale, block_table, seqlens,
                                                dev)
     if not good:
         for name, t in (("q", q), ("r", r)) + ((("out", out),) if out is not None else ()):
             _like(t, name, bf16, shape, dev)
-        _like(cu_g, "cu_g", torch.int32, (groups + 1,), dev)
-        _like(prefix_lens, "prefix_lens", torch.int32, (groups,), dev)
+        _like(cu_g, "cu_g", i32, (groups + 1,), dev)
+        _like(prefix_lens, "prefix_lens", i32, (groups,), dev)
     if out is None:
         out = _empty(shape, bf16, dev, stream)
     ws, ws_ptr, ws_bytes = _workspace(workspace, "plx_decode_shared_workspace_bytes",
@@ -907,62 +919,64 @@ def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale,
     x = q if q is not None else k if k is not None else r
     if x is None:
         _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, (q_out, k_out, r_out))
-    index, dtype, shape = x.get_device(), x.dtype, x.shape
-    packed = len(shape) == 3
-    good = index >= 0 and dtype in _ROTARY_DTYPES and (packed or len(shape) == 4)
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    index, dims, nseq = x.get_device(), len(shape), 0
+    packed = dims == 3
+    good = (index >= 0 and dtype in _ROTARY_DTYPES and (packed or dims == 4)
+            and inv_freq.dtype is torch.float64 and inv_freq.get_device() == index
+            and inv_freq.dim() == 1 and inv_freq.is_contiguous())
     if good:
         B, L, d = (1, shape[0], shape[2]) if packed else (shape[0], shape[2], shape[3])
-        Hq = Hkv = 0
-        ptrs, strides, results = [None] * 6, [0] * 18, [None] * 3
-        for at, t, o in ((0, q, q_out), (1, k, k_out), (2, r, r_out)):
-            if t is None:
-                continue
-            ts = t.shape
-            if len(ts) != len(shape):
-                good = False
-                break
-            H = ts[1]
-            if at == 1:
-                Hkv = H
-            else:
-                good = good and (Hq == 0 or H == Hq)
-                Hq = H
-            st = t.stride()
-            good = (good and H > 0 and t.dtype is dtype and t.get_device() == index and st[-1] == 1
-                    and ts == ((L, H, d) if packed else (B, H, L, d)))
-            # (sequence, token, head)
-            strides[3 * at:3 * at + 3] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
-            if o is None:
-                strides[9 + 3 * at:12 + 3 * at] = (0, H * d, d) if packed else (H * L * d, d, L * d)
-            else:
-                st = o.stride()
-                good = (good and o.shape == ts and o.dtype is dtype and o.get_device() == index
-                        and st[-1] == 1)
-                strides[9 + 3 * at:12 + 3 * at] = (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
-            ptrs[at] = t.data_ptr()
-    nseq = 0
-    good = (good and inv_freq.dtype is torch.float64 and inv_freq.get_device() == index
-            and inv_freq.dim() == 1 and inv_freq.is_contiguous())
-    if positions is not None:
-        good = (good and seqlens is None and cu_q is None
-                and _is(positions, torch.int32, (L,) if packed else (B, L), index))
-    elif seqlens is not None:
-        if good:
+        if positions is not None:
+            good = (seqlens is None and cu_q is None
+                    and _is(positions, torch.int32, (L,) if packed else (B, L), index))
+        elif seqlens is not None:
             nseq = seqlens.numel()
             good = (packed and _is(seqlens, torch.int32, (nseq,), index)
                     and (cu_q is None or _is(cu_q, torch.int32, (nseq + 1,), index)))
-    else:
-        good = good and cu_q is None and not packed
-    dev = x.device
+        else:
+            good = cu_q is None and not packed
+    Hq = Hkv = 0
+    ptrs, outs, results = [], [], []  # pointers; (sequence, token, head) strides
+    ins, to = [], []
+    for t, o, kv in ((q, q_out, False), (k, k_out, True), (r, r_out, False)) if good else ():
+        if t is None:
+            ptrs.append(None)
+            outs.append(None)
+            results.append(None)
+            ins += 0, 0, 0
+            to += 0, 0, 0
+            continue
+        ts, st = t.shape, t.stride()
+        if len(ts) != dims:
+            good = False
+            break
+        H = ts[1]
+        if kv:
+            Hkv = H
+        else:
+            good = good and (Hq == 0 or H == Hq)
+            Hq = H
+        good = (good and H > 0 and t.dtype is dtype and t.get_device() == index and st[-1] == 1
+                and ts[0] == shape[0] and ts[-1] == d and (packed or ts[2] == L))
+        ptrs.append(t.data_ptr())
+        ins += (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
+        if o is None:
+            o = _empty(ts, dtype, dev, stream)
+            to += (0, H * d, d) if packed else (H * L * d, d, L * d)
+        else:
+            st = o.stride()
+            good = (good and o.shape == ts and o.dtype is dtype and o.get_device() == index
+                    and st[-1] == 1)
+            to += (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
+        outs.append(o.data_ptr())
+        results.append(o)
     if not good:
         _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, (q_out, k_out, r_out))
-    for at, t, o in ((0, q, q_out), (1, k, k_out), (2, r, r_out)):
-        if t is not None:
-            results[at] = o = _empty(t.shape, dtype, dev, stream) if o is None else o
-            ptrs[3 + at] = o.data_ptr()
+        raise ValueError("rotary tensors with strides that do not go with their last dimension")
     if B > 0 and L > 0:
         _launch(fn, dev, stream,
-                (*ptrs, _strides(*strides), None if positions is None else positions.data_ptr(),
+                (*ptrs, *outs, _strides(*ins, *to), None if positions is None else positions.data_ptr(),
                  None if seqlens is None else seqlens.data_ptr(),
                  None if cu_q is None else cu_q.data_ptr(), inv_freq.data_ptr(), scale, nseq, B, L,
                  Hq or 1, Hkv or 1, d, 2 * inv_freq.shape[0], 1 if interleaved else 0,

@@ -177,6 +177,18 @@ def test_in_place_and_strides(R):
         assert a is c and torch.equal(a, b)
 
 
+def test_the_same_tensor_twice():
+    """As q, k and r at once, into results of their own."""
+    device()
+    freq, _ = plx_rotary_freqs(64, device="cuda")
+    x = rows((40, 3, 128), torch.bfloat16, 1)
+    pos = torch.arange(40, dtype=I32, device="cuda")
+    outs = plx_rotary_fwd(x, x, freq, x, positions=pos)
+    plx_check_device_error()
+    check(outs[0], x, np.arange(40.0)[:, None], freq, 1.0, False)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 def test_values_that_are_not_finite_stay_in_their_pairs():
     device()
     freq, _ = plx_rotary_freqs(64, device="cuda")
