@@ -383,8 +383,9 @@ size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
  *                 share (below zero counts as zero); not more than the first one's
  *                 seqlens. A sequence with fewer keys, or none, sees those it has.
  * Position p >= the prefix's length of a sequence is in its own pages; of its block
- * table, entries in front of the one with the prefix's length are not read (but for
- * the group's first sequence). The result is plx_decode_fwd_paged's up to rounding:
+ * table, entries in front of the one with the prefix's length are not read, and what
+ * the slots in front of it in that page hold does not matter (but for the group's
+ * first sequence). The result is plx_decode_fwd_paged's up to rounding:
  * the weights of a sequence meet in one softmax. A prefix that is longer than the
  * group's first sequence is taken for none, and ends of groups that decrease or pass
  * B as no group; plx_check_device_error reports PLX_ERR_INVALID_ARG for both.

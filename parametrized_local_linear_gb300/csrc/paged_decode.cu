@@ -557,7 +557,9 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
     const int *table = a.c.table + static_cast<long long>(SUFFIX ? it.s.first : it.b) * a.c.max_pages;
     auto page_of = [&](int t) {
       const int key = tile_key<KT, KEYS>(it, it.t0 + t) + lane;
-      return t < nt && key < it.s.len ? table[key >> a.c.page_shift] : -1;
+      // Keys in front of the first have no scale, as those behind the last: whatever
+      // their slots hold, their codes stay finite and get the weight zero.
+      return t < nt && key < it.s.len && !(SUFFIX && key < it.s.start) ? table[key >> a.c.page_shift] : -1;
     };
     auto scales_of = [&](int t, int page) -> uint32_t {
       if (page < 0 || page >= a.c.num_pages) return 0u;
@@ -1033,8 +1035,8 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const CombineArgs a) {
 // the prefix ([dims / 4][row] float4) are read in whole lines. Four threads share a
 // row's parts, so that all of them are on their way in one latency or two; places
 // are looked up before the kernels in front are done. 19 parts for each of 128 rows and
-// 8 kv heads, 22 MB: 5 to 6 us behind the kernels in front (one thread a row 9;
-// eight with fewer loads each 10; two with ten loads each the same).
+// 8 kv heads, 22 MB: 5 to 6 us behind the kernels in front (the whole call 75 us; with
+// eight threads and fewer loads each 79, with two and ten loads each 74).
 struct SharedArgs {
   PagedCache c;
   SharedGroups groups;

@@ -28,8 +28,8 @@ def ints(x):
 
 def cache(sizes, prefix, lens, Hq, Hkv, page, fp8, seed=3, hide=True):
     """A pool in which every group's sequences begin with the same keys, each with its
-    own pages: the whole ones in front of a sequence's own keys are then taken out of
-    its table (hide), but for the first of a group."""
+    own pages: but for the first of a group, the whole ones in front of a sequence's own
+    keys are then taken out of its table, and the slots in front of them get NaN (hide)."""
     pool = ref.filled_pool(lens, Hkv, page, fp8, seed)
     b = 0
     for n, p in zip(sizes, prefix):
@@ -47,6 +47,12 @@ def cache(sizes, prefix, lens, Hq, Hkv, page, fp8, seed=3, hide=True):
         if hide:
             for i in range(b + 1, b + n):
                 kw["block_table"][i, :max(0, p) // page] = -7
+                if p % page and lens[i] > p:  # the shared slots of its first own page
+                    at = pool.table[i, p // page].item()
+                    for name in ("kpages", "vpages"):
+                        kw[name].view(torch.uint8 if fp8 else torch.int16)[at, :, :p % page] = 0x7F if fp8 else 0x7FC0
+                    if fp8:
+                        kw["kscale"][at, :, :p % page] = kw["vscale"][at, :, :p % page] = 255
         b += n
     kw.update(seqlens=pool.seqlens.cuda(), cu_g=ends(sizes), prefix_lens=ints(prefix))
     return pool, q.cuda(), r.cuda(), kw
