@@ -11,14 +11,14 @@
 //   update: counts (rows give up and take over pages), claims of partial last pages,
 //     free pages of a block's segment and the rows' needs, the lowest free pages.
 //     The moves copy the used slots of copied pages and write the rows' entries.
-//     GB300, replays of a graph: 64 rows of 190 pages in a pool of 12773 that grow by a
-//     token 12.6 us (a cluster of four 14.7, one block 26.7); 64 rows that take over
-//     others of 32 to 130 pages 13.6 (13.7, 16.4); in a pool of 4 million pages 30 us
-//     in place and 143 with tables of 3.6 million entries written elsewhere.
+//     GB300, replays of a graph: 64 rows of 195 pages in a pool of 12773 that grow by a
+//     token 12.6 us (a cluster of four 14.7, one block 26.7); 46 rows that take over
+//     others of 37 to 132 pages 13.0 (13.7, 16.4); in a pool of 4 million pages 30 us
+//     in place with nothing to give away, and 143 with tables of 3.6 million entries written elsewhere.
 //   compact: used pages of a segment, then their ranks: a used page from U on goes to
 //     the free one below U of its rank among the moves. The moves are one copy of
-//     every moved page, 16 bytes a thread and four at a time: 417 MB there and back
-//     in 122 us, 6.8 TB/s, the rate of a copy (132 us with the plan); 48 pages of 33 KB
+//     every moved page, 16 bytes a thread and four at a time: 814 MB read and written
+//     in 120 us, 6.8 TB/s, the rate of a copy (132 us with the plan); 78 pages of 33 KB
 //     7.5 us; the plan and 3.6 million entries of a pool of 4 million pages 136 us.
 #include <limits.h>
 #include <string.h>
@@ -192,11 +192,12 @@ __device__ __forceinline__ Row load_row(const Row *r) {
   return x;
 }
 
-// Row b with `found` free pages for all: without those that it needs if they are not
-// among them, and then without a partial page that it would have had to copy.
+// Fresh pages that a row needs.
 __device__ __forceinline__ int need_of(const UpdateArgs &a, const Row &r) {
   return ((r.new_len + (1 << a.c.page_shift) - 1) >> a.c.page_shift) - r.full - r.keep;
 }
+// Row b with `found` free pages for all: without those that it needs if they are not
+// among them, and then without a partial page that it would have had to copy.
 __device__ __forceinline__ Row final_row(const UpdateArgs &a, int b, int found) {
   Row r = load_row(&a.rows[b]);
   const int need = need_of(a, r);
