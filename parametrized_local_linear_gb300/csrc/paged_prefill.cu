@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const float m_used = st[row], l = st[BM + row], sg = st[2 * BM + row];
       // Rows of the output; at most two parts a share, its first item's and its last's.
       const bool item_ok = PLX_IN_BOUNDS(
-          it.b < a.c.B && it.kvh >= 0 && it.kvh < a.c.Hkv && it.row0 >= 0 && it.ntok >= 1 &&
+          it.b < (SHARED ? a.groups.n : a.c.B) && it.kvh >= 0 && it.kvh < a.c.Hkv && it.row0 >= 0 && it.ntok >= 1 &&
               min(it.ntok, a.TQ) <= a.T - it.row0 && (!SHARED || it.table < a.c.B) && ((it.j0 == 0 && it.j1 == it.nt) || k == 0 || (it.j0 == 0 && !cut)),
           ab);
       auto o_read = [&] {  // O has been read: the next item's value UMMAs may overwrite it
