@@ -374,21 +374,23 @@ size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
 /*
  * Decode for sequences that share prefixes (several continuations of one prompt,
  * users behind one instruction): plx_decode_fwd_paged whose sequences come in
- * groups, the first keys of a group's sequences being the same. They are read once
- * for all of them, through the pages of the group's first sequence.
+ * groups, the first keys of a group's sequences being the same. They are read
+ * for all of them together, through the pages of the group's first sequence that has keys.
  *   cu_g        : int32 [ngroups + 1] on the device, non-decreasing from cu_g[0] =
  *                 0: group g is the sequences cu_g[g] .. cu_g[g + 1] - 1 (it may be
  *                 empty). Sequences behind cu_g[ngroups] are in no group.
  *   prefix_lens : int32 [ngroups] on the device: keys that the group's sequences
- *                 share (below zero counts as zero); not more than the first one's
- *                 seqlens. A sequence with fewer keys, or none, sees those it has.
+ *                 share (below zero counts as zero); not more than the seqlens of the
+ *                 group's first sequence that has keys. Sequences in front of that one
+ *                 have ended (seqlens 0), and all of a group may have. A sequence
+ *                 with fewer keys, or none, sees those it has.
  * Position p >= the prefix's length of a sequence is in its own pages; of its block
  * table, entries in front of the one with the prefix's length are not read, and what
  * the slots in front of it in that page hold does not matter (but for the group's
- * first sequence). The result is plx_decode_fwd_paged's up to rounding:
+ * first sequence that has keys). The result is plx_decode_fwd_paged's up to rounding:
  * the weights of a sequence meet in one softmax. A prefix that is longer than the
- * group's first sequence is taken for none, and ends of groups that decrease or pass
- * B as no group; plx_check_device_error reports PLX_ERR_INVALID_ARG for both.
+ * group's first sequence with keys is taken for none, and ends of groups that decrease or
+ * pass B as no group; plx_check_device_error reports PLX_ERR_INVALID_ARG for both.
  * ngroups is 1 .. 2^24, B * Hq at most 2^24. workspace as for plx_decode_fwd_paged, of
  * plx_decode_shared_workspace_bytes(B, Hq, Hkv, d) (for any ngroups).
  */

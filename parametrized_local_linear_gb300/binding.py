@@ -728,8 +728,8 @@ def plx_decode_fwd_shared(q, r, kpages, vpages, block_table, seqlens, cu_g, pref
                           vscale=None, out=None, workspace=None, stream=None):
     """Decode over a paged KV cache for groups of sequences that share their first
     keys (see include/plx.h): q, r bf16 [B, Hq, d]; group g is the sequences
-    cu_g[g] .. cu_g[g + 1] - 1, whose first prefix_lens[g] keys are read once, through
-    the first one's pages. Returns out."""
+    cu_g[g] .. cu_g[g + 1] - 1, whose first prefix_lens[g] keys are read for all of them
+    together, through the pages of the first one that has keys. Returns out."""
     dev, shape, bf16, i32 = q.device, q.shape, torch.bfloat16, torch.int32
     index = dev.index
     good = (seqlens is not None and cu_g is not None and prefix_lens is not None
