@@ -35,7 +35,7 @@ constexpr int ENTRIES = 4 * THREADS;  // block table entries of a block
 // ---------------------------------------------------------------- update
 // What a row of the new table is made of.
 struct Row {
-  int src, full, part, tail;  // old row; its whole pages, then `part` tokens of page `tail` (< 0: none)
+  int src, full, part, tail;  // old row; its whole pages, then `part` tokens (0: none) of page `tail`
   int keep, copies;           // the tail stays; or is copied into the first fresh page
   int new_len, start;         // length; place of its first fresh page in the list of free ones
 };
@@ -51,8 +51,9 @@ struct UpdateArgs {
   int *stage;   // old entries of the rows when the tables are updated in place, else null
 };
 
+__device__ __forceinline__ bool is_page(const PagedCache &c, int page) { return page >= 0 && page < c.num_pages; }
 __device__ __forceinline__ bool good_page(const PagedCache &c, int page) {
-  if (page >= 0 && page < c.num_pages) return true;
+  if (is_page(c, page)) return true;
   if (c.err) atomicOr(c.err, kErrBadInput);
   return false;
 }
@@ -156,8 +157,7 @@ __device__ __forceinline__ void count_row(const UpdateArgs &a, int b, int part_o
     want = old;
   }
   const int have = s == b ? old : s >= 0 ? cache_len(a.c, a.seqlens, s) : 0;
-  const int kept = min(want, have), full = kept >> a.c.page_shift;
-  int part = kept & (P - 1);
+  const int kept = min(want, have), full = kept >> a.c.page_shift, part = kept & (P - 1);
   const int *mine = a.c.table + static_cast<long long>(b) * a.c.max_pages;
   const int *from = a.c.table + static_cast<long long>(max(s, 0)) * a.c.max_pages;
   const int before = (old + P - 1) >> a.c.page_shift, first = 32 * part_of + lane, step = 32 * parts;
@@ -176,8 +176,8 @@ __device__ __forceinline__ void count_row(const UpdateArgs &a, int b, int part_o
     }
   }
   if (first == 0) {
-    int tail = part > 0 ? from[full] : -1;
-    if (part > 0 && !good_page(a.c, tail)) part = 0, tail = -1;
+    const int tail = part > 0 ? from[full] : -1;
+    if (part > 0) good_page(a.c, tail);  // reports; kept as an entry
     const Row r = {s, full, part, tail, 0, 0, want, 0};
     a.rows[b] = r;
   }
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
   cluster_sync();
   for (int b = rank * PLAN + threadIdx.x; b < B; b += CL * PLAN) {
     const int tail = __ldcg(&a.rows[b].tail);
-    if (tail < 0) continue;
+    if (!is_page(a.c, tail)) continue;
     const int v = __ldcg(&a.refs_out[tail]);
     if (v == 0 || v < INT_MIN / 2) atomicMin(&a.refs_out[tail], INT_MIN + b);
   }
@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
       Row r;
       if (b < B) {
         r = load_row(&a.rows[b]);
-        r.keep = r.tail >= 0 && __ldcg(&a.refs_out[r.tail]) == INT_MIN + b;
-        r.copies = r.tail >= 0 && !r.keep;
+        // An entry that is no page stays: there is nothing to copy.
+        r.keep = r.part > 0 && (!is_page(a.c, r.tail) || __ldcg(&a.refs_out[r.tail]) == INT_MIN + b);
+        r.copies = r.part > 0 && !r.keep;
         need = need_of(a, r);
       }
       long long all;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(PLAN, 1) __cluster_dims__(CL) update_plan_kern
       if (threadIdx.x == 0) a.counts[CL + 1] = found;
       for (int b = threadIdx.x; b < B; b += PLAN) {
         const Row r = a.rows[b];  // this thread's
-        if (r.keep) a.refs_out[r.tail] = 1;  // its claim is not read any more
+        if (r.keep && is_page(a.c, r.tail)) a.refs_out[r.tail] = 1;  // its claim is not read any more
       }
     }
     // Where the free pages do not do: the rows from the first one that they do not serve on.
