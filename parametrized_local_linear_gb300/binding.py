@@ -862,6 +862,9 @@ _strides = struct.Struct("18q").pack
 
 def _rotary_checks(q, k, r, inv_freq, positions, seqlens, cu_q, outs):
     """Raises for what is wrong with the tensors of a rotary call."""
+    for name, t, o in zip("qkr", (q, k, r), outs):
+        if t is None and o is not None:
+            raise ValueError(f"{name}_out without {name}")
     given = [(name, t, o) for name, t, o in zip("qkr", (q, k, r), outs) if t is not None]
     if not given:
         raise ValueError("q, k and r are all None")
@@ -941,6 +944,7 @@ def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale,
     ins, to = [], []
     for t, o, kv in ((q, q_out, False), (k, k_out, True), (r, r_out, False)) if good else ():
         if t is None:
+            good = good and o is None
             ptrs.append(None)
             outs.append(None)
             results.append(None)
