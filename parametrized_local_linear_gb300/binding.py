@@ -969,9 +969,11 @@ def _rotary(fn, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved, scale,
             o = _empty(ts, dtype, dev, stream)
             to += (0, H * d, d) if packed else (H * L * d, d, L * d)
         else:
+            if o.shape != ts:
+                good = False
+                break
             st = o.stride()
-            good = (good and o.shape == ts and o.dtype is dtype and o.get_device() == index
-                    and st[-1] == 1)
+            good = good and o.dtype is dtype and o.get_device() == index and st[-1] == 1
             to += (0, st[0], st[1]) if packed else (st[0], st[2], st[1])
         outs.append(o.data_ptr())
         results.append(o)
