@@ -997,7 +997,10 @@ def plx_rotary_fwd(q, k, inv_freq, r=None, positions=None, seqlens=None, cu_q=No
     first 2 * len(inv_freq) values of each row are turned. Positions: int32
     ``positions`` [B, L] or [T], or those of plx_kv_append's new tokens from ``seqlens``
     and ``cu_q`` (packed), or 0 .. L - 1. q, k or r may be None; ``q_out=q`` works in
-    place. Returns (q, k, r) turned."""
+    place. With ``seqlens``, rows of padding and rows behind the last sequence are not
+    written: an output that is given keeps what it held there, one that the call
+    allocates holds anything there, NaN included (give a zeroed one where they are
+    read, as in sums over rows). Returns (q, k, r) turned."""
     return _rotary(lib().plx_rotary_fwd, q, k, r, inv_freq, positions, seqlens, cu_q, interleaved,
                    scale, q_out, k_out, r_out, stream)
 
@@ -1006,7 +1009,8 @@ def plx_rotary_bwd(dq, dk, inv_freq, dr=None, positions=None, seqlens=None, cu_q
                    interleaved=False, scale=1.0, dq_out=None, dk_out=None, dr_out=None,
                    stream=None):
     """Backward of plx_rotary_fwd (see include/plx.h): from the gradients of its outputs
-    those of its inputs, with its other arguments. Returns (dq, dk, dr)."""
+    those of its inputs, with its other arguments; with ``seqlens``, rows that are not
+    written are as there. Returns (dq, dk, dr)."""
     return _rotary(lib().plx_rotary_bwd, dq, dk, dr, inv_freq, positions, seqlens, cu_q, interleaved,
                    scale, dq_out, dk_out, dr_out, stream)
 

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from parametrized_local_linear_gb300 import plx_rotary_fwd
+from parametrized_local_linear_gb300 import plx_check_device_error, plx_rotary_bwd, plx_rotary_freqs, plx_rotary_fwd
 
 from helpers import device
 
@@ -31,3 +31,34 @@ def test_outputs_of_another_shape_are_refused():
             plx_rotary_fwd(x, None, freq, q_out=out)
         with pytest.raises(ValueError, match="q_out has shape"):
             plx_rotary_fwd(rows, None, freq, positions=pos, q_out=out)
+
+
+@pytest.mark.parametrize("fn,names", [(plx_rotary_fwd, "qkr"), (plx_rotary_bwd, ("dq", "dk", "dr"))])
+@pytest.mark.parametrize("cu,lens,T", [([0, 5, 5, 6, 20], [5, 9, 100, 9], 23), (None, [0, 70, 0, 2], 4)])
+def test_rows_of_padding(fn, names, cu, lens, T):
+    """Of outputs that the call allocates, every row of a token is written; zeroed ones that
+    are given stay zero in the other rows, so that sums over all rows are right."""
+    device()
+    freq, _ = plx_rotary_freqs(128, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    x = [torch.randn(T, h, 128, generator=g).cuda() for h in (4, 2, 4)]
+    ends = list(range(len(lens) + 1)) if cu is None else cu
+    there = torch.zeros(T, dtype=torch.bool, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens):
+        for t in range(max(ends[b], ends[b + 1] - n), ends[b + 1]):
+            there[t], pos[t] = True, n - ends[b + 1] + t
+    assert 0 < there.sum() < T
+    for a in x:
+        a[~there] = float("nan")
+    kw = dict(seqlens=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+              cu_q=None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    want = fn(x[0], x[1], freq, x[2], positions=pos)
+    fresh = fn(x[0], x[1], freq, x[2], **kw)
+    given = [torch.zeros_like(a) for a in x]
+    same = fn(x[0], x[1], freq, x[2], **{n + "_out": o for n, o in zip(names, given)}, **kw)
+    plx_check_device_error()
+    for w, f, s, o in zip(want, fresh, same, given):
+        assert s is o
+        assert torch.equal(f[there], w[there]) and torch.equal(o[there], w[there]) and not o[~there].any()
+        assert torch.equal(o.sum(0), torch.where(there[:, None, None], w, 0).sum(0))
