@@ -469,7 +469,9 @@ size_t plx_kv_compact_workspace_bytes(int num_pages);
  * Rotary positions: pairs of the first rotary_dim = R values of every row of q, k and
  * r are turned by the angle position * inv_freq[i], i < R / 2:
  *   y0 = scale (x0 cos a - x1 sin a),   y1 = scale (x1 cos a + x0 sin a)
- * in fp32 from angles that are exact to 2^-33 of a turn, rounded once. The pairs are
+ * in fp32, rounded once. Angles are off by at most 2^-28 + 2^-32 + |position| (|inv_freq|
+ * 2^-54 + 2^-64) of a turn (2.5e-8 radians up to position 2^20, where the fp32 argument of
+ * sine and cosine bounds them; 8e-7 at 2^31 with inv_freq 1, where fp64's of the frequency in turns does). The pairs are
  * (x[i], x[i + R / 2]), or with interleaved != 0 (x[2 i], x[2 i + 1]). Values from R
  * on are copied. plx_rotary_bwd takes the gradients of the outputs and gives those of
  * the inputs (the angles negated, the same scale). The probe r meets the rotated keys:

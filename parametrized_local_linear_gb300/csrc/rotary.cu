@@ -10,10 +10,12 @@
 //
 // Angles. A far position times a frequency loses its fraction of a turn in fp32
 // (position 10^5: 0.008 radians), so f_i / (2 pi) becomes a 64-bit fraction of a
-// turn, once a block, and position times it modulo 2^64 is the fraction of the
-// angle, with no more error than the position times f_i's own in fp64. Its top
-// two bits (rounded) are the quarter of the turn, the rest an angle of at most an
-// eighth, which sincospif takes in fp32 with an error of 2^-33 of a turn.
+// turn, once a block, off by 2^-52 of itself (two roundings in fp64) and 2^-64, and
+// position times it modulo 2^64 is the fraction of the angle, off by position times
+// that. Its upper 32 bits are kept (cut: 2^-32 of a turn); their top two, rounded, are the
+// quarter of the turn, the rest an angle of at most an eighth, 2^29 units, which
+// sincospif takes in fp32: 24 bits, half a step is 2^-28 of a turn. That bounds near
+// positions; the fp64 fraction takes over from about 2^27 on for f_i near 1.
 //
 // A thread takes the same V pairs of several heads of one row: 16 bytes from two
 // places (or from 32 adjacent bytes), with one sine and cosine a pair for all of

@@ -1,4 +1,7 @@
 """Rotary positions on the GPU at the limits of a call."""
+import math
+from decimal import Decimal, localcontext
+
 import pytest
 import torch
 
@@ -62,3 +65,28 @@ def test_rows_of_padding(fn, names, cu, lens, T):
         assert s is o
         assert torch.equal(f[there], w[there]) and torch.equal(o[there], w[there]) and not o[~there].any()
         assert torch.equal(o.sum(0), torch.where(there[:, None, None], w, 0).sum(0))
+
+
+def test_angles_are_as_exact_as_stated():
+    """Rows (1, 0) give the cosine and the sine. Each is off by at most the angle's error,
+    2 pi (2^-28 + 2^-32 + |position| (|inv_freq| 2^-54 + 2^-64)), and sincospi's 2 ulp, at most
+    2^-23; the exact angle in 60 decimal digits, modulo a turn."""
+    device()
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620900")
+    freq, _ = plx_rotary_freqs(64, device="cuda")
+    freq[20:] = torch.tensor([7.5, -3.25, 1.0, 0.999, 0.5, math.pi / 4, 1e-3, 1e-9, 0.0, 2.0, -1.0, 0.3], dtype=torch.float64)
+    near = torch.randint(-(1 << 20), 1 << 20, (600,), generator=torch.Generator().manual_seed(2)).tolist()
+    pos = near + [0, 1, -1, 1 << 20, 1 << 26, 1 << 28, 2**31 - 1, -2**31, 2**31 - 12345]
+    x = torch.zeros(len(pos), 1, 64, device="cuda")
+    x[..., :32] = 1.0
+    y = plx_rotary_fwd(x, None, freq, positions=torch.tensor(pos, dtype=torch.int32, device="cuda"))[0]
+    plx_check_device_error()
+    y, f = y[:, 0].double().cpu(), freq.tolist()
+    with localcontext() as ctx:
+        ctx.prec = 60
+        for t, p in enumerate(pos):
+            for i in range(32):
+                turns = Decimal(p) * Decimal(f[i]) / (2 * pi)
+                a = 2 * math.pi * float(turns - turns.to_integral_value())
+                bound = 2 * math.pi * (2.0 ** -28 + 2.0 ** -32 + abs(p) * (abs(f[i]) * 2.0 ** -54 + 2.0 ** -64)) + 2.0 ** -23
+                assert abs(y[t, i].item() - math.cos(a)) <= bound and abs(y[t, 32 + i].item() - math.sin(a)) <= bound, (p, i)
