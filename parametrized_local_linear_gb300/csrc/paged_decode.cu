@@ -129,19 +129,28 @@ __device__ __forceinline__ int2 own_keys(const RowsArgs &a, int b) {
   return make_int2(len, min(group_with(a.c, a.groups, a.seqlens, b).prefix, len));
 }
 template <int KT, int GS, int KEYS>
-__device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b, const int2 *known) {
-  if constexpr (KEYS > 0) {
-    if (KEYS == kAll && b < a.groups.n) {
-      const Group g = group_of(a.c, a.groups, a.seqlens, b);
-      const long long rows = static_cast<long long>(g.n) * a.G;
-      const bool take = g.n > 0 && rows <= a.most;
-      return Seq{g.prefix, take ? (g.prefix + KT - 1) / KT : 0, g.first, g.n, take ? static_cast<int>((rows + GS - 1) / GS) : 0, 0};
-    }
-    if (KEYS == kAll) b -= a.groups.n;
-    const int2 x = b < KNOWN ? known[b] : own_keys(a, b);
-    const int tiles = x.y < x.x ? (x.x + KT - 1) / KT - x.y / KT : 0;
-    return Seq{x.x, tiles, b, 1, (a.G + GS - 1) / GS, x.y};
+__device__ __forceinline__ Seq shared_seq(const RowsArgs &a, int b, const int2 *known) {
+  if (KEYS == kAll && b < a.groups.n) {
+    const Group g = group_of(a.c, a.groups, a.seqlens, b);
+    const long long rows = static_cast<long long>(g.n) * a.G;
+    const bool take = g.n > 0 && rows <= a.most;
+    return Seq{g.prefix, take ? (g.prefix + KT - 1) / KT : 0, g.first, g.n, take ? static_cast<int>((rows + GS - 1) / GS) : 0, 0};
   }
+  if (KEYS == kAll) b -= a.groups.n;
+  const int2 x = b < KNOWN ? known[b] : own_keys(a, b);
+  const int tiles = x.y < x.x ? (x.x + KT - 1) / KT - x.y / KT : 0;
+  return Seq{x.x, tiles, b, 1, (a.G + GS - 1) / GS, x.y};
+}
+// As a call. The e4m3 consumers have no register to spare: with the lookup in line they
+// spill (16 prefixes of 8000 keys, 8 rows each: 88.6 us as a call, 97.7 in line). In bf16 the
+// calls cost more than they save (1024 sequences in groups of eight: 291 us in line, 298).
+template <int KT, int GS, int KEYS>
+__device__ __noinline__ Seq shared_seq_call(const RowsArgs &a, int b, const int2 *known) {
+  return shared_seq<KT, GS, KEYS>(a, b, known);
+}
+template <int KT, int GS, int KEYS>
+__device__ __forceinline__ Seq seq_of(const RowsArgs &a, int b, const int2 *known) {
+  if constexpr (KEYS > 0) return KT > 16 ? shared_seq_call<KT, GS, KEYS>(a, b, known) : shared_seq<KT, GS, KEYS>(a, b, known);
   // All loads first: they share one latency.
   const int n = a.seqlens[b], first = a.cu != nullptr ? a.cu[b] : b, end = a.cu != nullptr ? a.cu[b + 1] : b + 1;
   Seq s;
