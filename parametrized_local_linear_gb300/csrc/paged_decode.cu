@@ -124,9 +124,10 @@ struct Seq {
   int start;  // the first key; its tile is the sequence's first
 };
 // Keys of sequence b, and the first that its group does not share.
+template <bool TOGETHER = false>
 __device__ __forceinline__ int2 own_keys(const RowsArgs &a, int b) {
   const int len = cache_len(a.c, a.seqlens, b);
-  return make_int2(len, min(group_with(a.c, a.groups, a.seqlens, b).prefix, len));
+  return make_int2(len, min(group_with<TOGETHER>(a.c, a.groups, a.seqlens, b).prefix, len));
 }
 template <int KT, int GS, int KEYS>
 __device__ __forceinline__ Seq shared_seq(const RowsArgs &a, int b, const int2 *known) {
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm)
   const int2 *known = SUFFIX ? reinterpret_cast<const int2 *>(smem + OFF_KNOWN) : nullptr;
   if constexpr (SUFFIX) {
     int2 *to = reinterpret_cast<int2 *>(smem + OFF_KNOWN);
-    for (int i = threadIdx.x; i < min(a.c.B, KNOWN); i += THREADS) to[i] = own_keys(a, i);
+    for (int i = threadIdx.x; i < min(a.c.B, KNOWN); i += THREADS) to[i] = own_keys<true>(a, i);
     __syncthreads();
   }
 
@@ -1105,7 +1106,7 @@ __global__ void __launch_bounds__(CSL * D) shared_combine_kernel(const SharedArg
   Group g = {};
   if (there) {
     len = cache_len(a.c, a.seqlens, b);
-    g = group_with(a.c, a.groups, a.seqlens, b);
+    g = group_with<true>(a.c, a.groups, a.seqlens, b);
   }
   const int start = min(g.prefix, len);
   const int tile = there ? (b - g.first) / a.TQ * a.TQ + g.first : 0, row = (b - tile) * a.G + gh;

@@ -79,17 +79,52 @@ __device__ __forceinline__ int row_sequence(const int *cu, int B, int t) {
 struct Group {
   int first, n, prefix;
 };
-// The first of the sequences [b, end) that has keys, or end. Not inlined: the code in
-// front of the kernels' first loads would carry the loop (64 sequences in groups of eight
-// behind 500 keys, GB300: 26.8 us, 27.4 inlined, 26.1 without this step).
+// The first of the sequences [b, end) that has keys, or end; a length out of range is
+// none, as in checked_len. Not inlined: the code in front of the kernels' first loads
+// would carry the loop (64 sequences in groups of eight behind 500 keys, GB300: 26.8 us,
+// 27.4 inlined, 26.1 without this step).
 static __device__ __noinline__ int first_with_keys(const int *seqlens, int most, int b, int end) {
 #pragma unroll 1
-  for (; b < end; ++b) {
-    const int n = seqlens[b];
-    if (n > 0 && n <= most) break;  // out of range: none, as in checked_len
+  for (; b < end; b += 8) {
+    int n[8];  // on their way together
+#pragma unroll
+    for (int k = 0; k < 8; ++k) n[k] = seqlens[min(b + k, end - 1)];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (n[k] > 0 && n[k] <= most) return b + k;
   }
-  return b;
+  return end;
 }
+// The same where the lanes of a warp look together (where all threads look groups up: a
+// batch of 512 sequences whose first 511 have ended 85 us, 371 with each for itself).
+static __device__ __noinline__ int first_with_keys_together(const int *seqlens, int most, int b, int end) {
+  const unsigned lanes = __activemask(), lane = threadIdx.x & 31;
+  const int n = __popc(lanes), rank = __popc(lanes & ((1u << lane) - 1));
+  int found = end;
+  unsigned todo = lanes;
+#pragma unroll 1
+  while (todo != 0u) {
+    const int from = __ffs(todo) - 1;
+    const int first = __shfl_sync(lanes, b, from), last = __shfl_sync(lanes, end, from);
+    int at = last;
+#pragma unroll 1
+    for (int i = first; i < last && at == last; i += 4 * n) {
+      int x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = seqlens[min(i + k * n + rank, last - 1)];
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        const unsigned has = __ballot_sync(lanes, x[k] > 0 && x[k] <= most);
+        if (has != 0u) at = min(i + k * n + __popc(lanes & ((has & (0u - has)) - 1)), last - 1);
+      }
+    }
+    const bool mine = b == first && end == last;
+    if (mine) found = at;
+    todo &= ~__ballot_sync(lanes, mine);
+  }
+  return found;
+}
+template <bool TOGETHER = false>
 __device__ __forceinline__ Group group_of(const PagedCache &c, const SharedGroups &g, const int *seqlens, int i) {
   const int first = g.cu[i], end = g.cu[i + 1], want = g.prefix[i];
   if (first < 0 || end > c.B || end < first) {
@@ -98,7 +133,8 @@ __device__ __forceinline__ Group group_of(const PagedCache &c, const SharedGroup
   }
   Group r = {first, end - first, max(want, 0)};
   if (r.n > 0 && r.prefix > cache_len(c, seqlens, first)) {
-    r.first = first_with_keys(seqlens, c.max_pages << c.page_shift, first, end);
+    const int most = c.max_pages << c.page_shift;
+    r.first = TOGETHER ? first_with_keys_together(seqlens, most, first, end) : first_with_keys(seqlens, most, first, end);
     r.n = end - r.first;
     if (r.n > 0 && r.prefix > seqlens[r.first]) {
       if (c.err) atomicOr(c.err, kErrBadInput);
@@ -108,9 +144,10 @@ __device__ __forceinline__ Group group_of(const PagedCache &c, const SharedGroup
   return r;
 }
 // The group of sequence b; no sequences if it is in none.
+template <bool TOGETHER = false>
 __device__ __forceinline__ Group group_with(const PagedCache &c, const SharedGroups &g, const int *seqlens, int b) {
   const int i = row_sequence(g.cu, g.n, b);
-  return i < 0 ? Group{b, 0, 0} : group_of(c, g, seqlens, i);
+  return i < 0 ? Group{b, 0, 0} : group_of<TOGETHER>(c, g, seqlens, i);
 }
 
 // 2^(E - 127), 1 <= E <= 254.

@@ -44,6 +44,9 @@ ENDED = [  # sizes, sequences in front of each group's that have ended, prefix, 
     ([3, 20], [7, 1], [100, 333], [101, 20, 150] + [340] * 20, 4, 2, 16),          # both, fewer keys than the prefix
     ([40], [24], [4000], [4001 + i for i in range(40)], 8, 1, 64),                 # split between CTAs
     ([0, 2, 0], [4, 1, 3], [500, 129, 7], [130, 400], 6, 2, 128),                  # all of a group
+    ([1], [299], [100], [110], 4, 2, 16),                                          # one of 300 is left
+    ([33, 2], [260, 135], [90, 31], [91 + i for i in range(33)] + [32, 31], 4, 2, 32),
+    ([1, 3], [600, 41], [17, 64], [18, 65, 0, 70], 2, 1, 16),                      # more than are looked up ahead
     ([2] * 290, [1] * 290, [20 + b % 40 for b in range(290)],
      [20 + b % 40 + 1 + i for b in range(290) for i in range(2)], 2, 1, 16),       # 870 sequences
 ]
