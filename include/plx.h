@@ -391,6 +391,11 @@ size_t plx_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
  * the weights of a sequence meet in one softmax. A prefix that is longer than the
  * group's first sequence with keys is taken for none, and ends of groups that decrease or
  * pass B as no group; plx_check_device_error reports PLX_ERR_INVALID_ARG for both.
+ * What is read: a group's shared keys once for every 128 rows (sequence, query head) of
+ * a kv head, or, where groups have few rows, once for every eight; a sequence's own keys
+ * once for every eight query heads a kv head. It pays where a prefix is long or its rows
+ * are many: 64 sequences in groups of eight behind 500 keys take as long as in
+ * plx_decode_fwd_paged, 64 behind 32768 a ninth.
  * ngroups is 1 .. 2^24, B * Hq at most 2^24. workspace as for plx_decode_fwd_paged, of
  * plx_decode_shared_workspace_bytes(B, Hq, Hkv, d) (for any ngroups).
  */
@@ -476,7 +481,9 @@ size_t plx_kv_compact_workspace_bytes(int num_pages);
  * on are copied. plx_rotary_bwd takes the gradients of the outputs and gives those of
  * the inputs (the angles negated, the same scale). The probe r meets the rotated keys:
  * rotated like q, r.k depends on the distance of the positions, as q.k does; without
- * r (NULL), it is left to the caller.
+ * r (NULL), it is left to the caller. `scale` multiplies r as it does q and k, so r.k
+ * grows by its square; a probe that is turned but keeps its size takes a call of its own,
+ * with scale 1 (r.k then has the factor of k).
  *   q, k, r : [B, H, L, d] in any order of the three outer dimensions, H = Hq for q
  *             and r, Hkv for k; dtype PLX_BF16 or PLX_F32; each may be NULL, not all.
  *             Packed rows [T, H, d] are B = 1, L = T.

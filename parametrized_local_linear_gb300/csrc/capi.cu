@@ -690,14 +690,17 @@ namespace {
 // kv head by the tile kernel, or once for every eight by the rows kernel, which needs
 // no second launch and has no deep pipeline to fill. GB300, GPU time of the latter and
 // of the tile kernel, 200 own keys at most:
-//   - 8 rows a group: 1 prefix of 4000 keys x 8 kv heads 16.4 and 26.8 us (bf16; e4m3
-//     16.9 and 30.0), 16 of 8000 109 and 124 (93 and 154), 1 of 32000 x 1 23.2 and 27.5;
-//   - 16 rows: 1 of 4000 x 8 19.1 and 28.0 (19.1 and 31.9), 16 of 2000 70 and 73 (77
-//     and 84), 16 of 8000 194 and 135 (165 and 164);
-//   - 32 rows: 1 of 4000 x 8 24.8 and 29.4 (25.0 and 31.5), 1 of 32000 76 and 50.
+//   - 8 rows a group: 1 prefix of 4000 keys x 8 kv heads 17.1 and 23.5 us (bf16; e4m3
+//     17.1 and 26.4), 16 of 8000 107 and 113 (90 and 141), 1 of 32000 x 1 23.6 and 25.6;
+//   - 16 rows: 1 of 4000 x 8 19.8 and 24.4 (19.8 and 27.6), 16 of 2000 72 and 68 (74
+//     and 75), 16 of 8000 192 and 125 (162 and 152);
+//   - 32 rows: 1 of 4000 x 8 25.4 and 25.7 (25.8 and 26.6), 1 of 32000 79 and 45.
 // So the rows kernel takes the prefixes where groups have at most eight rows on
 // average, or more as long as its further passes are short (over at most kMorePasses
-// key rows, by the block table's width: lengths live on the device). It then takes the
+// key rows, by the block table's width: lengths live on the device; so wide tables of short
+// prefixes lose it: 16 rows over 4000 keys x 8 19.5 us in tables of 16384 keys, 24 in
+// tables of 32768 and more). With one kv head it gives the rows kernel long prefixes of
+// 24 rows and more that the tile kernel reads faster (1 of 32000 x 1 41 and 26). It then takes the
 // groups of up to `most` rows, and the tile kernel the others, if there can be any.
 // (Only up to kFewPlaces sequences x kv heads: the records of both have places.)
 constexpr int kFewPlaces = 4096;
